@@ -14,6 +14,11 @@ Two layers:
 * ``HashTable`` -- the same calls on torch tensors, raising ``HKVError`` on a
   non-zero status and allocating outputs.
 
+The operators on looked-up rows (4-bit microscaled copies and their product,
+the preference loss and its gradient, gradient clipping) have the same two
+layers: ``hkv_mx_quantize`` / ... here and ``mx_quantize`` / ... on tensors in
+``hash_table_cache_gb300.operators``, exported here too.
+
 Semantics follow "HierarchicalKV: A GPU Hash Table with Cache Semantics for
 Continuous Online Embedding Storage" (arXiv 2603.17168v1); see the header for
 the exact contract of each call.
@@ -45,6 +50,11 @@ HKV_ERR_TIMEOUT = -5
 SLOTS_PER_BUCKET = 128
 RESERVED_KEY_LO = 0xFFFFFFFFFFFFFFF0
 HKV_MAX_BATCH = 0x7FFFFFFF  # largest n a batched call accepts
+# element types of the operators' buffers
+HKV_F32 = 0
+HKV_BF16 = 1
+HKV_F16 = 2
+CLIP_WORK_BYTES = 16384
 
 # Every symbol include/hkv.h declares (checked by the CPU test suite).
 EXPORTS = (
@@ -52,7 +62,9 @@ EXPORTS = (
     "hkv_size", "hkv_export", "hkv_get_error_counts", "hkv_get_op_counts",
     "hkv_reset_op_counts", "hkv_get_info", "hkv_status_string", "hkv_insert_or_assign_noalloc",
     "hkv_insert_and_evict", "hkv_find_or_insert", "hkv_contains", "hkv_find_ptr",
-    "hkv_set_epoch",
+    "hkv_set_epoch", "hkv_mx_quantize", "hkv_mx_dequantize", "hkv_mx_matmul",
+    "hkv_preference_loss", "hkv_preference_loss_backward", "hkv_clip_grad_norm",
+    "hkv_get_wait_timeouts",
 )
 NOALLOC_SCRATCH_BYTES = 32 << 20
 
@@ -78,6 +90,11 @@ class Info(ctypes.Structure):
                 ("hbm_values_addr", ctypes.c_uint64), ("host_values_addr", ctypes.c_uint64)]
 
 
+class Grad(ctypes.Structure):
+    _fields_ = [("data", ctypes.c_void_p), ("out", ctypes.c_void_p), ("n", ctypes.c_uint64),
+                ("type", ctypes.c_int32), ("out_type", ctypes.c_int32)]
+
+
 _lib = None
 
 
@@ -95,6 +112,7 @@ def load(path: str = LIB_PATH):
                           "`python -m hash_table_cache_gb300._build` (nvcc, sm_103a)")
     lib = ctypes.CDLL(path)
     u64, u32, vp, st = ctypes.c_uint64, ctypes.c_uint32, ctypes.c_void_p, ctypes.c_int
+    i32, f32 = ctypes.c_int, ctypes.c_float
     sig = {
         "hkv_create": [u64, u32, u32, u64, ctypes.c_int, ctypes.POINTER(vp)],
         "hkv_destroy": [vp],
@@ -114,6 +132,15 @@ def load(path: str = LIB_PATH):
         "hkv_reset_op_counts": [vp],
         "hkv_get_info": [vp, ctypes.POINTER(Info)],
         "hkv_set_epoch": [vp, u32],
+        "hkv_mx_quantize": [u64, u64, vp, i32, u64, vp, vp, vp, vp, vp],
+        "hkv_mx_dequantize": [u64, u64, vp, vp, vp, i32, u64, vp],
+        "hkv_mx_matmul": [u64, u64, u64, vp, vp, vp, vp, vp, i32, u64, vp],
+        "hkv_preference_loss": [u64, u64, u64, vp, i32, u64, vp, vp, vp, f32, f32, i32, vp, vp, vp,
+                                vp, vp, vp, vp],
+        "hkv_preference_loss_backward": [u64, u64, u64, vp, i32, u64, vp, vp, vp, vp, vp, vp, u64,
+                                         vp],
+        "hkv_clip_grad_norm": [u64, vp, f32, vp, vp, vp],
+        "hkv_get_wait_timeouts": [ctypes.POINTER(u64)],
     }
     for name, args in sig.items():
         fn = getattr(lib, name)
@@ -240,6 +267,50 @@ def hkv_get_info(table):
 
 def hkv_set_epoch(table, epoch):
     return load().hkv_set_epoch(table, int(epoch) & 0xFFFFFFFF)
+
+
+def hkv_mx_quantize(rows, cols, x, x_type, x_stride, codes=None, scales=None, codes_t=None,
+                    scales_t=None, stream=None):
+    return load().hkv_mx_quantize(rows, cols, _p(x), x_type, x_stride, _p(codes), _p(scales),
+                                  _p(codes_t), _p(scales_t), _s(stream))
+
+
+def hkv_mx_dequantize(rows, cols, codes, scales, y, y_type, y_stride, stream=None):
+    return load().hkv_mx_dequantize(rows, cols, _p(codes), _p(scales), _p(y), y_type, y_stride,
+                                    _s(stream))
+
+
+def hkv_mx_matmul(m, n, k, a_codes, a_scales, b_codes, b_scales, y, y_type, y_stride, stream=None):
+    return load().hkv_mx_matmul(m, n, k, _p(a_codes), _p(a_scales), _p(b_codes), _p(b_scales),
+                                _p(y), y_type, y_stride, _s(stream))
+
+
+def hkv_preference_loss(pairs, rows, vocab, logits, type, stride, labels, offsets, ref_logps, beta,
+                        label_smoothing, average, losses, ratios, logps, lse, row_grad, row_pair,
+                        stream=None):
+    return load().hkv_preference_loss(pairs, rows, vocab, _p(logits), type, stride, _p(labels),
+                                      _p(offsets), _p(ref_logps), beta, label_smoothing,
+                                      int(average), _p(losses), _p(ratios), _p(logps), _p(lse),
+                                      _p(row_grad), _p(row_pair), _s(stream))
+
+
+def hkv_preference_loss_backward(pairs, rows, vocab, logits, type, stride, labels, lse, row_grad,
+                                 row_pair, dlosses, dlogits, dstride, stream=None):
+    return load().hkv_preference_loss_backward(pairs, rows, vocab, _p(logits), type, stride,
+                                               _p(labels), _p(lse), _p(row_grad), _p(row_pair),
+                                               _p(dlosses), _p(dlogits), dstride, _s(stream))
+
+
+def hkv_clip_grad_norm(count, grads, max_norm, norm_out, work, stream=None):
+    """`grads`: a ctypes array of Grad."""
+    return load().hkv_clip_grad_norm(count, grads, max_norm, _p(norm_out), _p(work), _s(stream))
+
+
+def hkv_get_wait_timeouts():
+    """Returns (status, timeouts)."""
+    v = ctypes.c_uint64()
+    st = load().hkv_get_wait_timeouts(ctypes.byref(v))
+    return st, int(v.value)
 
 
 def hkv_status_string(status):
@@ -395,3 +466,7 @@ class HashTable:
 
     def set_epoch(self, epoch):
         _check(hkv_set_epoch(self.handle, epoch), "hkv_set_epoch")
+
+
+from .operators import (MXMatrix, PreferenceLoss, clip_grad_norm, mx_matmul,  # noqa: E402
+                        mx_quantize, preference_loss, preference_loss_backward)

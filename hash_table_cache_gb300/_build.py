@@ -12,7 +12,8 @@ INCLUDE = os.path.join(ROOT, "include")
 BUILD = os.path.join(PKG, "_build")
 LIB = os.path.join(PKG, "libhkv.so")
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
-SOURCES = ["table.cu", "find.cu", "upsert.cu", "export.cu", "no_alloc.cu"]
+SOURCES = ["table.cu", "find.cu", "upsert.cu", "export.cu", "no_alloc.cu",
+           "mx_quantize.cu", "mx_matmul.cu", "preference.cu", "clip.cu"]
 # measurement helper used by bench.py, kept out of the table library
 PROBE_SOURCE = "access_probe.cu"
 PROBE_LIB = os.path.join(PKG, "libhkv_probe.so")

@@ -319,6 +319,135 @@ hkv_status hkv_set_epoch(hkv_table* table, uint32_t epoch);
 hkv_status hkv_insert_or_assign_noalloc(hkv_table* table, uint64_t n, const uint64_t* keys,
                                         const float* values, const uint64_t* scores, void* stream);
 
+/* ---------------------------------------------------------------------------
+ * Operators on looked-up rows.
+ *
+ * A training step on a table's rows runs find -> 4-bit copies -> products ->
+ * loss and gradient -> norm and clipping -> assign; a serving step scores
+ * hidden states against 4-bit copies of rows.  The calls below are the steps
+ * between the table's own.  They take no table: they run on the current
+ * device, which must be the device of `stream`, are asynchronous, allocate
+ * nothing, keep nothing between calls and may be captured into a CUDA graph.
+ * Argument errors are found on the host and enqueue nothing.  All matrices
+ * are row-major; a stride is the number of elements from one row to the next
+ * (at least the row length).  Rows, columns and counts are at most
+ * HKV_MAX_BATCH; element offsets are 64 bits wide.  Results do not depend on
+ * scheduling: no sum is taken in the order of atomics. */
+
+/* Element types of the operators' buffers. */
+enum { HKV_F32 = 0, HKV_BF16 = 1, HKV_F16 = 2 };
+
+/* Microscaled 4-bit matrices (OCP microscaling formats, MXFP4).  A row is cut
+ * into blocks of 32 columns.  A block's scale byte s stands for 2^(s - 127),
+ * s = max(E - 2, 0) with E the biased exponent of the block's largest
+ * magnitude as a float32 (0 for zero and subnormals); an element is the
+ * nearest of 0, 0.5, 1, 1.5, 2, 3, 4, 6 (e2m1, with a sign) to x / scale,
+ * ties to the even code, 6 above the range.  A block that holds a NaN or an
+ * infinity has s = 255 and stands for 32 NaNs (its codes are 0).
+ *  codes   rows x ceil(cols / 32) x 16 bytes, two codes a byte, the lower
+ *          column in the low half; columns past `cols` are 0.
+ *  scales  ceil(rows / 128) x ceil(cols / 128) groups of 512 bytes, one group
+ *          for 128 rows by 4 blocks, byte (r % 32) * 16 + (r / 32 % 4) * 4 +
+ *          block % 4 of it for row r; bytes of rows and blocks past the
+ *          matrix are 0.
+ * Both 16-byte aligned. */
+#define HKV_MX_BLOCK 32
+#define HKV_MX_CODE_BYTES(rows, cols) ((uint64_t)(rows) * (((uint64_t)(cols) + 31) / 32) * 16)
+#define HKV_MX_SCALE_BYTES(rows, cols) \
+  ((((uint64_t)(rows) + 127) / 128) * (((uint64_t)(cols) + 127) / 128) * 512)
+
+/* The 4-bit copy of x (rows x cols, float32, bfloat16 or float16): of its
+ * rows (codes, scales), of its columns (codes_t, scales_t: the copy of the
+ * cols x rows transpose, blocks running along x's rows), or both from one
+ * read.  Pass NULL for both pointers of a copy that is not wanted; at least
+ * one copy is.  The products of a backward pass need the copies along the
+ * other axis: dX = dY W takes the rows of dY and the columns of W, and
+ * dW = dY^T X the columns of dY and of X. */
+hkv_status hkv_mx_quantize(uint64_t rows, uint64_t cols, const void* x, int x_type,
+                           uint64_t x_stride, uint8_t* codes, uint8_t* scales, uint8_t* codes_t,
+                           uint8_t* scales_t, void* stream);
+
+/* The values a 4-bit matrix stands for, exact in float32 and bfloat16
+ * (float16: rounded, infinite past its range). */
+hkv_status hkv_mx_dequantize(uint64_t rows, uint64_t cols, const uint8_t* codes,
+                             const uint8_t* scales, void* y, int y_type, uint64_t y_stride,
+                             void* stream);
+
+/* y (m x n) = A B^T for 4-bit matrices A (m x k) and B (n x k): products of
+ * elements are exact, sums are taken in float32, y is rounded once.  k = 0
+ * gives zeros.  A block of NaNs makes its whole row (A) or column (B) of y
+ * NaN. */
+hkv_status hkv_mx_matmul(uint64_t m, uint64_t n, uint64_t k, const uint8_t* a_codes,
+                         const uint8_t* a_scales, const uint8_t* b_codes, const uint8_t* b_scales,
+                         void* y, int y_type, uint64_t y_stride, void* stream);
+
+/* Preference loss over pairs of token sequences (the logistic loss of paired
+ * log ratios), from logits.  `logits` holds one row of `vocab` logits for
+ * each of `rows` tokens.  Sequence s has rows offsets[s] .. offsets[s + 1]
+ * (offsets: device, 2 * pairs + 1 ascending values in 0 .. rows); sequence p
+ * is the chosen and sequence pairs + p the rejected one of pair p.  A token
+ * whose label lies outside 0 .. vocab - 1 is not counted: its logits have no
+ * effect, whatever they hold.  For counted tokens
+ *   logps[t]  = logits[t][labels[t]] - lse[t],  lse[t] = log sum exp logits[t]
+ *   ratios[s] = sum of logps[t] - ref_logps[t] over the counted tokens of s,
+ *               divided by their number when `average` is not 0 (0 for a
+ *               sequence without counted tokens; ref_logps NULL: zeros)
+ *   h         = beta * (ratios[p] - ratios[pairs + p])
+ *   losses[p] = -(1 - label_smoothing) log sigmoid(h)
+ *               - label_smoothing log sigmoid(-h)
+ * logps is 0 for tokens that are not counted.  For the backward call the
+ * forward call also writes row_grad[t] = d losses[p] / d logps[t] (0 for
+ * tokens that are not counted or lie in no sequence) and row_pair[t] = p (-1
+ * in no sequence).  beta is finite, 0 <= label_smoothing <= 1. */
+hkv_status hkv_preference_loss(uint64_t pairs, uint64_t rows, uint64_t vocab, const void* logits,
+                               int type, uint64_t stride, const int64_t* labels,
+                               const int64_t* offsets, const float* ref_logps, float beta,
+                               float label_smoothing, int average, float* losses, float* ratios,
+                               float* logps, float* lse, float* row_grad, int32_t* row_pair,
+                               void* stream);
+
+/* Gradient of sum_p dlosses[p] * losses[p] with respect to the logits
+ * (dlosses NULL: ones), in the logits' type:
+ *   dlogits[t][v] = g (1[v = labels[t]] - exp(logits[t][v] - lse[t])),
+ *   g = dlosses[row_pair[t]] * row_grad[t]
+ * and zeros for a token that is not counted or lies in no sequence.  dlogits
+ * may be the logits' own buffer with the same stride. */
+hkv_status hkv_preference_loss_backward(uint64_t pairs, uint64_t rows, uint64_t vocab,
+                                        const void* logits, int type, uint64_t stride,
+                                        const int64_t* labels, const float* lse,
+                                        const float* row_grad, const int32_t* row_pair,
+                                        const float* dlosses, void* dlogits, uint64_t dstride,
+                                        void* stream);
+
+/* One gradient: n elements of `type` at `data`.  Where `out` is not NULL the
+ * clipped gradient is written there as `out_type`; it may be `data` itself
+ * with the same type, and must not overlap it otherwise. */
+typedef struct hkv_grad {
+  const void* data;
+  void* out;
+  uint64_t n;
+  int32_t type, out_type;
+} hkv_grad;
+
+/* Global norm of `count` gradients and clipping to it:
+ *   *norm_out = sqrt(sum over all gradients and elements of g^2)   (device)
+ *   out       = f * g, f = 1 if *norm_out <= max_norm, else max_norm / *norm_out
+ * An infinite norm gives f = 0 and a NaN norm f = NaN.  Where f is 1, out is
+ * data and the types agree, nothing is written.  `grads` is a host array,
+ * read before the call returns.  `work` is device memory of
+ * HKV_CLIP_WORK_BYTES (4-byte aligned) that no other call uses meanwhile.
+ * Squares are summed in float32 and may overflow to infinity for elements
+ * above 1e18.  max_norm is not negative. */
+#define HKV_CLIP_WORK_BYTES 16384
+hkv_status hkv_clip_grad_norm(uint64_t count, const hkv_grad* grads, float max_norm,
+                              float* norm_out, void* work, void* stream);
+
+/* Bounded device-side waits of the operators that ran out since the library
+ * was loaded, on the current device (0 unless the device failed); such a call
+ * returned without complete results.  Waits for the device's outstanding
+ * work.  Returns HKV_ERR_TIMEOUT when the count is not 0. */
+hkv_status hkv_get_wait_timeouts(uint64_t* timeouts_host);
+
 /* Human-readable name of a status code (static storage). */
 const char* hkv_status_string(hkv_status status);
 
