@@ -1,53 +1,434 @@
-// mx_matmul.cu -- hkv_mx_matmul: the product of two 4-bit microscaled matrices.
+// mx_matmul.cu -- hkv_mx_matmul: the product of two 4-bit microscaled matrices
+// on the block-scaled 4-bit tensor cores.
+//
+// y[i][j] = sum_k A[i][k] B[j][k].  The rows of B are the rows of the tensor
+// core's tile (128 of them, one TMEM lane each) and the rows of A its columns
+// (16 to 192 of them), so one token still fills a tile with 128 useful rows,
+// and a store of one TMEM column is contiguous along y's rows whatever y's
+// alignment.  A step of k is 256 columns: 128 bytes of codes per row, brought
+// by TMA in the 128-byte swizzle the tensor core reads, and two 512-byte
+// groups of scales per 128 rows, which the format stores as they are copied
+// to TMEM.  One warp loads, one issues the copies of scales and the products,
+// four read the accumulators out; accumulators and scales are held twice, so
+// a tile's output leaves while the next one is computed.
+#include <cuda.h>
+
 #include "mx.cuh"
 
 namespace hkv {
 namespace {
 
-constexpr int kTile = 32;  // rows of A and of B per thread block
-
 __device__ unsigned long long g_wait_timeouts;
 
-// A 32 x 32 tile of y per thread block, 32 columns of k at a time.
-template <class T>
-__global__ void __launch_bounds__(256)
-    matmul_kernel(uint64_t m, uint64_t n, uint64_t k, const uint8_t* __restrict__ a_codes,
-                  const uint8_t* __restrict__ a_scales, const uint8_t* __restrict__ b_codes,
-                  const uint8_t* __restrict__ b_scales, T* y, uint64_t stride) {
-  __shared__ float a[kTile][33], b[kTile][33];
-  const uint64_t blocks = (k + 31) / 32, groups = (blocks + 3) / 4;
-  const uint64_t m0 = static_cast<uint64_t>(blockIdx.y) * kTile;
-  const uint64_t n0 = static_cast<uint64_t>(blockIdx.x) * kTile;
-  float acc[4] = {};
-  const int tx = threadIdx.x % 32, ty = threadIdx.x / 32;
-  for (uint64_t kb = 0; kb < blocks; ++kb) {
-    for (int i = threadIdx.x; i < kTile * 16; i += 256) {
-      const int r = i / 16, c = i % 16;
-      uint32_t ca = 0, cb = 0;
-      float sa = 0.f, sb = 0.f;
-      if (m0 + r < m) {
-        ca = a_codes[((m0 + r) * blocks + kb) * 16 + c];
-        sa = mx_scale_value(a_scales[mx_scale_at(m0 + r, kb, groups)]);
-      }
-      if (n0 + r < n) {
-        cb = b_codes[((n0 + r) * blocks + kb) * 16 + c];
-        sb = mx_scale_value(b_scales[mx_scale_at(n0 + r, kb, groups)]);
-      }
-      a[r][2 * c] = mx_code_value(ca & 15) * sa;
-      a[r][2 * c + 1] = mx_code_value(ca >> 4) * sa;
-      b[r][2 * c] = mx_code_value(cb & 15) * sb;
-      b[r][2 * c + 1] = mx_code_value(cb >> 4) * sb;
+constexpr int kRows = 128;       // rows of B per tile
+constexpr int kStepBytes = 128;  // bytes of codes per row and step: 256 columns
+constexpr int kStep = 256;
+constexpr int kThreads = 192;    // warp 0 loads, warp 1 multiplies, warps 2-5 store
+constexpr int kMaxSplits = 8;
+constexpr unsigned kSmemLimit = 232448 - 1024;  // 227 KB less the alignment of the stages
+
+struct Problem {
+  uint64_t m, n, k, groups;  // groups: 4-block scale groups of a row
+  uint64_t tiles_m, tiles_n;
+  const uint8_t* a_scales;
+  const uint8_t* b_scales;
+  void* y;
+  uint64_t stride;
+  int type;
+  bool pairs;  // two neighbours of a row of a 16-bit y are stored at once
+  int splits;  // thread blocks of a cluster that share a tile's k
+};
+
+template <int kCols>
+struct Shape {
+  static constexpr int kScaleRows = kCols > 128 ? 2 : 1;  // groups of 128 rows of A that a tile spans
+  static constexpr int kBBytes = kRows * kStepBytes, kABytes = kCols * kStepBytes;
+  static constexpr int kStageBytes = kBBytes + kABytes + 1024 + 1024 * kScaleRows;
+  static constexpr int kFit = (kSmemLimit - 1024) / kStageBytes;
+  static constexpr int kStages = kFit > 10 ? 10 : kFit;
+  static constexpr int kSmem = kStages * kStageBytes + 2048;
+  // TMEM columns: two buffers of 256, each an accumulator and two steps' scales
+  static constexpr int kScaleCol = kCols <= 192 ? 192 : 256;
+};
+
+// Bounded wait for a phase of a barrier: false after kWaitNs, with the
+// device's count of timeouts raised.
+constexpr uint64_t kWaitNs = 4000000000ull;
+__device__ __forceinline__ uint64_t now_ns() {
+  uint64_t t;
+  asm volatile("mov.u64 %0, %globaltimer;" : "=l"(t));
+  return t;
+}
+__device__ __noinline__ bool slow_wait(uint64_t* bar, uint32_t parity) {
+  const uint64_t begin = now_ns();
+  while (!mbar_try_wait(bar, parity))
+    if (now_ns() - begin > kWaitNs) {
+      atomicAdd(&g_wait_timeouts, 1ull);
+      return false;
     }
-    __syncthreads();
-    for (int q = 0; q < 32; ++q)
-#pragma unroll
-      for (int j = 0; j < 4; ++j) acc[j] += a[ty + 8 * j][q] * b[tx][q];
-    __syncthreads();
+  return true;
+}
+__device__ __forceinline__ bool wait(uint64_t* bar, uint32_t parity) {
+  return mbar_try_wait(bar, parity) || slow_wait(bar, parity);
+}
+__device__ __forceinline__ void mbar_arrive(uint64_t* bar) {
+  asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(smem_u32(bar)) : "memory");
+}
+
+__device__ __forceinline__ void tma_load(void* dst, const CUtensorMap* map, int x, int y,
+                                         uint64_t* bar) {
+  asm volatile(
+      "cp.async.bulk.tensor.2d.shared::cta.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3}], [%4];" ::
+          "r"(smem_u32(dst)),
+      "l"(map), "r"(x), "r"(y), "r"(smem_u32(bar))
+      : "memory");
+}
+
+// Shared-memory descriptors: version 1, K-major.  Codes: rows of 128 bytes in
+// the 128-byte swizzle, 1024 bytes from one group of 8 rows to the next.
+// Scales: 32 rows of 16 bytes without a swizzle, 128 bytes per 8 rows.
+__device__ __forceinline__ uint64_t codes_desc(uint32_t addr) {
+  return (uint64_t)((addr & 0x3FFFF) >> 4) | 1ull << 16 | (1024ull >> 4) << 32 | 1ull << 46 |
+         2ull << 61;
+}
+__device__ __forceinline__ uint64_t scales_desc(uint32_t addr) {
+  return (uint64_t)((addr & 0x3FFFF) >> 4) | (128ull >> 4) << 32 | 1ull << 46;
+}
+// Instruction descriptor of the block-scaled e2m1 product: both types e2m1,
+// ue8m0 scales, `cols` columns, 128 rows, the pair of a scale word's bytes
+// that a product of 64 columns takes (0 or 2).
+__host__ __device__ constexpr uint32_t product_desc(int cols, int pair) {
+  return (uint32_t)pair << 4 | 1u << 7 | 1u << 10 | (uint32_t)(cols >> 3) << 17 | 1u << 23 |
+         (uint32_t)(kRows >> 4) << 24 | (uint32_t)pair << 29;
+}
+
+__device__ __forceinline__ void copy_scales(uint32_t tmem, uint64_t desc) {
+  asm volatile("tcgen05.cp.cta_group::1.32x128b.warpx4 [%0], %1;" ::"r"(tmem), "l"(desc)
+               : "memory");
+}
+__device__ __forceinline__ void product(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc,
+                                        uint32_t sa, uint32_t sb, bool add) {
+  asm volatile(
+      "{\n .reg .pred p;\n setp.ne.u32 p, %6, 0;\n"
+      " tcgen05.mma.cta_group::1.kind::mxf4.block_scale.scale_vec::2X [%0], %1, %2, %3, [%4], [%5], p;\n}" ::
+          "r"(d),
+      "l"(a), "l"(b), "r"(idesc), "r"(sa), "r"(sb), "r"((uint32_t)add)
+      : "memory");
+}
+// The barrier is reached when the products issued so far by this thread are done.
+__device__ __forceinline__ void commit(uint64_t* bar) {
+  asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(
+                   smem_u32(bar))
+               : "memory");
+}
+__device__ __forceinline__ void read_columns(uint32_t tmem, float (&v)[16]) {
+  uint32_t* r = reinterpret_cast<uint32_t*>(v);
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15}, [%16];"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]),
+        "=r"(r[7]), "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]),
+        "=r"(r[14]), "=r"(r[15])
+      : "r"(tmem));
+  asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
+}
+
+__device__ __forceinline__ float remote_f32(uint32_t addr, uint32_t rank) {
+  uint32_t far;
+  float v;
+  asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(far) : "r"(addr), "r"(rank));
+  asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v) : "r"(far) : "memory");
+  return v;
+}
+__device__ __forceinline__ void cluster_sync() {
+  asm volatile("barrier.cluster.arrive.release.aligned;\n barrier.cluster.wait.acquire.aligned;" ::
+                   : "memory");
+}
+
+__device__ __forceinline__ void store_one(const Problem& p, uint64_t i, uint64_t j, float v) {
+  const uint64_t at = i * p.stride + j;
+  if (p.type == HKV_F32) static_cast<float*>(p.y)[at] = v;
+  else if (p.type == HKV_BF16) static_cast<__nv_bfloat16*>(p.y)[at] = __float2bfloat16_rn(v);
+  else static_cast<__half*>(p.y)[at] = __float2half_rn(v);
+}
+__device__ __forceinline__ uint32_t pack2(float lo, float hi, int type) {
+  if (type == HKV_BF16) {
+    const __nv_bfloat162 h = __floats2bfloat162_rn(lo, hi);
+    return *reinterpret_cast<const uint32_t*>(&h);
   }
+  const __half2 h = __floats2half2_rn(lo, hi);
+  return *reinterpret_cast<const uint32_t*>(&h);
+}
+
+// Sixteen accumulator columns (rows i .. i + 15 of y) of this lane's column j.
+__device__ __forceinline__ void store_columns(const Problem& p, uint64_t i, uint64_t j,
+                                              const float (&v)[16]) {
+  if (!p.pairs) {
+    if (j < p.n)
 #pragma unroll
-  for (int j = 0; j < 4; ++j)
-    if (m0 + ty + 8 * j < m && n0 + tx < n)
-      y[(m0 + ty + 8 * j) * stride + n0 + tx] = from_f32<T>(acc[j]);
+      for (int c = 0; c < 16; ++c)
+        if (i + c < p.m) store_one(p, i + c, j, v[c]);
+    return;
+  }
+  // neighbouring lanes trade values, so that an even lane stores both of
+  // their columns for one row and the odd lane for the next: 4-byte stores
+  const bool odd = threadIdx.x & 1;
+  const uint64_t je = j & ~1ull;
+#pragma unroll
+  for (int c = 0; c < 16; c += 2) {
+    const float got = __shfl_xor_sync(0xFFFFFFFFu, odd ? v[c] : v[c + 1], 1);
+    const float lo = odd ? got : v[c], hi = odd ? v[c + 1] : got;
+    const uint64_t row = i + c + odd;
+    if (row < p.m) {
+      if (je + 1 < p.n)
+        *reinterpret_cast<uint32_t*>(static_cast<uint16_t*>(p.y) + row * p.stride + je) =
+            pack2(lo, hi, p.type);
+      else if (je < p.n)
+        store_one(p, row, je, lo);
+    }
+  }
+}
+
+template <int kCols>
+__global__ void __launch_bounds__(kThreads, 1)
+    matmul_kernel(const __grid_constant__ CUtensorMap a_map, const __grid_constant__ CUtensorMap b_map,
+                  const __grid_constant__ Problem p) {
+  using S = Shape<kCols>;
+  extern __shared__ uint8_t raw[];
+  uint8_t* smem = raw + (1024 - (smem_u32(raw) & 1023)) % 1024;
+  __shared__ uint64_t full[S::kStages], empty[S::kStages], ready[2], drained[2];
+  __shared__ uint32_t tmem_base;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+
+  if (warp == 0 && lane == 0) {
+    for (int s = 0; s < S::kStages; ++s) {
+      mbar_init(&full[s], 1);
+      mbar_init(&empty[s], 1);
+    }
+    for (int b = 0; b < 2; ++b) {
+      mbar_init(&ready[b], 1);
+      mbar_init(&drained[b], 4);
+    }
+    fence_proxy_async_smem();
+  }
+  if (warp == 1) {
+    asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], 512;" ::"r"(
+                     smem_u32(&tmem_base))
+                 : "memory");
+    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;");
+  }
+  asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
+  __syncthreads();
+  asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
+  const uint32_t tmem = tmem_base;
+  pdl_trigger();
+  pdl_wait();  // every role: the bounded waits below start when the inputs are there
+
+  const uint64_t tiles = p.tiles_m * p.tiles_n;
+  const uint32_t splits = p.splits, rank = blockIdx.x % splits;
+  const uint64_t first = blockIdx.x / splits, step = gridDim.x / splits;
+  const uint64_t all = (p.k + kStep - 1) / kStep;
+  const uint64_t k0 = all * rank / splits, k1 = all * (rank + 1) / splits;
+
+  if (warp == 0 && lane == 0) {
+    uint32_t it = 0;
+    bool ok = true;
+    for (uint64_t t = first; t < tiles && ok; t += step) {
+      const uint64_t n0 = t % p.tiles_n * kRows, m0 = t / p.tiles_n * kCols;
+      const uint64_t g0 = m0 / 128, g1 = (p.m + 127) / 128;
+      for (uint64_t k = k0; k < k1; ++k, ++it) {
+        const uint32_t s = it % S::kStages;
+        if (it >= S::kStages && !wait(&empty[s], (it / S::kStages + 1) & 1)) {
+          ok = false;
+          break;
+        }
+        uint8_t* stage = smem + s * S::kStageBytes;
+        const uint32_t bytes = (p.groups - 2 * k >= 2 ? 2 : 1) * 512;
+        const int groups = g1 - g0 >= S::kScaleRows ? S::kScaleRows : 1;
+        mbar_arrive_expect_tx(&full[s], S::kBBytes + S::kABytes + bytes * (1 + groups));
+        tma_load(stage, &b_map, static_cast<int>(k * kStepBytes), static_cast<int>(n0), &full[s]);
+        tma_load(stage + S::kBBytes, &a_map, static_cast<int>(k * kStepBytes),
+                 static_cast<int>(m0), &full[s]);
+        uint8_t* sc = stage + S::kBBytes + S::kABytes;
+        bulk_load_smem(sc, p.b_scales + (n0 / 128 * p.groups + 2 * k) * 512, bytes, &full[s]);
+        for (int g = 0; g < groups; ++g)
+          bulk_load_smem(sc + 1024 + g * 1024, p.a_scales + ((g0 + g) * p.groups + 2 * k) * 512,
+                         bytes, &full[s]);
+      }
+    }
+    if (!ok)  // the loads still in flight end before the block does
+      for (uint32_t i = it > S::kStages ? it - S::kStages : 0; i < it; ++i)
+        wait(&full[i % S::kStages], (i / S::kStages) & 1);
+  } else if (warp == 1 && lane == 0) {
+    uint32_t it = 0, n_tile = 0;
+    bool ok = true;
+    for (uint64_t t = first; t < tiles && ok; t += step, ++n_tile) {
+      const uint32_t b = n_tile & 1;
+      const uint32_t d = tmem + b * 256;
+      const uint64_t m0 = t / p.tiles_n * kCols;
+      if (n_tile >= 2 && !wait(&drained[b], (n_tile / 2 + 1) & 1)) break;
+      asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
+      for (uint64_t k = k0; k < k1; ++k, ++it) {
+        const uint32_t s = it % S::kStages;
+        if (!wait(&full[s], (it / S::kStages) & 1)) {
+          ok = false;
+          break;
+        }
+        asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
+        const uint32_t stage = smem_u32(smem) + s * S::kStageBytes;
+        const uint32_t sc = stage + S::kBBytes + S::kABytes;
+        const uint64_t db = codes_desc(stage), da = codes_desc(stage + S::kBBytes);
+        // two sets of scale columns, used by turns: a step's copies do not
+        // wait for the products of the step before
+        const uint32_t sb = tmem + (it & 1) * 256 + S::kScaleCol, sa = sb + 8;
+        const int products = p.k - k * kStep >= kStep ? 4 : static_cast<int>((p.k - k * kStep + 63) / 64);
+#pragma unroll
+        for (int g = 0; g < 2; ++g) {
+          if (2 * g >= products) break;
+          const uint32_t sbg = sb + 4 * g, sag = sa + 4 * S::kScaleRows * g;
+          copy_scales(sbg, scales_desc(sc + 512 * g));
+#pragma unroll
+          for (int r = 0; r < S::kScaleRows; ++r)
+            copy_scales(sag + 4 * r, scales_desc(sc + 1024 + 1024 * r + 512 * g));
+#pragma unroll
+          for (int q = 2 * g; q < 2 * g + 2; ++q) {
+            if (q >= products) break;
+            product(d, db + 2 * q, da + 2 * q, product_desc(kCols, 2 * (q & 1)), sbg,
+                    sag + static_cast<uint32_t>(m0 % 128 / 32), k > k0 || q > 0);
+          }
+        }
+        commit(&empty[s]);
+      }
+      if (ok) commit(&ready[b]);
+    }
+    if (!ok) {  // products in flight end before TMEM is given back
+      commit(&ready[0]);
+      commit(&ready[1]);
+    }
+  } else if (warp >= 2) {
+    const int quarter = warp & 3;  // the TMEM lanes this warp can read
+    uint32_t n_tile = 0;
+    for (uint64_t t = first; t < tiles; t += step, ++n_tile) {
+      const uint32_t b = n_tile & 1;
+      if (!wait(&ready[b], (n_tile / 2) & 1)) break;
+      asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
+      const uint64_t j = t % p.tiles_n * kRows + quarter * 32 + lane, m0 = t / p.tiles_n * kCols;
+      const int cols = p.m - m0 < kCols ? static_cast<int>(p.m - m0) : kCols;
+      const uint32_t d = tmem + b * 256 + (static_cast<uint32_t>(quarter * 32) << 16);
+      for (int c = 0; c < cols; c += 16) {
+        float v[16];
+        read_columns(d + c, v);
+        if (splits == 1) {
+          store_columns(p, m0 + c, j, v);
+        } else {  // this block's part of the sum, for the cluster to add up
+          float* part = reinterpret_cast<float*>(smem) + quarter * 32 + lane;
+#pragma unroll
+          for (int q = 0; q < 16; ++q) part[(c + q) * kRows] = v[q];
+        }
+      }
+      asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&drained[b]);
+    }
+  }
+  __syncwarp();
+  if (splits > 1) {
+    cluster_sync();
+    if (warp >= 2) {
+      const uint64_t m0 = first / p.tiles_n * kCols;
+      const int row = (warp & 3) * 32 + lane;
+      const uint64_t j = first % p.tiles_n * kRows + row;
+      const int cols = p.m - m0 < kCols ? static_cast<int>(p.m - m0) : kCols;
+      const uint32_t part = smem_u32(smem) + row * 4;
+      for (int c = rank; c < cols; c += splits) {
+        float v = 0.f;
+        for (uint32_t r = 0; r < splits; ++r) v += remote_f32(part + c * kRows * 4, r);
+        if (j < p.n) store_one(p, m0 + c, j, v);
+      }
+    }
+    __syncwarp();
+    cluster_sync();  // the others may still read this block's part
+  }
+  asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
+  __syncthreads();
+  if (warp == 1)
+    asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, 512;" ::"r"(tmem));
+}
+
+__global__ void zero_kernel(const __grid_constant__ Problem p) {
+  pdl_wait();
+  const uint64_t step = static_cast<uint64_t>(gridDim.x) * blockDim.x;
+  for (uint64_t i = static_cast<uint64_t>(blockIdx.x) * blockDim.x + threadIdx.x; i < p.m * p.n; i += step)
+    store_one(p, i / p.n, i % p.n, 0.f);
+}
+
+using EncodeFn = decltype(&cuTensorMapEncodeTiled);
+EncodeFn encode_fn() {
+  static EncodeFn fn = [] {
+    void* f = nullptr;
+    cudaDriverEntryPointQueryResult r{};
+    if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &f, 12000, cudaEnableDefault, &r) !=
+            cudaSuccess || r != cudaDriverEntryPointSuccess)
+      f = nullptr;
+    return reinterpret_cast<EncodeFn>(f);
+  }();
+  return fn;
+}
+
+// The codes of a matrix as boxes of 128 bytes by `box` rows, swizzled; bytes
+// and rows past the matrix read as zeros.
+bool map_codes(CUtensorMap* map, const uint8_t* codes, uint64_t rows, uint64_t k, int box) {
+  const uint64_t bytes = (k + kMxBlock - 1) / kMxBlock * 16;
+  const cuuint64_t dims[2] = {bytes, rows}, strides[1] = {bytes};
+  const cuuint32_t boxes[2] = {kStepBytes, static_cast<cuuint32_t>(box)}, steps[2] = {1, 1};
+  EncodeFn f = encode_fn();
+  return f && f(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, const_cast<uint8_t*>(codes), dims, strides,
+                boxes, steps, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+                CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+template <int kCols>
+cudaError_t run(Problem p, const uint8_t* a_codes, const uint8_t* b_codes, cudaStream_t st) {
+  using S = Shape<kCols>;
+  CUtensorMap a_map, b_map;
+  if (!map_codes(&a_map, a_codes, p.m, p.k, kCols) || !map_codes(&b_map, b_codes, p.n, p.k, kRows))
+    return cudaErrorUnknown;
+  p.tiles_m = (p.m + kCols - 1) / kCols;
+  p.tiles_n = (p.n + kRows - 1) / kRows;
+  const uint64_t tiles = p.tiles_m * p.tiles_n, steps = (p.k + kStep - 1) / kStep;
+  const uint64_t sms = sm_count();
+  // few tiles: a cluster shares a tile's k while SMs are idle and each block
+  // keeps two steps at least
+  p.splits = 1;
+  while (p.splits < kMaxSplits && tiles * p.splits * 2 <= sms && steps >= 4ull * p.splits)
+    p.splits *= 2;
+  const uint64_t blocks = p.splits > 1 ? tiles * p.splits : tiles < sms ? tiles : sms;
+  cudaError_t e = cudaFuncSetAttribute(matmul_kernel<kCols>,
+                                       cudaFuncAttributeMaxDynamicSharedMemorySize, S::kSmem);
+  if (e != cudaSuccess) return e;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(static_cast<unsigned>(blocks));
+  cfg.blockDim = dim3(kThreads);
+  cfg.dynamicSmemBytes = S::kSmem;
+  cfg.stream = st;
+  cudaLaunchAttribute attr[2];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  attr[1].id = cudaLaunchAttributeClusterDimension;
+  attr[1].val.clusterDim.x = p.splits;
+  attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 2;
+  return cudaLaunchKernelEx(&cfg, matmul_kernel<kCols>, a_map, b_map, p);
+}
+
+cudaError_t matmul(const Problem& p, const uint8_t* a_codes, const uint8_t* b_codes,
+                   cudaStream_t st) {
+  if (p.k == 0) return launch_chained(zero_kernel, sm_count() * 4, 256, 0, st, p);
+  if (p.m <= 16) return run<16>(p, a_codes, b_codes, st);
+  if (p.m <= 32) return run<32>(p, a_codes, b_codes, st);
+  if (p.m <= 64) return run<64>(p, a_codes, b_codes, st);
+  if (p.m <= 128) return run<128>(p, a_codes, b_codes, st);
+  return run<192>(p, a_codes, b_codes, st);
 }
 
 }  // namespace
@@ -68,14 +449,18 @@ hkv_status hkv_mx_matmul(uint64_t m, uint64_t n, uint64_t k, const uint8_t* a_co
   if (!aligned(a_codes, 16) || !aligned(a_scales, 16) || !aligned(b_codes, 16) ||
       !aligned(b_scales, 16))
     return HKV_ERR_INVALID;
-  cudaStream_t st = static_cast<cudaStream_t>(stream);
-  const dim3 grid(static_cast<unsigned>((n + kTile - 1) / kTile),
-                  static_cast<unsigned>((m + kTile - 1) / kTile));
-  return op_status(with_type(y_type, [&](auto* t) {
-    matmul_kernel<<<grid, 256, 0, st>>>(m, n, k, a_codes, a_scales, b_codes, b_scales,
-                                        static_cast<decltype(t)>(y), y_stride);
-    return cudaGetLastError();
-  }));
+  Problem p{};
+  p.m = m;
+  p.n = n;
+  p.k = k;
+  p.groups = (k + 127) / 128;
+  p.a_scales = a_scales;
+  p.b_scales = b_scales;
+  p.y = y;
+  p.stride = y_stride;
+  p.type = y_type;
+  p.pairs = y_type != HKV_F32 && aligned(y, 4) && y_stride % 2 == 0;
+  return op_status(matmul(p, a_codes, b_codes, static_cast<cudaStream_t>(stream)));
 }
 
 hkv_status hkv_get_wait_timeouts(uint64_t* timeouts_host) {
