@@ -46,11 +46,23 @@ __device__ __forceinline__ uint32_t mx_codes8(const float (&v)[8]) {
   return r;
 }
 
-// Magnitude of an e2m1 code: 0, .5, 1, 1.5, 2, 3, 4, 6, with the sign of bit 3.
-__device__ __forceinline__ float mx_code_value(uint32_t code) {
-  const uint32_t e = (code >> 1) & 3, m = code & 1;
-  const float v = e ? __uint_as_float(((e + 126) << 23) | (m << 22)) : 0.5f * static_cast<float>(m);
-  return code & 8 ? -v : v;
+// The values of eight e2m1 codes, the first in the lowest bits.
+__device__ __forceinline__ void mx_values8(uint32_t codes, float (&v)[8]) {
+  uint32_t h[4];
+  asm("{\n .reg .b8 a, b, c, d;\n"
+      " mov.b32 {a, b, c, d}, %4;\n"
+      " cvt.rn.f16x2.e2m1x2 %0, a;\n"
+      " cvt.rn.f16x2.e2m1x2 %1, b;\n"
+      " cvt.rn.f16x2.e2m1x2 %2, c;\n"
+      " cvt.rn.f16x2.e2m1x2 %3, d;\n}"
+      : "=r"(h[0]), "=r"(h[1]), "=r"(h[2]), "=r"(h[3])
+      : "r"(codes));
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&h[i]));
+    v[2 * i] = f.x;
+    v[2 * i + 1] = f.y;
+  }
 }
 
 }  // namespace hkv

@@ -132,18 +132,6 @@ __device__ __forceinline__ void read_columns(uint32_t tmem, float (&v)[16]) {
   asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
 }
 
-__device__ __forceinline__ float remote_f32(uint32_t addr, uint32_t rank) {
-  uint32_t far;
-  float v;
-  asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(far) : "r"(addr), "r"(rank));
-  asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v) : "r"(far) : "memory");
-  return v;
-}
-__device__ __forceinline__ void cluster_sync() {
-  asm volatile("barrier.cluster.arrive.release.aligned;\n barrier.cluster.wait.acquire.aligned;" ::
-                   : "memory");
-}
-
 __device__ __forceinline__ void store_one(const Problem& p, uint64_t i, uint64_t j, float v) {
   const uint64_t at = i * p.stride + j;
   if (p.type == HKV_F32) static_cast<float*>(p.y)[at] = v;

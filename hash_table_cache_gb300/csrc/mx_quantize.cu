@@ -1,72 +1,211 @@
 // mx_quantize.cu -- hkv_mx_quantize and hkv_mx_dequantize: 4-bit microscaled
 // copies of a matrix's rows and columns, and their values.
+//
+// Both are bound by memory.  A thread block takes a tile of 128 rows by 128
+// columns, which is one 512-byte group of scales in either direction: 16
+// threads read 128 neighbouring columns of a row, 8 each, and every thread
+// has the rows r, r + 32, r + 64 and r + 96 in flight together, because those
+// four rows' scales are 16 neighbouring bytes of the group.  Four threads
+// share a block of 32 and agree on its largest magnitude by two shuffles.
+// For a copy along the columns the tile goes through shared memory as it was
+// read, and four threads take the 128 rows of a column (or of two neighbouring
+// 16-bit columns), so that they write 64 neighbouring bytes of codes; both
+// copies come from one read of x.
 #include "mx.cuh"
 
 namespace hkv {
 namespace {
 
 constexpr int kThreads = 256;
+constexpr int kTile = 128;
 
-// One thread per block of 32 elements, `step` elements apart in x; blocks and
-// rows of the padding get a zero scale byte.
-template <class T>
-__global__ void __launch_bounds__(kThreads)
-    quantize_kernel(uint64_t rows, uint64_t cols, const T* __restrict__ x, uint64_t row_step,
-                    uint64_t col_step, uint8_t* codes, uint8_t* scales) {
-  const uint64_t blocks = (cols + kMxBlock - 1) / kMxBlock, groups = (blocks + 3) / 4;
-  const uint64_t padded_rows = (rows + 127) / 128 * 128;
-  const uint64_t i = static_cast<uint64_t>(blockIdx.x) * kThreads + threadIdx.x;
-  const uint64_t row = row_step == 1 ? i % padded_rows : i / (groups * 4);
-  const uint64_t block = row_step == 1 ? i / padded_rows : i % (groups * 4);
-  if (row >= padded_rows || block >= groups * 4) return;
-  uint32_t byte = 0;
-  if (row < rows && block < blocks) {
-    float v[kMxBlock];
-    uint32_t most = 0;
+// The largest magnitude of eight elements, as float32 bits.
+__device__ __forceinline__ uint32_t most_of(const float (&v)[8]) {
+  uint32_t m = 0;
 #pragma unroll
-    for (int k = 0; k < kMxBlock; ++k) {
-      const uint64_t c = block * kMxBlock + k;
-      v[k] = c < cols ? to_f32(x[row * row_step + c * col_step]) : 0.f;
-      most = max(most, __float_as_uint(v[k]) & 0x7FFFFFFFu);
-    }
-    byte = mx_scale_byte(most);
-    const float inv = mx_inverse(byte);
-    uint4 out;
-    uint32_t* word = &out.x;
-#pragma unroll
-    for (int w = 0; w < 4; ++w) {
-      float u[8];
-#pragma unroll
-      for (int k = 0; k < 8; ++k) u[k] = byte == 255 ? 0.f : v[8 * w + k] * inv;
-      word[w] = mx_codes8(u);
-    }
-    *reinterpret_cast<uint4*>(codes + (row * blocks + block) * 16) = out;
-  }
-  scales[mx_scale_at(row, block, groups)] = static_cast<uint8_t>(byte);
+  for (int i = 0; i < 8; ++i) m = max(m, __float_as_uint(v[i]) & 0x7FFFFFFFu);
+  return m;
 }
 
-// One thread per two elements.
+__device__ __forceinline__ uint32_t encode8(const float (&v)[8], uint32_t byte) {
+  if (byte == 255) return 0;
+  const float inv = mx_inverse(byte);
+  float u[8];
+#pragma unroll
+  for (int i = 0; i < 8; ++i) u[i] = v[i] * inv;
+  return mx_codes8(u);
+}
+
+// One block of 32 elements down a column of the tile: its codes and scale byte.
+__device__ __forceinline__ uint32_t encode32(const float (&v)[32], uint4* codes) {
+  uint32_t most = 0;
+#pragma unroll
+  for (int i = 0; i < 32; ++i) most = max(most, __float_as_uint(v[i]) & 0x7FFFFFFFu);
+  const uint32_t byte = mx_scale_byte(most);
+  uint32_t w[4];
+#pragma unroll
+  for (int g = 0; g < 4; ++g) {
+    float u[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) u[i] = v[8 * g + i];
+    w[g] = encode8(u, byte);
+  }
+  *codes = make_uint4(w[0], w[1], w[2], w[3]);
+  return byte;
+}
+
+template <class T, bool kRowCopy, bool kColCopy>
+__global__ void __launch_bounds__(kThreads)
+    quantize_kernel(uint64_t rows, uint64_t cols, const T* __restrict__ x, uint64_t stride,
+                    int move, uint8_t* codes, uint8_t* scales, uint8_t* codes_t,
+                    uint8_t* scales_t) {
+  // The tile in 32-bit words; word w of a row in the tile's quarter q lies at
+  // w ^ 8q, which spreads the four quarters of a column over the banks.
+  constexpr int kWords = kTile * sizeof(T) / 4;
+  extern __shared__ uint32_t tile[];
+  pdl_trigger();
+  pdl_wait();
+  const uint64_t blocks = (cols + 31) / 32, groups = (cols + 127) / 128;
+  const uint64_t blocks_t = (rows + 31) / 32, groups_t = (rows + 127) / 128;
+  const int tx = threadIdx.x & 15, ty = threadIdx.x >> 4;
+  for (uint64_t t = blockIdx.x; t < groups * groups_t; t += gridDim.x) {
+    const uint64_t tile_c = t % groups, tile_r = t / groups;
+    const uint64_t c = tile_c * kTile + tx * 8;
+    const int valid = c + 8 <= cols ? 8 : c < cols ? static_cast<int>(cols - c) : 0;
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      const int r = ty + 16 * h;
+      Eight<T> e[4];
+#pragma unroll
+      for (int q = 0; q < 4; ++q) {
+        const uint64_t row = tile_r * kTile + r + 32 * q;
+        e[q].load(x + row * stride + c, row < rows ? valid : 0,
+                  valid == 8 && row < rows ? move : kSingly);
+      }
+      if (kColCopy) {
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {
+          uint32_t* line = tile + (r + 32 * q) * kWords;
+#pragma unroll
+          for (int i = 0; i < Eight<T>::kVecs; ++i)
+            *reinterpret_cast<uint4*>(line + ((tx * 4 * Eight<T>::kVecs) ^ (8 * q)) + 4 * i) = e[q].w[i];
+        }
+      }
+      if (kRowCopy) {
+        uint32_t packed[4];
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {
+          float v[8];
+          e[q].to(v);
+          uint32_t most = most_of(v);
+          most = max(most, __shfl_xor_sync(0xFFFFFFFFu, most, 1));
+          most = max(most, __shfl_xor_sync(0xFFFFFFFFu, most, 2));
+          const uint32_t byte = mx_scale_byte(most);
+          const uint32_t code = encode8(v, byte);
+          const uint64_t row = tile_r * kTile + r + 32 * q;
+          if (row < rows && (c >> 5) < blocks)
+            *reinterpret_cast<uint32_t*>(codes + row * blocks * 16 + c / 2) = code;
+          uint32_t word = byte << (8 * (tx >> 2));
+          word |= __shfl_xor_sync(0xFFFFFFFFu, word, 4);
+          word |= __shfl_xor_sync(0xFFFFFFFFu, word, 8);
+          packed[q] = word;
+        }
+        if (tx == 0)
+          *reinterpret_cast<uint4*>(scales + t * 512 + r * 16) =
+              make_uint4(packed[0], packed[1], packed[2], packed[3]);
+      }
+    }
+    if (kColCopy) {
+      __syncthreads();
+      const int q = threadIdx.x & 3;
+      constexpr int kPer = 4 / sizeof(T);  // columns in a word
+      for (int w = threadIdx.x >> 2; w < kWords; w += kThreads / 4) {
+        uint32_t word[32];
+#pragma unroll
+        for (int i = 0; i < 32; ++i) word[i] = tile[(32 * q + i) * kWords + (w ^ (8 * q))];
+#pragma unroll
+        for (int k = 0; k < kPer; ++k) {
+          float v[32];
+#pragma unroll
+          for (int i = 0; i < 32; ++i) v[i] = to_f32(reinterpret_cast<const T*>(&word[i])[k]);
+          uint4 out;
+          const uint32_t byte = encode32(v, &out);
+          const uint64_t col = tile_c * kTile + w * kPer + k, block = tile_r * 4 + q;
+          if (col < cols && block < blocks_t)
+            *reinterpret_cast<uint4*>(codes_t + (col * blocks_t + block) * 16) = out;
+          uint32_t packed = byte << (8 * q);
+          packed |= __shfl_xor_sync(0xFFFFFFFFu, packed, 1);
+          packed |= __shfl_xor_sync(0xFFFFFFFFu, packed, 2);
+          if (q == 0)
+            *reinterpret_cast<uint32_t*>(scales_t + mx_scale_at(col, block, groups_t)) = packed;
+        }
+      }
+      __syncthreads();
+    }
+  }
+}
+
 template <class T>
 __global__ void __launch_bounds__(kThreads)
     dequantize_kernel(uint64_t rows, uint64_t cols, const uint8_t* __restrict__ codes,
-                      const uint8_t* __restrict__ scales, T* y, uint64_t stride) {
-  const uint64_t blocks = (cols + kMxBlock - 1) / kMxBlock, groups = (blocks + 3) / 4;
-  const uint64_t i = static_cast<uint64_t>(blockIdx.x) * kThreads + threadIdx.x;
-  const uint64_t row = i / (blocks * 16), c = i % (blocks * 16) * 2;
-  if (row >= rows) return;
-  const float s = mx_scale_value(scales[mx_scale_at(row, c / kMxBlock, groups)]);
-  const uint32_t two = codes[row * blocks * 16 + c / 2];
-  if (c < cols) y[row * stride + c] = from_f32<T>(mx_code_value(two & 15) * s);
-  if (c + 1 < cols) y[row * stride + c + 1] = from_f32<T>(mx_code_value(two >> 4) * s);
+                      const uint8_t* __restrict__ scales, T* y, uint64_t stride, int move) {
+  pdl_trigger();
+  pdl_wait();
+  const uint64_t blocks = (cols + 31) / 32, groups = (cols + 127) / 128;
+  const int tx = threadIdx.x & 15, ty = threadIdx.x >> 4;
+  const uint64_t tiles = groups * ((rows + 127) / 128);
+  for (uint64_t t = blockIdx.x; t < tiles; t += gridDim.x) {
+    const uint64_t c = t % groups * kTile + tx * 8, row0 = t / groups * kTile;
+    if (c >= cols) continue;
+    const int valid = c + 8 <= cols ? 8 : static_cast<int>(cols - c);
+    uint32_t code[8];
+    uint4 scale[2];
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      scale[h] = ld_nc_v4(scales + t * 512 + (ty + 16 * h) * 16);
+#pragma unroll
+      for (int q = 0; q < 4; ++q) {
+        const uint64_t row = row0 + ty + 16 * h + 32 * q;
+        code[4 * h + q] = row < rows ? __ldg(reinterpret_cast<const uint32_t*>(
+                                           codes + row * blocks * 16 + c / 2))
+                                     : 0;
+      }
+    }
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      const uint64_t row = row0 + ty + 16 * (i >> 2) + 32 * (i & 3);
+      if (row >= rows) continue;
+      const uint32_t four = reinterpret_cast<const uint32_t*>(&scale[i >> 2])[i & 3];
+      const float s = mx_scale_value(four >> (8 * (tx >> 2)) & 255);
+      float v[8];
+      mx_values8(code[i], v);
+#pragma unroll
+      for (int k = 0; k < 8; ++k) v[k] *= s;
+      Eight<T> e;
+      e.from(v);
+      e.store(y + row * stride + c, valid, valid == 8 ? move : kSingly);
+    }
+  }
 }
 
-template <class T>
-cudaError_t quantize(uint64_t rows, uint64_t cols, const T* x, uint64_t row_step,
-                     uint64_t col_step, uint8_t* codes, uint8_t* scales, cudaStream_t st) {
-  const uint64_t threads = (rows + 127) / 128 * 128 * ((cols + 127) / 128 * 4);
-  quantize_kernel<T><<<static_cast<unsigned>((threads + kThreads - 1) / kThreads), kThreads, 0, st>>>(
-      rows, cols, x, row_step, col_step, codes, scales);
-  return cudaGetLastError();
+unsigned tile_grid(uint64_t rows, uint64_t cols) {
+  const uint64_t tiles = ((rows + 127) / 128) * ((cols + 127) / 128);
+  return static_cast<unsigned>(tiles < 0x7FFFFFFF ? tiles : 0x7FFFFFFF);
+}
+
+template <class T, bool kRowCopy, bool kColCopy>
+cudaError_t quantize(uint64_t rows, uint64_t cols, const T* x, uint64_t stride, uint8_t* codes,
+                     uint8_t* scales, uint8_t* codes_t, uint8_t* scales_t, cudaStream_t st) {
+  const int move = widest<T>(x, stride * sizeof(T));
+  const size_t smem = kColCopy ? kTile * kTile * sizeof(T) : 0;
+  auto* kernel = quantize_kernel<T, kRowCopy, kColCopy>;
+  if (smem > 48 * 1024) {
+    cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                         static_cast<int>(smem));
+    if (e != cudaSuccess) return e;
+  }
+  return launch_chained(kernel, tile_grid(rows, cols), kThreads, smem, st, rows, cols, x, stride,
+                        move, codes, scales, codes_t, scales_t);
 }
 
 bool shape_ok(uint64_t rows, uint64_t cols, uint64_t stride, int type) {
@@ -91,11 +230,12 @@ hkv_status hkv_mx_quantize(uint64_t rows, uint64_t cols, const void* x, int x_ty
     return HKV_ERR_INVALID;
   cudaStream_t st = static_cast<cudaStream_t>(stream);
   return op_status(with_type(x_type, [&](auto* t) {
-    auto* in = static_cast<decltype(t)>(const_cast<void*>(x));
-    cudaError_t e = cudaSuccess;
-    if (codes) e = quantize(rows, cols, in, x_stride, 1, codes, scales, st);
-    if (e == cudaSuccess && codes_t) e = quantize(cols, rows, in, 1, x_stride, codes_t, scales_t, st);
-    return e;
+    using T = std::remove_pointer_t<decltype(t)>;
+    const T* in = static_cast<const T*>(x);
+    return (!codes_t ? quantize<T, true, false>
+            : !codes ? quantize<T, false, true>
+                     : quantize<T, true, true>)(rows, cols, in, x_stride, codes, scales, codes_t,
+                                                scales_t, st);
   }));
 }
 
@@ -109,11 +249,11 @@ hkv_status hkv_mx_dequantize(uint64_t rows, uint64_t cols, const uint8_t* codes,
       !aligned(y, type_size(y_type)))
     return HKV_ERR_INVALID;
   cudaStream_t st = static_cast<cudaStream_t>(stream);
-  const uint64_t threads = rows * ((cols + 31) / 32) * 16;
   return op_status(with_type(y_type, [&](auto* t) {
-    dequantize_kernel<<<static_cast<unsigned>((threads + kThreads - 1) / kThreads), kThreads, 0, st>>>(
-        rows, cols, codes, scales, static_cast<decltype(t)>(y), y_stride);
-    return cudaGetLastError();
+    using T = std::remove_pointer_t<decltype(t)>;
+    return launch_chained(dequantize_kernel<T>, tile_grid(rows, cols), kThreads, 0, st, rows, cols,
+                          codes, scales, static_cast<T*>(y), y_stride,
+                          widest<T>(y, y_stride * sizeof(T)));
   }));
 }
 
