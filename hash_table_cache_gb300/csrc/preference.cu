@@ -1,5 +1,13 @@
 // preference.cu -- hkv_preference_loss and hkv_preference_loss_backward: the
 // logistic loss of paired log ratios, from logits, and its gradient.
+//
+// The logits are what costs: the forward call reads them once, keeping a
+// running maximum and the sum of exponentials relative to it (one pass over
+// a row, no second one for the maximum), and the backward call reads and
+// writes once.  A hidden token's row is not read.  Rows are taken by a warp
+// or by a block, depending on their length; a few long rows are shared by
+// the blocks of a cluster, which join their parts through distributed shared
+// memory in a fixed order, so no partial result goes through global memory.
 #include <cmath>
 
 #include "operators.cuh"
@@ -7,89 +15,227 @@
 namespace hkv {
 namespace {
 
-constexpr int kRowThreads = 256;
-constexpr int kPairThreads = 512;
+constexpr int kThreads = 256;
+constexpr int kPairThreads = 256;
+constexpr int kUnroll = 4;      // 16-byte loads in flight per thread
+constexpr int kMaxParts = 8;    // blocks of a cluster that share a row
 
-// Joins a running maximum and the sum of exp(x - maximum) with another pair.
-// An empty or all -inf part has m = -inf and s = 0.
-__device__ __forceinline__ void join(float& m, float& s, float m2, float s2) {
-  const float top = fmaxf(m, m2);
-  const float a = m == top ? 1.f : __expf(m - top);
-  const float b = m2 == top ? 1.f : __expf(m2 - top);
-  s = s * a + s2 * b;
-  m = top;
+// Neighbouring elements in 16 bytes.
+template <class T>
+struct Chunk {
+  static constexpr int kN = 16 / sizeof(T);
+  uint4 w;
+  __device__ __forceinline__ float at(int i) const {
+    return to_f32(reinterpret_cast<const T*>(&w)[i]);
+  }
+};
+template <class T>
+__device__ __forceinline__ uint32_t to_boundary(const T* p, uint64_t n) {
+  const uint32_t head = (16 - reinterpret_cast<uintptr_t>(p) % 16) % 16 / sizeof(T);
+  return n < head ? static_cast<uint32_t>(n) : head;
 }
 
-// A row's log-sum-exp in one pass, and its label's log probability.
+// A running maximum m and s = sum exp(x - m).  Nothing seen, or only -inf:
+// m = -inf, s = 0.  A NaN or +inf among the values makes s NaN.
+struct Running {
+  float m = -INFINITY, s = 0.f;
+
+  // Raises the maximum to that of the next values, and returns what to
+  // subtract from them (0 while all are -inf: their exponentials are 0).
+  __device__ __forceinline__ float raise(float top) {
+    if (top > m) {
+      s *= __expf(m - top);
+      m = top;
+    }
+    return m == -INFINITY ? 0.f : m;
+  }
+  __device__ __forceinline__ void one(float x) {
+    const float base = raise(x);
+    s += __expf(x - base);
+  }
+  __device__ __forceinline__ void join(float m2, float s2) {
+    const float top = fmaxf(m, m2);
+    s = (m == top ? s : s * __expf(m - top)) + (m2 == top ? s2 : s2 * __expf(m2 - top));
+    m = top;
+  }
+  __device__ __forceinline__ float log_sum() const {
+    return m == -INFINITY && s == 0.f ? -INFINITY : m + logf(s);
+  }
+};
+
+// One thread's share of a row of n elements, taken by kLanes threads.
+template <class T, int kLanes>
+__device__ __forceinline__ Running row_pass(const T* x, uint64_t n, int lane) {
+  Running r;
+  const uint32_t head = to_boundary(x, n);
+  if (lane < static_cast<int>(head)) r.one(to_f32(x[lane]));
+  constexpr int kN = Chunk<T>::kN;
+  const T* body = x + head;
+  const uint64_t chunks = (n - head) / kN;
+  auto take = [&](const Chunk<T>* c, int count) {
+    float top = -INFINITY;
+#pragma unroll
+    for (int u = 0; u < count; ++u)
+#pragma unroll
+      for (int i = 0; i < kN; ++i) top = fmaxf(top, c[u].at(i));
+    const float base = r.raise(top);
+    float part[2] = {};
+#pragma unroll
+    for (int u = 0; u < count; ++u)
+#pragma unroll
+      for (int i = 0; i < kN; ++i) part[i & 1] += __expf(c[u].at(i) - base);
+    r.s += part[0] + part[1];
+  };
+  uint64_t k = lane;
+  for (; k + (kUnroll - 1) * kLanes < chunks; k += kUnroll * kLanes) {
+    Chunk<T> c[kUnroll];
+#pragma unroll
+    for (int u = 0; u < kUnroll; ++u) c[u].w = ld_stream_v4(body + (k + u * kLanes) * kN);
+    take(c, kUnroll);
+  }
+  for (; k < chunks; k += kLanes) {
+    Chunk<T> c;
+    c.w = ld_stream_v4(body + k * kN);
+    take(&c, 1);
+  }
+  const uint64_t tail = head + chunks * kN + lane;
+  if (tail < n) r.one(to_f32(x[tail]));
+  return r;
+}
+
+__device__ __forceinline__ bool counts(int64_t label, uint64_t vocab) {
+  return label >= 0 && static_cast<uint64_t>(label) < vocab;
+}
+
+__device__ __forceinline__ Running join_lanes(Running r) {
+  for (int o = 16; o > 0; o >>= 1)
+    r.join(__shfl_xor_sync(0xFFFFFFFFu, r.m, o), __shfl_xor_sync(0xFFFFFFFFu, r.s, o));
+  return r;
+}
+
 template <class T>
-__global__ void __launch_bounds__(kRowThreads)
-    row_kernel(uint64_t vocab, const T* __restrict__ logits, uint64_t stride,
-               const int64_t* __restrict__ labels, float* logps, float* lse, float* row_grad,
-               int32_t* row_pair) {
-  __shared__ float ms[kRowThreads / 32], ss[kRowThreads / 32];
-  const uint64_t t = blockIdx.x;
+__device__ __forceinline__ void finish_row(const Running& r, const T* x, uint64_t t, int64_t label,
+                                           float* logps, float* lse) {
+  const float l = r.log_sum();
+  lse[t] = l;
+  logps[t] = to_f32(x[label]) - l;
+}
+
+// A warp per row: short rows.
+template <class T>
+__global__ void __launch_bounds__(kThreads)
+    short_rows_kernel(uint64_t rows, uint64_t vocab, const T* __restrict__ logits, uint64_t stride,
+                      const int64_t* __restrict__ labels, float* logps, float* lse,
+                      float* row_grad, int32_t* row_pair) {
+  pdl_trigger();
+  pdl_wait();
+  const uint64_t t = static_cast<uint64_t>(blockIdx.x) * (kThreads / 32) + threadIdx.x / 32;
+  if (t >= rows) return;
+  const int lane = threadIdx.x & 31;
   const int64_t label = labels[t];
-  const bool counted = label >= 0 && static_cast<uint64_t>(label) < vocab;
-  if (threadIdx.x == 0) {
+  if (lane == 0) {
     row_grad[t] = 0.f;
     row_pair[t] = -1;
-    if (!counted) logps[t] = lse[t] = 0.f;
   }
-  if (!counted) return;
   const T* x = logits + t * stride;
-  float m = -INFINITY, s = 0.f;
-  for (uint64_t v = threadIdx.x; v < vocab; v += kRowThreads) {
-    const float f = to_f32(x[v]);
-    if (f > m) {
-      s *= __expf(m - f);
-      m = f;
-    }
-    if (f != -INFINITY) s += __expf(f - m);
+  if (!counts(label, vocab)) {
+    if (lane == 0) logps[t] = lse[t] = 0.f;
+    return;
   }
-  for (int o = 16; o > 0; o >>= 1)
-    join(m, s, __shfl_xor_sync(0xFFFFFFFFu, m, o), __shfl_xor_sync(0xFFFFFFFFu, s, o));
+  const Running r = join_lanes(row_pass<T, 32>(x, vocab, lane));
+  if (lane == 0) finish_row(r, x, t, label, logps, lse);
+}
+
+// A block per row, or the `parts` blocks of a cluster.
+template <class T>
+__global__ void __launch_bounds__(kThreads)
+    long_rows_kernel(uint64_t vocab, const T* __restrict__ logits, uint64_t stride, uint32_t parts,
+                     const int64_t* __restrict__ labels, float* logps, float* lse, float* row_grad,
+                     int32_t* row_pair) {
+  __shared__ float ms[2][kThreads / 32 + 1];  // [maximum or sum][warp, then the block]
+  pdl_trigger();
+  pdl_wait();
+  const uint64_t t = blockIdx.x / parts;
+  const uint32_t part = blockIdx.x % parts;
+  const int64_t label = labels[t];
+  const bool writes = part == 0 && threadIdx.x == 0;
+  if (writes) {
+    row_grad[t] = 0.f;
+    row_pair[t] = -1;
+  }
+  if (!counts(label, vocab)) {
+    if (writes) logps[t] = lse[t] = 0.f;
+    return;  // every block of the cluster
+  }
+  const T* x = logits + t * stride;
+  // parts start at multiples of 64 elements of the row
+  const uint64_t size = ((vocab + parts - 1) / parts + 63) / 64 * 64;
+  const uint64_t lo = min(part * size, vocab), hi = min(lo + size, vocab);
+  Running r = join_lanes(row_pass<T, kThreads>(x + lo, hi - lo, threadIdx.x));
+  const int warp = threadIdx.x >> 5;
   if ((threadIdx.x & 31) == 0) {
-    ms[threadIdx.x >> 5] = m;
-    ss[threadIdx.x >> 5] = s;
+    ms[0][warp] = r.m;
+    ms[1][warp] = r.s;
   }
   __syncthreads();
   if (threadIdx.x == 0) {
-    for (int w = 1; w < kRowThreads / 32; ++w) join(m, s, ms[w], ss[w]);
-    const float l = m + logf(s);
-    lse[t] = l;
-    logps[t] = to_f32(x[label]) - l;
+    for (int w = 1; w < kThreads / 32; ++w) r.join(ms[0][w], ms[1][w]);
+    ms[0][kThreads / 32] = r.m;
+    ms[1][kThreads / 32] = r.s;
   }
+  if (parts > 1) {
+    __syncwarp();
+    cluster_sync();
+    if (writes)
+      for (uint32_t p = 1; p < parts; ++p)
+        r.join(remote_f32(smem_u32(&ms[0][kThreads / 32]), p),
+               remote_f32(smem_u32(&ms[1][kThreads / 32]), p));
+    __syncwarp();
+    cluster_sync();  // the others stay until their parts are read
+  }
+  if (writes) finish_row(r, x, t, label, logps, lse);
 }
 
-// One pair per thread block: the sums of both sequences, the loss, and the
-// loss's slope for each of their tokens.
+// One pair per block: the sums of both sequences, the loss, and the loss's
+// slope for each of their tokens.
 __global__ void __launch_bounds__(kPairThreads)
     pair_kernel(uint64_t pairs, uint64_t rows, uint64_t vocab, const int64_t* __restrict__ labels,
                 const int64_t* __restrict__ offsets, const float* __restrict__ ref, float beta,
                 float smoothing, int average, float* losses, float* ratios,
-                const float* __restrict__ logps, float* row_grad, int32_t* row_pair) {
-  __shared__ float red[kPairThreads / 32];
+                const float* logps, float* row_grad, int32_t* row_pair) {
+  __shared__ float red[kPairThreads / 32 * 4];
+  pdl_trigger();
+  pdl_wait();
   const uint64_t p = blockIdx.x;
-  float r[2], inv[2];
   uint64_t lo[2], hi[2];
+  float sums[4] = {};  // ratio and number of counted tokens, of either side
+#pragma unroll
   for (int side = 0; side < 2; ++side) {
     const uint64_t s = p + side * pairs;
     const int64_t a = offsets[s], b = offsets[s + 1];
-    hi[side] = b <= 0 ? 0 : min(static_cast<uint64_t>(b), rows);
     lo[side] = a <= 0 ? 0 : min(static_cast<uint64_t>(a), rows);
-    float sum = 0.f, count = 0.f;
+    hi[side] = b <= 0 ? 0 : min(static_cast<uint64_t>(b), rows);
+  }
+#pragma unroll
+  for (int side = 0; side < 2; ++side)
+#pragma unroll 4
     for (uint64_t t = lo[side] + threadIdx.x; t < hi[side]; t += kPairThreads) {
-      const int64_t label = labels[t];
-      if (label < 0 || static_cast<uint64_t>(label) >= vocab) continue;
-      sum += logps[t] - (ref ? ref[t] : 0.f);
-      count += 1.f;
+      const float lp = logps[t], re = ref ? ref[t] : 0.f;
+      if (counts(labels[t], vocab)) {
+        sums[2 * side] += lp - re;
+        sums[2 * side + 1] += 1.f;
+      }
     }
-    sum = block_sum(sum, red);
-    count = block_sum(count, red);
-    inv[side] = average ? (count > 0.f ? 1.f / count : 0.f) : 1.f;
-    r[side] = average ? sum * inv[side] : sum;
+  block_sums(sums, red);
+  float r[2], inv[2];
+#pragma unroll
+  for (int side = 0; side < 2; ++side) {
+    const float n = sums[2 * side + 1];
+    inv[side] = average ? (n > 0.f ? 1.f / n : 0.f) : 1.f;
+    r[side] = average ? sums[2 * side] * inv[side] : sums[2 * side];
   }
   const float h = beta * (r[0] - r[1]);
+  // a side with weight 0 is left out: its logarithm may be infinite
   const float tail = log1pf(expf(-fabsf(h)));
   float loss = 0.f, slope = 0.f;
   if (smoothing < 1.f) {
@@ -107,36 +253,85 @@ __global__ void __launch_bounds__(kPairThreads)
     ratios[p] = r[0];
     ratios[pairs + p] = r[1];
   }
+#pragma unroll
   for (int side = 0; side < 2; ++side) {
     const float g = (side ? -slope : slope) * inv[side];
+#pragma unroll 4
     for (uint64_t t = lo[side] + threadIdx.x; t < hi[side]; t += kPairThreads) {
-      const int64_t label = labels[t];
       row_pair[t] = static_cast<int32_t>(p);
-      if (label >= 0 && static_cast<uint64_t>(label) < vocab) row_grad[t] = g;
+      if (counts(labels[t], vocab)) row_grad[t] = g;
     }
   }
 }
 
+// A piece of a row per block: kUnroll chunks of 16 bytes per thread.  Rows run
+// from the last to the first, so that what the forward call read last is
+// taken from L2 while it is there.
 template <class T>
-__global__ void __launch_bounds__(kRowThreads)
-    backward_kernel(uint64_t pairs, uint64_t vocab, const T* logits, uint64_t stride,
-                    const int64_t* __restrict__ labels, const float* __restrict__ lse,
-                    const float* __restrict__ row_grad, const int32_t* __restrict__ row_pair,
-                    const float* __restrict__ dlosses, T* dlogits, uint64_t dstride) {
-  const uint64_t t = blockIdx.x;
-  const int64_t label = labels[t];
-  const int32_t p = row_pair[t];
-  T* d = dlogits + t * dstride;
-  if (p < 0 || static_cast<uint64_t>(p) >= pairs || label < 0 ||
-      static_cast<uint64_t>(label) >= vocab) {
-    for (uint64_t v = threadIdx.x; v < vocab; v += kRowThreads) d[v] = from_f32<T>(0.f);
-    return;
-  }
-  const float g = row_grad[t] * (dlosses ? dlosses[p] : 1.f), l = lse[t];
-  const T* x = logits + t * stride;
-  for (uint64_t v = threadIdx.x; v < vocab; v += kRowThreads) {
-    const float hit = v == static_cast<uint64_t>(label) ? 1.f : 0.f;
-    d[v] = from_f32<T>(g * (hit - __expf(to_f32(x[v]) - l)));
+__global__ void __launch_bounds__(kThreads)
+    backward_kernel(uint64_t pairs, uint64_t rows, uint64_t vocab, const T* logits, uint64_t stride,
+                    uint64_t pieces, const int64_t* __restrict__ labels,
+                    const float* __restrict__ lse, const float* __restrict__ row_grad,
+                    const int32_t* __restrict__ row_pair, const float* __restrict__ dlosses,
+                    T* dlogits, uint64_t dstride) {
+  constexpr int kN = Chunk<T>::kN;
+  constexpr uint64_t kPiece = kThreads * kUnroll * kN;
+  pdl_trigger();
+  pdl_wait();
+  for (uint64_t b = blockIdx.x; b < rows * pieces; b += gridDim.x) {
+    const uint64_t t = rows - 1 - b / pieces, lo = b % pieces * kPiece;
+    const int64_t label = labels[t];
+    const int32_t p = row_pair[t];
+    const bool counted = p >= 0 && static_cast<uint64_t>(p) < pairs && counts(label, vocab);
+    const float g = counted ? row_grad[t] * (dlosses ? dlosses[p] : 1.f) : 0.f;
+    const float l = counted ? lse[t] : 0.f;
+    const uint64_t hit = counted && static_cast<uint64_t>(label) >= lo
+                             ? static_cast<uint64_t>(label) - lo : ~0ull;
+    const T* x = logits + t * stride + lo;
+    T* d = dlogits + t * dstride + lo;
+    const uint64_t n = min(vocab - lo, kPiece);
+    auto value = [&](float v, uint64_t at) {
+      const float soft = __expf(v - l);
+      return at == hit ? g * (1.f - soft) : -g * soft;
+    };
+    auto one = [&](uint64_t at) { d[at] = from_f32<T>(counted ? value(to_f32(x[at]), at) : 0.f); };
+    const uint32_t head = to_boundary(d, n);
+    if (counted && to_boundary(x, n) != head) {  // the two lie differently: one by one
+      for (uint64_t k = threadIdx.x; k < n; k += kThreads) one(k);
+      continue;
+    }
+    if (threadIdx.x < head) one(threadIdx.x);
+    const uint32_t chunks = static_cast<uint32_t>((n - head) / kN);
+    uint4 w[kUnroll];
+#pragma unroll
+    for (int u = 0; u < kUnroll; ++u) {
+      const uint32_t k = threadIdx.x + u * kThreads;
+      if (counted && k < chunks) w[u] = __ldcs(reinterpret_cast<const uint4*>(x + head + k * kN));
+    }
+#pragma unroll
+    for (int u = 0; u < kUnroll; ++u) {
+      const uint32_t k = threadIdx.x + u * kThreads;
+      if (k >= chunks) break;
+      Chunk<T> out;
+      T* e = reinterpret_cast<T*>(&out.w);
+      if (!counted) {
+        out.w = make_uint4(0, 0, 0, 0);
+      } else {
+        Chunk<T> in;
+        in.w = w[u];
+        const uint64_t at = head + k * kN;
+        if (hit - at < kN) {
+#pragma unroll
+          for (int i = 0; i < kN; ++i) e[i] = from_f32<T>(value(in.at(i), at + i));
+        } else {
+#pragma unroll
+          for (int i = 0; i < kN; ++i) e[i] = from_f32<T>(-g * __expf(in.at(i) - l));
+        }
+      }
+      st_stream_v4(d + head + k * kN, out.w);
+    }
+    const uint64_t tail = head + static_cast<uint64_t>(chunks) * kN + threadIdx.x;
+    if (tail < n) one(tail);
   }
 }
 
@@ -145,6 +340,38 @@ bool logits_ok(uint64_t pairs, uint64_t rows, uint64_t vocab, const void* logits
   return pairs <= HKV_MAX_BATCH / 2 && rows <= HKV_MAX_BATCH && vocab >= 1 &&
          vocab <= HKV_MAX_BATCH && type_ok(type) && stride >= vocab &&
          (rows == 0 || (logits && aligned(logits, type_size(type))));
+}
+
+template <class T>
+cudaError_t forward_rows(uint64_t rows, uint64_t vocab, const T* logits, uint64_t stride,
+                         const int64_t* labels, float* logps, float* lse, float* row_grad,
+                         int32_t* row_pair, cudaStream_t st) {
+  const uint64_t sms = sm_count();
+  // a warp takes a row while that row is a few rounds of its loads
+  if (vocab * sizeof(T) <= 4096)
+    return launch_chained(short_rows_kernel<T>, static_cast<unsigned>((rows + 7) / 8), kThreads, 0,
+                          st, rows, vocab, logits, stride, labels, logps, lse, row_grad, row_pair);
+  // few rows: clusters share them while there is room on the SMs and a part
+  // keeps a round of its block's loads
+  uint32_t parts = 1;
+  while (parts < kMaxParts && rows * parts <= sms &&
+         vocab * sizeof(T) >= 2ull * parts * kThreads * kUnroll * 16)
+    parts *= 2;
+  if (rows > 0x7FFFFFFFull / parts) return cudaErrorInvalidValue;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(static_cast<unsigned>(rows * parts));
+  cfg.blockDim = dim3(kThreads);
+  cfg.stream = st;
+  cudaLaunchAttribute attr[2];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  attr[1].id = cudaLaunchAttributeClusterDimension;
+  attr[1].val.clusterDim.x = parts;
+  attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = parts > 1 ? 2 : 1;
+  return cudaLaunchKernelEx(&cfg, long_rows_kernel<T>, vocab, logits, stride, parts, labels, logps,
+                            lse, row_grad, row_pair);
 }
 
 }  // namespace
@@ -172,17 +399,14 @@ hkv_status hkv_preference_loss(uint64_t pairs, uint64_t rows, uint64_t vocab, co
   cudaError_t e = cudaSuccess;
   if (rows)
     e = with_type(type, [&](auto* t) {
-      row_kernel<<<static_cast<unsigned>(rows), kRowThreads, 0, st>>>(
-          vocab, static_cast<decltype(t)>(const_cast<void*>(logits)), stride, labels, logps, lse,
-          row_grad, row_pair);
-      return cudaGetLastError();
+      using T = std::remove_pointer_t<decltype(t)>;
+      return forward_rows(rows, vocab, static_cast<const T*>(logits), stride, labels, logps, lse,
+                          row_grad, row_pair, st);
     });
-  if (e == cudaSuccess && pairs) {
-    pair_kernel<<<static_cast<unsigned>(pairs), kPairThreads, 0, st>>>(
-        pairs, rows, vocab, labels, offsets, ref_logps, beta, label_smoothing, average, losses,
-        ratios, logps, row_grad, row_pair);
-    e = cudaGetLastError();
-  }
+  if (e == cudaSuccess && pairs)
+    e = launch_chained(pair_kernel, static_cast<unsigned>(pairs), kPairThreads, 0, st, pairs, rows,
+                       vocab, labels, offsets, ref_logps, beta, label_smoothing, average, losses,
+                       ratios, logps, row_grad, row_pair);
   return op_status(e);
 }
 
@@ -204,11 +428,13 @@ hkv_status hkv_preference_loss_backward(uint64_t pairs, uint64_t rows, uint64_t 
     return HKV_ERR_INVALID;
   cudaStream_t st = static_cast<cudaStream_t>(stream);
   return op_status(with_type(type, [&](auto* t) {
-    using P = decltype(t);
-    backward_kernel<<<static_cast<unsigned>(rows), kRowThreads, 0, st>>>(
-        pairs, vocab, static_cast<P>(const_cast<void*>(logits)), stride, labels, lse, row_grad,
-        row_pair, dlosses, static_cast<P>(dlogits), dstride);
-    return cudaGetLastError();
+    using T = std::remove_pointer_t<decltype(t)>;
+    constexpr uint64_t kPiece = kThreads * kUnroll * Chunk<T>::kN;
+    const uint64_t pieces = (vocab + kPiece - 1) / kPiece;
+    const uint64_t blocks = rows * pieces < 0x7FFFFFFF ? rows * pieces : 0x7FFFFFFF;
+    return launch_chained(backward_kernel<T>, static_cast<unsigned>(blocks), kThreads, 0, st, pairs,
+                          rows, vocab, static_cast<const T*>(logits), stride, pieces, labels, lse,
+                          row_grad, row_pair, dlosses, static_cast<T*>(dlogits), dstride);
   }));
 }
 
