@@ -1,11 +1,15 @@
 // clip.cu -- hkv_clip_grad_norm: the norm of many gradients taken as one
 // vector, and clipping to it.
 //
-// The gradients are cut into chunks of one size; a fixed grid of thread
-// blocks takes the chunks in turn and leaves one partial sum of squares per
-// block, so the sum's order depends on the sizes alone.  The second kernel
-// adds the partials again in every block (a few hundred floats) instead of
-// in a kernel of its own, and scales.
+// Bound by memory: the gradients are read once for the norm and once more,
+// and written, where they are clipped.  They are cut into chunks of one size
+// that a fixed number of thread blocks share evenly, each a run of
+// neighbouring chunks, and every block leaves one partial sum of squares: the
+// order of the sum depends on the sizes alone.  The second kernel adds the
+// partials again in every block (a few hundred floats) instead of in a launch
+// of its own, and takes each run from its end, where the first kernel left
+// off and L2 still holds it.
+#include <algorithm>
 #include <cmath>
 
 #include "operators.cuh"
@@ -14,6 +18,7 @@ namespace hkv {
 namespace {
 
 constexpr int kThreads = 512;
+constexpr int kUnroll = 4;  // groups of eight elements in flight per thread
 constexpr int kMaxPartials = HKV_CLIP_WORK_BYTES / 4;
 
 // One launch's gradients, passed as a kernel argument (no copy to the device
@@ -28,19 +33,8 @@ struct Batch {
   Entry e[N];
   uint32_t first[N + 1];  // number of chunks before entry i
   uint32_t count;
-  uint64_t chunk;         // elements of a chunk
+  uint32_t chunk;         // elements of a chunk
 };
-
-template <int N>
-__device__ __forceinline__ uint32_t entry_of(const Batch<N>& b, uint32_t c) {
-  uint32_t lo = 0, hi = b.count - 1;
-  while (lo < hi) {
-    const uint32_t mid = (lo + hi + 1) / 2;
-    if (b.first[mid] <= c) lo = mid;
-    else hi = mid - 1;
-  }
-  return lo;
-}
 
 template <class F>
 __device__ __forceinline__ void for_type(uint32_t type, F&& f) {
@@ -49,26 +43,89 @@ __device__ __forceinline__ void for_type(uint32_t type, F&& f) {
   else f(static_cast<__half*>(nullptr));
 }
 
+// The chunks of this block, lo .. hi - 1, by calls of f(entry, first element,
+// number of elements); from the last to the first if kBackwards.
+template <bool kBackwards, int N, class F>
+__device__ __forceinline__ void for_chunks(const Batch<N>& b, F&& f) {
+  const uint64_t chunks = b.count ? b.first[b.count] : 0;
+  const uint32_t lo = chunks * blockIdx.x / gridDim.x, hi = chunks * (blockIdx.x + 1) / gridDim.x;
+  if (lo == hi) return;
+  const uint32_t begin = kBackwards ? hi - 1 : lo;
+  uint32_t i = 0, end = b.count - 1;
+  while (i < end) {  // the entry that holds `begin`
+    const uint32_t mid = (i + end + 1) / 2;
+    if (b.first[mid] <= begin) i = mid;
+    else end = mid - 1;
+  }
+  for (uint32_t k = 0; k < hi - lo; ++k) {
+    const uint32_t c = kBackwards ? hi - 1 - k : lo + k;
+    if (kBackwards) {
+      while (c < b.first[i]) --i;
+    } else {
+      while (c >= b.first[i + 1]) ++i;
+    }
+    const uint64_t n = b.e[i].n_types & ((1ull << 56) - 1);
+    const uint64_t at = static_cast<uint64_t>(c - b.first[i]) * b.chunk;
+    f(b.e[i], at, static_cast<uint32_t>(min(n - at, static_cast<uint64_t>(b.chunk))));
+  }
+}
+
+// Elements up to the first place from which both arrays take whole moves of
+// eight, or -1 where there is none.
+template <class T, class U>
+__device__ __forceinline__ int lead(const T* x, const U* y) {
+  const uint32_t a = (reinterpret_cast<uintptr_t>(x) / sizeof(T)) & 7;
+  const uint32_t b = (reinterpret_cast<uintptr_t>(y) / sizeof(U)) & 7;
+  return a == b ? static_cast<int>((8 - a) & 7) : -1;
+}
+
 template <int N>
 __global__ void __launch_bounds__(kThreads)
     norm_kernel(const __grid_constant__ Batch<N> b, float* partial, bool more) {
   __shared__ float red[kThreads / 32];
-  float s = 0.f;
-  const uint32_t chunks = b.first[b.count];
-  for (uint32_t c = blockIdx.x; c < chunks; c += gridDim.x) {
-    const uint32_t i = entry_of(b, c);
-    const uint64_t n = b.e[i].n_types & ((1ull << 56) - 1);
-    const uint64_t lo = (c - b.first[i]) * b.chunk, hi = min(lo + b.chunk, n);
-    for_type(b.e[i].n_types >> 56 & 15, [&](auto* t) {
-      const auto* x = static_cast<decltype(t)>(const_cast<void*>(b.e[i].data));
-      for (uint64_t k = lo + threadIdx.x; k < hi; k += kThreads) {
-        const float v = to_f32(x[k]);
-        s = fmaf(v, v, s);
+  pdl_trigger();
+  pdl_wait();
+  float s[2] = {};
+  for_chunks<false>(b, [&](const Entry& e, uint64_t at, uint32_t n) {
+    for_type(e.n_types >> 56 & 15, [&](auto* t) {
+      using T = std::remove_pointer_t<decltype(t)>;
+      const T* x = static_cast<const T*>(e.data) + at;
+      const uint32_t head = min(static_cast<uint32_t>(lead(x, x)), n);
+      if (threadIdx.x < head) {
+        const float v = to_f32(x[threadIdx.x]);
+        s[0] = fmaf(v, v, s[0]);
+      }
+      const uint32_t eights = (n - head) / 8;
+      x += head;
+      auto add = [&](const Eight<T>& in) {
+        float v[8];
+        in.to(v);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) s[i & 1] = fmaf(v[i], v[i], s[i & 1]);
+      };
+      uint32_t k = threadIdx.x;
+      for (; k + (kUnroll - 1) * kThreads < eights; k += kUnroll * kThreads) {
+        Eight<T> in[kUnroll];
+#pragma unroll
+        for (int u = 0; u < kUnroll; ++u) in[u].load(x + (k + u * kThreads) * 8, 8, kWhole);
+#pragma unroll
+        for (int u = 0; u < kUnroll; ++u) add(in[u]);
+      }
+      for (; k < eights; k += kThreads) {
+        Eight<T> in;
+        in.load(x + k * 8, 8, kWhole);
+        add(in);
+      }
+      const uint32_t tail = eights * 8 + threadIdx.x;
+      if (tail < n - head) {
+        const float v = to_f32(x[tail]);
+        s[0] = fmaf(v, v, s[0]);
       }
     });
-  }
-  s = block_sum(s, red);
-  if (threadIdx.x == 0) partial[blockIdx.x] = more ? partial[blockIdx.x] + s : s;
+  });
+  float sum[1] = {s[0] + s[1]};
+  block_sums(sum, red);
+  if (threadIdx.x == 0) partial[blockIdx.x] = more ? partial[blockIdx.x] + sum[0] : sum[0];
 }
 
 template <int N>
@@ -76,48 +133,71 @@ __global__ void __launch_bounds__(kThreads)
     clip_kernel(const __grid_constant__ Batch<N> b, const float* partial, int partials,
                 float max_norm, float* norm_out) {
   __shared__ float red[kThreads / 32];
-  float s = 0.f;
-  for (int k = threadIdx.x; k < partials; k += kThreads) s += partial[k];
-  const float norm = sqrtf(block_sum(s, red));
+  pdl_trigger();
+  pdl_wait();
+  float sum[1] = {};
+  for (int k = threadIdx.x; k < partials; k += kThreads) sum[0] += partial[k];
+  block_sums(sum, red);
+  const float norm = sqrtf(sum[0]);
   if (blockIdx.x == 0 && threadIdx.x == 0) *norm_out = norm;
   const float f = norm <= max_norm ? 1.f : max_norm / norm;
-  const uint32_t chunks = b.count ? b.first[b.count] : 0;
-  for (uint32_t c = blockIdx.x; c < chunks; c += gridDim.x) {
-    const uint32_t i = entry_of(b, c);
-    const Entry& e = b.e[i];
+  for_chunks<true>(b, [&](const Entry& e, uint64_t at, uint32_t n) {
     const uint32_t type = e.n_types >> 56 & 15, out_type = e.n_types >> 60;
-    if (!e.out || (f == 1.f && e.out == e.data && type == out_type)) continue;
-    const uint64_t n = e.n_types & ((1ull << 56) - 1);
-    const uint64_t lo = (c - b.first[i]) * b.chunk, hi = min(lo + b.chunk, n);
+    if (!e.out || (f == 1.f && e.out == e.data && type == out_type)) return;
     for_type(type, [&](auto* t) {
       for_type(out_type, [&](auto* u) {
-        const auto* x = static_cast<decltype(t)>(const_cast<void*>(e.data));
-        auto* y = static_cast<decltype(u)>(e.out);
-        for (uint64_t k = lo + threadIdx.x; k < hi; k += kThreads) {
-          const float v = to_f32(x[k]) * f;
-          y[k] = from_f32<std::remove_pointer_t<decltype(u)>>(v);
+        using T = std::remove_pointer_t<decltype(t)>;
+        using U = std::remove_pointer_t<decltype(u)>;
+        const T* x = static_cast<const T*>(e.data) + at;
+        U* y = static_cast<U*>(e.out) + at;
+        const int ahead = lead(x, y);
+        const uint32_t head = ahead < 0 ? n : min(static_cast<uint32_t>(ahead), n);
+        for (uint32_t k = threadIdx.x; k < head; k += kThreads)
+          y[k] = from_f32<U>(to_f32(x[k]) * f);
+        const uint32_t eights = (n - head) / 8;
+        x += head;
+        y += head;
+        auto scale = [&](const Eight<T>& in, uint32_t k) {
+          float v[8];
+          in.to(v);
+#pragma unroll
+          for (int i = 0; i < 8; ++i) v[i] *= f;
+          Eight<U> out;
+          out.from(v);
+          out.store(y + k * 8, 8, kWhole);
+        };
+        uint32_t k = threadIdx.x;
+        for (; k + (kUnroll - 1) * kThreads < eights; k += kUnroll * kThreads) {
+          Eight<T> in[kUnroll];
+#pragma unroll
+          for (int q = 0; q < kUnroll; ++q) in[q].load_written(x + (k + q * kThreads) * 8);
+#pragma unroll
+          for (int q = 0; q < kUnroll; ++q) scale(in[q], k + q * kThreads);
         }
+        for (; k < eights; k += kThreads) {
+          Eight<T> in;
+          in.load_written(x + k * 8);
+          scale(in, k);
+        }
+        const uint32_t tail = eights * 8 + threadIdx.x;
+        if (tail < n - head) y[tail] = from_f32<U>(to_f32(x[tail]) * f);
       });
     });
-  }
+  });
 }
 
+// Calls f(batch) for the gradients in runs of at most N.
 template <int N, class F>
-cudaError_t for_batches(uint64_t count, const hkv_grad* g, uint64_t chunk, F&& f) {
+cudaError_t for_batches(uint64_t count, const hkv_grad* g, uint32_t chunk, F&& f) {
   Batch<N> b{};
   b.chunk = chunk;
-  auto flush = [&](bool last) {
-    cudaError_t e = f(b, last);
-    b.count = 0;
-    b.first[0] = 0;
-    return e;
-  };
   for (uint64_t i = 0; i < count; ++i) {
     if (g[i].n == 0) continue;
     const uint64_t chunks = (g[i].n + chunk - 1) / chunk;
     if (b.count == N || b.first[b.count] + chunks > 0x7FFFFFFFull) {
-      cudaError_t e = flush(false);
+      cudaError_t e = f(b);
       if (e != cudaSuccess) return e;
+      b.count = 0;
     }
     b.e[b.count] = {g[i].data, g[i].out,
                     g[i].n | static_cast<uint64_t>(g[i].type) << 56 |
@@ -125,30 +205,36 @@ cudaError_t for_batches(uint64_t count, const hkv_grad* g, uint64_t chunk, F&& f
     b.first[b.count + 1] = b.first[b.count] + static_cast<uint32_t>(chunks);
     ++b.count;
   }
-  return flush(true);
+  return f(b);
 }
 
 template <int N>
-cudaError_t clip(uint64_t count, const hkv_grad* g, uint64_t total, float max_norm,
+cudaError_t clip(uint64_t count, const hkv_grad* g, uint64_t total, bool writes, float max_norm,
                  float* norm_out, float* work, cudaStream_t st) {
-  const int grid_max = std::min(kMaxPartials, sm_count() * 4);
-  uint64_t chunk = 4096;
-  while (chunk < 65536 && total / chunk > static_cast<uint64_t>(grid_max) * 4) chunk *= 2;
-  bool more = false;
+  // four blocks of 512 threads fill an SM; small totals are cut finer, so
+  // that every SM has some
+  const int grid = std::min(kMaxPartials, sm_count() * 4);
+  uint32_t chunk = 4096;
+  while (chunk < 16384 && total / chunk > static_cast<uint64_t>(grid)) chunk *= 2;
+  auto blocks = [&](const Batch<N>& b) {
+    return std::max(1, static_cast<int>(std::min<uint32_t>(grid, b.count ? b.first[b.count] : 0)));
+  };
   int partials = 0;
-  cudaError_t e = for_batches<N>(count, g, chunk, [&](const Batch<N>& b, bool) {
-    if (!more) partials = std::max(1, std::min<int>(grid_max, b.first[b.count]));
-    if (b.count == 0 && more) return cudaSuccess;
-    norm_kernel<N><<<more ? std::min<int>(partials, b.first[b.count]) : partials, kThreads, 0, st>>>(
-        b, work, more);
-    more = true;
-    return cudaGetLastError();
+  cudaError_t e = for_batches<N>(count, g, chunk, [&](const Batch<N>& b) {
+    // the first launch sets its partials; later ones add to those that are
+    // there, so they keep to its number of blocks
+    const bool more = partials > 0;
+    if (!more) partials = blocks(b);
+    return launch_chained(norm_kernel<N>, std::min(partials, blocks(b)), kThreads, 0, st, b, work,
+                          more);
   });
   if (e != cudaSuccess) return e;
-  return for_batches<N>(count, g, chunk, [&](const Batch<N>& b, bool) {
-    clip_kernel<N><<<std::max(1, std::min<int>(grid_max, b.first[b.count])), kThreads, 0, st>>>(
-        b, work, partials, max_norm, norm_out);
-    return cudaGetLastError();
+  if (!writes)
+    return launch_chained(clip_kernel<1>, 1, kThreads, 0, st, Batch<1>{}, work, partials, max_norm,
+                          norm_out);
+  return for_batches<N>(count, g, chunk, [&](const Batch<N>& b) {
+    return launch_chained(clip_kernel<N>, blocks(b), kThreads, 0, st, b, work, partials, max_norm,
+                          norm_out);
   });
 }
 
@@ -162,18 +248,21 @@ extern "C" hkv_status hkv_clip_grad_norm(uint64_t count, const hkv_grad* grads, 
       !aligned(norm_out, 4) || !aligned(work, 4))
     return HKV_ERR_INVALID;
   uint64_t total = 0;
+  bool writes = false;
   for (uint64_t i = 0; i < count; ++i) {
     const hkv_grad& g = grads[i];
     if (!type_ok(g.type) || (g.out && !type_ok(g.out_type)) || g.n >= 1ull << 40)
       return HKV_ERR_INVALID;
-    if (g.n && (!g.data || !aligned(g.data, type_size(g.type)) ||
-                (g.out && !aligned(g.out, type_size(g.out_type)))))
-      return HKV_ERR_INVALID;
-    if (g.n && g.out == g.data && g.out_type != g.type) return HKV_ERR_INVALID;
+    if (g.n == 0) continue;
+    if (!g.data || !aligned(g.data, type_size(g.type))) return HKV_ERR_INVALID;
+    if (g.out && !aligned(g.out, type_size(g.out_type))) return HKV_ERR_INVALID;
+    if (g.out == g.data && g.out_type != g.type) return HKV_ERR_INVALID;
     total += g.n;
+    writes |= g.out != nullptr;
   }
   cudaStream_t st = static_cast<cudaStream_t>(stream);
   float* w = static_cast<float*>(work);
-  return op_status(count <= 64 ? clip<64>(count, grads, total, max_norm, norm_out, w, st)
-                               : clip<1024>(count, grads, total, max_norm, norm_out, w, st));
+  return op_status(
+      count <= 64 ? clip<64>(count, grads, total, writes, max_norm, norm_out, w, st)
+                  : clip<1024>(count, grads, total, writes, max_norm, norm_out, w, st));
 }
