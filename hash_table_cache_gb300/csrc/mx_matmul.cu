@@ -23,7 +23,8 @@ __device__ unsigned long long g_wait_timeouts;
 constexpr int kRows = 128;       // rows of B per tile
 constexpr int kStepBytes = 128;  // bytes of codes per row and step: 256 columns
 constexpr int kStep = 256;
-constexpr int kThreads = 192;    // warp 0 loads, warp 1 multiplies, warps 2-5 store
+constexpr int kStoreWarps = 8;   // two for each quarter of the TMEM lanes
+constexpr int kThreads = 64 + 32 * kStoreWarps;  // warp 0 loads, warp 1 multiplies, the others store
 constexpr int kMaxSplits = 8;
 constexpr unsigned kSmemLimit = 232448 - 1024;  // 227 KB less the alignment of the stages
 
@@ -138,8 +139,9 @@ __device__ __forceinline__ void store_one(const Problem& p, uint64_t i, uint64_t
   else if (p.type == HKV_BF16) static_cast<__nv_bfloat16*>(p.y)[at] = __float2bfloat16_rn(v);
   else static_cast<__half*>(p.y)[at] = __float2half_rn(v);
 }
-__device__ __forceinline__ uint32_t pack2(float lo, float hi, int type) {
-  if (type == HKV_BF16) {
+template <bool kBf16>
+__device__ __forceinline__ uint32_t pack2(float lo, float hi) {
+  if constexpr (kBf16) {
     const __nv_bfloat162 h = __floats2bfloat162_rn(lo, hi);
     return *reinterpret_cast<const uint32_t*>(&h);
   }
@@ -147,34 +149,68 @@ __device__ __forceinline__ uint32_t pack2(float lo, float hi, int type) {
   return *reinterpret_cast<const uint32_t*>(&h);
 }
 
-// Sixteen accumulator columns (rows i .. i + 15 of y) of this lane's column j.
-__device__ __forceinline__ void store_columns(const Problem& p, uint64_t i, uint64_t j,
-                                              const float (&v)[16]) {
-  if (!p.pairs) {
-    if (j < p.n)
-#pragma unroll
-      for (int c = 0; c < 16; ++c)
-        if (i + c < p.m) store_one(p, i + c, j, v[c]);
-    return;
-  }
-  // neighbouring lanes trade values, so that an even lane stores both of
-  // their columns for one row and the odd lane for the next: 4-byte stores
-  const bool odd = threadIdx.x & 1;
-  const uint64_t je = j & ~1ull;
+// Sixteen accumulator columns (rows i .. i + 15 of y, all of them in y) of
+// this lane's column j of a 16-bit y: neighbouring lanes trade values, so
+// that an even lane stores both lanes' columns of one row and the odd lane
+// those of the next, 4 bytes at a time.
+template <bool kBf16>
+__device__ __forceinline__ void store_pairs(const Problem& p, uint64_t i, uint64_t j,
+                                            const float (&v)[16]) {
+  const uint32_t odd = j & 1, pick = odd ? 0x3276 : 0x5410;
+  const uint64_t step = 4 * p.stride;
+  char* y = static_cast<char*>(p.y) + ((i + odd) * p.stride + (j & ~1ull)) * 2;
 #pragma unroll
   for (int c = 0; c < 16; c += 2) {
-    const float got = __shfl_xor_sync(0xFFFFFFFFu, odd ? v[c] : v[c + 1], 1);
-    const float lo = odd ? got : v[c], hi = odd ? v[c + 1] : got;
-    const uint64_t row = i + c + odd;
-    if (row < p.m) {
-      if (je + 1 < p.n)
-        *reinterpret_cast<uint32_t*>(static_cast<uint16_t*>(p.y) + row * p.stride + je) =
-            pack2(lo, hi, p.type);
-      else if (je < p.n)
-        store_one(p, row, je, lo);
-    }
+    const uint32_t own = pack2<kBf16>(v[c], v[c + 1]);
+    const uint32_t other = __shfl_xor_sync(0xFFFFFFFFu, own, 1);
+    *reinterpret_cast<uint32_t*>(y) = __byte_perm(own, other, pick);
+    y += step;
   }
 }
+
+// Sixteen accumulator columns of this lane's column j.
+__device__ __forceinline__ void store_columns(const Problem& p, uint64_t i, uint64_t j,
+                                              const float (&v)[16]) {
+  // a whole warp's columns lie in y, and all sixteen rows
+  const bool inside = i + 16 <= p.m && (j | 31) < p.n;
+  if (inside && p.pairs) {
+    if (p.type == HKV_BF16) store_pairs<true>(p, i, j, v);
+    else store_pairs<false>(p, i, j, v);
+  } else if (inside && p.type == HKV_F32) {
+    char* y = reinterpret_cast<char*>(static_cast<float*>(p.y) + i * p.stride + j);
+#pragma unroll
+    for (int c = 0; c < 16; ++c) {
+      *reinterpret_cast<float*>(y) = v[c];
+      y += 4 * p.stride;
+    }
+  } else if (j < p.n) {
+#pragma unroll
+    for (int c = 0; c < 16; ++c)
+      if (i + c < p.m) store_one(p, i + c, j, v[c]);
+  }
+}
+
+// The tiles of a block: every `step`-th from `first`, along y's rows first.
+struct Tiles {
+  uint64_t row, col, step_row, step_col, left;  // in tiles; left: tiles still to come
+  __device__ __forceinline__ Tiles(const Problem& p, uint64_t first, uint64_t step) {
+    const uint64_t all = p.tiles_m * p.tiles_n;
+    row = first / p.tiles_n;
+    col = first % p.tiles_n;
+    step_row = step / p.tiles_n;
+    step_col = step % p.tiles_n;
+    left = first < all ? (all - first + step - 1) / step : 0;
+  }
+  __device__ __forceinline__ void next(const Problem& p) {
+    row += step_row;
+    col += step_col;
+    if (col >= p.tiles_n) {
+      col -= p.tiles_n;
+      ++row;
+    }
+    --left;
+  }
+};
 
 template <int kCols>
 __global__ void __launch_bounds__(kThreads, 1)
@@ -194,7 +230,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
     for (int b = 0; b < 2; ++b) {
       mbar_init(&ready[b], 1);
-      mbar_init(&drained[b], 4);
+      mbar_init(&drained[b], kStoreWarps);
     }
     fence_proxy_async_smem();
   }
@@ -211,17 +247,16 @@ __global__ void __launch_bounds__(kThreads, 1)
   pdl_trigger();
   pdl_wait();  // every role: the bounded waits below start when the inputs are there
 
-  const uint64_t tiles = p.tiles_m * p.tiles_n;
   const uint32_t splits = p.splits, rank = blockIdx.x % splits;
-  const uint64_t first = blockIdx.x / splits, step = gridDim.x / splits;
+  Tiles t(p, blockIdx.x / splits, gridDim.x / splits);
   const uint64_t all = (p.k + kStep - 1) / kStep;
   const uint64_t k0 = all * rank / splits, k1 = all * (rank + 1) / splits;
 
   if (warp == 0 && lane == 0) {
     uint32_t it = 0;
     bool ok = true;
-    for (uint64_t t = first; t < tiles && ok; t += step) {
-      const uint64_t n0 = t % p.tiles_n * kRows, m0 = t / p.tiles_n * kCols;
+    for (; t.left && ok; t.next(p)) {
+      const uint64_t n0 = t.col * kRows, m0 = t.row * kCols;
       const uint64_t g0 = m0 / 128, g1 = (p.m + 127) / 128;
       for (uint64_t k = k0; k < k1; ++k, ++it) {
         const uint32_t s = it % S::kStages;
@@ -249,10 +284,10 @@ __global__ void __launch_bounds__(kThreads, 1)
   } else if (warp == 1 && lane == 0) {
     uint32_t it = 0, n_tile = 0;
     bool ok = true;
-    for (uint64_t t = first; t < tiles && ok; t += step, ++n_tile) {
+    for (; t.left && ok; t.next(p), ++n_tile) {
       const uint32_t b = n_tile & 1;
       const uint32_t d = tmem + b * 256;
-      const uint64_t m0 = t / p.tiles_n * kCols;
+      const uint64_t m0 = t.row * kCols;
       if (n_tile >= 2 && !wait(&drained[b], (n_tile / 2 + 1) & 1)) break;
       asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
       for (uint64_t k = k0; k < k1; ++k, ++it) {
@@ -293,22 +328,23 @@ __global__ void __launch_bounds__(kThreads, 1)
       commit(&ready[1]);
     }
   } else if (warp >= 2) {
-    const int quarter = warp & 3;  // the TMEM lanes this warp can read
+    const int quarter = warp & 3, half = (warp - 2) >> 2;  // the TMEM lanes this warp can read
+    const int row = quarter * 32 + lane;
     uint32_t n_tile = 0;
-    for (uint64_t t = first; t < tiles; t += step, ++n_tile) {
+    for (Tiles u = t; u.left; u.next(p), ++n_tile) {
       const uint32_t b = n_tile & 1;
       if (!wait(&ready[b], (n_tile / 2) & 1)) break;
       asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
-      const uint64_t j = t % p.tiles_n * kRows + quarter * 32 + lane, m0 = t / p.tiles_n * kCols;
+      const uint64_t j = u.col * kRows + row, m0 = u.row * kCols;
       const int cols = p.m - m0 < kCols ? static_cast<int>(p.m - m0) : kCols;
       const uint32_t d = tmem + b * 256 + (static_cast<uint32_t>(quarter * 32) << 16);
-      for (int c = 0; c < cols; c += 16) {
+      for (int c = 16 * half; c < cols; c += 32) {
         float v[16];
         read_columns(d + c, v);
         if (splits == 1) {
           store_columns(p, m0 + c, j, v);
         } else {  // this block's part of the sum, for the cluster to add up
-          float* part = reinterpret_cast<float*>(smem) + quarter * 32 + lane;
+          float* part = reinterpret_cast<float*>(smem) + row;
 #pragma unroll
           for (int q = 0; q < 16; ++q) part[(c + q) * kRows] = v[q];
         }
@@ -322,12 +358,11 @@ __global__ void __launch_bounds__(kThreads, 1)
   if (splits > 1) {
     cluster_sync();
     if (warp >= 2) {
-      const uint64_t m0 = first / p.tiles_n * kCols;
-      const int row = (warp & 3) * 32 + lane;
-      const uint64_t j = first % p.tiles_n * kRows + row;
+      const int row = (warp & 3) * 32 + lane, half = (warp - 2) >> 2;
+      const uint64_t j = t.col * kRows + row, m0 = t.row * kCols;
       const int cols = p.m - m0 < kCols ? static_cast<int>(p.m - m0) : kCols;
       const uint32_t part = smem_u32(smem) + row * 4;
-      for (int c = rank; c < cols; c += splits) {
+      for (int c = 2 * rank + half; c < cols; c += 2 * splits) {
         float v = 0.f;
         for (uint32_t r = 0; r < splits; ++r) v += remote_f32(part + c * kRows * 4, r);
         if (j < p.n) store_one(p, m0 + c, j, v);
