@@ -20,7 +20,7 @@ namespace {
 
 __device__ unsigned long long g_wait_timeouts;
 
-constexpr int kRows = 128;       // rows of B per tile
+constexpr int kRows = 128;       // rows of B per block
 constexpr int kStepBytes = 128;  // bytes of codes per row and step: 256 columns
 constexpr int kStep = 256;
 constexpr int kStoreWarps = 8;   // two for each quarter of the TMEM lanes
@@ -29,10 +29,8 @@ constexpr int kMaxSplits = 8;
 constexpr unsigned kSmemLimit = 232448 - 1024;  // 227 KB less the alignment of the stages
 
 struct Problem {
-  uint64_t m, n, k, groups;  // groups: 4-block scale groups of a row
+  uint64_t m, n, k;
   uint64_t tiles_m, tiles_n;
-  const uint8_t* a_scales;
-  const uint8_t* b_scales;
   void* y;
   uint64_t stride;
   int type;
@@ -40,16 +38,26 @@ struct Problem {
   int splits;  // thread blocks of a cluster that share a tile's k
 };
 
-template <int kCols>
+struct Maps {  // the codes and the scales of A and B
+  CUtensorMap a, b, a_scales, b_scales;
+};
+
+// A tile of kBlocks * 128 rows of B by kCols rows of A, computed by one block
+// or by the two of a pair.  Either block of a pair holds its own 128 rows of
+// B, half of the rows of A, and the scales of its rows of B and of all of A's.
+template <int kCols, int kBlocks>
 struct Shape {
   static constexpr int kScaleRows = kCols > 128 ? 2 : 1;  // groups of 128 rows of A that a tile spans
-  static constexpr int kBBytes = kRows * kStepBytes, kABytes = kCols * kStepBytes;
+  static constexpr int kACols = kCols / kBlocks;          // rows of A that a block loads
+  static constexpr int kBBytes = kRows * kStepBytes, kABytes = kACols * kStepBytes;
   static constexpr int kStageBytes = kBBytes + kABytes + 1024 + 1024 * kScaleRows;
   static constexpr int kFit = (kSmemLimit - 1024) / kStageBytes;
   static constexpr int kStages = kFit > 10 ? 10 : kFit;
   static constexpr int kSmem = kStages * kStageBytes + 2048;
-  // TMEM columns: two buffers of 256, each an accumulator and two steps' scales
-  static constexpr int kScaleCol = kCols <= 192 ? 192 : 256;
+  // TMEM columns: two buffers of 256, each an accumulator and a step's scales
+  static constexpr int kScaleCol = 192;
+  static_assert(kCols <= kScaleCol && kScaleCol + 8 + 8 * kScaleRows <= 256, "TMEM columns");
+  static_assert(kABytes % 1024 == 0, "swizzle");
 };
 
 // Bounded wait for a phase of a barrier: false after kWaitNs, with the
@@ -76,13 +84,33 @@ __device__ __forceinline__ void mbar_arrive(uint64_t* bar) {
   asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(smem_u32(bar)) : "memory");
 }
 
+__device__ __forceinline__ uint32_t cluster_address(const void* p, uint32_t rank) {
+  uint32_t far;
+  asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(far) : "r"(smem_u32(p)), "r"(rank));
+  return far;
+}
+__device__ __forceinline__ void mbar_arrive_at(uint32_t cluster_bar) {
+  asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(cluster_bar)
+               : "memory");
+}
+
+// A box into this block's shared memory, counted on a barrier given by its
+// cluster address; a pair's loads are counted on its first block's barrier.
+template <int kBlocks>
 __device__ __forceinline__ void tma_load(void* dst, const CUtensorMap* map, int x, int y,
-                                         uint64_t* bar) {
-  asm volatile(
-      "cp.async.bulk.tensor.2d.shared::cta.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3}], [%4];" ::
-          "r"(smem_u32(dst)),
-      "l"(map), "r"(x), "r"(y), "r"(smem_u32(bar))
-      : "memory");
+                                         uint32_t bar) {
+  if constexpr (kBlocks == 2)
+    asm volatile(
+        "cp.async.bulk.tensor.2d.cta_group::2.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3}], [%4];" ::
+            "r"(smem_u32(dst)),
+        "l"(map), "r"(x), "r"(y), "r"(bar)
+        : "memory");
+  else
+    asm volatile(
+        "cp.async.bulk.tensor.2d.shared::cta.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3}], [%4];" ::
+            "r"(smem_u32(dst)),
+        "l"(map), "r"(x), "r"(y), "r"(bar)
+        : "memory");
 }
 
 // Shared-memory descriptors: version 1, K-major.  Codes: rows of 128 bytes in
@@ -96,31 +124,78 @@ __device__ __forceinline__ uint64_t scales_desc(uint32_t addr) {
   return (uint64_t)((addr & 0x3FFFF) >> 4) | (128ull >> 4) << 32 | 1ull << 46;
 }
 // Instruction descriptor of the block-scaled e2m1 product: both types e2m1,
-// ue8m0 scales, `cols` columns, 128 rows, the pair of a scale word's bytes
-// that a product of 64 columns takes (0 or 2).
-__host__ __device__ constexpr uint32_t product_desc(int cols, int pair) {
+// ue8m0 scales, `cols` columns, 128 or 256 rows, the pair of a scale word's
+// bytes that a product of 64 columns takes (0 or 2).
+__host__ __device__ constexpr uint32_t product_desc(int blocks, int cols, int pair) {
   return (uint32_t)pair << 4 | 1u << 7 | 1u << 10 | (uint32_t)(cols >> 3) << 17 | 1u << 23 |
-         (uint32_t)(kRows >> 4) << 24 | (uint32_t)pair << 29;
+         (uint32_t)(blocks * kRows >> 4) << 24 | (uint32_t)pair << 29;
 }
 
+// For a pair, the first block's thread issues these for both blocks: each
+// copies its own scales and multiplies its own rows of B by both halves of A.
+template <int kBlocks>
 __device__ __forceinline__ void copy_scales(uint32_t tmem, uint64_t desc) {
-  asm volatile("tcgen05.cp.cta_group::1.32x128b.warpx4 [%0], %1;" ::"r"(tmem), "l"(desc)
-               : "memory");
+  if constexpr (kBlocks == 2)
+    asm volatile("tcgen05.cp.cta_group::2.32x128b.warpx4 [%0], %1;" ::"r"(tmem), "l"(desc)
+                 : "memory");
+  else
+    asm volatile("tcgen05.cp.cta_group::1.32x128b.warpx4 [%0], %1;" ::"r"(tmem), "l"(desc)
+                 : "memory");
 }
+template <int kBlocks>
 __device__ __forceinline__ void product(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc,
                                         uint32_t sa, uint32_t sb, bool add) {
-  asm volatile(
-      "{\n .reg .pred p;\n setp.ne.u32 p, %6, 0;\n"
-      " tcgen05.mma.cta_group::1.kind::mxf4.block_scale.scale_vec::2X [%0], %1, %2, %3, [%4], [%5], p;\n}" ::
-          "r"(d),
-      "l"(a), "l"(b), "r"(idesc), "r"(sa), "r"(sb), "r"((uint32_t)add)
-      : "memory");
+  if constexpr (kBlocks == 2)
+    asm volatile(
+        "{\n .reg .pred p;\n setp.ne.u32 p, %6, 0;\n"
+        " tcgen05.mma.cta_group::2.kind::mxf4.block_scale.scale_vec::2X [%0], %1, %2, %3, [%4], [%5], p;\n}" ::
+            "r"(d),
+        "l"(a), "l"(b), "r"(idesc), "r"(sa), "r"(sb), "r"((uint32_t)add)
+        : "memory");
+  else
+    asm volatile(
+        "{\n .reg .pred p;\n setp.ne.u32 p, %6, 0;\n"
+        " tcgen05.mma.cta_group::1.kind::mxf4.block_scale.scale_vec::2X [%0], %1, %2, %3, [%4], [%5], p;\n}" ::
+            "r"(d),
+        "l"(a), "l"(b), "r"(idesc), "r"(sa), "r"(sb), "r"((uint32_t)add)
+        : "memory");
 }
-// The barrier is reached when the products issued so far by this thread are done.
+// The barrier (in both blocks of a pair) is reached when the products issued
+// so far by this thread are done.
+template <int kBlocks>
 __device__ __forceinline__ void commit(uint64_t* bar) {
-  asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(
-                   smem_u32(bar))
-               : "memory");
+  if constexpr (kBlocks == 2)
+    asm volatile(
+        "tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;" ::
+            "r"(smem_u32(bar)),
+        "h"((uint16_t)3)
+        : "memory");
+  else
+    asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::
+                     "r"(smem_u32(bar))
+                 : "memory");
+}
+// All of an SM's TMEM, by one warp of each block.
+template <int kBlocks>
+__device__ __forceinline__ void take_tmem(uint32_t* base) {
+  if constexpr (kBlocks == 2) {
+    asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], 512;" ::"r"(
+                     smem_u32(base))
+                 : "memory");
+    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;");
+  } else {
+    asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], 512;" ::"r"(
+                     smem_u32(base))
+                 : "memory");
+    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;");
+  }
+}
+template <int kBlocks>
+__device__ __forceinline__ void give_tmem(uint32_t tmem) {
+  if constexpr (kBlocks == 2)
+    asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, 512;" ::"r"(tmem));
+  else
+    asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, 512;" ::"r"(tmem));
 }
 __device__ __forceinline__ void read_columns(uint32_t tmem, float (&v)[16]) {
   uint32_t* r = reinterpret_cast<uint32_t*>(v);
@@ -190,6 +265,16 @@ __device__ __forceinline__ void store_columns(const Problem& p, uint64_t i, uint
   }
 }
 
+// One lane of a converged warp.  What only that lane does is then known to be
+// the work of one thread: a branch on the lane's number leaves the operands
+// of the tensor core's instructions in per-lane registers, and issuing them
+// took longer than the products.
+__device__ __forceinline__ bool elect() {
+  uint32_t r;
+  asm volatile("{\n .reg .pred p;\n elect.sync _|p, 0xFFFFFFFF;\n selp.u32 %0, 1, 0, p;\n}" : "=r"(r));
+  return r;
+}
+
 // The tiles of a block: every `step`-th from `first`, along y's rows first.
 struct Tiles {
   uint64_t row, col, step_row, step_col, left;  // in tiles; left: tiles still to come
@@ -212,16 +297,20 @@ struct Tiles {
   }
 };
 
-template <int kCols>
+template <int kCols, int kBlocks>
 __global__ void __launch_bounds__(kThreads, 1)
-    matmul_kernel(const __grid_constant__ CUtensorMap a_map, const __grid_constant__ CUtensorMap b_map,
-                  const __grid_constant__ Problem p) {
-  using S = Shape<kCols>;
+    matmul_kernel(const __grid_constant__ Maps maps, const __grid_constant__ Problem p) {
+  using S = Shape<kCols, kBlocks>;
   extern __shared__ uint8_t raw[];
   uint8_t* smem = raw + (1024 - (smem_u32(raw) & 1023)) % 1024;
   __shared__ uint64_t full[S::kStages], empty[S::kStages], ready[2], drained[2];
   __shared__ uint32_t tmem_base;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  // The blocks of a cluster: a pair (kBlocks 2), or the `splits` that share a
+  // tile's k (kBlocks 1).
+  const uint32_t splits = kBlocks == 2 ? 1 : p.splits;
+  const uint32_t rank = blockIdx.x % (splits * kBlocks);
+  const uint32_t half_of = kBlocks == 2 ? rank : 0, part = kBlocks == 2 ? 0 : rank;
 
   if (warp == 0 && lane == 0) {
     for (int s = 0; s < S::kStages; ++s) {
@@ -230,34 +319,29 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
     for (int b = 0; b < 2; ++b) {
       mbar_init(&ready[b], 1);
-      mbar_init(&drained[b], kStoreWarps);
+      mbar_init(&drained[b], kStoreWarps * kBlocks);
     }
     fence_proxy_async_smem();
   }
-  if (warp == 1) {
-    asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], 512;" ::"r"(
-                     smem_u32(&tmem_base))
-                 : "memory");
-    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;");
-  }
+  if (warp == 1) take_tmem<kBlocks>(&tmem_base);
   asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
   __syncthreads();
+  if (kBlocks == 2) cluster_sync();  // the other block's barriers are ready
   asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
   const uint32_t tmem = tmem_base;
   pdl_trigger();
   pdl_wait();  // every role: the bounded waits below start when the inputs are there
 
-  const uint32_t splits = p.splits, rank = blockIdx.x % splits;
-  Tiles t(p, blockIdx.x / splits, gridDim.x / splits);
+  Tiles t(p, blockIdx.x / (splits * kBlocks), gridDim.x / (splits * kBlocks));
   const uint64_t all = (p.k + kStep - 1) / kStep;
-  const uint64_t k0 = all * rank / splits, k1 = all * (rank + 1) / splits;
+  const uint64_t k0 = all * part / splits, k1 = all * (part + 1) / splits;
 
-  if (warp == 0 && lane == 0) {
+  if (warp == 0 && elect()) {
     uint32_t it = 0;
     bool ok = true;
     for (; t.left && ok; t.next(p)) {
-      const uint64_t n0 = t.col * kRows, m0 = t.row * kCols;
-      const uint64_t g0 = m0 / 128, g1 = (p.m + 127) / 128;
+      const int n0 = static_cast<int>((t.col * kBlocks + half_of) * kRows);
+      const uint64_t m0 = t.row * kCols;
       for (uint64_t k = k0; k < k1; ++k, ++it) {
         const uint32_t s = it % S::kStages;
         if (it >= S::kStages && !wait(&empty[s], (it / S::kStages + 1) & 1)) {
@@ -265,29 +349,32 @@ __global__ void __launch_bounds__(kThreads, 1)
           break;
         }
         uint8_t* stage = smem + s * S::kStageBytes;
-        const uint32_t bytes = (p.groups - 2 * k >= 2 ? 2 : 1) * 512;
-        const int groups = g1 - g0 >= S::kScaleRows ? S::kScaleRows : 1;
-        mbar_arrive_expect_tx(&full[s], S::kBBytes + S::kABytes + bytes * (1 + groups));
-        tma_load(stage, &b_map, static_cast<int>(k * kStepBytes), static_cast<int>(n0), &full[s]);
-        tma_load(stage + S::kBBytes, &a_map, static_cast<int>(k * kStepBytes),
-                 static_cast<int>(m0), &full[s]);
-        uint8_t* sc = stage + S::kBBytes + S::kABytes;
-        bulk_load_smem(sc, p.b_scales + (n0 / 128 * p.groups + 2 * k) * 512, bytes, &full[s]);
-        for (int g = 0; g < groups; ++g)
-          bulk_load_smem(sc + 1024 + g * 1024, p.a_scales + ((g0 + g) * p.groups + 2 * k) * 512,
-                         bytes, &full[s]);
+        uint8_t* scales = stage + S::kBBytes + S::kABytes;
+        const int x = static_cast<int>(k * kStepBytes), xs = static_cast<int>(k * 256);
+        uint32_t bar = smem_u32(&full[s]);
+        if (kBlocks == 2) bar = cluster_address(&full[s], 0);
+        if (half_of == 0) mbar_arrive_expect_tx(&full[s], kBlocks * S::kStageBytes);
+        tma_load<kBlocks>(stage, &maps.b, x, n0, bar);
+        tma_load<kBlocks>(stage + S::kBBytes, &maps.a, x,
+                          static_cast<int>(m0 + half_of * S::kACols), bar);
+        tma_load<kBlocks>(scales, &maps.b_scales, xs, n0 / 128, bar);
+        tma_load<kBlocks>(scales + 1024, &maps.a_scales, xs, static_cast<int>(m0 / 128), bar);
       }
     }
-    if (!ok)  // the loads still in flight end before the block does
+    // Before the block ends: the loads still in flight where a wait ran out,
+    // and in a pair the products' arrivals on this block's barriers.
+    if (!ok || kBlocks == 2)
       for (uint32_t i = it > S::kStages ? it - S::kStages : 0; i < it; ++i)
-        wait(&full[i % S::kStages], (i / S::kStages) & 1);
-  } else if (warp == 1 && lane == 0) {
+        if (!wait(ok ? &empty[i % S::kStages] : &full[i % S::kStages], (i / S::kStages) & 1)) break;
+  } else if (warp == 1 && half_of == 0 && elect()) {
     uint32_t it = 0, n_tile = 0;
     bool ok = true;
     for (; t.left && ok; t.next(p), ++n_tile) {
       const uint32_t b = n_tile & 1;
       const uint32_t d = tmem + b * 256;
-      const uint64_t m0 = t.row * kCols;
+      // the scales of a tile that starts in the middle of a group of 128 rows
+      // (192 columns: at 0 or 64, so that the shift is even, as it has to be)
+      const uint32_t shift = kCols > 128 ? t.row * kCols % 128 / 32 : 0;
       if (n_tile >= 2 && !wait(&drained[b], (n_tile / 2 + 1) & 1)) break;
       asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
       for (uint64_t k = k0; k < k1; ++k, ++it) {
@@ -306,26 +393,26 @@ __global__ void __launch_bounds__(kThreads, 1)
         const int products = p.k - k * kStep >= kStep ? 4 : static_cast<int>((p.k - k * kStep + 63) / 64);
 #pragma unroll
         for (int g = 0; g < 2; ++g) {
-          if (2 * g >= products) break;
-          const uint32_t sbg = sb + 4 * g, sag = sa + 4 * S::kScaleRows * g;
-          copy_scales(sbg, scales_desc(sc + 512 * g));
+          copy_scales<kBlocks>(sb + 4 * g, scales_desc(sc + 512 * g));
 #pragma unroll
           for (int r = 0; r < S::kScaleRows; ++r)
-            copy_scales(sag + 4 * r, scales_desc(sc + 1024 + 1024 * r + 512 * g));
-#pragma unroll
-          for (int q = 2 * g; q < 2 * g + 2; ++q) {
-            if (q >= products) break;
-            product(d, db + 2 * q, da + 2 * q, product_desc(kCols, 2 * (q & 1)), sbg,
-                    sag + static_cast<uint32_t>(m0 % 128 / 32), k > k0 || q > 0);
-          }
+            copy_scales<kBlocks>(sa + 4 * (S::kScaleRows * g + r),
+                                 scales_desc(sc + 1024 + 1024 * r + 512 * g));
         }
-        commit(&empty[s]);
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {
+          if (q >= products) break;
+          product<kBlocks>(d, db + 2 * q, da + 2 * q, product_desc(kBlocks, kCols, 2 * (q & 1)),
+                           sb + 4 * (q / 2), sa + 4 * S::kScaleRows * (q / 2) + shift,
+                           k > k0 || q > 0);
+        }
+        commit<kBlocks>(&empty[s]);
       }
-      if (ok) commit(&ready[b]);
+      if (ok) commit<kBlocks>(&ready[b]);
     }
     if (!ok) {  // products in flight end before TMEM is given back
-      commit(&ready[0]);
-      commit(&ready[1]);
+      commit<kBlocks>(&ready[0]);
+      commit<kBlocks>(&ready[1]);
     }
   } else if (warp >= 2) {
     const int quarter = warp & 3, half = (warp - 2) >> 2;  // the TMEM lanes this warp can read
@@ -335,8 +422,10 @@ __global__ void __launch_bounds__(kThreads, 1)
       const uint32_t b = n_tile & 1;
       if (!wait(&ready[b], (n_tile / 2) & 1)) break;
       asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
-      const uint64_t j = u.col * kRows + row, m0 = u.row * kCols;
-      const int cols = p.m - m0 < kCols ? static_cast<int>(p.m - m0) : kCols;
+      const uint64_t j = (u.col * kBlocks + half_of) * kRows + row, m0 = u.row * kCols;
+      const int cols = j - lane >= p.n     ? 0
+                       : p.m - m0 < kCols ? static_cast<int>(p.m - m0)
+                                          : kCols;
       const uint32_t d = tmem + b * 256 + (static_cast<uint32_t>(quarter * 32) << 16);
       for (int c = 16 * half; c < cols; c += 32) {
         float v[16];
@@ -344,14 +433,17 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (splits == 1) {
           store_columns(p, m0 + c, j, v);
         } else {  // this block's part of the sum, for the cluster to add up
-          float* part = reinterpret_cast<float*>(smem) + row;
+          float* mine = reinterpret_cast<float*>(smem) + row;
 #pragma unroll
-          for (int q = 0; q < 16; ++q) part[(c + q) * kRows] = v[q];
+          for (int q = 0; q < 16; ++q) mine[(c + q) * kRows] = v[q];
         }
       }
       asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
       __syncwarp();
-      if (lane == 0) mbar_arrive(&drained[b]);
+      if (lane == 0) {
+        if (kBlocks == 2) mbar_arrive_at(cluster_address(&drained[b], 0));
+        else mbar_arrive(&drained[b]);
+      }
     }
   }
   __syncwarp();
@@ -361,10 +453,10 @@ __global__ void __launch_bounds__(kThreads, 1)
       const int row = (warp & 3) * 32 + lane, half = (warp - 2) >> 2;
       const uint64_t j = t.col * kRows + row, m0 = t.row * kCols;
       const int cols = p.m - m0 < kCols ? static_cast<int>(p.m - m0) : kCols;
-      const uint32_t part = smem_u32(smem) + row * 4;
-      for (int c = 2 * rank + half; c < cols; c += 2 * splits) {
+      const uint32_t parts = smem_u32(smem) + row * 4;
+      for (int c = 2 * part + half; c < cols; c += 2 * splits) {
         float v = 0.f;
-        for (uint32_t r = 0; r < splits; ++r) v += remote_f32(part + c * kRows * 4, r);
+        for (uint32_t r = 0; r < splits; ++r) v += remote_f32(parts + c * kRows * 4, r);
         if (j < p.n) store_one(p, m0 + c, j, v);
       }
     }
@@ -373,8 +465,9 @@ __global__ void __launch_bounds__(kThreads, 1)
   }
   asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
   __syncthreads();
-  if (warp == 1)
-    asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, 512;" ::"r"(tmem));
+  // in a pair the other block may still use this one's barriers and TMEM
+  if (kBlocks == 2) cluster_sync();
+  if (warp == 1) give_tmem<kBlocks>(tmem);
 }
 
 __global__ void zero_kernel(const __grid_constant__ Problem p) {
@@ -397,39 +490,56 @@ EncodeFn encode_fn() {
   return fn;
 }
 
-// The codes of a matrix as boxes of 128 bytes by `box` rows, swizzled; bytes
-// and rows past the matrix read as zeros.
-bool map_codes(CUtensorMap* map, const uint8_t* codes, uint64_t rows, uint64_t k, int box) {
+// A matrix's codes as boxes of 128 bytes by `box` rows, swizzled, and its
+// scales as boxes of two 512-byte groups by `groups`; what lies past the
+// matrix reads as zeros.
+bool make_maps(CUtensorMap* codes_map, CUtensorMap* scales_map, const uint8_t* codes,
+               const uint8_t* scales, uint64_t rows, uint64_t k, int box, int groups) {
+  EncodeFn f = encode_fn();
+  if (!f) return false;
+  const cuuint32_t steps[2] = {1, 1};
   const uint64_t bytes = (k + kMxBlock - 1) / kMxBlock * 16;
   const cuuint64_t dims[2] = {bytes, rows}, strides[1] = {bytes};
-  const cuuint32_t boxes[2] = {kStepBytes, static_cast<cuuint32_t>(box)}, steps[2] = {1, 1};
-  EncodeFn f = encode_fn();
-  return f && f(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, const_cast<uint8_t*>(codes), dims, strides,
-                boxes, steps, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
-                CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+  const cuuint32_t boxes[2] = {kStepBytes, static_cast<cuuint32_t>(box)};
+  const uint64_t words = (k + 127) / 128 * 128;  // of 4 bytes
+  const cuuint64_t sdims[2] = {words, (rows + 127) / 128}, sstrides[1] = {words * 4};
+  const cuuint32_t sboxes[2] = {256, static_cast<cuuint32_t>(groups)};
+  return f(codes_map, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, const_cast<uint8_t*>(codes), dims, strides,
+           boxes, steps, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+           CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS &&
+         f(scales_map, CU_TENSOR_MAP_DATA_TYPE_UINT32, 2, const_cast<uint8_t*>(scales), sdims,
+           sstrides, sboxes, steps, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_NONE,
+           CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-template <int kCols>
-cudaError_t run(Problem p, const uint8_t* a_codes, const uint8_t* b_codes, cudaStream_t st) {
-  using S = Shape<kCols>;
-  CUtensorMap a_map, b_map;
-  if (!map_codes(&a_map, a_codes, p.m, p.k, kCols) || !map_codes(&b_map, b_codes, p.n, p.k, kRows))
-    return cudaErrorUnknown;
+struct Operands {
+  const uint8_t *a_codes, *a_scales, *b_codes, *b_scales;
+};
+
+template <int kCols, int kBlocks>
+cudaError_t run(Problem p, const Operands& o, cudaStream_t st) {
+  using S = Shape<kCols, kBlocks>;
   p.tiles_m = (p.m + kCols - 1) / kCols;
-  p.tiles_n = (p.n + kRows - 1) / kRows;
+  p.tiles_n = (p.n + kRows * kBlocks - 1) / (kRows * kBlocks);
   const uint64_t tiles = p.tiles_m * p.tiles_n, steps = (p.k + kStep - 1) / kStep;
   const uint64_t sms = sm_count();
   // few tiles: a cluster shares a tile's k while SMs are idle and each block
   // keeps two steps at least
   p.splits = 1;
-  while (p.splits < kMaxSplits && tiles * p.splits * 2 <= sms && steps >= 4ull * p.splits)
+  while (kBlocks == 1 && p.splits < kMaxSplits && tiles * p.splits * 2 <= sms &&
+         steps >= 4ull * p.splits)
     p.splits *= 2;
-  const uint64_t blocks = p.splits > 1 ? tiles * p.splits : tiles < sms ? tiles : sms;
-  cudaError_t e = cudaFuncSetAttribute(matmul_kernel<kCols>,
-                                       cudaFuncAttributeMaxDynamicSharedMemorySize, S::kSmem);
+  Maps maps;
+  if (!make_maps(&maps.a, &maps.a_scales, o.a_codes, o.a_scales, p.m, p.k, S::kACols, S::kScaleRows) ||
+      !make_maps(&maps.b, &maps.b_scales, o.b_codes, o.b_scales, p.n, p.k, kRows, 1))
+    return cudaErrorUnknown;
+  auto* kernel = matmul_kernel<kCols, kBlocks>;
+  cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, S::kSmem);
   if (e != cudaSuccess) return e;
+  const uint32_t cluster = p.splits * kBlocks;
+  const uint64_t clusters = p.splits > 1 || tiles < sms / kBlocks ? tiles : sms / kBlocks;
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(static_cast<unsigned>(blocks));
+  cfg.gridDim = dim3(static_cast<unsigned>(clusters * cluster));
   cfg.blockDim = dim3(kThreads);
   cfg.dynamicSmemBytes = S::kSmem;
   cfg.stream = st;
@@ -437,21 +547,24 @@ cudaError_t run(Problem p, const uint8_t* a_codes, const uint8_t* b_codes, cudaS
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   attr[1].id = cudaLaunchAttributeClusterDimension;
-  attr[1].val.clusterDim.x = p.splits;
+  attr[1].val.clusterDim.x = cluster;
   attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 2;
-  return cudaLaunchKernelEx(&cfg, matmul_kernel<kCols>, a_map, b_map, p);
+  return cudaLaunchKernelEx(&cfg, kernel, maps, p);
 }
 
-cudaError_t matmul(const Problem& p, const uint8_t* a_codes, const uint8_t* b_codes,
-                   cudaStream_t st) {
+cudaError_t matmul(const Problem& p, const Operands& o, cudaStream_t st) {
   if (p.k == 0) return launch_chained(zero_kernel, sm_count() * 4, 256, 0, st, p);
-  if (p.m <= 16) return run<16>(p, a_codes, b_codes, st);
-  if (p.m <= 32) return run<32>(p, a_codes, b_codes, st);
-  if (p.m <= 64) return run<64>(p, a_codes, b_codes, st);
-  if (p.m <= 128) return run<128>(p, a_codes, b_codes, st);
-  return run<192>(p, a_codes, b_codes, st);
+  if (p.m <= 16) return run<16, 1>(p, o, st);
+  if (p.m <= 32) return run<32, 1>(p, o, st);
+  if (p.m <= 64) return run<64, 1>(p, o, st);
+  if (p.m <= 128) return run<128, 1>(p, o, st);
+  // pairs halve what a block loads of A; one block per tile has twice as many
+  // tiles to spread over the SMs
+  const uint64_t pairs = (p.m + 191) / 192 * ((p.n + 255) / 256);
+  if (pairs * 2 > static_cast<uint64_t>(sm_count())) return run<192, 2>(p, o, st);
+  return run<192, 1>(p, o, st);
 }
 
 }  // namespace
@@ -476,14 +589,11 @@ hkv_status hkv_mx_matmul(uint64_t m, uint64_t n, uint64_t k, const uint8_t* a_co
   p.m = m;
   p.n = n;
   p.k = k;
-  p.groups = (k + 127) / 128;
-  p.a_scales = a_scales;
-  p.b_scales = b_scales;
   p.y = y;
   p.stride = y_stride;
   p.type = y_type;
   p.pairs = y_type != HKV_F32 && aligned(y, 4) && y_stride % 2 == 0;
-  return op_status(matmul(p, a_codes, b_codes, static_cast<cudaStream_t>(stream)));
+  return op_status(matmul(p, {a_codes, a_scales, b_codes, b_scales}, static_cast<cudaStream_t>(stream)));
 }
 
 hkv_status hkv_get_wait_timeouts(uint64_t* timeouts_host) {

@@ -198,6 +198,14 @@ def test_product_of_long_rows_and_many(hkv, m, n, k):
     _check_product(hkv, _randn(m, (m, k)), _randn(n + 1, (n, k), scale=0.1), BF16)
 
 
+@pytest.mark.parametrize("m,n,k", [(1300, 3100, 600), (1537, 2561, 64), (3000, 1500, 33), (193, 20001, 300),
+                                   (2500, 4000, 2100), (5000, 900, 515)])
+@pytest.mark.parametrize("dtype", [F32, BF16])
+def test_product_of_many_tiles(hkv, m, n, k, dtype):
+    """More tiles than SMs: several tiles per block, ragged in every direction."""
+    _check_product(hkv, _randn(m, (m, k)), _randn(n + 1, (n, k), scale=0.1), dtype)
+
+
 @pytest.mark.parametrize("extra,shift", [(0, 1), (1, 0), (3, 3), (2, 0), (8, 8)])
 @pytest.mark.parametrize("dtype", [F32, BF16])
 def test_product_into_strided_rows(hkv, extra, shift, dtype):
