@@ -11,17 +11,22 @@ caller's back) and ``HKVError`` for a status of the library.  ``stream``
 (default: the current stream of the tensors' device) is the stream the
 kernels run on and the one that results are allocated on; tensors made on
 another stream are the caller's to order, as with any CUDA call.
+
+The smallest calls take a few microseconds on the GPU, so the host's share is
+kept small: one allocation per result, and no context is entered unless the
+stream or the device has to change.
 """
 from __future__ import annotations
 
-import contextlib
-import ctypes
+from array import array
+from operator import attrgetter
 
 import torch
 
 import hash_table_cache_gb300 as _abi
 
 _TYPES = {torch.float32: 0, torch.bfloat16: 1, torch.float16: 2}
+_dtype_of = attrgetter("dtype")
 
 
 def _type(t, what):
@@ -36,13 +41,13 @@ def _matrix(t, what):
     if t.dim() != 2:
         raise ValueError(f"{what}: a matrix, not {t.dim()} dimensions")
     rows, cols = t.shape
-    if cols > 1 and t.stride(1) != 1:
+    stride, step = t.stride()
+    if step != 1 and cols > 1:
         raise ValueError(f"{what}: columns have to be adjacent (stride 1)")
-    stride = t.stride(0)
-    if rows < 2:
-        stride = max(stride, cols)
-    elif stride < cols:
-        raise ValueError(f"{what}: rows overlap")
+    if stride < cols:
+        if rows > 1:
+            raise ValueError(f"{what}: rows overlap")
+        stride = cols
     return rows, cols, stride
 
 
@@ -50,7 +55,6 @@ def _vector(t, n, dtype, what, device):
     if t.dtype != dtype or t.dim() != 1 or t.numel() != n or not t.is_contiguous():
         raise ValueError(f"{what}: {n} contiguous values of {dtype}")
     _same(t, device, what)
-    return t
 
 
 def _same(t, device, what):
@@ -59,29 +63,30 @@ def _same(t, device, what):
 
 
 def _cuda(t, what):
-    if not t.is_cuda:
+    device = t.device
+    if device.type != "cuda":
         raise ValueError(f"{what}: a CUDA tensor")
-    return t.device
+    return device
 
 
-@contextlib.contextmanager
-def _switched(device, stream):
+# the handle of a device's current stream, without a Stream object (2 us less
+# per call) where torch offers it
+_current = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
+    lambda index: torch.cuda.current_stream(index).cuda_stream)
+
+
+def _call(device, stream, f, *args):
+    """f(stream handle, *args) with the device current and the caching allocator
+    on the stream."""
+    if stream is None and torch.cuda.current_device() == device.index:
+        return f(_current(device.index), *args)
     with torch.cuda.device(device):
         if stream is None:
-            yield torch.cuda.current_stream(device).cuda_stream
-        else:
-            if not hasattr(stream, "cuda_stream"):
-                stream = torch.cuda.ExternalStream(int(stream), device=device)
-            with torch.cuda.stream(stream):
-                yield stream.cuda_stream
-
-
-def _on(device, stream):
-    """The stream handle to launch on, with its device current and the caching
-    allocator on that stream."""
-    if stream is None and torch.cuda.current_device() == device.index:
-        return contextlib.nullcontext(torch.cuda.current_stream(device).cuda_stream)
-    return _switched(device, stream)
+            return f(_current(device.index), *args)
+        if not hasattr(stream, "cuda_stream"):
+            stream = torch.cuda.ExternalStream(int(stream), device=device)
+        with torch.cuda.stream(stream):
+            return f(stream.cuda_stream, *args)
 
 
 def _ok(status, what):
@@ -89,54 +94,83 @@ def _ok(status, what):
         raise _abi.HKVError(status, what)
 
 
+def _mx_bytes(rows, cols):
+    """Bytes of the codes and of the scales of a 4-bit matrix."""
+    return rows * -(-cols // 32) * 16, -(-rows // 128) * -(-cols // 128) * 512
+
+
 class MXMatrix:
     """A 4-bit microscaled matrix (MXFP4) of ``rows`` x ``cols``: ``codes`` and
     ``scales`` are uint8 tensors in the layout of ``include/hkv.h``."""
 
-    __slots__ = ("codes", "scales", "rows", "cols")
+    __slots__ = ("rows", "cols", "device", "_codes", "_scales", "_base", "_at")
 
     def __init__(self, codes, scales, rows, cols):
         rows, cols = int(rows), int(cols)
-        device = _cuda(codes, "codes")
-        _same(scales, device, "scales")
-        need = (rows * -(-cols // 32) * 16, -(-rows // 128) * -(-cols // 128) * 512)
+        self.device = _cuda(codes, "codes")
+        _same(scales, self.device, "scales")
+        need = _mx_bytes(rows, cols)
         for t, n, what in ((codes, need[0], "codes"), (scales, need[1], "scales")):
             if t.dtype != torch.uint8 or not t.is_contiguous() or t.numel() != n:
                 raise ValueError(f"{what}: {n} contiguous bytes for {rows} x {cols}")
-        self.codes, self.scales, self.rows, self.cols = codes, scales, rows, cols
+        self.rows, self.cols = rows, cols
+        self._codes, self._scales = codes, scales
+        self._at = codes.data_ptr(), scales.data_ptr()
 
     @classmethod
-    def empty(cls, rows, cols, device):
-        """Room for a matrix, not initialised."""
+    def _inside(cls, base, offset, rows, cols):
+        """A matrix inside a buffer of bytes, `offset` bytes in; also the offset
+        after it."""
         m = cls.__new__(cls)
-        m.codes = torch.empty((rows, -(-cols // 32) * 16), dtype=torch.uint8, device=device)
-        m.scales = torch.empty((-(-rows // 128), -(-cols // 128), 512), dtype=torch.uint8,
-                               device=device)
-        m.rows, m.cols = rows, cols
+        codes, scales = _mx_bytes(rows, cols)
+        codes = -(-codes // 512) * 512
+        at = base.data_ptr() + offset
+        m.rows, m.cols, m.device = rows, cols, base.device
+        m._codes = m._scales = None
+        m._base = base, offset, codes
+        m._at = at, at + codes
         return m
+
+    def _piece(self, skip, size, shape):
+        base, offset, codes = self._base
+        start = offset + (codes if skip else 0)
+        return base[start:start + size].view(shape)
+
+    @property
+    def codes(self):
+        if self._codes is None:
+            self._codes = self._piece(False, _mx_bytes(self.rows, self.cols)[0],
+                                      (self.rows, -(-self.cols // 32) * 16))
+        return self._codes
+
+    @property
+    def scales(self):
+        if self._scales is None:
+            self._scales = self._piece(True, _mx_bytes(self.rows, self.cols)[1],
+                                       (-(-self.rows // 128), -(-self.cols // 128), 512))
+        return self._scales
 
     @property
     def shape(self):
         return (self.rows, self.cols)
 
-    @property
-    def device(self):
-        return self.codes.device
-
     def dequantize(self, dtype=torch.float32, out=None, stream=None):
         """The values the matrix stands for."""
-        with _on(self.device, stream) as s:
-            if out is None:
-                out = torch.empty((self.rows, self.cols), dtype=dtype, device=self.device)
-            kind = _type(out, "out")
-            _same(out, self.device, "out")
-            rows, cols, stride = _matrix(out, "out")
-            if (rows, cols) != self.shape:
-                raise ValueError(f"out: {self.rows} x {self.cols}")
-            _ok(_abi.load().hkv_mx_dequantize(rows, cols, self.codes.data_ptr(),
-                                              self.scales.data_ptr(), out.data_ptr(), kind, stride,
-                                              s), "hkv_mx_dequantize")
-        return out
+        return _call(self.device, stream, _dequantize, self, dtype, out)
+
+
+def _dequantize(s, q, dtype, out):
+    if out is None:
+        out = torch.empty((q.rows, q.cols), dtype=dtype, device=q.device)
+    kind = _type(out, "out")
+    rows, cols, stride = _matrix(out, "out")
+    if rows != q.rows or cols != q.cols:
+        raise ValueError(f"out: {q.rows} x {q.cols}")
+    _same(out, q.device, "out")
+    codes, scales = q._at
+    _ok(_abi.load().hkv_mx_dequantize(rows, cols, codes, scales, out.data_ptr(), kind, stride, s),
+        "hkv_mx_dequantize")
+    return out
 
 
 def mx_quantize(x, along="rows", stream=None):
@@ -145,18 +179,32 @@ def mx_quantize(x, along="rows", stream=None):
     of ``x``)."""
     if along not in ("rows", "columns", "both"):
         raise ValueError(f"along: rows, columns or both, not {along!r}")
-    device = _cuda(x, "x")
+    return _call(_cuda(x, "x"), stream, _quantize, x, along)
+
+
+def _quantize(s, x, along):
     kind = _type(x, "x")
     rows, cols, stride = _matrix(x, "x")
-    with _on(device, stream) as s:
-        q = MXMatrix.empty(rows, cols, device) if along != "columns" else None
-        qt = MXMatrix.empty(cols, rows, device) if along != "rows" else None
-        _ok(_abi.load().hkv_mx_quantize(
-            rows, cols, x.data_ptr(), kind, stride,
-            q.codes.data_ptr() if q else None, q.scales.data_ptr() if q else None,
-            qt.codes.data_ptr() if qt else None, qt.scales.data_ptr() if qt else None, s),
-            "hkv_mx_quantize")
-    return (q, qt) if along == "both" else q or qt
+    q = qt = None
+    at = at_t = (None, None)
+    if along == "both":
+        sizes = _mx_bytes(rows, cols), _mx_bytes(cols, rows)
+        room = [-(-c // 512) * 512 + e for c, e in sizes]
+        base = torch.empty(room[0] + room[1], dtype=torch.uint8, device=x.device)
+        q, qt = MXMatrix._inside(base, 0, rows, cols), MXMatrix._inside(base, room[0], cols, rows)
+        at, at_t = q._at, qt._at
+    else:
+        shape = (rows, cols) if along == "rows" else (cols, rows)
+        codes, scales = _mx_bytes(*shape)
+        base = torch.empty(-(-codes // 512) * 512 + scales, dtype=torch.uint8, device=x.device)
+        q = MXMatrix._inside(base, 0, *shape)
+        if along == "rows":
+            at = q._at
+        else:
+            at_t = q._at
+    _ok(_abi.load().hkv_mx_quantize(rows, cols, x.data_ptr(), kind, stride, at[0], at[1], at_t[0],
+                                    at_t[1], s), "hkv_mx_quantize")
+    return (q, qt) if along == "both" else q
 
 
 def mx_matmul(a, b, dtype=torch.bfloat16, out=None, stream=None):
@@ -164,19 +212,25 @@ def mx_matmul(a, b, dtype=torch.bfloat16, out=None, stream=None):
     m x n tensor of ``dtype``, or ``out``."""
     if a.cols != b.cols:
         raise ValueError(f"a has {a.cols} columns, b {b.cols}")
-    device = a.device
-    _same(b.codes, device, "b")
-    with _on(device, stream) as s:
-        if out is None:
-            out = torch.empty((a.rows, b.rows), dtype=dtype, device=device)
+    if a.device != b.device:
+        raise ValueError(f"b: on {b.device}, not {a.device}")
+    return _call(a.device, stream, _matmul, a, b, dtype, out)
+
+
+def _matmul(s, a, b, dtype, out):
+    m, n = a.rows, b.rows
+    if out is None:
+        out = torch.empty((m, n), dtype=dtype, device=a.device)
+        kind, stride = _type(out, "out"), n
+    else:
         kind = _type(out, "out")
-        _same(out, device, "out")
-        m, n, stride = _matrix(out, "out")
-        if (m, n) != (a.rows, b.rows):
-            raise ValueError(f"out: {a.rows} x {b.rows}")
-        _ok(_abi.load().hkv_mx_matmul(m, n, a.cols, a.codes.data_ptr(), a.scales.data_ptr(),
-                                      b.codes.data_ptr(), b.scales.data_ptr(), out.data_ptr(), kind,
-                                      stride, s), "hkv_mx_matmul")
+        rows, cols, stride = _matrix(out, "out")
+        if rows != m or cols != n:
+            raise ValueError(f"out: {m} x {n}")
+        _same(out, a.device, "out")
+    at, bt = a._at, b._at
+    _ok(_abi.load().hkv_mx_matmul(m, n, a.cols, at[0], at[1], bt[0], bt[1], out.data_ptr(), kind,
+                                  stride, s), "hkv_mx_matmul")
     return out
 
 
@@ -184,7 +238,7 @@ class PreferenceLoss:
     """What ``preference_loss`` returns: ``losses`` [pairs], ``ratios`` [2 * pairs],
     ``logps`` [tokens], and what the backward call needs."""
 
-    __slots__ = ("losses", "ratios", "logps", "logits", "labels", "lse", "row_grad", "row_pair")
+    __slots__ = ("losses", "ratios", "logps", "logits", "labels", "_saved")
 
 
 def preference_loss(logits, labels, offsets, ref_logps=None, beta=0.1, label_smoothing=0.0,
@@ -196,30 +250,33 @@ def preference_loss(logits, labels, offsets, ref_logps=None, beta=0.1, label_smo
     [2 * pairs + 1] on the device, the chosen sequences first, then the
     rejected ones; ``ref_logps`` float32 [tokens], the reference model's log
     probabilities of the labels.  Returns a ``PreferenceLoss``."""
-    device = _cuda(logits, "logits")
+    return _call(_cuda(logits, "logits"), stream, _loss, logits, labels, offsets, ref_logps, beta,
+                 label_smoothing, average)
+
+
+def _loss(s, logits, labels, offsets, ref_logps, beta, label_smoothing, average):
+    device = logits.device
     kind = _type(logits, "logits")
     rows, vocab, stride = _matrix(logits, "logits")
     _vector(labels, rows, torch.int64, "labels", device)
-    if offsets.dim() != 1 or offsets.numel() % 2 == 0:
+    pairs, odd = divmod(offsets.numel(), 2)
+    if not odd:
         raise ValueError("offsets: 2 * pairs + 1 values")
-    pairs = offsets.numel() // 2
     _vector(offsets, 2 * pairs + 1, torch.int64, "offsets", device)
     if ref_logps is not None:
         _vector(ref_logps, rows, torch.float32, "ref_logps", device)
     f = PreferenceLoss()
     f.logits, f.labels = logits, labels
-    with _on(device, stream) as s:
-        f.losses = torch.empty(pairs, dtype=torch.float32, device=device)
-        f.ratios = torch.empty(2 * pairs, dtype=torch.float32, device=device)
-        f.logps, f.lse, f.row_grad = (torch.empty(rows, dtype=torch.float32, device=device)
-                                      for _ in range(3))
-        f.row_pair = torch.empty(rows, dtype=torch.int32, device=device)
-        _ok(_abi.load().hkv_preference_loss(
-            pairs, rows, vocab, logits.data_ptr(), kind, stride, labels.data_ptr(),
-            offsets.data_ptr(), ref_logps.data_ptr() if ref_logps is not None else None, beta,
-            label_smoothing, int(bool(average)), f.losses.data_ptr(), f.ratios.data_ptr(),
-            f.logps.data_ptr(), f.lse.data_ptr(), f.row_grad.data_ptr(), f.row_pair.data_ptr(), s),
-            "hkv_preference_loss")
+    # losses, ratios, logps, then lse, row_grad and row_pair of 4 bytes each
+    base = torch.empty(3 * pairs + 4 * rows, dtype=torch.float32, device=device)
+    f.losses, f.ratios, f.logps, f._saved = base.split_with_sizes((pairs, 2 * pairs, rows, 3 * rows))
+    at = base.data_ptr()
+    logps = at + 12 * pairs
+    _ok(_abi.load().hkv_preference_loss(
+        pairs, rows, vocab, logits.data_ptr(), kind, stride, labels.data_ptr(), offsets.data_ptr(),
+        None if ref_logps is None else ref_logps.data_ptr(), beta, label_smoothing,
+        1 if average else 0, at, at + 4 * pairs, logps, logps + 4 * rows, logps + 8 * rows,
+        logps + 12 * rows, s), "hkv_preference_loss")
     return f
 
 
@@ -227,31 +284,34 @@ def preference_loss_backward(loss, dlosses=None, out=None, stream=None):
     """The gradient of ``(dlosses * loss.losses).sum()`` with respect to the
     logits, in their type, from what ``preference_loss`` returned.  ``out`` may be
     the logits themselves, which then hold the gradient."""
+    return _call(loss.logits.device, stream, _loss_backward, loss, dlosses, out)
+
+
+def _loss_backward(s, loss, dlosses, out):
     logits = loss.logits
     device = logits.device
     rows, vocab, stride = _matrix(logits, "logits")
     pairs = loss.losses.numel()
     if dlosses is not None:
         _vector(dlosses, pairs, torch.float32, "dlosses", device)
-    with _on(device, stream) as s:
-        if out is None:
-            out = torch.empty((rows, vocab), dtype=logits.dtype, device=device)
+    if out is None:
+        out = torch.empty((rows, vocab), dtype=logits.dtype, device=device)
+        dstride = vocab
+    else:
         if out.dtype != logits.dtype or out.shape != logits.shape:
             raise ValueError(f"out: {rows} x {vocab} of {logits.dtype}")
         _same(out, device, "out")
-        _, _, dstride = _matrix(out, "out")
-        _ok(_abi.load().hkv_preference_loss_backward(
-            pairs, rows, vocab, logits.data_ptr(), _TYPES[logits.dtype], stride,
-            loss.labels.data_ptr(), loss.lse.data_ptr(), loss.row_grad.data_ptr(),
-            loss.row_pair.data_ptr(), dlosses.data_ptr() if dlosses is not None else None,
-            out.data_ptr(), dstride, s), "hkv_preference_loss_backward")
+        dstride = _matrix(out, "out")[2]
+    saved = loss._saved.data_ptr()
+    _ok(_abi.load().hkv_preference_loss_backward(
+        pairs, rows, vocab, logits.data_ptr(), _TYPES[logits.dtype], stride, loss.labels.data_ptr(),
+        saved, saved + 4 * rows, saved + 8 * rows, None if dlosses is None else dlosses.data_ptr(),
+        out.data_ptr(), dstride, s), "hkv_preference_loss_backward")
     return out
 
 
 def _dense(t):
     """Whether the tensor's elements fill one piece of memory, in any order."""
-    if t.is_contiguous():
-        return True
     n = 1
     for stride, size in sorted((st, sz) for st, sz in zip(t.stride(), t.shape) if sz != 1):
         if stride != n:
@@ -267,36 +327,57 @@ def clip_grad_norm(grads, max_norm, outs="in place", stream=None):
     (``outs=()``: the norm alone).  Tensors have to be dense; an out tensor has
     its gradient's shape and strides."""
     grads = [grads] if isinstance(grads, torch.Tensor) else list(grads)
-    if outs is None or isinstance(outs, str):
-        if isinstance(outs, str) and outs != "in place":
-            raise ValueError(f"outs: tensors, () or 'in place', not {outs!r}")
-        targets = grads
-    else:
-        targets = [outs] if isinstance(outs, torch.Tensor) else list(outs)
-        if targets and len(targets) != len(grads):
-            raise ValueError(f"outs: {len(grads)} tensors")
     if not grads:
         raise ValueError("grads: at least one tensor")
-    device = _cuda(grads[0], "grads")
-    table = (_abi.Grad * len(grads))()
-    for i, g in enumerate(grads):
-        _same(g, device, "grads")
-        if not _dense(g):
-            raise ValueError("grads: tensors have to be dense")
-        o = targets[i] if targets else None
-        e = table[i]
-        e.data, e.n, e.type = g.data_ptr(), g.numel(), _type(g, "grads")
-        if o is not None:
-            if o is not g:
-                _same(o, device, "outs")
-                if o.shape != g.shape or (o.stride() != g.stride() and not (
-                        o.is_contiguous() and g.is_contiguous())):
-                    raise ValueError("outs: the shapes and strides of the gradients")
-            e.out, e.out_type = o.data_ptr(), _type(o, "outs")
-    with _on(device, stream) as s:
-        norm = torch.empty((), dtype=torch.float32, device=device)
-        work = torch.empty(_abi.CLIP_WORK_BYTES, dtype=torch.uint8, device=device)
-        _ok(_abi.load().hkv_clip_grad_norm(len(grads), ctypes.addressof(table), max_norm,
-                                           norm.data_ptr(), work.data_ptr(), s),
-            "hkv_clip_grad_norm")
+    if isinstance(outs, str) and outs != "in place":
+        raise ValueError(f"outs: tensors, () or 'in place', not {outs!r}")
+    if outs is None or isinstance(outs, str):
+        outs = grads
+    else:
+        outs = [outs] if isinstance(outs, torch.Tensor) else list(outs)
+        if outs and len(outs) != len(grads):
+            raise ValueError(f"outs: {len(grads)} tensors")
+    return _call(_cuda(grads[0], "grads"), stream, _clip, grads, outs, max_norm)
+
+
+def _fields(tensors, what, device):
+    """Addresses and types of dense tensors of one device, and whether all of
+    them are contiguous.  One C call per tensor and field: hundreds of tensors
+    are common here."""
+    of = torch.Tensor
+    if set(map(of.get_device, tensors)) != {device.index}:
+        raise ValueError(f"{what}: tensors of {device}")
+    plain = all(map(of.is_contiguous, tensors))
+    if not plain and not all(map(_dense, tensors)):
+        raise ValueError(f"{what}: tensors have to be dense")
+    try:
+        types = array("Q", map(_TYPES.__getitem__, map(_dtype_of, tensors)))
+    except KeyError as e:
+        raise ValueError(f"{what}: float32, bfloat16 or float16, not {e.args[0]}") from None
+    return array("Q", map(of.data_ptr, tensors)), types, plain
+
+
+def _clip(s, grads, outs, max_norm):
+    device = grads[0].device
+    n = len(grads)
+    data, types, plain = _fields(grads, "grads", device)
+    table = array("Q", bytes(32 * n))  # hkv_grad: data, out, n, type | out_type << 32
+    table[0::4] = data
+    table[2::4] = array("Q", map(torch.Tensor.numel, grads))
+    if outs is grads:
+        table[1::4] = data
+        table[3::4] = array("Q", [t | t << 32 for t in types])
+    elif outs:
+        to, out_types, out_plain = _fields(outs, "outs", device)
+        for o, g in zip(outs, grads):
+            if o.shape != g.shape or not (plain and out_plain) and o.stride() != g.stride():
+                raise ValueError("outs: the shapes and strides of the gradients")
+        table[1::4] = to
+        table[3::4] = array("Q", [t | u << 32 for t, u in zip(types, out_types)])
+    else:
+        table[3::4] = types
+    norm = torch.empty((), dtype=torch.float32, device=device)
+    work = torch.empty(_abi.CLIP_WORK_BYTES, dtype=torch.uint8, device=device)
+    _ok(_abi.load().hkv_clip_grad_norm(n, table.buffer_info()[0], max_norm, norm.data_ptr(),
+                                       work.data_ptr(), s), "hkv_clip_grad_norm")
     return norm
