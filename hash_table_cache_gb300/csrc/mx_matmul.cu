@@ -34,13 +34,19 @@ struct Problem {
   void* y;
   uint64_t stride;
   int type;
-  bool pairs;  // two neighbours of a row of a 16-bit y are stored at once
+  bool pairs;   // two neighbours of a row of a 16-bit y may be stored at once
+  bool staged;  // y is stored by TMA: its rows start on 16-byte boundaries
+  bool whole;   // and end on them
   int splits;  // thread blocks of a cluster that share a tile's k
 };
 
-struct Maps {  // the codes and the scales of A and B
-  CUtensorMap a, b, a_scales, b_scales;
+struct Maps {  // the codes and the scales of A and B, and y
+  CUtensorMap a, b, a_scales, b_scales, y;
 };
+
+// Rows of y that leave through shared memory at once, 128 columns of them: 8 KB.
+constexpr int kStageOut = 8192;
+__host__ __device__ inline int rows_out(int type) { return type == HKV_F32 ? 16 : 32; }
 
 // A tile of kBlocks * 128 rows of B by kCols rows of A, computed by one block
 // or by the two of a pair.  Either block of a pair holds its own 128 rows of
@@ -51,9 +57,10 @@ struct Shape {
   static constexpr int kACols = kCols / kBlocks;          // rows of A that a block loads
   static constexpr int kBBytes = kRows * kStepBytes, kABytes = kACols * kStepBytes;
   static constexpr int kStageBytes = kBBytes + kABytes + 1024 + 1024 * kScaleRows;
-  static constexpr int kFit = (kSmemLimit - 1024) / kStageBytes;
+  static constexpr int kFit = (kSmemLimit - 1024 - 4 * kStageOut) / kStageBytes;
   static constexpr int kStages = kFit > 10 ? 10 : kFit;
-  static constexpr int kSmem = kStages * kStageBytes + 2048;
+  static constexpr int kOutAt = kStages * kStageBytes;  // four buffers for rows of y
+  static constexpr int kSmem = kOutAt + 4 * kStageOut + 1024;
   // TMEM columns: two buffers of 256, each an accumulator and a step's scales
   static constexpr int kScaleCol = 192;
   static_assert(kCols <= kScaleCol && kScaleCol + 8 + 8 * kScaleRows <= 256, "TMEM columns");
@@ -275,6 +282,49 @@ __device__ __forceinline__ bool elect() {
   return r;
 }
 
+// The four storing warps that share a set of columns: a barrier, and whether
+// something holds for all of them.
+__device__ __forceinline__ void group_sync(int group) {
+  __syncwarp();
+  asm volatile("bar.sync %0, 128;" ::"r"(group + 1) : "memory");
+}
+__device__ __forceinline__ bool group_all(int group, bool v) {
+  uint32_t r;
+  asm volatile(
+      "{\n .reg .pred p, q;\n setp.ne.u32 p, %1, 0;\n barrier.cta.red.and.pred q, %2, 128, p;\n"
+      " selp.u32 %0, 1, 0, q;\n}"
+      : "=r"(r)
+      : "r"((uint32_t)v), "r"(group + 1)
+      : "memory");
+  return r != 0;
+}
+
+// Sixteen accumulator columns of column `j` of the tile into sixteen rows of a
+// buffer of 128 columns.
+__device__ __forceinline__ void stage_columns(uint8_t* buffer, int j, int type,
+                                              const float (&v)[16]) {
+  if (type == HKV_F32) {
+    float* to = reinterpret_cast<float*>(buffer) + j;
+#pragma unroll
+    for (int c = 0; c < 16; ++c) to[c * kRows] = v[c];
+  } else {
+    uint16_t* to = reinterpret_cast<uint16_t*>(buffer) + j;
+#pragma unroll
+    for (int c = 0; c < 16; c += 2) {
+      const uint32_t two = type == HKV_BF16 ? pack2<true>(v[c], v[c + 1]) : pack2<false>(v[c], v[c + 1]);
+      to[c * kRows] = static_cast<uint16_t>(two);
+      to[(c + 1) * kRows] = static_cast<uint16_t>(two >> 16);
+    }
+  }
+}
+// A buffer's rows to y; rows and 16-byte pieces past y are left out.
+__device__ __forceinline__ void tma_store(const CUtensorMap* map, int x, int y, const void* from) {
+  asm volatile("cp.async.bulk.tensor.2d.global.shared::cta.tile.bulk_group [%0, {%1, %2}], [%3];" ::
+                   "l"(map), "r"(x), "r"(y), "r"(smem_u32(from))
+               : "memory");
+  asm volatile("cp.async.bulk.commit_group;" ::: "memory");
+}
+
 // The tiles of a block: every `step`-th from `first`, along y's rows first.
 struct Tiles {
   uint64_t row, col, step_row, step_col, left;  // in tiles; left: tiles still to come
@@ -417,21 +467,42 @@ __global__ void __launch_bounds__(kThreads, 1)
   } else if (warp >= 2) {
     const int quarter = warp & 3, half = (warp - 2) >> 2;  // the TMEM lanes this warp can read
     const int row = quarter * 32 + lane;
-    uint32_t n_tile = 0;
+    const bool issues = quarter == 0 && lane == 0;  // this group's stores by TMA
+    uint8_t* out = smem + S::kOutAt + half * 2 * kStageOut;
+    uint32_t n_tile = 0, n_out = 0;
     for (Tiles u = t; u.left; u.next(p), ++n_tile) {
       const uint32_t b = n_tile & 1;
-      if (!wait(&ready[b], (n_tile / 2) & 1)) break;
+      // all four warps of a group go on, or none
+      if (!group_all(half, wait(&ready[b], (n_tile / 2) & 1))) break;
       asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
-      const uint64_t j = (u.col * kBlocks + half_of) * kRows + row, m0 = u.row * kCols;
-      const int cols = j - lane >= p.n     ? 0
+      const uint64_t n0 = (u.col * kBlocks + half_of) * kRows, m0 = u.row * kCols;
+      const int cols = n0 >= p.n          ? 0
                        : p.m - m0 < kCols ? static_cast<int>(p.m - m0)
                                           : kCols;
       const uint32_t d = tmem + b * 256 + (static_cast<uint32_t>(quarter * 32) << 16);
-      for (int c = 16 * half; c < cols; c += 32) {
+      // TMA writes whole 16 bytes: a ragged end of y's rows is not its work
+      const bool staged = p.staged && (p.whole || n0 + kRows <= p.n);
+      const int at_once = staged ? rows_out(p.type) : 16;
+      for (int c = at_once * half; c < cols; c += 2 * at_once) {
         float v[16];
+        if (staged) {
+          uint8_t* buffer = out + (n_out++ & 1) * kStageOut;
+          if (issues)  // the buffer's rows of two rounds ago have left it
+            asm volatile("cp.async.bulk.wait_group.read 1;" ::: "memory");
+          group_sync(half);
+          for (int q = 0; q < at_once && c + q < cols; q += 16) {
+            read_columns(d + c + q, v);
+            stage_columns(buffer + q * kRows * (p.type == HKV_F32 ? 4 : 2), row, p.type, v);
+          }
+          fence_proxy_async_smem();
+          group_sync(half);
+          if (issues)
+            tma_store(&maps.y, static_cast<int>(n0), static_cast<int>(m0 + c), buffer);
+          continue;
+        }
         read_columns(d + c, v);
         if (splits == 1) {
-          store_columns(p, m0 + c, j, v);
+          store_columns(p, m0 + c, n0 + row, v);
         } else {  // this block's part of the sum, for the cluster to add up
           float* mine = reinterpret_cast<float*>(smem) + row;
 #pragma unroll
@@ -445,6 +516,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         else mbar_arrive(&drained[b]);
       }
     }
+    if (issues) asm volatile("cp.async.bulk.wait_group 0;" ::: "memory");
   }
   __syncwarp();
   if (splits > 1) {
@@ -512,6 +584,20 @@ bool make_maps(CUtensorMap* codes_map, CUtensorMap* scales_map, const uint8_t* c
            CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
+// y as boxes of 128 columns.
+bool make_y_map(CUtensorMap* map, const Problem& p) {
+  const CUtensorMapDataType type = p.type == HKV_F32    ? CU_TENSOR_MAP_DATA_TYPE_FLOAT32
+                                   : p.type == HKV_BF16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16
+                                                        : CU_TENSOR_MAP_DATA_TYPE_FLOAT16;
+  const cuuint32_t steps[2] = {1, 1};
+  const cuuint64_t dims[2] = {p.n, p.m}, strides[1] = {p.stride * type_size(p.type)};
+  const cuuint32_t boxes[2] = {kRows, static_cast<cuuint32_t>(rows_out(p.type))};
+  EncodeFn f = encode_fn();
+  return f && f(map, type, 2, p.y, dims, strides, boxes, steps, CU_TENSOR_MAP_INTERLEAVE_NONE,
+                CU_TENSOR_MAP_SWIZZLE_NONE, CU_TENSOR_MAP_L2_PROMOTION_NONE,
+                CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
 struct Operands {
   const uint8_t *a_codes, *a_scales, *b_codes, *b_scales;
 };
@@ -529,10 +615,15 @@ cudaError_t run(Problem p, const Operands& o, cudaStream_t st) {
   while (kBlocks == 1 && p.splits < kMaxSplits && tiles * p.splits * 2 <= sms &&
          steps >= 4ull * p.splits)
     p.splits *= 2;
-  Maps maps;
+  Maps maps{};
   if (!make_maps(&maps.a, &maps.a_scales, o.a_codes, o.a_scales, p.m, p.k, S::kACols, S::kScaleRows) ||
       !make_maps(&maps.b, &maps.b_scales, o.b_codes, o.b_scales, p.n, p.k, kRows, 1))
     return cudaErrorUnknown;
+  // TMA wants 16-byte boundaries and a stride below 2^40 bytes
+  const uint64_t row_bytes = p.stride * type_size(p.type);
+  p.staged = p.splits == 1 && aligned(p.y, 16) && row_bytes % 16 == 0 && row_bytes < 1ull << 40;
+  p.whole = p.n * type_size(p.type) % 16 == 0;
+  if (p.staged && !make_y_map(&maps.y, p)) return cudaErrorUnknown;
   auto* kernel = matmul_kernel<kCols, kBlocks>;
   cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, S::kSmem);
   if (e != cudaSuccess) return e;
