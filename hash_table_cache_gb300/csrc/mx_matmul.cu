@@ -1,17 +1,26 @@
 // mx_matmul.cu -- hkv_mx_matmul: the product of two 4-bit microscaled matrices
 // on the block-scaled 4-bit tensor cores.
 //
-// y[i][j] = sum_k A[i][k] B[j][k].  The rows of B are the rows of the tensor
-// core's tile (128 of them, one TMEM lane each) and the rows of A its columns
-// (16 to 192 of them), so one token still fills a tile with 128 useful rows,
-// and a store of one TMEM column is contiguous along y's rows whatever y's
-// alignment.  A step of k is 256 columns: 128 bytes of codes per row, brought
-// by TMA in the 128-byte swizzle the tensor core reads, and two 512-byte
-// groups of scales per 128 rows, which the format stores as they are copied
-// to TMEM.  One warp loads, one issues the copies of scales and the products,
-// four read the accumulators out; accumulators and scales are held twice, so
-// a tile's output leaves while the next one is computed.
+// y[i][j] = sum_k A[i][k] B[j][k].  One of the two matrices lies along the
+// lanes of the tensor core's tile (128 rows, one TMEM lane each, or 256 for a
+// pair of blocks), the other along its columns (16 to 192).  A step of k is
+// 256 columns: 128 bytes of codes per row, brought by TMA in the 128-byte
+// swizzle the tensor core reads, and two 512-byte groups of scales per 128
+// rows, which the format stores as they are copied to TMEM.  One warp loads,
+// one issues the copies of scales and the products, eight read the
+// accumulators out; accumulators and scales are held twice, so a tile's
+// output leaves while the next one is computed.
+//
+// TMEM hands a thread one lane: neighbouring columns of one row of the tile.
+// With A in the lanes that is a piece of a row of y, and a warp turns its 32
+// pieces around in shared memory so that a store covers whole 128-byte lines
+// (a thread storing its own piece, a 32-byte sector of 32 rows at once,
+// reached 4.4 TB/s of y where this reaches 5.8: 2048 x 131072 x 64).  With B in the lanes a warp's
+// lanes are 32 neighbouring columns of one row of y: that is for the few rows
+// of a token or a small batch, which would leave most lanes empty the other
+// way, and for a y whose rows do not start on 16-byte boundaries.
 #include <cuda.h>
+#include <type_traits>
 
 #include "mx.cuh"
 
@@ -29,42 +38,45 @@ constexpr int kMaxSplits = 8;
 constexpr unsigned kSmemLimit = 232448 - 1024;  // 227 KB less the alignment of the stages
 
 struct Problem {
-  uint64_t m, n, k;
-  uint64_t tiles_m, tiles_n;
+  uint64_t lanes, cols, k;      // rows of the matrix in the lanes and of the one in the columns
+  uint32_t along, down;         // tiles along y's rows and down its columns
   void* y;
   uint64_t stride;
   int type;
-  bool pairs;   // two neighbours of a row of a 16-bit y may be stored at once
-  bool staged;  // y is stored by TMA: its rows start on 16-byte boundaries
-  bool whole;   // and end on them
+  bool wide;   // y's rows start on 16-byte boundaries
   int splits;  // thread blocks of a cluster that share a tile's k
 };
 
-struct Maps {  // the codes and the scales of A and B, and y
-  CUtensorMap a, b, a_scales, b_scales, y;
+// Where a warp turns 32 pieces of rows around: 128 bytes and 16 of padding
+// each, so that neither side of the turn meets a bank twice.
+constexpr int kTurnPitch = 144, kTurnWarp = 32 * kTurnPitch;
+
+struct Maps {  // codes and scales of the two matrices
+  CUtensorMap lanes, cols, lanes_scales, cols_scales;
 };
 
-// Rows of y that leave through shared memory at once, 128 columns of them: 8 KB.
-constexpr int kStageOut = 8192;
-__host__ __device__ inline int rows_out(int type) { return type == HKV_F32 ? 16 : 32; }
-
-// A tile of kBlocks * 128 rows of B by kCols rows of A, computed by one block
-// or by the two of a pair.  Either block of a pair holds its own 128 rows of
-// B, half of the rows of A, and the scales of its rows of B and of all of A's.
+// A tile of kBlocks * 128 lanes by kCols columns, computed by one block or by
+// the two of a pair.  Either block of a pair holds its own 128 rows of the
+// lanes' matrix, half of the columns' matrix's rows, and the scales of its
+// lanes and of all columns.
 template <int kCols, int kBlocks>
 struct Shape {
-  static constexpr int kScaleRows = kCols > 128 ? 2 : 1;  // groups of 128 rows of A that a tile spans
-  static constexpr int kACols = kCols / kBlocks;          // rows of A that a block loads
-  static constexpr int kBBytes = kRows * kStepBytes, kABytes = kACols * kStepBytes;
-  static constexpr int kStageBytes = kBBytes + kABytes + 1024 + 1024 * kScaleRows;
-  static constexpr int kFit = (kSmemLimit - 1024 - 4 * kStageOut) / kStageBytes;
+  static constexpr int kScaleRows = kCols > 128 ? 2 : 1;  // groups of 128 rows that the columns span
+  static constexpr int kOwnCols = kCols / kBlocks;        // columns' rows that a block loads
+  static constexpr int kLaneBytes = kRows * kStepBytes, kColBytes = kOwnCols * kStepBytes;
+  static constexpr int kStageBytes = kLaneBytes + kColBytes + 1024 + 1024 * kScaleRows;
+  // columns that one group of four storing warps takes
+  static constexpr int kGroupCols = kCols > 32 ? kCols / 2 : 16;
+  static constexpr int kGroups = kCols / kGroupCols;
+  static constexpr int kTurnBytes = kCols == 192 ? kStoreWarps * kTurnWarp : 0;
+  static constexpr int kFit = (kSmemLimit - 1024 - kTurnBytes) / kStageBytes;
   static constexpr int kStages = kFit > 10 ? 10 : kFit;
-  static constexpr int kOutAt = kStages * kStageBytes;  // four buffers for rows of y
-  static constexpr int kSmem = kOutAt + 4 * kStageOut + 1024;
+  static constexpr int kTurnAt = kStages * kStageBytes;
+  static constexpr int kSmem = kTurnAt + kTurnBytes + 1024;
   // TMEM columns: two buffers of 256, each an accumulator and a step's scales
   static constexpr int kScaleCol = 192;
   static_assert(kCols <= kScaleCol && kScaleCol + 8 + 8 * kScaleRows <= 256, "TMEM columns");
-  static_assert(kABytes % 1024 == 0, "swizzle");
+  static_assert(kColBytes % 1024 == 0, "swizzle");
 };
 
 // Bounded wait for a phase of a barrier: false after kWaitNs, with the
@@ -120,16 +132,15 @@ __device__ __forceinline__ void tma_load(void* dst, const CUtensorMap* map, int 
         : "memory");
 }
 
-// Shared-memory descriptors: version 1, K-major.  Codes: rows of 128 bytes in
+// Shared-memory descriptors, version 1, K-major.  Codes: rows of 128 bytes in
 // the 128-byte swizzle, 1024 bytes from one group of 8 rows to the next.
-// Scales: 32 rows of 16 bytes without a swizzle, 128 bytes per 8 rows.
-__device__ __forceinline__ uint64_t codes_desc(uint32_t addr) {
-  return (uint64_t)((addr & 0x3FFFF) >> 4) | 1ull << 16 | (1024ull >> 4) << 32 | 1ull << 46 |
-         2ull << 61;
-}
-__device__ __forceinline__ uint64_t scales_desc(uint32_t addr) {
-  return (uint64_t)((addr & 0x3FFFF) >> 4) | (128ull >> 4) << 32 | 1ull << 46;
-}
+// Scales: 32 rows of 16 bytes without a swizzle, 128 bytes per 8 rows.  The
+// upper halves are constants; the lower halves hold the address in 16-byte
+// units, in which the issuing thread counts.
+constexpr uint32_t kCodesDesc = (1024 >> 4) | 1u << 14 | 2u << 29;
+constexpr uint32_t kScalesDesc = (128 >> 4) | 1u << 14;
+__device__ __forceinline__ uint32_t desc_units(uint32_t addr) { return (addr & 0x3FFFF) >> 4; }
+
 // Instruction descriptor of the block-scaled e2m1 product: both types e2m1,
 // ue8m0 scales, `cols` columns, 128 or 256 rows, the pair of a scale word's
 // bytes that a product of 64 columns takes (0 or 2).
@@ -141,30 +152,38 @@ __host__ __device__ constexpr uint32_t product_desc(int blocks, int cols, int pa
 // For a pair, the first block's thread issues these for both blocks: each
 // copies its own scales and multiplies its own rows of B by both halves of A.
 template <int kBlocks>
-__device__ __forceinline__ void copy_scales(uint32_t tmem, uint64_t desc) {
-  if constexpr (kBlocks == 2)
-    asm volatile("tcgen05.cp.cta_group::2.32x128b.warpx4 [%0], %1;" ::"r"(tmem), "l"(desc)
-                 : "memory");
-  else
-    asm volatile("tcgen05.cp.cta_group::1.32x128b.warpx4 [%0], %1;" ::"r"(tmem), "l"(desc)
-                 : "memory");
-}
-template <int kBlocks>
-__device__ __forceinline__ void product(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc,
-                                        uint32_t sa, uint32_t sb, bool add) {
+__device__ __forceinline__ void copy_scales(uint32_t tmem, uint32_t from) {
   if constexpr (kBlocks == 2)
     asm volatile(
-        "{\n .reg .pred p;\n setp.ne.u32 p, %6, 0;\n"
-        " tcgen05.mma.cta_group::2.kind::mxf4.block_scale.scale_vec::2X [%0], %1, %2, %3, [%4], [%5], p;\n}" ::
-            "r"(d),
-        "l"(a), "l"(b), "r"(idesc), "r"(sa), "r"(sb), "r"((uint32_t)add)
+        "{\n .reg .b64 d;\n mov.b64 d, {%1, %2};\n"
+        " tcgen05.cp.cta_group::2.32x128b.warpx4 [%0], d;\n}" ::"r"(tmem),
+        "r"(from), "n"(kScalesDesc)
         : "memory");
   else
     asm volatile(
-        "{\n .reg .pred p;\n setp.ne.u32 p, %6, 0;\n"
-        " tcgen05.mma.cta_group::1.kind::mxf4.block_scale.scale_vec::2X [%0], %1, %2, %3, [%4], [%5], p;\n}" ::
+        "{\n .reg .b64 d;\n mov.b64 d, {%1, %2};\n"
+        " tcgen05.cp.cta_group::1.32x128b.warpx4 [%0], d;\n}" ::"r"(tmem),
+        "r"(from), "n"(kScalesDesc)
+        : "memory");
+}
+template <int kBlocks>
+__device__ __forceinline__ void product(uint32_t d, uint32_t lanes, uint32_t cols, uint32_t idesc,
+                                        uint32_t s_lanes, uint32_t s_cols, uint32_t add) {
+  if constexpr (kBlocks == 2)
+    asm volatile(
+        "{\n .reg .pred p;\n .reg .b64 a, b;\n setp.ne.u32 p, %6, 0;\n"
+        " mov.b64 a, {%1, %7};\n mov.b64 b, {%2, %7};\n"
+        " tcgen05.mma.cta_group::2.kind::mxf4.block_scale.scale_vec::2X [%0], a, b, %3, [%4], [%5], p;\n}" ::
             "r"(d),
-        "l"(a), "l"(b), "r"(idesc), "r"(sa), "r"(sb), "r"((uint32_t)add)
+        "r"(lanes), "r"(cols), "r"(idesc), "r"(s_lanes), "r"(s_cols), "r"(add), "n"(kCodesDesc)
+        : "memory");
+  else
+    asm volatile(
+        "{\n .reg .pred p;\n .reg .b64 a, b;\n setp.ne.u32 p, %6, 0;\n"
+        " mov.b64 a, {%1, %7};\n mov.b64 b, {%2, %7};\n"
+        " tcgen05.mma.cta_group::1.kind::mxf4.block_scale.scale_vec::2X [%0], a, b, %3, [%4], [%5], p;\n}" ::
+            "r"(d),
+        "r"(lanes), "r"(cols), "r"(idesc), "r"(s_lanes), "r"(s_cols), "r"(add), "n"(kCodesDesc)
         : "memory");
 }
 // The barrier (in both blocks of a pair) is reached when the products issued
@@ -204,15 +223,27 @@ __device__ __forceinline__ void give_tmem(uint32_t tmem) {
   else
     asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, 512;" ::"r"(tmem));
 }
-__device__ __forceinline__ void read_columns(uint32_t tmem, float (&v)[16]) {
-  uint32_t* r = reinterpret_cast<uint32_t*>(v);
-  asm volatile(
-      "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15}, [%16];"
-      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]),
-        "=r"(r[7]), "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]),
-        "=r"(r[14]), "=r"(r[15])
-      : "r"(tmem));
+// kN accumulator columns of this warp's TMEM lanes into v from kFrom on, on
+// their way until columns_read().
+template <int kFrom, int kN, int N>
+__device__ __forceinline__ void read_columns(uint32_t tmem, float (&v)[N]) {
+  static_assert(kN % 16 == 0 && kFrom + kN <= N, "columns");
+#pragma unroll
+  for (int c = 0; c < kN; c += 16) {
+    uint32_t* r = reinterpret_cast<uint32_t*>(v) + kFrom + c;
+    asm volatile(
+        "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15}, [%16];"
+        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]),
+          "=r"(r[7]), "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]),
+          "=r"(r[14]), "=r"(r[15])
+        : "r"(tmem + c));
+  }
+}
+template <int N>
+__device__ __forceinline__ void columns_read(float (&v)[N]) {
   asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
+#pragma unroll
+  for (int c = 0; c < N; ++c) asm volatile("" : "+f"(v[c]));  // used after the wait only
 }
 
 __device__ __forceinline__ void store_one(const Problem& p, uint64_t i, uint64_t j, float v) {
@@ -231,45 +262,73 @@ __device__ __forceinline__ uint32_t pack2(float lo, float hi) {
   return *reinterpret_cast<const uint32_t*>(&h);
 }
 
-// Sixteen accumulator columns (rows i .. i + 15 of y, all of them in y) of
-// this lane's column j of a 16-bit y: neighbouring lanes trade values, so
-// that an even lane stores both lanes' columns of one row and the odd lane
-// those of the next, 4 bytes at a time.
-template <bool kBf16>
-__device__ __forceinline__ void store_pairs(const Problem& p, uint64_t i, uint64_t j,
-                                            const float (&v)[16]) {
-  const uint32_t odd = j & 1, pick = odd ? 0x3276 : 0x5410;
-  const uint64_t step = 4 * p.stride;
-  char* y = static_cast<char*>(p.y) + ((i + odd) * p.stride + (j & ~1ull)) * 2;
+// B in the lanes: N accumulator columns are rows of y from i on, of this
+// lane's column j.
+template <int N>
+__device__ __forceinline__ void store_columns(const Problem& p, uint64_t i, uint64_t j,
+                                              const float (&v)[N]) {
+  if (j >= p.lanes) return;
+  if (i + N <= p.cols && p.type != HKV_F32) {  // no test per row
+    uint16_t* y = static_cast<uint16_t*>(p.y) + i * p.stride + j;
 #pragma unroll
-  for (int c = 0; c < 16; c += 2) {
-    const uint32_t own = pack2<kBf16>(v[c], v[c + 1]);
-    const uint32_t other = __shfl_xor_sync(0xFFFFFFFFu, own, 1);
-    *reinterpret_cast<uint32_t*>(y) = __byte_perm(own, other, pick);
-    y += step;
+    for (int c = 0; c < N; c += 2) {
+      const uint32_t two = p.type == HKV_BF16 ? pack2<true>(v[c], v[c + 1]) : pack2<false>(v[c], v[c + 1]);
+      *y = static_cast<uint16_t>(two);
+      y[p.stride] = static_cast<uint16_t>(two >> 16);
+      y += 2 * p.stride;
+    }
+    return;
   }
+#pragma unroll
+  for (int c = 0; c < N; ++c)
+    if (i + c < p.cols) store_one(p, i + c, j, v[c]);
 }
 
-// Sixteen accumulator columns of this lane's column j.
-__device__ __forceinline__ void store_columns(const Problem& p, uint64_t i, uint64_t j,
-                                              const float (&v)[16]) {
-  // a whole warp's columns lie in y, and all sixteen rows
-  const bool inside = i + 16 <= p.m && (j | 31) < p.n;
-  if (inside && p.pairs) {
-    if (p.type == HKV_BF16) store_pairs<true>(p, i, j, v);
-    else store_pairs<false>(p, i, j, v);
-  } else if (inside && p.type == HKV_F32) {
-    char* y = reinterpret_cast<char*>(static_cast<float*>(p.y) + i * p.stride + j);
+// A in the lanes: columns kFrom .. kFrom + kN - 1 of v are columns j ..
+// j + kN - 1 of y; the warp's lanes are its rows from i on.
+template <int kType, int kFrom, int kN, int N>
+__device__ __forceinline__ void turn_and_store(uint8_t* room, const Problem& p, uint64_t i,
+                                               uint64_t j, const float (&v)[N]) {
+  constexpr int kSize = kType == HKV_F32 ? 4 : 2, kPer = 16 / kSize;
+  constexpr int kLanes = kN * kSize / 16;  // threads that store a row's piece, 16 bytes each
+  static_assert(kN * kSize <= 128 && 32 % kLanes == 0, "a piece of a row");
+  const int lane = threadIdx.x & 31;
 #pragma unroll
-    for (int c = 0; c < 16; ++c) {
-      *reinterpret_cast<float*>(y) = v[c];
-      y += 4 * p.stride;
-    }
-  } else if (j < p.n) {
+  for (int c = 0; c < kN; c += kPer) {
+    uint32_t w[4];
 #pragma unroll
-    for (int c = 0; c < 16; ++c)
-      if (i + c < p.m) store_one(p, i + c, j, v[c]);
+    for (int e = 0; e < 4; ++e)
+      w[e] = kType == HKV_F32 ? __float_as_uint(v[kFrom + c + e])
+                              : pack2<kType == HKV_BF16>(v[kFrom + c + 2 * e % kPer],
+                                                         v[kFrom + c + (2 * e + 1) % kPer]);
+    *reinterpret_cast<uint4*>(room + lane * kTurnPitch + c * kSize) = make_uint4(w[0], w[1], w[2], w[3]);
   }
+  __syncwarp();
+  const int first = lane / kLanes, at = lane % kLanes;
+  const uint64_t col = j + at * kPer;
+  const uint8_t* from = room + first * kTurnPitch + at * 16;
+  char* y = static_cast<char*>(p.y) + ((i + first) * p.stride + col) * kSize;
+  const uint64_t step = 32 / kLanes * p.stride * kSize;
+  if (i + 32 <= p.lanes && col + kPer <= p.cols) {
+#pragma unroll
+    for (int r = 0; r < kLanes; ++r, y += step)
+      st_stream_v4(y, *reinterpret_cast<const uint4*>(from + r * (32 / kLanes) * kTurnPitch));
+  } else {  // the ends of y
+    for (int r = 0; r < kLanes; ++r, y += step, from += 32 / kLanes * kTurnPitch) {
+      if (i + first + r * (32 / kLanes) >= p.lanes) break;
+      if (col + kPer <= p.cols) {
+        st_stream_v4(y, *reinterpret_cast<const uint4*>(from));
+        continue;
+      }
+      for (int e = 0; e < kPer && col + e < p.cols; ++e) {
+        if constexpr (kSize == 4)
+          reinterpret_cast<float*>(y)[e] = reinterpret_cast<const float*>(from)[e];
+        else
+          reinterpret_cast<uint16_t*>(y)[e] = reinterpret_cast<const uint16_t*>(from)[e];
+      }
+    }
+  }
+  __syncwarp();
 }
 
 // One lane of a converged warp.  What only that lane does is then known to be
@@ -282,72 +341,33 @@ __device__ __forceinline__ bool elect() {
   return r;
 }
 
-// The four storing warps that share a set of columns: a barrier, and whether
-// something holds for all of them.
-__device__ __forceinline__ void group_sync(int group) {
-  __syncwarp();
-  asm volatile("bar.sync %0, 128;" ::"r"(group + 1) : "memory");
-}
-__device__ __forceinline__ bool group_all(int group, bool v) {
-  uint32_t r;
-  asm volatile(
-      "{\n .reg .pred p, q;\n setp.ne.u32 p, %1, 0;\n barrier.cta.red.and.pred q, %2, 128, p;\n"
-      " selp.u32 %0, 1, 0, q;\n}"
-      : "=r"(r)
-      : "r"((uint32_t)v), "r"(group + 1)
-      : "memory");
-  return r != 0;
-}
-
-// Sixteen accumulator columns of column `j` of the tile into sixteen rows of a
-// buffer of 128 columns.
-__device__ __forceinline__ void stage_columns(uint8_t* buffer, int j, int type,
-                                              const float (&v)[16]) {
-  if (type == HKV_F32) {
-    float* to = reinterpret_cast<float*>(buffer) + j;
-#pragma unroll
-    for (int c = 0; c < 16; ++c) to[c * kRows] = v[c];
-  } else {
-    uint16_t* to = reinterpret_cast<uint16_t*>(buffer) + j;
-#pragma unroll
-    for (int c = 0; c < 16; c += 2) {
-      const uint32_t two = type == HKV_BF16 ? pack2<true>(v[c], v[c + 1]) : pack2<false>(v[c], v[c + 1]);
-      to[c * kRows] = static_cast<uint16_t>(two);
-      to[(c + 1) * kRows] = static_cast<uint16_t>(two >> 16);
-    }
-  }
-}
-// A buffer's rows to y; rows and 16-byte pieces past y are left out.
-__device__ __forceinline__ void tma_store(const CUtensorMap* map, int x, int y, const void* from) {
-  asm volatile("cp.async.bulk.tensor.2d.global.shared::cta.tile.bulk_group [%0, {%1, %2}], [%3];" ::
-                   "l"(map), "r"(x), "r"(y), "r"(smem_u32(from))
-               : "memory");
-  asm volatile("cp.async.bulk.commit_group;" ::: "memory");
-}
-
-// The tiles of a block: every `step`-th from `first`, along y's rows first.
+// The tiles of a block: every `step`-th from `first`, in an order that goes down
+// kDown tiles of y before it goes along its rows: the blocks that run side by
+// side then share their lanes' matrix with few and their columns' with few,
+// and no line of L2 is asked for by all of them at once.
+constexpr uint32_t kDown = 8;
 struct Tiles {
-  uint64_t row, col, step_row, step_col, left;  // in tiles; left: tiles still to come
-  __device__ __forceinline__ Tiles(const Problem& p, uint64_t first, uint64_t step) {
-    const uint64_t all = p.tiles_m * p.tiles_n;
-    row = first / p.tiles_n;
-    col = first % p.tiles_n;
-    step_row = step / p.tiles_n;
-    step_col = step % p.tiles_n;
-    left = first < all ? (all - first + step - 1) / step : 0;
+  uint32_t row, col, at, step, all;
+  __device__ __forceinline__ Tiles(const Problem& p, uint32_t first, uint32_t by)
+      : at(first), step(by), all(p.down * p.along) {
+    place(p);
   }
+  __device__ __forceinline__ void place(const Problem& p) {
+    const uint32_t band = at / (kDown * p.along), rest = at % (kDown * p.along);
+    const uint32_t high = min(kDown, p.down - min(p.down, band * kDown));
+    if (high == 0) return;  // past the last tile
+    col = rest / high;
+    row = band * kDown + rest % high;
+  }
+  __device__ __forceinline__ bool left() const { return at < all; }
   __device__ __forceinline__ void next(const Problem& p) {
-    row += step_row;
-    col += step_col;
-    if (col >= p.tiles_n) {
-      col -= p.tiles_n;
-      ++row;
-    }
-    --left;
+    at += step;
+    place(p);
   }
 };
 
-template <int kCols, int kBlocks>
+// kAInLanes: the rows of A in the lanes, else the rows of B.
+template <int kCols, int kBlocks, bool kAInLanes>
 __global__ void __launch_bounds__(kThreads, 1)
     matmul_kernel(const __grid_constant__ Maps maps, const __grid_constant__ Problem p) {
   using S = Shape<kCols, kBlocks>;
@@ -358,9 +378,9 @@ __global__ void __launch_bounds__(kThreads, 1)
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   // The blocks of a cluster: a pair (kBlocks 2), or the `splits` that share a
   // tile's k (kBlocks 1).
-  const uint32_t splits = kBlocks == 2 ? 1 : p.splits;
+  const uint32_t splits = kBlocks == 2 || kAInLanes ? 1 : p.splits;
   const uint32_t rank = blockIdx.x % (splits * kBlocks);
-  const uint32_t half_of = kBlocks == 2 ? rank : 0, part = kBlocks == 2 ? 0 : rank;
+  const uint32_t half_of = kBlocks == 2 ? rank : 0, part = splits > 1 ? rank : 0;
 
   if (warp == 0 && lane == 0) {
     for (int s = 0; s < S::kStages; ++s) {
@@ -383,80 +403,93 @@ __global__ void __launch_bounds__(kThreads, 1)
   pdl_wait();  // every role: the bounded waits below start when the inputs are there
 
   Tiles t(p, blockIdx.x / (splits * kBlocks), gridDim.x / (splits * kBlocks));
-  const uint64_t all = (p.k + kStep - 1) / kStep;
-  const uint64_t k0 = all * part / splits, k1 = all * (part + 1) / splits;
+  const uint32_t all = static_cast<uint32_t>((p.k + kStep - 1) / kStep);
+  const uint32_t k0 = static_cast<uint64_t>(all) * part / splits;
+  const uint32_t k1 = static_cast<uint64_t>(all) * (part + 1) / splits;
 
   if (warp == 0 && elect()) {
-    uint32_t it = 0;
+    uint32_t s = 0, round = 0;  // the next stage, and how often the stages have been used up
     bool ok = true;
-    for (; t.left && ok; t.next(p)) {
-      const int n0 = static_cast<int>((t.col * kBlocks + half_of) * kRows);
-      const uint64_t m0 = t.row * kCols;
-      for (uint64_t k = k0; k < k1; ++k, ++it) {
-        const uint32_t s = it % S::kStages;
-        if (it >= S::kStages && !wait(&empty[s], (it / S::kStages + 1) & 1)) {
+    const uint32_t bars = kBlocks == 2 ? cluster_address(&full[0], 0) : smem_u32(&full[0]);
+    for (; t.left() && ok; t.next(p)) {
+      const int lane0 =
+          static_cast<int>((static_cast<uint64_t>(kAInLanes ? t.row : t.col) * kBlocks + half_of) * kRows);
+      const int col0 = static_cast<int>(static_cast<uint64_t>(kAInLanes ? t.col : t.row) * kCols);
+      for (uint32_t k = k0; k < k1; ++k) {
+        if (round > 0 && !wait(&empty[s], (round + 1) & 1)) {
           ok = false;
           break;
         }
         uint8_t* stage = smem + s * S::kStageBytes;
-        uint8_t* scales = stage + S::kBBytes + S::kABytes;
+        uint8_t* scales = stage + S::kLaneBytes + S::kColBytes;
         const int x = static_cast<int>(k * kStepBytes), xs = static_cast<int>(k * 256);
-        uint32_t bar = smem_u32(&full[s]);
-        if (kBlocks == 2) bar = cluster_address(&full[s], 0);
+        const uint32_t bar = bars + 8 * s;
         if (half_of == 0) mbar_arrive_expect_tx(&full[s], kBlocks * S::kStageBytes);
-        tma_load<kBlocks>(stage, &maps.b, x, n0, bar);
-        tma_load<kBlocks>(stage + S::kBBytes, &maps.a, x,
-                          static_cast<int>(m0 + half_of * S::kACols), bar);
-        tma_load<kBlocks>(scales, &maps.b_scales, xs, n0 / 128, bar);
-        tma_load<kBlocks>(scales + 1024, &maps.a_scales, xs, static_cast<int>(m0 / 128), bar);
+        tma_load<kBlocks>(stage, &maps.lanes, x, lane0, bar);
+        tma_load<kBlocks>(stage + S::kLaneBytes, &maps.cols, x, col0 + half_of * S::kOwnCols, bar);
+        tma_load<kBlocks>(scales, &maps.lanes_scales, xs, lane0 / 128, bar);
+        tma_load<kBlocks>(scales + 1024, &maps.cols_scales, xs, col0 / 128, bar);
+        if (++s == S::kStages) {
+          s = 0;
+          ++round;
+        }
       }
     }
     // Before the block ends: the loads still in flight where a wait ran out,
     // and in a pair the products' arrivals on this block's barriers.
     if (!ok || kBlocks == 2)
-      for (uint32_t i = it > S::kStages ? it - S::kStages : 0; i < it; ++i)
-        if (!wait(ok ? &empty[i % S::kStages] : &full[i % S::kStages], (i / S::kStages) & 1)) break;
+      for (uint32_t i = 0; i < S::kStages; ++i) {
+        const uint32_t uses = round + (i < s);
+        if (uses && !wait(ok ? &empty[i] : &full[i], (uses + 1) & 1)) break;
+      }
   } else if (warp == 1 && half_of == 0 && elect()) {
-    uint32_t it = 0, n_tile = 0;
+    // This thread sets the pace: a step is 4 products of 70 to 80 cycles each,
+    // so everything that does not change from step to step is outside.
+    uint32_t s = 0, parity = 0, set = 0, n_tile = 0;
     bool ok = true;
-    for (; t.left && ok; t.next(p), ++n_tile) {
+    const uint32_t units = desc_units(smem_u32(smem));
+    const uint32_t rest = static_cast<uint32_t>(p.k % kStep);
+    const int last = rest == 0 ? 4 : static_cast<int>((rest + 63) / 64);  // products of the last step
+    for (; t.left() && ok; t.next(p), ++n_tile) {
       const uint32_t b = n_tile & 1;
       const uint32_t d = tmem + b * 256;
       // the scales of a tile that starts in the middle of a group of 128 rows
       // (192 columns: at 0 or 64, so that the shift is even, as it has to be)
-      const uint32_t shift = kCols > 128 ? t.row * kCols % 128 / 32 : 0;
+      const uint32_t shift = kCols > 128 ? (kAInLanes ? t.col : t.row) % 2 * 2 : 0;
       if (n_tile >= 2 && !wait(&drained[b], (n_tile / 2 + 1) & 1)) break;
       asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
-      for (uint64_t k = k0; k < k1; ++k, ++it) {
-        const uint32_t s = it % S::kStages;
-        if (!wait(&full[s], (it / S::kStages) & 1)) {
+      for (uint32_t k = k0; k < k1; ++k) {
+        if (!wait(&full[s], parity)) {
           ok = false;
           break;
         }
         asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
-        const uint32_t stage = smem_u32(smem) + s * S::kStageBytes;
-        const uint32_t sc = stage + S::kBBytes + S::kABytes;
-        const uint64_t db = codes_desc(stage), da = codes_desc(stage + S::kBBytes);
+        const uint32_t lanes = units + s * (S::kStageBytes / 16), cols = lanes + S::kLaneBytes / 16;
+        const uint32_t sc = cols + S::kColBytes / 16;
         // two sets of scale columns, used by turns: a step's copies do not
         // wait for the products of the step before
-        const uint32_t sb = tmem + (it & 1) * 256 + S::kScaleCol, sa = sb + 8;
-        const int products = p.k - k * kStep >= kStep ? 4 : static_cast<int>((p.k - k * kStep + 63) / 64);
+        const uint32_t s_lanes = tmem + S::kScaleCol + set, s_cols = s_lanes + 8;
 #pragma unroll
         for (int g = 0; g < 2; ++g) {
-          copy_scales<kBlocks>(sb + 4 * g, scales_desc(sc + 512 * g));
+          copy_scales<kBlocks>(s_lanes + 4 * g, sc + 32 * g);
 #pragma unroll
           for (int r = 0; r < S::kScaleRows; ++r)
-            copy_scales<kBlocks>(sa + 4 * (S::kScaleRows * g + r),
-                                 scales_desc(sc + 1024 + 1024 * r + 512 * g));
+            copy_scales<kBlocks>(s_cols + 4 * (S::kScaleRows * g + r), sc + 64 + 64 * r + 32 * g);
         }
+        const int products = k + 1 == all ? last : 4;
 #pragma unroll
         for (int q = 0; q < 4; ++q) {
-          if (q >= products) break;
-          product<kBlocks>(d, db + 2 * q, da + 2 * q, product_desc(kBlocks, kCols, 2 * (q & 1)),
-                           sb + 4 * (q / 2), sa + 4 * S::kScaleRows * (q / 2) + shift,
-                           k > k0 || q > 0);
+          if (q > 0 && q >= products) break;
+          product<kBlocks>(d, lanes + 2 * q, cols + 2 * q, product_desc(kBlocks, kCols, 2 * (q & 1)),
+                           s_lanes + 4 * (q / 2), s_cols + shift + 4 * S::kScaleRows * (q / 2),
+                           q > 0 ? 1 : k - k0);
         }
         commit<kBlocks>(&empty[s]);
+        set ^= 256;
+        if (++s == S::kStages) {
+          s = 0;
+          parity ^= 1;
+        }
       }
       if (ok) commit<kBlocks>(&ready[b]);
     }
@@ -466,48 +499,30 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
   } else if (warp >= 2) {
     const int quarter = warp & 3, half = (warp - 2) >> 2;  // the TMEM lanes this warp can read
-    const int row = quarter * 32 + lane;
-    const bool issues = quarter == 0 && lane == 0;  // this group's stores by TMA
-    uint8_t* out = smem + S::kOutAt + half * 2 * kStageOut;
-    uint32_t n_tile = 0, n_out = 0;
-    for (Tiles u = t; u.left; u.next(p), ++n_tile) {
+    // This group's columns of a tile: neighbours, or with A in the lanes 64
+    // (a 128-byte line of a 16-bit y) and 32 more.
+    const int from = kAInLanes ? half * 64 : half * S::kGroupCols, more = 128 + half * 32;
+    uint8_t* room = smem + S::kTurnAt + (warp - 2) * kTurnWarp;
+    uint32_t n_tile = 0;
+    for (Tiles u = t; u.left(); u.next(p), ++n_tile) {
       const uint32_t b = n_tile & 1;
-      // all four warps of a group go on, or none
-      if (!group_all(half, wait(&ready[b], (n_tile / 2) & 1))) break;
+      if (!wait(&ready[b], (n_tile / 2) & 1)) break;
       asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
-      const uint64_t n0 = (u.col * kBlocks + half_of) * kRows, m0 = u.row * kCols;
-      const int cols = n0 >= p.n          ? 0
-                       : p.m - m0 < kCols ? static_cast<int>(p.m - m0)
-                                          : kCols;
+      const uint64_t l = (static_cast<uint64_t>(kAInLanes ? u.row : u.col) * kBlocks + half_of) * kRows + quarter * 32;
+      const uint64_t c = static_cast<uint64_t>(kAInLanes ? u.col : u.row) * kCols;
+      const bool any = half < S::kGroups && l < p.lanes && c + from < p.cols;
       const uint32_t d = tmem + b * 256 + (static_cast<uint32_t>(quarter * 32) << 16);
-      // TMA writes whole 16 bytes: a ragged end of y's rows is not its work
-      const bool staged = p.staged && (p.whole || n0 + kRows <= p.n);
-      const int at_once = staged ? rows_out(p.type) : 16;
-      for (int c = at_once * half; c < cols; c += 2 * at_once) {
-        float v[16];
-        if (staged) {
-          uint8_t* buffer = out + (n_out++ & 1) * kStageOut;
-          if (issues)  // the buffer's rows of two rounds ago have left it
-            asm volatile("cp.async.bulk.wait_group.read 1;" ::: "memory");
-          group_sync(half);
-          for (int q = 0; q < at_once && c + q < cols; q += 16) {
-            read_columns(d + c + q, v);
-            stage_columns(buffer + q * kRows * (p.type == HKV_F32 ? 4 : 2), row, p.type, v);
-          }
-          fence_proxy_async_smem();
-          group_sync(half);
-          if (issues)
-            tma_store(&maps.y, static_cast<int>(n0), static_cast<int>(m0 + c), buffer);
-          continue;
+      // the accumulators are given back as soon as they are read: the stores
+      // run beside the products of the tile after the next
+      float v[S::kGroupCols];
+      if (any) {
+        if constexpr (kAInLanes) {
+          read_columns<0, 64>(d + from, v);
+          read_columns<64, 32>(d + more, v);
+        } else {
+          read_columns<0, S::kGroupCols>(d + from, v);
         }
-        read_columns(d + c, v);
-        if (splits == 1) {
-          store_columns(p, m0 + c, n0 + row, v);
-        } else {  // this block's part of the sum, for the cluster to add up
-          float* mine = reinterpret_cast<float*>(smem) + row;
-#pragma unroll
-          for (int q = 0; q < 16; ++q) mine[(c + q) * kRows] = v[q];
-        }
+        columns_read(v);
       }
       asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
       __syncwarp();
@@ -515,21 +530,43 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (kBlocks == 2) mbar_arrive_at(cluster_address(&drained[b], 0));
         else mbar_arrive(&drained[b]);
       }
+      if (!any) continue;
+      if constexpr (kAInLanes) {
+        auto store = [&](auto type) {
+          constexpr int kType = decltype(type)::value;
+          if constexpr (kType == HKV_F32) {
+            turn_and_store<kType, 0, 32>(room, p, l, c + from, v);
+            turn_and_store<kType, 32, 32>(room, p, l, c + from + 32, v);
+          } else {
+            turn_and_store<kType, 0, 64>(room, p, l, c + from, v);
+          }
+          turn_and_store<kType, 64, 32>(room, p, l, c + more, v);
+        };
+        if (p.type == HKV_F32) store(std::integral_constant<int, HKV_F32>{});
+        else if (p.type == HKV_BF16) store(std::integral_constant<int, HKV_BF16>{});
+        else store(std::integral_constant<int, HKV_F16>{});
+      } else if (splits > 1) {  // this block's part of the sum, for the cluster to add up
+        float* mine = reinterpret_cast<float*>(smem) + from * kRows + quarter * 32 + lane;
+#pragma unroll
+        for (int q = 0; q < S::kGroupCols; ++q) mine[q * kRows] = v[q];
+      } else {
+        store_columns(p, c + from, l + lane, v);
+      }
     }
-    if (issues) asm volatile("cp.async.bulk.wait_group 0;" ::: "memory");
   }
   __syncwarp();
   if (splits > 1) {
     cluster_sync();
     if (warp >= 2) {
       const int row = (warp & 3) * 32 + lane, half = (warp - 2) >> 2;
-      const uint64_t j = t.col * kRows + row, m0 = t.row * kCols;
-      const int cols = p.m - m0 < kCols ? static_cast<int>(p.m - m0) : kCols;
+      const uint64_t l = static_cast<uint64_t>(t.col) * kRows + row;
+      const uint64_t c0 = static_cast<uint64_t>(t.row) * kCols;
+      const int cols = p.cols - c0 < kCols ? static_cast<int>(p.cols - c0) : kCols;
       const uint32_t parts = smem_u32(smem) + row * 4;
       for (int c = 2 * part + half; c < cols; c += 2 * splits) {
         float v = 0.f;
         for (uint32_t r = 0; r < splits; ++r) v += remote_f32(parts + c * kRows * 4, r);
-        if (j < p.n) store_one(p, m0 + c, j, v);
+        if (l < p.lanes) store_one(p, c0 + c, l, v);
       }
     }
     __syncwarp();
@@ -545,8 +582,9 @@ __global__ void __launch_bounds__(kThreads, 1)
 __global__ void zero_kernel(const __grid_constant__ Problem p) {
   pdl_wait();
   const uint64_t step = static_cast<uint64_t>(gridDim.x) * blockDim.x;
-  for (uint64_t i = static_cast<uint64_t>(blockIdx.x) * blockDim.x + threadIdx.x; i < p.m * p.n; i += step)
-    store_one(p, i / p.n, i % p.n, 0.f);
+  for (uint64_t i = static_cast<uint64_t>(blockIdx.x) * blockDim.x + threadIdx.x;
+       i < p.cols * p.lanes; i += step)
+    store_one(p, i / p.lanes, i % p.lanes, 0.f);
 }
 
 using EncodeFn = decltype(&cuTensorMapEncodeTiled);
@@ -562,75 +600,57 @@ EncodeFn encode_fn() {
   return fn;
 }
 
+struct Operand {
+  const uint8_t *codes, *scales;
+  uint64_t rows;
+};
+
 // A matrix's codes as boxes of 128 bytes by `box` rows, swizzled, and its
 // scales as boxes of two 512-byte groups by `groups`; what lies past the
 // matrix reads as zeros.
-bool make_maps(CUtensorMap* codes_map, CUtensorMap* scales_map, const uint8_t* codes,
-               const uint8_t* scales, uint64_t rows, uint64_t k, int box, int groups) {
+bool make_maps(CUtensorMap* codes_map, CUtensorMap* scales_map, const Operand& o, uint64_t k,
+               int box, int groups) {
   EncodeFn f = encode_fn();
   if (!f) return false;
   const cuuint32_t steps[2] = {1, 1};
   const uint64_t bytes = (k + kMxBlock - 1) / kMxBlock * 16;
-  const cuuint64_t dims[2] = {bytes, rows}, strides[1] = {bytes};
+  const cuuint64_t dims[2] = {bytes, o.rows}, strides[1] = {bytes};
   const cuuint32_t boxes[2] = {kStepBytes, static_cast<cuuint32_t>(box)};
   const uint64_t words = (k + 127) / 128 * 128;  // of 4 bytes
-  const cuuint64_t sdims[2] = {words, (rows + 127) / 128}, sstrides[1] = {words * 4};
+  const cuuint64_t sdims[2] = {words, (o.rows + 127) / 128}, sstrides[1] = {words * 4};
   const cuuint32_t sboxes[2] = {256, static_cast<cuuint32_t>(groups)};
-  return f(codes_map, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, const_cast<uint8_t*>(codes), dims, strides,
+  return f(codes_map, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, const_cast<uint8_t*>(o.codes), dims, strides,
            boxes, steps, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
            CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS &&
-         f(scales_map, CU_TENSOR_MAP_DATA_TYPE_UINT32, 2, const_cast<uint8_t*>(scales), sdims,
+         f(scales_map, CU_TENSOR_MAP_DATA_TYPE_UINT32, 2, const_cast<uint8_t*>(o.scales), sdims,
            sstrides, sboxes, steps, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_NONE,
            CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-// y as boxes of 128 columns.
-bool make_y_map(CUtensorMap* map, const Problem& p) {
-  const CUtensorMapDataType type = p.type == HKV_F32    ? CU_TENSOR_MAP_DATA_TYPE_FLOAT32
-                                   : p.type == HKV_BF16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16
-                                                        : CU_TENSOR_MAP_DATA_TYPE_FLOAT16;
-  const cuuint32_t steps[2] = {1, 1};
-  const cuuint64_t dims[2] = {p.n, p.m}, strides[1] = {p.stride * type_size(p.type)};
-  const cuuint32_t boxes[2] = {kRows, static_cast<cuuint32_t>(rows_out(p.type))};
-  EncodeFn f = encode_fn();
-  return f && f(map, type, 2, p.y, dims, strides, boxes, steps, CU_TENSOR_MAP_INTERLEAVE_NONE,
-                CU_TENSOR_MAP_SWIZZLE_NONE, CU_TENSOR_MAP_L2_PROMOTION_NONE,
-                CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
-}
-
-struct Operands {
-  const uint8_t *a_codes, *a_scales, *b_codes, *b_scales;
-};
-
-template <int kCols, int kBlocks>
-cudaError_t run(Problem p, const Operands& o, cudaStream_t st) {
+template <int kCols, int kBlocks, bool kAInLanes>
+cudaError_t run(Problem p, const Operand& a, const Operand& b, int splits, cudaStream_t st) {
   using S = Shape<kCols, kBlocks>;
-  p.tiles_m = (p.m + kCols - 1) / kCols;
-  p.tiles_n = (p.n + kRows * kBlocks - 1) / (kRows * kBlocks);
-  const uint64_t tiles = p.tiles_m * p.tiles_n, steps = (p.k + kStep - 1) / kStep;
-  const uint64_t sms = sm_count();
-  // few tiles: a cluster shares a tile's k while SMs are idle and each block
-  // keeps two steps at least
-  p.splits = 1;
-  while (kBlocks == 1 && p.splits < kMaxSplits && tiles * p.splits * 2 <= sms &&
-         steps >= 4ull * p.splits)
-    p.splits *= 2;
+  const Operand &lanes = kAInLanes ? a : b, &cols = kAInLanes ? b : a;
+  p.lanes = lanes.rows;
+  p.cols = cols.rows;
+  const uint64_t along_lanes = (p.lanes + kRows * kBlocks - 1) / (kRows * kBlocks);
+  const uint64_t along_cols = (p.cols + kCols - 1) / kCols;
+  const uint64_t tiles = along_lanes * along_cols;
+  if (tiles > 0x3FFFFFFF) return cudaErrorInvalidValue;  // no y in memory has as many
+  p.along = static_cast<uint32_t>(kAInLanes ? along_cols : along_lanes);
+  p.down = static_cast<uint32_t>(kAInLanes ? along_lanes : along_cols);
+  p.splits = splits;
   Maps maps{};
-  if (!make_maps(&maps.a, &maps.a_scales, o.a_codes, o.a_scales, p.m, p.k, S::kACols, S::kScaleRows) ||
-      !make_maps(&maps.b, &maps.b_scales, o.b_codes, o.b_scales, p.n, p.k, kRows, 1))
+  if (!make_maps(&maps.lanes, &maps.lanes_scales, lanes, p.k, kRows, 1) ||
+      !make_maps(&maps.cols, &maps.cols_scales, cols, p.k, S::kOwnCols, S::kScaleRows))
     return cudaErrorUnknown;
-  // TMA wants 16-byte boundaries and a stride below 2^40 bytes
-  const uint64_t row_bytes = p.stride * type_size(p.type);
-  p.staged = p.splits == 1 && aligned(p.y, 16) && row_bytes % 16 == 0 && row_bytes < 1ull << 40;
-  p.whole = p.n * type_size(p.type) % 16 == 0;
-  if (p.staged && !make_y_map(&maps.y, p)) return cudaErrorUnknown;
-  auto* kernel = matmul_kernel<kCols, kBlocks>;
+  auto* kernel = matmul_kernel<kCols, kBlocks, kAInLanes>;
   cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, S::kSmem);
   if (e != cudaSuccess) return e;
-  const uint32_t cluster = p.splits * kBlocks;
-  const uint64_t clusters = p.splits > 1 || tiles < sms / kBlocks ? tiles : sms / kBlocks;
+  const uint32_t cluster = splits * kBlocks;
+  const uint64_t room = sm_count() / kBlocks;
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(static_cast<unsigned>(clusters * cluster));
+  cfg.gridDim = dim3(static_cast<unsigned>((splits > 1 || tiles < room ? tiles : room) * cluster));
   cfg.blockDim = dim3(kThreads);
   cfg.dynamicSmemBytes = S::kSmem;
   cfg.stream = st;
@@ -645,17 +665,30 @@ cudaError_t run(Problem p, const Operands& o, cudaStream_t st) {
   return cudaLaunchKernelEx(&cfg, kernel, maps, p);
 }
 
-cudaError_t matmul(const Problem& p, const Operands& o, cudaStream_t st) {
+cudaError_t matmul(Problem p, const Operand& a, const Operand& b, cudaStream_t st) {
+  p.lanes = b.rows;
+  p.cols = a.rows;
   if (p.k == 0) return launch_chained(zero_kernel, sm_count() * 4, 256, 0, st, p);
-  if (p.m <= 16) return run<16, 1>(p, o, st);
-  if (p.m <= 32) return run<32, 1>(p, o, st);
-  if (p.m <= 64) return run<64, 1>(p, o, st);
-  if (p.m <= 128) return run<128, 1>(p, o, st);
-  // pairs halve what a block loads of A; one block per tile has twice as many
-  // tiles to spread over the SMs
-  const uint64_t pairs = (p.m + 191) / 192 * ((p.n + 255) / 256);
-  if (pairs * 2 > static_cast<uint64_t>(sm_count())) return run<192, 2>(p, o, st);
-  return run<192, 1>(p, o, st);
+  const uint64_t sms = sm_count(), m = a.rows, n = b.rows, steps = (p.k + kStep - 1) / kStep;
+  const int cols = m <= 16 ? 16 : m <= 32 ? 32 : m <= 64 ? 64 : m <= 128 ? 128 : 192;
+  const uint64_t tiles = (n + kRows - 1) / kRows * ((m + cols - 1) / cols);
+  // few tiles: a cluster shares a tile's k while SMs are idle and each block
+  // keeps two steps at least
+  int splits = 1;
+  while (splits < kMaxSplits && tiles * splits * 2 <= sms && steps >= 4ull * splits) splits *= 2;
+  if (cols == 16) return run<16, 1, false>(p, a, b, splits, st);
+  if (cols == 32) return run<32, 1, false>(p, a, b, splits, st);
+  if (cols == 64) return run<64, 1, false>(p, a, b, splits, st);
+  if (cols == 128) return run<128, 1, false>(p, a, b, splits, st);
+  if (splits > 1) return run<192, 1, false>(p, a, b, splits, st);
+  // A pair loads 31 KB per block and step where a single block loads 43, and
+  // an SM takes in 54 bytes a cycle; but a tile's way from the products to the
+  // stores and back crosses the cluster.  Measured at 8192 x 16384, single and
+  // pair: k 512 52 and 75 us, 1024 72 and 86, 1280 85 and 91, 2048 119 and 101.
+  // Where pairs leave SMs without a tile, single blocks have twice as many.
+  const bool pair = steps > 5 && (m + 191) / 192 * ((n + 255) / 256) * 2 > sms;
+  if (p.wide) return pair ? run<192, 2, true>(p, a, b, 1, st) : run<192, 1, true>(p, a, b, 1, st);
+  return pair ? run<192, 2, false>(p, a, b, 1, st) : run<192, 1, false>(p, a, b, 1, st);
 }
 
 }  // namespace
@@ -677,14 +710,13 @@ hkv_status hkv_mx_matmul(uint64_t m, uint64_t n, uint64_t k, const uint8_t* a_co
       !aligned(b_scales, 16))
     return HKV_ERR_INVALID;
   Problem p{};
-  p.m = m;
-  p.n = n;
   p.k = k;
   p.y = y;
   p.stride = y_stride;
   p.type = y_type;
-  p.pairs = y_type != HKV_F32 && aligned(y, 4) && y_stride % 2 == 0;
-  return op_status(matmul(p, {a_codes, a_scales, b_codes, b_scales}, static_cast<cudaStream_t>(stream)));
+  p.wide = aligned(y, 16) && y_stride * type_size(y_type) % 16 == 0;
+  return op_status(matmul(p, {a_codes, a_scales, m}, {b_codes, b_scales, n},
+                          static_cast<cudaStream_t>(stream)));
 }
 
 hkv_status hkv_get_wait_timeouts(uint64_t* timeouts_host) {
