@@ -107,13 +107,13 @@ __global__ void __launch_bounds__(kThreads)
       for (; k + (kUnroll - 1) * kThreads < eights; k += kUnroll * kThreads) {
         Eight<T> in[kUnroll];
 #pragma unroll
-        for (int u = 0; u < kUnroll; ++u) in[u].load(x + (k + u * kThreads) * 8, 8, kWhole);
+        for (int u = 0; u < kUnroll; ++u) in[u].load_aligned(x + (k + u * kThreads) * 8, kWhole);
 #pragma unroll
         for (int u = 0; u < kUnroll; ++u) add(in[u]);
       }
       for (; k < eights; k += kThreads) {
         Eight<T> in;
-        in.load(x + k * 8, 8, kWhole);
+        in.load_aligned(x + k * 8, kWhole);
         add(in);
       }
       const uint32_t tail = eights * 8 + threadIdx.x;
@@ -164,7 +164,7 @@ __global__ void __launch_bounds__(kThreads)
           for (int i = 0; i < 8; ++i) v[i] *= f;
           Eight<U> out;
           out.from(v);
-          out.store(y + k * 8, 8, kWhole);
+          out.store_aligned(y + k * 8, kWhole);
         };
         uint32_t k = threadIdx.x;
         for (; k + (kUnroll - 1) * kThreads < eights; k += kUnroll * kThreads) {

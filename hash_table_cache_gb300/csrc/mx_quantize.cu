@@ -19,6 +19,13 @@ namespace {
 constexpr int kThreads = 256;
 constexpr int kTile = 128;
 
+// The end of a row of `cols` elements as seen from element c, within -32 .. 32:
+// what Eight takes.
+__device__ __forceinline__ int limit(uint64_t cols, uint64_t c) {
+  const int64_t d = static_cast<int64_t>(cols) - static_cast<int64_t>(c);
+  return static_cast<int>(min(max(d, static_cast<int64_t>(-32)), static_cast<int64_t>(32)));
+}
+
 // The largest magnitude of eight elements, as float32 bits.
 __device__ __forceinline__ uint32_t most_of(const float (&v)[8]) {
   uint32_t m = 0;
@@ -71,7 +78,7 @@ __global__ void __launch_bounds__(kThreads)
   for (uint64_t t = blockIdx.x; t < groups * groups_t; t += gridDim.x) {
     const uint64_t tile_c = t % groups, tile_r = t / groups;
     const uint64_t c = tile_c * kTile + tx * 8;
-    const int valid = c + 8 <= cols ? 8 : c < cols ? static_cast<int>(cols - c) : 0;
+    const int lo = tile_c ? -16 : -8 * tx, hi = limit(cols, c);
 #pragma unroll
     for (int h = 0; h < 2; ++h) {
       const int r = ty + 16 * h;
@@ -79,8 +86,7 @@ __global__ void __launch_bounds__(kThreads)
 #pragma unroll
       for (int q = 0; q < 4; ++q) {
         const uint64_t row = tile_r * kTile + r + 32 * q;
-        e[q].load(x + row * stride + c, row < rows ? valid : 0,
-                  valid == 8 && row < rows ? move : kSingly);
+        e[q].load(x + row * stride + c, row < rows ? lo : 0, row < rows ? hi : 0, move, tx);
       }
       if (kColCopy) {
 #pragma unroll
@@ -156,8 +162,7 @@ __global__ void __launch_bounds__(kThreads)
   const uint64_t tiles = groups * ((rows + 127) / 128);
   for (uint64_t t = blockIdx.x; t < tiles; t += gridDim.x) {
     const uint64_t c = t % groups * kTile + tx * 8, row0 = t / groups * kTile;
-    if (c >= cols) continue;
-    const int valid = c + 8 <= cols ? 8 : static_cast<int>(cols - c);
+    const int hi = limit(cols, c);
     uint32_t code[8];
     uint4 scale[2];
 #pragma unroll
@@ -166,7 +171,7 @@ __global__ void __launch_bounds__(kThreads)
 #pragma unroll
       for (int q = 0; q < 4; ++q) {
         const uint64_t row = row0 + ty + 16 * h + 32 * q;
-        code[4 * h + q] = row < rows ? __ldg(reinterpret_cast<const uint32_t*>(
+        code[4 * h + q] = row < rows && hi > 0 ? __ldg(reinterpret_cast<const uint32_t*>(
                                            codes + row * blocks * 16 + c / 2))
                                      : 0;
       }
@@ -174,7 +179,6 @@ __global__ void __launch_bounds__(kThreads)
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
       const uint64_t row = row0 + ty + 16 * (i >> 2) + 32 * (i & 3);
-      if (row >= rows) continue;
       const uint32_t four = reinterpret_cast<const uint32_t*>(&scale[i >> 2])[i & 3];
       const float s = mx_scale_value(four >> (8 * (tx >> 2)) & 255);
       float v[8];
@@ -183,7 +187,7 @@ __global__ void __launch_bounds__(kThreads)
       for (int k = 0; k < 8; ++k) v[k] *= s;
       Eight<T> e;
       e.from(v);
-      e.store(y + row * stride + c, valid, valid == 8 ? move : kSingly);
+      e.store(y + row * stride + c, row < rows ? hi : 0, move, tx);
     }
   }
 }

@@ -47,20 +47,36 @@ template <>
 __device__ __forceinline__ __half from_f32<__half>(float v) { return __float2half_rn(v); }
 
 // How eight neighbouring elements are moved: in one access of 16 bytes (32 of
-// float32), in two of 16 (float32 alone), or one by one.
-enum Move : int { kSingly = 0, kHalves = 1, kWhole = 2 };
+// float32), in two of 16 (float32 alone), or, where rows start anywhere, in
+// the 16-byte pieces around them that neighbouring threads share.
+enum Move : int { kShifted = 0, kHalves = 1, kWhole = 2 };
 
 // The widest move that an address and a row stride in bytes allow.
 template <class T>
 __host__ __device__ inline int widest(const void* p, uint64_t stride_bytes) {
   const uint64_t a = reinterpret_cast<uintptr_t>(p) | stride_bytes;
   if (a % (8 * sizeof(T)) == 0) return kWhole;
-  return sizeof(T) == 4 && a % 16 == 0 ? kHalves : kSingly;
+  return sizeof(T) == 4 && a % 16 == 0 ? kHalves : kShifted;
 }
 
-// Eight neighbouring elements as they lie in memory.  `valid` of them belong
-// to the row; the others read as zeros and are not written.  Moves other
-// than kSingly take all eight.
+// x[i] = the 32 bits that start `bytes` (even, below 16) into x[i]; the last
+// four words are only taken from.
+template <int N>
+__device__ __forceinline__ void shift_bytes(uint32_t (&x)[N], uint32_t bytes) {
+#pragma unroll
+  for (int i = 0; i < N - 1; ++i) x[i] = bytes & 4 ? x[i + 1] : x[i];
+#pragma unroll
+  for (int i = 0; i < N - 2; ++i) x[i] = bytes & 8 ? x[i + 2] : x[i];
+#pragma unroll
+  for (int i = 0; i < N - 4; ++i) x[i] = __byte_perm(x[i], x[i + 1], bytes & 2 ? 0x5432 : 0x3210);
+}
+
+// Eight neighbouring elements of a row as they lie in memory.  `lo` and `hi`
+// bound the row: elements lo .. hi - 1 from the thread's first one belong to
+// it (hi may be above 8, or not above 0); the others read as zeros and are not
+// written.  Sixteen neighbouring threads, a half-warp, `at` of it, hold 128
+// neighbouring elements; all threads of a warp take part.  `move` is the same
+// for all rows.
 template <class T>
 struct Eight {
   static constexpr int kVecs = sizeof(T) / 2;
@@ -81,44 +97,105 @@ struct Eight {
                    : "l"(p)
                    : "memory");
   }
-  __device__ __forceinline__ void load(const T* p, int valid, int move) {
-    if (move == kWhole) {
-      if constexpr (kVecs == 1)
-        w[0] = ld_stream_v4(p);
-      else
-        asm volatile("ld.global.nc.L1::no_allocate.v8.b32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8];"
-                     : "=r"(w[0].x), "=r"(w[0].y), "=r"(w[0].z), "=r"(w[0].w),
-                       "=r"(w[kVecs - 1].x), "=r"(w[kVecs - 1].y), "=r"(w[kVecs - 1].z),
-                       "=r"(w[kVecs - 1].w)
-                     : "l"(p));
-    } else if (move == kHalves) {
+  // All eight, by one access or two.
+  __device__ __forceinline__ void load_aligned(const T* p, int move) {
+    if (kVecs == 2 && move == kWhole) {
+      asm volatile("ld.global.nc.L1::no_allocate.v8.b32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8];"
+                   : "=r"(w[0].x), "=r"(w[0].y), "=r"(w[0].z), "=r"(w[0].w),
+                     "=r"(w[kVecs - 1].x), "=r"(w[kVecs - 1].y), "=r"(w[kVecs - 1].z),
+                     "=r"(w[kVecs - 1].w)
+                   : "l"(p));
+    } else if (kVecs == 2) {
       // the halves of a sector come by two instructions: through L1
 #pragma unroll
-      for (int i = 0; i < kVecs; ++i) w[i] = ld_nc_v4(p + i * (16 / sizeof(T)));
+      for (int i = 0; i < kVecs; ++i) w[i] = ld_nc_v4(p + i * 4);
     } else {
-      T* e = reinterpret_cast<T*>(w);
-#pragma unroll
-      for (int i = 0; i < 8; ++i) e[i] = i < valid ? p[i] : from_f32<T>(0.f);
+      w[0] = ld_stream_v4(p);
     }
   }
-  __device__ __forceinline__ void store(T* p, int valid, int move) const {
-    if (move == kWhole) {
-      if constexpr (kVecs == 1)
-        st_stream_v4(p, w[0]);
-      else
-        asm volatile("st.global.cs.v8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"l"(p), "r"(w[0].x),
-                     "r"(w[0].y), "r"(w[0].z), "r"(w[0].w), "r"(w[kVecs - 1].x),
-                     "r"(w[kVecs - 1].y), "r"(w[kVecs - 1].z), "r"(w[kVecs - 1].w)
-                     : "memory");
-    } else if (move == kHalves) {
+  __device__ __forceinline__ void store_aligned(T* p, int move) const {
+    if (kVecs == 2 && move == kWhole) {
+      asm volatile("st.global.cs.v8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"l"(p), "r"(w[0].x),
+                   "r"(w[0].y), "r"(w[0].z), "r"(w[0].w), "r"(w[kVecs - 1].x),
+                   "r"(w[kVecs - 1].y), "r"(w[kVecs - 1].z), "r"(w[kVecs - 1].w)
+                   : "memory");
+    } else {
 #pragma unroll
       for (int i = 0; i < kVecs; ++i) st_stream_v4(p + i * (16 / sizeof(T)), w[i]);
-    } else {
-      const T* e = reinterpret_cast<const T*>(w);
-#pragma unroll
-      for (int i = 0; i < 8; ++i)
-        if (i < valid) p[i] = e[i];
     }
+  }
+
+  // The 16 bytes at p + from, a boundary.
+  static __device__ __forceinline__ uint4 piece(const T* p, int from, int lo, int hi) {
+    constexpr int kPer = 16 / sizeof(T);
+    if (from >= lo && from + kPer <= hi) return ld_nc_v4(p + from);
+    uint4 v;
+    T* e = reinterpret_cast<T*>(&v);
+#pragma unroll
+    for (int i = 0; i < kPer; ++i)
+      e[i] = from + i >= lo && from + i < hi ? p[from + i] : from_f32<T>(0.f);
+    return v;
+  }
+
+  __device__ __forceinline__ void load(const T* p, int lo, int hi, int move, int at) {
+    constexpr int kPer = 16 / sizeof(T);
+    if (move != kShifted) {
+      if (hi >= 8) load_aligned(p, move);
+      else
+#pragma unroll
+        for (int i = 0; i < kVecs; ++i) w[i] = piece(p, i * kPer, 0, hi);
+      return;
+    }
+    // the pieces from the boundary below p on, and the next thread's first one
+    const uint32_t off = reinterpret_cast<uintptr_t>(p) & 15;
+    const int back = static_cast<int>(off / sizeof(T));
+    uint32_t x[4 * kVecs + 4];
+    uint4* v = reinterpret_cast<uint4*>(x);
+#pragma unroll
+    for (int i = 0; i < kVecs; ++i) v[i] = piece(p, i * kPer - back, lo, hi);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) x[4 * kVecs + i] = __shfl_down_sync(0xFFFFFFFFu, x[i], 1, 16);
+    if (at == 15 && off) v[kVecs] = piece(p, kVecs * kPer - back, lo, hi);
+    shift_bytes(x, off);
+#pragma unroll
+    for (int i = 0; i < kVecs; ++i) w[i] = v[i];
+  }
+
+  __device__ __forceinline__ void store(T* p, int hi, int move, int at) const {
+    constexpr int kPer = 16 / sizeof(T);
+    const T* e = reinterpret_cast<const T*>(w);
+    if (move != kShifted) {
+      if (hi >= 8) store_aligned(p, move);
+      else
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+          if (i < hi) p[i] = e[i];
+      return;
+    }
+    // The pieces from the boundary above p on; the last one ends with the next
+    // thread's first elements, and that thread leaves those out.
+    const uint32_t up = (16 - (reinterpret_cast<uintptr_t>(p) & 15)) & 15;
+    const int ahead = static_cast<int>(up / sizeof(T));
+    uint32_t x[4 * kVecs + 4];
+    uint4* v = reinterpret_cast<uint4*>(x);
+#pragma unroll
+    for (int i = 0; i < kVecs; ++i) v[i] = w[i];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) x[4 * kVecs + i] = __shfl_down_sync(0xFFFFFFFFu, x[i], 1, 16);
+    shift_bytes(x, up);
+    const bool head = at == 0 || hi < ahead;
+    bool whole[kVecs];
+#pragma unroll
+    for (int i = 0; i < kVecs; ++i) {
+      whole[i] = hi >= ahead + (i + 1) * kPer && (i + 1 < kVecs || at < 15 || ahead == 0);
+      if (whole[i]) st_stream_v4(p + ahead + i * kPer, v[i]);
+    }
+    if ((head && ahead) || !whole[0] || !whole[kVecs - 1])
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        const bool alone = i < ahead ? head : !whole[kVecs > 1 && i - ahead >= kPer ? kVecs - 1 : 0];
+        if (alone && i < hi) p[i] = e[i];
+      }
   }
   __device__ __forceinline__ void to(float (&v)[8]) const {
     const T* e = reinterpret_cast<const T*>(w);
