@@ -11,6 +11,8 @@
 // read, and four threads take the 128 rows of a column (or of two neighbouring
 // 16-bit columns), so that they write 64 neighbouring bytes of codes; both
 // copies come from one read of x.
+#include <type_traits>
+
 #include "mx.cuh"
 
 namespace hkv {
@@ -26,12 +28,27 @@ __device__ __forceinline__ int limit(uint64_t cols, uint64_t c) {
   return static_cast<int>(min(max(d, static_cast<int64_t>(-32)), static_cast<int64_t>(32)));
 }
 
-// The largest magnitude of eight elements, as float32 bits.
-__device__ __forceinline__ uint32_t most_of(const float (&v)[8]) {
-  uint32_t m = 0;
-#pragma unroll
-  for (int i = 0; i < 8; ++i) m = max(m, __float_as_uint(v[i]) & 0x7FFFFFFFu);
-  return m;
+// Running maxima of magnitudes, compared as integers (which puts NaNs above
+// infinity).  A word holds one float32 or two 16-bit elements, whose maxima
+// are kept apart until the end: one instruction for two elements.
+template <class T>
+__device__ __forceinline__ uint32_t most(uint32_t m, uint32_t word) {
+  if constexpr (sizeof(T) == 4) return max(m, word & 0x7FFFFFFFu);
+  return __vmaxu2(m, word & 0x7FFF7FFFu);
+}
+template <class T>
+__device__ __forceinline__ uint32_t most_of(uint32_t m, uint32_t other) {
+  if constexpr (sizeof(T) == 4) return max(m, other);
+  return __vmaxu2(m, other);
+}
+// One of them as float32 bits: of a float32, or of the lower (0) or upper (1)
+// elements of the words.
+template <class T>
+__device__ __forceinline__ uint32_t magnitude(uint32_t m, int k) {
+  if constexpr (sizeof(T) == 4) return m;
+  const uint32_t h = k ? m >> 16 : m & 0xFFFFu;
+  if constexpr (std::is_same_v<T, __nv_bfloat16>) return h << 16;
+  return __float_as_uint(__half2float(__ushort_as_half(static_cast<unsigned short>(h))));
 }
 
 __device__ __forceinline__ uint32_t encode8(const float (&v)[8], uint32_t byte) {
@@ -43,26 +60,9 @@ __device__ __forceinline__ uint32_t encode8(const float (&v)[8], uint32_t byte) 
   return mx_codes8(u);
 }
 
-// One block of 32 elements down a column of the tile: its codes and scale byte.
-__device__ __forceinline__ uint32_t encode32(const float (&v)[32], uint4* codes) {
-  uint32_t most = 0;
-#pragma unroll
-  for (int i = 0; i < 32; ++i) most = max(most, __float_as_uint(v[i]) & 0x7FFFFFFFu);
-  const uint32_t byte = mx_scale_byte(most);
-  uint32_t w[4];
-#pragma unroll
-  for (int g = 0; g < 4; ++g) {
-    float u[8];
-#pragma unroll
-    for (int i = 0; i < 8; ++i) u[i] = v[8 * g + i];
-    w[g] = encode8(u, byte);
-  }
-  *codes = make_uint4(w[0], w[1], w[2], w[3]);
-  return byte;
-}
-
+// Four blocks per SM: while one waits for its tile another encodes.
 template <class T, bool kRowCopy, bool kColCopy>
-__global__ void __launch_bounds__(kThreads)
+__global__ void __launch_bounds__(kThreads, 4)
     quantize_kernel(uint64_t rows, uint64_t cols, const T* __restrict__ x, uint64_t stride,
                     int move, uint8_t* codes, uint8_t* scales, uint8_t* codes_t,
                     uint8_t* scales_t) {
@@ -101,12 +101,15 @@ __global__ void __launch_bounds__(kThreads)
         uint32_t packed[4];
 #pragma unroll
         for (int q = 0; q < 4; ++q) {
+          const uint32_t* words = reinterpret_cast<const uint32_t*>(e[q].w);
+          uint32_t m = 0;
+#pragma unroll
+          for (int i = 0; i < 4 * Eight<T>::kVecs; ++i) m = most<T>(m, words[i]);
+          m = most_of<T>(m, __shfl_xor_sync(0xFFFFFFFFu, m, 1));
+          m = most_of<T>(m, __shfl_xor_sync(0xFFFFFFFFu, m, 2));
+          const uint32_t byte = mx_scale_byte(max(magnitude<T>(m, 0), magnitude<T>(m, 1)));
           float v[8];
           e[q].to(v);
-          uint32_t most = most_of(v);
-          most = max(most, __shfl_xor_sync(0xFFFFFFFFu, most, 1));
-          most = max(most, __shfl_xor_sync(0xFFFFFFFFu, most, 2));
-          const uint32_t byte = mx_scale_byte(most);
           const uint32_t code = encode8(v, byte);
           const uint64_t row = tile_r * kTile + r + 32 * q;
           if (row < rows && (c >> 5) < blocks)
@@ -126,16 +129,24 @@ __global__ void __launch_bounds__(kThreads)
       const int q = threadIdx.x & 3;
       constexpr int kPer = 4 / sizeof(T);  // columns in a word
       for (int w = threadIdx.x >> 2; w < kWords; w += kThreads / 4) {
-        uint32_t word[32];
+        uint32_t word[32], m = 0;
 #pragma unroll
-        for (int i = 0; i < 32; ++i) word[i] = tile[(32 * q + i) * kWords + (w ^ (8 * q))];
+        for (int i = 0; i < 32; ++i) {
+          word[i] = tile[(32 * q + i) * kWords + (w ^ (8 * q))];
+          m = most<T>(m, word[i]);
+        }
 #pragma unroll
         for (int k = 0; k < kPer; ++k) {
-          float v[32];
+          const uint32_t byte = mx_scale_byte(magnitude<T>(m, k));
+          uint32_t code[4];
 #pragma unroll
-          for (int i = 0; i < 32; ++i) v[i] = to_f32(reinterpret_cast<const T*>(&word[i])[k]);
-          uint4 out;
-          const uint32_t byte = encode32(v, &out);
+          for (int g = 0; g < 4; ++g) {
+            float v[8];
+#pragma unroll
+            for (int i = 0; i < 8; ++i) v[i] = to_f32(reinterpret_cast<const T*>(&word[8 * g + i])[k]);
+            code[g] = encode8(v, byte);
+          }
+          const uint4 out = make_uint4(code[0], code[1], code[2], code[3]);
           const uint64_t col = tile_c * kTile + w * kPer + k, block = tile_r * 4 + q;
           if (col < cols && block < blocks_t)
             *reinterpret_cast<uint4*>(codes_t + (col * blocks_t + block) * 16) = out;
