@@ -9,16 +9,26 @@
 // the blocks of a cluster, which join their parts through distributed shared
 // memory in a fixed order, so no partial result goes through global memory.
 #include <cmath>
+#include <type_traits>
 
 #include "operators.cuh"
 
 namespace hkv {
 namespace {
 
-constexpr int kThreads = 256;
+constexpr int kThreads = 256;       // a row's or a piece's, where a block takes it
+constexpr int kWarpThreads = 128;   // four rows, where a warp takes one
 constexpr int kPairThreads = 256;
-constexpr int kUnroll = 4;      // 16-byte loads in flight per thread
-constexpr int kMaxParts = 8;    // blocks of a cluster that share a row
+constexpr int kMaxParts = 8;  // blocks of a cluster that share a row
+// 16-byte loads in flight per thread where kLanes threads share a row
+__host__ __device__ constexpr int unroll(int lanes) { return lanes == 32 ? 8 : 4; }
+constexpr float kLog2e = 1.44269504f;
+
+__device__ __forceinline__ float exp2_approx(float x) {
+  float y;
+  asm("ex2.approx.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
 
 // Neighbouring elements in 16 bytes.
 template <class T>
@@ -28,7 +38,34 @@ struct Chunk {
   __device__ __forceinline__ float at(int i) const {
     return to_f32(reinterpret_cast<const T*>(&w)[i]);
   }
+  __device__ __forceinline__ void fill_lowest() {  // -inf
+    const uint32_t v = sizeof(T) == 4                         ? 0xFF800000u
+                       : std::is_same_v<T, __nv_bfloat16> ? 0xFF80FF80u
+                                                          : 0xFC00FC00u;
+    w = make_uint4(v, v, v, v);
+  }
 };
+// The largest of N chunks' elements; 16-bit ones two at a time.  NaNs are
+// passed over: the sum of exponentials brings them in.
+template <class T, int N>
+__device__ __forceinline__ float largest(const Chunk<T> (&c)[N]) {
+  if constexpr (sizeof(T) == 4) {
+    float m = -INFINITY;
+#pragma unroll
+    for (int u = 0; u < N; ++u)
+#pragma unroll
+      for (int i = 0; i < 4; ++i) m = fmaxf(m, c[u].at(i));
+    return m;
+  } else {
+    using T2 = std::conditional_t<std::is_same_v<T, __nv_bfloat16>, __nv_bfloat162, __half2>;
+    T2 m = *reinterpret_cast<const T2*>(&c[0].w.x);
+#pragma unroll
+    for (int u = 0; u < N; ++u)
+#pragma unroll
+      for (int i = 0; i < 4; ++i) m = __hmax2(m, reinterpret_cast<const T2*>(&c[u].w)[i]);
+    return fmaxf(to_f32(m.x), to_f32(m.y));
+  }
+}
 template <class T>
 __device__ __forceinline__ uint32_t to_boundary(const T* p, uint64_t n) {
   const uint32_t head = (16 - reinterpret_cast<uintptr_t>(p) % 16) % 16 / sizeof(T);
@@ -66,37 +103,39 @@ struct Running {
 // One thread's share of a row of n elements, taken by kLanes threads.
 template <class T, int kLanes>
 __device__ __forceinline__ Running row_pass(const T* x, uint64_t n, int lane) {
+  constexpr int kN = Chunk<T>::kN, kUnroll = unroll(kLanes);
   Running r;
   const uint32_t head = to_boundary(x, n);
   if (lane < static_cast<int>(head)) r.one(to_f32(x[lane]));
-  constexpr int kN = Chunk<T>::kN;
   const T* body = x + head;
   const uint64_t chunks = (n - head) / kN;
-  auto take = [&](const Chunk<T>* c, int count) {
-    float top = -INFINITY;
-#pragma unroll
-    for (int u = 0; u < count; ++u)
-#pragma unroll
-      for (int i = 0; i < kN; ++i) top = fmaxf(top, c[u].at(i));
-    const float base = r.raise(top);
-    float part[2] = {};
-#pragma unroll
-    for (int u = 0; u < count; ++u)
-#pragma unroll
-      for (int i = 0; i < kN; ++i) part[i & 1] += __expf(c[u].at(i) - base);
-    r.s += part[0] + part[1];
-  };
-  uint64_t k = lane;
-  for (; k + (kUnroll - 1) * kLanes < chunks; k += kUnroll * kLanes) {
+  for (uint64_t k = lane; k < chunks; k += kUnroll * kLanes) {
     Chunk<T> c[kUnroll];
 #pragma unroll
-    for (int u = 0; u < kUnroll; ++u) c[u].w = ld_stream_v4(body + (k + u * kLanes) * kN);
-    take(c, kUnroll);
-  }
-  for (; k < chunks; k += kLanes) {
-    Chunk<T> c;
-    c.w = ld_stream_v4(body + k * kN);
-    take(&c, 1);
+    for (int u = 0; u < kUnroll; ++u) {
+      if (k + u * kLanes < chunks) c[u].w = ld_stream_v4(body + (k + u * kLanes) * kN);
+      else c[u].fill_lowest();
+    }
+    const float base = r.raise(largest(c));
+    float part[4] = {};
+    if (fabsf(base) < 1e37f) {
+      // exp(x - base) as 2^(x log2 e - base log2 e), one multiply-add each.
+      // The same rounded base log2 e is in every term; what it is off by is
+      // taken out of their sum.
+      const float scaled = base * kLog2e, off = fmaf(base, kLog2e, -scaled);
+#pragma unroll
+      for (int u = 0; u < kUnroll; ++u)
+#pragma unroll
+        for (int i = 0; i < kN; ++i)
+          part[i & 3] += exp2_approx(fmaf(c[u].at(i), kLog2e, -scaled));
+      r.s = fmaf((part[0] + part[1]) + (part[2] + part[3]), exp2_approx(-off), r.s);
+    } else {  // a product with log2 e might overflow
+#pragma unroll
+      for (int u = 0; u < kUnroll; ++u)
+#pragma unroll
+        for (int i = 0; i < kN; ++i) part[i & 3] += __expf(c[u].at(i) - base);
+      r.s += (part[0] + part[1]) + (part[2] + part[3]);
+    }
   }
   const uint64_t tail = head + chunks * kN + lane;
   if (tail < n) r.one(to_f32(x[tail]));
@@ -113,23 +152,22 @@ __device__ __forceinline__ Running join_lanes(Running r) {
   return r;
 }
 
-template <class T>
-__device__ __forceinline__ void finish_row(const Running& r, const T* x, uint64_t t, int64_t label,
-                                           float* logps, float* lse) {
+__device__ __forceinline__ void finish_row(const Running& r, float chosen, uint64_t t, float* logps,
+                                           float* lse) {
   const float l = r.log_sum();
   lse[t] = l;
-  logps[t] = to_f32(x[label]) - l;
+  logps[t] = chosen - l;
 }
 
 // A warp per row: short rows.
 template <class T>
-__global__ void __launch_bounds__(kThreads)
+__global__ void __launch_bounds__(kWarpThreads)
     short_rows_kernel(uint64_t rows, uint64_t vocab, const T* __restrict__ logits, uint64_t stride,
                       const int64_t* __restrict__ labels, float* logps, float* lse,
                       float* row_grad, int32_t* row_pair) {
   pdl_trigger();
   pdl_wait();
-  const uint64_t t = static_cast<uint64_t>(blockIdx.x) * (kThreads / 32) + threadIdx.x / 32;
+  const uint64_t t = static_cast<uint64_t>(blockIdx.x) * (kWarpThreads / 32) + threadIdx.x / 32;
   if (t >= rows) return;
   const int lane = threadIdx.x & 31;
   const int64_t label = labels[t];
@@ -142,8 +180,9 @@ __global__ void __launch_bounds__(kThreads)
     if (lane == 0) logps[t] = lse[t] = 0.f;
     return;
   }
+  const float chosen = lane == 0 ? to_f32(x[label]) : 0.f;
   const Running r = join_lanes(row_pass<T, 32>(x, vocab, lane));
-  if (lane == 0) finish_row(r, x, t, label, logps, lse);
+  if (lane == 0) finish_row(r, chosen, t, logps, lse);
 }
 
 // A block per row, or the `parts` blocks of a cluster.
@@ -168,6 +207,7 @@ __global__ void __launch_bounds__(kThreads)
     return;  // every block of the cluster
   }
   const T* x = logits + t * stride;
+  const float chosen = writes ? to_f32(x[label]) : 0.f;  // on its way while the row is read
   // parts start at multiples of 64 elements of the row
   const uint64_t size = ((vocab + parts - 1) / parts + 63) / 64 * 64;
   const uint64_t lo = min(part * size, vocab), hi = min(lo + size, vocab);
@@ -193,7 +233,7 @@ __global__ void __launch_bounds__(kThreads)
     __syncwarp();
     cluster_sync();  // the others stay until their parts are read
   }
-  if (writes) finish_row(r, x, t, label, logps, lse);
+  if (writes) finish_row(r, chosen, t, logps, lse);
 }
 
 // One pair per block: the sums of both sequences, the loss, and the loss's
@@ -264,21 +304,25 @@ __global__ void __launch_bounds__(kPairThreads)
   }
 }
 
-// A piece of a row per block: kUnroll chunks of 16 bytes per thread.  Rows run
-// from the last to the first, so that what the forward call read last is
-// taken from L2 while it is there.
-template <class T>
-__global__ void __launch_bounds__(kThreads)
+// A piece of a row for every kLanes threads, as many chunks of 16 bytes per
+// thread as it keeps in flight.  Rows run from the last to the first, so that
+// what the forward call read last is taken from L2 while it is there.
+template <class T, int kLanes>
+__global__ void __launch_bounds__(kLanes == 32 ? kWarpThreads : kThreads)
     backward_kernel(uint64_t pairs, uint64_t rows, uint64_t vocab, const T* logits, uint64_t stride,
                     uint64_t pieces, const int64_t* __restrict__ labels,
                     const float* __restrict__ lse, const float* __restrict__ row_grad,
                     const int32_t* __restrict__ row_pair, const float* __restrict__ dlosses,
                     T* dlogits, uint64_t dstride) {
-  constexpr int kN = Chunk<T>::kN;
-  constexpr uint64_t kPiece = kThreads * kUnroll * kN;
+  constexpr int kN = Chunk<T>::kN, kUnroll = unroll(kLanes);
+  constexpr int kTeams = (kLanes == 32 ? kWarpThreads : kThreads) / kLanes;
+  constexpr uint64_t kPiece = kLanes * kUnroll * kN;
+  const uint32_t lane = threadIdx.x % kLanes;
   pdl_trigger();
   pdl_wait();
-  for (uint64_t b = blockIdx.x; b < rows * pieces; b += gridDim.x) {
+  const uint64_t step = static_cast<uint64_t>(gridDim.x) * kTeams;
+  for (uint64_t b = static_cast<uint64_t>(blockIdx.x) * kTeams + threadIdx.x / kLanes;
+       b < rows * pieces; b += step) {
     const uint64_t t = rows - 1 - b / pieces, lo = b % pieces * kPiece;
     const int64_t label = labels[t];
     const int32_t p = row_pair[t];
@@ -297,20 +341,20 @@ __global__ void __launch_bounds__(kThreads)
     auto one = [&](uint64_t at) { d[at] = from_f32<T>(counted ? value(to_f32(x[at]), at) : 0.f); };
     const uint32_t head = to_boundary(d, n);
     if (counted && to_boundary(x, n) != head) {  // the two lie differently: one by one
-      for (uint64_t k = threadIdx.x; k < n; k += kThreads) one(k);
+      for (uint64_t k = lane; k < n; k += kLanes) one(k);
       continue;
     }
-    if (threadIdx.x < head) one(threadIdx.x);
+    if (lane < head) one(lane);
     const uint32_t chunks = static_cast<uint32_t>((n - head) / kN);
     uint4 w[kUnroll];
 #pragma unroll
     for (int u = 0; u < kUnroll; ++u) {
-      const uint32_t k = threadIdx.x + u * kThreads;
+      const uint32_t k = lane + u * kLanes;
       if (counted && k < chunks) w[u] = __ldcs(reinterpret_cast<const uint4*>(x + head + k * kN));
     }
 #pragma unroll
     for (int u = 0; u < kUnroll; ++u) {
-      const uint32_t k = threadIdx.x + u * kThreads;
+      const uint32_t k = lane + u * kLanes;
       if (k >= chunks) break;
       Chunk<T> out;
       T* e = reinterpret_cast<T*>(&out.w);
@@ -330,9 +374,15 @@ __global__ void __launch_bounds__(kThreads)
       }
       st_stream_v4(d + head + k * kN, out.w);
     }
-    const uint64_t tail = head + static_cast<uint64_t>(chunks) * kN + threadIdx.x;
+    const uint64_t tail = head + static_cast<uint64_t>(chunks) * kN + lane;
     if (tail < n) one(tail);
   }
+}
+
+// A warp takes a row (not a block) of at most 4 KB, a few rounds of its loads,
+// or of 16 KB where there are enough rows for every warp of the GPU.
+bool by_warps(uint64_t rows, uint64_t row_bytes) {
+  return row_bytes <= 4096 || (row_bytes <= 16384 && rows >= 32ull * sm_count());
 }
 
 bool logits_ok(uint64_t pairs, uint64_t rows, uint64_t vocab, const void* logits, int type,
@@ -347,15 +397,14 @@ cudaError_t forward_rows(uint64_t rows, uint64_t vocab, const T* logits, uint64_
                          const int64_t* labels, float* logps, float* lse, float* row_grad,
                          int32_t* row_pair, cudaStream_t st) {
   const uint64_t sms = sm_count();
-  // a warp takes a row while that row is a few rounds of its loads
-  if (vocab * sizeof(T) <= 4096)
-    return launch_chained(short_rows_kernel<T>, static_cast<unsigned>((rows + 7) / 8), kThreads, 0,
-                          st, rows, vocab, logits, stride, labels, logps, lse, row_grad, row_pair);
+  if (by_warps(rows, vocab * sizeof(T)))
+    return launch_chained(short_rows_kernel<T>, static_cast<unsigned>((rows + 3) / 4), kWarpThreads,
+                          0, st, rows, vocab, logits, stride, labels, logps, lse, row_grad, row_pair);
   // few rows: clusters share them while there is room on the SMs and a part
   // keeps a round of its block's loads
   uint32_t parts = 1;
   while (parts < kMaxParts && rows * parts <= sms &&
-         vocab * sizeof(T) >= 2ull * parts * kThreads * kUnroll * 16)
+         vocab * sizeof(T) >= 2ull * parts * kThreads * unroll(kThreads) * 16)
     parts *= 2;
   if (rows > 0x7FFFFFFFull / parts) return cudaErrorInvalidValue;
   cudaLaunchConfig_t cfg = {};
@@ -429,12 +478,16 @@ hkv_status hkv_preference_loss_backward(uint64_t pairs, uint64_t rows, uint64_t 
   cudaStream_t st = static_cast<cudaStream_t>(stream);
   return op_status(with_type(type, [&](auto* t) {
     using T = std::remove_pointer_t<decltype(t)>;
-    constexpr uint64_t kPiece = kThreads * kUnroll * Chunk<T>::kN;
-    const uint64_t pieces = (vocab + kPiece - 1) / kPiece;
-    const uint64_t blocks = rows * pieces < 0x7FFFFFFF ? rows * pieces : 0x7FFFFFFF;
-    return launch_chained(backward_kernel<T>, static_cast<unsigned>(blocks), kThreads, 0, st, pairs,
-                          rows, vocab, static_cast<const T*>(logits), stride, pieces, labels, lse,
-                          row_grad, row_pair, dlosses, static_cast<T*>(dlogits), dstride);
+    const bool warps = by_warps(rows, vocab * sizeof(T));
+    const int lanes = warps ? 32 : kThreads;
+    const uint64_t piece = static_cast<uint64_t>(lanes) * unroll(lanes) * Chunk<T>::kN;
+    const uint64_t pieces = (vocab + piece - 1) / piece;
+    const int threads = warps ? kWarpThreads : kThreads;
+    const uint64_t blocks = (rows * pieces * lanes + threads - 1) / threads;
+    return launch_chained(warps ? backward_kernel<T, 32> : backward_kernel<T, kThreads>,
+                          static_cast<unsigned>(blocks < 0x7FFFFFFF ? blocks : 0x7FFFFFFF), threads,
+                          0, st, pairs, rows, vocab, static_cast<const T*>(logits), stride, pieces,
+                          labels, lse, row_grad, row_pair, dlosses, static_cast<T*>(dlogits), dstride);
   }));
 }
 
