@@ -17,8 +17,11 @@
 namespace hkv {
 namespace {
 
-constexpr int kThreads = 512;
-constexpr int kUnroll = 4;  // groups of eight elements in flight per thread
+constexpr int kThreads = 256;
+constexpr int kPerSm = 4;  // blocks
+// groups of eight elements in flight per thread: 128 bytes
+template <class T>
+constexpr int kUnroll = sizeof(T) == 4 ? 4 : 8;
 constexpr int kMaxPartials = HKV_CLIP_WORK_BYTES / 4;
 
 // One launch's gradients, passed as a kernel argument (no copy to the device
@@ -80,7 +83,7 @@ __device__ __forceinline__ int lead(const T* x, const U* y) {
 }
 
 template <int N>
-__global__ void __launch_bounds__(kThreads)
+__global__ void __launch_bounds__(kThreads, kPerSm)
     norm_kernel(const __grid_constant__ Batch<N> b, float* partial, bool more) {
   __shared__ float red[kThreads / 32];
   pdl_trigger();
@@ -104,12 +107,12 @@ __global__ void __launch_bounds__(kThreads)
         for (int i = 0; i < 8; ++i) s[i & 1] = fmaf(v[i], v[i], s[i & 1]);
       };
       uint32_t k = threadIdx.x;
-      for (; k + (kUnroll - 1) * kThreads < eights; k += kUnroll * kThreads) {
-        Eight<T> in[kUnroll];
+      for (; k + (kUnroll<T> - 1) * kThreads < eights; k += kUnroll<T> * kThreads) {
+        Eight<T> in[kUnroll<T>];
 #pragma unroll
-        for (int u = 0; u < kUnroll; ++u) in[u].load_aligned(x + (k + u * kThreads) * 8, kWhole);
+        for (int u = 0; u < kUnroll<T>; ++u) in[u].load_aligned(x + (k + u * kThreads) * 8, kWhole);
 #pragma unroll
-        for (int u = 0; u < kUnroll; ++u) add(in[u]);
+        for (int u = 0; u < kUnroll<T>; ++u) add(in[u]);
       }
       for (; k < eights; k += kThreads) {
         Eight<T> in;
@@ -129,7 +132,7 @@ __global__ void __launch_bounds__(kThreads)
 }
 
 template <int N>
-__global__ void __launch_bounds__(kThreads)
+__global__ void __launch_bounds__(kThreads, kPerSm)
     clip_kernel(const __grid_constant__ Batch<N> b, const float* partial, int partials,
                 float max_norm, float* norm_out) {
   __shared__ float red[kThreads / 32];
@@ -167,12 +170,12 @@ __global__ void __launch_bounds__(kThreads)
           out.store_aligned(y + k * 8, kWhole);
         };
         uint32_t k = threadIdx.x;
-        for (; k + (kUnroll - 1) * kThreads < eights; k += kUnroll * kThreads) {
-          Eight<T> in[kUnroll];
+        for (; k + (kUnroll<T> - 1) * kThreads < eights; k += kUnroll<T> * kThreads) {
+          Eight<T> in[kUnroll<T>];
 #pragma unroll
-          for (int q = 0; q < kUnroll; ++q) in[q].load_written(x + (k + q * kThreads) * 8);
+          for (int q = 0; q < kUnroll<T>; ++q) in[q].load_written(x + (k + q * kThreads) * 8);
 #pragma unroll
-          for (int q = 0; q < kUnroll; ++q) scale(in[q], k + q * kThreads);
+          for (int q = 0; q < kUnroll<T>; ++q) scale(in[q], k + q * kThreads);
         }
         for (; k < eights; k += kThreads) {
           Eight<T> in;
@@ -211,9 +214,9 @@ cudaError_t for_batches(uint64_t count, const hkv_grad* g, uint32_t chunk, F&& f
 template <int N>
 cudaError_t clip(uint64_t count, const hkv_grad* g, uint64_t total, bool writes, float max_norm,
                  float* norm_out, float* work, cudaStream_t st) {
-  // four blocks of 512 threads fill an SM; small totals are cut finer, so
-  // that every SM has some
-  const int grid = std::min(kMaxPartials, sm_count() * 4);
+  // every block resident, so that none starts when others end; small totals
+  // are cut finer, so that every SM has some
+  const int grid = std::min(kMaxPartials, sm_count() * kPerSm);
   uint32_t chunk = 4096;
   while (chunk < 16384 && total / chunk > static_cast<uint64_t>(grid)) chunk *= 2;
   auto blocks = [&](const Batch<N>& b) {
