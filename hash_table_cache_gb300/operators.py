@@ -325,7 +325,8 @@ def clip_grad_norm(grads, max_norm, outs="in place", stream=None):
     and clipping to ``max_norm``: in place (the default, also ``outs=None``), into
     the tensors ``outs`` (of any of the three types), or not at all
     (``outs=()``: the norm alone).  Tensors have to be dense; an out tensor has
-    its gradient's shape and strides."""
+    as many elements as its gradient, and lies in memory in the same order
+    (both contiguous, or the same shape and strides)."""
     grads = [grads] if isinstance(grads, torch.Tensor) else list(grads)
     if not grads:
         raise ValueError("grads: at least one tensor")
@@ -363,15 +364,18 @@ def _clip(s, grads, outs, max_norm):
     data, types, plain = _fields(grads, "grads", device)
     table = array("Q", bytes(32 * n))  # hkv_grad: data, out, n, type | out_type << 32
     table[0::4] = data
-    table[2::4] = array("Q", map(torch.Tensor.numel, grads))
+    sizes = array("Q", map(torch.Tensor.numel, grads))
+    table[2::4] = sizes
     if outs is grads:
         table[1::4] = data
         table[3::4] = array("Q", [t | t << 32 for t in types])
     elif outs:
         to, out_types, out_plain = _fields(outs, "outs", device)
-        for o, g in zip(outs, grads):
-            if o.shape != g.shape or not (plain and out_plain) and o.stride() != g.stride():
-                raise ValueError("outs: the shapes and strides of the gradients")
+        same = array("Q", map(torch.Tensor.numel, outs)) == sizes
+        if same and not (plain and out_plain):
+            same = all(o.shape == g.shape and o.stride() == g.stride() for o, g in zip(outs, grads))
+        if not same:
+            raise ValueError("outs: the sizes and the order in memory of the gradients")
         table[1::4] = to
         table[3::4] = array("Q", [t | u << 32 for t, u in zip(types, out_types)])
     else:
