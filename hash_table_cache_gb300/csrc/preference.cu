@@ -22,7 +22,9 @@ constexpr int kPairThreads = 256;
 constexpr int kMaxParts = 8;  // blocks of a cluster that share a row
 // 16-byte loads in flight per thread where kLanes threads share a row
 __host__ __device__ constexpr int unroll(int lanes) { return lanes == 32 ? 8 : 4; }
-constexpr float kLog2e = 1.44269504f;
+// log2 e in two floats: one alone is off by 1e-8 of it, which leans one way in
+// every exponential
+constexpr float kLog2e = 1.44269504f, kLog2eRest = 1.92596299e-8f;
 
 __device__ __forceinline__ float exp2_approx(float x) {
   float y;
@@ -119,15 +121,17 @@ __device__ __forceinline__ Running row_pass(const T* x, uint64_t n, int lane) {
     const float base = r.raise(largest(c));
     float part[4] = {};
     if (fabsf(base) < 1e37f) {
-      // exp(x - base) as 2^(x log2 e - base log2 e), one multiply-add each.
-      // The same rounded base log2 e is in every term; what it is off by is
-      // taken out of their sum.
-      const float scaled = base * kLog2e, off = fmaf(base, kLog2e, -scaled);
+      // exp(x - base) as 2^(x log2 e - base log2 e), by two multiply-adds.  The
+      // same rounded base log2 e is in every term; what it is off by is taken
+      // out of their sum.
+      const float scaled = base * kLog2e;
+      const float off = fmaf(base, kLog2eRest, fmaf(base, kLog2e, -scaled));
 #pragma unroll
       for (int u = 0; u < kUnroll; ++u)
 #pragma unroll
         for (int i = 0; i < kN; ++i)
-          part[i & 3] += exp2_approx(fmaf(c[u].at(i), kLog2e, -scaled));
+          part[i & 3] += exp2_approx(
+              fmaf(c[u].at(i), kLog2eRest, fmaf(c[u].at(i), kLog2e, -scaled)));
       r.s = fmaf((part[0] + part[1]) + (part[2] + part[3]), exp2_approx(-off), r.s);
     } else {  // a product with log2 e might overflow
 #pragma unroll
