@@ -8,6 +8,7 @@
 // or by a block, depending on their length; a few long rows are shared by
 // the blocks of a cluster, which join their parts through distributed shared
 // memory in a fixed order, so no partial result goes through global memory.
+#include <cfloat>
 #include <cmath>
 #include <type_traits>
 
@@ -30,6 +31,28 @@ __device__ __forceinline__ float exp2_approx(float x) {
   float y;
   asm("ex2.approx.f32 %0, %1;" : "=f"(y) : "f"(x));
   return y;
+}
+
+// Two floats in one 64-bit register: one instruction works on both.
+__device__ __forceinline__ uint64_t both(float a, float b) {
+  uint64_t r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(a), "f"(b));
+  return r;
+}
+__device__ __forceinline__ float2 parts(uint64_t v) {
+  float2 r;
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(r.x), "=f"(r.y) : "l"(v));
+  return r;
+}
+__device__ __forceinline__ uint64_t fma_both(uint64_t a, uint64_t b, uint64_t c) {
+  uint64_t r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+  return r;
+}
+__device__ __forceinline__ uint64_t add_both(uint64_t a, uint64_t b) {
+  uint64_t r;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
 }
 
 // Neighbouring elements in 16 bytes.
@@ -83,7 +106,7 @@ struct Running {
   // subtract from them (0 while all are -inf: their exponentials are 0).
   __device__ __forceinline__ float raise(float top) {
     if (top > m) {
-      s *= __expf(m - top);
+      s *= expf(m - top);
       m = top;
     }
     return m == -INFINITY ? 0.f : m;
@@ -94,11 +117,25 @@ struct Running {
   }
   __device__ __forceinline__ void join(float m2, float s2) {
     const float top = fmaxf(m, m2);
-    s = (m == top ? s : s * __expf(m - top)) + (m2 == top ? s2 : s2 * __expf(m2 - top));
+    s = (m == top ? s : s * expf(m - top)) + (m2 == top ? s2 : s2 * expf(m2 - top));
     m = top;
   }
-  __device__ __forceinline__ float log_sum() const {
-    return m == -INFINITY && s == 0.f ? -INFINITY : m + logf(s);
+  // m + log s as a float and what it leaves out.  With s = 2^e f the product
+  // of e and the upper digits of log 2 is exact (Cody and Waite), and so is
+  // what the addition to m rounds off.
+  __device__ __forceinline__ float log_sum(float& rest) const {
+    rest = 0.f;
+    if (!(s >= FLT_MIN && s <= FLT_MAX && fabsf(m) <= FLT_MAX))
+      return m == -INFINITY && s == 0.f ? -INFINITY : m + logf(s);
+    const int bits = __float_as_int(s), e = (bits >> 23) - 127;
+    const float f = __int_as_float((bits & 0x7FFFFF) | 0x3F800000);
+    const float a = static_cast<float>(e) * 0.693145751953125f;
+    const float hi = m + a, back = hi - m;
+    const float lo = (m - (hi - back)) + (a - back) +
+                     (logf(f) + static_cast<float>(e) * 1.42860682e-6f);
+    const float l = hi + lo;
+    rest = lo - (l - hi);
+    return l;
   }
 };
 
@@ -119,26 +156,32 @@ __device__ __forceinline__ Running row_pass(const T* x, uint64_t n, int lane) {
       else c[u].fill_lowest();
     }
     const float base = r.raise(largest(c));
-    float part[4] = {};
     if (fabsf(base) < 1e37f) {
       // exp(x - base) as 2^(x log2 e - base log2 e), by two multiply-adds.  The
       // same rounded base log2 e is in every term; what it is off by is taken
       // out of their sum.
       const float scaled = base * kLog2e;
       const float off = fmaf(base, kLog2eRest, fmaf(base, kLog2e, -scaled));
+      const uint64_t l = both(kLog2e, kLog2e), rest = both(kLog2eRest, kLog2eRest);
+      const uint64_t minus = both(-scaled, -scaled);
+      uint64_t sum[2] = {};
 #pragma unroll
       for (int u = 0; u < kUnroll; ++u)
 #pragma unroll
-        for (int i = 0; i < kN; ++i)
-          part[i & 3] += exp2_approx(
-              fmaf(c[u].at(i), kLog2eRest, fmaf(c[u].at(i), kLog2e, -scaled)));
-      r.s = fmaf((part[0] + part[1]) + (part[2] + part[3]), exp2_approx(-off), r.s);
+        for (int i = 0; i < kN; i += 2) {
+          const uint64_t x2 = both(c[u].at(i), c[u].at(i + 1));
+          const float2 a = parts(fma_both(x2, rest, fma_both(x2, l, minus)));
+          sum[i / 2 & 1] = add_both(sum[i / 2 & 1], both(exp2_approx(a.x), exp2_approx(a.y)));
+        }
+      const float2 t = parts(add_both(sum[0], sum[1]));
+      r.s = fmaf(t.x + t.y, exp2_approx(-off), r.s);
     } else {  // a product with log2 e might overflow
+      float part = 0.f;
 #pragma unroll
       for (int u = 0; u < kUnroll; ++u)
 #pragma unroll
-        for (int i = 0; i < kN; ++i) part[i & 3] += __expf(c[u].at(i) - base);
-      r.s += (part[0] + part[1]) + (part[2] + part[3]);
+        for (int i = 0; i < kN; ++i) part += __expf(c[u].at(i) - base);
+      r.s += part;
     }
   }
   const uint64_t tail = head + chunks * kN + lane;
@@ -150,17 +193,22 @@ __device__ __forceinline__ bool counts(int64_t label, uint64_t vocab) {
   return label >= 0 && static_cast<uint64_t>(label) < vocab;
 }
 
+// A warp's lanes: the maximum first, so that each sum is brought to it once.
 __device__ __forceinline__ Running join_lanes(Running r) {
-  for (int o = 16; o > 0; o >>= 1)
-    r.join(__shfl_xor_sync(0xFFFFFFFFu, r.m, o), __shfl_xor_sync(0xFFFFFFFFu, r.s, o));
+  float top = r.m;
+  for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xFFFFFFFFu, top, o));
+  if (r.m != top) r.s *= expf(r.m - top);
+  r.m = top;
+  for (int o = 16; o > 0; o >>= 1) r.s += __shfl_xor_sync(0xFFFFFFFFu, r.s, o);
   return r;
 }
 
 __device__ __forceinline__ void finish_row(const Running& r, float chosen, uint64_t t, float* logps,
                                            float* lse) {
-  const float l = r.log_sum();
+  float rest;
+  const float l = r.log_sum(rest);
   lse[t] = l;
-  logps[t] = chosen - l;
+  logps[t] = (chosen - l) - rest;
 }
 
 // A warp per row: short rows.
@@ -222,10 +270,17 @@ __global__ void __launch_bounds__(kThreads)
     ms[1][warp] = r.s;
   }
   __syncthreads();
-  if (threadIdx.x == 0) {
-    for (int w = 1; w < kThreads / 32; ++w) r.join(ms[0][w], ms[1][w]);
-    ms[0][kThreads / 32] = r.m;
-    ms[1][kThreads / 32] = r.s;
+  if (warp == 0) {
+    r = Running{};
+    if (threadIdx.x < kThreads / 32) {
+      r.m = ms[0][threadIdx.x];
+      r.s = ms[1][threadIdx.x];
+    }
+    r = join_lanes(r);
+    if (threadIdx.x == 0) {
+      ms[0][kThreads / 32] = r.m;
+      ms[1][kThreads / 32] = r.s;
+    }
   }
   if (parts > 1) {
     __syncwarp();
