@@ -239,7 +239,7 @@ __global__ void __launch_bounds__(kWarpThreads)
 
 // A block per row, or the `parts` blocks of a cluster.
 template <class T>
-__global__ void __launch_bounds__(kThreads)
+__global__ void __launch_bounds__(kThreads, 8)
     long_rows_kernel(uint64_t vocab, const T* __restrict__ logits, uint64_t stride, uint32_t parts,
                      const int64_t* __restrict__ labels, float* logps, float* lse, float* row_grad,
                      int32_t* row_pair) {
