@@ -342,8 +342,8 @@ def clip_grad_norm(grads, max_norm, outs="in place", stream=None):
 
 
 def _fields(tensors, what, device):
-    """Addresses and types of dense tensors of one device, and whether all of
-    them are contiguous.  One C call per tensor and field: hundreds of tensors
+    """Addresses of dense tensors of one device, their types (one number where
+    they share it), and whether all of them are contiguous.  One C call per tensor and field: hundreds of tensors
     are common here."""
     of = torch.Tensor
     if set(map(of.get_device, tensors)) != {device.index}:
@@ -351,11 +351,23 @@ def _fields(tensors, what, device):
     plain = all(map(of.is_contiguous, tensors))
     if not plain and not all(map(_dense, tensors)):
         raise ValueError(f"{what}: tensors have to be dense")
+    kinds = list(map(_dtype_of, tensors))
     try:
-        types = array("Q", map(_TYPES.__getitem__, map(_dtype_of, tensors)))
+        if kinds.count(kinds[0]) == len(kinds):
+            types = _TYPES[kinds[0]]
+        else:
+            types = list(map(_TYPES.__getitem__, kinds))
     except KeyError as e:
         raise ValueError(f"{what}: float32, bfloat16 or float16, not {e.args[0]}") from None
     return array("Q", map(of.data_ptr, tensors)), types, plain
+
+
+def _both_types(types, out_types, n):
+    """type | out_type << 32 of every gradient; a number stands for all of them."""
+    if isinstance(types, int) and isinstance(out_types, int):
+        return array("Q", (types | out_types << 32,)) * n
+    types, out_types = ([t] * n if isinstance(t, int) else t for t in (types, out_types))
+    return array("Q", [t | u << 32 for t, u in zip(types, out_types)])
 
 
 def _clip(s, grads, outs, max_norm):
@@ -368,7 +380,7 @@ def _clip(s, grads, outs, max_norm):
     table[2::4] = sizes
     if outs is grads:
         table[1::4] = data
-        table[3::4] = array("Q", [t | t << 32 for t in types])
+        table[3::4] = _both_types(types, types, n)
     elif outs:
         to, out_types, out_plain = _fields(outs, "outs", device)
         same = array("Q", map(torch.Tensor.numel, outs)) == sizes
@@ -377,9 +389,9 @@ def _clip(s, grads, outs, max_norm):
         if not same:
             raise ValueError("outs: the sizes and the order in memory of the gradients")
         table[1::4] = to
-        table[3::4] = array("Q", [t | u << 32 for t, u in zip(types, out_types)])
+        table[3::4] = _both_types(types, out_types, n)
     else:
-        table[3::4] = types
+        table[3::4] = _both_types(types, 0, n)
     norm = torch.empty((), dtype=torch.float32, device=device)
     work = torch.empty(_abi.CLIP_WORK_BYTES, dtype=torch.uint8, device=device)
     _ok(_abi.load().hkv_clip_grad_norm(n, table.buffer_info()[0], max_norm, norm.data_ptr(),
