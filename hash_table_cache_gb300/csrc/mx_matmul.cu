@@ -262,6 +262,24 @@ __device__ __forceinline__ uint32_t pack2(float lo, float hi) {
   return *reinterpret_cast<const uint32_t*>(&h);
 }
 
+// Columns j .. j + 3 of row i of y, with B in the lanes.
+__device__ __forceinline__ void store_four(const Problem& p, uint64_t i, uint64_t j, float4 v) {
+  const uint64_t at = i * p.stride + j;
+  if (p.wide && j + 4 <= p.lanes) {
+    if (p.type == HKV_F32)
+      *reinterpret_cast<float4*>(static_cast<float*>(p.y) + at) = v;
+    else
+      *reinterpret_cast<uint2*>(static_cast<uint16_t*>(p.y) + at) =
+          p.type == HKV_BF16 ? make_uint2(pack2<true>(v.x, v.y), pack2<true>(v.z, v.w))
+                             : make_uint2(pack2<false>(v.x, v.y), pack2<false>(v.z, v.w));
+    return;
+  }
+  const float e[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+  for (int k = 0; k < 4; ++k)
+    if (j + k < p.lanes) store_one(p, i, j + k, e[k]);
+}
+
 // B in the lanes: N accumulator columns are rows of y from i on, of this
 // lane's column j.
 template <int N>
@@ -383,6 +401,10 @@ __global__ void __launch_bounds__(kThreads, 1)
   const uint32_t half_of = kBlocks == 2 ? rank : 0, part = splits > 1 ? rank : 0;
 
   if (warp == 0 && lane == 0) {
+    const CUtensorMap* map[4] = {&maps.lanes, &maps.cols, &maps.lanes_scales, &maps.cols_scales};
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+      asm volatile("prefetch.tensormap [%0];" ::"l"(map[i]) : "memory");
     for (int s = 0; s < S::kStages; ++s) {
       mbar_init(&full[s], 1);
       mbar_init(&empty[s], 1);
@@ -558,15 +580,28 @@ __global__ void __launch_bounds__(kThreads, 1)
   if (splits > 1) {
     cluster_sync();
     if (warp >= 2) {
-      const int row = (warp & 3) * 32 + lane, half = (warp - 2) >> 2;
-      const uint64_t l = static_cast<uint64_t>(t.col) * kRows + row;
+      // a warp takes a column, a thread four neighbouring lanes of it; all
+      // blocks' parts are on their way together and added in their order
+      const uint64_t l = static_cast<uint64_t>(t.col) * kRows + lane * 4;
       const uint64_t c0 = static_cast<uint64_t>(t.row) * kCols;
       const int cols = p.cols - c0 < kCols ? static_cast<int>(p.cols - c0) : kCols;
-      const uint32_t parts = smem_u32(smem) + row * 4;
-      for (int c = 2 * part + half; c < cols; c += 2 * splits) {
-        float v = 0.f;
-        for (uint32_t r = 0; r < splits; ++r) v += remote_f32(parts + c * kRows * 4, r);
-        if (l < p.lanes) store_one(p, c0 + c, l, v);
+#pragma unroll 2
+      for (int c = part + splits * (warp - 2); c < cols; c += kStoreWarps * splits) {
+        const uint32_t at = smem_u32(smem) + (c * kRows + lane * 4) * 4;
+        float4 v[kMaxSplits];
+#pragma unroll
+        for (uint32_t r = 0; r < kMaxSplits; ++r)
+          if (r < splits) v[r] = remote_f32x4(at, r);
+        float4 sum = v[0];
+#pragma unroll
+        for (uint32_t r = 1; r < kMaxSplits; ++r)
+          if (r < splits) {
+            sum.x += v[r].x;
+            sum.y += v[r].y;
+            sum.z += v[r].z;
+            sum.w += v[r].w;
+          }
+        store_four(p, c0 + c, l, sum);
       }
     }
     __syncwarp();
