@@ -15,10 +15,10 @@
 // With A in the lanes that is a piece of a row of y, and a warp turns its 32
 // pieces around in shared memory so that a store covers whole 128-byte lines
 // (a thread storing its own piece, a 32-byte sector of 32 rows at once,
-// reached 4.4 TB/s of y where this reaches 5.8: 2048 x 131072 x 64).  With B in the lanes a warp's
-// lanes are 32 neighbouring columns of one row of y: that is for the few rows
-// of a token or a small batch, which would leave most lanes empty the other
-// way, and for a y whose rows do not start on 16-byte boundaries.
+// reached 4.4 TB/s of y where this reaches 5.6: 2048 x 131072 x 64).  With B
+// in the lanes a warp's lanes are 32 neighbouring columns of one row of y:
+// that is for the few rows of a token or a small batch, which would leave most
+// lanes empty the other way.
 #include <cuda.h>
 #include <type_traits>
 
@@ -303,13 +303,19 @@ __device__ __forceinline__ void store_columns(const Problem& p, uint64_t i, uint
 }
 
 // A in the lanes: columns kFrom .. kFrom + kN - 1 of v are columns j ..
-// j + kN - 1 of y; the warp's lanes are its rows from i on.
-template <int kType, int kFrom, int kN, int N>
+// j + kN - 1 of y; the warp's lanes are its rows from i on.  kWide: y's rows
+// start on 16-byte boundaries; otherwise every row's piece is cut at the
+// boundaries that it has in y, the 16-byte words between them are put
+// together from two of the turned ones, and what lies before the first and
+// after the last boundary is stored element by element.
+template <int kType, bool kWide, int kFrom, int kN, int N>
 __device__ __forceinline__ void turn_and_store(uint8_t* room, const Problem& p, uint64_t i,
                                                uint64_t j, const float (&v)[N]) {
   constexpr int kSize = kType == HKV_F32 ? 4 : 2, kPer = 16 / kSize;
   constexpr int kLanes = kN * kSize / 16;  // threads that store a row's piece, 16 bytes each
+  constexpr int kRowsAtOnce = 32 / kLanes;
   static_assert(kN * kSize <= 128 && 32 % kLanes == 0, "a piece of a row");
+  using E = std::conditional_t<kSize == 4, uint32_t, uint16_t>;
   const int lane = threadIdx.x & 31;
 #pragma unroll
   for (int c = 0; c < kN; c += kPer) {
@@ -323,28 +329,40 @@ __device__ __forceinline__ void turn_and_store(uint8_t* room, const Problem& p, 
   }
   __syncwarp();
   const int first = lane / kLanes, at = lane % kLanes;
-  const uint64_t col = j + at * kPer;
-  const uint8_t* from = room + first * kTurnPitch + at * 16;
-  char* y = static_cast<char*>(p.y) + ((i + first) * p.stride + col) * kSize;
-  const uint64_t step = 32 / kLanes * p.stride * kSize;
-  if (i + 32 <= p.lanes && col + kPer <= p.cols) {
+  const uint8_t* from = room + first * kTurnPitch;
+  char* y = static_cast<char*>(p.y) + ((i + first) * p.stride + j) * kSize;
+  const uint64_t step = kRowsAtOnce * p.stride * kSize;
+  // what of the piece lies in y, and how many of this thread's rows
+  const int cols = p.cols - j < kN ? static_cast<int>(p.cols - j) : kN;
+  const int rows = p.lanes - i < 32 ? (static_cast<int>(p.lanes - i) - first + kRowsAtOnce - 1) / kRowsAtOnce
+                                    : kLanes;
+  // (__stcs, not the library's asm store, behind which no load would move up)
+  if (cols == kN && rows == kLanes) {
 #pragma unroll
-    for (int r = 0; r < kLanes; ++r, y += step)
-      st_stream_v4(y, *reinterpret_cast<const uint4*>(from + r * (32 / kLanes) * kTurnPitch));
-  } else {  // the ends of y
-    for (int r = 0; r < kLanes; ++r, y += step, from += 32 / kLanes * kTurnPitch) {
-      if (i + first + r * (32 / kLanes) >= p.lanes) break;
-      if (col + kPer <= p.cols) {
-        st_stream_v4(y, *reinterpret_cast<const uint4*>(from));
-        continue;
-      }
-      for (int e = 0; e < kPer && col + e < p.cols; ++e) {
-        if constexpr (kSize == 4)
-          reinterpret_cast<float*>(y)[e] = reinterpret_cast<const float*>(from)[e];
-        else
-          reinterpret_cast<uint16_t*>(y)[e] = reinterpret_cast<const uint16_t*>(from)[e];
+    for (int r = 0; r < kLanes; ++r, y += step, from += kRowsAtOnce * kTurnPitch) {
+      uint4 word = *reinterpret_cast<const uint4*>(from + at * 16);
+      if constexpr (kWide) {
+        __stcs(reinterpret_cast<uint4*>(y) + at, word);
+      } else {
+        const uint32_t up = (16 - (reinterpret_cast<uintptr_t>(y) & 15)) & 15;
+        // past the piece's last word lies padding, which is not stored
+        const uint4 next = *reinterpret_cast<const uint4*>(from + at * 16 + 16);
+        uint32_t x[8] = {word.x, word.y, word.z, word.w, next.x, next.y, next.z, next.w};
+        shift_bytes(x, up);
+        if (at < kLanes - 1 || up == 0)
+          __stcs(reinterpret_cast<uint4*>(y + up) + at, make_uint4(x[0], x[1], x[2], x[3]));
+        const int ahead = static_cast<int>(up / kSize);
+#pragma unroll
+        for (int t = 0; t < kPer; t += kLanes) {
+          const int e = t + at < ahead ? t + at : kN - kPer + t + at;
+          if (t + at < kPer && ahead) reinterpret_cast<E*>(y)[e] = reinterpret_cast<const E*>(from)[e];
+        }
       }
     }
+  } else {  // the ends of y, element by element
+    for (int r = 0; r < rows; ++r, y += step, from += kRowsAtOnce * kTurnPitch)
+      for (int e = at; e < cols; e += kLanes)
+        reinterpret_cast<E*>(y)[e] = reinterpret_cast<const E*>(from)[e];
   }
   __syncwarp();
 }
@@ -554,19 +572,25 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
       if (!any) continue;
       if constexpr (kAInLanes) {
-        auto store = [&](auto type) {
+        auto store = [&](auto type, auto wide) {
           constexpr int kType = decltype(type)::value;
+          constexpr bool kWide = decltype(wide)::value;
           if constexpr (kType == HKV_F32) {
-            turn_and_store<kType, 0, 32>(room, p, l, c + from, v);
-            turn_and_store<kType, 32, 32>(room, p, l, c + from + 32, v);
+            turn_and_store<kType, kWide, 0, 32>(room, p, l, c + from, v);
+            if (c + from + 32 < p.cols)
+              turn_and_store<kType, kWide, 32, 32>(room, p, l, c + from + 32, v);
           } else {
-            turn_and_store<kType, 0, 64>(room, p, l, c + from, v);
+            turn_and_store<kType, kWide, 0, 64>(room, p, l, c + from, v);
           }
-          turn_and_store<kType, 64, 32>(room, p, l, c + more, v);
+          if (c + more < p.cols) turn_and_store<kType, kWide, 64, 32>(room, p, l, c + more, v);
         };
-        if (p.type == HKV_F32) store(std::integral_constant<int, HKV_F32>{});
-        else if (p.type == HKV_BF16) store(std::integral_constant<int, HKV_BF16>{});
-        else store(std::integral_constant<int, HKV_F16>{});
+        auto with = [&](auto wide) {
+          if (p.type == HKV_F32) store(std::integral_constant<int, HKV_F32>{}, wide);
+          else if (p.type == HKV_BF16) store(std::integral_constant<int, HKV_BF16>{}, wide);
+          else store(std::integral_constant<int, HKV_F16>{}, wide);
+        };
+        if (p.wide) with(std::true_type{});
+        else with(std::false_type{});
       } else if (splits > 1) {  // this block's part of the sum, for the cluster to add up
         float* mine = reinterpret_cast<float*>(smem) + from * kRows + quarter * 32 + lane;
 #pragma unroll
@@ -722,8 +746,7 @@ cudaError_t matmul(Problem p, const Operand& a, const Operand& b, cudaStream_t s
   // pair: k 512 52 and 75 us, 1024 72 and 86, 1280 85 and 91, 2048 119 and 101.
   // Where pairs leave SMs without a tile, single blocks have twice as many.
   const bool pair = steps > 5 && (m + 191) / 192 * ((n + 255) / 256) * 2 > sms;
-  if (p.wide) return pair ? run<192, 2, true>(p, a, b, 1, st) : run<192, 1, true>(p, a, b, 1, st);
-  return pair ? run<192, 2, false>(p, a, b, 1, st) : run<192, 1, false>(p, a, b, 1, st);
+  return pair ? run<192, 2, true>(p, a, b, 1, st) : run<192, 1, true>(p, a, b, 1, st);
 }
 
 }  // namespace
