@@ -395,10 +395,12 @@ hkv_status hkv_mx_matmul(uint64_t m, uint64_t n, uint64_t k, const uint8_t* a_co
  *   h         = beta * (ratios[p] - ratios[pairs + p])
  *   losses[p] = -(1 - label_smoothing) log sigmoid(h)
  *               - label_smoothing log sigmoid(-h)
- * logps is 0 for tokens that are not counted.  For the backward call the
- * forward call also writes row_grad[t] = d losses[p] / d logps[t] (0 for
- * tokens that are not counted or lie in no sequence) and row_pair[t] = p (-1
- * in no sequence).  beta is finite, 0 <= label_smoothing <= 1. */
+ * logps is 0 for tokens that are not counted.  Sums are taken in float32, so
+ * ratios of logits near that type's range may overflow to infinities.  For the
+ * backward call the forward call also writes row_grad[t] = d losses[p] /
+ * d logps[t] (0 for tokens that are not counted or lie in no sequence) and
+ * row_pair[t] = p (-1 in no sequence).  beta is finite,
+ * 0 <= label_smoothing <= 1. */
 hkv_status hkv_preference_loss(uint64_t pairs, uint64_t rows, uint64_t vocab, const void* logits,
                                int type, uint64_t stride, const int64_t* labels,
                                const int64_t* offsets, const float* ref_logps, float beta,
