@@ -23,6 +23,11 @@ constexpr int kPairThreads = 256;
 constexpr int kMaxParts = 8;  // blocks of a cluster that share a row
 // 16-byte loads in flight per thread where kLanes threads share a row
 __host__ __device__ constexpr int unroll(int lanes) { return lanes == 32 ? 8 : 4; }
+// ex2.approx returns a little less than 2^x on average.  On the logarithm of a
+// row's sum that came to 1e-8 to 3.3e-8 (rows of 1000 to 131072 logits of
+// three types): nothing beside the rounding of one token, but a sequence adds
+// its tokens up.
+constexpr float kExpMean = 2.2e-8f;
 // log2 e in two floats: one alone is off by 1e-8 of it, which leans one way in
 // every exponential
 constexpr float kLog2e = 1.44269504f, kLog2eRest = 1.92596299e-8f;
@@ -132,7 +137,7 @@ struct Running {
     const float a = static_cast<float>(e) * 0.693145751953125f;
     const float hi = m + a, back = hi - m;
     const float lo = (m - (hi - back)) + (a - back) +
-                     (logf(f) + static_cast<float>(e) * 1.42860682e-6f);
+                     (logf(f) + (static_cast<float>(e) * 1.42860682e-6f + kExpMean));
     const float l = hi + lo;
     rest = lo - (l - hi);
     return l;
