@@ -47,8 +47,9 @@ struct Problem {
   int splits;  // thread blocks of a cluster that share a tile's k
 };
 
-// Where a warp turns 32 pieces of rows around: 128 bytes and 16 of padding
-// each, so that neither side of the turn meets a bank twice.
+// Where a warp turns 32 pieces of rows around: 128 bytes, and 16 before them
+// for what precedes the piece in its row, which also keeps either side of the
+// turn from meeting a bank twice.
 constexpr int kTurnPitch = 144, kTurnWarp = 32 * kTurnPitch;
 
 struct Maps {  // codes and scales of the two matrices
@@ -239,6 +240,15 @@ __device__ __forceinline__ void read_columns(uint32_t tmem, float (&v)[N]) {
         : "r"(tmem + c));
   }
 }
+template <int kFrom, int N>
+__device__ __forceinline__ void read_eight(uint32_t tmem, float (&v)[N]) {
+  uint32_t* r = reinterpret_cast<uint32_t*>(v) + kFrom;
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]),
+        "=r"(r[7])
+      : "r"(tmem));
+}
 template <int N>
 __device__ __forceinline__ void columns_read(float (&v)[N]) {
   asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
@@ -302,34 +312,49 @@ __device__ __forceinline__ void store_columns(const Problem& p, uint64_t i, uint
     if (i + c < p.cols) store_one(p, i + c, j, v[c]);
 }
 
+// 16 bytes of a row of y from accumulator columns kFrom on.
+template <int kType, int kFrom, int N>
+__device__ __forceinline__ uint4 word_of(const float (&v)[N]) {
+  if constexpr (kType == HKV_F32)
+    return make_uint4(__float_as_uint(v[kFrom]), __float_as_uint(v[kFrom + 1]),
+                      __float_as_uint(v[kFrom + 2]), __float_as_uint(v[kFrom + 3]));
+  else
+    return make_uint4(pack2<kType == HKV_BF16>(v[kFrom], v[kFrom + 1]),
+                      pack2<kType == HKV_BF16>(v[kFrom + 2], v[kFrom + 3]),
+                      pack2<kType == HKV_BF16>(v[kFrom + 4], v[kFrom + 5]),
+                      pack2<kType == HKV_BF16>(v[kFrom + 6], v[kFrom + 7]));
+}
+template <int kType, int kFrom, int kN, int N>
+__device__ __forceinline__ void stage_row(uint8_t* row, const float (&v)[N]) {
+  constexpr int kPer = kType == HKV_F32 ? 4 : 8;
+  *reinterpret_cast<uint4*>(row) = word_of<kType, kFrom>(v);
+  if constexpr (kN > kPer) stage_row<kType, kFrom + kPer, kN - kPer>(row + 16, v);
+}
+
 // A in the lanes: columns kFrom .. kFrom + kN - 1 of v are columns j ..
-// j + kN - 1 of y; the warp's lanes are its rows from i on.  kWide: y's rows
-// start on 16-byte boundaries; otherwise every row's piece is cut at the
-// boundaries that it has in y, the 16-byte words between them are put
-// together from two of the turned ones, and what lies before the first and
-// after the last boundary is stored element by element.
-template <int kType, bool kWide, int kFrom, int kN, int N>
+// j + kN - 1 of y, a piece of each of the warp's rows, from i on.  kWide: y's
+// rows start on 16-byte boundaries.  Otherwise every row is cut at the
+// boundaries that it has in y.  A word that lies across the start of a piece
+// is the work of that piece, for which `before` are the columns before it (the
+// last of them in before[kBefore + 7]); the tile's first and last words, whose
+// rest belongs to other tiles, are stored element by element (`starts`, `ends`).
+template <int kType, bool kWide, int kFrom, int kN, int kBefore, int N, int M>
 __device__ __forceinline__ void turn_and_store(uint8_t* room, const Problem& p, uint64_t i,
-                                               uint64_t j, const float (&v)[N]) {
+                                               uint64_t j, const float (&v)[N],
+                                               const float (&before)[M], bool starts, bool ends) {
   constexpr int kSize = kType == HKV_F32 ? 4 : 2, kPer = 16 / kSize;
   constexpr int kLanes = kN * kSize / 16;  // threads that store a row's piece, 16 bytes each
   constexpr int kRowsAtOnce = 32 / kLanes;
   static_assert(kN * kSize <= 128 && 32 % kLanes == 0, "a piece of a row");
   using E = std::conditional_t<kSize == 4, uint32_t, uint16_t>;
   const int lane = threadIdx.x & 31;
-#pragma unroll
-  for (int c = 0; c < kN; c += kPer) {
-    uint32_t w[4];
-#pragma unroll
-    for (int e = 0; e < 4; ++e)
-      w[e] = kType == HKV_F32 ? __float_as_uint(v[kFrom + c + e])
-                              : pack2<kType == HKV_BF16>(v[kFrom + c + 2 * e % kPer],
-                                                         v[kFrom + c + (2 * e + 1) % kPer]);
-    *reinterpret_cast<uint4*>(room + lane * kTurnPitch + c * kSize) = make_uint4(w[0], w[1], w[2], w[3]);
-  }
+  uint8_t* mine = room + lane * kTurnPitch;
+  if constexpr (!kWide)
+    *reinterpret_cast<uint4*>(mine) = word_of<kType, kBefore + 8 - kPer>(before);
+  stage_row<kType, kFrom, kN>(mine + 16, v);
   __syncwarp();
   const int first = lane / kLanes, at = lane % kLanes;
-  const uint8_t* from = room + first * kTurnPitch;
+  const uint8_t* from = room + first * kTurnPitch + 16;
   char* y = static_cast<char*>(p.y) + ((i + first) * p.stride + j) * kSize;
   const uint64_t step = kRowsAtOnce * p.stride * kSize;
   // what of the piece lies in y, and how many of this thread's rows
@@ -338,31 +363,37 @@ __device__ __forceinline__ void turn_and_store(uint8_t* room, const Problem& p, 
                                     : kLanes;
   // (__stcs, not the library's asm store, behind which no load would move up)
   if (cols == kN && rows == kLanes) {
+    ends |= j + kN == p.cols;
 #pragma unroll
     for (int r = 0; r < kLanes; ++r, y += step, from += kRowsAtOnce * kTurnPitch) {
-      uint4 word = *reinterpret_cast<const uint4*>(from + at * 16);
+      const uint4 word = *reinterpret_cast<const uint4*>(from + at * 16);
       if constexpr (kWide) {
         __stcs(reinterpret_cast<uint4*>(y) + at, word);
       } else {
-        const uint32_t up = (16 - (reinterpret_cast<uintptr_t>(y) & 15)) & 15;
-        // past the piece's last word lies padding, which is not stored
-        const uint4 next = *reinterpret_cast<const uint4*>(from + at * 16 + 16);
-        uint32_t x[8] = {word.x, word.y, word.z, word.w, next.x, next.y, next.z, next.w};
-        shift_bytes(x, up);
-        if (at < kLanes - 1 || up == 0)
-          __stcs(reinterpret_cast<uint4*>(y + up) + at, make_uint4(x[0], x[1], x[2], x[3]));
-        const int ahead = static_cast<int>(up / kSize);
+        // the word from the boundary at or before the piece's start on
+        const uint32_t off = static_cast<uint32_t>(reinterpret_cast<uintptr_t>(y) & 15);
+        const uint4 left = *reinterpret_cast<const uint4*>(from + at * 16 - 16);
+        uint32_t x[8] = {left.x, left.y, left.z, left.w, word.x, word.y, word.z, word.w};
+        shift_bytes(x, (16 - off) & 15);
+        const int head = static_cast<int>((16 - off) / kSize), tail = static_cast<int>(off / kSize);
+        const uint4 cut = make_uint4(off ? x[0] : word.x, off ? x[1] : word.y, off ? x[2] : word.z,
+                                     off ? x[3] : word.w);
+        if (off == 0 || at > 0 || !starts) __stcs(reinterpret_cast<uint4*>(y - off) + at, cut);
+        if (off && (starts || ends))
 #pragma unroll
-        for (int t = 0; t < kPer; t += kLanes) {
-          const int e = t + at < ahead ? t + at : kN - kPer + t + at;
-          if (t + at < kPer && ahead) reinterpret_cast<E*>(y)[e] = reinterpret_cast<const E*>(from)[e];
-        }
+          for (int t = at; t < kPer; t += kLanes) {
+            if (starts && t < head) reinterpret_cast<E*>(y)[t] = reinterpret_cast<const E*>(from)[t];
+            if (ends && t < tail)
+              reinterpret_cast<E*>(y)[kN - tail + t] = reinterpret_cast<const E*>(from)[kN - tail + t];
+          }
       }
     }
   } else {  // the ends of y, element by element
-    for (int r = 0; r < rows; ++r, y += step, from += kRowsAtOnce * kTurnPitch)
-      for (int e = at; e < cols; e += kLanes)
+    for (int r = 0; r < rows; ++r, y += step, from += kRowsAtOnce * kTurnPitch) {
+      const int tail = kWide || starts ? 0 : static_cast<int>((reinterpret_cast<uintptr_t>(y) & 15) / kSize);
+      for (int e = at - tail; e < cols; e += kLanes)
         reinterpret_cast<E*>(y)[e] = reinterpret_cast<const E*>(from)[e];
+    }
   }
   __syncwarp();
 }
@@ -554,11 +585,16 @@ __global__ void __launch_bounds__(kThreads, 1)
       const uint32_t d = tmem + b * 256 + (static_cast<uint32_t>(quarter * 32) << 16);
       // the accumulators are given back as soon as they are read: the stores
       // run beside the products of the tile after the next
-      float v[S::kGroupCols];
+      float v[S::kGroupCols], before[16];
       if (any) {
         if constexpr (kAInLanes) {
           read_columns<0, 64>(d + from, v);
           read_columns<64, 32>(d + more, v);
+          if (!p.wide) {
+            read_eight<0>(d + (from ? from - 8 : 0), before);
+            read_eight<8>(d + more - 8, before);
+          }
+          columns_read(before);
         } else {
           read_columns<0, S::kGroupCols>(d + from, v);
         }
@@ -575,14 +611,16 @@ __global__ void __launch_bounds__(kThreads, 1)
         auto store = [&](auto type, auto wide) {
           constexpr int kType = decltype(type)::value;
           constexpr bool kWide = decltype(wide)::value;
+          const bool first = half == 0;  // of the tile
           if constexpr (kType == HKV_F32) {
-            turn_and_store<kType, kWide, 0, 32>(room, p, l, c + from, v);
+            turn_and_store<kType, kWide, 0, 32, 0>(room, p, l, c + from, v, before, first, false);
             if (c + from + 32 < p.cols)
-              turn_and_store<kType, kWide, 32, 32>(room, p, l, c + from + 32, v);
+              turn_and_store<kType, kWide, 32, 32, 24>(room, p, l, c + from + 32, v, v, false, false);
           } else {
-            turn_and_store<kType, kWide, 0, 64>(room, p, l, c + from, v);
+            turn_and_store<kType, kWide, 0, 64, 0>(room, p, l, c + from, v, before, first, false);
           }
-          if (c + more < p.cols) turn_and_store<kType, kWide, 64, 32>(room, p, l, c + more, v);
+          if (c + more < p.cols)
+            turn_and_store<kType, kWide, 64, 32, 8>(room, p, l, c + more, v, before, false, !first);
         };
         auto with = [&](auto wide) {
           if (p.type == HKV_F32) store(std::integral_constant<int, HKV_F32>{}, wide);
