@@ -9,6 +9,10 @@
 // partials again in every block (a few hundred floats) instead of in a launch
 // of its own, and takes each run from its end, where the first kernel left
 // off and L2 still holds it.
+//
+// Times (GB300): the norm of 10^8 float32 in 300 tensors 66 us, 6.0 TB/s; 10^9
+// bfloat16 in 400 tensors into float32 1,258 us, 6.4 TB/s of two reads and a
+// write; 10^5 elements in 24 tensors 5.8 us, two launches.
 #include <algorithm>
 #include <cfloat>
 #include <cmath>

@@ -19,6 +19,13 @@
 // in the lanes a warp's lanes are 32 neighbouring columns of one row of y:
 // that is for the few rows of a token or a small batch, which would leave most
 // lanes empty the other way.
+//
+// Bounds and times (GB300): 8192 x 8192 x 8192 into bfloat16 159 us, 6.9
+// PFLOP/s, the tensor pipe active for 78% of the cycles (137 us without the
+// loads, 142 without the products); 4096 x 4096 x 4096 27 us; 2048 x 131072 x
+// 64 97 us, bound by the writes of y; 16 x 8192 x 8192 9.9 us, 3.6 TB/s of
+// codes and scales; one row by 4096 x 4096 4.7 us, a launch and the latencies
+// of one pass.
 #include <cuda.h>
 #include <type_traits>
 
@@ -29,7 +36,7 @@ namespace {
 
 __device__ unsigned long long g_wait_timeouts;
 
-constexpr int kRows = 128;       // rows of B per block
+constexpr int kRows = 128;       // lanes per block
 constexpr int kStepBytes = 128;  // bytes of codes per row and step: 256 columns
 constexpr int kStep = 256;
 constexpr int kStoreWarps = 8;   // two for each quarter of the TMEM lanes
@@ -151,7 +158,7 @@ __host__ __device__ constexpr uint32_t product_desc(int blocks, int cols, int pa
 }
 
 // For a pair, the first block's thread issues these for both blocks: each
-// copies its own scales and multiplies its own rows of B by both halves of A.
+// copies its own scales and multiplies its own lanes by both blocks' columns.
 template <int kBlocks>
 __device__ __forceinline__ void copy_scales(uint32_t tmem, uint32_t from) {
   if constexpr (kBlocks == 2)
@@ -224,6 +231,7 @@ __device__ __forceinline__ void give_tmem(uint32_t tmem) {
   else
     asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, 512;" ::"r"(tmem));
 }
+
 // kN accumulator columns of this warp's TMEM lanes into v from kFrom on, on
 // their way until columns_read().
 template <int kFrom, int kN, int N>
@@ -240,6 +248,7 @@ __device__ __forceinline__ void read_columns(uint32_t tmem, float (&v)[N]) {
         : "r"(tmem + c));
   }
 }
+// Eight of them.
 template <int kFrom, int N>
 __device__ __forceinline__ void read_eight(uint32_t tmem, float (&v)[N]) {
   uint32_t* r = reinterpret_cast<uint32_t*>(v) + kFrom;
@@ -433,7 +442,9 @@ struct Tiles {
   }
 };
 
-// kAInLanes: the rows of A in the lanes, else the rows of B.
+// kAInLanes: the rows of A in the lanes, else the rows of B.  The tile of 192
+// columns leaves room in TMEM for two accumulators and two sets of scales, and
+// in shared memory for six (a pair) or four stages.
 template <int kCols, int kBlocks, bool kAInLanes>
 __global__ void __launch_bounds__(kThreads, 1)
     matmul_kernel(const __grid_constant__ Maps maps, const __grid_constant__ Problem p) {

@@ -11,6 +11,12 @@
 // read, and four threads take the 128 rows of a column (or of two neighbouring
 // 16-bit columns), so that they write 64 neighbouring bytes of codes; both
 // copies come from one read of x.
+//
+// Times (GB300): rows of 1000003 x 128 float32 82 us, 7.1 TB/s, and their
+// values as bfloat16 49 us, 6.6 TB/s; rows of 8192 x 8192 bfloat16 29 us, 5.8
+// TB/s; both copies 47 us, 4.4 TB/s, where the conversions and maxima of two
+// copies take longer than the memory (SM 70% busy).  Rows that start off
+// 16-byte boundaries: 8200 x 4095 bfloat16 33 us, its values 26 us.
 #include <type_traits>
 
 #include "mx.cuh"
