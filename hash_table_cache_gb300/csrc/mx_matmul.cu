@@ -39,8 +39,6 @@ __device__ unsigned long long g_wait_timeouts;
 constexpr int kRows = 128;       // lanes per block
 constexpr int kStepBytes = 128;  // bytes of codes per row and step: 256 columns
 constexpr int kStep = 256;
-constexpr int kStoreWarps = 8;   // two for each quarter of the TMEM lanes
-constexpr int kThreads = 64 + 32 * kStoreWarps;  // warp 0 loads, warp 1 multiplies, the others store
 constexpr int kMaxSplits = 8;
 constexpr unsigned kSmemLimit = 232448 - 1024;  // 227 KB less the alignment of the stages
 
@@ -66,16 +64,16 @@ struct Maps {  // codes and scales of the two matrices
 // A tile of kBlocks * 128 lanes by kCols columns, computed by one block or by
 // the two of a pair.  Either block of a pair holds its own 128 rows of the
 // lanes' matrix, half of the columns' matrix's rows, and the scales of its
-// lanes and of all columns.
-template <int kCols, int kBlocks>
+// lanes and of all columns.  Warp 0 loads, warp 1 multiplies; kGroups groups of
+// four warps, one for each quarter of the lanes, share the columns.
+template <int kCols, int kBlocks, int kGroups>
 struct Shape {
   static constexpr int kScaleRows = kCols > 128 ? 2 : 1;  // groups of 128 rows that the columns span
   static constexpr int kOwnCols = kCols / kBlocks;        // columns' rows that a block loads
   static constexpr int kLaneBytes = kRows * kStepBytes, kColBytes = kOwnCols * kStepBytes;
   static constexpr int kStageBytes = kLaneBytes + kColBytes + 1024 + 1024 * kScaleRows;
-  // columns that one group of four storing warps takes
-  static constexpr int kGroupCols = kCols > 32 ? kCols / 2 : 16;
-  static constexpr int kGroups = kCols / kGroupCols;
+  static constexpr int kGroupCols = kCols / kGroups;
+  static constexpr int kStoreWarps = 4 * kGroups, kThreads = 64 + 32 * kStoreWarps;
   static constexpr int kTurnBytes = kCols == 192 ? kStoreWarps * kTurnWarp : 0;
   static constexpr int kFit = (kSmemLimit - 1024 - kTurnBytes) / kStageBytes;
   static constexpr int kStages = kFit > 10 ? 10 : kFit;
@@ -444,11 +442,11 @@ struct Tiles {
 
 // kAInLanes: the rows of A in the lanes, else the rows of B.  The tile of 192
 // columns leaves room in TMEM for two accumulators and two sets of scales, and
-// in shared memory for six (a pair) or four stages.
-template <int kCols, int kBlocks, bool kAInLanes>
-__global__ void __launch_bounds__(kThreads, 1)
+// in shared memory for six (a pair) or four stages, three with 3 groups.
+template <int kCols, int kBlocks, bool kAInLanes, int kGroups>
+__global__ void __launch_bounds__(Shape<kCols, kBlocks, kGroups>::kThreads, 1)
     matmul_kernel(const __grid_constant__ Maps maps, const __grid_constant__ Problem p) {
-  using S = Shape<kCols, kBlocks>;
+  using S = Shape<kCols, kBlocks, kGroups>;
   extern __shared__ uint8_t raw[];
   uint8_t* smem = raw + (1024 - (smem_u32(raw) & 1023)) % 1024;
   __shared__ uint64_t full[S::kStages], empty[S::kStages], ready[2], drained[2];
@@ -471,7 +469,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
     for (int b = 0; b < 2; ++b) {
       mbar_init(&ready[b], 1);
-      mbar_init(&drained[b], kStoreWarps * kBlocks);
+      mbar_init(&drained[b], S::kStoreWarps * kBlocks);
     }
     fence_proxy_async_smem();
   }
@@ -580,10 +578,11 @@ __global__ void __launch_bounds__(kThreads, 1)
       commit<kBlocks>(&ready[1]);
     }
   } else if (warp >= 2) {
-    const int quarter = warp & 3, half = (warp - 2) >> 2;  // the TMEM lanes this warp can read
+    const int quarter = warp & 3, group = (warp - 2) >> 2;  // the TMEM lanes this warp can read
     // This group's columns of a tile: neighbours, or with A in the lanes 64
-    // (a 128-byte line of a 16-bit y) and 32 more.
-    const int from = kAInLanes ? half * 64 : half * S::kGroupCols, more = 128 + half * 32;
+    // (a 128-byte line of a 16-bit y) and, of two groups, 32 more.
+    constexpr bool kMore = kAInLanes && kGroups == 2;
+    const int from = kAInLanes ? group * 64 : group * S::kGroupCols, more = 128 + group * 32;
     uint8_t* room = smem + S::kTurnAt + (warp - 2) * kTurnWarp;
     uint32_t n_tile = 0;
     for (Tiles u = t; u.left(); u.next(p), ++n_tile) {
@@ -592,7 +591,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
       const uint64_t l = (static_cast<uint64_t>(kAInLanes ? u.row : u.col) * kBlocks + half_of) * kRows + quarter * 32;
       const uint64_t c = static_cast<uint64_t>(kAInLanes ? u.col : u.row) * kCols;
-      const bool any = half < S::kGroups && l < p.lanes && c + from < p.cols;
+      const bool any = l < p.lanes && c + from < p.cols;
       const uint32_t d = tmem + b * 256 + (static_cast<uint32_t>(quarter * 32) << 16);
       // the accumulators are given back as soon as they are read: the stores
       // run beside the products of the tile after the next
@@ -600,10 +599,10 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (any) {
         if constexpr (kAInLanes) {
           read_columns<0, 64>(d + from, v);
-          read_columns<64, 32>(d + more, v);
+          if constexpr (kMore) read_columns<64, 32>(d + more, v);
           if (!p.wide) {
             read_eight<0>(d + (from ? from - 8 : 0), before);
-            read_eight<8>(d + more - 8, before);
+            if constexpr (kMore) read_eight<8>(d + more - 8, before);
           }
           columns_read(before);
         } else {
@@ -622,16 +621,17 @@ __global__ void __launch_bounds__(kThreads, 1)
         auto store = [&](auto type, auto wide) {
           constexpr int kType = decltype(type)::value;
           constexpr bool kWide = decltype(wide)::value;
-          const bool first = half == 0;  // of the tile
+          const bool first = group == 0, ends = !kMore && group == kGroups - 1;  // of the tile
           if constexpr (kType == HKV_F32) {
             turn_and_store<kType, kWide, 0, 32, 0>(room, p, l, c + from, v, before, first, false);
             if (c + from + 32 < p.cols)
-              turn_and_store<kType, kWide, 32, 32, 24>(room, p, l, c + from + 32, v, v, false, false);
+              turn_and_store<kType, kWide, 32, 32, 24>(room, p, l, c + from + 32, v, v, false, ends);
           } else {
-            turn_and_store<kType, kWide, 0, 64, 0>(room, p, l, c + from, v, before, first, false);
+            turn_and_store<kType, kWide, 0, 64, 0>(room, p, l, c + from, v, before, first, ends);
           }
-          if (c + more < p.cols)
-            turn_and_store<kType, kWide, 64, 32, 8>(room, p, l, c + more, v, before, false, !first);
+          if constexpr (kMore)
+            if (c + more < p.cols)
+              turn_and_store<kType, kWide, 64, 32, 8>(room, p, l, c + more, v, before, false, !first);
         };
         auto with = [&](auto wide) {
           if (p.type == HKV_F32) store(std::integral_constant<int, HKV_F32>{}, wide);
@@ -659,7 +659,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       const uint64_t c0 = static_cast<uint64_t>(t.row) * kCols;
       const int cols = p.cols - c0 < kCols ? static_cast<int>(p.cols - c0) : kCols;
 #pragma unroll 2
-      for (int c = part + splits * (warp - 2); c < cols; c += kStoreWarps * splits) {
+      for (int c = part + splits * (warp - 2); c < cols; c += S::kStoreWarps * splits) {
         const uint32_t at = smem_u32(smem) + (c * kRows + lane * 4) * 4;
         float4 v[kMaxSplits];
 #pragma unroll
@@ -735,9 +735,9 @@ bool make_maps(CUtensorMap* codes_map, CUtensorMap* scales_map, const Operand& o
            CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-template <int kCols, int kBlocks, bool kAInLanes>
+template <int kCols, int kBlocks, bool kAInLanes, int kGroups = (kCols > 16 ? 2 : 1)>
 cudaError_t run(Problem p, const Operand& a, const Operand& b, int splits, cudaStream_t st) {
-  using S = Shape<kCols, kBlocks>;
+  using S = Shape<kCols, kBlocks, kGroups>;
   const Operand &lanes = kAInLanes ? a : b, &cols = kAInLanes ? b : a;
   p.lanes = lanes.rows;
   p.cols = cols.rows;
@@ -752,14 +752,14 @@ cudaError_t run(Problem p, const Operand& a, const Operand& b, int splits, cudaS
   if (!make_maps(&maps.lanes, &maps.lanes_scales, lanes, p.k, kRows, 1) ||
       !make_maps(&maps.cols, &maps.cols_scales, cols, p.k, S::kOwnCols, S::kScaleRows))
     return cudaErrorUnknown;
-  auto* kernel = matmul_kernel<kCols, kBlocks, kAInLanes>;
+  auto* kernel = matmul_kernel<kCols, kBlocks, kAInLanes, kGroups>;
   cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, S::kSmem);
   if (e != cudaSuccess) return e;
   const uint32_t cluster = splits * kBlocks;
   const uint64_t room = sm_count() / kBlocks;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(static_cast<unsigned>((splits > 1 || tiles < room ? tiles : room) * cluster));
-  cfg.blockDim = dim3(kThreads);
+  cfg.blockDim = dim3(S::kThreads);
   cfg.dynamicSmemBytes = S::kSmem;
   cfg.stream = st;
   cudaLaunchAttribute attr[2];
@@ -795,7 +795,10 @@ cudaError_t matmul(Problem p, const Operand& a, const Operand& b, cudaStream_t s
   // pair: k 512 52 and 75 us, 1024 72 and 86, 1280 85 and 91, 2048 119 and 101.
   // Where pairs leave SMs without a tile, single blocks have twice as many.
   const bool pair = steps > 5 && (m + 191) / 192 * ((n + 255) / 256) * 2 > sms;
-  return pair ? run<192, 2, true>(p, a, b, 1, st) : run<192, 1, true>(p, a, b, 1, st);
+  if (pair) return run<192, 2, true>(p, a, b, 1, st);
+  // Short k is bound by the stores: twelve warps for them, at the price of a
+  // stage (8192 x 16384: k 512 49 and 52 us, 768 66 and 60).
+  return steps <= 2 ? run<192, 1, true, 3>(p, a, b, 1, st) : run<192, 1, true>(p, a, b, 1, st);
 }
 
 }  // namespace
