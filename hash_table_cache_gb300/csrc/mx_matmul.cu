@@ -796,9 +796,11 @@ cudaError_t matmul(Problem p, const Operand& a, const Operand& b, cudaStream_t s
   // Where pairs leave SMs without a tile, single blocks have twice as many.
   const bool pair = steps > 5 && (m + 191) / 192 * ((n + 255) / 256) * 2 > sms;
   if (pair) return run<192, 2, true>(p, a, b, 1, st);
-  // Short k is bound by the stores: twelve warps for them, at the price of a
-  // stage (8192 x 16384: k 512 49 and 52 us, 768 66 and 60).
-  return steps <= 2 ? run<192, 1, true, 3>(p, a, b, 1, st) : run<192, 1, true>(p, a, b, 1, st);
+  // Short k is bound by the stores, the more so where rows of y have to be cut:
+  // twelve warps for them, at the price of a stage (8192 x 16384: k 512 49 and
+  // 52 us, 768 66 and 60; 8192 x 16383: k 1024 92 and 103, 1280 106 and 107).
+  return steps <= (p.wide ? 2 : 5) ? run<192, 1, true, 3>(p, a, b, 1, st)
+                                   : run<192, 1, true>(p, a, b, 1, st);
 }
 
 }  // namespace

@@ -170,7 +170,10 @@ __global__ void __launch_bounds__(kThreads, sizeof(T) == 2 ? 5 : 4)
   }
 }
 
-template <class T>
+// kShifted: y's rows start anywhere.  A thread then takes, instead of its eight
+// columns, the eight that lie between boundaries in y, `tail` of them before
+// its own: the codes are shifted, not the values.
+template <class T, bool kShifted>
 __global__ void __launch_bounds__(kThreads)
     dequantize_kernel(uint64_t rows, uint64_t cols, const uint8_t* __restrict__ codes,
                       const uint8_t* __restrict__ scales, T* y, uint64_t stride, int move) {
@@ -180,33 +183,71 @@ __global__ void __launch_bounds__(kThreads)
   const int tx = threadIdx.x & 15, ty = threadIdx.x >> 4;
   const uint64_t tiles = groups * ((rows + 127) / 128);
   for (uint64_t t = blockIdx.x; t < tiles; t += gridDim.x) {
-    const uint64_t c = t % groups * kTile + tx * 8, row0 = t / groups * kTile;
-    const int hi = limit(cols, c);
-    uint32_t code[8];
-    uint4 scale[2];
+    const uint64_t tile_c = t % groups, c = tile_c * kTile + tx * 8, row0 = t / groups * kTile;
+    const bool own = c < cols, left = kShifted && c > 0 && c - 8 < cols;
+    if (!own && !left) continue;
+    uint32_t code[8], code_left[8];
+    uint4 scale[2], scale_left[2];
 #pragma unroll
     for (int h = 0; h < 2; ++h) {
-      scale[h] = ld_nc_v4(scales + t * 512 + (ty + 16 * h) * 16);
+      const uint64_t at = t * 512 + (ty + 16 * h) * 16;
+      scale[h] = scale_left[h] = ld_nc_v4(scales + at);
+      if (kShifted && tx == 0 && left) scale_left[h] = ld_nc_v4(scales + at - 512);
 #pragma unroll
       for (int q = 0; q < 4; ++q) {
         const uint64_t row = row0 + ty + 16 * h + 32 * q;
-        code[4 * h + q] = row < rows && hi > 0 ? __ldg(reinterpret_cast<const uint32_t*>(
-                                           codes + row * blocks * 16 + c / 2))
-                                     : 0;
+        const uint32_t* word = reinterpret_cast<const uint32_t*>(codes + row * blocks * 16 + c / 2);
+        code[4 * h + q] = own && row < rows ? __ldg(word) : 0;
+        code_left[4 * h + q] = left && row < rows ? __ldg(word - 1) : 0;
       }
     }
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
       const uint64_t row = row0 + ty + 16 * (i >> 2) + 32 * (i & 3);
+      if (row >= rows) continue;
+      T* out = y + row * stride + c;
       const uint32_t four = reinterpret_cast<const uint32_t*>(&scale[i >> 2])[i & 3];
       const float s = mx_scale_value(four >> (8 * (tx >> 2)) & 255);
       float v[8];
-      mx_values8(code[i], v);
-#pragma unroll
-      for (int k = 0; k < 8; ++k) v[k] *= s;
       Eight<T> e;
-      e.from(v);
-      e.store(y + row * stride + c, row < rows ? hi : 0, move, tx);
+      if constexpr (!kShifted) {
+        mx_values8(code[i], v);
+#pragma unroll
+        for (int k = 0; k < 8; ++k) v[k] *= s;
+        e.from(v);
+        if (c + 8 <= cols) {
+          e.store_aligned(out, move);
+        } else {
+#pragma unroll
+          for (int k = 0; k < 8; ++k)
+            if (c + k < cols) out[k] = from_f32<T>(v[k]);
+        }
+      } else {
+        const int tail = static_cast<int>((reinterpret_cast<uintptr_t>(out) & 15) / sizeof(T));
+        const uint32_t four_left = reinterpret_cast<const uint32_t*>(&scale_left[i >> 2])[i & 3];
+        const float s_left = mx_scale_value(four_left >> (8 * ((tx + 15 & 15) >> 2)) & 255);
+        mx_values8(__funnelshift_l(code_left[i], code[i], 4 * tail), v);
+#pragma unroll
+        for (int k = 0; k < 8; ++k) v[k] *= k < tail ? s_left : s;
+        e.from(v);
+        out -= tail;
+        // the columns of out[0 .. 7] that lie in the row
+        const int lo = c ? 0 : tail, hi = limit(cols, c) + tail;
+        if (lo == 0 && hi >= 8) {
+          e.store_aligned(out, kHalves);
+        } else {
+#pragma unroll
+          for (int k = 0; k < 8; ++k)
+            if (k >= lo && k < hi) out[k] = from_f32<T>(v[k]);
+        }
+        // a row that ends with this tile has no thread for what is left of it
+        if (tx == 15 && tile_c == groups - 1 && tail && own) {
+          mx_values8(code[i], v);
+#pragma unroll
+          for (int k = 1; k < 8; ++k)
+            if (k >= 8 - tail && c + k < cols) out[tail + k] = from_f32<T>(v[k] * s);
+        }
+      }
     }
   }
 }
@@ -274,9 +315,10 @@ hkv_status hkv_mx_dequantize(uint64_t rows, uint64_t cols, const uint8_t* codes,
   cudaStream_t st = static_cast<cudaStream_t>(stream);
   return op_status(with_type(y_type, [&](auto* t) {
     using T = std::remove_pointer_t<decltype(t)>;
-    return launch_chained(dequantize_kernel<T>, tile_grid(rows, cols), kThreads, 0, st, rows, cols,
-                          codes, scales, static_cast<T*>(y), y_stride,
-                          widest<T>(y, y_stride * sizeof(T)));
+    const int move = widest<T>(y, y_stride * sizeof(T));
+    return launch_chained(move == kShifted ? dequantize_kernel<T, true> : dequantize_kernel<T, false>,
+                          tile_grid(rows, cols), kThreads, 0, st, rows, cols, codes, scales,
+                          static_cast<T*>(y), y_stride, move);
   }));
 }
 

@@ -73,8 +73,7 @@ __device__ __forceinline__ void shift_bytes(uint32_t (&x)[N], uint32_t bytes) {
 
 // Eight neighbouring elements of a row as they lie in memory.  `lo` and `hi`
 // bound the row: elements lo .. hi - 1 from the thread's first one belong to
-// it (hi may be above 8, or not above 0); the others read as zeros and are not
-// written.  Sixteen neighbouring threads, a half-warp, `at` of it, hold 128
+// it (hi may be above 8, or not above 0); the others read as zeros.  Sixteen neighbouring threads, a half-warp, `at` of it, hold 128
 // neighbouring elements; all threads of a warp take part.  `move` is the same
 // for all rows.
 template <class T>
@@ -161,42 +160,6 @@ struct Eight {
     for (int i = 0; i < kVecs; ++i) w[i] = v[i];
   }
 
-  __device__ __forceinline__ void store(T* p, int hi, int move, int at) const {
-    constexpr int kPer = 16 / sizeof(T);
-    const T* e = reinterpret_cast<const T*>(w);
-    if (move != kShifted) {
-      if (hi >= 8) store_aligned(p, move);
-      else
-#pragma unroll
-        for (int i = 0; i < 8; ++i)
-          if (i < hi) p[i] = e[i];
-      return;
-    }
-    // The pieces from the boundary above p on; the last one ends with the next
-    // thread's first elements, and that thread leaves those out.
-    const uint32_t up = (16 - (reinterpret_cast<uintptr_t>(p) & 15)) & 15;
-    const int ahead = static_cast<int>(up / sizeof(T));
-    uint32_t x[4 * kVecs + 4];
-    uint4* v = reinterpret_cast<uint4*>(x);
-#pragma unroll
-    for (int i = 0; i < kVecs; ++i) v[i] = w[i];
-#pragma unroll
-    for (int i = 0; i < 4; ++i) x[4 * kVecs + i] = __shfl_down_sync(0xFFFFFFFFu, x[i], 1, 16);
-    shift_bytes(x, up);
-    const bool head = at == 0 || hi < ahead;
-    bool whole[kVecs];
-#pragma unroll
-    for (int i = 0; i < kVecs; ++i) {
-      whole[i] = hi >= ahead + (i + 1) * kPer && (i + 1 < kVecs || at < 15 || ahead == 0);
-      if (whole[i]) st_stream_v4(p + ahead + i * kPer, v[i]);
-    }
-    if ((head && ahead) || !whole[0] || !whole[kVecs - 1])
-#pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        const bool alone = i < ahead ? head : !whole[kVecs > 1 && i - ahead >= kPer ? kVecs - 1 : 0];
-        if (alone && i < hi) p[i] = e[i];
-      }
-  }
   __device__ __forceinline__ void to(float (&v)[8]) const {
     const T* e = reinterpret_cast<const T*>(w);
 #pragma unroll
