@@ -15,7 +15,7 @@
 // With A in the lanes that is a piece of a row of y, and a warp turns its 32
 // pieces around in shared memory so that a store covers whole 128-byte lines
 // (a thread storing its own piece, a 32-byte sector of 32 rows at once,
-// reached 4.4 TB/s of y where this reaches 5.6: 2048 x 131072 x 64).  With B
+// reached 4.4 TB/s of y where this reaches 5.7: 2048 x 131072 x 64).  With B
 // in the lanes a warp's lanes are 32 neighbouring columns of one row of y:
 // that is for the few rows of a token or a small batch, which would leave most
 // lanes empty the other way.
@@ -23,7 +23,7 @@
 // Bounds and times (GB300): 8192 x 8192 x 8192 into bfloat16 159 us, 6.9
 // PFLOP/s, the tensor pipe active for 78% of the cycles (137 us without the
 // loads, 142 without the products); 4096 x 4096 x 4096 27 us; 2048 x 131072 x
-// 64 97 us, bound by the writes of y; 16 x 8192 x 8192 9.9 us, 3.6 TB/s of
+// 64 95 us, bound by the writes of y; 16 x 8192 x 8192 9.9 us, 3.6 TB/s of
 // codes and scales; one row by 4096 x 4096 4.7 us, a launch and the latencies
 // of one pass.
 #include <cuda.h>
