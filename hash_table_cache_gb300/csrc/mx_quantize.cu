@@ -12,10 +12,10 @@
 // 16-bit columns), so that they write 64 neighbouring bytes of codes; both
 // copies come from one read of x.
 //
-// Times (GB300): rows of 1000003 x 128 float32 82 us, 7.1 TB/s, and their
-// values as bfloat16 49 us, 6.6 TB/s; rows of 8192 x 8192 bfloat16 29 us, 5.8
-// TB/s; both copies 47 us, 4.4 TB/s, where the conversions and maxima of two
-// copies take longer than the memory (SM 70% busy).  Rows that start off
+// Times (GB300): rows of 1000003 x 128 float32 81 us, 7.2 TB/s, and their
+// values as bfloat16 49 us, 6.6 TB/s; rows of 8192 x 8192 bfloat16 26 us, 6.5
+// TB/s; both copies 42 us, 4.9 TB/s, where the conversions and maxima of two
+// copies take longer than the memory.  Rows that start off
 // 16-byte boundaries: 8200 x 4095 bfloat16 33 us, its values 23 us.
 #include <type_traits>
 
@@ -34,14 +34,20 @@ __device__ __forceinline__ int limit(uint64_t cols, uint64_t c) {
   return static_cast<int>(min(max(d, static_cast<int64_t>(-32)), static_cast<int64_t>(32)));
 }
 
-// Running maxima of magnitudes, compared as integers (which puts NaNs above
-// infinity).  A word holds one float32 or two 16-bit elements, whose maxima
-// are kept apart until the end: one instruction for two elements.
+// Running maxima of magnitudes.  A word holds one float32 (compared as an
+// integer, which puts NaNs above infinity) or two 16-bit elements, whose maxima
+// are kept apart until the end: one instruction for two elements.  A NaN stays.
 template <class T>
 __device__ __forceinline__ uint32_t most(uint32_t m, uint32_t word) {
-  if constexpr (sizeof(T) == 4) return max(m, word & 0x7FFFFFFFu);
-  return __vmaxu2(m, word & 0x7FFF7FFFu);
+  if constexpr (sizeof(T) == 4) {
+    return max(m, word & 0x7FFFFFFFu);
+  } else {
+    using T2 = std::conditional_t<std::is_same_v<T, __nv_bfloat16>, __nv_bfloat162, __half2>;
+    const T2 r = __hmax2_nan(*reinterpret_cast<const T2*>(&m), __habs2(*reinterpret_cast<const T2*>(&word)));
+    return *reinterpret_cast<const uint32_t*>(&r);
+  }
 }
+// Of two of them.
 template <class T>
 __device__ __forceinline__ uint32_t most_of(uint32_t m, uint32_t other) {
   if constexpr (sizeof(T) == 4) return max(m, other);
@@ -57,18 +63,17 @@ __device__ __forceinline__ uint32_t magnitude(uint32_t m, int k) {
   return __float_as_uint(__half2float(__ushort_as_half(static_cast<unsigned short>(h))));
 }
 
-__device__ __forceinline__ uint32_t encode8(const float (&v)[8], uint32_t byte) {
-  if (byte == 255) return 0;
-  const float inv = mx_inverse(byte);
+__device__ __forceinline__ uint32_t encode8(const float (&v)[8], uint32_t byte, float inverse) {
   float u[8];
 #pragma unroll
-  for (int i = 0; i < 8; ++i) u[i] = v[i] * inv;
-  return mx_codes8(u);
+  for (int i = 0; i < 8; ++i) u[i] = v[i] * inverse;
+  const uint32_t code = mx_codes8(u);
+  return byte == 255 ? 0 : code;
 }
 
 // While one block waits for its tile another encodes: five per SM for 16-bit
-// elements (rows of 8200 x 4095: 33 us, with four 39), four for float32
-// (both copies of 8192 x 8192: 65 us, with five 71).
+// elements (rows of 8200 x 4095: 33 us, with four 38), four for float32
+// (both copies of 8192 x 8192: 62 us, with five 71).
 template <class T, bool kRowCopy, bool kColCopy>
 __global__ void __launch_bounds__(kThreads, sizeof(T) == 2 ? 5 : 4)
     quantize_kernel(uint64_t rows, uint64_t cols, const T* __restrict__ x, uint64_t stride,
@@ -85,16 +90,25 @@ __global__ void __launch_bounds__(kThreads, sizeof(T) == 2 ? 5 : 4)
   const int tx = threadIdx.x & 15, ty = threadIdx.x >> 4;
   for (uint64_t t = blockIdx.x; t < groups * groups_t; t += gridDim.x) {
     const uint64_t tile_c = t % groups, tile_r = t / groups;
-    const uint64_t c = tile_c * kTile + tx * 8;
+    const uint64_t c = tile_c * kTile + tx * 8, row0 = tile_r * kTile;
     const int lo = tile_c ? -16 : -8 * tx, hi = limit(cols, c);
+    const int rows_here = rows - row0 < kTile ? static_cast<int>(rows - row0) : kTile;
+    const bool inside = move != kShifted && hi >= 8 && rows_here == kTile;
+    const T* in = x + (row0 + ty) * stride + c;
+    uint8_t* out = codes + (row0 + ty) * blocks * 16 + c / 2;
 #pragma unroll
-    for (int h = 0; h < 2; ++h) {
+    for (int h = 0; h < 2; ++h, in += 16 * stride, out += 256 * blocks) {
       const int r = ty + 16 * h;
       Eight<T> e[4];
+      if (inside) {
 #pragma unroll
-      for (int q = 0; q < 4; ++q) {
-        const uint64_t row = tile_r * kTile + r + 32 * q;
-        e[q].load(x + row * stride + c, row < rows ? lo : 0, row < rows ? hi : 0, move, tx);
+        for (int q = 0; q < 4; ++q) e[q].load_aligned(in + q * (32 * stride), move);
+      } else {
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {
+          const bool row = r + 32 * q < rows_here;
+          e[q].load(in + q * (32 * stride), row ? lo : 0, row ? hi : 0, move, tx);
+        }
       }
       if (kColCopy) {
 #pragma unroll
@@ -106,7 +120,8 @@ __global__ void __launch_bounds__(kThreads, sizeof(T) == 2 ? 5 : 4)
         }
       }
       if (kRowCopy) {
-        uint32_t packed[4];
+        // this block's scale bytes of the four rows, one byte each
+        uint32_t four = 0;
 #pragma unroll
         for (int q = 0; q < 4; ++q) {
           const uint32_t* words = reinterpret_cast<const uint32_t*>(e[q].w);
@@ -118,18 +133,22 @@ __global__ void __launch_bounds__(kThreads, sizeof(T) == 2 ? 5 : 4)
           const uint32_t byte = mx_scale_byte(max(magnitude<T>(m, 0), magnitude<T>(m, 1)));
           float v[8];
           e[q].to(v);
-          const uint32_t code = encode8(v, byte);
-          const uint64_t row = tile_r * kTile + r + 32 * q;
-          if (row < rows && (c >> 5) < blocks)
-            *reinterpret_cast<uint32_t*>(codes + row * blocks * 16 + c / 2) = code;
-          uint32_t word = byte << (8 * (tx >> 2));
-          word |= __shfl_xor_sync(0xFFFFFFFFu, word, 4);
-          word |= __shfl_xor_sync(0xFFFFFFFFu, word, 8);
-          packed[q] = word;
+          const uint32_t code = encode8(v, byte, mx_inverse(byte));
+          if (inside || (r + 32 * q < rows_here && (c >> 5) < blocks))
+            *reinterpret_cast<uint32_t*>(out + q * (512 * blocks)) = code;
+          four |= byte << (8 * q);
         }
-        if (tx == 0)
+        // four blocks' bytes of a row are neighbours in the group
+        const uint32_t b1 = __shfl_down_sync(0xFFFFFFFFu, four, 4);
+        const uint32_t b2 = __shfl_down_sync(0xFFFFFFFFu, four, 8);
+        const uint32_t b3 = __shfl_down_sync(0xFFFFFFFFu, four, 12);
+        if (tx == 0) {
+          const uint32_t a01 = __byte_perm(four, b1, 0x5140), a23 = __byte_perm(b2, b3, 0x5140);
+          const uint32_t c01 = __byte_perm(four, b1, 0x7362), c23 = __byte_perm(b2, b3, 0x7362);
           *reinterpret_cast<uint4*>(scales + t * 512 + r * 16) =
-              make_uint4(packed[0], packed[1], packed[2], packed[3]);
+              make_uint4(__byte_perm(a01, a23, 0x5410), __byte_perm(a01, a23, 0x7632),
+                         __byte_perm(c01, c23, 0x5410), __byte_perm(c01, c23, 0x7632));
+        }
       }
     }
     if (kColCopy) {
@@ -146,18 +165,19 @@ __global__ void __launch_bounds__(kThreads, sizeof(T) == 2 ? 5 : 4)
 #pragma unroll
         for (int k = 0; k < kPer; ++k) {
           const uint32_t byte = mx_scale_byte(magnitude<T>(m, k));
+          const float inverse = mx_inverse(byte);
           uint32_t code[4];
 #pragma unroll
           for (int g = 0; g < 4; ++g) {
             float v[8];
 #pragma unroll
             for (int i = 0; i < 8; ++i) v[i] = to_f32(reinterpret_cast<const T*>(&word[8 * g + i])[k]);
-            code[g] = encode8(v, byte);
+            code[g] = encode8(v, byte, inverse);
           }
-          const uint4 out = make_uint4(code[0], code[1], code[2], code[3]);
+          const uint4 all = make_uint4(code[0], code[1], code[2], code[3]);
           const uint64_t col = tile_c * kTile + w * kPer + k, block = tile_r * 4 + q;
           if (col < cols && block < blocks_t)
-            *reinterpret_cast<uint4*>(codes_t + (col * blocks_t + block) * 16) = out;
+            *reinterpret_cast<uint4*>(codes_t + (col * blocks_t + block) * 16) = all;
           uint32_t packed = byte << (8 * q);
           packed |= __shfl_xor_sync(0xFFFFFFFFu, packed, 1);
           packed |= __shfl_xor_sync(0xFFFFFFFFu, packed, 2);
