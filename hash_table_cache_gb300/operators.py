@@ -63,14 +63,14 @@ def _same(t, device, what):
 
 
 def _cuda(t, what):
-    device = t.device
-    if device.type != "cuda":
+    if not t.is_cuda:
         raise ValueError(f"{what}: a CUDA tensor")
-    return device
+    return t.device
 
 
-# the handle of a device's current stream, without a Stream object (2 us less
-# per call) where torch offers it
+# the current device and the handle of its current stream, without a Stream
+# object (2 us less per call) where torch offers it
+_device_now = getattr(torch._C, "_cuda_getDevice", None) or torch.cuda.current_device
 _current = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
     lambda index: torch.cuda.current_stream(index).cuda_stream)
 
@@ -78,8 +78,10 @@ _current = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
 def _call(device, stream, f, *args):
     """f(stream handle, *args) with the device current and the caching allocator
     on the stream."""
-    if stream is None and torch.cuda.current_device() == device.index:
-        return f(_current(device.index), *args)
+    if stream is None:
+        index = device.index
+        if _device_now() == index:
+            return f(_current(index), *args)
     with torch.cuda.device(device):
         if stream is None:
             return f(_current(device.index), *args)
@@ -97,6 +99,11 @@ def _ok(status, what):
 def _mx_bytes(rows, cols):
     """Bytes of the codes and of the scales of a 4-bit matrix."""
     return rows * -(-cols // 32) * 16, -(-rows // 128) * -(-cols // 128) * 512
+
+
+def _mx_room(rows, cols):
+    """Bytes of both, the codes in whole groups of 512."""
+    return (-(-rows * -(-cols // 32) // 32) + -(-rows // 128) * -(-cols // 128)) * 512
 
 
 class MXMatrix:
@@ -122,8 +129,7 @@ class MXMatrix:
         """A matrix inside a buffer of bytes, `offset` bytes in; also the offset
         after it."""
         m = cls.__new__(cls)
-        codes, scales = _mx_bytes(rows, cols)
-        codes = -(-codes // 512) * 512
+        codes = -(-rows * -(-cols // 32) // 32) * 512  # in whole groups
         at = base.data_ptr() + offset
         m.rows, m.cols, m.device = rows, cols, base.device
         m._codes = m._scales = None
@@ -185,26 +191,25 @@ def mx_quantize(x, along="rows", stream=None):
 def _quantize(s, x, along):
     kind = _type(x, "x")
     rows, cols, stride = _matrix(x, "x")
-    q = qt = None
-    at = at_t = (None, None)
-    if along == "both":
-        sizes = _mx_bytes(rows, cols), _mx_bytes(cols, rows)
-        room = [-(-c // 512) * 512 + e for c, e in sizes]
-        base = torch.empty(room[0] + room[1], dtype=torch.uint8, device=x.device)
-        q, qt = MXMatrix._inside(base, 0, rows, cols), MXMatrix._inside(base, room[0], cols, rows)
-        at, at_t = q._at, qt._at
+    device = x.device
+    if along == "rows":
+        q = MXMatrix._inside(torch.empty(_mx_room(rows, cols), dtype=torch.uint8, device=device), 0,
+                             rows, cols)
+        codes, scales = q._at
+        codes_t = scales_t = None
+    elif along == "columns":
+        q = MXMatrix._inside(torch.empty(_mx_room(cols, rows), dtype=torch.uint8, device=device), 0,
+                             cols, rows)
+        codes = scales = None
+        codes_t, scales_t = q._at
     else:
-        shape = (rows, cols) if along == "rows" else (cols, rows)
-        codes, scales = _mx_bytes(*shape)
-        base = torch.empty(-(-codes // 512) * 512 + scales, dtype=torch.uint8, device=x.device)
-        q = MXMatrix._inside(base, 0, *shape)
-        if along == "rows":
-            at = q._at
-        else:
-            at_t = q._at
-    _ok(_abi.load().hkv_mx_quantize(rows, cols, x.data_ptr(), kind, stride, at[0], at[1], at_t[0],
-                                    at_t[1], s), "hkv_mx_quantize")
-    return (q, qt) if along == "both" else q
+        room = _mx_room(rows, cols)
+        base = torch.empty(room + _mx_room(cols, rows), dtype=torch.uint8, device=device)
+        q = (MXMatrix._inside(base, 0, rows, cols), MXMatrix._inside(base, room, cols, rows))
+        (codes, scales), (codes_t, scales_t) = q[0]._at, q[1]._at
+    _ok(_abi.load().hkv_mx_quantize(rows, cols, x.data_ptr(), kind, stride, codes, scales, codes_t,
+                                    scales_t, s), "hkv_mx_quantize")
+    return q
 
 
 def mx_matmul(a, b, dtype=torch.bfloat16, out=None, stream=None):
@@ -343,8 +348,8 @@ def clip_grad_norm(grads, max_norm, outs="in place", stream=None):
 
 def _fields(tensors, what, device):
     """Addresses of dense tensors of one device, their types (one number where
-    they share it), and whether all of them are contiguous.  One C call per tensor and field: hundreds of tensors
-    are common here."""
+    they share it), and whether all of them are contiguous.  One C call per
+    tensor and field: hundreds of tensors are common here."""
     of = torch.Tensor
     if set(map(of.get_device, tensors)) != {device.index}:
         raise ValueError(f"{what}: tensors of {device}")
