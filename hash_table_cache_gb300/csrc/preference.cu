@@ -11,7 +11,7 @@
 //
 // Times (GB300): 8192 x 131072 bfloat16, a quarter of the tokens hidden,
 // forward 252 us (6.4 TB/s of what is read), backward 540 us (6.9 TB/s); 4096
-// x 32768 forward 42 us (4.8 TB/s: 8 blocks per SM take 3072 rows in two and a
+// x 32768 forward 42 us (4.8 TB/s: 8 blocks per SM take the rows in two and a
 // half rounds, and the exponentials alone would take 20 us), backward 70 us;
 // 32768 x 2000 27 and 37 us; 96 x 1000 float32 5.0 and 2.7 us.
 #include <cfloat>
