@@ -37,6 +37,12 @@ constexpr float kExpMean = 2.2e-8f;
 // log2 e in two floats: one alone is off by 1e-8 of it, which leans one way in
 // every exponential
 constexpr float kLog2e = 1.44269504f, kLog2eRest = 1.92596299e-8f;
+// Below this maximum exp(x - max) may be taken as 2^(x log2 e - c) 2^(c - max
+// log2 e), c the rounded max log2 e: the second exponent is half a unit of c, at
+// most 0.09 here.  It grows with the maximum (a mask such as -1e10 where a
+// thread has met nothing else), past 127 from 2e9 on, where one factor would be
+// infinite and the other 0.
+constexpr float kFactored = 1048576.f;
 
 __device__ __forceinline__ float exp2_approx(float x) {
   float y;
@@ -167,7 +173,7 @@ __device__ __forceinline__ Running row_pass(const T* x, uint64_t n, int lane) {
       else c[u].fill_lowest();
     }
     const float base = r.raise(largest(c));
-    if (fabsf(base) < 1e37f) {
+    if (fabsf(base) < kFactored) {
       // exp(x - base) as 2^(x log2 e - base log2 e), by two multiply-adds.  The
       // same rounded base log2 e is in every term; what it is off by is taken
       // out of their sum.
@@ -186,7 +192,7 @@ __device__ __forceinline__ Running row_pass(const T* x, uint64_t n, int lane) {
         }
       const float2 t = parts(add_both(sum[0], sum[1]));
       r.s = fmaf(t.x + t.y, exp2_approx(-off), r.s);
-    } else {  // a product with log2 e might overflow
+    } else {
       float part = 0.f;
 #pragma unroll
       for (int u = 0; u < kUnroll; ++u)
