@@ -29,20 +29,19 @@ constexpr int kPairThreads = 256;
 constexpr int kMaxParts = 8;  // blocks of a cluster that share a row
 // 16-byte loads in flight per thread where kLanes threads share a row
 __host__ __device__ constexpr int unroll(int lanes) { return lanes == 32 ? 8 : 4; }
-// ex2.approx returns a little less than 2^x on average.  On the logarithm of a
-// row's sum that came to 1e-8 to 3.3e-8 (rows of 1000 to 131072 logits of
-// three types): nothing beside the rounding of one token, but a sequence adds
-// its tokens up.
-constexpr float kExpMean = 2.2e-8f;
 // log2 e in two floats: one alone is off by 1e-8 of it, which leans one way in
 // every exponential
 constexpr float kLog2e = 1.44269504f, kLog2eRest = 1.92596299e-8f;
-// Below this maximum exp(x - max) may be taken as 2^(x log2 e - c) 2^(c - max
-// log2 e), c the rounded max log2 e: the second exponent is half a unit of c, at
-// most 0.09 here.  It grows with the maximum (a mask such as -1e10 where a
-// thread has met nothing else), past 127 from 2e9 on, where one factor would be
-// infinite and the other 0.
-constexpr float kFactored = 1048576.f;
+// Below this maximum exp(x - max) is taken as 2^(x log2 e - c) 2^(c - max log2
+// e), c the rounded max log2 e: the second exponent is half a unit of c, at most
+// 0.0013 here, and its power three terms of a series (left out: 1.2e-10).  It
+// grows with the maximum (a mask such as -1e10 where a thread has met nothing
+// else), past 127 from 2e9 on, where one factor would be infinite and the other 0.
+constexpr float kFactored = 16384.f;
+// 2^-x for |x| below 0.0013
+__device__ __forceinline__ float exp2_of_minus(float x) {
+  return fmaf(x * x, 0.240226507f, fmaf(-x, 0.693147181f, 1.f));
+}
 
 __device__ __forceinline__ float exp2_approx(float x) {
   float y;
@@ -149,7 +148,7 @@ struct Running {
     const float a = static_cast<float>(e) * 0.693145751953125f;
     const float hi = m + a, back = hi - m;
     const float lo = (m - (hi - back)) + (a - back) +
-                     (logf(f) + (static_cast<float>(e) * 1.42860682e-6f + kExpMean));
+                     (logf(f) + static_cast<float>(e) * 1.42860682e-6f);
     const float l = hi + lo;
     rest = lo - (l - hi);
     return l;
@@ -191,7 +190,7 @@ __device__ __forceinline__ Running row_pass(const T* x, uint64_t n, int lane) {
           sum[i / 2 & 1] = add_both(sum[i / 2 & 1], both(exp2_approx(a.x), exp2_approx(a.y)));
         }
       const float2 t = parts(add_both(sum[0], sum[1]));
-      r.s = fmaf(t.x + t.y, exp2_approx(-off), r.s);
+      r.s = fmaf(t.x + t.y, exp2_of_minus(off), r.s);
     } else {
       float part = 0.f;
 #pragma unroll
