@@ -412,8 +412,11 @@ hkv_status hkv_preference_loss(uint64_t pairs, uint64_t rows, uint64_t vocab, co
  * (dlosses NULL: ones), in the logits' type:
  *   dlogits[t][v] = g (1[v = labels[t]] - exp(logits[t][v] - lse[t])),
  *   g = dlosses[row_pair[t]] * row_grad[t]
- * and zeros for a token that is not counted or lies in no sequence.  dlogits
- * may be the logits' own buffer with the same stride. */
+ * and zeros for a token that is not counted or lies in no sequence.  Where
+ * lse[t] is too large for one float to give the exponent (1024 or more in
+ * magnitude: a row whose mask leaves nothing), the row's softmax is taken from
+ * its maximum.  dlogits may be the logits' own buffer with the same stride, and
+ * must not overlap them otherwise. */
 hkv_status hkv_preference_loss_backward(uint64_t pairs, uint64_t rows, uint64_t vocab,
                                         const void* logits, int type, uint64_t stride,
                                         const int64_t* labels, const float* lse,

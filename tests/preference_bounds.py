@@ -31,8 +31,9 @@ def tokens(x, label):
     at = torch.arange(x.shape[0], device=x.device)
     lp = (x[at, label] - top[:, 0]) - spread
     e = 2.0 ** -20 + (chain(x.shape[1], kind) + 64) * U + 3 * U * (p * near.abs()).sum(1) + 4 * U * spread
-    # the gradient's exponents come from the log-sum-exp in one float
+    # the gradient's exponents come from the log-sum-exp in one float, or where
+    # that would be above 1024 from the row's maximum
     lse = top[:, 0] + spread
-    e_soft = e + lse.abs() * U
+    e_soft = e + torch.where(lse.abs() < 1025, lse.abs(), spread) * U
     e_soft = p * (e_soft[:, None] + 2.0 ** -20 + 4 * U * (x - lse[:, None]).nan_to_num(0, 0, 0).abs().clamp_max(200))
     return lp, e + 2 * U * lp.abs(), p, e_soft

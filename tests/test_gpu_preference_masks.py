@@ -98,3 +98,32 @@ def test_gradient_beside_finite_masks(hkv, dtype):
     bound = g.abs() * (e + (hot - p).abs() * 2.0 ** -20 + 2.0 ** -23 * hot) * (1 + u) + want.abs() * u + 2.0 ** -132
     over = (d - want).abs() - bound
     assert float(over.max()) <= 0, f"row {int(over.amax(1).argmax())}: {float(over.max()):.3g} over its bound"
+
+
+@pytest.mark.parametrize("dtype", [F32, BF16, F16])
+@pytest.mark.parametrize("vocab", [1, 7, 64, 1001, 40000])
+@pytest.mark.parametrize("in_place", [False, True])
+def test_gradient_of_rows_that_are_all_mask(hkv, dtype, vocab, in_place):
+    """A counted row whose mask leaves nothing, or whose logits are all large,
+    has a softmax that adds up to 1; rows beside it stay as they are."""
+    low = [v for v in MASKS if dtype != F16 or v > -65504] + [torch.finfo(dtype).min, 3e4]
+    rows = 2 * len(low)
+    x, labels = _logits(rows, vocab, dtype, vocab)
+    for i, v in enumerate(low):
+        x[2 * i] = v
+        x[2 * i, vocab // 2:] += torch.tensor(0.75, device=DEV).to(dtype)
+    pairs = rows // 2
+    f = hkv.preference_loss(x, labels, torch.arange(rows + 1, device=DEV))
+    lp, _, p, e = bounds.tokens(x, labels)
+    h = 0.1 * (f.ratios[:pairs] - f.ratios[pairs:]).double()
+    slope = -0.1 * torch.sigmoid(-h)
+    g = torch.cat((slope, -slope))[:, None]
+    hot = torch.zeros_like(p)
+    hot[torch.arange(rows, device=DEV), labels] = 1
+    want = g * (hot - p)
+    u = {F32: 2.0 ** -24, BF16: 2.0 ** -8, F16: 2.0 ** -11}[dtype]
+    tiny = 2.0 ** -24 if dtype == F16 else 2.0 ** -132
+    bound = g.abs() * (e + (hot - p).abs() * 2.0 ** -20 + 2.0 ** -23 * hot) * (1 + u) + want.abs() * u + tiny
+    d = hkv.preference_loss_backward(f, out=x if in_place else None).double()
+    over = (d - want).abs() - bound
+    assert float(over.max()) <= 0, f"row {int(over.amax(1).argmax())}: {float(over.max()):.3g} over its bound"
