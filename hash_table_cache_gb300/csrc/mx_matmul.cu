@@ -105,6 +105,12 @@ __device__ __noinline__ bool slow_wait(uint64_t* bar, uint32_t parity) {
 __device__ __forceinline__ bool wait(uint64_t* bar, uint32_t parity) {
   return mbar_try_wait(bar, parity) || slow_wait(bar, parity);
 }
+// The same by a whole warp, with one answer for all of its lanes: each lane has a
+// limit of its own, and a warp that parted at it must not run instructions that
+// its lanes have to run together.
+__device__ __forceinline__ bool wait_warp(uint64_t* bar, uint32_t parity) {
+  return __all_sync(0xFFFFFFFFu, wait(bar, parity));
+}
 __device__ __forceinline__ void mbar_arrive(uint64_t* bar) {
   asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(smem_u32(bar)) : "memory");
 }
@@ -587,7 +593,7 @@ __global__ void __launch_bounds__(Shape<kCols, kBlocks, kGroups>::kThreads, 1)
     uint32_t n_tile = 0;
     for (Tiles u = t; u.left(); u.next(p), ++n_tile) {
       const uint32_t b = n_tile & 1;
-      if (!wait(&ready[b], (n_tile / 2) & 1)) break;
+      if (!wait_warp(&ready[b], (n_tile / 2) & 1)) break;
       asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
       const uint64_t l = (static_cast<uint64_t>(kAInLanes ? u.row : u.col) * kBlocks + half_of) * kRows + quarter * 32;
       const uint64_t c = static_cast<uint64_t>(kAInLanes ? u.col : u.row) * kCols;
