@@ -542,7 +542,10 @@ __global__ void __launch_bounds__(Shape<kCols, kBlocks, kGroups>::kThreads, 1)
       // the scales of a tile that starts in the middle of a group of 128 rows
       // (192 columns: at 0 or 64, so that the shift is even, as it has to be)
       const uint32_t shift = kCols > 128 ? (kAInLanes ? t.col : t.row) % 2 * 2 : 0;
-      if (n_tile >= 2 && !wait(&drained[b], (n_tile / 2 + 1) & 1)) break;
+      if (n_tile >= 2 && !wait(&drained[b], (n_tile / 2 + 1) & 1)) {
+        ok = false;
+        break;
+      }
       asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
       for (uint32_t k = k0; k < k1; ++k) {
         if (!wait(&full[s], parity)) {
@@ -582,6 +585,13 @@ __global__ void __launch_bounds__(Shape<kCols, kBlocks, kGroups>::kThreads, 1)
     if (!ok) {  // products in flight end before TMEM is given back
       commit<kBlocks>(&ready[0]);
       commit<kBlocks>(&ready[1]);
+      // and loads before the block ends: the loading thread may have issued its
+      // last one and be gone (stages without a load run out once more)
+      for (int i = 0; i < S::kStages && wait(&full[s], parity); ++i)
+        if (++s == S::kStages) {
+          s = 0;
+          parity ^= 1;
+        }
     }
   } else if (warp >= 2) {
     const int quarter = warp & 3, group = (warp - 2) >> 2;  // the TMEM lanes this warp can read

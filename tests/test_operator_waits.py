@@ -31,3 +31,15 @@ def test_a_warp_wait_is_a_vote():
     text = open(os.path.join(ROOT, "hash_table_cache_gb300", "csrc", "mx_matmul.cu")).read()
     body = re.search(r"bool wait_warp\(uint64_t\* bar, uint32_t parity\) \{(.*?)\}", text, re.S).group(1)
     assert "__all_sync(0xFFFFFFFFu, wait(bar, parity))" in body
+
+
+def test_a_block_ends_after_its_loads(kernel):
+    """Where the issuing thread gives up, on either of its waits, it waits for the
+    loads that follow in the order of the stages before it ends: the loading
+    thread may have issued its last load and be gone."""
+    issuing = kernel.split("warp == 1 && half_of == 0 && elect()")[1].split("else if (warp >= 2)")[0]
+    for name in ("drained[b]", "full[s]"):
+        assert re.search(r"if \([^;{]*!wait\(&" + re.escape(name) + r"[^{;]*\{\s*ok = false;\s*break;", issuing), name
+    given_up = issuing[issuing.rindex("if (!ok) {"):]
+    assert re.search(r"for \(int i = 0; i < S::kStages && wait\(&full\[s\], parity\); \+\+i\)\s*"
+                     r"if \(\+\+s == S::kStages\) \{\s*s = 0;\s*parity \^= 1;", given_up)
