@@ -468,5 +468,20 @@ class HashTable:
         _check(hkv_set_epoch(self.handle, epoch), "hkv_set_epoch")
 
 
-from .operators import (MXMatrix, PreferenceLoss, clip_grad_norm, mx_matmul,  # noqa: E402
-                        mx_quantize, preference_loss, preference_loss_backward)
+# The operators work on torch tensors, and this module is of use without torch
+# (and is imported in 10 ms, not in seconds): they are imported when first named.
+_OPERATORS = ("MXMatrix", "PreferenceLoss", "clip_grad_norm", "mx_matmul", "mx_quantize",
+              "preference_loss", "preference_loss_backward")
+
+
+def __getattr__(name):
+    if name not in _OPERATORS and name != "operators":
+        raise AttributeError(f"module {__name__!r} has no attribute {name!r}")
+    import importlib
+    module = importlib.import_module(".operators", __name__)
+    globals().update({k: getattr(module, k) for k in _OPERATORS})
+    return module if name == "operators" else globals()[name]
+
+
+def __dir__():
+    return sorted({*globals(), *_OPERATORS, "operators"})
