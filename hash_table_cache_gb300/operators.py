@@ -12,6 +12,10 @@ caller's back) and ``HKVError`` for a status of the library.  ``stream``
 kernels run on and the one that results are allocated on; tensors made on
 another stream are the caller's to order, as with any CUDA call.
 
+The operators are outside autograd: a result carries no gradient function,
+also where an input requires a gradient (the backward passes are calls of
+their own).  A tensor that a call writes counts as modified in place.
+
 The smallest calls take a few microseconds on the GPU, so the host's share is
 kept small: one allocation per result, and no context is entered unless the
 stream or the device has to change.
@@ -91,6 +95,11 @@ def _call(device, stream, f, *args):
             return f(stream.cuda_stream, *args)
 
 
+# For tensors of the caller's that a kernel has written: autograd counts what it
+# sees written, and would otherwise use one that it had saved as if unchanged.
+_written = torch.autograd.graph.increment_version
+
+
 def _ok(status, what):
     if status:
         raise _abi.HKVError(status, what)
@@ -166,6 +175,7 @@ class MXMatrix:
 
 
 def _dequantize(s, q, dtype, out):
+    given = out
     if out is None:
         out = torch.empty((q.rows, q.cols), dtype=dtype, device=q.device)
     kind = _type(out, "out")
@@ -176,6 +186,8 @@ def _dequantize(s, q, dtype, out):
     codes, scales = q._at
     _ok(_abi.load().hkv_mx_dequantize(rows, cols, codes, scales, out.data_ptr(), kind, stride, s),
         "hkv_mx_dequantize")
+    if given is not None:
+        _written(given)
     return out
 
 
@@ -224,6 +236,7 @@ def mx_matmul(a, b, dtype=torch.bfloat16, out=None, stream=None):
 
 def _matmul(s, a, b, dtype, out):
     m, n = a.rows, b.rows
+    given = out
     if out is None:
         out = torch.empty((m, n), dtype=dtype, device=a.device)
         kind, stride = _type(out, "out"), n
@@ -236,6 +249,8 @@ def _matmul(s, a, b, dtype, out):
     at, bt = a._at, b._at
     _ok(_abi.load().hkv_mx_matmul(m, n, a.cols, at[0], at[1], bt[0], bt[1], out.data_ptr(), kind,
                                   stride, s), "hkv_mx_matmul")
+    if given is not None:
+        _written(given)
     return out
 
 
@@ -297,6 +312,7 @@ def _loss_backward(s, loss, dlosses, out):
     device = logits.device
     rows, vocab, stride = _matrix(logits, "logits")
     pairs = loss.losses.numel()
+    given = out
     if dlosses is not None:
         _vector(dlosses, pairs, torch.float32, "dlosses", device)
     if out is None:
@@ -312,6 +328,8 @@ def _loss_backward(s, loss, dlosses, out):
         pairs, rows, vocab, logits.data_ptr(), _TYPES[logits.dtype], stride, loss.labels.data_ptr(),
         saved, saved + 4 * rows, saved + 8 * rows, None if dlosses is None else dlosses.data_ptr(),
         out.data_ptr(), dstride, s), "hkv_preference_loss_backward")
+    if given is not None:
+        _written(given)
     return out
 
 
@@ -332,7 +350,8 @@ def clip_grad_norm(grads, max_norm, outs="in place", stream=None):
     (``outs=()``: the norm alone).  Tensors have to be dense; an out tensor has
     as many elements as its gradient, and lies in memory in the same order
     (both contiguous, or the same shape and strides)."""
-    grads = [grads] if isinstance(grads, torch.Tensor) else list(grads)
+    if type(grads) is not list:
+        grads = [grads] if isinstance(grads, torch.Tensor) else list(grads)
     if not grads:
         raise ValueError("grads: at least one tensor")
     if isinstance(outs, str) and outs != "in place":
@@ -351,7 +370,7 @@ def _fields(tensors, what, device):
     they share it), and whether all of them are contiguous.  One C call per
     tensor and field: hundreds of tensors are common here."""
     of = torch.Tensor
-    if set(map(of.get_device, tensors)) != {device.index}:
+    if list(map(of.get_device, tensors)).count(device.index) != len(tensors):
         raise ValueError(f"{what}: tensors of {device}")
     plain = all(map(of.is_contiguous, tensors))
     if not plain and not all(map(_dense, tensors)):
@@ -364,7 +383,7 @@ def _fields(tensors, what, device):
             types = list(map(_TYPES.__getitem__, kinds))
     except KeyError as e:
         raise ValueError(f"{what}: float32, bfloat16 or float16, not {e.args[0]}") from None
-    return array("Q", map(of.data_ptr, tensors)), types, plain
+    return array("Q", list(map(of.data_ptr, tensors))), types, plain
 
 
 def _both_types(types, out_types, n):
@@ -381,7 +400,7 @@ def _clip(s, grads, outs, max_norm):
     data, types, plain = _fields(grads, "grads", device)
     table = array("Q", bytes(32 * n))  # hkv_grad: data, out, n, type | out_type << 32
     table[0::4] = data
-    sizes = array("Q", map(torch.Tensor.numel, grads))
+    sizes = array("Q", list(map(torch.Tensor.numel, grads)))
     table[2::4] = sizes
     if outs is grads:
         table[1::4] = data
@@ -401,4 +420,6 @@ def _clip(s, grads, outs, max_norm):
     work = torch.empty(_abi.CLIP_WORK_BYTES, dtype=torch.uint8, device=device)
     _ok(_abi.load().hkv_clip_grad_norm(n, table.buffer_info()[0], max_norm, norm.data_ptr(),
                                        work.data_ptr(), s), "hkv_clip_grad_norm")
+    if outs:
+        _written(outs)
     return norm
