@@ -9,8 +9,9 @@ Every function takes tensors of one CUDA device and raises ``ValueError`` for
 a tensor it cannot take as it is (nothing is copied or cast behind the
 caller's back) and ``HKVError`` for a status of the library.  ``stream``
 (default: the current stream of the tensors' device) is the stream the
-kernels run on and the one that results are allocated on; tensors made on
-another stream are the caller's to order, as with any CUDA call.
+kernels run on and the one that results are allocated on.  Work on other
+streams that the call depends on is the caller's to order, as with any CUDA
+call; tensors passed with a ``stream`` may be dropped right after the call.
 
 The operators are outside autograd: a result carries no gradient function,
 also where an input requires a gradient (the backward passes are calls of
@@ -92,7 +93,23 @@ def _call(device, stream, f, *args):
         if not hasattr(stream, "cuda_stream"):
             stream = torch.cuda.ExternalStream(int(stream), device=device)
         with torch.cuda.stream(stream):
-            return f(stream.cuda_stream, *args)
+            result = f(stream.cuda_stream, *args)
+        # their memory is not used again before the stream is done with it
+        for t in _tensors(args):
+            t.record_stream(stream)
+        return result
+
+
+def _tensors(args):
+    for a in args:
+        if isinstance(a, torch.Tensor):
+            yield a
+        elif isinstance(a, (list, tuple)):
+            yield from _tensors(a)
+        elif isinstance(a, MXMatrix):
+            yield from (a._codes, a._scales) if a._base is None else a._base[:1]
+        elif isinstance(a, PreferenceLoss):
+            yield from (a.logits, a.labels, a._saved)
 
 
 # For tensors of the caller's that a kernel has written: autograd counts what it
@@ -130,7 +147,7 @@ class MXMatrix:
             if t.dtype != torch.uint8 or not t.is_contiguous() or t.numel() != n:
                 raise ValueError(f"{what}: {n} contiguous bytes for {rows} x {cols}")
         self.rows, self.cols = rows, cols
-        self._codes, self._scales = codes, scales
+        self._codes, self._scales, self._base = codes, scales, None
         self._at = codes.data_ptr(), scales.data_ptr()
 
     @classmethod
