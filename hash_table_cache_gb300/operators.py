@@ -92,6 +92,8 @@ def _call(device, stream, f, *args):
             return f(_current(device.index), *args)
         if not hasattr(stream, "cuda_stream"):
             stream = torch.cuda.ExternalStream(int(stream), device=device)
+        elif stream.device != device:
+            raise ValueError(f"stream: of {stream.device}, not {device}")
         with torch.cuda.stream(stream):
             result = f(stream.cuda_stream, *args)
         # their memory is not used again before the stream is done with it

@@ -1,5 +1,5 @@
 """Calls on a stream of the caller's choosing: memory of tensors that are
-dropped after the call."""
+dropped after the call, and streams of another device."""
 import pytest
 import torch
 
@@ -91,3 +91,12 @@ def test_dropped_tensors_are_not_used_again_too_early(hkv, call, handle):
     assert not side.query(), "the stream was done too early to show anything"
     side.synchronize()
     del keep, result
+
+
+def test_a_stream_of_another_device_is_refused(hkv):
+    class Elsewhere:
+        cuda_stream = 0
+        device = torch.device("cuda", 1)
+
+    with pytest.raises(ValueError):
+        hkv.mx_quantize(torch.zeros((4, 64), device=DEV), stream=Elsewhere())
