@@ -306,16 +306,19 @@ def _loss(s, logits, labels, offsets, ref_logps, beta, label_smoothing, average)
         _vector(ref_logps, rows, torch.float32, "ref_logps", device)
     f = PreferenceLoss()
     f.logits, f.labels = logits, labels
-    # losses, ratios, logps, then lse, row_grad and row_pair of 4 bytes each
-    base = torch.empty(3 * pairs + 4 * rows, dtype=torch.float32, device=device)
-    f.losses, f.ratios, f.logps, f._saved = base.split_with_sizes((pairs, 2 * pairs, rows, 3 * rows))
-    at = base.data_ptr()
-    logps = at + 12 * pairs
+    # what a caller may keep longer than the rest (the losses of every step, a
+    # reference's logps) has memory of its own
+    base = torch.empty(3 * pairs, dtype=torch.float32, device=device)
+    f.losses, f.ratios = base.split_with_sizes((pairs, 2 * pairs))
+    f.logps = torch.empty(rows, dtype=torch.float32, device=device)
+    # lse, row_grad and row_pair of 4 bytes each
+    f._saved = torch.empty(3 * rows, dtype=torch.float32, device=device)
+    at, saved = base.data_ptr(), f._saved.data_ptr()
     _ok(_abi.load().hkv_preference_loss(
         pairs, rows, vocab, logits.data_ptr(), kind, stride, labels.data_ptr(), offsets.data_ptr(),
         None if ref_logps is None else ref_logps.data_ptr(), beta, label_smoothing,
-        1 if average else 0, at, at + 4 * pairs, logps, logps + 4 * rows, logps + 8 * rows,
-        logps + 12 * rows, s), "hkv_preference_loss")
+        1 if average else 0, at, at + 4 * pairs, f.logps.data_ptr(), saved, saved + 4 * rows,
+        saved + 8 * rows, s), "hkv_preference_loss")
     return f
 
 
