@@ -129,11 +129,6 @@ def _mx_bytes(rows, cols):
     return rows * -(-cols // 32) * 16, -(-rows // 128) * -(-cols // 128) * 512
 
 
-def _mx_room(rows, cols):
-    """Bytes of both, the codes in whole groups of 512."""
-    return (-(-rows * -(-cols // 32) // 32) + -(-rows // 128) * -(-cols // 128)) * 512
-
-
 class MXMatrix:
     """A 4-bit microscaled matrix (MXFP4) of ``rows`` x ``cols``: ``codes`` and
     ``scales`` are uint8 tensors in the layout of ``include/hkv.h``."""
@@ -153,21 +148,23 @@ class MXMatrix:
         self._at = codes.data_ptr(), scales.data_ptr()
 
     @classmethod
-    def _inside(cls, base, offset, rows, cols):
-        """A matrix inside a buffer of bytes, `offset` bytes in; also the offset
-        after it."""
+    def _empty(cls, rows, cols, device):
+        """A matrix to be written, codes and scales in one allocation of its own:
+        of two copies from one call either may be kept without the other."""
         m = cls.__new__(cls)
         codes = -(-rows * -(-cols // 32) // 32) * 512  # in whole groups
-        at = base.data_ptr() + offset
-        m.rows, m.cols, m.device = rows, cols, base.device
+        room = codes + -(-rows // 128) * -(-cols // 128) * 512
+        base = torch.empty(room, dtype=torch.uint8, device=device)
+        at = base.data_ptr()
+        m.rows, m.cols, m.device = rows, cols, device
         m._codes = m._scales = None
-        m._base = base, offset, codes
+        m._base = base, codes
         m._at = at, at + codes
         return m
 
     def _piece(self, skip, size, shape):
-        base, offset, codes = self._base
-        start = offset + (codes if skip else 0)
+        base, codes = self._base
+        start = codes if skip else 0
         return base[start:start + size].view(shape)
 
     @property
@@ -223,24 +220,16 @@ def _quantize(s, x, along):
     kind = _type(x, "x")
     rows, cols, stride = _matrix(x, "x")
     device = x.device
-    if along == "rows":
-        q = MXMatrix._inside(torch.empty(_mx_room(rows, cols), dtype=torch.uint8, device=device), 0,
-                             rows, cols)
+    codes = scales = codes_t = scales_t = None
+    if along != "columns":
+        q = MXMatrix._empty(rows, cols, device)
         codes, scales = q._at
-        codes_t = scales_t = None
-    elif along == "columns":
-        q = MXMatrix._inside(torch.empty(_mx_room(cols, rows), dtype=torch.uint8, device=device), 0,
-                             cols, rows)
-        codes = scales = None
-        codes_t, scales_t = q._at
-    else:
-        room = _mx_room(rows, cols)
-        base = torch.empty(room + _mx_room(cols, rows), dtype=torch.uint8, device=device)
-        q = (MXMatrix._inside(base, 0, rows, cols), MXMatrix._inside(base, room, cols, rows))
-        (codes, scales), (codes_t, scales_t) = q[0]._at, q[1]._at
+    if along != "rows":
+        q_t = MXMatrix._empty(cols, rows, device)
+        codes_t, scales_t = q_t._at
     _ok(_abi.load().hkv_mx_quantize(rows, cols, x.data_ptr(), kind, stride, codes, scales, codes_t,
                                     scales_t, s), "hkv_mx_quantize")
-    return q
+    return (q, q_t) if along == "both" else q if along == "rows" else q_t
 
 
 def mx_matmul(a, b, dtype=torch.bfloat16, out=None, stream=None):

@@ -24,3 +24,15 @@ def test_losses_and_logps_keep_no_more_than_themselves(hkv):
     assert f.losses.untyped_storage().nbytes() <= 3 * pairs * 4
     assert f.ratios.untyped_storage().nbytes() <= 3 * pairs * 4
     assert f.logps.untyped_storage().nbytes() == 4 * rows
+
+
+@pytest.mark.parametrize("along", ["rows", "columns", "both"])
+def test_each_copy_has_memory_of_its_own(hkv, along):
+    rows, cols = 700, 4100
+    got = hkv.mx_quantize(torch.randn((rows, cols), device=DEV), along)
+    copies = got if along == "both" else (got,)
+    for q in copies:
+        own = q.rows * -(-q.cols // 32) * 16 + -(-q.rows // 128) * -(-q.cols // 128) * 512
+        assert q.codes.untyped_storage().nbytes() < own + 512
+        assert q.scales.untyped_storage().data_ptr() == q.codes.untyped_storage().data_ptr()
+    assert along != "both" or copies[0].codes.untyped_storage().data_ptr() != copies[1].codes.untyped_storage().data_ptr()
