@@ -16,6 +16,7 @@
 #include <algorithm>
 #include <cfloat>
 #include <cmath>
+#include <new>
 
 #include "operators.cuh"
 
@@ -262,6 +263,60 @@ cudaError_t clip(uint64_t count, const hkv_grad* g, uint64_t total, bool writes,
   });
 }
 
+// Whether memory that the call writes is written once and read by nothing else:
+// blocks take the gradients in no fixed order, so one that is listed twice, or
+// lies in another's out, would be scaled once or twice by chance.  Outs that
+// follow one another in memory, away from the gradients, are seen in one pass;
+// others are sorted.
+hkv_status written_once(uint64_t count, const hkv_grad* g) {
+  struct Range {
+    uintptr_t begin, end;
+    bool out;
+  };
+  auto of = [](const void* p, uint64_t n, int type, bool out) {
+    const uintptr_t begin = reinterpret_cast<uintptr_t>(p);
+    return Range{begin, begin + n * type_size(type), out};
+  };
+  auto join = [](Range& all, const Range& r) {
+    all.begin = std::min(all.begin, r.begin);
+    all.end = std::max(all.end, r.end);
+  };
+  Range outs{UINTPTR_MAX, 0, true}, data{UINTPTR_MAX, 0, false};
+  uint64_t ranges = 0;
+  bool ascending = true;
+  for (uint64_t i = 0; i < count; ++i) {
+    if (!g[i].data || g[i].n == 0) continue;
+    if (g[i].out != g[i].data) {
+      join(data, of(g[i].data, g[i].n, g[i].type, false));
+      ++ranges;
+    }
+    if (!g[i].out) continue;
+    const Range out = of(g[i].out, g[i].n, g[i].out_type, true);
+    ascending &= out.begin >= outs.end;
+    join(outs, out);
+    ++ranges;
+  }
+  if (ascending && (data.begin >= outs.end || outs.begin >= data.end)) return HKV_OK;
+  Range* all = new (std::nothrow) Range[ranges];
+  if (!all) return HKV_ERR_OOM;
+  uint64_t k = 0;
+  for (uint64_t i = 0; i < count; ++i) {
+    if (!g[i].data || g[i].n == 0) continue;
+    if (g[i].out != g[i].data) all[k++] = of(g[i].data, g[i].n, g[i].type, false);
+    if (g[i].out) all[k++] = of(g[i].out, g[i].n, g[i].out_type, true);
+  }
+  std::sort(all, all + ranges, [](const Range& a, const Range& b) { return a.begin < b.begin; });
+  uintptr_t any_end = 0, out_end = 0;
+  bool once = true;
+  for (k = 0; k < ranges; ++k) {
+    once &= all[k].begin >= (all[k].out ? any_end : out_end);
+    any_end = std::max(any_end, all[k].end);
+    if (all[k].out) out_end = std::max(out_end, all[k].end);
+  }
+  delete[] all;
+  return once ? HKV_OK : HKV_ERR_INVALID;
+}
+
 }  // namespace
 }  // namespace hkv
 
@@ -283,6 +338,10 @@ extern "C" hkv_status hkv_clip_grad_norm(uint64_t count, const hkv_grad* grads, 
     if (g.out == g.data && g.out_type != g.type) return HKV_ERR_INVALID;
     total += g.n;
     writes |= g.out != nullptr;
+  }
+  if (writes) {
+    const hkv_status apart = written_once(count, grads);
+    if (apart != HKV_OK) return apart;
   }
   cudaStream_t st = static_cast<cudaStream_t>(stream);
   float* w = static_cast<float*>(work);

@@ -360,7 +360,9 @@ def clip_grad_norm(grads, max_norm, outs="in place", stream=None):
     the tensors ``outs`` (of any of the three types), or not at all
     (``outs=()``: the norm alone).  Tensors have to be dense; an out tensor has
     as many elements as its gradient, and lies in memory in the same order
-    (both contiguous, or the same shape and strides)."""
+    (both contiguous, or the same shape and strides).  What is written must not
+    overlap another tensor of the call: the gradient of a parameter that is
+    used twice is listed once."""
     if type(grads) is not list:
         grads = [grads] if isinstance(grads, torch.Tensor) else list(grads)
     if not grads:

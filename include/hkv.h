@@ -426,7 +426,8 @@ hkv_status hkv_preference_loss_backward(uint64_t pairs, uint64_t rows, uint64_t 
 
 /* One gradient: n elements of `type` at `data`.  Where `out` is not NULL the
  * clipped gradient is written there as `out_type`; it may be `data` itself
- * with the same type, and must not overlap it otherwise. */
+ * with the same type, and must not overlap it otherwise, nor another gradient
+ * of the call or its out (HKV_ERR_INVALID; a gradient is listed once). */
 typedef struct hkv_grad {
   const void* data;
   void* out;

@@ -36,3 +36,27 @@ def test_each_copy_has_memory_of_its_own(hkv, along):
         assert q.codes.untyped_storage().nbytes() < own + 512
         assert q.scales.untyped_storage().data_ptr() == q.codes.untyped_storage().data_ptr()
     assert along != "both" or copies[0].codes.untyped_storage().data_ptr() != copies[1].codes.untyped_storage().data_ptr()
+
+
+def test_clipping_takes_any_order_without_overlaps(hkv):
+    """Outs and gradients side by side in one buffer, in every order; gradients
+    that are only read may be listed twice."""
+    for seed in range(4):
+        g = torch.Generator(device=DEV).manual_seed(seed)
+        part = torch.randn(24 * 1000, generator=g, device=DEV).split(1000)
+        order = torch.randperm(24, generator=torch.Generator().manual_seed(seed)).tolist()
+        grads, outs = [part[i] for i in order[:12]], [part[i] for i in order[12:]]
+        want = torch.cat(grads).double()
+        norm = hkv.clip_grad_norm(grads, 1.0, outs=outs)
+        assert abs(float(norm) - float(want.norm())) <= 1e-5 * float(want.norm())
+        assert float((torch.cat(outs).double() - want / want.norm()).abs().max()) < 1e-6
+        hkv.clip_grad_norm(grads[::-1], 1.0)
+        assert float((torch.cat(grads).double() - want / want.norm()).abs().max()) < 1e-6
+    x = torch.ones(50, device=DEV)
+    assert abs(float(hkv.clip_grad_norm([x, x], 1.0, outs=())) - 10.0) < 1e-5
+    with pytest.raises(hkv.HKVError):
+        hkv.clip_grad_norm([x, x], 1.0)
+    with pytest.raises(hkv.HKVError):
+        hkv.clip_grad_norm([x, x.view(5, 10)], 1.0, outs=[torch.zeros_like(x), x])
+    assert (x == 1).all()
+    hkv.clip_grad_norm([x, x], 100.0, outs=[torch.zeros_like(x), torch.zeros_like(x)])
