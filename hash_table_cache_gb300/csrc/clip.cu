@@ -5,14 +5,19 @@
 // and written, where they are clipped.  They are cut into chunks of one size
 // that a fixed number of thread blocks share evenly, each a run of
 // neighbouring chunks, and every block leaves one partial sum of squares: the
-// order of the sum depends on the sizes alone.  The second kernel adds the
+// order of the sum depends on the sizes, on where the tensors start within 32
+// bytes, and on the number of SMs, and not on the order in which blocks run.  The
+// second kernel adds the
 // partials again in every block (a few hundred floats) instead of in a launch
 // of its own, and takes each run from its end, where the first kernel left
 // off and L2 still holds it.
 //
 // Times (GB300): the norm of 10^8 float32 in 300 tensors 66 us, 6.0 TB/s; 10^9
 // bfloat16 in 400 tensors into float32 1,258 us, 6.4 TB/s of two reads and a
-// write; 10^5 elements in 24 tensors 5.8 us, two launches.
+// write, and clipped in place 913 us, 6.6 TB/s; 10^8 float32 in place 185 us; 10^5
+// elements in 24 tensors 5.9 us, two launches.  Outs that do not lie as their
+// gradients do within 8 elements go one element at a time: the 10^9 into a
+// float32 buffer without padding take 3,600 us.
 #include <algorithm>
 #include <cfloat>
 #include <cmath>
@@ -237,7 +242,9 @@ template <int N>
 cudaError_t clip(uint64_t count, const hkv_grad* g, uint64_t total, bool writes, float max_norm,
                  float* norm_out, float* work, cudaStream_t st) {
   // every block resident, so that none starts when others end; small totals
-  // are cut finer, so that every SM has some
+  // are cut finer, so that every SM has some.  Chunks of 1024, 4096, 16384 and
+  // 65536: 10^5 elements 6.2, 6.1, 6.5 and 7.0 us, 3 * 10^6 13.1, 10.5, 9.9 and 14.0
+  // (9.4 by this rule), 10^9 2919, 1412, 1237 and 1232.
   const int grid = std::min(kMaxPartials, sm_count() * kPerSm);
   uint32_t chunk = 4096;
   while (chunk < 16384 && total / chunk > static_cast<uint64_t>(grid)) chunk *= 2;

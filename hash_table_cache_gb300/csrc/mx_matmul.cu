@@ -7,9 +7,9 @@
 // 256 columns: 128 bytes of codes per row, brought by TMA in the 128-byte
 // swizzle the tensor core reads, and two 512-byte groups of scales per 128
 // rows, which the format stores as they are copied to TMEM.  One warp loads,
-// one issues the copies of scales and the products, eight read the
-// accumulators out; accumulators and scales are held twice, so a tile's
-// output leaves while the next one is computed.
+// one issues the copies of scales and the products, and 4 (16 columns), 8, or 12
+// (192 columns and short k) read the accumulators out; accumulators and scales
+// are held twice, so a tile's output leaves while the next one is computed.
 //
 // TMEM hands a thread one lane: neighbouring columns of one row of the tile.
 // With A in the lanes that is a piece of a row of y, and a warp turns its 32
@@ -21,11 +21,11 @@
 // lanes empty the other way.
 //
 // Bounds and times (GB300): 8192 x 8192 x 8192 into bfloat16 159 us, 6.9
-// PFLOP/s, the tensor pipe active for 78% of the cycles (137 us without the
-// loads, 142 without the products); 4096 x 4096 x 4096 27 us; 2048 x 131072 x
-// 64 95 us, bound by the writes of y; 16 x 8192 x 8192 9.9 us, 3.6 TB/s of
-// codes and scales; one row by 4096 x 4096 4.7 us, a launch and the latencies
-// of one pass.
+// PFLOP/s, the tensor pipe active for 74% of the cycles (137 us without the
+// loads, 142 without the products), into float32 178 us; 4096 x 4096 x 4096 27
+// and 34 us; 2048 x 131072 x 64 95 and 173 us, bound by the writes of y; 16 x
+// 8192 x 8192 9.9 us, 3.6 TB/s of codes and scales; one row by 4096 x 4096 4.5
+// us, a launch and the latencies of one pass.
 #include <cuda.h>
 #include <type_traits>
 
@@ -424,7 +424,9 @@ __device__ __forceinline__ bool elect() {
 // The tiles of a block: every `step`-th from `first`, in an order that goes down
 // kDown tiles of y before it goes along its rows: the blocks that run side by
 // side then share their lanes' matrix with few and their columns' with few,
-// and no line of L2 is asked for by all of them at once.
+// and no line of L2 is asked for by all of them at once.  Bands of 1, 4, 8, 16 and
+// 64: 2048 x 131072 x 64 115, 101, 93, 93, 93 us; 8192 x 16384 x 1024 73, 71, 72,
+// 74, 78; 8192^3 155 to 158 with all.
 constexpr uint32_t kDown = 8;
 struct Tiles {
   uint32_t row, col, at, step, all;
@@ -529,8 +531,8 @@ __global__ void __launch_bounds__(Shape<kCols, kBlocks, kGroups>::kThreads, 1)
         if (uses && !wait(ok ? &empty[i] : &full[i], (uses + 1) & 1)) break;
       }
   } else if (warp == 1 && half_of == 0 && elect()) {
-    // This thread sets the pace: a step is 4 products of 70 to 80 cycles each,
-    // so everything that does not change from step to step is outside.
+    // This thread sets the pace: a step is 4 products of 92 cycles each (192
+    // columns), so everything that does not change from step to step is outside.
     uint32_t s = 0, parity = 0, set = 0, n_tile = 0;
     bool ok = true;
     const uint32_t units = desc_units(smem_u32(smem));
@@ -797,7 +799,11 @@ cudaError_t matmul(Problem p, const Operand& a, const Operand& b, cudaStream_t s
   const int cols = m <= 16 ? 16 : m <= 32 ? 32 : m <= 64 ? 64 : m <= 128 ? 128 : 192;
   const uint64_t tiles = (n + kRows - 1) / kRows * ((m + cols - 1) / cols);
   // few tiles: a cluster shares a tile's k while SMs are idle and each block
-  // keeps two steps at least
+  // keeps two steps at least.  With and without: 1 x 4096 x 4096 4.5 and 6.2 us,
+  // 300 x 300 x 5000 8.2 and 13.7, 16 x 4096 x 16384 9.9 and 16.1, 64 x 2048 x 2048
+  // 4.7 and 4.6.  One step a block and two rounds of SMs instead: 1 x 4096 x 4096
+  // 10.7, 64 x 2048 x 2048 9.3; four steps a block: 300 x 300 x 5000 8.7, 64 x 2048
+  // x 2048 5.4.
   int splits = 1;
   while (splits < kMaxSplits && tiles * splits * 2 <= sms && steps >= 4ull * splits) splits *= 2;
   if (cols == 16) return run<16, 1, false>(p, a, b, splits, st);

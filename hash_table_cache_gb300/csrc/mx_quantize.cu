@@ -12,11 +12,12 @@
 // 16-bit columns), so that they write 64 neighbouring bytes of codes; both
 // copies come from one read of x.
 //
-// Times (GB300): rows of 1000003 x 128 float32 81 us, 7.2 TB/s, and their
-// values as bfloat16 49 us, 6.6 TB/s; rows of 8192 x 8192 bfloat16 26 us, 6.5
-// TB/s; both copies 42 us, 4.9 TB/s, where the conversions and maxima of two
-// copies take longer than the memory.  Rows that start off
-// 16-byte boundaries: 8200 x 4095 bfloat16 33 us, its values 23 us.
+// Times (GB300): rows of 1000003 x 128 float32 81 us, 7.2 TB/s, their columns 95
+// us, both 110 us, and the rows' values as bfloat16 48 us, 6.7 TB/s; 8192 x 8192
+// bfloat16 rows 26 us, 6.5 TB/s, columns 32 us, 5.4 TB/s, both copies 42 us, 5.0
+// TB/s, where the conversions and maxima of two copies take longer than the
+// memory.  Rows that start off 16-byte boundaries: 8200 x 4095 bfloat16 rows 33
+// us, columns 34, both 39, values 23 us.
 #include <type_traits>
 
 #include "mx.cuh"

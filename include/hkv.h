@@ -387,7 +387,9 @@ hkv_status hkv_mx_matmul(uint64_t m, uint64_t n, uint64_t k, const uint8_t* a_co
  * (offsets: device, 2 * pairs + 1 ascending values in 0 .. rows); sequence p
  * is the chosen and sequence pairs + p the rejected one of pair p.  A token
  * whose label lies outside 0 .. vocab - 1 is not counted: its logits have no
- * effect, whatever they hold.  For counted tokens
+ * effect, whatever they hold.  Banned entries may hold -inf or any finite
+ * number; a counted row that holds a NaN or +inf, or nothing above -inf, gives
+ * NaN.  For counted tokens
  *   logps[t]  = logits[t][labels[t]] - lse[t],  lse[t] = log sum exp logits[t]
  *   ratios[s] = sum of logps[t] - ref_logps[t] over the counted tokens of s,
  *               divided by their number when `average` is not 0 (0 for a
@@ -438,12 +440,15 @@ typedef struct hkv_grad {
 /* Global norm of `count` gradients and clipping to it:
  *   *norm_out = sqrt(sum over all gradients and elements of g^2)   (device)
  *   out       = f * g, f = 1 if *norm_out <= max_norm, else max_norm / *norm_out
- * An infinite norm gives f = 0 and a NaN norm f = NaN.  Where f is 1, out is
- * data and the types agree, nothing is written.  `grads` is a host array,
+ * An infinite norm gives f = 0 and a NaN norm f = NaN (and nothing is added to
+ * the norm that max_norm is divided by, as some libraries do).  Where f is 1, out
+ * is data and the types agree, nothing is written.  `grads` is a host array,
  * read before the call returns.  `work` is device memory of
  * HKV_CLIP_WORK_BYTES (4-byte aligned) that no other call uses meanwhile.
- * Squares are summed in float32 and may overflow to infinity for elements
- * above 1e18.  max_norm is not negative. */
+ * Squares are summed in float32: their sum is infinite from 3.4e38 on, and
+ * elements below 1e-19 lose digits of theirs, all of them below 1e-23.  The sum's
+ * order depends on the sizes, on the tensors' addresses within 32 bytes and on
+ * the number of SMs.  max_norm is not negative. */
 #define HKV_CLIP_WORK_BYTES 16384
 hkv_status hkv_clip_grad_norm(uint64_t count, const hkv_grad* grads, float max_norm,
                               float* norm_out, void* work, void* stream);
