@@ -100,3 +100,32 @@ def test_a_stream_of_another_device_is_refused(hkv):
 
     with pytest.raises(ValueError):
         hkv.mx_quantize(torch.zeros((4, 64), device=DEV), stream=Elsewhere())
+
+
+@pytest.mark.parametrize("stream", [0, "default", "current"])
+def test_the_default_stream_by_any_name(hkv, stream):
+    x = torch.randn((70, 300), device=DEV)
+    want = hkv.mx_quantize(x).dequantize()
+    s = {"default": torch.cuda.default_stream(), "current": torch.cuda.current_stream()}.get(stream, stream)
+    assert torch.equal(hkv.mx_quantize(x, stream=s).dequantize(stream=s), want)
+
+
+def test_a_given_stream_in_a_graph(hkv):
+    """The capturing stream named in every call, on tensors of another stream."""
+    x, grads = torch.randn((70, 256), device=DEV), [torch.randn(5000, device=DEV)]
+    outs = [torch.zeros(5000, device=DEV)]
+    graph = torch.cuda.CUDAGraph()
+    side = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    with torch.cuda.graph(graph, stream=side):
+        q = hkv.mx_quantize(x, stream=side)
+        y = hkv.mx_matmul(q, q, dtype=torch.float32, stream=side)
+        norm = hkv.clip_grad_norm(grads, 1.0, outs=outs, stream=side)
+    x.normal_()
+    grads[0].normal_()
+    graph.replay()
+    torch.cuda.synchronize()
+    q = hkv.mx_quantize(x)
+    assert torch.equal(y, hkv.mx_matmul(q, q, dtype=torch.float32))
+    want = torch.zeros_like(outs[0])
+    assert torch.equal(norm, hkv.clip_grad_norm(grads, 1.0, outs=[want])) and torch.equal(outs[0], want)
