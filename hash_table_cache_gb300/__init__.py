@@ -15,8 +15,8 @@ Two layers:
   non-zero status and allocating outputs.
 
 The operators on looked-up rows (4-bit microscaled copies and their product,
-the preference loss and its gradient, gradient clipping) have the same two
-layers: ``hkv_mx_quantize`` / ... here and ``mx_quantize`` / ... on tensors in
+the preference loss and its gradient, token log probabilities and theirs,
+gradient clipping) have the same two layers: ``hkv_mx_quantize`` / ... here and ``mx_quantize`` / ... on tensors in
 ``hash_table_cache_gb300.operators``, exported here too.
 
 Semantics follow "HierarchicalKV: A GPU Hash Table with Cache Semantics for
@@ -55,6 +55,7 @@ HKV_F32 = 0
 HKV_BF16 = 1
 HKV_F16 = 2
 CLIP_WORK_BYTES = 16384
+MAX_TOP = 32  # alternatives that hkv_token_logps gives at most
 
 # Every symbol include/hkv.h declares (checked by the CPU test suite).
 EXPORTS = (
@@ -64,7 +65,7 @@ EXPORTS = (
     "hkv_insert_and_evict", "hkv_find_or_insert", "hkv_contains", "hkv_find_ptr",
     "hkv_set_epoch", "hkv_mx_quantize", "hkv_mx_dequantize", "hkv_mx_matmul",
     "hkv_preference_loss", "hkv_preference_loss_backward", "hkv_clip_grad_norm",
-    "hkv_get_wait_timeouts",
+    "hkv_get_wait_timeouts", "hkv_token_logps", "hkv_token_logps_backward",
 )
 NOALLOC_SCRATCH_BYTES = 32 << 20
 
@@ -141,6 +142,8 @@ def load(path: str = LIB_PATH):
                                          vp],
         "hkv_clip_grad_norm": [u64, vp, f32, vp, vp, vp],
         "hkv_get_wait_timeouts": [ctypes.POINTER(u64)],
+        "hkv_token_logps": [u64, u64, vp, i32, u64, vp, u32, vp, vp, vp, vp, vp, vp],
+        "hkv_token_logps_backward": [u64, u64, vp, i32, u64, vp, vp, vp, vp, vp, vp, u64, vp],
     }
     for name, args in sig.items():
         fn = getattr(lib, name)
@@ -304,6 +307,19 @@ def hkv_preference_loss_backward(pairs, rows, vocab, logits, type, stride, label
 def hkv_clip_grad_norm(count, grads, max_norm, norm_out, work, stream=None):
     """`grads`: a ctypes array of Grad."""
     return load().hkv_clip_grad_norm(count, grads, max_norm, _p(norm_out), _p(work), _s(stream))
+
+
+def hkv_token_logps(rows, vocab, logits, type, stride, labels, top, logps, entropy, top_logps, top_ids,
+                    lse=None, stream=None):
+    return load().hkv_token_logps(rows, vocab, _p(logits), type, stride, _p(labels), top, _p(logps),
+                                  _p(entropy), _p(top_logps), _p(top_ids), _p(lse), _s(stream))
+
+
+def hkv_token_logps_backward(rows, vocab, logits, type, stride, labels, lse, entropy, dlogps, dentropy,
+                             dlogits, dstride, stream=None):
+    return load().hkv_token_logps_backward(rows, vocab, _p(logits), type, stride, _p(labels), _p(lse),
+                                           _p(entropy), _p(dlogps), _p(dentropy), _p(dlogits), dstride,
+                                           _s(stream))
 
 
 def hkv_get_wait_timeouts():
@@ -470,8 +486,9 @@ class HashTable:
 
 # The operators work on torch tensors, and this module is of use without torch
 # (and is imported in 10 ms, not in seconds): they are imported when first named.
-_OPERATORS = ("MXMatrix", "PreferenceLoss", "clip_grad_norm", "mx_matmul", "mx_quantize",
-              "preference_loss", "preference_loss_backward")
+_OPERATORS = ("MXMatrix", "PreferenceLoss", "TokenLogps", "clip_grad_norm", "mx_matmul",
+              "mx_quantize", "preference_loss", "preference_loss_backward", "token_logps",
+              "token_logps_backward")
 
 
 def __getattr__(name):

@@ -112,6 +112,8 @@ def _tensors(args):
             yield from (a._codes, a._scales) if a._base is None else a._base[:1]
         elif isinstance(a, PreferenceLoss):
             yield from (a.logits, a.labels, a._saved)
+        elif isinstance(a, TokenLogps):
+            yield from (t for t in (a.logits, a.labels, a.entropy, a._lse) if t is not None)
 
 
 # For tensors of the caller's that a kernel has written: autograd counts what it
@@ -339,6 +341,84 @@ def _loss_backward(s, loss, dlosses, out):
         pairs, rows, vocab, logits.data_ptr(), _TYPES[logits.dtype], stride, loss.labels.data_ptr(),
         saved, saved + 4 * rows, saved + 8 * rows, None if dlosses is None else dlosses.data_ptr(),
         out.data_ptr(), dstride, s), "hkv_preference_loss_backward")
+    if given is not None:
+        _written(given)
+    return out
+
+
+class TokenLogps:
+    """What ``token_logps`` returns: ``logps`` [tokens] (None without labels),
+    ``entropy`` [tokens], ``top_logps`` and int64 ``top_ids`` [tokens, top] (None where
+    ``top`` is 0), and what the backward call needs."""
+
+    __slots__ = ("logps", "entropy", "top_logps", "top_ids", "logits", "labels", "_lse")
+
+
+def token_logps(logits, labels=None, top=0, stream=None):
+    """Log probabilities of given tokens, with the entropy and the ``top`` (at most
+    32) largest entries of their rows of logits.
+
+    ``logits`` [tokens, vocab]; ``labels`` int64 [tokens], a value outside the
+    vocabulary for tokens that are not counted, or None: entropy and alternatives
+    of every row.  Alternatives go from the largest down, equal ones by the lower
+    index.  Returns a ``TokenLogps``."""
+    return _call(_cuda(logits, "logits"), stream, _token_logps, logits, labels, top)
+
+
+def _token_logps(s, logits, labels, top):
+    device = logits.device
+    kind = _type(logits, "logits")
+    rows, vocab, stride = _matrix(logits, "logits")
+    if not 0 <= top <= min(vocab, _abi.MAX_TOP):
+        raise ValueError(f"top: 0 to {min(vocab, _abi.MAX_TOP)}, not {top}")
+    f = TokenLogps()
+    f.logits, f.labels = logits, labels
+    f.logps = f.top_logps = f.top_ids = None
+    if labels is not None:
+        _vector(labels, rows, torch.int64, "labels", device)
+        f.logps = torch.empty(rows, dtype=torch.float32, device=device)
+    f.entropy = torch.empty(rows, dtype=torch.float32, device=device)
+    f._lse = torch.empty(2 * rows, dtype=torch.float32, device=device)
+    if top:
+        f.top_logps = torch.empty((rows, top), dtype=torch.float32, device=device)
+        f.top_ids = torch.empty((rows, top), dtype=torch.int64, device=device)
+    at = [None if t is None else t.data_ptr() for t in (labels, f.logps, f.top_logps, f.top_ids)]
+    _ok(_abi.load().hkv_token_logps(rows, vocab, logits.data_ptr(), kind, stride, at[0], top, at[1],
+                                    f.entropy.data_ptr(), at[2], at[3], f._lse.data_ptr(), s),
+        "hkv_token_logps")
+    return f
+
+
+def token_logps_backward(f, dlogps=None, dentropy=None, out=None, stream=None):
+    """The gradient of ``(dlogps * f.logps + dentropy * f.entropy).sum()`` with
+    respect to the logits, in their type, from what ``token_logps`` returned.
+    ``out`` may be the logits themselves, which then hold the gradient."""
+    return _call(f.logits.device, stream, _token_logps_backward, f, dlogps, dentropy, out)
+
+
+def _token_logps_backward(s, f, dlogps, dentropy, out):
+    logits = f.logits
+    device = logits.device
+    rows, vocab, stride = _matrix(logits, "logits")
+    given = out
+    if dlogps is not None:
+        if f.labels is None:
+            raise ValueError("dlogps: there were no labels")
+        _vector(dlogps, rows, torch.float32, "dlogps", device)
+    if dentropy is not None:
+        _vector(dentropy, rows, torch.float32, "dentropy", device)
+    if out is None:
+        out = torch.empty((rows, vocab), dtype=logits.dtype, device=device)
+        dstride = vocab
+    else:
+        if out.dtype != logits.dtype or out.shape != logits.shape:
+            raise ValueError(f"out: {rows} x {vocab} of {logits.dtype}")
+        _same(out, device, "out")
+        dstride = _matrix(out, "out")[2]
+    at = [None if t is None else t.data_ptr() for t in (f.labels, dlogps, dentropy)]
+    _ok(_abi.load().hkv_token_logps_backward(
+        rows, vocab, logits.data_ptr(), _TYPES[logits.dtype], stride, at[0], f._lse.data_ptr(),
+        f.entropy.data_ptr(), at[1], at[2], out.data_ptr(), dstride, s), "hkv_token_logps_backward")
     if given is not None:
         _written(given)
     return out

@@ -426,6 +426,40 @@ hkv_status hkv_preference_loss_backward(uint64_t pairs, uint64_t rows, uint64_t 
                                         const float* dlosses, void* dlogits, uint64_t dstride,
                                         void* stream);
 
+/* Log probabilities of given tokens, with the entropy and the largest entries
+ * of their rows of logits.  `logits` holds one row of `vocab` logits for each
+ * of `rows` tokens.  A token whose label lies outside 0 .. vocab - 1 is not
+ * counted: its logits have no effect, whatever they hold, its logps and
+ * entropy are 0, its top_ids -1 and its top_logps -inf.  With labels NULL (and
+ * logps NULL) every row is counted.  For counted tokens
+ *   logps[t]        = logits[t][labels[t]] - lse[t],  lse[t] = log sum exp logits[t]
+ *   entropy[t]      = -sum_v p_v log p_v,  log p_v = logits[t][v] - lse[t]
+ *   top_ids[t][j]   = the j-th largest entry's index, of equal ones the lower
+ *                     first (-0 equals 0), j < top
+ *   top_logps[t][j] = its log p
+ * Entries may hold -inf or any finite mask (log p -inf, and 0 to the entropy);
+ * a counted row that holds a NaN or +inf, or nothing above -inf, gives NaNs and
+ * top_ids of -1.  For the backward call lse (NULL where it is not wanted) gets
+ * two floats for each row, lse[t] and what that float leaves out of it.  top is
+ * at most HKV_MAX_TOP and at most vocab. */
+#define HKV_MAX_TOP 32
+hkv_status hkv_token_logps(uint64_t rows, uint64_t vocab, const void* logits, int type,
+                           uint64_t stride, const int64_t* labels, uint32_t top, float* logps,
+                           float* entropy, float* top_logps, int64_t* top_ids, float* lse,
+                           void* stream);
+
+/* Gradient of sum_t dlogps[t] * logps[t] + dentropy[t] * entropy[t] with
+ * respect to the logits (either may be NULL: zeros), in their type:
+ *   dlogits[t][v] = dlogps[t] (1[v = labels[t]] - p_v)
+ *                   - dentropy[t] p_v (log p_v + entropy[t])
+ * and zeros for a token that is not counted.  labels, lse and entropy are the
+ * forward call's.  dlogits may be the logits' own buffer with the same stride,
+ * and must not overlap them otherwise. */
+hkv_status hkv_token_logps_backward(uint64_t rows, uint64_t vocab, const void* logits, int type,
+                                    uint64_t stride, const int64_t* labels, const float* lse,
+                                    const float* entropy, const float* dlogps, const float* dentropy,
+                                    void* dlogits, uint64_t dstride, void* stream);
+
 /* One gradient: n elements of `type` at `data`.  Where `out` is not NULL the
  * clipped gradient is written there as `out_type`; it may be `data` itself
  * with the same type, and must not overlap it otherwise, nor another gradient
