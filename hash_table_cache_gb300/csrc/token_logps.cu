@@ -7,6 +7,17 @@
 // so one pass with a running maximum gives both; when the maximum rises by d,
 // w becomes (w - s d) exp(-d) and s becomes s exp(-d).  Rows are taken by a
 // warp, a block or a cluster's blocks, as in preference.cu.
+//
+// The `top` largest entries come from the same pass.  Lanes of equal number in
+// all warps form one of 32 groups; the top-th largest of the groups' maxima is a
+// value that at least `top` entries reach, and few more do: 32 log(32 / (32 -
+// top)) of a row without order, 31 for 20, about 130 for 32.  Each thread keeps
+// the maximum of each of its rounds of loads (a cell: 32 16-bit entries), so that
+// only cells that reach the value are read again, and the entries found there are
+// ranked by counting.  Rows with too many entries that reach it (ties at a mask)
+// are read once more for the groups' largest entries by value and index, and rows
+// where that is not enough (entries that repeat with the groups) once for each
+// alternative.
 #include "logits.cuh"
 
 namespace hkv {
@@ -69,15 +80,43 @@ __device__ __forceinline__ Moments join_lanes(Moments r) {
   return r;
 }
 
-// One thread's share of a row of n elements, taken by kLanes threads.
+// The clamp that keeps a product of 0 and -inf out of w: masks below it have
+// exponential 0 in any case where it is used (a maximum within kFactored).
+template <class T>
+__device__ __forceinline__ void clamp(Chunk<T>& c) {
+  if constexpr (sizeof(T) == 4) {
+    float* e = reinterpret_cast<float*>(&c.w);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) e[i] = max_nan(e[i], kLeast);
+  } else {
+    using T2 = std::conditional_t<std::is_same_v<T, __nv_bfloat16>, __nv_bfloat162, __half2>;
+    T2* e = reinterpret_cast<T2*>(&c.w);
+    T2 least;
+    if constexpr (std::is_same_v<T, __nv_bfloat16>) least = __float2bfloat162_rn(kLeast);
+    else least = __float2half2_rn(-65504.f);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) e[i] = __hmax2_nan(e[i], least);
+  }
+}
+
+// Cells that a thread keeps at most of a row (a cell is one round of loads or, of
+// longer rows, several).
 template <class T, int kLanes>
-__device__ __forceinline__ Moments row_pass(const T* x, uint64_t n, int lane) {
+constexpr int cells_of() { return kLanes == 32 ? 4 : 64 / static_cast<int>(sizeof(T)); }
+
+// One thread's share of a row of n elements, taken by kLanes threads.  With kTop
+// cells[i * kLanes] gets the maximum of its rounds i * per .. (i + 1) * per - 1.
+template <class T, int kLanes, bool kTop>
+__device__ __forceinline__ Moments row_pass(const T* x, uint64_t n, int lane, T* cells, uint32_t per,
+                                            uint32_t count) {
   constexpr int kN = Chunk<T>::kN, kUnroll = unroll(kLanes);
   Moments r;
   const uint32_t head = to_boundary(x, n);
   if (lane < static_cast<int>(head)) r.one(to_f32(x[lane]));
   const T* body = x + head;
   const uint64_t chunks = (n - head) / kN;
+  float cell = -INFINITY;
+  uint32_t in_cell = 0, kept = 0;
   for (uint64_t k = lane; k < chunks; k += kUnroll * kLanes) {
     Chunk<T> c[kUnroll];
 #pragma unroll
@@ -85,12 +124,54 @@ __device__ __forceinline__ Moments row_pass(const T* x, uint64_t n, int lane) {
       if (k + u * kLanes < chunks) c[u].w = ld_stream_v4(body + (k + u * kLanes) * kN);
       else c[u].fill_lowest();
     }
-    const float base = r.raise(largest(c));
+    const float top = largest(c);
+    const float base = r.raise(top);
+    if constexpr (kTop) {
+      cell = fmaxf(cell, top);
+      if (++in_cell == per) {
+        cells[kept++ * kLanes] = from_f32<T>(cell);
+        cell = -INFINITY;
+        in_cell = 0;
+      }
+    }
+    if (fabsf(base) < kFactored) {
+      // exp(x - base) as 2^a, a = x log2 e - base log2 e by two multiply-adds.  The
+      // same rounded base log2 e is in every a; what it is off by is taken out of
+      // the sums.
+      const float scaled = base * kLog2e;
+      const float off = fmaf(base, kLog2eRest, fmaf(base, kLog2e, -scaled));
+      const uint64_t l = both(kLog2e, kLog2e), rest = both(kLog2eRest, kLog2eRest);
+      const uint64_t minus = both(-scaled, -scaled);
+      uint64_t sum[2] = {}, wsum[2] = {};
 #pragma unroll
-    for (int u = 0; u < kUnroll; ++u)
+      for (int u = 0; u < kUnroll; ++u) {
+        clamp(c[u]);
 #pragma unroll
-      for (int i = 0; i < kN; ++i) r.add(c[u].at(i), base);
+        for (int i = 0; i < kN; i += 2) {
+          const uint64_t x2 = both(c[u].at(i), c[u].at(i + 1));
+          const uint64_t a2 = fma_both(x2, rest, fma_both(x2, l, minus));
+          const float2 a = parts(a2);
+          const uint64_t e2 = both(exp2_approx(a.x), exp2_approx(a.y));
+          sum[i / 2 & 1] = add_both(sum[i / 2 & 1], e2);
+          wsum[i / 2 & 1] = fma_both(e2, a2, wsum[i / 2 & 1]);
+        }
+      }
+      const float2 t = parts(add_both(sum[0], sum[1])), v = parts(add_both(wsum[0], wsum[1]));
+      const float back = exp2_of_minus(off), total = t.x + t.y;
+      r.s = fmaf(total, back, r.s);
+      r.w = fmaf((v.x + v.y) - off * total, back * 0.693147181f, r.w);
+    } else {
+#pragma unroll
+      for (int u = 0; u < kUnroll; ++u)
+#pragma unroll
+        for (int i = 0; i < kN; ++i) r.add(c[u].at(i), base);
+    }
   }
+  if constexpr (kTop)
+    for (; kept < count; ++kept) {
+      cells[kept * kLanes] = from_f32<T>(cell);
+      cell = -INFINITY;
+    }
   const uint64_t tail = head + chunks * kN + lane;
   if (tail < n) r.one(to_f32(x[tail]));
   return r;
@@ -115,17 +196,164 @@ __device__ __forceinline__ uint64_t largest_of_warp(uint64_t key) {
   return key;
 }
 
-// The largest entry of x[lo .. hi) below `limit` among this thread's.
+// The threads of a row or a part of one, and what they share to find its
+// largest entries.
 template <class T, int kLanes>
-__device__ __forceinline__ uint64_t largest_below(const T* x, uint64_t lo, uint64_t hi,
-                                                  uint64_t limit, int lane) {
-  uint64_t best = 0;
-  for (uint64_t i = lo + lane; i < hi; i += kLanes) {
-    const uint64_t key = key_of(to_f32(x[i]), i);
-    if (key < limit) best = max(best, key);
+struct Team {
+  static constexpr int kCells = cells_of<T, kLanes>(), kKeys = kLanes == 32 ? 384 : 512;
+  static constexpr int kItems = kLanes == 32 ? 128 : 512;
+  uint64_t keys[kKeys];
+  uint64_t best[kLanes];
+  uint64_t list[HKV_MAX_TOP];  // the result: largest first, 0 where there are no more
+  T cells[kCells * kLanes];
+  float most[kLanes];
+  uint16_t items[kItems];  // cell * kLanes + lane
+  uint32_t items_found, keys_found;
+  float bound;
+  uint64_t limit;
+
+  static __device__ __forceinline__ void sync() {
+    if constexpr (kLanes == 32) __syncwarp();
+    else __syncthreads();
   }
-  return best;
-}
+  __device__ __forceinline__ void add(uint64_t key) {
+    const uint32_t i = atomicAdd(&keys_found, 1);
+    if (i < kKeys) keys[i] = key;
+  }
+  // Ranks the keys found (which are all different) and keeps the first `top`.
+  __device__ __forceinline__ void rank(uint32_t top, uint32_t lane) {
+    const uint32_t n = keys_found;
+    for (uint32_t i = lane; i < n; i += kLanes) {
+      const uint64_t key = keys[i];
+      uint32_t above = 0;
+      for (uint32_t j = 0; j < n; ++j) above += keys[j] > key;
+      if (above < top) list[above] = key;
+    }
+  }
+  // Rounds of loads to a cell, and cells, of n elements from x on.
+  static __device__ __forceinline__ void plan(const T* x, uint64_t n, uint32_t& per, uint32_t& count) {
+    constexpr uint64_t kRound = kLanes * unroll(kLanes);
+    const uint64_t chunks = (n - to_boundary(x, n)) / Chunk<T>::kN;
+    const uint64_t rounds = (chunks + kRound - 1) / kRound;
+    per = 1;
+    if (rounds > kCells) per = static_cast<uint32_t>((rounds + kCells - 1) / kCells);
+    count = static_cast<uint32_t>(per == 1 ? rounds : (rounds + per - 1) / per);
+  }
+
+  // The `top` largest of x[lo .. hi), m being this thread's maximum of them and
+  // cells written.  All of the team's threads call it.
+  __device__ __forceinline__ void pick(const T* x, uint64_t lo, uint64_t hi, float m, uint32_t per,
+                                       uint32_t count, uint32_t top, uint32_t lane) {
+    constexpr int kN = Chunk<T>::kN, kUnroll = unroll(kLanes);
+    most[lane] = m;
+    if (lane < HKV_MAX_TOP) list[lane] = 0;
+    if (lane == 0) items_found = keys_found = 0;
+    sync();
+    if (lane < 32) {
+      float v = m;
+      for (uint32_t i = lane + 32; i < kLanes; i += 32) v = fmaxf(v, most[i]);
+      uint32_t above = 0;
+      for (int i = 0; i < 32; ++i) above += __shfl_sync(0xFFFFFFFFu, v, i) > v;
+      float least = above < top ? v : INFINITY;
+      for (int o = 16; o > 0; o >>= 1) least = fminf(least, __shfl_xor_sync(0xFFFFFFFFu, least, o));
+      if (lane == 0) bound = least;
+    }
+    sync();
+    const float b = bound;
+    const T* part = x + lo;
+    const uint64_t n = hi - lo;
+    const uint32_t head = to_boundary(part, n);
+    const uint64_t chunks = (n - head) / kN;
+    for (uint32_t i = 0; i < count; ++i)
+      if (to_f32(cells[i * kLanes + lane]) >= b) {
+        const uint32_t at = atomicAdd(&items_found, 1);
+        if (at < kItems) items[at] = static_cast<uint16_t>(i * kLanes + lane);
+      }
+    // what lies before the first and behind the last whole chunk
+    if (lane < head && to_f32(part[lane]) >= b) add(key_of(to_f32(part[lane]), lo + lane));
+    const uint64_t tail = head + chunks * kN + lane;
+    if (tail < n && to_f32(part[tail]) >= b) add(key_of(to_f32(part[tail]), lo + tail));
+    sync();
+    const uint32_t found = items_found;
+    bool done = found <= kItems;
+    if (done) {
+      const uint32_t each = per * kUnroll;
+      for (uint32_t j = lane; j < found * each; j += kLanes) {
+        const uint32_t item = items[j / each];
+        const uint64_t k = (static_cast<uint64_t>(item / kLanes) * each + j % each) * kLanes + item % kLanes;
+        if (k >= chunks) continue;
+        Chunk<T> c;
+        c.w = ld_nc_v4(part + head + k * kN);
+#pragma unroll
+        for (int i = 0; i < kN; ++i)
+          if (c.at(i) >= b) add(key_of(c.at(i), lo + head + k * kN + i));
+      }
+      sync();
+      done = keys_found <= kKeys;
+    }
+    if (!done) {
+      done = pick_by_keys(x, lo, hi, top, lane);
+      if (!done) {
+        pick_each(x, lo, hi, top, lane);
+        return;
+      }
+    }
+    rank(top, lane);
+    sync();
+  }
+
+  // The same with the groups' largest entries by value and index.  False where
+  // too many entries are left all the same.
+  __device__ __noinline__ bool pick_by_keys(const T* x, uint64_t lo, uint64_t hi, uint32_t top,
+                                            uint32_t lane) {
+    uint64_t mine = 0;
+#pragma unroll 8
+    for (uint64_t i = lo + lane; i < hi; i += kLanes) mine = max(mine, key_of(to_f32(x[i]), i));
+    best[lane] = mine;
+    sync();  // all have read keys_found
+    if (lane == 0) keys_found = 0;
+    if (lane < 32) {
+      for (uint32_t i = lane + 32; i < kLanes; i += 32) mine = max(mine, best[i]);
+      uint32_t above = 0;
+      for (int i = 0; i < 32; ++i) above += __shfl_sync(0xFFFFFFFFu, mine, i) > mine;
+      uint64_t least = above < top ? mine : ~0ull;
+      for (int o = 16; o > 0; o >>= 1) least = min(least, __shfl_xor_sync(0xFFFFFFFFu, least, o));
+      if (lane == 0) limit = least;
+    }
+    sync();
+    const uint64_t l = limit;
+#pragma unroll 8
+    for (uint64_t i = lo + lane; i < hi; i += kLanes) {
+      const uint64_t key = key_of(to_f32(x[i]), i);
+      if (key >= l) add(key);
+    }
+    sync();
+    return keys_found <= kKeys;
+  }
+
+  // The largest, the largest below it, and so on.
+  __device__ __noinline__ void pick_each(const T* x, uint64_t lo, uint64_t hi, uint32_t top,
+                                         uint32_t lane) {
+    uint64_t below = ~0ull;
+    for (uint32_t j = 0; j < top && below; ++j) {
+      uint64_t key = 0;
+#pragma unroll 8
+      for (uint64_t i = lo + lane; i < hi; i += kLanes) {
+        const uint64_t other = key_of(to_f32(x[i]), i);
+        if (other < below) key = max(key, other);
+      }
+      best[lane] = key;
+      sync();
+      if (lane < 32) {
+        for (uint32_t i = lane + 32; i < kLanes; i += 32) key = max(key, best[i]);
+        key = largest_of_warp(key);
+        if (lane == 0) list[j] = limit = key;
+      }
+      sync();
+      below = limit;
+    }
+  }
+};
 
 __device__ __forceinline__ uint64_t remote_u64(uint32_t addr, uint32_t rank) {
   uint32_t far;
@@ -171,11 +399,20 @@ __device__ __forceinline__ void put_top(uint64_t at, uint64_t key, const Row& ro
   out.top_logps[at] = row.bad ? NAN : row.logp(logit_of(key));
 }
 
+__device__ __forceinline__ void no_top(uint64_t t, uint32_t top, uint32_t lane, const Out& out) {
+  if (lane < top) {
+    out.top_ids[t * top + lane] = -1;
+    out.top_logps[t * top + lane] = -INFINITY;
+  }
+}
+
 // A warp per row: short rows.
-template <class T>
+template <class T, bool kTop>
 __global__ void __launch_bounds__(kWarpThreads)
     short_rows_kernel(uint64_t rows, uint64_t vocab, const T* __restrict__ logits, uint64_t stride,
                       const int64_t* __restrict__ labels, uint32_t top, Out out) {
+  using Warp = Team<T, 32>;
+  extern __shared__ uint64_t smem[];
   pdl_trigger();
   pdl_wait();
   const uint64_t t = static_cast<uint64_t>(blockIdx.x) * (kWarpThreads / 32) + threadIdx.x / 32;
@@ -184,45 +421,43 @@ __global__ void __launch_bounds__(kWarpThreads)
   const int64_t label = labels ? labels[t] : 0;
   if (!counts(label, vocab)) {
     if (lane == 0) no_row(t, out);
-    if (lane < top) {
-      out.top_ids[t * top + lane] = -1;
-      out.top_logps[t * top + lane] = -INFINITY;
-    }
+    if (kTop) no_top(t, top, lane, out);
     return;
   }
   const T* x = logits + t * stride;
   const float chosen = to_f32(x[label]);
-  const Moments r = join_lanes(row_pass<T, 32>(x, vocab, lane));
+  Warp* team = reinterpret_cast<Warp*>(smem) + threadIdx.x / 32;
+  uint32_t per = 0, count = 0;
+  if constexpr (kTop) Warp::plan(x, vocab, per, count);
+  const Moments own = row_pass<T, 32, kTop>(x, vocab, lane, kTop ? team->cells + lane : nullptr, per, count);
+  const Moments r = join_lanes(own);
   const Row row(r);
   if (lane == 0) finish_row(r, row, true, chosen, t, out);
-  uint64_t limit = ~0ull;
-  for (uint32_t j = 0; j < top; ++j) {
-    limit = largest_of_warp(largest_below<T, 32>(x, 0, vocab, limit, lane));
-    if (lane == 0) put_top(t * top + j, limit, row, out);
+  if constexpr (kTop) {
+    if (!row.bad) team->pick(x, 0, vocab, own.m, per, count, top, lane);
+    if (lane < top) put_top(t * top + lane, row.bad ? 0 : team->list[lane], row, out);
   }
 }
 
 // A block per row, or the `parts` blocks of a cluster.
-template <class T>
-__global__ void __launch_bounds__(kThreads)
+template <class T, bool kTop>
+__global__ void __launch_bounds__(kThreads, kTop ? 5 : 6)
     long_rows_kernel(uint64_t vocab, const T* __restrict__ logits, uint64_t stride, uint32_t parts,
                      const int64_t* __restrict__ labels, uint32_t top, Out out) {
   constexpr int kWarps = kThreads / 32;
+  using Block = Team<T, kThreads>;
+  extern __shared__ uint64_t smem[];
   __shared__ float ms[3][kWarps + 1];  // [maximum, sum, weighted sum][warp, then the block]
-  __shared__ uint64_t red[2][kWarps];
-  __shared__ uint64_t mine[HKV_MAX_TOP], all[HKV_MAX_TOP * kMaxParts];
+  Block* team = reinterpret_cast<Block*>(smem);
   pdl_trigger();
   pdl_wait();
   const uint64_t t = blockIdx.x / parts;
-  const uint32_t part = blockIdx.x % parts;
+  const uint32_t part = blockIdx.x % parts, lane = threadIdx.x;
   const int64_t label = labels ? labels[t] : 0;
-  const bool writes = part == 0 && threadIdx.x == 0;
+  const bool writes = part == 0 && lane == 0;
   if (!counts(label, vocab)) {
     if (writes) no_row(t, out);
-    if (part == 0 && threadIdx.x < top) {
-      out.top_ids[t * top + threadIdx.x] = -1;
-      out.top_logps[t * top + threadIdx.x] = -INFINITY;
-    }
+    if (kTop && part == 0) no_top(t, top, lane, out);
     return;  // every block of the cluster
   }
   const T* x = logits + t * stride;
@@ -230,9 +465,13 @@ __global__ void __launch_bounds__(kThreads)
   // parts start at multiples of 64 elements of the row
   const uint64_t size = ((vocab + parts - 1) / parts + 63) / 64 * 64;
   const uint64_t lo = min(part * size, vocab), hi = min(lo + size, vocab);
-  Moments r = join_lanes(row_pass<T, kThreads>(x + lo, hi - lo, threadIdx.x));
-  const int warp = threadIdx.x >> 5;
-  if ((threadIdx.x & 31) == 0) {
+  uint32_t per = 0, count = 0;
+  if constexpr (kTop) Block::plan(x + lo, hi - lo, per, count);
+  Moments r = row_pass<T, kThreads, kTop>(x + lo, hi - lo, lane, kTop ? team->cells + lane : nullptr, per, count);
+  const float own = r.m;
+  r = join_lanes(r);
+  const int warp = lane >> 5;
+  if ((lane & 31) == 0) {
     ms[0][warp] = r.m;
     ms[1][warp] = r.s;
     ms[2][warp] = r.w;
@@ -240,51 +479,44 @@ __global__ void __launch_bounds__(kThreads)
   __syncthreads();
   if (warp == 0) {
     r = Moments{};
-    if (threadIdx.x < kWarps) r = Moments{ms[0][threadIdx.x], ms[1][threadIdx.x], ms[2][threadIdx.x]};
+    if (lane < kWarps) r = Moments{ms[0][lane], ms[1][lane], ms[2][lane]};
     r = join_lanes(r);
-    if (threadIdx.x == 0) {
+    if (lane == 0) {
       ms[0][kWarps] = r.m;
       ms[1][kWarps] = r.s;
       ms[2][kWarps] = r.w;
     }
   }
-  uint64_t limit = ~0ull;
-  for (uint32_t j = 0; j < top; ++j) {
-    const uint64_t best =
-        largest_of_warp(largest_below<T, kThreads>(x, lo, hi, limit, threadIdx.x));
-    if ((threadIdx.x & 31) == 0) red[j & 1][warp] = best;
-    __syncthreads();
-    limit = red[j & 1][0];
-    for (int i = 1; i < kWarps; ++i) limit = max(limit, red[j & 1][i]);
-    if (threadIdx.x == 0) mine[j] = limit;
-  }
-  __syncthreads();
+  if constexpr (kTop) team->pick(x, lo, hi, own, per, count, top, lane);
   if (parts > 1) {
+    __syncthreads();
     cluster_sync();
     if (part == 0) {
       r = Moments{ms[0][kWarps], ms[1][kWarps], ms[2][kWarps]};
       for (uint32_t p = 1; p < parts; ++p)
         r.join(Moments{remote_f32(smem_u32(&ms[0][kWarps]), p), remote_f32(smem_u32(&ms[1][kWarps]), p),
                        remote_f32(smem_u32(&ms[2][kWarps]), p)});
-      if (threadIdx.x < parts * top)
-        all[threadIdx.x] = remote_u64(smem_u32(&mine[threadIdx.x % top]), threadIdx.x / top);
+      if constexpr (kTop)  // the parts' entries, each where no other thread's is
+        if (lane < parts * top) team->keys[lane] = remote_u64(smem_u32(&team->list[lane % top]), lane / top);
     }
     cluster_sync();  // the others stay until their parts are read
     if (part) return;
     const Row row(r);
     if (writes) finish_row(r, row, true, chosen, t, out);
-    if (threadIdx.x < parts * top) {
-      const uint64_t key = all[threadIdx.x];
-      uint32_t rank = 0;
-      for (uint32_t i = 0; i < parts * top; ++i) rank += all[i] > key;
-      if (key && rank < top) put_top(t * top + rank, key, row, out);
-    }
+    if constexpr (kTop)
+      if (lane < parts * top) {
+        const uint64_t key = team->keys[lane];
+        uint32_t above = 0;
+        for (uint32_t i = 0; i < parts * top; ++i) above += team->keys[i] > key;
+        if (row.bad ? lane < top : key && above < top) put_top(t * top + (row.bad ? lane : above), key, row, out);
+      }
     return;
   }
+  __syncthreads();
   r = Moments{ms[0][kWarps], ms[1][kWarps], ms[2][kWarps]};
   const Row row(r);
   if (writes) finish_row(r, row, true, chosen, t, out);
-  if (threadIdx.x < top) put_top(t * top + threadIdx.x, mine[threadIdx.x], row, out);
+  if (kTop && lane < top) put_top(t * top + lane, team->list[lane], row, out);
 }
 
 // A piece of a row for every kLanes threads, rows from the last to the first, so
@@ -367,8 +599,10 @@ cudaError_t forward_rows(uint64_t rows, uint64_t vocab, const T* logits, uint64_
                          const int64_t* labels, uint32_t top, const Out& out, cudaStream_t st) {
   const uint64_t sms = sm_count();
   if (by_warps(rows, vocab * sizeof(T)))
-    return launch_chained(short_rows_kernel<T>, static_cast<unsigned>((rows + 3) / 4), kWarpThreads,
-                          0, st, rows, vocab, logits, stride, labels, top, out);
+    return launch_chained(top ? short_rows_kernel<T, true> : short_rows_kernel<T, false>,
+                          static_cast<unsigned>((rows + 3) / 4), kWarpThreads,
+                          top ? kWarpThreads / 32 * sizeof(Team<T, 32>) : 0, st, rows, vocab, logits,
+                          stride, labels, top, out);
   // few rows: clusters share them while there is room on the SMs and a part
   // keeps a round of its block's loads
   uint32_t parts = 1;
@@ -379,6 +613,7 @@ cudaError_t forward_rows(uint64_t rows, uint64_t vocab, const T* logits, uint64_
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(static_cast<unsigned>(rows * parts));
   cfg.blockDim = dim3(kThreads);
+  cfg.dynamicSmemBytes = top ? sizeof(Team<T, kThreads>) : 0;
   cfg.stream = st;
   cudaLaunchAttribute attr[2];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
@@ -388,7 +623,7 @@ cudaError_t forward_rows(uint64_t rows, uint64_t vocab, const T* logits, uint64_
   attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
   cfg.attrs = attr;
   cfg.numAttrs = parts > 1 ? 2 : 1;
-  return cudaLaunchKernelEx(&cfg, long_rows_kernel<T>, vocab, logits, stride, parts, labels, top, out);
+  return cudaLaunchKernelEx(&cfg, top ? long_rows_kernel<T, true> : long_rows_kernel<T, false>, vocab, logits, stride, parts, labels, top, out);
 }
 
 }  // namespace
