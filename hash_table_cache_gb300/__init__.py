@@ -16,7 +16,7 @@ Two layers:
 
 The operators on looked-up rows (4-bit microscaled copies and their product,
 the preference loss and its gradient, token log probabilities and theirs,
-gradient clipping) have the same two layers: ``hkv_mx_quantize`` / ... here and ``mx_quantize`` / ... on tensors in
+low-rank adapters and theirs, gradient clipping) have the same two layers: ``hkv_mx_quantize`` / ... here and ``mx_quantize`` / ... on tensors in
 ``hash_table_cache_gb300.operators``, exported here too.
 
 Semantics follow "HierarchicalKV: A GPU Hash Table with Cache Semantics for
@@ -55,6 +55,7 @@ HKV_F32 = 0
 HKV_BF16 = 1
 HKV_F16 = 2
 CLIP_WORK_BYTES = 16384
+MAX_RANK = 64  # of an adapter
 MAX_TOP = 32  # alternatives that hkv_token_logps gives at most
 
 # Every symbol include/hkv.h declares (checked by the CPU test suite).
@@ -66,6 +67,7 @@ EXPORTS = (
     "hkv_set_epoch", "hkv_mx_quantize", "hkv_mx_dequantize", "hkv_mx_matmul",
     "hkv_preference_loss", "hkv_preference_loss_backward", "hkv_clip_grad_norm",
     "hkv_get_wait_timeouts", "hkv_token_logps", "hkv_token_logps_backward",
+    "hkv_adapter_matmul", "hkv_adapter_matmul_backward",
 )
 NOALLOC_SCRATCH_BYTES = 32 << 20
 
@@ -94,6 +96,13 @@ class Info(ctypes.Structure):
 class Grad(ctypes.Structure):
     _fields_ = [("data", ctypes.c_void_p), ("out", ctypes.c_void_p), ("n", ctypes.c_uint64),
                 ("type", ctypes.c_int32), ("out_type", ctypes.c_int32)]
+
+
+class Adapters(ctypes.Structure):
+    _fields_ = [("count", ctypes.c_uint64),
+                ("down", ctypes.c_void_p), ("down_step", ctypes.c_uint64), ("down_stride", ctypes.c_uint64),
+                ("up", ctypes.c_void_p), ("up_step", ctypes.c_uint64), ("up_stride", ctypes.c_uint64),
+                ("scales", ctypes.c_void_p), ("rank", ctypes.c_uint32)]
 
 
 _lib = None
@@ -142,6 +151,9 @@ def load(path: str = LIB_PATH):
                                          vp],
         "hkv_clip_grad_norm": [u64, vp, f32, vp, vp, vp],
         "hkv_get_wait_timeouts": [ctypes.POINTER(u64)],
+        "hkv_adapter_matmul": [u64, u64, u64, i32, vp, u64, vp, vp, vp, u64, vp, u64, vp, u64, vp, vp],
+        "hkv_adapter_matmul_backward": [u64, u64, u64, i32, vp, u64, vp, vp, vp, u64, vp, u64, vp, vp,
+                                        u64, vp, u64, vp, vp, vp, vp],
         "hkv_token_logps": [u64, u64, vp, i32, u64, vp, u32, vp, vp, vp, vp, vp, vp],
         "hkv_token_logps_backward": [u64, u64, vp, i32, u64, vp, vp, vp, vp, vp, vp, u64, vp],
     }
@@ -307,6 +319,24 @@ def hkv_preference_loss_backward(pairs, rows, vocab, logits, type, stride, label
 def hkv_clip_grad_norm(count, grads, max_norm, norm_out, work, stream=None):
     """`grads`: a ctypes array of Grad."""
     return load().hkv_clip_grad_norm(count, grads, max_norm, _p(norm_out), _p(work), _s(stream))
+
+
+def hkv_adapter_matmul(tokens, k, n, type, adapters, requests, offsets, which, x, x_stride, base,
+                       base_stride, y, y_stride, hidden=None, stream=None):
+    """`adapters`: an Adapters, by reference (ctypes.byref) or address."""
+    return load().hkv_adapter_matmul(tokens, k, n, type, adapters, requests, _p(offsets), _p(which),
+                                     _p(x), x_stride, _p(base), base_stride, _p(y), y_stride,
+                                     _p(hidden), _s(stream))
+
+
+def hkv_adapter_matmul_backward(tokens, k, n, type, adapters, requests, offsets, which, x, x_stride, dy,
+                                dy_stride, hidden, base, base_stride, dx, dx_stride, ddown, dup,
+                                dhidden, stream=None):
+    """`adapters`: an Adapters, by reference (ctypes.byref) or address."""
+    return load().hkv_adapter_matmul_backward(
+        tokens, k, n, type, adapters, requests, _p(offsets), _p(which), _p(x), x_stride, _p(dy),
+        dy_stride, _p(hidden), _p(base), base_stride, _p(dx), dx_stride, _p(ddown), _p(dup),
+        _p(dhidden), _s(stream))
 
 
 def hkv_token_logps(rows, vocab, logits, type, stride, labels, top, logps, entropy, top_logps, top_ids,
@@ -486,8 +516,8 @@ class HashTable:
 
 # The operators work on torch tensors, and this module is of use without torch
 # (and is imported in 10 ms, not in seconds): they are imported when first named.
-_OPERATORS = ("MXMatrix", "PreferenceLoss", "TokenLogps", "clip_grad_norm", "mx_matmul",
-              "mx_quantize", "preference_loss", "preference_loss_backward", "token_logps",
+_OPERATORS = ("AdapterMatmul", "MXMatrix", "PreferenceLoss", "TokenLogps", "adapter_matmul",
+              "adapter_matmul_backward", "clip_grad_norm", "mx_matmul", "mx_quantize", "preference_loss", "preference_loss_backward", "token_logps",
               "token_logps_backward")
 
 

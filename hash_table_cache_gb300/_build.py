@@ -13,7 +13,8 @@ BUILD = os.path.join(PKG, "_build")
 LIB = os.path.join(PKG, "libhkv.so")
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 SOURCES = ["table.cu", "find.cu", "upsert.cu", "export.cu", "no_alloc.cu",
-           "mx_quantize.cu", "mx_matmul.cu", "preference.cu", "clip.cu", "token_logps.cu"]
+           "mx_quantize.cu", "mx_matmul.cu", "preference.cu", "clip.cu", "token_logps.cu",
+           "adapter.cu", "adapter_f32.cu", "adapter_bf16.cu", "adapter_f16.cu"]
 # measurement helper used by bench.py, kept out of the table library
 PROBE_SOURCE = "access_probe.cu"
 PROBE_LIB = os.path.join(PKG, "libhkv_probe.so")

@@ -24,6 +24,7 @@ stream or the device has to change.
 from __future__ import annotations
 
 from array import array
+from ctypes import addressof
 from operator import attrgetter
 
 import torch
@@ -112,6 +113,8 @@ def _tensors(args):
             yield from (a._codes, a._scales) if a._base is None else a._base[:1]
         elif isinstance(a, PreferenceLoss):
             yield from (a.logits, a.labels, a._saved)
+        elif isinstance(a, AdapterMatmul):
+            yield from (t for t in (a.x, a.down, a.up, a.offsets, a.which, a.scales, a.hidden) if t is not None)
         elif isinstance(a, TokenLogps):
             yield from (t for t in (a.logits, a.labels, a.entropy, a._lse) if t is not None)
 
@@ -422,6 +425,124 @@ def _token_logps_backward(s, f, dlogps, dentropy, out):
     if given is not None:
         _written(given)
     return out
+
+
+class AdapterMatmul:
+    """What ``adapter_matmul`` returns: ``out`` [tokens, n] and the float32
+    ``hidden`` [tokens, rank], and what the backward call needs."""
+
+    __slots__ = ("out", "hidden", "x", "down", "up", "offsets", "which", "scales", "_adapters", "_shape")
+
+
+def adapter_matmul(x, down, up, offsets, which, scales=None, base=None, out=None, stream=None):
+    """Low-rank adapters of many requests beside a shared projection:
+    ``base + scale * (x @ down[a].t()) @ up[a].t()`` for the rows of each request, with
+    the request's adapter a.
+
+    ``x`` [tokens, k]; ``down`` [adapters, rank, k] and ``up`` [adapters, n, rank] of
+    its type, rank at most 64, each adapter's rows of adjacent columns (an adapter
+    may be a row of a larger tensor, as of a table's rows); request s has the rows
+    ``offsets[s]`` to ``offsets[s + 1]`` and the adapter ``which[s]`` (int64, on the
+    device; a value outside the adapters for a request without one); ``scales``
+    float32 [adapters]; ``base`` [tokens, n], the shared projection's result (None:
+    zeros), which may be ``out``.  Rows without an adapter are ``base``'s.  Returns an
+    ``AdapterMatmul``."""
+    return _call(_cuda(x, "x"), stream, _adapter_matmul, x, down, up, offsets, which, scales, base, out)
+
+
+def _thin(t, rows, cols, dtype, what, device):
+    """(step, row stride) of the matrices of one tensor."""
+    if t.dtype != dtype or t.dim() != 3 or t.shape[1:] != (rows, cols):
+        raise ValueError(f"{what}: adapters x {rows} x {cols} of {dtype}")
+    _same(t, device, what)
+    step, stride, one = t.stride()
+    if one != 1 and cols > 1:
+        raise ValueError(f"{what}: columns have to be adjacent (stride 1)")
+    if stride < cols:
+        if rows > 1:
+            raise ValueError(f"{what}: rows overlap")
+        stride = cols
+    return step, stride
+
+
+def _taken(t, rows, cols, dtype, what, device):
+    """The row stride of a given matrix of that shape and type."""
+    if t.dtype != dtype or t.shape != (rows, cols):
+        raise ValueError(f"{what}: {rows} x {cols} of {dtype}")
+    _same(t, device, what)
+    return _matrix(t, what)[2]
+
+
+def _adapter_matmul(s, x, down, up, offsets, which, scales, base, out):
+    device, dtype = x.device, x.dtype
+    kind = _type(x, "x")
+    tokens, k, x_stride = _matrix(x, "x")
+    if down.dim() != 3 or up.dim() != 3 or down.shape[0] != up.shape[0]:
+        raise ValueError("down, up: adapters x rank x k and adapters x n x rank")
+    count, rank = down.shape[:2]
+    n = up.shape[1]
+    if not 1 <= rank <= _abi.MAX_RANK or not k or not n:
+        raise ValueError(f"down: a rank of 1 to {_abi.MAX_RANK}, not {rank}, and k and n of at least 1")
+    down_step, down_stride = _thin(down, rank, k, dtype, "down", device)
+    up_step, up_stride = _thin(up, n, rank, dtype, "up", device)
+    requests = which.numel()
+    _vector(which, requests, torch.int64, "which", device)
+    _vector(offsets, requests + 1, torch.int64, "offsets", device)
+    if scales is not None:
+        _vector(scales, count, torch.float32, "scales", device)
+    base_stride = 0 if base is None else _taken(base, tokens, n, dtype, "base", device)
+    f = AdapterMatmul()
+    given = out
+    if out is None:
+        out = torch.empty((tokens, n), dtype=dtype, device=device)
+        stride = n
+    else:
+        stride = _taken(out, tokens, n, dtype, "out", device)
+    f.out, f.hidden = out, torch.empty((tokens, rank), dtype=torch.float32, device=device)
+    f.x, f.down, f.up, f.offsets, f.which, f.scales = x, down, up, offsets, which, scales
+    f._adapters = _abi.Adapters(count, down.data_ptr(), down_step, down_stride, up.data_ptr(), up_step,
+                                up_stride, None if scales is None else scales.data_ptr(), rank)
+    f._shape = tokens, k, n, kind, x_stride, requests
+    _ok(_abi.load().hkv_adapter_matmul(
+        tokens, k, n, kind, addressof(f._adapters), requests, offsets.data_ptr(), which.data_ptr(),
+        x.data_ptr(), x_stride, None if base is None else base.data_ptr(), base_stride, out.data_ptr(),
+        stride, f.hidden.data_ptr(), s), "hkv_adapter_matmul")
+    if given is not None:
+        _written(given)
+    return f
+
+
+def adapter_matmul_backward(f, dout, base=None, out=None, stream=None):
+    """The gradients of ``(dout * f.out).sum()``: (dx, ddown, dup), in the matrices'
+    type, from what ``adapter_matmul`` returned.  ``base`` [tokens, k] is added to dx
+    (the gradient through the shared projection), and may be ``out``, which takes dx."""
+    return _call(f.x.device, stream, _adapter_matmul_backward, f, dout, base, out)
+
+
+def _adapter_matmul_backward(s, f, dout, base, out):
+    x = f.x
+    device, dtype = x.device, x.dtype
+    tokens, k, n, kind, x_stride, requests = f._shape
+    count, rank = f._adapters.count, f._adapters.rank
+    d_stride = _taken(dout, tokens, n, dtype, "dout", device)
+    base_stride = 0 if base is None else _taken(base, tokens, k, dtype, "base", device)
+    given = out
+    if out is None:
+        out = torch.empty((tokens, k), dtype=dtype, device=device)
+        stride = k
+    else:
+        stride = _taken(out, tokens, k, dtype, "out", device)
+    ddown = torch.empty((count, rank, k), dtype=dtype, device=device)
+    dup = torch.empty((count, n, rank), dtype=dtype, device=device)
+    dhidden = torch.empty((tokens, rank), dtype=torch.float32, device=device)
+    _ok(_abi.load().hkv_adapter_matmul_backward(
+        tokens, k, n, kind, addressof(f._adapters), requests, f.offsets.data_ptr(), f.which.data_ptr(),
+        x.data_ptr(), x_stride, dout.data_ptr(), d_stride, f.hidden.data_ptr(),
+        None if base is None else base.data_ptr(), base_stride, out.data_ptr(), stride, ddown.data_ptr(),
+        dup.data_ptr(), dhidden.data_ptr(), s), "hkv_adapter_matmul_backward")
+    if given is not None:
+        _written(given)
+    return out, ddown, dup
 
 
 def _dense(t):

@@ -460,6 +460,61 @@ hkv_status hkv_token_logps_backward(uint64_t rows, uint64_t vocab, const void* l
                                     const float* entropy, const float* dlogps, const float* dentropy,
                                     void* dlogits, uint64_t dstride, void* stream);
 
+/* Low-rank adapters: `count` pairs of thin matrices of `type` (the call's),
+ * down (rank x k) and up (n x rank).  Adapter a's row r starts a * down_step +
+ * r * down_stride (up: up_step, up_stride) elements in, so that an adapter may
+ * be a row of a larger buffer, as of a table's rows.  scales (device) has a
+ * float32 factor for each adapter, NULL: 1.  1 <= rank <= HKV_MAX_RANK; strides
+ * are at most 2^31, steps at most 2^40. */
+#define HKV_MAX_RANK 64
+typedef struct hkv_adapters {
+  uint64_t count;
+  const void* down;
+  uint64_t down_step, down_stride;
+  const void* up;
+  uint64_t up_step, up_stride;
+  const float* scales;
+  uint32_t rank;
+} hkv_adapters;
+
+/* Adapters of many requests beside a shared projection.  Request s has the rows
+ * offsets[s] .. offsets[s + 1] - 1 of x (tokens x k) and of y (tokens x n), and
+ * the adapter which[s] (offsets, which: device, requests + 1 ascending values in
+ * 0 .. tokens, and requests values):
+ *   hidden[t] = down x[t]                          (float32, tokens x rank)
+ *   y[t]      = base[t] + scale * up hidden[t]
+ * with sums in float32 and y rounded once.  base (NULL: zeros) may be y itself,
+ * with the same stride.  Rows of no request, and of one whose which[s] lies
+ * outside 0 .. count - 1, have y[t] = base[t] and zeros in hidden; where y is
+ * base they are left as they are.  y must not overlap base otherwise, nor x
+ * (columns of one buffer side by side do not).  hidden (NULL where it is not
+ * wanted) is for the backward call.  The hidden numbers go on with 16 bits and
+ * more of their digits (24 for float32 matrices); a row with an infinity in it
+ * may give NaN where the formula gives an infinity.  `adapters` is read before
+ * the call returns. */
+hkv_status hkv_adapter_matmul(uint64_t tokens, uint64_t k, uint64_t n, int type,
+                              const hkv_adapters* adapters, uint64_t requests,
+                              const int64_t* offsets, const int64_t* which, const void* x,
+                              uint64_t x_stride, const void* base, uint64_t base_stride, void* y,
+                              uint64_t y_stride, float* hidden, void* stream);
+
+/* Its gradients, from dy (tokens x n) and the forward call's x and hidden:
+ *   dhidden[t] = scale * up^T dy[t]                (float32, tokens x rank)
+ *   dx[t]      = base[t] + down^T dhidden[t]       (base, tokens x k: as above)
+ *   ddown[a]   = sum over the rows t of a's requests of dhidden[t] x[t]^T
+ *   dup[a]     = scale * sum of dy[t] hidden[t]^T
+ * ddown (count x rank x k) and dup (count x n x rank) are contiguous, in the
+ * matrices' type, rounded once, and zero for an adapter of no request; either may
+ * be NULL.  dhidden is an output, or scratch, of the caller's.  dx must not
+ * overlap x or dy, nor base unless it is base. */
+hkv_status hkv_adapter_matmul_backward(uint64_t tokens, uint64_t k, uint64_t n, int type,
+                                       const hkv_adapters* adapters, uint64_t requests,
+                                       const int64_t* offsets, const int64_t* which, const void* x,
+                                       uint64_t x_stride, const void* dy, uint64_t dy_stride,
+                                       const float* hidden, const void* base, uint64_t base_stride,
+                                       void* dx, uint64_t dx_stride, void* ddown, void* dup,
+                                       float* dhidden, void* stream);
+
 /* One gradient: n elements of `type` at `data`.  Where `out` is not NULL the
  * clipped gradient is written there as `out_type`; it may be `data` itself
  * with the same type, and must not overlap it otherwise, nor another gradient
