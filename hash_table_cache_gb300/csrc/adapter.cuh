@@ -798,7 +798,7 @@ template <class A>
 cudaError_t launch_clusters(void (*kernel)(A), const A& args, uint64_t blocks, uint32_t parts, int smem,
                             cudaStream_t st) {
   if (blocks > 0x7FFFFFFFull) return cudaErrorInvalidValue;
-  if (smem > 48 * 1024) {
+  if (smem > 40 * 1024) {  // static shared memory counts too
     const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
     if (e != cudaSuccess) return e;
   }
