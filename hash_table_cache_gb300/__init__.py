@@ -98,6 +98,11 @@ class Grad(ctypes.Structure):
                 ("type", ctypes.c_int32), ("out_type", ctypes.c_int32)]
 
 
+def adapter_hidden_bytes(tokens, rank, type):
+    """HKV_ADAPTER_HIDDEN_BYTES."""
+    return tokens * (16 if rank <= 16 else 32 if rank <= 32 else 64) * (6 if type == HKV_F32 else 4)
+
+
 class Adapters(ctypes.Structure):
     _fields_ = [("count", ctypes.c_uint64),
                 ("down", ctypes.c_void_p), ("down_step", ctypes.c_uint64), ("down_stride", ctypes.c_uint64),
@@ -322,7 +327,7 @@ def hkv_clip_grad_norm(count, grads, max_norm, norm_out, work, stream=None):
 
 
 def hkv_adapter_matmul(tokens, k, n, type, adapters, requests, offsets, which, x, x_stride, base,
-                       base_stride, y, y_stride, hidden=None, stream=None):
+                       base_stride, y, y_stride, hidden, stream=None):
     """`adapters`: an Adapters, by reference (ctypes.byref) or address."""
     return load().hkv_adapter_matmul(tokens, k, n, type, adapters, requests, _p(offsets), _p(which),
                                      _p(x), x_stride, _p(base), base_stride, _p(y), y_stride,

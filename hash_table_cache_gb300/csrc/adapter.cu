@@ -53,9 +53,9 @@ Factor<T> factor(const void* p, uint64_t step, uint64_t stride) {
           aligned(p, 16) && step * sizeof(T) % 16 == 0 && stride * sizeof(T) % 16 == 0};
 }
 
-// y = base + second (scaled) (first x), or the same the other way through the adapters.
+// y = base + c second (first x), or the same the other way through the adapters.
 cudaError_t run(bool back, int type, const Requests& q, const hkv_adapters& w, const Matrix& x,
-                const Matrix& base, const Matrix& y, float* hidden, cudaStream_t st) {
+                const Matrix& base, const Matrix& y, void* hidden, cudaStream_t st) {
   return with_type(type, [&](auto* t) {
     using T = std::remove_pointer_t<decltype(t)>;
     const Factor<T> down = factor<T>(w.down, w.down_step, w.down_stride);
@@ -73,7 +73,7 @@ cudaError_t run(bool back, int type, const Requests& q, const hkv_adapters& w, c
     c.base_stride = base.stride;
     c.y = static_cast<T*>(const_cast<void*>(y.p));
     c.y_stride = y.stride;
-    c.hidden = hidden;
+    c.hidden = static_cast<__nv_bfloat16*>(hidden);
     c.x_whole = whole(x);
     c.base_whole = whole(base);
     c.y_whole = whole(y);
@@ -90,7 +90,7 @@ hkv_status hkv_adapter_matmul(uint64_t tokens, uint64_t k, uint64_t n, int type,
                               const hkv_adapters* adapters, uint64_t requests,
                               const int64_t* offsets, const int64_t* which, const void* x,
                               uint64_t x_stride, const void* base, uint64_t base_stride, void* y,
-                              uint64_t y_stride, float* hidden, void* stream) {
+                              uint64_t y_stride, void* hidden, void* stream) {
   using namespace hkv;
   if (!type_ok(type) || k < 1 || n < 1 || k > HKV_MAX_BATCH || n > HKV_MAX_BATCH) return HKV_ERR_INVALID;
   if (!requests_ok(tokens, requests, offsets, which) || !adapters_ok(adapters, k, n, type))
@@ -98,7 +98,8 @@ hkv_status hkv_adapter_matmul(uint64_t tokens, uint64_t k, uint64_t n, int type,
   const size_t size = type_size(type);
   const Matrix mx{x, tokens, k, x_stride, size}, my{y, tokens, n, y_stride, size};
   const Matrix mb{base, base ? tokens : 0, n, base ? base_stride : n, size};
-  if (!matrix_ok(mx) || !matrix_ok(my) || !matrix_ok(mb) || !aligned(hidden, 4)) return HKV_ERR_INVALID;
+  if (!matrix_ok(mx) || !matrix_ok(my) || !matrix_ok(mb)) return HKV_ERR_INVALID;
+  if ((tokens && !hidden) || !aligned(hidden, 16)) return HKV_ERR_INVALID;
   if (meet(my, mx) || (meet(my, mb) && !same(my, mb))) return HKV_ERR_INVALID;
   if (tokens == 0) return HKV_OK;
   const Requests q{tokens, requests, adapters->count, offsets, which, adapters->scales};
@@ -109,9 +110,9 @@ hkv_status hkv_adapter_matmul_backward(uint64_t tokens, uint64_t k, uint64_t n, 
                                        const hkv_adapters* adapters, uint64_t requests,
                                        const int64_t* offsets, const int64_t* which, const void* x,
                                        uint64_t x_stride, const void* dy, uint64_t dy_stride,
-                                       const float* hidden, const void* base, uint64_t base_stride,
+                                       const void* hidden, const void* base, uint64_t base_stride,
                                        void* dx, uint64_t dx_stride, void* ddown, void* dup,
-                                       float* dhidden, void* stream) {
+                                       void* dhidden, void* stream) {
   using namespace hkv;
   if (!type_ok(type) || k < 1 || n < 1 || k > HKV_MAX_BATCH || n > HKV_MAX_BATCH) return HKV_ERR_INVALID;
   if (!requests_ok(tokens, requests, offsets, which) || !adapters_ok(adapters, k, n, type))
@@ -122,7 +123,7 @@ hkv_status hkv_adapter_matmul_backward(uint64_t tokens, uint64_t k, uint64_t n, 
   const Matrix mb{base, base ? tokens : 0, k, base ? base_stride : k, size};
   if (!matrix_ok(mx) || !matrix_ok(md) || !matrix_ok(mdx) || !matrix_ok(mb)) return HKV_ERR_INVALID;
   if (tokens && (!hidden || !dhidden)) return HKV_ERR_INVALID;
-  if (!aligned(hidden, 4) || !aligned(dhidden, 4) || !aligned(ddown, size) || !aligned(dup, size))
+  if (!aligned(hidden, 16) || !aligned(dhidden, 16) || !aligned(ddown, size) || !aligned(dup, size))
     return HKV_ERR_INVALID;
   if (meet(mdx, mx) || meet(mdx, md) || (meet(mdx, mb) && !same(mdx, mb))) return HKV_ERR_INVALID;
   cudaStream_t st = static_cast<cudaStream_t>(stream);
@@ -141,8 +142,8 @@ hkv_status hkv_adapter_matmul_backward(uint64_t tokens, uint64_t k, uint64_t n, 
       g.m[1] = static_cast<const T*>(dy);
       g.stride[0] = x_stride;
       g.stride[1] = dy_stride;
-      g.p[0] = dhidden;
-      g.p[1] = hidden;
+      g.p[0] = static_cast<const __nv_bfloat16*>(dhidden);
+      g.p[1] = static_cast<const __nv_bfloat16*>(hidden);
       g.out[0] = static_cast<T*>(ddown);
       g.out[1] = static_cast<T*>(dup);
       g.whole[0] = whole(mx);

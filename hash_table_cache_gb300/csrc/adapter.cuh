@@ -4,24 +4,25 @@
 // A request s is the rows offsets[s] .. offsets[s + 1] - 1 of the batch and has
 // the adapter a = which[s], two thin matrices D (rank x k) and U (n x rank) and a
 // scale c:
-//   h = D x,  y = base + c U h            dh = c U^T dy,  dx = base + D^T dh
-//   dD = sum_t dh_t x_t^T                 dU = sum_t c dy_t h_t^T
-// Both chains are one kernel: a tile of rows of one request is multiplied by the
-// first factor along its whole length, which the blocks of a cluster share and
-// join through distributed shared memory in a fixed order, and the tile's rank
-// numbers a row, which never leave the SM, go through the second factor, whose
-// columns the same blocks share.
+//   h = c D x,  y = base + U h            dh = c U^T dy,  dx = base + D^T dh
+//   dD = sum_t dh_t x_t^T                 dU = sum_t dy_t h_t^T
+// Three kernels: the first product (x or dy with the first factor, its columns
+// shared by a cluster's blocks, whose sums meet in distributed shared memory in a
+// fixed order), the second product (onto base; it starts while the first one ends
+// and has its factor and base on their way by then), and the adapters' gradients.
 //
 // The products are thin: 2 rank operations for each element that is read or
-// written, 16 to 128 where the tensor cores could take 280 and more, so memory is
-// the bound and mma.sync, which takes ragged tiles, either order of either factor
+// written, 16 to 64 where the tensor cores could take 280 and more, so memory is
+// the bound, and mma.sync, which takes ragged tiles, either order of either factor
 // and sums in registers, is enough.  It multiplies bfloat16 (float16 in the first
 // product of float16 matrices); what has more digits is split into two or three
 // bfloat16 numbers (planes), whose products are added in float32:
 //   float32 = three planes exactly, products of planes i + j <= 2 (what is left
-//   out is below 2^-23 of a term); float16 = two planes exactly; the float32 h and
-//   dh in two planes where matrices have 16 bits (2^-16 of it is left out, where
-//   the result is rounded to 2^-8 or 2^-11), in three where they have 32.
+//   out is below 2^-22 of a term); float16 = two planes exactly; h and dh, sums in
+//   float32, in two planes where matrices have 16 bits (below 2^-16 of it is left
+//   out, where a result is rounded to 2^-8 or 2^-11), in three where they have 32.
+// Tiles come by asynchronous copies as they lie in memory, and are split on the
+// way to the tensor core.
 #pragma once
 
 #include <type_traits>
@@ -33,19 +34,17 @@ namespace hkv {
 constexpr int kAdapterThreads = 256;
 constexpr int kAdapterParts = 8;  // blocks of a cluster at most
 
-// Planes of the first product's operands, of the second factor, and of h.
+// Planes of the first product's operands, of a matrix that meets h or dh, and of
+// these.
 template <class T>
 struct Planes {
   static constexpr int kIn = sizeof(T) == 4 ? 3 : 1;
   static constexpr int kW = sizeof(T) == 4 ? 3 : std::is_same_v<T, __half> ? 2 : 1;
   static constexpr int kP = sizeof(T) == 4 ? 3 : 2;
-  // Whether the product of planes i and j is taken.
-  static __device__ __forceinline__ constexpr bool takes(int i, int j) {
-    return sizeof(T) != 4 || i + j <= 2;
-  }
 };
 
-// What the requests are, as the kernels take it.
+// What the requests are, as the kernels take it.  (Read past L1: the second
+// product's kernel reads before it has waited.)
 struct Requests {
   uint64_t tokens, requests, adapters;
   const int64_t *offsets, *which;
@@ -56,12 +55,12 @@ struct Requests {
     if (s == 0) return 0;
     if (s > requests + 1) return tokens;
     if (!offsets) return 0;
-    const int64_t v = offsets[s - 1];
+    const int64_t v = __ldcg(reinterpret_cast<const long long*>(offsets) + (s - 1));
     return v <= 0 ? 0 : min(static_cast<uint64_t>(v), tokens);
   }
   __device__ __forceinline__ int64_t adapter(uint64_t s) const {
     if (s == 0 || s > requests) return -1;
-    const int64_t a = which[s - 1];
+    const int64_t a = __ldcg(reinterpret_cast<const long long*>(which) + (s - 1));
     return a >= 0 && static_cast<uint64_t>(a) < adapters ? a : -1;
   }
 };
@@ -86,43 +85,54 @@ inline uint64_t slots_of(uint64_t tokens, uint64_t requests, int tile) {
   return tokens / tile + requests + 2;
 }
 
-// Eight neighbouring elements as they lie in memory, the first `n` of them.
+// ---------------------------------------------------------------------------
+// tiles
+// ---------------------------------------------------------------------------
+// Eight neighbouring elements into shared memory, the first n of them and zeros
+// behind (none for n <= 0): asynchronous where 16 bytes lie on a boundary (`whole`).
+__device__ __forceinline__ void copy_16(uint32_t to, const void* from, int bytes) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(to), "l"(from), "r"(bytes) : "memory");
+}
 template <class T>
-struct Raw {
-  static constexpr int kVecs = sizeof(T) / 2;
-  uint4 v[kVecs];
-  // kWritten: of memory that the kernel may also write (by the same thread, later).
-  template <bool kWritten = false>
-  __device__ __forceinline__ void load(const T* p, int64_t n, bool whole) {
-    if (n >= 8 && whole) {
+__device__ __forceinline__ void copy_eight(T* to, const T* from, int64_t n, bool whole) {
+  constexpr int kVecs = sizeof(T) / 2, kPer = 16 / sizeof(T);
+  if (whole) {
+    const int have = n <= 0 ? 0 : n >= 8 ? 8 : static_cast<int>(n);
 #pragma unroll
-      for (int i = 0; i < kVecs; ++i)
-        if constexpr (kWritten)
-          asm volatile("ld.global.L1::no_allocate.v4.u32 {%0,%1,%2,%3}, [%4];"
-                       : "=r"(v[i].x), "=r"(v[i].y), "=r"(v[i].z), "=r"(v[i].w)
-                       : "l"(p + i * (16 / sizeof(T)))
-                       : "memory");
-        else
-          v[i] = ld_nc_v4(p + i * (16 / sizeof(T)));
-    } else {
-      T* e = reinterpret_cast<T*>(v);
-#pragma unroll
-      for (int i = 0; i < 8; ++i) e[i] = i < n ? p[i] : from_f32<T>(0.f);
+    for (int i = 0; i < kVecs; ++i) {
+      const int left = min(max(have - i * kPer, 0), kPer);
+      copy_16(smem_u32(to + i * kPer), from + i * kPer, left * static_cast<int>(sizeof(T)));
     }
-  }
-  __device__ __forceinline__ void store(T* p, int64_t n, bool whole) const {
-    if (n >= 8 && whole) {
+  } else {
+    uint4 v[kVecs];
+    T* e = reinterpret_cast<T*>(v);
 #pragma unroll
-      for (int i = 0; i < kVecs; ++i) st_stream_v4(p + i * (16 / sizeof(T)), v[i]);
-    } else {
-      const T* e = reinterpret_cast<const T*>(v);
+    for (int i = 0; i < 8; ++i) e[i] = i < n ? __ldcg(from + i) : from_f32<T>(0.f);
 #pragma unroll
-      for (int i = 0; i < 8; ++i)
-        if (i < n) p[i] = e[i];
-    }
+    for (int i = 0; i < kVecs; ++i) reinterpret_cast<uint4*>(to)[i] = v[i];
   }
-  __device__ __forceinline__ float at(int i) const { return to_f32(reinterpret_cast<const T*>(v)[i]); }
-};
+}
+__device__ __forceinline__ void copies_end() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int kLeft>
+__device__ __forceinline__ void copies_wait() {
+  asm volatile("cp.async.wait_group %0;" ::"n"(kLeft) : "memory");
+}
+
+// kRows x kCols elements into a tile of that pitch by all threads: row r of the
+// matrix is at data + r * stride, `rows` rows and `cols` columns of it are there.
+template <class T, int kRows, int kCols, int kPitch>
+__device__ __forceinline__ void copy_tile(T* tile, const T* data, uint64_t stride, int64_t rows, int64_t cols,
+                                          bool whole) {
+  constexpr int kChunks = kRows * kCols / 8;
+#pragma unroll
+  for (int i = 0; i < (kChunks + kAdapterThreads - 1) / kAdapterThreads; ++i) {
+    const int at = threadIdx.x + i * kAdapterThreads;
+    if (kChunks % kAdapterThreads && at >= kChunks) break;
+    const int row = at / (kCols / 8), col = at % (kCols / 8) * 8;
+    const bool there = row < rows && col < cols;
+    copy_eight(tile + row * kPitch + col, there ? data + row * stride + col : data, there ? cols - col : 0, whole);
+  }
+}
 
 // Two floats as kN planes of two bfloat16 each: all but the last cut off, which
 // leaves an exact rest, the last rounded.
@@ -136,22 +146,6 @@ __device__ __forceinline__ void split_pair(float a, float b, uint32_t (&out)[kN]
   }
   const __nv_bfloat162 r = __floats2bfloat162_rn(a, b);
   out[kN - 1] = *reinterpret_cast<const uint32_t*>(&r);
-}
-// Eight elements as planes of eight; one plane is the 16-bit elements as they are.
-template <class T, int kN>
-__device__ __forceinline__ void split(const Raw<T>& r, uint4 (&out)[kN]) {
-  if constexpr (kN == 1) {
-    out[0] = r.v[0];
-  } else {
-    uint32_t* w = reinterpret_cast<uint32_t*>(out);
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      uint32_t pair[kN];
-      split_pair<kN>(r.at(2 * i), r.at(2 * i + 1), pair);
-#pragma unroll
-      for (int p = 0; p < kN; ++p) w[4 * p + i] = pair[p];
-    }
-  }
 }
 
 __device__ __forceinline__ void ldsm(uint32_t (&r)[4], uint32_t addr) {
@@ -173,25 +167,92 @@ __device__ __forceinline__ void mma(float (&d)[4], const uint32_t (&a)[4], uint3
                  : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
                  : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
 }
+
+// The planes of a 16 x 16 piece of a tile as the tensor core's first operand: rows
+// row .. row + 15, columns k .. k + 15.
+template <class T, int kN, int kPitch>
+__device__ __forceinline__ void rows_operand(uint32_t (&a)[kN][4], const T* tile, int row, int k) {
+  const int lane = threadIdx.x & 31;
+  if constexpr (sizeof(T) == 2) {
+    static_assert(kN == 1);
+    ldsm(a[0], smem_u32(tile + (row + lane % 16) * kPitch + k + lane / 16 * 8));
+  } else {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const float2 v = *reinterpret_cast<const float2*>(tile + (row + lane / 4 + i % 2 * 8) * kPitch + k + lane % 4 * 2 + i / 2 * 8);
+      uint32_t p[kN];
+      split_pair<kN>(v.x, v.y, p);
+#pragma unroll
+      for (int j = 0; j < kN; ++j) a[j][i] = p[j];
+    }
+  }
+}
+// And as its second operand, for 16 columns n .. n + 15 of the product ([0], [1] for
+// the first eight): the tile holds them as rows, or, with kT, as columns.
+template <class T, int kN, int kPitch, bool kT>
+__device__ __forceinline__ void cols_operand(uint32_t (&b)[kN][4], const T* tile, int n, int k) {
+  const int lane = threadIdx.x & 31;
+  if constexpr (sizeof(T) == 2) {
+    uint32_t r[4];
+    if constexpr (kT) ldsm_t(r, smem_u32(tile + (k + lane % 16) * kPitch + n + lane / 16 * 8));
+    else ldsm(r, smem_u32(tile + (n + lane % 8 + lane / 16 * 8) * kPitch + k + lane / 8 % 2 * 8));
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      if constexpr (kN == 1) {
+        b[0][i] = r[i];
+      } else {  // float16 in two planes
+        const float2 v = __half22float2(*reinterpret_cast<const __half2*>(&r[i]));
+        uint32_t p[kN];
+        split_pair<kN>(v.x, v.y, p);
+#pragma unroll
+        for (int j = 0; j < kN; ++j) b[j][i] = p[j];
+      }
+    }
+  } else {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const int col = n + i / 2 * 8 + lane / 4, row = k + i % 2 * 8 + lane % 4 * 2;
+      float2 v;
+      if constexpr (kT) v = make_float2(tile[row * kPitch + col], tile[(row + 1) * kPitch + col]);
+      else v = *reinterpret_cast<const float2*>(tile + col * kPitch + row);
+      uint32_t p[kN];
+      split_pair<kN>(v.x, v.y, p);
+#pragma unroll
+      for (int j = 0; j < kN; ++j) b[j][i] = p[j];
+    }
+  }
+}
+
+// A 16 x 8 piece of a product.  The tensor core cuts what it adds up, so float32
+// matrices keep the large terms in short chains of their own (`high`), the products
+// with lower planes, 2^-8 of them, in another, and join both by rounding additions.
+template <class T>
+struct Sum {
+  float high[4] = {}, low[4] = {};
+  template <int kA, int kB, bool kF16 = false>
+  __device__ __forceinline__ void add(const uint32_t (&a)[kA][4], const uint32_t (&b)[kB][4], int half) {
+#pragma unroll
+    for (int i = 0; i < kA; ++i)
+#pragma unroll
+      for (int j = 0; j < kB; ++j) {
+        if (sizeof(T) == 4 && i + j > 2) continue;
+        mma<kF16>(sizeof(T) == 4 && i + j > 0 ? low : high, a[i], b[j][half * 2], b[j][half * 2 + 1]);
+      }
+  }
+  __device__ __forceinline__ float at(int i) const { return sizeof(T) == 4 ? high[i] + low[i] : high[i]; }
+};
+
 // The cluster's barrier, for warps whose threads may have parted.
 __device__ __forceinline__ void cluster_meet() {
   __syncwarp();
   cluster_sync();
-}
-__device__ __forceinline__ void cluster_arrive() {
-  __syncwarp();
-  asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
-}
-__device__ __forceinline__ void cluster_wait() {
-  __syncwarp();
-  asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
 }
 __device__ __forceinline__ float4 operator+(float4 a, float4 b) {
   return make_float4(a.x + b.x, a.y + b.y, a.z + b.z, a.w + b.w);
 }
 
 // A factor of the adapters: adapter a's row r starts a * step + r * stride
-// elements in.  whole: rows of eight elements may be taken by 16-byte loads.
+// elements in.  whole: eight elements of a row may be taken by 16-byte copies.
 template <class T>
 struct Factor {
   const T* data;
@@ -211,369 +272,293 @@ struct Chain {
   uint64_t base_stride;
   T* y;
   uint64_t y_stride;
-  float* hidden;     // tokens x rank, or null
-  uint32_t parts, groups;  // blocks of a cluster, and clusters that share a tile's columns
-  uint64_t part_in, part_out;  // columns of x to a block, columns of y to a block
+  __nv_bfloat16* hidden;  // tokens x planes x kRank, c h or dh
+  uint32_t parts;         // first product: blocks of a cluster
+  uint64_t part_in;       //   and columns of x to each
+  uint32_t groups;        // second product: blocks of a tile of rows
+  uint64_t group_out;     //   and columns of y to each
   bool x_whole, base_whole, y_whole;
+  bool follows;           // the second product comes after a first one
 };
 
-// Shared memory of a chain, in bytes.
+// The rows of a block's tile: false where the slot has none.
+struct Tile {
+  uint64_t row0;
+  int rows;
+  int64_t adapter;
+  template <int kTile>
+  __device__ __forceinline__ static bool find(const Requests& q, uint64_t slot, Tile& t) {
+    const uint64_t seg = find_segment<kTile>(q, slot);
+    const uint64_t start = q.start(seg), end = q.start(seg + 1);
+    t.adapter = q.adapter(seg);
+    t.row0 = start + (slot - (start / kTile + seg)) * kTile;
+    if (t.row0 >= end) return false;
+    t.rows = static_cast<int>(min(end - t.row0, static_cast<uint64_t>(kTile)));
+    return true;
+  }
+};
+
+// ---------------------------------------------------------------------------
+// the first product
+// ---------------------------------------------------------------------------
 template <class T, int kRank, int kTile, bool kBack>
-struct ChainShape {
-  using P = Planes<T>;
-  static constexpr int kRowWarps = kTile / 16, kOther = 8 / kRowWarps;
-  static constexpr int kStep = kTile == 64 ? 64 : 128;   // columns of x to a stage
-  static constexpr int kCols = kOther * (kTile == 64 ? 64 : 32);  // columns of y to a step
-  static constexpr int kInPitch = kStep + 8, kRankPitch = kRank + 8, kColPitch = kCols + 8;
-  static constexpr int kX = P::kIn * kTile * kInPitch * 2;
-  static constexpr int kFirst = P::kIn * (kBack ? kStep * kRankPitch : kRank * kInPitch) * 2;
-  static constexpr int kStage = kX + kFirst;
-  static constexpr int kSecond = P::kW * (kBack ? kRank * kColPitch : kCols * kRankPitch) * 2;
-  static constexpr int kSums = kOther * kTile * kRank * 4;
-  static constexpr int most(int a, int b) { return a > b ? a : b; }
-  static constexpr int kWork = most(most(2 * kStage, 2 * kSecond), kSums);
-  // this block's part of the sums.  A few are read from all parts by every block;
-  // many are shared out first, and their planes take this part's place.
-  static constexpr bool kDirect = kTile * kRank <= 1024;
-  static constexpr int kOwn = kTile * kRank * 4;
-  static constexpr int kPlanes = P::kP * kTile * kRankPitch * 2;
-  static constexpr int kPlanesAt = kWork + (kDirect ? kOwn : 0);
-  static constexpr int kShareAt = kWork + most(kOwn, kPlanes);
-  static constexpr int kBytes = kDirect ? kPlanesAt + kPlanes : kShareAt + kOwn / 2;
+struct FirstShape {
+  static constexpr int kRowWarps = kTile / 16, kOther = 8 / kRowWarps;  // warps along rows, along columns of x
+  static constexpr int kStep = kTile == 64 ? 64 : 128;                  // columns of x to a stage
+  static constexpr int kStages = sizeof(T) == 4 ? 3 : 4;
+  static constexpr int kPitch = kStep + 8, kFirstPitch = kBack ? kRank + 8 : kPitch;
+  static constexpr int kX = kTile * kPitch, kFirst = (kBack ? kStep : kRank) * kFirstPitch;
+  static constexpr int kStage = kX + kFirst;  // elements
+  static constexpr int kSums = (kOther + 1) * kTile * kRank * 4;
+  static constexpr int kBytes = kStages * kStage * static_cast<int>(sizeof(T)) > kSums
+                                    ? kStages * kStage * static_cast<int>(sizeof(T)) : kSums;
 };
-
-// Where column c of 32 stands in shared memory, so that the tensor core's result
-// gives a thread eight neighbouring columns.
-__device__ __forceinline__ int place(int c) { return (c >> 1 & 3) * 8 + (c >> 3 & 3) * 2 + (c & 1); }
 
 template <class T, int kRank, int kTile, bool kBack>
 __global__ void __launch_bounds__(kAdapterThreads)
-    chain_kernel(const __grid_constant__ Chain<T> a) {
-  using S = ChainShape<T, kRank, kTile, kBack>;
+    first_kernel(const __grid_constant__ Chain<T> a) {
+  using S = FirstShape<T, kRank, kTile, kBack>;
   using P = Planes<T>;
-  constexpr int kThreads = kAdapterThreads;
-  constexpr bool kF16 = std::is_same_v<T, __half>;
-  constexpr int kXLoads = (kTile * S::kStep / 8 + kThreads - 1) / kThreads;
-  constexpr int kFirstChunks = kRank * S::kStep / 8, kFirstLoads = (kFirstChunks + kThreads - 1) / kThreads;
-  constexpr int kSecondChunks = kRank * S::kCols / 8, kSecondLoads = (kSecondChunks + kThreads - 1) / kThreads;
   extern __shared__ __align__(16) uint8_t smem[];
-  float* const sums = reinterpret_cast<float*>(smem);             // [other][tile][rank]
-  float* const own = reinterpret_cast<float*>(smem + S::kWork);   // [tile][rank]
-  float* const share = reinterpret_cast<float*>(smem + S::kShareAt);
-  uint8_t* const planes = smem + S::kPlanesAt;
+  T* const stages = reinterpret_cast<T*>(smem);
   const uint32_t tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const uint32_t row_warp = warp % S::kRowWarps, other = warp / S::kRowWarps;
-  pdl_trigger();
   pdl_wait();
+  pdl_trigger();  // what the second product reads before it waits is complete from here on
 
   const uint32_t part = blockIdx.x % a.parts;
-  const uint32_t group = blockIdx.x / a.parts % a.groups;
-  const uint64_t slot = blockIdx.x / a.parts / a.groups;
-  const uint64_t seg = find_segment<kTile>(a.q, slot);
-  const uint64_t seg_start = a.q.start(seg), seg_end = a.q.start(seg + 1);
-  const uint64_t row0 = seg_start + (slot - (seg_start / kTile + seg)) * kTile;
-  if (row0 >= seg_end) return;  // the cluster's other blocks as well
-  const int rows = static_cast<int>(min(seg_end - row0, static_cast<uint64_t>(kTile)));
-  const int64_t adapter = a.q.adapter(seg);
-  const uint64_t col0 = (static_cast<uint64_t>(group) * a.parts + part) * a.part_out;
-  const uint64_t col1 = min(col0 + a.part_out, a.out);
-
-  if (adapter < 0) {  // base as it is
-    if (a.hidden && group == 0 && part == 0)
-      for (uint64_t i = tid; i < rows * static_cast<uint64_t>(a.rank); i += kThreads) a.hidden[row0 * a.rank + i] = 0.f;
-    if (a.y == a.base || col0 >= col1) return;
-    const uint64_t eights = (col1 - col0 + 7) / 8;
-    for (uint64_t i = tid; i < rows * eights; i += kThreads) {
-      const uint64_t row = row0 + i / eights, col = col0 + i % eights * 8;
-      const int64_t n = col1 - col;
-      Raw<T> r;
-      r.template load<true>(a.base + row * a.base_stride + col, a.base ? n : 0, a.base_whole);
-      r.store(a.y + row * a.y_stride + col, n, a.y_whole);
-    }
-    return;
-  }
-  const T* const first = a.first.data + adapter * a.first.step;
-  const T* const second = a.second.data + adapter * a.second.step;
-  const float scale = a.q.scales ? a.q.scales[adapter] : 1.f;
-
-  // ---- the first product: this block's part of the columns of x
+  Tile t;
+  if (!Tile::find<kTile>(a.q, blockIdx.x / a.parts, t) || t.adapter < 0) return;  // the whole cluster
   const uint64_t in0 = min(part * a.part_in, a.in), in1 = min(in0 + a.part_in, a.in);
-  Raw<T> x_raw[kXLoads], first_raw[kFirstLoads], second_raw[kSecondLoads];
-  auto load_stage = [&](uint64_t k) {
-#pragma unroll
-    for (int i = 0; i < kXLoads; ++i) {
-      const int at = tid + i * kThreads, row = at / (S::kStep / 8);
-      const uint64_t col = k + at % (S::kStep / 8) * 8;
-      x_raw[i].load(a.x + (row0 + row) * a.x_stride + col, row < rows ? static_cast<int64_t>(in1 - col) : 0, a.x_whole);
-    }
-#pragma unroll
-    for (int i = 0; i < kFirstLoads; ++i) {
-      const int at = tid + i * kThreads;
-      if (kFirstChunks % kThreads && at >= kFirstChunks) break;
-      if constexpr (kBack) {
-        const uint64_t row = k + at / (kRank / 8);
-        const int col = at % (kRank / 8) * 8;
-        first_raw[i].load(first + row * a.first.stride + col, row < in1 ? static_cast<int64_t>(a.rank) - col : 0, a.first.whole);
-      } else {
-        const uint32_t row = at / (S::kStep / 8);
-        const uint64_t col = k + at % (S::kStep / 8) * 8;
-        first_raw[i].load(first + row * a.first.stride + col, row < a.rank ? static_cast<int64_t>(in1 - col) : 0, a.first.whole);
-      }
-    }
-  };
-  auto store_stage = [&](int buffer) {
-    uint8_t* const to = smem + buffer * S::kStage;
-#pragma unroll
-    for (int i = 0; i < kXLoads; ++i) {
-      const int at = tid + i * kThreads, row = at / (S::kStep / 8), col = at % (S::kStep / 8) * 8;
-      uint4 v[P::kIn];
-      split<T, P::kIn>(x_raw[i], v);
-#pragma unroll
-      for (int p = 0; p < P::kIn; ++p)
-        *reinterpret_cast<uint4*>(to + ((p * kTile + row) * S::kInPitch + col) * 2) = v[p];
-    }
-#pragma unroll
-    for (int i = 0; i < kFirstLoads; ++i) {
-      const int at = tid + i * kThreads;
-      if (kFirstChunks % kThreads && at >= kFirstChunks) break;
-      constexpr int kPer = (kBack ? kRank : S::kStep) / 8, kRows = kBack ? S::kStep : kRank;
-      constexpr int kPitch = kBack ? S::kRankPitch : S::kInPitch;
-      const int row = at / kPer, col = at % kPer * 8;
-      uint4 v[P::kIn];
-      split<T, P::kIn>(first_raw[i], v);
-#pragma unroll
-      for (int p = 0; p < P::kIn; ++p)
-        *reinterpret_cast<uint4*>(to + S::kX + ((p * kRows + row) * kPitch + col) * 2) = v[p];
-    }
-  };
-  // the second factor's first columns are on their way while the sums are joined
-  auto load_second = [&](uint64_t c) {
-#pragma unroll
-    for (int i = 0; i < kSecondLoads; ++i) {
-      const int at = tid + i * kThreads;
-      if (kSecondChunks % kThreads && at >= kSecondChunks) break;
-      if constexpr (kBack) {
-        const uint32_t row = at / (S::kCols / 8);
-        const uint64_t col = c + at % (S::kCols / 8) * 8;
-        second_raw[i].load(second + row * a.second.stride + col, row < a.rank ? static_cast<int64_t>(col1 - col) : 0, a.second.whole);
-      } else {
-        const uint64_t row = c + at / (kRank / 8);
-        const int col = at % (kRank / 8) * 8;
-        second_raw[i].load(second + row * a.second.stride + col, row < col1 ? static_cast<int64_t>(a.rank) - col : 0, a.second.whole);
-      }
-    }
-  };
-  auto store_second = [&](int buffer) {
-    uint8_t* const to = smem + buffer * S::kSecond;
-#pragma unroll
-    for (int i = 0; i < kSecondLoads; ++i) {
-      const int at = tid + i * kThreads;
-      if (kSecondChunks % kThreads && at >= kSecondChunks) break;
-      uint4 v[P::kW];
-      split<T, P::kW>(second_raw[i], v);
-      if constexpr (kBack) {
-        const int row = at / (S::kCols / 8), col = at % (S::kCols / 8) * 8;
-#pragma unroll
-        for (int p = 0; p < P::kW; ++p) {
-          uint8_t* const r = to + (p * kRank + row) * S::kColPitch * 2;
-          const uint32_t* const w = reinterpret_cast<const uint32_t*>(&v[p]);
-#pragma unroll
-          for (int j = 0; j < 4; ++j)
-            *reinterpret_cast<uint32_t*>(r + ((col & ~31) + place((col & 31) + 2 * j)) * 2) = w[j];
-        }
-      } else {
-        const int row = at / (kRank / 8), col = at % (kRank / 8) * 8;
-        const int placed = (row & ~31) + place(row & 31);
-#pragma unroll
-        for (int p = 0; p < P::kW; ++p)
-          *reinterpret_cast<uint4*>(to + ((p * S::kCols + placed) * S::kRankPitch + col) * 2) = v[p];
-      }
-    }
-  };
-
-  float acc[kRank / 8][4] = {};
+  const T* const x = a.x + t.row0 * a.x_stride;
+  const T* const first = a.first.data + t.adapter * a.first.step;
   const int steps = static_cast<int>((in1 - in0 + S::kStep - 1) / S::kStep);
-  if (steps) {
-    load_stage(in0);
-    store_stage(0);
-    __syncthreads();
-  }
+  auto load = [&](int step) {
+    if (step < steps) {
+      T* const to = stages + step % S::kStages * S::kStage;
+      const uint64_t k = in0 + static_cast<uint64_t>(step) * S::kStep;
+      const int64_t left = in1 - k;
+      copy_tile<T, kTile, S::kStep, S::kPitch>(to, x + k, a.x_stride, t.rows, left, a.x_whole);
+      if constexpr (kBack)
+        copy_tile<T, S::kStep, kRank, S::kFirstPitch>(to + S::kX, first + k * a.first.stride, a.first.stride, left, a.rank, a.first.whole);
+      else
+        copy_tile<T, kRank, S::kStep, S::kFirstPitch>(to + S::kX, first + k, a.first.stride, a.rank, left, a.first.whole);
+    }
+    copies_end();
+  };
+  float acc[kRank / 8][4] = {};
+#pragma unroll
+  for (int s = 0; s + 1 < S::kStages; ++s) load(s);
   for (int step = 0; step < steps; ++step) {
-    if (step + 1 < steps) load_stage(in0 + static_cast<uint64_t>(step + 1) * S::kStep);
-    const uint32_t xs = smem_u32(smem) + (step & 1) * S::kStage, ws = xs + S::kX;
-    // sums of 32 bits in the tensor core are cut, not rounded: short chains, added
-    // up by rounding additions, where the result has 32 bits
-    float chain[kRank / 8][4] = {};
-    constexpr bool kShort = sizeof(T) == 4;
+    copies_wait<S::kStages - 2>();
+    __syncthreads();
+    load(step + S::kStages - 1);
+    const T* const xs = stages + step % S::kStages * S::kStage;
+    const T* const ws = xs + S::kX;
     constexpr int kEach = S::kStep / 16 / S::kOther;
+    Sum<T> d[kRank / 8];
+    if constexpr (sizeof(T) == 2)
+#pragma unroll
+      for (int n = 0; n < kRank / 8; ++n)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) d[n].high[i] = acc[n][i];
 #pragma unroll
     for (int s = 0; s < kEach; ++s) {
       const int k = (other * kEach + s) * 16;
       uint32_t xa[P::kIn][4];
+      rows_operand<T, P::kIn, S::kPitch>(xa, xs, row_warp * 16, k);
 #pragma unroll
-      for (int p = 0; p < P::kIn; ++p)
-        ldsm(xa[p], xs + ((p * kTile + row_warp * 16 + lane % 16) * S::kInPitch + k + lane / 16 * 8) * 2);
-#pragma unroll
-      for (int n = 0; n < kRank / 16; ++n)
-#pragma unroll
-        for (int j = 0; j < P::kIn; ++j) {
-          uint32_t w[4];
-          if constexpr (kBack)
-            ldsm_t(w, ws + ((j * S::kStep + k + lane % 16) * S::kRankPitch + n * 16 + lane / 16 * 8) * 2);
-          else
-            ldsm(w, ws + ((j * kRank + n * 16 + lane % 8 + lane / 16 * 8) * S::kInPitch + k + lane / 8 % 2 * 8) * 2);
-#pragma unroll
-          for (int i = 0; i < P::kIn; ++i)
-            if (P::takes(i, j)) {
-              mma<kF16>(kShort ? chain[2 * n] : acc[2 * n], xa[i], w[0], w[1]);
-              mma<kF16>(kShort ? chain[2 * n + 1] : acc[2 * n + 1], xa[i], w[2], w[3]);
-            }
-        }
+      for (int n = 0; n < kRank / 16; ++n) {
+        uint32_t w[P::kIn][4];
+        cols_operand<T, P::kIn, S::kFirstPitch, kBack>(w, ws, n * 16, k);
+        d[2 * n].template add<P::kIn, P::kIn, std::is_same_v<T, __half>>(xa, w, 0);
+        d[2 * n + 1].template add<P::kIn, P::kIn, std::is_same_v<T, __half>>(xa, w, 1);
+      }
     }
-    if constexpr (kShort) {
 #pragma unroll
-      for (int n = 0; n < kRank / 8; ++n)
+    for (int n = 0; n < kRank / 8; ++n)
 #pragma unroll
-        for (int i = 0; i < 4; ++i) acc[n][i] += chain[n][i];
-    }
-    if (step + 1 < steps) store_stage((step + 1) & 1);
-    __syncthreads();
+      for (int i = 0; i < 4; ++i) acc[n][i] = sizeof(T) == 2 ? d[n].high[i] : acc[n][i] + d[n].at(i);
   }
-  const bool writes = col0 < col1;
-  if (writes) load_second(col0);
+  copies_wait<0>();
+  __syncthreads();
 
-  // ---- the warps' sums, then the blocks'
-  {
-    float* const to = sums + (other * kTile + row_warp * 16 + lane / 4) * kRank + lane % 4 * 2;
+  // the warps' sums, then the blocks', each block a share of them
+  float* const sums = reinterpret_cast<float*>(smem);  // [other][tile][rank]
+  float* const own = sums + S::kOther * kTile * kRank;
+  float* const to = sums + (other * kTile + row_warp * 16 + lane / 4) * kRank + lane % 4 * 2;
 #pragma unroll
-    for (int n = 0; n < kRank / 8; ++n) {
-      *reinterpret_cast<float2*>(to + n * 8) = make_float2(acc[n][0], acc[n][1]);
-      *reinterpret_cast<float2*>(to + 8 * kRank + n * 8) = make_float2(acc[n][2], acc[n][3]);
-    }
+  for (int n = 0; n < kRank / 8; ++n) {
+    *reinterpret_cast<float2*>(to + n * 8) = make_float2(acc[n][0], acc[n][1]);
+    *reinterpret_cast<float2*>(to + 8 * kRank + n * 8) = make_float2(acc[n][2], acc[n][3]);
   }
   __syncthreads();
   constexpr int kQuads = kTile * kRank / 4;
-  for (int i = tid; i < kQuads; i += kThreads) {
+  const float scale = a.q.scales ? a.q.scales[t.adapter] : 1.f;
+  auto block_sum = [&](int i) {
     float4 v = reinterpret_cast<const float4*>(sums)[i];
 #pragma unroll
     for (int o = 1; o < S::kOther; ++o) v = v + reinterpret_cast<const float4*>(sums)[o * kQuads + i];
-    reinterpret_cast<float4*>(own)[i] = v;
-  }
-  const uint32_t used = static_cast<uint32_t>((a.in + a.part_in - 1) / a.part_in);  // parts with columns
-  auto joined = [&](int i) {
-    float4 v = remote_f32x4(smem_u32(own) + i * 16, 0);
-    for (uint32_t p = 1; p < used; ++p) v = v + remote_f32x4(smem_u32(own) + i * 16, p);
     return v;
   };
-  auto put = [&](int i, float4 v, bool keeps) {
+  auto put = [&](int i, float4 v) {
     const int row = i * 4 / kRank, col = i * 4 % kRank;
-    float e[4] = {v.x, v.y, v.z, v.w};
-    if (kBack)
-#pragma unroll
-      for (int j = 0; j < 4; ++j) e[j] *= scale;
-    if (keeps && row < rows)
-#pragma unroll
-      for (int j = 0; j < 4; ++j)
-        if (col + j < static_cast<int>(a.rank)) a.hidden[(row0 + row) * a.rank + col + j] = e[j];
-    if (!kBack)
-#pragma unroll
-      for (int j = 0; j < 4; ++j) e[j] *= scale;
+    if (row >= t.rows) return;
     uint32_t lo[P::kP], hi[P::kP];
-    split_pair<P::kP>(e[0], e[1], lo);
-    split_pair<P::kP>(e[2], e[3], hi);
+    split_pair<P::kP>(v.x * scale, v.y * scale, lo);
+    split_pair<P::kP>(v.z * scale, v.w * scale, hi);
+    __nv_bfloat16* const h = a.hidden + (t.row0 + row) * (P::kP * kRank) + col;
 #pragma unroll
-    for (int p = 0; p < P::kP; ++p)
-      *reinterpret_cast<uint2*>(planes + ((p * kTile + row) * S::kRankPitch + col) * 2) = make_uint2(lo[p], hi[p]);
+    for (int p = 0; p < P::kP; ++p) *reinterpret_cast<uint2*>(h + p * kRank) = make_uint2(lo[p], hi[p]);
   };
-  const bool keeps = a.hidden && group == 0;
-  constexpr int kPuts = (kQuads + kThreads - 1) / kThreads;
   if (a.parts == 1) {
-    float4 v[kPuts];  // out of the planes' way
-    __syncthreads();
-#pragma unroll
-    for (int j = 0; j < kPuts; ++j)
-      if (kQuads % kThreads == 0 || tid + j * kThreads < kQuads) v[j] = reinterpret_cast<const float4*>(own)[tid + j * kThreads];
-    __syncthreads();
-#pragma unroll
-    for (int j = 0; j < kPuts; ++j)
-      if (kQuads % kThreads == 0 || tid + j * kThreads < kQuads) put(tid + j * kThreads, v[j], keeps);
-  } else if constexpr (S::kDirect) {
-    cluster_meet();
-    for (int i = tid; i < kQuads; i += kThreads) put(i, joined(i), keeps && part == 0);
-    cluster_arrive();
-  } else {
-    cluster_meet();
-    const int each = kQuads / a.parts;
-    for (int i = tid; i < each; i += kThreads) reinterpret_cast<float4*>(share)[i] = joined(part * each + i);
-    cluster_meet();
-    for (int i = tid; i < kQuads; i += kThreads)
-      put(i, remote_f32x4(smem_u32(share) + i % each * 16, i / each), keeps && part == static_cast<uint32_t>(i / each));
-    cluster_arrive();
+    for (int i = tid; i < kQuads; i += kAdapterThreads) put(i, block_sum(i));
+    return;
   }
-  // (the work space has been read: the barriers above)
-  // ---- the second product: this block's columns of y
-  const int col_steps = writes ? static_cast<int>((col1 - col0 + S::kCols - 1) / S::kCols) : 0;
-  if (col_steps) store_second(0);
-  __syncthreads();
-  constexpr int kSets = S::kCols / 32 / S::kOther;  // of 32 columns, to a warp
-  const uint32_t quad = lane % 4;
-  for (int step = 0; step < col_steps; ++step) {
-    const uint64_t c0 = col0 + static_cast<uint64_t>(step) * S::kCols;
-    Raw<T> base[kSets][2];
-#pragma unroll
-    for (int set = 0; set < kSets; ++set)
-#pragma unroll
-      for (int half = 0; half < 2; ++half) {
-        const int row = row_warp * 16 + lane / 4 + half * 8;
-        const uint64_t col = c0 + (other * kSets + set) * 32 + quad * 8;
-        base[set][half].template load<true>(a.base + (row0 + row) * a.base_stride + col,
-                                            a.base && row < rows ? static_cast<int64_t>(col1 - col) : 0, a.base_whole);
-      }
-    if (step + 1 < col_steps) load_second(c0 + S::kCols);
-    const uint32_t ps = smem_u32(planes), ws = smem_u32(smem) + (step & 1) * S::kSecond;
-#pragma unroll
-    for (int set = 0; set < kSets; ++set) {
-      const int c = (other * kSets + set) * 32;
-      float d[4][4] = {};
-#pragma unroll
-      for (int k = 0; k < kRank; k += 16) {
-        uint32_t h[P::kP][4];
-#pragma unroll
-        for (int p = 0; p < P::kP; ++p)
-          ldsm(h[p], ps + ((p * kTile + row_warp * 16 + lane % 16) * S::kRankPitch + k + lane / 16 * 8) * 2);
-#pragma unroll
-        for (int n = 0; n < 2; ++n)
-#pragma unroll
-          for (int j = 0; j < P::kW; ++j) {
-            uint32_t w[4];
-            if constexpr (kBack)
-              ldsm_t(w, ws + ((j * kRank + k + lane % 16) * S::kColPitch + c + n * 16 + lane / 16 * 8) * 2);
-            else
-              ldsm(w, ws + ((j * S::kCols + c + n * 16 + lane % 8 + lane / 16 * 8) * S::kRankPitch + k + lane / 8 % 2 * 8) * 2);
-#pragma unroll
-            for (int i = 0; i < P::kP; ++i)
-              if (P::takes(i, j)) {
-                mma<false>(d[2 * n], h[i], w[0], w[1]);
-                mma<false>(d[2 * n + 1], h[i], w[2], w[3]);
-              }
-          }
-      }
-#pragma unroll
-      for (int half = 0; half < 2; ++half) {
-        const int row = row_warp * 16 + lane / 4 + half * 8;
-        const uint64_t col = c0 + c + quad * 8;
-        const int64_t n = row < rows ? static_cast<int64_t>(col1 - col) : 0;
-        Raw<T> r;
-        T* const e = reinterpret_cast<T*>(r.v);
-#pragma unroll
-        for (int j = 0; j < 8; ++j) e[j] = from_f32<T>(base[set][half].at(j) + d[j / 2][half * 2 + j % 2]);
-        r.store(a.y + (row0 + row) * a.y_stride + col, n, a.y_whole);
+  for (int i = tid; i < kQuads; i += kAdapterThreads) reinterpret_cast<float4*>(own)[i] = block_sum(i);
+  cluster_meet();
+  const uint32_t used = static_cast<uint32_t>((a.in + a.part_in - 1) / a.part_in);  // parts with columns
+  const int each = kQuads / a.parts;
+  for (int e = tid; e < each; e += kAdapterThreads) {
+    const int i = part * each + e;
+    float4 v = remote_f32x4(smem_u32(own) + i * 16, 0);
+    for (uint32_t p = 1; p < used; ++p) v = v + remote_f32x4(smem_u32(own) + i * 16, p);
+    put(i, v);
+  }
+  cluster_meet();  // the others stay until their sums are read
+}
+
+// ---------------------------------------------------------------------------
+// the second product
+// ---------------------------------------------------------------------------
+template <class T, int kRank, int kTile, bool kBack>
+struct SecondShape {
+  static constexpr int kRowWarps = kTile / 16, kOther = 8 / kRowWarps;
+  static constexpr int kWarpCols = kTile == 64 ? (sizeof(T) == 4 ? 32 : 64) : (sizeof(T) == 4 ? 16 : 32);
+  static constexpr int kCols = kOther * kWarpCols;  // columns of y to a stage
+  static constexpr int kStages = sizeof(T) == 4 || kRank == 64 ? 2 : 3;
+  static constexpr int kPitch = kCols + 8, kSecondPitch = kBack ? kPitch : kRank + 8, kHiddenPitch = kRank + 8;
+  static constexpr int kBase = kTile * kPitch, kSecond = (kBack ? kRank : kCols) * kSecondPitch;
+  static constexpr int kStage = kBase + kSecond;  // elements
+  static constexpr int kHidden = Planes<T>::kP * kTile * kHiddenPitch * 2;
+  static constexpr int kBytes = kStages * kStage * static_cast<int>(sizeof(T)) + kHidden;
+};
+
+template <class T, int kRank, int kTile, bool kBack>
+__global__ void __launch_bounds__(kAdapterThreads)
+    second_kernel(const __grid_constant__ Chain<T> a) {
+  using S = SecondShape<T, kRank, kTile, kBack>;
+  using P = Planes<T>;
+  extern __shared__ __align__(16) uint8_t smem[];
+  T* const stages = reinterpret_cast<T*>(smem);
+  __nv_bfloat16* const hidden = reinterpret_cast<__nv_bfloat16*>(smem + S::kStages * S::kStage * sizeof(T));
+  const uint32_t tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const uint32_t row_warp = warp % S::kRowWarps, other = warp / S::kRowWarps;
+
+  // before the first product's end: its kernel lets this one start when all that
+  // came before is complete, and it writes `hidden` alone
+  if (!a.follows) pdl_wait();
+  const uint64_t col0 = static_cast<uint64_t>(blockIdx.x % a.groups) * a.group_out;
+  const uint64_t col1 = min(col0 + a.group_out, a.out);
+  Tile t;
+  const bool any = Tile::find<kTile>(a.q, blockIdx.x / a.groups, t) && col0 < col1;
+  const bool adapts = any && t.adapter >= 0;
+  const bool copies = any && (adapts || a.y != a.base);
+  const T* const base = a.base ? a.base + t.row0 * a.base_stride : nullptr;
+  const T* const second = a.second.data + (adapts ? t.adapter * a.second.step : 0);
+  const int steps = copies ? static_cast<int>((col1 - col0 + S::kCols - 1) / S::kCols) : 0;
+  auto load = [&](int step) {
+    if (step < steps) {
+      T* const to = stages + step % S::kStages * S::kStage;
+      const uint64_t c = col0 + static_cast<uint64_t>(step) * S::kCols;
+      const int64_t left = col1 - c;
+      copy_tile<T, kTile, S::kCols, S::kPitch>(to, base ? base + c : reinterpret_cast<const T*>(a.hidden), a.base_stride, base ? t.rows : 0, left, a.base_whole);
+      if (adapts) {
+        if constexpr (kBack)
+          copy_tile<T, kRank, S::kCols, S::kSecondPitch>(to + S::kBase, second + c, a.second.stride, a.rank, left, a.second.whole);
+        else
+          copy_tile<T, S::kCols, kRank, S::kSecondPitch>(to + S::kBase, second + c * a.second.stride, a.second.stride, left, a.rank, a.second.whole);
       }
     }
-    if (step + 1 < col_steps) store_second((step + 1) & 1);
-    __syncthreads();
+    copies_end();
+  };
+#pragma unroll
+  for (int s = 0; s + 1 < S::kStages; ++s) load(s);
+  pdl_wait();
+  pdl_trigger();
+  if (!copies) {
+    copies_wait<0>();
+    return;
   }
-  if (a.parts > 1) cluster_wait();  // the others have read this block's sums
+  uint32_t h[kRank / 16][P::kP][4];
+  if (adapts) {
+    constexpr int kChunks = P::kP * kTile * kRank / 8;
+    for (int i = tid; i < kChunks; i += kAdapterThreads) {
+      const int row = i / (P::kP * kRank / 8), plane = i / (kRank / 8) % P::kP, col = i % (kRank / 8) * 8;
+      const bool there = row < t.rows;
+      copy_16(smem_u32(hidden + (plane * kTile + row) * S::kHiddenPitch + col),
+              a.hidden + (t.row0 + (there ? row : 0)) * (P::kP * kRank) + plane * kRank + col, there ? 16 : 0);
+    }
+    copies_end();
+    copies_wait<0>();
+    __syncthreads();
+#pragma unroll
+    for (int k = 0; k < kRank / 16; ++k)
+#pragma unroll
+      for (int p = 0; p < P::kP; ++p)
+        ldsm(h[k][p], smem_u32(hidden + (p * kTile + row_warp * 16 + lane % 16) * S::kHiddenPitch + k * 16 + lane / 16 * 8));
+  }
+  T* const y = a.y + t.row0 * a.y_stride;
+  for (int step = 0; step < steps; ++step) {
+    copies_wait<S::kStages - 2>();
+    __syncthreads();
+    load(step + S::kStages - 1);
+    T* const bs = stages + step % S::kStages * S::kStage;
+    const T* const ws = bs + S::kBase;
+    if (adapts) {
+#pragma unroll
+      for (int n = 0; n < S::kWarpCols; n += 16) {
+        const int c = other * S::kWarpCols + n;
+        Sum<T> d[2];
+#pragma unroll
+        for (int k = 0; k < kRank / 16; ++k) {
+          uint32_t w[P::kW][4];
+          cols_operand<T, P::kW, S::kSecondPitch, kBack>(w, ws, c, k * 16);
+          d[0].add(h[k], w, 0);
+          d[1].add(h[k], w, 1);
+        }
+        // onto base, in its place
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          T* const at = bs + (row_warp * 16 + lane / 4 + i % 2 * 8) * S::kPitch + c + i / 2 * 8 + lane % 4 * 2;
+          at[0] = from_f32<T>(to_f32(at[0]) + d[i / 2].at(i % 2 * 2));
+          at[1] = from_f32<T>(to_f32(at[1]) + d[i / 2].at(i % 2 * 2 + 1));
+        }
+      }
+      __syncwarp();
+    }
+    // a warp's rows of kWarpCols columns, eight to a lane
+    const uint64_t c0 = col0 + static_cast<uint64_t>(step) * S::kCols + other * S::kWarpCols;
+    constexpr int kLanes = S::kWarpCols / 8;
+#pragma unroll
+    for (int r = lane / kLanes; r < 16; r += 32 / kLanes) {
+      const int row = row_warp * 16 + r;
+      const uint64_t col = c0 + lane % kLanes * 8;
+      const int64_t n = row < t.rows ? static_cast<int64_t>(col1 - col) : 0;
+      const T* const from = bs + row * S::kPitch + other * S::kWarpCols + lane % kLanes * 8;
+      T* const out = y + row * a.y_stride + col;
+      if (n >= 8 && a.y_whole) {
+#pragma unroll
+        for (int i = 0; i < static_cast<int>(sizeof(T)) / 2; ++i)
+          st_stream_v4(out + i * (16 / sizeof(T)), reinterpret_cast<const uint4*>(from)[i]);
+      } else {
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+          if (i < n) out[i] = from[i];
+      }
+    }
+  }
+  copies_wait<0>();
 }
 
 // ---------------------------------------------------------------------------
@@ -589,7 +574,7 @@ struct Grads {
   uint64_t cols[2];     // k, n
   const T* m[2];        // x, dy
   uint64_t stride[2];
-  const float* p[2];    // dh, h
+  const __nv_bfloat16* p[2];  // dh, c h: tokens x planes x kRank
   T* out[2];            // adapters x rank x k, adapters x n x rank
   bool whole[2];
 };
@@ -598,12 +583,14 @@ template <class T, int kRank>
 struct GradShape {
   using P = Planes<T>;
   static constexpr int kRows = 64, kCols = 128;
-  static constexpr int kRankPitch = kRank + 8, kColPitch = kCols + 8;
-  static constexpr int kM = P::kW * kRows * kColPitch * 2;
+  static constexpr int kStages = sizeof(T) == 4 ? 2 : 3;
+  static constexpr int kRankWarps = kRank / 16, kColWarps = 8 / kRankWarps, kWarpCols = kCols / kColWarps;
+  static constexpr int kRankPitch = kRank + 8, kPitch = kCols + 8;
+  static constexpr int kM = kRows * kPitch * static_cast<int>(sizeof(T));
   static constexpr int kP = P::kP * kRows * kRankPitch * 2;
   static constexpr int kStage = kM + kP;
   static constexpr int kSums = kRank * kCols * 4;
-  static constexpr int kBytes = 2 * kStage > kSums ? 2 * kStage : kSums;
+  static constexpr int kBytes = kStages * kStage > kSums ? kStages * kStage : kSums;
 };
 
 template <class T, int kRank>
@@ -612,12 +599,11 @@ __global__ void __launch_bounds__(kAdapterThreads)
   using S = GradShape<T, kRank>;
   using P = Planes<T>;
   constexpr int kThreads = kAdapterThreads;
-  constexpr int kMLoads = S::kRows * S::kCols / 8 / kThreads;
-  constexpr int kPQuads = S::kRows * kRank / 4, kPLoads = (kPQuads + kThreads - 1) / kThreads;
   extern __shared__ __align__(16) uint8_t smem[];
   __shared__ uint64_t from[kThreads], to[kThreads];  // rows of the adapter's requests
   __shared__ uint32_t counts[kThreads / 32];
   const uint32_t tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const uint32_t rank_warp = warp % S::kRankWarps, col_warp = warp / S::kRankWarps;
   pdl_trigger();
   pdl_wait();
   const uint32_t part = blockIdx.x % a.parts;
@@ -626,87 +612,52 @@ __global__ void __launch_bounds__(kAdapterThreads)
   uint64_t block = blockIdx.x / a.parts % all;
   const int sel = block >= a.blocks[0];
   if (sel) block -= a.blocks[0];
-  const uint64_t col0 = block * S::kCols, cols = a.cols[sel];
-  const T* const m = a.m[sel];
-  const float* const p = a.p[sel];
-  const uint64_t stride = a.stride[sel];
+  const uint64_t col0 = block * S::kCols, cols = a.cols[sel], stride = a.stride[sel];
+  const T* const m = a.m[sel] + col0;
+  const __nv_bfloat16* const p = a.p[sel];
   const bool whole = a.whole[sel];
-  const float scale = sel && a.q.scales ? a.q.scales[adapter] : 1.f;
 
-  float acc[kRank / 16][2][4] = {};
-  Raw<T> m_raw[kMLoads];
-  float4 p_raw[kPLoads];
-  auto load_stage = [&](uint64_t row0, int rows) {
+  auto load = [&](int stage, uint64_t row0, int rows) {
+    uint8_t* const b = smem + stage * S::kStage;
+    copy_tile<T, S::kRows, S::kCols, S::kPitch>(reinterpret_cast<T*>(b), m + row0 * stride, stride, rows, cols - col0, whole);
+    __nv_bfloat16* const planes = reinterpret_cast<__nv_bfloat16*>(b + S::kM);
+    constexpr int kChunks = P::kP * S::kRows * kRank / 8;
 #pragma unroll
-    for (int i = 0; i < kMLoads; ++i) {
-      const int at = tid + i * kThreads, row = at / (S::kCols / 8);
-      const uint64_t col = col0 + at % (S::kCols / 8) * 8;
-      m_raw[i].load(m + (row0 + row) * stride + col, row < rows ? static_cast<int64_t>(cols - col) : 0, whole);
-    }
-#pragma unroll
-    for (int i = 0; i < kPLoads; ++i) {
-      const int at = tid + i * kThreads, row = at * 4 / kRank, col = at * 4 % kRank;
-      float* const e = reinterpret_cast<float*>(&p_raw[i]);
-#pragma unroll
-      for (int j = 0; j < 4; ++j)
-        e[j] = row < rows && col + j < static_cast<int>(a.rank) ? p[(row0 + row) * a.rank + col + j] * scale : 0.f;
+    for (int i = 0; i < (kChunks + kThreads - 1) / kThreads; ++i) {
+      const int at = tid + i * kThreads;
+      if (kChunks % kThreads && at >= kChunks) break;
+      const int row = at / (P::kP * kRank / 8), plane = at / (kRank / 8) % P::kP, col = at % (kRank / 8) * 8;
+      const bool there = row < rows;
+      copy_16(smem_u32(planes + (plane * S::kRows + row) * S::kRankPitch + col),
+              p + (row0 + (there ? row : 0)) * (P::kP * kRank) + plane * kRank + col, there ? 16 : 0);
     }
   };
-  auto store_stage = [&](int buffer) {
-    uint8_t* const b = smem + buffer * S::kStage;
-#pragma unroll
-    for (int i = 0; i < kMLoads; ++i) {
-      const int at = tid + i * kThreads, row = at / (S::kCols / 8), col = at % (S::kCols / 8) * 8;
-      uint4 v[P::kW];
-      split<T, P::kW>(m_raw[i], v);
-#pragma unroll
-      for (int q = 0; q < P::kW; ++q)
-        *reinterpret_cast<uint4*>(b + ((q * S::kRows + row) * S::kColPitch + col) * 2) = v[q];
-    }
-#pragma unroll
-    for (int i = 0; i < kPLoads; ++i) {
-      const int at = tid + i * kThreads, row = at * 4 / kRank, col = at * 4 % kRank;
-      if (kPQuads % kThreads && at >= kPQuads) break;
-      uint32_t lo[P::kP], hi[P::kP];
-      split_pair<P::kP>(p_raw[i].x, p_raw[i].y, lo);
-      split_pair<P::kP>(p_raw[i].z, p_raw[i].w, hi);
-#pragma unroll
-      for (int q = 0; q < P::kP; ++q)
-        *reinterpret_cast<uint2*>(b + S::kM + ((q * S::kRows + row) * S::kRankPitch + col) * 2) = make_uint2(lo[q], hi[q]);
-    }
-  };
-  auto multiply = [&](int buffer) {
-    const uint32_t ms = smem_u32(smem) + buffer * S::kStage, ps = ms + S::kM;
-    constexpr bool kShort = sizeof(T) == 4;
-    float chain[kRank / 16][2][4] = {};
+  float acc[S::kWarpCols / 8][4] = {};
+  auto multiply = [&](int stage) {
+    const T* const ms = reinterpret_cast<const T*>(smem + stage * S::kStage);
+    const __nv_bfloat16* const ps = reinterpret_cast<const __nv_bfloat16*>(smem + stage * S::kStage + S::kM);
 #pragma unroll
     for (int t = 0; t < S::kRows; t += 16) {
-      uint32_t w[P::kW][4];
+      uint32_t h[P::kP][4];  // rows of the product are ranks
 #pragma unroll
-      for (int j = 0; j < P::kW; ++j)
-        ldsm_t(w[j], ms + ((j * S::kRows + t + lane % 16) * S::kColPitch + warp * 16 + lane / 16 * 8) * 2);
+      for (int i = 0; i < P::kP; ++i)
+        ldsm_t(h[i], smem_u32(ps + (i * S::kRows + t + lane % 8 + lane / 16 * 8) * S::kRankPitch + rank_warp * 16 + lane / 8 % 2 * 8));
 #pragma unroll
-      for (int r = 0; r < kRank / 16; ++r)
+      for (int n = 0; n < S::kWarpCols / 16; ++n) {
+        uint32_t w[P::kW][4];
+        cols_operand<T, P::kW, S::kPitch, true>(w, ms, col_warp * S::kWarpCols + n * 16, t);
 #pragma unroll
-        for (int i = 0; i < P::kP; ++i) {
-          // rows of the product are ranks: the planes lie the other way around
-          uint32_t h[4];
-          ldsm_t(h, ps + ((i * S::kRows + t + lane % 8 + lane / 16 * 8) * S::kRankPitch + r * 16 + lane / 8 % 2 * 8) * 2);
+        for (int half = 0; half < 2; ++half) {
+          Sum<T> d;
+          if constexpr (sizeof(T) == 2)
 #pragma unroll
-          for (int j = 0; j < P::kW; ++j)
-            if (P::takes(i, j)) {
-              mma<false>(kShort ? chain[r][0] : acc[r][0], h, w[j][0], w[j][1]);
-              mma<false>(kShort ? chain[r][1] : acc[r][1], h, w[j][2], w[j][3]);
-            }
+            for (int i = 0; i < 4; ++i) d.high[i] = acc[2 * n + half][i];
+          d.add(h, w, half);
+#pragma unroll
+          for (int i = 0; i < 4; ++i)
+            acc[2 * n + half][i] = sizeof(T) == 2 ? d.high[i] : acc[2 * n + half][i] + d.at(i);
         }
-    }
-    if constexpr (kShort) {
-#pragma unroll
-      for (int r = 0; r < kRank / 16; ++r)
-#pragma unroll
-        for (int n = 0; n < 2; ++n)
-#pragma unroll
-          for (int i = 0; i < 4; ++i) acc[r][n][i] += chain[r][n][i];
+      }
     }
   };
 
@@ -728,50 +679,49 @@ __global__ void __launch_bounds__(kAdapterThreads)
       to[at] = a.q.start(s + 2);
     }
     __syncthreads();
-    // this block's tiles of theirs, the next one's loads on the way
+    // this block's tiles of theirs, the next ones' loads on the way
     uint32_t i = 0;
     uint64_t row = found ? from[0] : 0;
-    auto next = [&](uint64_t& row0, int& rows) {  // false: none left
+    auto next = [&](int stage) {  // loads one; false: none left
       while (i < found) {
         if (row >= to[i]) {
           if (++i < found) row = from[i];
           continue;
         }
-        row0 = row;
-        rows = static_cast<int>(min(to[i] - row, static_cast<uint64_t>(S::kRows)));
+        const uint64_t row0 = row;
         row += S::kRows;
-        if (tile++ % a.parts == part) return true;
+        if (tile++ % a.parts != part) continue;
+        load(stage, row0, static_cast<int>(min(to[i] - row0, static_cast<uint64_t>(S::kRows))));
+        return true;
       }
       return false;
     };
-    uint64_t row0;
-    int rows, buffer = 0;
-    bool more = next(row0, rows);
-    if (more) {
-      load_stage(row0, rows);
-      store_stage(0);
+    int ahead = 0;  // tiles loaded and not yet multiplied
+#pragma unroll
+    for (int st = 0; st + 1 < S::kStages; ++st) {
+      ahead += next(st);
+      copies_end();
     }
-    __syncthreads();
-    while (more) {
-      more = next(row0, rows);
-      if (more) load_stage(row0, rows);
-      multiply(buffer);
-      buffer ^= 1;
-      if (more) store_stage(buffer);
+    for (int step = 0; ahead; ++step) {
+      copies_wait<S::kStages - 2>();
       __syncthreads();
+      ahead += next((step + S::kStages - 1) % S::kStages);
+      copies_end();
+      multiply(step % S::kStages);
+      --ahead;
     }
+    copies_wait<0>();
+    __syncthreads();
   }
 
   // the parts' sums in a fixed order, and the result
   float* const sums = reinterpret_cast<float*>(smem);  // [rank][cols]
 #pragma unroll
-  for (int r = 0; r < kRank / 16; ++r)
+  for (int n = 0; n < S::kWarpCols / 8; ++n)
 #pragma unroll
-    for (int n = 0; n < 2; ++n)
-#pragma unroll
-      for (int half = 0; half < 2; ++half)
-        *reinterpret_cast<float2*>(sums + (r * 16 + lane / 4 + half * 8) * S::kCols + warp * 16 + n * 8 + lane % 4 * 2) =
-            make_float2(acc[r][n][half * 2], acc[r][n][half * 2 + 1]);
+    for (int half = 0; half < 2; ++half)
+      *reinterpret_cast<float2*>(sums + (rank_warp * 16 + lane / 4 + half * 8) * S::kCols + col_warp * S::kWarpCols + n * 8 + lane % 4 * 2) =
+          make_float2(acc[n][half * 2], acc[n][half * 2 + 1]);
   if (a.parts > 1) cluster_meet();
   else __syncthreads();
   T* const out = a.out[sel];
@@ -820,25 +770,31 @@ cudaError_t launch_clusters(void (*kernel)(A), const A& args, uint64_t blocks, u
 
 template <class T, int kRank, int kTile, bool kBack>
 cudaError_t launch_chain(Chain<T> a, cudaStream_t st) {
-  using S = ChainShape<T, kRank, kTile, kBack>;
+  using F = FirstShape<T, kRank, kTile, kBack>;
+  using S = SecondShape<T, kRank, kTile, kBack>;
   const uint64_t slots = slots_of(a.q.tokens, a.q.requests, kTile);
-  a.parts = 1;
-  while (a.parts < kAdapterParts && a.in >= 2ull * a.parts * 128) a.parts *= 2;
-  auto share = [](uint64_t n, uint64_t by, uint64_t unit) { return ((n + by - 1) / by + unit - 1) / unit * unit; };
-  a.part_in = share(a.in, a.parts, 64);
   const uint64_t tiles = a.q.tokens / kTile + (a.q.requests < a.q.tokens ? a.q.requests : a.q.tokens) + 1;
-  const uint64_t most = a.out / (static_cast<uint64_t>(a.parts) * S::kCols) + 1;
-  uint64_t groups = (4ull * sm_count() + tiles * a.parts - 1) / (tiles * a.parts);
-  if (groups > most) groups = most;
-  a.groups = static_cast<uint32_t>(groups);
-  a.part_out = share(a.out, groups * a.parts, 32);
-  return launch_clusters(chain_kernel<T, kRank, kTile, kBack>, a, slots * groups * a.parts, a.parts, S::kBytes, st);
+  a.parts = 1;
+  while (a.parts < kAdapterParts && a.in >= 4ull * a.parts * F::kStep && tiles * a.parts < 8ull * sm_count()) a.parts *= 2;
+  a.part_in = ((a.in + a.parts - 1) / a.parts + 63) / 64 * 64;
+  a.follows = a.q.requests > 0;
+  if (a.follows) {  // (without a request all rows are base's)
+    const cudaError_t e = launch_clusters(first_kernel<T, kRank, kTile, kBack>, a, slots * a.parts, a.parts, F::kBytes, st);
+    if (e != cudaSuccess) return e;
+  }
+  // blocks for every SM several times over, of up to eight stages
+  uint64_t steps = (a.out + S::kCols - 1) / S::kCols, each = (tiles * steps + 8ull * sm_count() - 1) / (8ull * sm_count());
+  if (each > 8) each = 8;
+  a.groups = static_cast<uint32_t>((steps + each - 1) / each);
+  a.group_out = each * S::kCols;
+  return launch_clusters(second_kernel<T, kRank, kTile, kBack>, a, slots * a.groups, 1, S::kBytes, st);
 }
 
 template <class T, bool kBack>
 cudaError_t chain(const Chain<T>& a, cudaStream_t st) {
   const bool tall = a.q.tokens >= 32 * a.q.requests;
   if (a.rank <= 16) return tall ? launch_chain<T, 16, 64, kBack>(a, st) : launch_chain<T, 16, 16, kBack>(a, st);
+  if (a.rank <= 32) return tall ? launch_chain<T, 32, 64, kBack>(a, st) : launch_chain<T, 32, 16, kBack>(a, st);
   return tall ? launch_chain<T, 64, 64, kBack>(a, st) : launch_chain<T, 64, 16, kBack>(a, st);
 }
 
@@ -857,7 +813,7 @@ cudaError_t launch_grads(Grads<T> a, cudaStream_t st) {
 }
 template <class T>
 cudaError_t grads(const Grads<T>& a, cudaStream_t st) {
-  return a.rank <= 16 ? launch_grads<T, 16>(a, st) : launch_grads<T, 64>(a, st);
+  return a.rank <= 16 ? launch_grads<T, 16>(a, st) : a.rank <= 32 ? launch_grads<T, 32>(a, st) : launch_grads<T, 64>(a, st);
 }
 
 // adapter_f32.cu, adapter_bf16.cu, adapter_f16.cu

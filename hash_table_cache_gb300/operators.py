@@ -114,7 +114,7 @@ def _tensors(args):
         elif isinstance(a, PreferenceLoss):
             yield from (a.logits, a.labels, a._saved)
         elif isinstance(a, AdapterMatmul):
-            yield from (t for t in (a.x, a.down, a.up, a.offsets, a.which, a.scales, a.hidden) if t is not None)
+            yield from (t for t in (a.x, a.down, a.up, a.offsets, a.which, a.scales, a._hidden) if t is not None)
         elif isinstance(a, TokenLogps):
             yield from (t for t in (a.logits, a.labels, a.entropy, a._lse) if t is not None)
 
@@ -428,10 +428,10 @@ def _token_logps_backward(s, f, dlogps, dentropy, out):
 
 
 class AdapterMatmul:
-    """What ``adapter_matmul`` returns: ``out`` [tokens, n] and the float32
-    ``hidden`` [tokens, rank], and what the backward call needs."""
+    """What ``adapter_matmul`` returns: ``out`` [tokens, n], and what the backward call
+    needs."""
 
-    __slots__ = ("out", "hidden", "x", "down", "up", "offsets", "which", "scales", "_adapters", "_shape")
+    __slots__ = ("out", "x", "down", "up", "offsets", "which", "scales", "_adapters", "_shape", "_hidden")
 
 
 def adapter_matmul(x, down, up, offsets, which, scales=None, base=None, out=None, stream=None):
@@ -498,7 +498,8 @@ def _adapter_matmul(s, x, down, up, offsets, which, scales, base, out):
         stride = n
     else:
         stride = _taken(out, tokens, n, dtype, "out", device)
-    f.out, f.hidden = out, torch.empty((tokens, rank), dtype=torch.float32, device=device)
+    f.out = out
+    f._hidden = torch.empty(_abi.adapter_hidden_bytes(tokens, rank, kind), dtype=torch.uint8, device=device)
     f.x, f.down, f.up, f.offsets, f.which, f.scales = x, down, up, offsets, which, scales
     f._adapters = _abi.Adapters(count, down.data_ptr(), down_step, down_stride, up.data_ptr(), up_step,
                                 up_stride, None if scales is None else scales.data_ptr(), rank)
@@ -506,7 +507,7 @@ def _adapter_matmul(s, x, down, up, offsets, which, scales, base, out):
     _ok(_abi.load().hkv_adapter_matmul(
         tokens, k, n, kind, addressof(f._adapters), requests, offsets.data_ptr(), which.data_ptr(),
         x.data_ptr(), x_stride, None if base is None else base.data_ptr(), base_stride, out.data_ptr(),
-        stride, f.hidden.data_ptr(), s), "hkv_adapter_matmul")
+        stride, f._hidden.data_ptr(), s), "hkv_adapter_matmul")
     if given is not None:
         _written(given)
     return f
@@ -534,10 +535,10 @@ def _adapter_matmul_backward(s, f, dout, base, out):
         stride = _taken(out, tokens, k, dtype, "out", device)
     ddown = torch.empty((count, rank, k), dtype=dtype, device=device)
     dup = torch.empty((count, n, rank), dtype=dtype, device=device)
-    dhidden = torch.empty((tokens, rank), dtype=torch.float32, device=device)
+    dhidden = torch.empty_like(f._hidden)
     _ok(_abi.load().hkv_adapter_matmul_backward(
         tokens, k, n, kind, addressof(f._adapters), requests, f.offsets.data_ptr(), f.which.data_ptr(),
-        x.data_ptr(), x_stride, dout.data_ptr(), d_stride, f.hidden.data_ptr(),
+        x.data_ptr(), x_stride, dout.data_ptr(), d_stride, f._hidden.data_ptr(),
         None if base is None else base.data_ptr(), base_stride, out.data_ptr(), stride, ddown.data_ptr(),
         dup.data_ptr(), dhidden.data_ptr(), s), "hkv_adapter_matmul_backward")
     if given is not None:

@@ -481,39 +481,38 @@ typedef struct hkv_adapters {
  * offsets[s] .. offsets[s + 1] - 1 of x (tokens x k) and of y (tokens x n), and
  * the adapter which[s] (offsets, which: device, requests + 1 ascending values in
  * 0 .. tokens, and requests values):
- *   hidden[t] = down x[t]                          (float32, tokens x rank)
- *   y[t]      = base[t] + scale * up hidden[t]
+ *   h[t] = scale * down x[t]          y[t] = base[t] + up h[t]
  * with sums in float32 and y rounded once.  base (NULL: zeros) may be y itself,
  * with the same stride.  Rows of no request, and of one whose which[s] lies
- * outside 0 .. count - 1, have y[t] = base[t] and zeros in hidden; where y is
- * base they are left as they are.  y must not overlap base otherwise, nor x
- * (columns of one buffer side by side do not).  hidden (NULL where it is not
- * wanted) is for the backward call.  The hidden numbers go on with 16 bits and
- * more of their digits (24 for float32 matrices); a row with an infinity in it
- * may give NaN where the formula gives an infinity.  `adapters` is read before
- * the call returns. */
+ * outside 0 .. count - 1, have y[t] = base[t]; where y is base they are left as
+ * they are.  y must not overlap base otherwise, nor x (columns of one buffer side
+ * by side do not).  hidden (device memory of HKV_ADAPTER_HIDDEN_BYTES, 16-byte
+ * aligned) gets h for the backward call; of h, 16 digits go on for 16-bit
+ * matrices, 24 for float32.  A row with an infinity in it may give NaN where the
+ * formula gives an infinity.  `adapters` is read before the call returns. */
+#define HKV_ADAPTER_HIDDEN_BYTES(tokens, rank, type) \
+  ((uint64_t)(tokens) * ((rank) <= 16 ? 16 : (rank) <= 32 ? 32 : 64) * ((type) == HKV_F32 ? 6 : 4))
 hkv_status hkv_adapter_matmul(uint64_t tokens, uint64_t k, uint64_t n, int type,
                               const hkv_adapters* adapters, uint64_t requests,
                               const int64_t* offsets, const int64_t* which, const void* x,
                               uint64_t x_stride, const void* base, uint64_t base_stride, void* y,
-                              uint64_t y_stride, float* hidden, void* stream);
+                              uint64_t y_stride, void* hidden, void* stream);
 
 /* Its gradients, from dy (tokens x n) and the forward call's x and hidden:
- *   dhidden[t] = scale * up^T dy[t]                (float32, tokens x rank)
- *   dx[t]      = base[t] + down^T dhidden[t]       (base, tokens x k: as above)
- *   ddown[a]   = sum over the rows t of a's requests of dhidden[t] x[t]^T
- *   dup[a]     = scale * sum of dy[t] hidden[t]^T
- * ddown (count x rank x k) and dup (count x n x rank) are contiguous, in the
- * matrices' type, rounded once, and zero for an adapter of no request; either may
- * be NULL.  dhidden is an output, or scratch, of the caller's.  dx must not
- * overlap x or dy, nor base unless it is base. */
+ *   dh[t]    = scale * up^T dy[t]     dx[t] = base[t] + down^T dh[t]
+ *   ddown[a] = sum over the rows t of a's requests of dh[t] x[t]^T
+ *   dup[a]   = sum of dy[t] h[t]^T
+ * (base, tokens x k: as above).  ddown (count x rank x k) and dup (count x n x
+ * rank) are contiguous, in the matrices' type, rounded once, and zero for an
+ * adapter of no request; either may be NULL.  dhidden is scratch like hidden.  dx
+ * must not overlap x or dy, nor base unless it is base. */
 hkv_status hkv_adapter_matmul_backward(uint64_t tokens, uint64_t k, uint64_t n, int type,
                                        const hkv_adapters* adapters, uint64_t requests,
                                        const int64_t* offsets, const int64_t* which, const void* x,
                                        uint64_t x_stride, const void* dy, uint64_t dy_stride,
-                                       const float* hidden, const void* base, uint64_t base_stride,
+                                       const void* hidden, const void* base, uint64_t base_stride,
                                        void* dx, uint64_t dx_stride, void* ddown, void* dup,
-                                       float* dhidden, void* stream);
+                                       void* dhidden, void* stream);
 
 /* One gradient: n elements of `type` at `data`.  Where `out` is not NULL the
  * clipped gradient is written there as `out_type`; it may be `data` itself

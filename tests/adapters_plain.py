@@ -24,7 +24,7 @@ def _product(a, b, e_a, rest, wide):
 
 
 def adapter_matmul(x, down, up, offsets, which, scales=None, base=None, dy=None, dx_base=None):
-    """{name: (value, bound)} of out and hidden, and of dx, ddown and dup where dy is given."""
+    """{name: (value, bound)} of out, and of dx, ddown and dup where dy is given."""
     kind = x.dtype
     wide = kind == torch.float32
     first = 2.0 ** -22 if wide else 0.0
@@ -40,7 +40,7 @@ def adapter_matmul(x, down, up, offsets, which, scales=None, base=None, dy=None,
         return v, e * (1 + U[kind]) + (v.abs() * U[kind]).nan_to_num(0, 0, 0) + TINY[kind]
 
     y = zero(tokens, n) if base is None else base.double().clone()
-    e_y, hid, e_hid = zero(tokens, n), zero(tokens, rank), zero(tokens, rank)
+    e_y = zero(tokens, n)
     if dy is not None:
         dx = zero(tokens, k) if dx_base is None else dx_base.double().clone()
         e_dx = zero(tokens, k)
@@ -52,7 +52,6 @@ def adapter_matmul(x, down, up, offsets, which, scales=None, base=None, dy=None,
         c = 1.0 if scales is None else float(scales[w])
         d, v, xs = down[w].double(), up[w].double(), x[a:b].double()
         h, e_h = _product(xs, d, None, first, wide)
-        hid[a:b], e_hid[a:b] = h, e_h + u * h.abs()
         p, e_p = _product(h, v, e_h, then + 4 * u, wide)
         y[a:b] += c * p
         e_y[a:b] = abs(c) * e_p + 2 * u * y[a:b].abs()
@@ -70,7 +69,7 @@ def adapter_matmul(x, down, up, offsets, which, scales=None, base=None, dy=None,
         p, e_p = _product(g.t(), (c * h).t(), None, then + 4 * u, wide)
         du[w] += p
         e_du[w] += e_p + abs(c) * (g.abs().t() @ e_h) + 2.0 ** -20 * abs(c) * (g.abs().t() @ h.abs())
-    out = {"out": rounded(y, e_y), "hidden": (hid, e_hid)}
+    out = {"out": rounded(y, e_y)}
     if dy is not None:
         out |= {"dx": rounded(dx, e_dx), "ddown": rounded(dd, e_dd), "dup": rounded(du, e_du)}
     return out

@@ -59,7 +59,7 @@ BAD_ADAPTERS = [dict(count=BIG), dict(rank=0), dict(rank=65), dict(down=None), d
                 dict(up_step=1 << 41), dict(down=P + 2), dict(up=P + 1), dict(scales=P + 2)]
 BAD = [dict(tokens=BIG), dict(k=0), dict(n=0), dict(k=BIG), dict(n=BIG), dict(type=3), dict(requests=BIG), dict(offsets=None),
        dict(which=None), dict(offsets=P + 4), dict(which=P + 4), dict(x=None), dict(x=P + 2), dict(x_stride=63),
-       dict(x_stride=1 << 32), dict(hidden=P + 2), dict(base=P + 2), dict(adapters=None)]
+       dict(x_stride=1 << 32), dict(hidden=None), dict(hidden=P + 8), dict(base=P + 2), dict(adapters=None)]
 
 
 def test_adapters(lib):
@@ -73,7 +73,7 @@ def test_adapters(lib):
                 dict(y=P + 256), dict(y=2 * P, y_stride=49), dict(y=2 * P + 4)]),
             ("hkv_adapter_matmul_backward", BACKWARD, BAD + [
                 dict(base_stride=63), dict(dy=None), dict(dy=2 * P + 2), dict(dy_stride=47), dict(dx=None), dict(dx=4 * P + 1),
-                dict(dx_stride=63), dict(hidden=None), dict(dhidden=None), dict(dhidden=P + 2), dict(ddown=P + 2),
+                dict(dx_stride=63), dict(dhidden=None), dict(dhidden=P + 8), dict(ddown=P + 2),
                 dict(dup=P + 2), dict(dx=P), dict(dx=2 * P), dict(dx=3 * P, dx_stride=65)])):
         _refused(lib, name, dict(base, adapters=at), bad)
         for change in BAD_ADAPTERS:
@@ -87,6 +87,9 @@ def test_adapters(lib):
 def test_the_structure_is_the_header_s():
     import ctypes
     import hash_table_cache_gb300 as hkv
+    text = open(os.path.join(ROOT, "include", "hkv.h")).read()
+    assert re.search(r"\(rank\) <= 16 \? 16 : \(rank\) <= 32 \? 32 : 64\) \* \(\(type\) == HKV_F32 \? 6 : 4\)", text)
+    assert [hkv.adapter_hidden_bytes(3, r, t) for r, t in ((1, 0), (17, 1), (33, 2), (64, 0))] == [288, 384, 768, 1152]
     assert ctypes.sizeof(hkv.Adapters) == 72 and hkv.Adapters.rank.offset == 64 and hkv.Adapters.scales.offset == 56
 
 
