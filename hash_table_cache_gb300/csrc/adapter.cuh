@@ -29,6 +29,18 @@
 
 #include "operators.cuh"
 
+#ifndef HKV_PM
+#define HKV_PM 4
+#endif
+#ifndef HKV_GM
+#define HKV_GM 8
+#endif
+#ifndef HKV_EM
+#define HKV_EM 8
+#endif
+#ifndef HKV_S2
+#define HKV_S2 2
+#endif
 namespace hkv {
 
 constexpr int kAdapterThreads = 256;
@@ -89,20 +101,18 @@ inline uint64_t slots_of(uint64_t tokens, uint64_t requests, int tile) {
 // tiles
 // ---------------------------------------------------------------------------
 // Eight neighbouring elements into shared memory, the first n of them and zeros
-// behind (none for n <= 0): asynchronous where 16 bytes lie on a boundary (`whole`).
+// behind: asynchronous where 16 bytes lie on a boundary (`whole`).
 __device__ __forceinline__ void copy_16(uint32_t to, const void* from, int bytes) {
   asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(to), "l"(from), "r"(bytes) : "memory");
 }
 template <class T>
-__device__ __forceinline__ void copy_eight(T* to, const T* from, int64_t n, bool whole) {
+__device__ __forceinline__ void copy_eight(T* to, const T* from, int n, bool whole) {
   constexpr int kVecs = sizeof(T) / 2, kPer = 16 / sizeof(T);
   if (whole) {
-    const int have = n <= 0 ? 0 : n >= 8 ? 8 : static_cast<int>(n);
 #pragma unroll
-    for (int i = 0; i < kVecs; ++i) {
-      const int left = min(max(have - i * kPer, 0), kPer);
-      copy_16(smem_u32(to + i * kPer), from + i * kPer, left * static_cast<int>(sizeof(T)));
-    }
+    for (int i = 0; i < kVecs; ++i)
+      copy_16(smem_u32(to + i * kPer), from + i * kPer,
+              (kVecs == 1 ? n : min(max(n - i * kPer, 0), kPer)) * static_cast<int>(sizeof(T)));
   } else {
     uint4 v[kVecs];
     T* e = reinterpret_cast<T*>(v);
@@ -123,14 +133,18 @@ __device__ __forceinline__ void copies_wait() {
 template <class T, int kRows, int kCols, int kPitch>
 __device__ __forceinline__ void copy_tile(T* tile, const T* data, uint64_t stride, int64_t rows, int64_t cols,
                                           bool whole) {
-  constexpr int kChunks = kRows * kCols / 8;
+  constexpr int kLanes = kCols / 8, kPass = kAdapterThreads / kLanes;  // threads to a row, rows at a time
+  static_assert(kAdapterThreads % kLanes == 0 && (kRows % kPass == 0 || kRows < kPass));
+  const int row = threadIdx.x / kLanes, col = threadIdx.x % kLanes * 8;
+  if (kRows < kPass && row >= kRows) return;
+  const int there = static_cast<int>(min(rows, static_cast<int64_t>(kRows))) - row;
+  const int n = static_cast<int>(max(min(cols - col, static_cast<int64_t>(8)), static_cast<int64_t>(0)));
+  const T* const from = data + row * stride + col;
+  T* const to = tile + row * kPitch + col;
 #pragma unroll
-  for (int i = 0; i < (kChunks + kAdapterThreads - 1) / kAdapterThreads; ++i) {
-    const int at = threadIdx.x + i * kAdapterThreads;
-    if (kChunks % kAdapterThreads && at >= kChunks) break;
-    const int row = at / (kCols / 8), col = at % (kCols / 8) * 8;
-    const bool there = row < rows && col < cols;
-    copy_eight(tile + row * kPitch + col, there ? data + row * stride + col : data, there ? cols - col : 0, whole);
+  for (int i = 0; i < (kRows + kPass - 1) / kPass; ++i) {
+    const bool has = i * kPass < there && n > 0;
+    copy_eight(to + i * kPass * kPitch, has ? from + i * kPass * stride : data, has ? n : 0, whole);
   }
 }
 
@@ -223,24 +237,56 @@ __device__ __forceinline__ void cols_operand(uint32_t (&b)[kN][4], const T* tile
   }
 }
 
-// A 16 x 8 piece of a product.  The tensor core cuts what it adds up, so float32
-// matrices keep the large terms in short chains of their own (`high`), the products
-// with lower planes, 2^-8 of them, in another, and join both by rounding additions.
+// A 16 x 16 piece of a product, as two of eight columns.  The tensor core cuts what
+// it adds up, so float32 matrices keep the large terms in short chains of their own
+// (`high`), the products with lower planes, 2^-8 of them, in another, and join both
+// by rounding additions.
 template <class T>
 struct Sum {
-  float high[4] = {}, low[4] = {};
+  static constexpr bool kTwo = sizeof(T) == 4;
+  float high[2][4] = {}, low[2][4] = {};
   template <int kA, int kB, bool kF16 = false>
-  __device__ __forceinline__ void add(const uint32_t (&a)[kA][4], const uint32_t (&b)[kB][4], int half) {
+  __device__ __forceinline__ void add(const uint32_t (&a)[kA][4], const uint32_t (&b)[kB][4]) {
 #pragma unroll
     for (int i = 0; i < kA; ++i)
 #pragma unroll
       for (int j = 0; j < kB; ++j) {
-        if (sizeof(T) == 4 && i + j > 2) continue;
-        mma<kF16>(sizeof(T) == 4 && i + j > 0 ? low : high, a[i], b[j][half * 2], b[j][half * 2 + 1]);
+        if (kTwo && i + j > 2) continue;
+#pragma unroll
+        for (int half = 0; half < 2; ++half)
+          mma<kF16>(kTwo && i + j > 0 ? low[half] : high[half], a[i], b[j][half * 2], b[j][half * 2 + 1]);
       }
   }
-  __device__ __forceinline__ float at(int i) const { return sizeof(T) == 4 ? high[i] + low[i] : high[i]; }
+  __device__ __forceinline__ float at(int half, int i) const {
+    return kTwo ? high[half][i] + low[half][i] : high[half][i];
+  }
 };
+// Chains that go on from one stage to the next where they need not be short.
+template <class T, int kA, int kB, bool kF16>
+__device__ __forceinline__ void add_onto(float (&acc)[2][4], const uint32_t (&a)[kA][4], const uint32_t (&b)[kB][4]) {
+  Sum<T> d;
+  if constexpr (!Sum<T>::kTwo)
+#pragma unroll
+    for (int i = 0; i < 8; ++i) d.high[i / 4][i % 4] = acc[i / 4][i % 4];
+  d.template add<kA, kB, kF16>(a, b);
+#pragma unroll
+  for (int i = 0; i < 8; ++i)
+    acc[i / 4][i % 4] = Sum<T>::kTwo ? acc[i / 4][i % 4] + d.at(i / 4, i % 4) : d.high[i / 4][i % 4];
+}
+
+// Two neighbouring elements in shared memory.
+template <class T>
+__device__ __forceinline__ float2 pair_at(const T* p) {
+  if constexpr (std::is_same_v<T, __nv_bfloat16>) return __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162*>(p));
+  else if constexpr (std::is_same_v<T, __half>) return __half22float2(*reinterpret_cast<const __half2*>(p));
+  else return *reinterpret_cast<const float2*>(p);
+}
+template <class T>
+__device__ __forceinline__ void put_pair(T* p, float a, float b) {
+  if constexpr (std::is_same_v<T, __nv_bfloat16>) *reinterpret_cast<__nv_bfloat162*>(p) = __floats2bfloat162_rn(a, b);
+  else if constexpr (std::is_same_v<T, __half>) *reinterpret_cast<__half2*>(p) = __floats2half2_rn(a, b);
+  else *reinterpret_cast<float2*>(p) = make_float2(a, b);
+}
 
 // The cluster's barrier, for warps whose threads may have parted.
 __device__ __forceinline__ void cluster_meet() {
@@ -346,7 +392,7 @@ __global__ void __launch_bounds__(kAdapterThreads)
     }
     copies_end();
   };
-  float acc[kRank / 8][4] = {};
+  float acc[kRank / 16][2][4] = {};
 #pragma unroll
   for (int s = 0; s + 1 < S::kStages; ++s) load(s);
   for (int step = 0; step < steps; ++step) {
@@ -356,12 +402,6 @@ __global__ void __launch_bounds__(kAdapterThreads)
     const T* const xs = stages + step % S::kStages * S::kStage;
     const T* const ws = xs + S::kX;
     constexpr int kEach = S::kStep / 16 / S::kOther;
-    Sum<T> d[kRank / 8];
-    if constexpr (sizeof(T) == 2)
-#pragma unroll
-      for (int n = 0; n < kRank / 8; ++n)
-#pragma unroll
-        for (int i = 0; i < 4; ++i) d[n].high[i] = acc[n][i];
 #pragma unroll
     for (int s = 0; s < kEach; ++s) {
       const int k = (other * kEach + s) * 16;
@@ -371,14 +411,9 @@ __global__ void __launch_bounds__(kAdapterThreads)
       for (int n = 0; n < kRank / 16; ++n) {
         uint32_t w[P::kIn][4];
         cols_operand<T, P::kIn, S::kFirstPitch, kBack>(w, ws, n * 16, k);
-        d[2 * n].template add<P::kIn, P::kIn, std::is_same_v<T, __half>>(xa, w, 0);
-        d[2 * n + 1].template add<P::kIn, P::kIn, std::is_same_v<T, __half>>(xa, w, 1);
+        add_onto<T, P::kIn, P::kIn, std::is_same_v<T, __half>>(acc[n], xa, w);
       }
     }
-#pragma unroll
-    for (int n = 0; n < kRank / 8; ++n)
-#pragma unroll
-      for (int i = 0; i < 4; ++i) acc[n][i] = sizeof(T) == 2 ? d[n].high[i] : acc[n][i] + d[n].at(i);
   }
   copies_wait<0>();
   __syncthreads();
@@ -389,8 +424,9 @@ __global__ void __launch_bounds__(kAdapterThreads)
   float* const to = sums + (other * kTile + row_warp * 16 + lane / 4) * kRank + lane % 4 * 2;
 #pragma unroll
   for (int n = 0; n < kRank / 8; ++n) {
-    *reinterpret_cast<float2*>(to + n * 8) = make_float2(acc[n][0], acc[n][1]);
-    *reinterpret_cast<float2*>(to + 8 * kRank + n * 8) = make_float2(acc[n][2], acc[n][3]);
+    const float(&v)[4] = acc[n / 2][n % 2];
+    *reinterpret_cast<float2*>(to + n * 8) = make_float2(v[0], v[1]);
+    *reinterpret_cast<float2*>(to + 8 * kRank + n * 8) = make_float2(v[2], v[3]);
   }
   __syncthreads();
   constexpr int kQuads = kTile * kRank / 4;
@@ -436,7 +472,7 @@ struct SecondShape {
   static constexpr int kRowWarps = kTile / 16, kOther = 8 / kRowWarps;
   static constexpr int kWarpCols = kTile == 64 ? (sizeof(T) == 4 ? 32 : 64) : (sizeof(T) == 4 ? 16 : 32);
   static constexpr int kCols = kOther * kWarpCols;  // columns of y to a stage
-  static constexpr int kStages = sizeof(T) == 4 || kRank == 64 ? 2 : 3;
+  static constexpr int kStages = sizeof(T) == 4 || kRank == 64 ? 2 : HKV_S2;
   static constexpr int kPitch = kCols + 8, kSecondPitch = kBack ? kPitch : kRank + 8, kHiddenPitch = kRank + 8;
   static constexpr int kBase = kTile * kPitch, kSecond = (kBack ? kRank : kCols) * kSecondPitch;
   static constexpr int kStage = kBase + kSecond;  // elements
@@ -519,20 +555,19 @@ __global__ void __launch_bounds__(kAdapterThreads)
 #pragma unroll
       for (int n = 0; n < S::kWarpCols; n += 16) {
         const int c = other * S::kWarpCols + n;
-        Sum<T> d[2];
+        Sum<T> d;
 #pragma unroll
         for (int k = 0; k < kRank / 16; ++k) {
           uint32_t w[P::kW][4];
           cols_operand<T, P::kW, S::kSecondPitch, kBack>(w, ws, c, k * 16);
-          d[0].add(h[k], w, 0);
-          d[1].add(h[k], w, 1);
+          d.add(h[k], w);
         }
         // onto base, in its place
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
           T* const at = bs + (row_warp * 16 + lane / 4 + i % 2 * 8) * S::kPitch + c + i / 2 * 8 + lane % 4 * 2;
-          at[0] = from_f32<T>(to_f32(at[0]) + d[i / 2].at(i % 2 * 2));
-          at[1] = from_f32<T>(to_f32(at[1]) + d[i / 2].at(i % 2 * 2 + 1));
+          const float2 v = pair_at(at);
+          put_pair(at, v.x + d.at(i / 2, i % 2 * 2), v.y + d.at(i / 2, i % 2 * 2 + 1));
         }
       }
       __syncwarp();
@@ -589,7 +624,8 @@ struct GradShape {
   static constexpr int kM = kRows * kPitch * static_cast<int>(sizeof(T));
   static constexpr int kP = P::kP * kRows * kRankPitch * 2;
   static constexpr int kStage = kM + kP;
-  static constexpr int kSums = kRank * kCols * 4;
+  static constexpr int kSumPitch = kCols + 2;  // threads along either axis of the sums
+  static constexpr int kSums = kRank * kSumPitch * 4;
   static constexpr int kBytes = kStages * kStage > kSums ? kStages * kStage : kSums;
 };
 
@@ -632,7 +668,7 @@ __global__ void __launch_bounds__(kAdapterThreads)
               p + (row0 + (there ? row : 0)) * (P::kP * kRank) + plane * kRank + col, there ? 16 : 0);
     }
   };
-  float acc[S::kWarpCols / 8][4] = {};
+  float acc[S::kWarpCols / 16][2][4] = {};
   auto multiply = [&](int stage) {
     const T* const ms = reinterpret_cast<const T*>(smem + stage * S::kStage);
     const __nv_bfloat16* const ps = reinterpret_cast<const __nv_bfloat16*>(smem + stage * S::kStage + S::kM);
@@ -646,17 +682,7 @@ __global__ void __launch_bounds__(kAdapterThreads)
       for (int n = 0; n < S::kWarpCols / 16; ++n) {
         uint32_t w[P::kW][4];
         cols_operand<T, P::kW, S::kPitch, true>(w, ms, col_warp * S::kWarpCols + n * 16, t);
-#pragma unroll
-        for (int half = 0; half < 2; ++half) {
-          Sum<T> d;
-          if constexpr (sizeof(T) == 2)
-#pragma unroll
-            for (int i = 0; i < 4; ++i) d.high[i] = acc[2 * n + half][i];
-          d.add(h, w, half);
-#pragma unroll
-          for (int i = 0; i < 4; ++i)
-            acc[2 * n + half][i] = sizeof(T) == 2 ? d.high[i] : acc[2 * n + half][i] + d.at(i);
-        }
+        add_onto<T, P::kP, P::kW, false>(acc[n], h, w);
       }
     }
   };
@@ -715,13 +741,13 @@ __global__ void __launch_bounds__(kAdapterThreads)
   }
 
   // the parts' sums in a fixed order, and the result
-  float* const sums = reinterpret_cast<float*>(smem);  // [rank][cols]
+  float* const sums = reinterpret_cast<float*>(smem);  // [rank][kSumPitch]
 #pragma unroll
   for (int n = 0; n < S::kWarpCols / 8; ++n)
 #pragma unroll
     for (int half = 0; half < 2; ++half)
-      *reinterpret_cast<float2*>(sums + (rank_warp * 16 + lane / 4 + half * 8) * S::kCols + col_warp * S::kWarpCols + n * 8 + lane % 4 * 2) =
-          make_float2(acc[n][half * 2], acc[n][half * 2 + 1]);
+      *reinterpret_cast<float2*>(sums + (rank_warp * 16 + lane / 4 + half * 8) * S::kSumPitch + col_warp * S::kWarpCols + n * 8 + lane % 4 * 2) =
+          make_float2(acc[n / 2][n % 2][half * 2], acc[n / 2][n % 2][half * 2 + 1]);
   if (a.parts > 1) cluster_meet();
   else __syncthreads();
   T* const out = a.out[sel];
@@ -732,9 +758,9 @@ __global__ void __launch_bounds__(kAdapterThreads)
     const int r = sel ? at % kRank : at / S::kCols, c = sel ? at / kRank : at % S::kCols;
     if (r >= static_cast<int>(a.rank) || col0 + c >= cols) continue;
     float v = 0.f;
-    if (a.parts == 1) v = sums[r * S::kCols + c];
+    if (a.parts == 1) v = sums[r * S::kSumPitch + c];
     else
-      for (uint32_t q = 0; q < a.parts; ++q) v += remote_f32(smem_u32(sums + r * S::kCols + c), q);
+      for (uint32_t q = 0; q < a.parts; ++q) v += remote_f32(smem_u32(sums + r * S::kSumPitch + c), q);
     const uint64_t to_at = sel ? (adapter * cols + col0 + c) * a.rank + r : (adapter * a.rank + r) * cols + col0 + c;
     out[to_at] = from_f32<T>(v);
   }
@@ -775,7 +801,7 @@ cudaError_t launch_chain(Chain<T> a, cudaStream_t st) {
   const uint64_t slots = slots_of(a.q.tokens, a.q.requests, kTile);
   const uint64_t tiles = a.q.tokens / kTile + (a.q.requests < a.q.tokens ? a.q.requests : a.q.tokens) + 1;
   a.parts = 1;
-  while (a.parts < kAdapterParts && a.in >= 4ull * a.parts * F::kStep && tiles * a.parts < 8ull * sm_count()) a.parts *= 2;
+  while (a.parts < kAdapterParts && a.in >= 4ull * a.parts * F::kStep && tiles * a.parts < HKV_PM * 1ull * sm_count()) a.parts *= 2;
   a.part_in = ((a.in + a.parts - 1) / a.parts + 63) / 64 * 64;
   a.follows = a.q.requests > 0;
   if (a.follows) {  // (without a request all rows are base's)
@@ -783,8 +809,8 @@ cudaError_t launch_chain(Chain<T> a, cudaStream_t st) {
     if (e != cudaSuccess) return e;
   }
   // blocks for every SM several times over, of up to eight stages
-  uint64_t steps = (a.out + S::kCols - 1) / S::kCols, each = (tiles * steps + 8ull * sm_count() - 1) / (8ull * sm_count());
-  if (each > 8) each = 8;
+  uint64_t steps = (a.out + S::kCols - 1) / S::kCols, each = (tiles * steps + HKV_GM * 1ull * sm_count() - 1) / (HKV_GM * 1ull * sm_count());
+  if (each > HKV_EM) each = HKV_EM;
   a.groups = static_cast<uint32_t>((steps + each - 1) / each);
   a.group_out = each * S::kCols;
   return launch_clusters(second_kernel<T, kRank, kTile, kBack>, a, slots * a.groups, 1, S::kBytes, st);
