@@ -30,13 +30,25 @@
 #include "operators.cuh"
 
 #ifndef HKV_PM
-#define HKV_PM 4
+#define HKV_PM 150
+#endif
+#ifndef HKV_GS
+#define HKV_GS 3
+#endif
+#ifndef HKV_GB
+#define HKV_GB 2
+#endif
+#ifndef HKV_THIN
+#define HKV_THIN 2
+#endif
+#ifndef HKV_GP
+#define HKV_GP 2
 #endif
 #ifndef HKV_GM
 #define HKV_GM 8
 #endif
 #ifndef HKV_EM
-#define HKV_EM 8
+#define HKV_EM 16
 #endif
 #ifndef HKV_S2
 #define HKV_S2 2
@@ -164,11 +176,11 @@ __device__ __forceinline__ void split_pair(float a, float b, uint32_t (&out)[kN]
 
 __device__ __forceinline__ void ldsm(uint32_t (&r)[4], uint32_t addr) {
   asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0,%1,%2,%3}, [%4];"
-               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]) : "r"(addr) : "memory");
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]) : "r"(addr));
 }
 __device__ __forceinline__ void ldsm_t(uint32_t (&r)[4], uint32_t addr) {
   asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0,%1,%2,%3}, [%4];"
-               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]) : "r"(addr) : "memory");
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]) : "r"(addr));
 }
 template <bool kF16>
 __device__ __forceinline__ void mma(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
@@ -477,7 +489,10 @@ struct SecondShape {
   static constexpr int kBase = kTile * kPitch, kSecond = (kBack ? kRank : kCols) * kSecondPitch;
   static constexpr int kStage = kBase + kSecond;  // elements
   static constexpr int kHidden = Planes<T>::kP * kTile * kHiddenPitch * 2;
-  static constexpr int kBytes = kStages * kStage * static_cast<int>(sizeof(T)) + kHidden;
+  // the hidden numbers come by way of the last stage, before it has a tile
+  static constexpr int kHiddenAt = (kStages - 1) * kStage * static_cast<int>(sizeof(T));
+  static constexpr int kLast = kStage * static_cast<int>(sizeof(T));
+  static constexpr int kBytes = kHiddenAt + (kLast > kHidden ? kLast : kHidden);
 };
 
 template <class T, int kRank, int kTile, bool kBack>
@@ -487,7 +502,7 @@ __global__ void __launch_bounds__(kAdapterThreads)
   using P = Planes<T>;
   extern __shared__ __align__(16) uint8_t smem[];
   T* const stages = reinterpret_cast<T*>(smem);
-  __nv_bfloat16* const hidden = reinterpret_cast<__nv_bfloat16*>(smem + S::kStages * S::kStage * sizeof(T));
+  __nv_bfloat16* const hidden = reinterpret_cast<__nv_bfloat16*>(smem + S::kHiddenAt);
   const uint32_t tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const uint32_t row_warp = warp % S::kRowWarps, other = warp / S::kRowWarps;
 
@@ -565,6 +580,7 @@ __global__ void __launch_bounds__(kAdapterThreads)
         // onto base, in its place
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
+          if (kTile == 16 && i % 2 && t.rows <= 8) continue;
           T* const at = bs + (row_warp * 16 + lane / 4 + i % 2 * 8) * S::kPitch + c + i / 2 * 8 + lane % 4 * 2;
           const float2 v = pair_at(at);
           put_pair(at, v.x + d.at(i / 2, i % 2 * 2), v.y + d.at(i / 2, i % 2 * 2 + 1));
@@ -578,8 +594,9 @@ __global__ void __launch_bounds__(kAdapterThreads)
 #pragma unroll
     for (int r = lane / kLanes; r < 16; r += 32 / kLanes) {
       const int row = row_warp * 16 + r;
+      if (row >= t.rows) break;
       const uint64_t col = c0 + lane % kLanes * 8;
-      const int64_t n = row < t.rows ? static_cast<int64_t>(col1 - col) : 0;
+      const int64_t n = col1 - col;
       const T* const from = bs + row * S::kPitch + other * S::kWarpCols + lane % kLanes * 8;
       T* const out = y + row * a.y_stride + col;
       if (n >= 8 && a.y_whole) {
@@ -594,6 +611,174 @@ __global__ void __launch_bounds__(kAdapterThreads)
     }
   }
   copies_wait<0>();
+}
+
+// ---------------------------------------------------------------------------
+// Single tokens: tiles of few rows, whose products are sums over a factor that is
+// read once, past shared memory.
+// ---------------------------------------------------------------------------
+constexpr int kThinRows = 4;
+
+// Eight neighbouring elements, the first n of them and zeros behind.
+template <class T>
+struct Eight16 {
+  uint4 v[sizeof(T) / 2];
+  __device__ __forceinline__ void load(const T* p, int64_t n, bool whole) {
+    if (n >= 8 && whole) {
+#pragma unroll
+      for (int i = 0; i < static_cast<int>(sizeof(T)) / 2; ++i)
+        v[i] = __ldcg(reinterpret_cast<const uint4*>(p + i * (16 / sizeof(T))));
+    } else {
+      T* e = reinterpret_cast<T*>(v);
+#pragma unroll
+      for (int i = 0; i < 8; ++i) e[i] = i < n ? __ldcg(p + i) : from_f32<T>(0.f);
+    }
+  }
+  __device__ __forceinline__ float2 pair(int i) const { return pair_at(reinterpret_cast<const T*>(v) + 2 * i); }
+};
+
+// h = c D x: a warp takes two ranks at a time, its lanes the columns, eight each.
+// Where there are fewer pairs of ranks than warps, the others take other columns.
+template <class T, int kRank>
+__global__ void __launch_bounds__(kAdapterThreads)
+    thin_first_kernel(const __grid_constant__ Chain<T> a) {
+  using P = Planes<T>;
+  constexpr int kWarps = kAdapterThreads / 32, kMost = 4;  // loads of a rank in flight
+  __shared__ __align__(16) float sums[kWarps][kThinRows][kRank];
+  const uint32_t tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  pdl_wait();
+  pdl_trigger();  // as above
+  const uint32_t part = blockIdx.x % a.parts;
+  Tile t;
+  if (!Tile::find<kThinRows>(a.q, blockIdx.x / a.parts, t) || t.adapter < 0) return;  // the whole cluster
+  const uint64_t in0 = min(part * a.part_in, a.in), in1 = min(in0 + a.part_in, a.in);
+  const uint32_t pairs = (a.rank + 1) / 2;
+  uint32_t slices = 1;  // of the columns
+  while (slices * 2 * pairs <= kWarps) slices *= 2;
+  const uint32_t slice = warp % slices;
+  const T* const first = a.first.data + t.adapter * a.first.step;
+  const T* const x = a.x + t.row0 * a.x_stride;
+  for (uint32_t i = tid; i < kWarps * kThinRows * kRank; i += kAdapterThreads) (&sums[0][0][0])[i] = 0.f;
+  __syncthreads();
+  for (uint32_t pair = warp / slices; pair < pairs; pair += kWarps / slices) {
+    const T* const d0 = first + 2 * pair * a.first.stride;
+    const bool two = 2 * pair + 1 < a.rank;
+    float acc[2][kThinRows] = {};
+    for (uint64_t k = in0 + slice * 256 + lane * 8; k < in1; k += slices * 256 * kMost) {
+      Eight16<T> d[2][kMost];
+#pragma unroll
+      for (int u = 0; u < kMost; ++u) {
+        const uint64_t at = k + u * slices * 256;
+        const int64_t n = at < in1 ? static_cast<int64_t>(in1 - at) : 0;
+        d[0][u].load(d0 + at, n, a.first.whole);
+        d[1][u].load(d0 + a.first.stride + at, two ? n : 0, a.first.whole);
+      }
+#pragma unroll
+      for (int row = 0; row < kThinRows; ++row) {
+        if (row >= t.rows) break;
+#pragma unroll
+        for (int u = 0; u < kMost; ++u) {
+          const uint64_t at = k + u * slices * 256;
+          if (at >= in1) break;
+          Eight16<T> e;
+          e.load(x + row * a.x_stride + at, in1 - at, a.x_whole);
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            const float2 v = e.pair(i), p = d[0][u].pair(i), q = d[1][u].pair(i);
+            acc[0][row] = fmaf(v.y, p.y, fmaf(v.x, p.x, acc[0][row]));
+            acc[1][row] = fmaf(v.y, q.y, fmaf(v.x, q.x, acc[1][row]));
+          }
+        }
+      }
+    }
+#pragma unroll
+    for (int row = 0; row < kThinRows; ++row) {
+      if (row >= t.rows) break;
+#pragma unroll
+      for (int r = 0; r < 2; ++r) {
+        float v = acc[r][row];
+        for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xFFFFFFFFu, v, o);
+        if (lane == 0 && (r == 0 || two)) sums[slice][row][2 * pair + r] = v;
+      }
+    }
+  }
+  __syncthreads();
+  const float scale = a.q.scales ? a.q.scales[t.adapter] : 1.f;
+  constexpr int kQuads = kThinRows * kRank / 4;  // one to a thread
+  static_assert(kQuads <= kAdapterThreads);
+  float4* const quads = reinterpret_cast<float4*>(sums);
+  float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
+  if (tid < kQuads) {
+    v = quads[tid];
+    for (uint32_t s = 1; s < slices; ++s) v = v + quads[s * kQuads + tid];
+  }
+  if (a.parts > 1) {
+    if (tid < kQuads) quads[tid] = v;
+    cluster_meet();
+    if (part == 0 && tid < kQuads)
+      for (uint32_t p = 1; p < a.parts; ++p) v = v + remote_f32x4(smem_u32(quads + tid), p);
+    cluster_meet();  // the others stay until their sums are read
+  }
+  const int row = tid * 4 / kRank, col = tid * 4 % kRank;
+  if (part || tid >= kQuads || row >= t.rows) return;
+  uint32_t lo[P::kP], hi[P::kP];
+  split_pair<P::kP>(v.x * scale, v.y * scale, lo);
+  split_pair<P::kP>(v.z * scale, v.w * scale, hi);
+  __nv_bfloat16* const h = a.hidden + (t.row0 + row) * (P::kP * kRank) + col;
+#pragma unroll
+  for (int p = 0; p < P::kP; ++p) *reinterpret_cast<uint2*>(h + p * kRank) = make_uint2(lo[p], hi[p]);
+}
+
+// y = base + U h: a column to a thread at a time.
+template <class T, int kRank>
+__global__ void __launch_bounds__(kAdapterThreads)
+    thin_second_kernel(const __grid_constant__ Chain<T> a) {
+  using P = Planes<T>;
+  __shared__ __align__(16) float hidden[kThinRows][kRank];
+  const uint32_t tid = threadIdx.x;
+  if (!a.follows) pdl_wait();
+  const uint64_t col0 = static_cast<uint64_t>(blockIdx.x % a.groups) * a.group_out;
+  const uint64_t col1 = min(col0 + a.group_out, a.out);
+  Tile t;
+  const bool any = Tile::find<kThinRows>(a.q, blockIdx.x / a.groups, t) && col0 < col1;
+  const bool adapts = any && t.adapter >= 0;
+  const T* const second = a.second.data + (adapts ? t.adapter * a.second.step : 0);
+  uint64_t col = col0 + tid;
+  Eight16<T> u[kRank / 8];
+  auto load = [&]() {
+#pragma unroll
+    for (int i = 0; i < kRank / 8; ++i)
+      u[i].load(second + col * a.second.stride + i * 8, adapts && col < col1 ? static_cast<int64_t>(a.rank) - i * 8 : 0,
+                a.second.whole);
+  };
+  load();  // on its way before the first product's end, as above
+  pdl_wait();
+  pdl_trigger();
+  if (!any || (!adapts && a.y == a.base)) return;
+  for (uint32_t i = tid; i < kThinRows * kRank; i += kAdapterThreads) {
+    const int row = i / kRank;
+    float v = 0.f;
+    if (adapts && row < t.rows)
+#pragma unroll
+      for (int p = P::kP - 1; p >= 0; --p)
+        v += __bfloat162float(__ldcg(a.hidden + (t.row0 + row) * (P::kP * kRank) + p * kRank + i % kRank));
+    hidden[row][i % kRank] = v;
+  }
+  __syncthreads();
+  for (; col < col1; col += kAdapterThreads, load()) {
+#pragma unroll
+    for (int row = 0; row < kThinRows; ++row) {
+      if (row >= t.rows) break;
+      float v = a.base ? to_f32(a.base[(t.row0 + row) * a.base_stride + col]) : 0.f, w = 0.f;
+#pragma unroll
+      for (int i = 0; i < kRank / 2; i += 2) {
+        const float4 h = *reinterpret_cast<const float4*>(&hidden[row][2 * i]);
+        const float2 p = u[i / 4].pair(i % 4), q = u[i / 4].pair(i % 4 + 1);
+        w = fmaf(h.w, q.y, fmaf(h.z, q.x, fmaf(h.y, p.y, fmaf(h.x, p.x, w))));
+      }
+      a.y[(t.row0 + row) * a.y_stride + col] = from_f32<T>(v + w);
+    }
+  }
 }
 
 // ---------------------------------------------------------------------------
@@ -618,19 +803,19 @@ template <class T, int kRank>
 struct GradShape {
   using P = Planes<T>;
   static constexpr int kRows = 64, kCols = 128;
-  static constexpr int kStages = sizeof(T) == 4 ? 2 : 3;
+  static constexpr int kStages = sizeof(T) == 4 ? 2 : HKV_GS;
   static constexpr int kRankWarps = kRank / 16, kColWarps = 8 / kRankWarps, kWarpCols = kCols / kColWarps;
   static constexpr int kRankPitch = kRank + 8, kPitch = kCols + 8;
   static constexpr int kM = kRows * kPitch * static_cast<int>(sizeof(T));
   static constexpr int kP = P::kP * kRows * kRankPitch * 2;
   static constexpr int kStage = kM + kP;
-  static constexpr int kSumPitch = kCols + 2;  // threads along either axis of the sums
+  static constexpr int kSumPitch = kCols + 4;  // threads go along either axis of the sums
   static constexpr int kSums = kRank * kSumPitch * 4;
-  static constexpr int kBytes = kStages * kStage > kSums ? kStages * kStage : kSums;
+  static constexpr int kBytes = kStages * kStage > 2 * kSums ? kStages * kStage : 2 * kSums;  // own and joined
 };
 
 template <class T, int kRank>
-__global__ void __launch_bounds__(kAdapterThreads)
+__global__ void __launch_bounds__(kAdapterThreads, sizeof(T) == 2 ? HKV_GB : 1)
     grads_kernel(const __grid_constant__ Grads<T> a) {
   using S = GradShape<T, kRank>;
   using P = Planes<T>;
@@ -748,21 +933,27 @@ __global__ void __launch_bounds__(kAdapterThreads)
     for (int half = 0; half < 2; ++half)
       *reinterpret_cast<float2*>(sums + (rank_warp * 16 + lane / 4 + half * 8) * S::kSumPitch + col_warp * S::kWarpCols + n * 8 + lane % 4 * 2) =
           make_float2(acc[n / 2][n % 2][half * 2], acc[n / 2][n % 2][half * 2 + 1]);
-  if (a.parts > 1) cluster_meet();
-  else __syncthreads();
+  // a part's share are whole rows (ranks)
+  const int each = kRank / a.parts, r0 = part * each;
+  if (a.parts > 1) {
+    cluster_meet();
+    constexpr int kQuads = S::kCols / 4;
+    for (int e = tid; e < each * kQuads; e += kThreads) {
+      const uint32_t at = smem_u32(sums + (r0 + e / kQuads) * S::kSumPitch + e % kQuads * 4);
+      float4 v = remote_f32x4(at, 0);
+      for (uint32_t q = 1; q < a.parts; ++q) v = v + remote_f32x4(at, q);
+      reinterpret_cast<float4*>(sums + S::kSums / 4 + e / kQuads * S::kSumPitch)[e % kQuads] = v;
+    }
+  }
+  __syncthreads();
+  const float* const total = a.parts > 1 ? sums + S::kSums / 4 : sums;
   T* const out = a.out[sel];
-  const int each = kRank * S::kCols / a.parts;
-  for (int e = tid; e < each; e += kThreads) {
+  for (int e = tid; e < each * S::kCols; e += kThreads) {
     // neighbouring threads write neighbouring elements of either layout
-    const int at = part * each + e;
-    const int r = sel ? at % kRank : at / S::kCols, c = sel ? at / kRank : at % S::kCols;
-    if (r >= static_cast<int>(a.rank) || col0 + c >= cols) continue;
-    float v = 0.f;
-    if (a.parts == 1) v = sums[r * S::kSumPitch + c];
-    else
-      for (uint32_t q = 0; q < a.parts; ++q) v += remote_f32(smem_u32(sums + r * S::kSumPitch + c), q);
-    const uint64_t to_at = sel ? (adapter * cols + col0 + c) * a.rank + r : (adapter * a.rank + r) * cols + col0 + c;
-    out[to_at] = from_f32<T>(v);
+    const int r = sel ? e % each : e / S::kCols, c = sel ? e / each : e % S::kCols;
+    if (r0 + r >= static_cast<int>(a.rank) || col0 + c >= cols) continue;
+    const uint64_t to_at = sel ? (adapter * cols + col0 + c) * a.rank + r0 + r : (adapter * a.rank + r0 + r) * cols + col0 + c;
+    out[to_at] = from_f32<T>(total[r * S::kSumPitch + c]);
   }
   if (a.parts > 1) cluster_meet();  // the others stay until their parts are read
 }
@@ -801,7 +992,9 @@ cudaError_t launch_chain(Chain<T> a, cudaStream_t st) {
   const uint64_t slots = slots_of(a.q.tokens, a.q.requests, kTile);
   const uint64_t tiles = a.q.tokens / kTile + (a.q.requests < a.q.tokens ? a.q.requests : a.q.tokens) + 1;
   a.parts = 1;
-  while (a.parts < kAdapterParts && a.in >= 4ull * a.parts * F::kStep && tiles * a.parts < HKV_PM * 1ull * sm_count()) a.parts *= 2;
+  // all blocks at once on the SMs, each with four stages of columns at least
+  const uint64_t room = sm_count() * (HKV_PM * 227ull * 1024 / (F::kBytes + 1024)) / 100;
+  while (a.parts < kAdapterParts && a.in >= 4ull * a.parts * F::kStep && 2 * tiles * a.parts <= room) a.parts *= 2;
   a.part_in = ((a.in + a.parts - 1) / a.parts + 63) / 64 * 64;
   a.follows = a.q.requests > 0;
   if (a.follows) {  // (without a request all rows are base's)
@@ -816,8 +1009,30 @@ cudaError_t launch_chain(Chain<T> a, cudaStream_t st) {
   return launch_clusters(second_kernel<T, kRank, kTile, kBack>, a, slots * a.groups, 1, S::kBytes, st);
 }
 
+template <class T, int kRank>
+cudaError_t launch_thin(Chain<T> a, cudaStream_t st) {
+  const uint64_t slots = slots_of(a.q.tokens, a.q.requests, kThinRows);
+  // few tokens: clusters share their columns, a round of a block's loads to each
+  a.parts = 1;
+  while (a.parts < kAdapterParts && a.in >= 1024ull * a.parts && 2 * a.q.tokens * a.parts <= 1ull * sm_count()) a.parts *= 2;
+  a.part_in = ((a.in + a.parts - 1) / a.parts + 63) / 64 * 64;
+  a.follows = a.q.requests > 0;
+  if (a.follows) {
+    const cudaError_t e = launch_clusters(thin_first_kernel<T, kRank>, a, slots * a.parts, a.parts, 0, st);
+    if (e != cudaSuccess) return e;
+  }
+  const uint64_t steps = (a.out + kAdapterThreads - 1) / kAdapterThreads;
+  uint64_t each = (a.q.tokens * steps + 8ull * sm_count() - 1) / (8ull * sm_count());
+  if (each > 8) each = 8;
+  a.groups = static_cast<uint32_t>((steps + each - 1) / each);
+  a.group_out = each * kAdapterThreads;
+  return launch_clusters(thin_second_kernel<T, kRank>, a, slots * a.groups, 1, 0, st);
+}
+
 template <class T, bool kBack>
 cudaError_t chain(const Chain<T>& a, cudaStream_t st) {
+  if (!kBack && a.q.tokens <= HKV_THIN * a.q.requests)
+    return a.rank <= 16 ? launch_thin<T, 16>(a, st) : a.rank <= 32 ? launch_thin<T, 32>(a, st) : launch_thin<T, 64>(a, st);
   const bool tall = a.q.tokens >= 32 * a.q.requests;
   if (a.rank <= 16) return tall ? launch_chain<T, 16, 64, kBack>(a, st) : launch_chain<T, 16, 16, kBack>(a, st);
   if (a.rank <= 32) return tall ? launch_chain<T, 32, 64, kBack>(a, st) : launch_chain<T, 32, 16, kBack>(a, st);
@@ -832,9 +1047,9 @@ cudaError_t launch_grads(Grads<T> a, cudaStream_t st) {
   const uint64_t blocks = a.q.adapters * (a.blocks[0] + a.blocks[1]);
   if (!blocks) return cudaSuccess;
   a.parts = 1;
-  while (a.parts < kAdapterParts && blocks * a.parts < 4ull * sm_count() &&
+  while (a.parts < kAdapterParts && blocks * a.parts < HKV_GP * 1ull * sm_count() &&
          a.q.tokens >= 2ull * a.parts * S::kRows)
-    a.parts *= 2;
+    a.parts *= 2;  // (kRank is a multiple of it)
   return launch_clusters(grads_kernel<T, kRank>, a, blocks * a.parts, a.parts, S::kBytes, st);
 }
 template <class T>
