@@ -35,11 +35,17 @@
 #ifndef HKV_GS
 #define HKV_GS 3
 #endif
-#ifndef HKV_GB
-#define HKV_GB 2
-#endif
 #ifndef HKV_THIN
-#define HKV_THIN 2
+#define HKV_THIN 1
+#endif
+#ifndef HKV_TP
+#define HKV_TP 1
+#endif
+#ifndef HKV_TB
+#define HKV_TB 2
+#endif
+#ifndef HKV_TC
+#define HKV_TC 2
 #endif
 #ifndef HKV_GP
 #define HKV_GP 2
@@ -89,24 +95,45 @@ struct Requests {
   }
 };
 
-// Tiles of kTile rows: segment s has the slots start(s) / kTile + s up to
-// start(s + 1) / kTile + s + 1, at least as many as it has tiles, so that a block
-// finds its rows by one search and no list of tiles has to be made.
-template <int kTile>
-__device__ __forceinline__ uint64_t find_segment(const Requests& q, uint64_t slot) {
-  const uint32_t lane = threadIdx.x & 31;
-  uint64_t lo = 0, hi = q.requests + 2;
-  while (hi - lo > 1) {  // every turn leaves a thirty-second part
-    const uint64_t step = (hi - lo + 31) / 32, at = lo + (lane + 1) * step;
-    const bool before = at < hi && q.start(at) / kTile + at <= slot;
-    const uint64_t n = __popc(__ballot_sync(0xFFFFFFFFu, before));
-    lo += n * step;
-    hi = min(lo + step, hi);
+// The rows of a block's tile.  Segment s has the slots start(s) / kTile + s up to
+// start(s + 1) / kTile + s + 1, at least as many as it has tiles of kTile rows, so
+// that a block finds its rows by one search and no list of tiles has to be made.
+// (Tiles of one row: as many slots as rows.)
+struct Tile {
+  uint64_t row0;
+  int rows;
+  int64_t adapter;
+  template <int kTile>
+  static __device__ __forceinline__ uint64_t first_slot(uint64_t start, uint64_t seg) {
+    return kTile == 1 ? start : start / kTile + seg;
   }
-  return lo;
-}
+  // False where the slot has none.  All threads of a warp call it.
+  template <int kTile>
+  __device__ __forceinline__ static bool find(const Requests& q, uint64_t slot, Tile& t) {
+    const uint32_t lane = threadIdx.x & 31;
+    uint64_t lo = 0, hi = q.requests + 2;  // the segment is one of lo .. hi - 1
+    while (hi - lo > 31) {  // every turn leaves a thirty-second part
+      const uint64_t step = (hi - lo + 31) / 32, at = lo + (lane + 1) * step;
+      const bool before = at < hi && first_slot<kTile>(q.start(at), at) <= slot;
+      const uint64_t n = __popc(__ballot_sync(0xFFFFFFFFu, before));
+      lo += n * step;
+      hi = min(lo + step, hi);
+    }
+    // the last ones all at once, with the next one's start and their adapters
+    const uint64_t at = lo + lane, start = at <= hi ? q.start(at) : 0;
+    const int64_t mine = at < hi ? q.adapter(at) : -1;
+    const uint32_t before = __ballot_sync(0xFFFFFFFFu, at < hi && first_slot<kTile>(start, at) <= slot);
+    const int seg = max(__popc(before) - 1, 0);
+    const uint64_t from = __shfl_sync(0xFFFFFFFFu, start, seg), to = __shfl_sync(0xFFFFFFFFu, start, seg + 1);
+    t.adapter = __shfl_sync(0xFFFFFFFFu, mine, seg);
+    t.row0 = from + (slot - first_slot<kTile>(from, lo + seg)) * kTile;
+    if (t.row0 < from || t.row0 >= to) return false;
+    t.rows = static_cast<int>(min(to - t.row0, static_cast<uint64_t>(kTile)));
+    return true;
+  }
+};
 inline uint64_t slots_of(uint64_t tokens, uint64_t requests, int tile) {
-  return tokens / tile + requests + 2;
+  return tile == 1 ? tokens : tokens / tile + requests + 2;
 }
 
 // ---------------------------------------------------------------------------
@@ -337,23 +364,6 @@ struct Chain {
   uint64_t group_out;     //   and columns of y to each
   bool x_whole, base_whole, y_whole;
   bool follows;           // the second product comes after a first one
-};
-
-// The rows of a block's tile: false where the slot has none.
-struct Tile {
-  uint64_t row0;
-  int rows;
-  int64_t adapter;
-  template <int kTile>
-  __device__ __forceinline__ static bool find(const Requests& q, uint64_t slot, Tile& t) {
-    const uint64_t seg = find_segment<kTile>(q, slot);
-    const uint64_t start = q.start(seg), end = q.start(seg + 1);
-    t.adapter = q.adapter(seg);
-    t.row0 = start + (slot - (start / kTile + seg)) * kTile;
-    if (t.row0 >= end) return false;
-    t.rows = static_cast<int>(min(end - t.row0, static_cast<uint64_t>(kTile)));
-    return true;
-  }
 };
 
 // ---------------------------------------------------------------------------
@@ -617,22 +627,16 @@ __global__ void __launch_bounds__(kAdapterThreads)
 // Single tokens: tiles of few rows, whose products are sums over a factor that is
 // read once, past shared memory.
 // ---------------------------------------------------------------------------
-constexpr int kThinRows = 4;
+constexpr int kThinRows = 1;
 
-// Eight neighbouring elements, the first n of them and zeros behind.
+// Eight neighbouring elements from a 16-byte boundary on, or zeros.
 template <class T>
-struct Eight16 {
+struct Vector {
   uint4 v[sizeof(T) / 2];
-  __device__ __forceinline__ void load(const T* p, int64_t n, bool whole) {
-    if (n >= 8 && whole) {
+  __device__ __forceinline__ void load(const T* p, bool there) {
 #pragma unroll
-      for (int i = 0; i < static_cast<int>(sizeof(T)) / 2; ++i)
-        v[i] = __ldcg(reinterpret_cast<const uint4*>(p + i * (16 / sizeof(T))));
-    } else {
-      T* e = reinterpret_cast<T*>(v);
-#pragma unroll
-      for (int i = 0; i < 8; ++i) e[i] = i < n ? __ldcg(p + i) : from_f32<T>(0.f);
-    }
+    for (int i = 0; i < static_cast<int>(sizeof(T)) / 2; ++i)
+      v[i] = there ? __ldcg(reinterpret_cast<const uint4*>(p + i * (16 / sizeof(T)))) : make_uint4(0, 0, 0, 0);
   }
   __device__ __forceinline__ float2 pair(int i) const { return pair_at(reinterpret_cast<const T*>(v) + 2 * i); }
 };
@@ -640,7 +644,7 @@ struct Eight16 {
 // h = c D x: a warp takes two ranks at a time, its lanes the columns, eight each.
 // Where there are fewer pairs of ranks than warps, the others take other columns.
 template <class T, int kRank>
-__global__ void __launch_bounds__(kAdapterThreads)
+__global__ void __launch_bounds__(kAdapterThreads, HKV_TB)
     thin_first_kernel(const __grid_constant__ Chain<T> a) {
   using P = Planes<T>;
   constexpr int kWarps = kAdapterThreads / 32, kMost = 4;  // loads of a rank in flight
@@ -665,13 +669,12 @@ __global__ void __launch_bounds__(kAdapterThreads)
     const bool two = 2 * pair + 1 < a.rank;
     float acc[2][kThinRows] = {};
     for (uint64_t k = in0 + slice * 256 + lane * 8; k < in1; k += slices * 256 * kMost) {
-      Eight16<T> d[2][kMost];
+      Vector<T> d[2][kMost];
 #pragma unroll
       for (int u = 0; u < kMost; ++u) {
         const uint64_t at = k + u * slices * 256;
-        const int64_t n = at < in1 ? static_cast<int64_t>(in1 - at) : 0;
-        d[0][u].load(d0 + at, n, a.first.whole);
-        d[1][u].load(d0 + a.first.stride + at, two ? n : 0, a.first.whole);
+        d[0][u].load(d0 + at, at < in1);
+        d[1][u].load(d0 + a.first.stride + at, two && at < in1);
       }
 #pragma unroll
       for (int row = 0; row < kThinRows; ++row) {
@@ -679,9 +682,8 @@ __global__ void __launch_bounds__(kAdapterThreads)
 #pragma unroll
         for (int u = 0; u < kMost; ++u) {
           const uint64_t at = k + u * slices * 256;
-          if (at >= in1) break;
-          Eight16<T> e;
-          e.load(x + row * a.x_stride + at, in1 - at, a.x_whole);
+          Vector<T> e;
+          e.load(x + row * a.x_stride + at, at < in1);
 #pragma unroll
           for (int i = 0; i < 4; ++i) {
             const float2 v = e.pair(i), p = d[0][u].pair(i), q = d[1][u].pair(i);
@@ -729,29 +731,36 @@ __global__ void __launch_bounds__(kAdapterThreads)
   for (int p = 0; p < P::kP; ++p) *reinterpret_cast<uint2*>(h + p * kRank) = make_uint2(lo[p], hi[p]);
 }
 
-// y = base + U h: a column to a thread at a time.
+// y = base + U h: kEach columns to a thread, whose rows of U and numbers of base (of
+// the first row) are on their way before the first product ends, as above.
 template <class T, int kRank>
-__global__ void __launch_bounds__(kAdapterThreads)
+__host__ __device__ constexpr int thin_columns() { return sizeof(T) == 2 ? 64 / kRank : kRank == 16 ? 2 : 1; }
+template <class T, int kRank>
+__global__ void __launch_bounds__(kAdapterThreads, HKV_TC)
     thin_second_kernel(const __grid_constant__ Chain<T> a) {
   using P = Planes<T>;
+  constexpr int kEach = thin_columns<T, kRank>();
   __shared__ __align__(16) float hidden[kThinRows][kRank];
   const uint32_t tid = threadIdx.x;
   if (!a.follows) pdl_wait();
-  const uint64_t col0 = static_cast<uint64_t>(blockIdx.x % a.groups) * a.group_out;
-  const uint64_t col1 = min(col0 + a.group_out, a.out);
+  const uint64_t col0 = static_cast<uint64_t>(blockIdx.x % a.groups) * (kEach * kAdapterThreads) + tid;
   Tile t;
-  const bool any = Tile::find<kThinRows>(a.q, blockIdx.x / a.groups, t) && col0 < col1;
+  const bool any = Tile::find<kThinRows>(a.q, blockIdx.x / a.groups, t);
   const bool adapts = any && t.adapter >= 0;
   const T* const second = a.second.data + (adapts ? t.adapter * a.second.step : 0);
-  uint64_t col = col0 + tid;
-  Eight16<T> u[kRank / 8];
-  auto load = [&]() {
+  Vector<T> u[kEach][kRank / 8];
+  float base[kEach];
+  auto base_at = [&](int row, uint64_t col) {
+    return a.base && col < a.out ? to_f32(__ldcg(a.base + (t.row0 + row) * a.base_stride + col)) : 0.f;
+  };
+#pragma unroll
+  for (int c = 0; c < kEach; ++c) {
+    const uint64_t col = col0 + c * kAdapterThreads;
 #pragma unroll
     for (int i = 0; i < kRank / 8; ++i)
-      u[i].load(second + col * a.second.stride + i * 8, adapts && col < col1 ? static_cast<int64_t>(a.rank) - i * 8 : 0,
-                a.second.whole);
-  };
-  load();  // on its way before the first product's end, as above
+      u[c][i].load(second + col * a.second.stride + i * 8, adapts && col < a.out && i * 8 < static_cast<int>(a.rank));
+    base[c] = any ? base_at(0, col) : 0.f;
+  }
   pdl_wait();
   pdl_trigger();
   if (!any || (!adapts && a.y == a.base)) return;
@@ -765,18 +774,20 @@ __global__ void __launch_bounds__(kAdapterThreads)
     hidden[row][i % kRank] = v;
   }
   __syncthreads();
-  for (; col < col1; col += kAdapterThreads, load()) {
+  for (int row = 0; row < t.rows; ++row) {
 #pragma unroll
-    for (int row = 0; row < kThinRows; ++row) {
-      if (row >= t.rows) break;
-      float v = a.base ? to_f32(a.base[(t.row0 + row) * a.base_stride + col]) : 0.f, w = 0.f;
+    for (int c = 0; c < kEach; ++c) {
+      const uint64_t col = col0 + c * kAdapterThreads;
+      if (col >= a.out) break;
+      const float b = row ? base_at(row, col) : base[c];
+      float w = 0.f;
 #pragma unroll
       for (int i = 0; i < kRank / 2; i += 2) {
         const float4 h = *reinterpret_cast<const float4*>(&hidden[row][2 * i]);
-        const float2 p = u[i / 4].pair(i % 4), q = u[i / 4].pair(i % 4 + 1);
+        const float2 p = u[c][i / 4].pair(i % 4), q = u[c][i / 4].pair(i % 4 + 1);
         w = fmaf(h.w, q.y, fmaf(h.z, q.x, fmaf(h.y, p.y, fmaf(h.x, p.x, w))));
       }
-      a.y[(t.row0 + row) * a.y_stride + col] = from_f32<T>(v + w);
+      a.y[(t.row0 + row) * a.y_stride + col] = from_f32<T>(b + w);
     }
   }
 }
@@ -802,8 +813,9 @@ struct Grads {
 template <class T, int kRank>
 struct GradShape {
   using P = Planes<T>;
-  static constexpr int kRows = 64, kCols = 128;
+  static constexpr int kRows = sizeof(T) == 4 ? 32 : 64, kCols = 128;
   static constexpr int kStages = sizeof(T) == 4 ? 2 : HKV_GS;
+  static constexpr int kBlocks = sizeof(T) == 4 && kRank == 16 ? 3 : 2;  // of an SM
   static constexpr int kRankWarps = kRank / 16, kColWarps = 8 / kRankWarps, kWarpCols = kCols / kColWarps;
   static constexpr int kRankPitch = kRank + 8, kPitch = kCols + 8;
   static constexpr int kM = kRows * kPitch * static_cast<int>(sizeof(T));
@@ -815,7 +827,7 @@ struct GradShape {
 };
 
 template <class T, int kRank>
-__global__ void __launch_bounds__(kAdapterThreads, sizeof(T) == 2 ? HKV_GB : 1)
+__global__ void __launch_bounds__(kAdapterThreads, GradShape<T, kRank>::kBlocks)
     grads_kernel(const __grid_constant__ Grads<T> a) {
   using S = GradShape<T, kRank>;
   using P = Planes<T>;
@@ -854,11 +866,16 @@ __global__ void __launch_bounds__(kAdapterThreads, sizeof(T) == 2 ? HKV_GB : 1)
     }
   };
   float acc[S::kWarpCols / 16][2][4] = {};
+  int in_stage[S::kStages];  // rows of the tile there
   auto multiply = [&](int stage) {
+    int rows = in_stage[0];
+#pragma unroll
+    for (int i = 1; i < S::kStages; ++i) rows = stage == i ? in_stage[i] : rows;
     const T* const ms = reinterpret_cast<const T*>(smem + stage * S::kStage);
     const __nv_bfloat16* const ps = reinterpret_cast<const __nv_bfloat16*>(smem + stage * S::kStage + S::kM);
 #pragma unroll
     for (int t = 0; t < S::kRows; t += 16) {
+      if (t >= rows) break;
       uint32_t h[P::kP][4];  // rows of the product are ranks
 #pragma unroll
       for (int i = 0; i < P::kP; ++i)
@@ -902,7 +919,10 @@ __global__ void __launch_bounds__(kAdapterThreads, sizeof(T) == 2 ? HKV_GB : 1)
         const uint64_t row0 = row;
         row += S::kRows;
         if (tile++ % a.parts != part) continue;
-        load(stage, row0, static_cast<int>(min(to[i] - row0, static_cast<uint64_t>(S::kRows))));
+        const int rows = static_cast<int>(min(to[i] - row0, static_cast<uint64_t>(S::kRows)));
+        load(stage, row0, rows);
+#pragma unroll
+        for (int j = 0; j < S::kStages; ++j) in_stage[j] = stage == j ? rows : in_stage[j];
         return true;
       }
       return false;
@@ -1014,25 +1034,23 @@ cudaError_t launch_thin(Chain<T> a, cudaStream_t st) {
   const uint64_t slots = slots_of(a.q.tokens, a.q.requests, kThinRows);
   // few tokens: clusters share their columns, a round of a block's loads to each
   a.parts = 1;
-  while (a.parts < kAdapterParts && a.in >= 1024ull * a.parts && 2 * a.q.tokens * a.parts <= 1ull * sm_count()) a.parts *= 2;
+  while (a.parts < kAdapterParts && a.in >= 1024ull * a.parts && a.q.tokens * a.parts <= HKV_TP * 1ull * sm_count()) a.parts *= 2;
   a.part_in = ((a.in + a.parts - 1) / a.parts + 63) / 64 * 64;
   a.follows = a.q.requests > 0;
   if (a.follows) {
     const cudaError_t e = launch_clusters(thin_first_kernel<T, kRank>, a, slots * a.parts, a.parts, 0, st);
     if (e != cudaSuccess) return e;
   }
-  const uint64_t steps = (a.out + kAdapterThreads - 1) / kAdapterThreads;
-  uint64_t each = (a.q.tokens * steps + 8ull * sm_count() - 1) / (8ull * sm_count());
-  if (each > 8) each = 8;
-  a.groups = static_cast<uint32_t>((steps + each - 1) / each);
-  a.group_out = each * kAdapterThreads;
+  constexpr uint64_t kCols = thin_columns<T, kRank>() * kAdapterThreads;
+  a.groups = static_cast<uint32_t>((a.out + kCols - 1) / kCols);
   return launch_clusters(thin_second_kernel<T, kRank>, a, slots * a.groups, 1, 0, st);
 }
 
 template <class T, bool kBack>
 cudaError_t chain(const Chain<T>& a, cudaStream_t st) {
-  if (!kBack && a.q.tokens <= HKV_THIN * a.q.requests)
-    return a.rank <= 16 ? launch_thin<T, 16>(a, st) : a.rank <= 32 ? launch_thin<T, 32>(a, st) : launch_thin<T, 64>(a, st);
+  if constexpr (!kBack)
+    if (a.q.tokens <= HKV_THIN * a.q.requests && a.x_whole && a.first.whole && a.second.whole && a.in % 8 == 0 && a.rank % 8 == 0)
+      return a.rank <= 16 ? launch_thin<T, 16>(a, st) : a.rank <= 32 ? launch_thin<T, 32>(a, st) : launch_thin<T, 64>(a, st);
   const bool tall = a.q.tokens >= 32 * a.q.requests;
   if (a.rank <= 16) return tall ? launch_chain<T, 16, 64, kBack>(a, st) : launch_chain<T, 16, 16, kBack>(a, st);
   if (a.rank <= 32) return tall ? launch_chain<T, 32, 64, kBack>(a, st) : launch_chain<T, 32, 16, kBack>(a, st);
