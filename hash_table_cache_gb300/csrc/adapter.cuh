@@ -25,6 +25,7 @@
 // way to the tensor core.
 #pragma once
 
+#include <atomic>
 #include <type_traits>
 
 #include "operators.cuh"
@@ -981,13 +982,20 @@ __global__ void __launch_bounds__(kAdapterThreads, GradShape<T, kRank>::kBlocks)
 // ---------------------------------------------------------------------------
 // launches
 // ---------------------------------------------------------------------------
-template <class A>
-cudaError_t launch_clusters(void (*kernel)(A), const A& args, uint64_t blocks, uint32_t parts, int smem,
-                            cudaStream_t st) {
+template <auto kKernel, class A>
+cudaError_t launch_clusters(const A& args, uint64_t blocks, uint32_t parts, int smem, cudaStream_t st) {
   if (blocks > 0x7FFFFFFFull) return cudaErrorInvalidValue;
-  if (smem > 40 * 1024) {  // static shared memory counts too
-    const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+  if (smem > 40 * 1024) {  // static shared memory counts too; once for each device
+    static std::atomic<uint64_t> allowed{0};
+    int device = 0;
+    cudaError_t e = cudaGetDevice(&device);
     if (e != cudaSuccess) return e;
+    const uint64_t bit = device < 64 ? 1ull << device : 0;
+    if (!(allowed.load(std::memory_order_relaxed) & bit)) {
+      e = cudaFuncSetAttribute(kKernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+      if (e != cudaSuccess) return e;
+      allowed.fetch_or(bit, std::memory_order_relaxed);
+    }
   }
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(static_cast<unsigned>(blocks));
@@ -1002,7 +1010,7 @@ cudaError_t launch_clusters(void (*kernel)(A), const A& args, uint64_t blocks, u
   attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
   cfg.attrs = attr;
   cfg.numAttrs = parts > 1 ? 2 : 1;
-  return cudaLaunchKernelEx(&cfg, kernel, args);
+  return cudaLaunchKernelEx(&cfg, kKernel, args);
 }
 
 template <class T, int kRank, int kTile, bool kBack>
@@ -1018,7 +1026,7 @@ cudaError_t launch_chain(Chain<T> a, cudaStream_t st) {
   a.part_in = ((a.in + a.parts - 1) / a.parts + 63) / 64 * 64;
   a.follows = a.q.requests > 0;
   if (a.follows) {  // (without a request all rows are base's)
-    const cudaError_t e = launch_clusters(first_kernel<T, kRank, kTile, kBack>, a, slots * a.parts, a.parts, F::kBytes, st);
+    const cudaError_t e = launch_clusters<first_kernel<T, kRank, kTile, kBack>>(a, slots * a.parts, a.parts, F::kBytes, st);
     if (e != cudaSuccess) return e;
   }
   // blocks for every SM several times over, of up to eight stages
@@ -1026,7 +1034,7 @@ cudaError_t launch_chain(Chain<T> a, cudaStream_t st) {
   if (each > HKV_EM) each = HKV_EM;
   a.groups = static_cast<uint32_t>((steps + each - 1) / each);
   a.group_out = each * S::kCols;
-  return launch_clusters(second_kernel<T, kRank, kTile, kBack>, a, slots * a.groups, 1, S::kBytes, st);
+  return launch_clusters<second_kernel<T, kRank, kTile, kBack>>(a, slots * a.groups, 1, S::kBytes, st);
 }
 
 template <class T, int kRank>
@@ -1038,12 +1046,12 @@ cudaError_t launch_thin(Chain<T> a, cudaStream_t st) {
   a.part_in = ((a.in + a.parts - 1) / a.parts + 63) / 64 * 64;
   a.follows = a.q.requests > 0;
   if (a.follows) {
-    const cudaError_t e = launch_clusters(thin_first_kernel<T, kRank>, a, slots * a.parts, a.parts, 0, st);
+    const cudaError_t e = launch_clusters<thin_first_kernel<T, kRank>>(a, slots * a.parts, a.parts, 0, st);
     if (e != cudaSuccess) return e;
   }
   constexpr uint64_t kCols = thin_columns<T, kRank>() * kAdapterThreads;
   a.groups = static_cast<uint32_t>((a.out + kCols - 1) / kCols);
-  return launch_clusters(thin_second_kernel<T, kRank>, a, slots * a.groups, 1, 0, st);
+  return launch_clusters<thin_second_kernel<T, kRank>>(a, slots * a.groups, 1, 0, st);
 }
 
 template <class T, bool kBack>
@@ -1068,7 +1076,7 @@ cudaError_t launch_grads(Grads<T> a, cudaStream_t st) {
   while (a.parts < kAdapterParts && blocks * a.parts < HKV_GP * 1ull * sm_count() &&
          a.q.tokens >= 2ull * a.parts * S::kRows)
     a.parts *= 2;  // (kRank is a multiple of it)
-  return launch_clusters(grads_kernel<T, kRank>, a, blocks * a.parts, a.parts, S::kBytes, st);
+  return launch_clusters<grads_kernel<T, kRank>>(a, blocks * a.parts, a.parts, S::kBytes, st);
 }
 template <class T>
 cudaError_t grads(const Grads<T>& a, cudaStream_t st) {

@@ -24,7 +24,6 @@ stream or the device has to change.
 from __future__ import annotations
 
 from array import array
-from ctypes import addressof
 from operator import attrgetter
 
 import torch
@@ -372,22 +371,24 @@ def _token_logps(s, logits, labels, top):
     device = logits.device
     kind = _type(logits, "logits")
     rows, vocab, stride = _matrix(logits, "logits")
-    if not 0 <= top <= min(vocab, _abi.MAX_TOP):
+    if not 0 <= top <= _abi.MAX_TOP or top > vocab:
         raise ValueError(f"top: 0 to {min(vocab, _abi.MAX_TOP)}, not {top}")
+    empty, f32 = torch.empty, torch.float32
     f = TokenLogps()
     f.logits, f.labels = logits, labels
-    f.logps = f.top_logps = f.top_ids = None
+    f.entropy = entropy = empty(rows, dtype=f32, device=device)
+    f._lse = lse = empty(2 * rows, dtype=f32, device=device)
+    f.logps = f.top_logps = f.top_ids = at_labels = at_logps = at_top = at_ids = None
     if labels is not None:
         _vector(labels, rows, torch.int64, "labels", device)
-        f.logps = torch.empty(rows, dtype=torch.float32, device=device)
-    f.entropy = torch.empty(rows, dtype=torch.float32, device=device)
-    f._lse = torch.empty(2 * rows, dtype=torch.float32, device=device)
+        f.logps = t = empty(rows, dtype=f32, device=device)
+        at_labels, at_logps = labels.data_ptr(), t.data_ptr()
     if top:
-        f.top_logps = torch.empty((rows, top), dtype=torch.float32, device=device)
-        f.top_ids = torch.empty((rows, top), dtype=torch.int64, device=device)
-    at = [None if t is None else t.data_ptr() for t in (labels, f.logps, f.top_logps, f.top_ids)]
-    _ok(_abi.load().hkv_token_logps(rows, vocab, logits.data_ptr(), kind, stride, at[0], top, at[1],
-                                    f.entropy.data_ptr(), at[2], at[3], f._lse.data_ptr(), s),
+        f.top_logps = t = empty((rows, top), dtype=f32, device=device)
+        f.top_ids = u = empty((rows, top), dtype=torch.int64, device=device)
+        at_top, at_ids = t.data_ptr(), u.data_ptr()
+    _ok(_abi.load().hkv_token_logps(rows, vocab, logits.data_ptr(), kind, stride, at_labels, top,
+                                    at_logps, entropy.data_ptr(), at_top, at_ids, lse.data_ptr(), s),
         "hkv_token_logps")
     return f
 
@@ -450,64 +451,73 @@ def adapter_matmul(x, down, up, offsets, which, scales=None, base=None, out=None
     return _call(_cuda(x, "x"), stream, _adapter_matmul, x, down, up, offsets, which, scales, base, out)
 
 
-def _thin(t, rows, cols, dtype, what, device):
-    """(step, row stride) of the matrices of one tensor."""
-    if t.dtype != dtype or t.dim() != 3 or t.shape[1:] != (rows, cols):
-        raise ValueError(f"{what}: adapters x {rows} x {cols} of {dtype}")
-    _same(t, device, what)
-    step, stride, one = t.stride()
-    if one != 1 and cols > 1:
+def _given(t, shape, dtype, index, what):
+    """The strides of a tensor that has to have that shape, type and device."""
+    if t.shape != shape or t.dtype != dtype or t.get_device() != index:
+        raise ValueError(f"{what}: {' x '.join(map(str, shape))} of {dtype} on cuda:{index}")
+    return t.stride()
+
+
+def _row_stride(strides, shape, what):
+    """The stride of a matrix's (or of each of some matrices') rows."""
+    if strides[-1] != 1 and shape[-1] > 1:
         raise ValueError(f"{what}: columns have to be adjacent (stride 1)")
-    if stride < cols:
-        if rows > 1:
+    stride = strides[-2]
+    if stride < shape[-1]:
+        if shape[-2] > 1:
             raise ValueError(f"{what}: rows overlap")
-        stride = cols
-    return step, stride
-
-
-def _taken(t, rows, cols, dtype, what, device):
-    """The row stride of a given matrix of that shape and type."""
-    if t.dtype != dtype or t.shape != (rows, cols):
-        raise ValueError(f"{what}: {rows} x {cols} of {dtype}")
-    _same(t, device, what)
-    return _matrix(t, what)[2]
+        stride = shape[-1]
+    return stride
 
 
 def _adapter_matmul(s, x, down, up, offsets, which, scales, base, out):
-    device, dtype = x.device, x.dtype
-    kind = _type(x, "x")
-    tokens, k, x_stride = _matrix(x, "x")
-    if down.dim() != 3 or up.dim() != 3 or down.shape[0] != up.shape[0]:
-        raise ValueError("down, up: adapters x rank x k and adapters x n x rank")
-    count, rank = down.shape[:2]
-    n = up.shape[1]
+    dtype, index = x.dtype, x.get_device()
+    kind = _TYPES.get(dtype)
+    if kind is None or x.dim() != 2 or down.dim() != 3 or up.dim() != 3 or which.dim() != 1:
+        raise ValueError("x: a matrix of float32, bfloat16 or float16; down, up: adapters x rank x k and "
+                         "adapters x n x rank; which: a vector")
+    tokens, k = shape_x = x.shape
+    x_stride = _row_stride(x.stride(), shape_x, "x")
+    count, n, rank = shape_up = up.shape
     if not 1 <= rank <= _abi.MAX_RANK or not k or not n:
-        raise ValueError(f"down: a rank of 1 to {_abi.MAX_RANK}, not {rank}, and k and n of at least 1")
-    down_step, down_stride = _thin(down, rank, k, dtype, "down", device)
-    up_step, up_stride = _thin(up, n, rank, dtype, "up", device)
-    requests = which.numel()
-    _vector(which, requests, torch.int64, "which", device)
-    _vector(offsets, requests + 1, torch.int64, "offsets", device)
+        raise ValueError(f"up: a rank of 1 to {_abi.MAX_RANK}, not {rank}, and k and n of at least 1")
+    shape_down = count, rank, k
+    strides = _given(down, shape_down, dtype, index, "down")
+    down_step, down_stride = strides[0], _row_stride(strides, shape_down, "down")
+    strides = _given(up, shape_up, dtype, index, "up")
+    up_step, up_stride = strides[0], _row_stride(strides, shape_up, "up")
+    requests, = shape = which.shape
+    if (_given(which, shape, torch.int64, index, "which")[0] != 1 and requests > 1) or \
+            (_given(offsets, (requests + 1,), torch.int64, index, "offsets")[0] != 1 and requests):
+        raise ValueError("which, offsets: contiguous vectors")
+    at_scales = at_base = None
+    base_stride = 0
     if scales is not None:
-        _vector(scales, count, torch.float32, "scales", device)
-    base_stride = 0 if base is None else _taken(base, tokens, n, dtype, "base", device)
+        if _given(scales, (count,), torch.float32, index, "scales")[0] != 1 and count > 1:
+            raise ValueError("scales: a contiguous vector")
+        at_scales = scales.data_ptr()
+    shape = tokens, n
+    if base is not None:
+        base_stride = _row_stride(_given(base, shape, dtype, index, "base"), shape, "base")
+        at_base = base.data_ptr()
     f = AdapterMatmul()
     given = out
     if out is None:
-        out = torch.empty((tokens, n), dtype=dtype, device=device)
+        out = torch.empty(shape, dtype=dtype, device=x.device)
         stride = n
     else:
-        stride = _taken(out, tokens, n, dtype, "out", device)
-    f.out = out
-    f._hidden = torch.empty(_abi.adapter_hidden_bytes(tokens, rank, kind), dtype=torch.uint8, device=device)
-    f.x, f.down, f.up, f.offsets, f.which, f.scales = x, down, up, offsets, which, scales
-    f._adapters = _abi.Adapters(count, down.data_ptr(), down_step, down_stride, up.data_ptr(), up_step,
-                                up_stride, None if scales is None else scales.data_ptr(), rank)
-    f._shape = tokens, k, n, kind, x_stride, requests
+        stride = _row_stride(_given(out, shape, dtype, index, "out"), shape, "out")
+    f.out, f.x, f.down, f.up, f.offsets, f.which, f.scales = out, x, down, up, offsets, which, scales
+    f._hidden = hidden = torch.empty(_abi.adapter_hidden_bytes(tokens, rank, kind), dtype=torch.uint8,
+                                     device=x.device)
+    # hkv_adapters
+    f._adapters = adapters = array("Q", (count, down.data_ptr(), down_step, down_stride, up.data_ptr(),
+                                         up_step, up_stride, at_scales or 0, rank))
+    f._shape = tokens, k, n, kind, x_stride, requests, count, rank
     _ok(_abi.load().hkv_adapter_matmul(
-        tokens, k, n, kind, addressof(f._adapters), requests, offsets.data_ptr(), which.data_ptr(),
-        x.data_ptr(), x_stride, None if base is None else base.data_ptr(), base_stride, out.data_ptr(),
-        stride, f._hidden.data_ptr(), s), "hkv_adapter_matmul")
+        tokens, k, n, kind, adapters.buffer_info()[0], requests, offsets.data_ptr(), which.data_ptr(),
+        x.data_ptr(), x_stride, at_base, base_stride, out.data_ptr(), stride, hidden.data_ptr(), s),
+        "hkv_adapter_matmul")
     if given is not None:
         _written(given)
     return f
@@ -521,26 +531,31 @@ def adapter_matmul_backward(f, dout, base=None, out=None, stream=None):
 
 
 def _adapter_matmul_backward(s, f, dout, base, out):
-    x = f.x
-    device, dtype = x.device, x.dtype
-    tokens, k, n, kind, x_stride, requests = f._shape
-    count, rank = f._adapters.count, f._adapters.rank
-    d_stride = _taken(dout, tokens, n, dtype, "dout", device)
-    base_stride = 0 if base is None else _taken(base, tokens, k, dtype, "base", device)
+    x, adapters = f.x, f._adapters
+    dtype, device = x.dtype, x.device
+    index = device.index
+    tokens, k, n, kind, x_stride, requests, count, rank = f._shape
+    shape = tokens, n
+    d_stride = _row_stride(_given(dout, shape, dtype, index, "dout"), shape, "dout")
+    shape = tokens, k
+    at_base, base_stride = None, 0
+    if base is not None:
+        base_stride = _row_stride(_given(base, shape, dtype, index, "base"), shape, "base")
+        at_base = base.data_ptr()
     given = out
     if out is None:
-        out = torch.empty((tokens, k), dtype=dtype, device=device)
+        out = torch.empty(shape, dtype=dtype, device=device)
         stride = k
     else:
-        stride = _taken(out, tokens, k, dtype, "out", device)
+        stride = _row_stride(_given(out, shape, dtype, index, "out"), shape, "out")
     ddown = torch.empty((count, rank, k), dtype=dtype, device=device)
     dup = torch.empty((count, n, rank), dtype=dtype, device=device)
     dhidden = torch.empty_like(f._hidden)
     _ok(_abi.load().hkv_adapter_matmul_backward(
-        tokens, k, n, kind, addressof(f._adapters), requests, f.offsets.data_ptr(), f.which.data_ptr(),
-        x.data_ptr(), x_stride, dout.data_ptr(), d_stride, f._hidden.data_ptr(),
-        None if base is None else base.data_ptr(), base_stride, out.data_ptr(), stride, ddown.data_ptr(),
-        dup.data_ptr(), dhidden.data_ptr(), s), "hkv_adapter_matmul_backward")
+        tokens, k, n, kind, adapters.buffer_info()[0], requests, f.offsets.data_ptr(), f.which.data_ptr(),
+        x.data_ptr(), x_stride, dout.data_ptr(), d_stride, f._hidden.data_ptr(), at_base, base_stride,
+        out.data_ptr(), stride, ddown.data_ptr(), dup.data_ptr(), dhidden.data_ptr(), s),
+        "hkv_adapter_matmul_backward")
     if given is not None:
         _written(given)
     return out, ddown, dup
