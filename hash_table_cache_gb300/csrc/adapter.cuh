@@ -36,8 +36,8 @@
 #ifndef HKV_GS
 #define HKV_GS 3
 #endif
-#ifndef HKV_THIN
-#define HKV_THIN 1
+#ifndef HKV_ROOM
+#define HKV_ROOM 2
 #endif
 #ifndef HKV_TP
 #define HKV_TP 1
@@ -333,6 +333,14 @@ __device__ __forceinline__ void cluster_meet() {
   __syncwarp();
   cluster_sync();
 }
+__device__ __forceinline__ void cluster_arrive() {
+  __syncwarp();
+  asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
+}
+__device__ __forceinline__ void cluster_wait() {
+  __syncwarp();
+  asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
 __device__ __forceinline__ float4 operator+(float4 a, float4 b) {
   return make_float4(a.x + b.x, a.y + b.y, a.z + b.z, a.w + b.w);
 }
@@ -383,22 +391,15 @@ struct FirstShape {
                                     ? kStages * kStage * static_cast<int>(sizeof(T)) : kSums;
 };
 
+// acc = columns in0 .. in1 - 1 of x's tile times the first factor's: a warp's rows
+// by all ranks, from its share of the columns.  All warps are through with the stages
+// when it returns.
 template <class T, int kRank, int kTile, bool kBack>
-__global__ void __launch_bounds__(kAdapterThreads)
-    first_kernel(const __grid_constant__ Chain<T> a) {
+__device__ __forceinline__ void first_product(float (&acc)[kRank / 16][2][4], T* stages, const Chain<T>& a,
+                                              const Tile& t, uint64_t in0, uint64_t in1) {
   using S = FirstShape<T, kRank, kTile, kBack>;
   using P = Planes<T>;
-  extern __shared__ __align__(16) uint8_t smem[];
-  T* const stages = reinterpret_cast<T*>(smem);
-  const uint32_t tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  const uint32_t row_warp = warp % S::kRowWarps, other = warp / S::kRowWarps;
-  pdl_wait();
-  pdl_trigger();  // what the second product reads before it waits is complete from here on
-
-  const uint32_t part = blockIdx.x % a.parts;
-  Tile t;
-  if (!Tile::find<kTile>(a.q, blockIdx.x / a.parts, t) || t.adapter < 0) return;  // the whole cluster
-  const uint64_t in0 = min(part * a.part_in, a.in), in1 = min(in0 + a.part_in, a.in);
+  const uint32_t warp = threadIdx.x >> 5, row_warp = warp % S::kRowWarps, other = warp / S::kRowWarps;
   const T* const x = a.x + t.row0 * a.x_stride;
   const T* const first = a.first.data + t.adapter * a.first.step;
   const int steps = static_cast<int>((in1 - in0 + S::kStep - 1) / S::kStep);
@@ -415,7 +416,10 @@ __global__ void __launch_bounds__(kAdapterThreads)
     }
     copies_end();
   };
-  float acc[kRank / 16][2][4] = {};
+#pragma unroll
+  for (int n = 0; n < kRank / 16; ++n)
+#pragma unroll
+    for (int i = 0; i < 8; ++i) acc[n][i / 4][i % 4] = 0.f;
 #pragma unroll
   for (int s = 0; s + 1 < S::kStages; ++s) load(s);
   for (int step = 0; step < steps; ++step) {
@@ -440,10 +444,12 @@ __global__ void __launch_bounds__(kAdapterThreads)
   }
   copies_wait<0>();
   __syncthreads();
+}
 
-  // the warps' sums, then the blocks', each block a share of them
-  float* const sums = reinterpret_cast<float*>(smem);  // [other][tile][rank]
-  float* const own = sums + S::kOther * kTile * kRank;
+// A warp's sums as sums[other][tile][rank].
+template <int kRank, int kTile>
+__device__ __forceinline__ void put_sums(float* sums, const float (&acc)[kRank / 16][2][4], int other, int row_warp) {
+  const int lane = threadIdx.x & 31;
   float* const to = sums + (other * kTile + row_warp * 16 + lane / 4) * kRank + lane % 4 * 2;
 #pragma unroll
   for (int n = 0; n < kRank / 8; ++n) {
@@ -451,6 +457,28 @@ __global__ void __launch_bounds__(kAdapterThreads)
     *reinterpret_cast<float2*>(to + n * 8) = make_float2(v[0], v[1]);
     *reinterpret_cast<float2*>(to + 8 * kRank + n * 8) = make_float2(v[2], v[3]);
   }
+}
+
+template <class T, int kRank, int kTile, bool kBack>
+__global__ void __launch_bounds__(kAdapterThreads)
+    first_kernel(const __grid_constant__ Chain<T> a) {
+  using S = FirstShape<T, kRank, kTile, kBack>;
+  using P = Planes<T>;
+  extern __shared__ __align__(16) uint8_t smem[];
+  const uint32_t tid = threadIdx.x, warp = tid >> 5;
+  pdl_wait();
+  pdl_trigger();  // what the second product reads before it waits is complete from here on
+  const uint32_t part = blockIdx.x % a.parts;
+  Tile t;
+  if (!Tile::find<kTile>(a.q, blockIdx.x / a.parts, t) || t.adapter < 0) return;  // the whole cluster
+  const uint64_t in0 = min(part * a.part_in, a.in), in1 = min(in0 + a.part_in, a.in);
+  float acc[kRank / 16][2][4];
+  first_product<T, kRank, kTile, kBack>(acc, reinterpret_cast<T*>(smem), a, t, in0, in1);
+
+  // the warps' sums, then the blocks', each block a share of them
+  float* const sums = reinterpret_cast<float*>(smem);  // [other][tile][rank]
+  float* const own = sums + S::kOther * kTile * kRank;
+  put_sums<kRank, kTile>(sums, acc, warp / S::kRowWarps, warp % S::kRowWarps);
   __syncthreads();
   constexpr int kQuads = kTile * kRank / 4;
   const float scale = a.q.scales ? a.q.scales[t.adapter] : 1.f;
@@ -506,6 +534,59 @@ struct SecondShape {
   static constexpr int kBytes = kHiddenAt + (kLast > kHidden ? kLast : kHidden);
 };
 
+// One stage of base, in shared memory, and its columns c0 .. of the second factor
+// behind it: y's columns c0 .. col1 - 1 of the stage.
+template <class T, int kRank, int kTile, bool kBack>
+__device__ __forceinline__ void second_step(T* stage, const uint32_t (&h)[kRank / 16][Planes<T>::kP][4], bool adapts,
+                                            int rows, T* y, uint64_t c0, uint64_t col1, uint64_t stride, bool whole) {
+  using S = SecondShape<T, kRank, kTile, kBack>;
+  using P = Planes<T>;
+  const uint32_t lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const uint32_t row_warp = warp % S::kRowWarps, other = warp / S::kRowWarps;
+  if (adapts) {
+#pragma unroll
+    for (int n = 0; n < S::kWarpCols; n += 16) {
+      const int c = other * S::kWarpCols + n;
+      Sum<T> d;
+#pragma unroll
+      for (int k = 0; k < kRank / 16; ++k) {
+        uint32_t w[P::kW][4];
+        cols_operand<T, P::kW, S::kSecondPitch, kBack>(w, stage + S::kBase, c, k * 16);
+        d.add(h[k], w);
+      }
+      // onto base, in its place
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        if (kTile == 16 && i % 2 && rows <= 8) continue;
+        T* const at = stage + (row_warp * 16 + lane / 4 + i % 2 * 8) * S::kPitch + c + i / 2 * 8 + lane % 4 * 2;
+        const float2 v = pair_at(at);
+        put_pair(at, v.x + d.at(i / 2, i % 2 * 2), v.y + d.at(i / 2, i % 2 * 2 + 1));
+      }
+    }
+    __syncwarp();
+  }
+  // a warp's rows of kWarpCols columns, eight to a lane
+  constexpr int kLanes = S::kWarpCols / 8;
+  const uint64_t col = c0 + other * S::kWarpCols + lane % kLanes * 8;
+#pragma unroll
+  for (int r = lane / kLanes; r < 16; r += 32 / kLanes) {
+    const int row = row_warp * 16 + r;
+    if (row >= rows) break;
+    const int64_t n = col1 - col;
+    const T* const from = stage + row * S::kPitch + other * S::kWarpCols + lane % kLanes * 8;
+    T* const out = y + row * stride + col;
+    if (n >= 8 && whole) {
+#pragma unroll
+      for (int i = 0; i < static_cast<int>(sizeof(T)) / 2; ++i)
+        st_stream_v4(out + i * (16 / sizeof(T)), reinterpret_cast<const uint4*>(from)[i]);
+    } else {
+#pragma unroll
+      for (int i = 0; i < 8; ++i)
+        if (i < n) out[i] = from[i];
+    }
+  }
+}
+
 template <class T, int kRank, int kTile, bool kBack>
 __global__ void __launch_bounds__(kAdapterThreads)
     second_kernel(const __grid_constant__ Chain<T> a) {
@@ -515,7 +596,7 @@ __global__ void __launch_bounds__(kAdapterThreads)
   T* const stages = reinterpret_cast<T*>(smem);
   __nv_bfloat16* const hidden = reinterpret_cast<__nv_bfloat16*>(smem + S::kHiddenAt);
   const uint32_t tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  const uint32_t row_warp = warp % S::kRowWarps, other = warp / S::kRowWarps;
+  const uint32_t row_warp = warp % S::kRowWarps;
 
   // before the first product's end: its kernel lets this one start when all that
   // came before is complete, and it writes `hidden` alone
@@ -575,61 +656,141 @@ __global__ void __launch_bounds__(kAdapterThreads)
     copies_wait<S::kStages - 2>();
     __syncthreads();
     load(step + S::kStages - 1);
-    T* const bs = stages + step % S::kStages * S::kStage;
-    const T* const ws = bs + S::kBase;
-    if (adapts) {
-#pragma unroll
-      for (int n = 0; n < S::kWarpCols; n += 16) {
-        const int c = other * S::kWarpCols + n;
-        Sum<T> d;
-#pragma unroll
-        for (int k = 0; k < kRank / 16; ++k) {
-          uint32_t w[P::kW][4];
-          cols_operand<T, P::kW, S::kSecondPitch, kBack>(w, ws, c, k * 16);
-          d.add(h[k], w);
-        }
-        // onto base, in its place
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          if (kTile == 16 && i % 2 && t.rows <= 8) continue;
-          T* const at = bs + (row_warp * 16 + lane / 4 + i % 2 * 8) * S::kPitch + c + i / 2 * 8 + lane % 4 * 2;
-          const float2 v = pair_at(at);
-          put_pair(at, v.x + d.at(i / 2, i % 2 * 2), v.y + d.at(i / 2, i % 2 * 2 + 1));
-        }
-      }
-      __syncwarp();
-    }
-    // a warp's rows of kWarpCols columns, eight to a lane
-    const uint64_t c0 = col0 + static_cast<uint64_t>(step) * S::kCols + other * S::kWarpCols;
-    constexpr int kLanes = S::kWarpCols / 8;
-#pragma unroll
-    for (int r = lane / kLanes; r < 16; r += 32 / kLanes) {
-      const int row = row_warp * 16 + r;
-      if (row >= t.rows) break;
-      const uint64_t col = c0 + lane % kLanes * 8;
-      const int64_t n = col1 - col;
-      const T* const from = bs + row * S::kPitch + other * S::kWarpCols + lane % kLanes * 8;
-      T* const out = y + row * a.y_stride + col;
-      if (n >= 8 && a.y_whole) {
-#pragma unroll
-        for (int i = 0; i < static_cast<int>(sizeof(T)) / 2; ++i)
-          st_stream_v4(out + i * (16 / sizeof(T)), reinterpret_cast<const uint4*>(from)[i]);
-      } else {
-#pragma unroll
-        for (int i = 0; i < 8; ++i)
-          if (i < n) out[i] = from[i];
-      }
-    }
+    second_step<T, kRank, kTile, kBack>(stages + step % S::kStages * S::kStage, h, adapts, t.rows, y,
+                                        col0 + static_cast<uint64_t>(step) * S::kCols, col1, a.y_stride, a.y_whole);
   }
   copies_wait<0>();
 }
 
 // ---------------------------------------------------------------------------
-// Single tokens: tiles of few rows, whose products are sums over a factor that is
-// read once, past shared memory.
+// Short requests: both products of a tile of 16 rows in one kernel.  A cluster's
+// blocks share the tile's columns of x, put the sums together in every one of them,
+// and share its columns of y.
 // ---------------------------------------------------------------------------
-constexpr int kThinRows = 1;
+template <class T, int kRank, bool kBack>
+struct ShortShape {
+  using F = FirstShape<T, kRank, 16, kBack>;
+  using S = SecondShape<T, kRank, 16, kBack>;
+  static constexpr int kHidden = Planes<T>::kP * 16 * S::kHiddenPitch * 2;
+  // sums, the block's own and the planes lie where the first product's stages were,
+  // the second one's stages behind them
+  static constexpr int kSecondAt = F::kSums + kHidden;
+  static constexpr int kSecond = kSecondAt + S::kStages * S::kStage * static_cast<int>(sizeof(T));
+  static constexpr int kFirst = F::kStages * F::kStage * static_cast<int>(sizeof(T));
+  static constexpr int kBytes = kFirst > kSecond ? kFirst : kSecond;
+};
 
+template <class T, int kRank, bool kBack>
+__global__ void __launch_bounds__(kAdapterThreads)
+    short_kernel(const __grid_constant__ Chain<T> a) {
+  using Shape = ShortShape<T, kRank, kBack>;
+  using F = typename Shape::F;
+  using S = typename Shape::S;
+  using P = Planes<T>;
+  constexpr int kTile = 16;
+  extern __shared__ __align__(16) uint8_t smem[];
+  const uint32_t tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  pdl_trigger();
+  pdl_wait();
+  const uint32_t part = blockIdx.x % a.parts, group = blockIdx.x / a.parts % a.groups;
+  Tile t;
+  if (!Tile::find<kTile>(a.q, blockIdx.x / a.parts / a.groups, t)) return;  // the whole cluster
+  const uint64_t col0 = (static_cast<uint64_t>(group) * a.parts + part) * a.group_out;
+  const uint64_t col1 = min(col0 + a.group_out, a.out);
+  const bool adapts = t.adapter >= 0;
+  if (!adapts && (a.y == a.base || col0 >= col1)) return;  // no block of the cluster meets another
+
+  float* const sums = reinterpret_cast<float*>(smem);  // [warp][tile][rank]
+  float* const own = sums + F::kOther * kTile * kRank;
+  __nv_bfloat16* const hidden = reinterpret_cast<__nv_bfloat16*>(smem + F::kSums);
+  T* const stages = reinterpret_cast<T*>(smem + Shape::kSecondAt);
+  const T* const base = a.base ? a.base + t.row0 * a.base_stride : nullptr;
+  const T* const second = a.second.data + (adapts ? t.adapter * a.second.step : 0);
+  const int col_steps = col0 < col1 ? static_cast<int>((col1 - col0 + S::kCols - 1) / S::kCols) : 0;
+  auto load_second = [&](int step) {
+    if (step < col_steps) {
+      T* const to = stages + step % S::kStages * S::kStage;
+      const uint64_t c = col0 + static_cast<uint64_t>(step) * S::kCols;
+      const int64_t left = col1 - c;
+      copy_tile<T, kTile, S::kCols, S::kPitch>(to, base ? base + c : reinterpret_cast<const T*>(a.hidden), a.base_stride, base ? t.rows : 0, left, a.base_whole);
+      if (adapts) {
+        if constexpr (kBack)
+          copy_tile<T, kRank, S::kCols, S::kSecondPitch>(to + S::kBase, second + c, a.second.stride, a.rank, left, a.second.whole);
+        else
+          copy_tile<T, S::kCols, kRank, S::kSecondPitch>(to + S::kBase, second + c * a.second.stride, a.second.stride, left, a.rank, a.second.whole);
+      }
+    }
+    copies_end();
+  };
+  uint32_t h[kRank / 16][P::kP][4];
+  if (adapts) {
+    const uint64_t in0 = min(part * a.part_in, a.in), in1 = min(in0 + a.part_in, a.in);
+    float acc[kRank / 16][2][4];
+    first_product<T, kRank, kTile, kBack>(acc, reinterpret_cast<T*>(smem), a, t, in0, in1);
+    // (all warps are through with the stages)
+#pragma unroll
+    for (int s = 0; s + 1 < S::kStages; ++s) load_second(s);  // on their way meanwhile
+    put_sums<kRank, kTile>(sums, acc, warp, 0);
+    __syncthreads();
+    constexpr int kQuads = kTile * kRank / 4;
+    static_assert(kQuads <= kAdapterThreads);
+    const float scale = a.q.scales ? a.q.scales[t.adapter] : 1.f;
+    float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
+    if (tid < kQuads) {
+      v = reinterpret_cast<const float4*>(sums)[tid];
+#pragma unroll
+      for (int o = 1; o < F::kOther; ++o) v = v + reinterpret_cast<const float4*>(sums)[o * kQuads + tid];
+    }
+    if (a.parts > 1) {
+      if (tid < kQuads) reinterpret_cast<float4*>(own)[tid] = v;
+      cluster_meet();
+      const uint32_t used = static_cast<uint32_t>((a.in + a.part_in - 1) / a.part_in);  // parts with columns
+      if (tid < kQuads) {
+        v = remote_f32x4(smem_u32(own) + tid * 16, 0);
+        for (uint32_t p = 1; p < used; ++p) v = v + remote_f32x4(smem_u32(own) + tid * 16, p);
+      }
+      cluster_arrive();
+    }
+    if (tid < kQuads) {
+      const int row = tid * 4 / kRank, col = tid * 4 % kRank;
+      uint32_t lo[P::kP], hi[P::kP];
+      split_pair<P::kP>(v.x * scale, v.y * scale, lo);
+      split_pair<P::kP>(v.z * scale, v.w * scale, hi);
+#pragma unroll
+      for (int p = 0; p < P::kP; ++p) {
+        *reinterpret_cast<uint2*>(hidden + (p * kTile + row) * S::kHiddenPitch + col) = make_uint2(lo[p], hi[p]);
+        if (group == 0 && part == 0 && row < t.rows)
+          *reinterpret_cast<uint2*>(a.hidden + (t.row0 + row) * (P::kP * kRank) + p * kRank + col) = make_uint2(lo[p], hi[p]);
+      }
+    }
+    __syncthreads();
+#pragma unroll
+    for (int k = 0; k < kRank / 16; ++k)
+#pragma unroll
+      for (int p = 0; p < P::kP; ++p)
+        ldsm(h[k][p], smem_u32(hidden + (p * kTile + lane % 16) * S::kHiddenPitch + k * 16 + lane / 16 * 8));
+  } else {
+#pragma unroll
+    for (int s = 0; s + 1 < S::kStages; ++s) load_second(s);
+  }
+  T* const y = a.y + t.row0 * a.y_stride;
+  for (int step = 0; step < col_steps; ++step) {
+    copies_wait<S::kStages - 2>();
+    __syncthreads();
+    load_second(step + S::kStages - 1);
+    second_step<T, kRank, kTile, kBack>(stages + step % S::kStages * S::kStage, h, adapts, t.rows, y,
+                                        col0 + static_cast<uint64_t>(step) * S::kCols, col1, a.y_stride, a.y_whole);
+  }
+  copies_wait<0>();
+  if (adapts && a.parts > 1) cluster_wait();  // the others have read this block's sums
+}
+
+// ---------------------------------------------------------------------------
+// Single tokens: one row to a cluster, whose products are sums over factors that are
+// read once, past shared memory.  h = c D x: a warp takes two ranks at a time, its
+// lanes the columns, eight each; where there are fewer pairs of ranks than warps, the
+// others take other columns.  y = base + U h: a column to a thread at a time.
+// ---------------------------------------------------------------------------
 // Eight neighbouring elements from a 16-byte boundary on, or zeros.
 template <class T>
 struct Vector {
@@ -637,160 +798,132 @@ struct Vector {
   __device__ __forceinline__ void load(const T* p, bool there) {
 #pragma unroll
     for (int i = 0; i < static_cast<int>(sizeof(T)) / 2; ++i)
-      v[i] = there ? __ldcg(reinterpret_cast<const uint4*>(p + i * (16 / sizeof(T)))) : make_uint4(0, 0, 0, 0);
+      v[i] = there ? ld_nc_v4(p + i * (16 / sizeof(T))) : make_uint4(0, 0, 0, 0);
   }
   __device__ __forceinline__ float2 pair(int i) const { return pair_at(reinterpret_cast<const T*>(v) + 2 * i); }
 };
 
-// h = c D x: a warp takes two ranks at a time, its lanes the columns, eight each.
-// Where there are fewer pairs of ranks than warps, the others take other columns.
+// Columns of y that a thread has on their way at a time.
 template <class T, int kRank>
-__global__ void __launch_bounds__(kAdapterThreads, HKV_TB)
-    thin_first_kernel(const __grid_constant__ Chain<T> a) {
+__host__ __device__ constexpr int thin_columns() { return kRank == 64 || (kRank == 32 && sizeof(T) == 4) ? 1 : 2; }
+
+template <class T, int kRank>
+__global__ void __launch_bounds__(kAdapterThreads, 2)
+    thin_kernel(const __grid_constant__ Chain<T> a) {
   using P = Planes<T>;
   constexpr int kWarps = kAdapterThreads / 32, kMost = 4;  // loads of a rank in flight
-  __shared__ __align__(16) float sums[kWarps][kThinRows][kRank];
+  constexpr int kEach = thin_columns<T, kRank>();
+  __shared__ __align__(16) float sums[kWarps][kRank], hidden[kRank];
   const uint32_t tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  pdl_trigger();
   pdl_wait();
-  pdl_trigger();  // as above
-  const uint32_t part = blockIdx.x % a.parts;
+  const uint32_t part = blockIdx.x % a.parts, group = blockIdx.x / a.parts % a.groups;
   Tile t;
-  if (!Tile::find<kThinRows>(a.q, blockIdx.x / a.parts, t) || t.adapter < 0) return;  // the whole cluster
-  const uint64_t in0 = min(part * a.part_in, a.in), in1 = min(in0 + a.part_in, a.in);
-  const uint32_t pairs = (a.rank + 1) / 2;
-  uint32_t slices = 1;  // of the columns
-  while (slices * 2 * pairs <= kWarps) slices *= 2;
-  const uint32_t slice = warp % slices;
-  const T* const first = a.first.data + t.adapter * a.first.step;
-  const T* const x = a.x + t.row0 * a.x_stride;
-  for (uint32_t i = tid; i < kWarps * kThinRows * kRank; i += kAdapterThreads) (&sums[0][0][0])[i] = 0.f;
-  __syncthreads();
-  for (uint32_t pair = warp / slices; pair < pairs; pair += kWarps / slices) {
-    const T* const d0 = first + 2 * pair * a.first.stride;
-    const bool two = 2 * pair + 1 < a.rank;
-    float acc[2][kThinRows] = {};
-    for (uint64_t k = in0 + slice * 256 + lane * 8; k < in1; k += slices * 256 * kMost) {
-      Vector<T> d[2][kMost];
+  if (!Tile::find<1>(a.q, blockIdx.x / a.parts / a.groups, t)) return;  // the whole cluster
+  const uint64_t col0 = (static_cast<uint64_t>(group) * a.parts + part) * a.group_out;
+  const uint64_t col1 = min(col0 + a.group_out, a.out);
+  const bool adapts = t.adapter >= 0;
+  if (!adapts && a.y == a.base) return;
+  const T* const second = a.second.data + (adapts ? t.adapter * a.second.step : 0);
+  const T* const base = a.base + t.row0 * a.base_stride;
+  Vector<T> u[kEach][kRank / 8];
+  float onto[kEach];
+  auto load_columns = [&](uint64_t c) {
 #pragma unroll
-      for (int u = 0; u < kMost; ++u) {
-        const uint64_t at = k + u * slices * 256;
-        d[0][u].load(d0 + at, at < in1);
-        d[1][u].load(d0 + a.first.stride + at, two && at < in1);
-      }
+    for (int e = 0; e < kEach; ++e) {
+      const uint64_t col = c + e * kAdapterThreads + tid;
 #pragma unroll
-      for (int row = 0; row < kThinRows; ++row) {
-        if (row >= t.rows) break;
+      for (int i = 0; i < kRank / 8; ++i)
+        u[e][i].load(second + col * a.second.stride + i * 8, adapts && col < col1 && i * 8 < static_cast<int>(a.rank));
+      onto[e] = a.base && col < col1 ? to_f32(base[col]) : 0.f;
+    }
+  };
+  load_columns(col0);  // on their way during the first product
+  if (adapts) {
+    const uint64_t in0 = min(part * a.part_in, a.in), in1 = min(in0 + a.part_in, a.in);
+    const uint32_t pairs = (a.rank + 1) / 2;
+    uint32_t slices = 1;  // of the columns
+    while (slices * 2 * pairs <= kWarps) slices *= 2;
+    const uint32_t slice = warp % slices;
+    const T* const first = a.first.data + t.adapter * a.first.step;
+    const T* const x = a.x + t.row0 * a.x_stride;
+    for (uint32_t i = tid; i < kWarps * kRank; i += kAdapterThreads) (&sums[0][0])[i] = 0.f;
+    __syncthreads();
+    for (uint32_t pair = warp / slices; pair < pairs; pair += kWarps / slices) {
+      const T* const d0 = first + 2 * pair * a.first.stride;
+      const bool two = 2 * pair + 1 < a.rank;
+      float acc[2] = {};
+      for (uint64_t k = in0 + slice * 256 + lane * 8; k < in1; k += slices * 256 * kMost) {
+        Vector<T> d[2][kMost];
 #pragma unroll
-        for (int u = 0; u < kMost; ++u) {
-          const uint64_t at = k + u * slices * 256;
+        for (int m = 0; m < kMost; ++m) {
+          const uint64_t at = k + m * slices * 256;
+          d[0][m].load(d0 + at, at < in1);
+          d[1][m].load(d0 + a.first.stride + at, two && at < in1);
+        }
+#pragma unroll
+        for (int m = 0; m < kMost; ++m) {
+          const uint64_t at = k + m * slices * 256;
           Vector<T> e;
-          e.load(x + row * a.x_stride + at, at < in1);
+          e.load(x + at, at < in1);
 #pragma unroll
           for (int i = 0; i < 4; ++i) {
-            const float2 v = e.pair(i), p = d[0][u].pair(i), q = d[1][u].pair(i);
-            acc[0][row] = fmaf(v.y, p.y, fmaf(v.x, p.x, acc[0][row]));
-            acc[1][row] = fmaf(v.y, q.y, fmaf(v.x, q.x, acc[1][row]));
+            const float2 v = e.pair(i), p = d[0][m].pair(i), q = d[1][m].pair(i);
+            acc[0] = fmaf(v.y, p.y, fmaf(v.x, p.x, acc[0]));
+            acc[1] = fmaf(v.y, q.y, fmaf(v.x, q.x, acc[1]));
           }
         }
       }
-    }
-#pragma unroll
-    for (int row = 0; row < kThinRows; ++row) {
-      if (row >= t.rows) break;
 #pragma unroll
       for (int r = 0; r < 2; ++r) {
-        float v = acc[r][row];
-        for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xFFFFFFFFu, v, o);
-        if (lane == 0 && (r == 0 || two)) sums[slice][row][2 * pair + r] = v;
+        for (int o = 16; o > 0; o >>= 1) acc[r] += __shfl_xor_sync(0xFFFFFFFFu, acc[r], o);
+        if (lane == 0 && (r == 0 || two)) sums[slice][2 * pair + r] = acc[r];
       }
     }
-  }
-  __syncthreads();
-  const float scale = a.q.scales ? a.q.scales[t.adapter] : 1.f;
-  constexpr int kQuads = kThinRows * kRank / 4;  // one to a thread
-  static_assert(kQuads <= kAdapterThreads);
-  float4* const quads = reinterpret_cast<float4*>(sums);
-  float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
-  if (tid < kQuads) {
-    v = quads[tid];
-    for (uint32_t s = 1; s < slices; ++s) v = v + quads[s * kQuads + tid];
-  }
-  if (a.parts > 1) {
-    if (tid < kQuads) quads[tid] = v;
-    cluster_meet();
-    if (part == 0 && tid < kQuads)
-      for (uint32_t p = 1; p < a.parts; ++p) v = v + remote_f32x4(smem_u32(quads + tid), p);
-    cluster_meet();  // the others stay until their sums are read
-  }
-  const int row = tid * 4 / kRank, col = tid * 4 % kRank;
-  if (part || tid >= kQuads || row >= t.rows) return;
-  uint32_t lo[P::kP], hi[P::kP];
-  split_pair<P::kP>(v.x * scale, v.y * scale, lo);
-  split_pair<P::kP>(v.z * scale, v.w * scale, hi);
-  __nv_bfloat16* const h = a.hidden + (t.row0 + row) * (P::kP * kRank) + col;
-#pragma unroll
-  for (int p = 0; p < P::kP; ++p) *reinterpret_cast<uint2*>(h + p * kRank) = make_uint2(lo[p], hi[p]);
-}
-
-// y = base + U h: kEach columns to a thread, whose rows of U and numbers of base (of
-// the first row) are on their way before the first product ends, as above.
-template <class T, int kRank>
-__host__ __device__ constexpr int thin_columns() { return sizeof(T) == 2 ? 64 / kRank : kRank == 16 ? 2 : 1; }
-template <class T, int kRank>
-__global__ void __launch_bounds__(kAdapterThreads, HKV_TC)
-    thin_second_kernel(const __grid_constant__ Chain<T> a) {
-  using P = Planes<T>;
-  constexpr int kEach = thin_columns<T, kRank>();
-  __shared__ __align__(16) float hidden[kThinRows][kRank];
-  const uint32_t tid = threadIdx.x;
-  if (!a.follows) pdl_wait();
-  const uint64_t col0 = static_cast<uint64_t>(blockIdx.x % a.groups) * (kEach * kAdapterThreads) + tid;
-  Tile t;
-  const bool any = Tile::find<kThinRows>(a.q, blockIdx.x / a.groups, t);
-  const bool adapts = any && t.adapter >= 0;
-  const T* const second = a.second.data + (adapts ? t.adapter * a.second.step : 0);
-  Vector<T> u[kEach][kRank / 8];
-  float base[kEach];
-  auto base_at = [&](int row, uint64_t col) {
-    return a.base && col < a.out ? to_f32(__ldcg(a.base + (t.row0 + row) * a.base_stride + col)) : 0.f;
-  };
-#pragma unroll
-  for (int c = 0; c < kEach; ++c) {
-    const uint64_t col = col0 + c * kAdapterThreads;
-#pragma unroll
-    for (int i = 0; i < kRank / 8; ++i)
-      u[c][i].load(second + col * a.second.stride + i * 8, adapts && col < a.out && i * 8 < static_cast<int>(a.rank));
-    base[c] = any ? base_at(0, col) : 0.f;
-  }
-  pdl_wait();
-  pdl_trigger();
-  if (!any || (!adapts && a.y == a.base)) return;
-  for (uint32_t i = tid; i < kThinRows * kRank; i += kAdapterThreads) {
-    const int row = i / kRank;
+    __syncthreads();
     float v = 0.f;
-    if (adapts && row < t.rows)
-#pragma unroll
-      for (int p = P::kP - 1; p >= 0; --p)
-        v += __bfloat162float(__ldcg(a.hidden + (t.row0 + row) * (P::kP * kRank) + p * kRank + i % kRank));
-    hidden[row][i % kRank] = v;
-  }
-  __syncthreads();
-  for (int row = 0; row < t.rows; ++row) {
-#pragma unroll
-    for (int c = 0; c < kEach; ++c) {
-      const uint64_t col = col0 + c * kAdapterThreads;
-      if (col >= a.out) break;
-      const float b = row ? base_at(row, col) : base[c];
-      float w = 0.f;
-#pragma unroll
-      for (int i = 0; i < kRank / 2; i += 2) {
-        const float4 h = *reinterpret_cast<const float4*>(&hidden[row][2 * i]);
-        const float2 p = u[c][i / 4].pair(i % 4), q = u[c][i / 4].pair(i % 4 + 1);
-        w = fmaf(h.w, q.y, fmaf(h.z, q.x, fmaf(h.y, p.y, fmaf(h.x, p.x, w))));
+    if (tid < kRank)
+      for (uint32_t s = 0; s < slices; ++s) v += sums[s][tid];
+    if (a.parts > 1) {
+      __syncthreads();
+      if (tid < kRank) sums[0][tid] = v;
+      cluster_meet();
+      if (tid < kRank) {
+        v = 0.f;
+        for (uint32_t p = 0; p < a.parts; ++p) v += remote_f32(smem_u32(&sums[0][tid]), p);
       }
-      a.y[(t.row0 + row) * a.y_stride + col] = from_f32<T>(b + w);
+      cluster_arrive();
+    }
+    if (tid < kRank) {
+      hidden[tid] = v *= a.q.scales ? a.q.scales[t.adapter] : 1.f;
+      if (group == 0 && part == 0) {  // for the backward call
+        uint32_t w[P::kP];
+        split_pair<P::kP>(v, 0.f, w);
+#pragma unroll
+        for (int p = 0; p < P::kP; ++p)
+          reinterpret_cast<uint16_t*>(a.hidden)[t.row0 * (P::kP * kRank) + p * kRank + tid] = static_cast<uint16_t>(w[p]);
+      }
+    }
+    __syncthreads();
+  }
+  T* const y = a.y + t.row0 * a.y_stride;
+  for (uint64_t c = col0; c < col1; c += kEach * kAdapterThreads) {
+    if (c > col0) load_columns(c);
+#pragma unroll
+    for (int e = 0; e < kEach; ++e) {
+      const uint64_t col = c + e * kAdapterThreads + tid;
+      float w = 0.f;
+      if (adapts)
+#pragma unroll
+        for (int i = 0; i < kRank / 2; i += 2) {
+          const float4 h = *reinterpret_cast<const float4*>(&hidden[2 * i]);
+          const float2 p = u[e][i / 4].pair(i % 4), q = u[e][i / 4].pair(i % 4 + 1);
+          w = fmaf(h.w, q.y, fmaf(h.z, q.x, fmaf(h.y, p.y, fmaf(h.x, p.x, w))));
+        }
+      if (col < col1) y[col] = from_f32<T>(onto[e] + w);
     }
   }
+  if (adapts && a.parts > 1) cluster_wait();  // the others have read this block's sums
 }
 
 // ---------------------------------------------------------------------------
@@ -1037,32 +1170,38 @@ cudaError_t launch_chain(Chain<T> a, cudaStream_t st) {
   return launch_clusters<second_kernel<T, kRank, kTile, kBack>>(a, slots * a.groups, 1, S::kBytes, st);
 }
 
-template <class T, int kRank>
-cudaError_t launch_thin(Chain<T> a, cudaStream_t st) {
-  const uint64_t slots = slots_of(a.q.tokens, a.q.requests, kThinRows);
-  // few tokens: clusters share their columns, a round of a block's loads to each
+// Few rows: one kernel, clusters of as many blocks as fill the SMs, and several
+// clusters to a tile where its columns of y are many.
+template <auto kKernel, class T>
+cudaError_t launch_few(Chain<T> a, uint64_t slots, uint64_t tiles, uint64_t cols, int smem, cudaStream_t st) {
+  const uint64_t room = HKV_ROOM * sm_count();
   a.parts = 1;
-  while (a.parts < kAdapterParts && a.in >= 1024ull * a.parts && a.q.tokens * a.parts <= HKV_TP * 1ull * sm_count()) a.parts *= 2;
+  while (a.parts < kAdapterParts && 2 * tiles * a.parts <= room && (a.in >= 256ull * a.parts || a.out > cols * a.parts)) a.parts *= 2;
   a.part_in = ((a.in + a.parts - 1) / a.parts + 63) / 64 * 64;
-  a.follows = a.q.requests > 0;
-  if (a.follows) {
-    const cudaError_t e = launch_clusters<thin_first_kernel<T, kRank>>(a, slots * a.parts, a.parts, 0, st);
-    if (e != cudaSuccess) return e;
-  }
-  constexpr uint64_t kCols = thin_columns<T, kRank>() * kAdapterThreads;
-  a.groups = static_cast<uint32_t>((a.out + kCols - 1) / kCols);
-  return launch_clusters<thin_second_kernel<T, kRank>>(a, slots * a.groups, 1, 0, st);
+  const uint64_t most = (a.out + cols * a.parts - 1) / (cols * a.parts);
+  uint64_t groups = (room + tiles * a.parts - 1) / (tiles * a.parts);
+  // every group has the first product anew
+  if (groups > 1 + a.out / a.in) groups = 1 + a.out / a.in;
+  if (groups > most) groups = most;
+  a.groups = static_cast<uint32_t>(groups);
+  a.group_out = ((a.out + groups * a.parts - 1) / (groups * a.parts) + 31) / 32 * 32;
+  return launch_clusters<kKernel>(a, slots * groups * a.parts, a.parts, smem, st);
 }
 
+template <class T, int kRank, bool kBack>
+cudaError_t chain_of(const Chain<T>& a, cudaStream_t st) {
+  const uint64_t tokens = a.q.tokens, requests = a.q.requests;
+  if constexpr (!kBack)
+    if (tokens <= requests && a.x_whole && a.first.whole && a.second.whole && a.in % 8 == 0 && a.rank % 8 == 0)
+      return launch_few<thin_kernel<T, kRank>>(a, slots_of(tokens, requests, 1), tokens, thin_columns<T, kRank>() * kAdapterThreads, 0, st);
+  if (tokens < 32 * requests)
+    return launch_few<short_kernel<T, kRank, kBack>>(a, slots_of(tokens, requests, 16), tokens / 16 + (requests < tokens ? requests : tokens) + 1,
+                                                     SecondShape<T, kRank, 16, kBack>::kCols, ShortShape<T, kRank, kBack>::kBytes, st);
+  return launch_chain<T, kRank, 64, kBack>(a, st);
+}
 template <class T, bool kBack>
 cudaError_t chain(const Chain<T>& a, cudaStream_t st) {
-  if constexpr (!kBack)
-    if (a.q.tokens <= HKV_THIN * a.q.requests && a.x_whole && a.first.whole && a.second.whole && a.in % 8 == 0 && a.rank % 8 == 0)
-      return a.rank <= 16 ? launch_thin<T, 16>(a, st) : a.rank <= 32 ? launch_thin<T, 32>(a, st) : launch_thin<T, 64>(a, st);
-  const bool tall = a.q.tokens >= 32 * a.q.requests;
-  if (a.rank <= 16) return tall ? launch_chain<T, 16, 64, kBack>(a, st) : launch_chain<T, 16, 16, kBack>(a, st);
-  if (a.rank <= 32) return tall ? launch_chain<T, 32, 64, kBack>(a, st) : launch_chain<T, 32, 16, kBack>(a, st);
-  return tall ? launch_chain<T, 64, 64, kBack>(a, st) : launch_chain<T, 64, 16, kBack>(a, st);
+  return a.rank <= 16 ? chain_of<T, 16, kBack>(a, st) : a.rank <= 32 ? chain_of<T, 32, kBack>(a, st) : chain_of<T, 64, kBack>(a, st);
 }
 
 template <class T, int kRank>
