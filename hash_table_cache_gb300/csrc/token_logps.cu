@@ -19,6 +19,15 @@
 // where that is not enough (entries that repeat with the groups) once for each
 // alternative.
 #include "logits.cuh"
+#ifndef HKV_L1
+#define HKV_L1 5
+#endif
+#ifndef HKV_L0
+#define HKV_L0 6
+#endif
+#ifndef HKV_LB
+#define HKV_LB 7
+#endif
 
 namespace hkv {
 namespace {
@@ -441,7 +450,7 @@ __global__ void __launch_bounds__(kWarpThreads)
 
 // A block per row, or the `parts` blocks of a cluster.
 template <class T, bool kTop>
-__global__ void __launch_bounds__(kThreads, kTop ? 5 : 6)
+__global__ void __launch_bounds__(kThreads, kTop ? HKV_L1 : HKV_L0)
     long_rows_kernel(uint64_t vocab, const T* __restrict__ logits, uint64_t stride, uint32_t parts,
                      const int64_t* __restrict__ labels, uint32_t top, Out out) {
   constexpr int kWarps = kThreads / 32;
@@ -519,10 +528,22 @@ __global__ void __launch_bounds__(kThreads, kTop ? 5 : 6)
   if (kTop && lane < top) put_top(t * top + lane, team->list[lane], row, out);
 }
 
+// Two neighbouring elements of a chunk.
+__device__ __forceinline__ void put_both(float* e, float a, float b) {
+  e[0] = a;
+  e[1] = b;
+}
+__device__ __forceinline__ void put_both(__nv_bfloat16* e, float a, float b) {
+  *reinterpret_cast<__nv_bfloat162*>(e) = __floats2bfloat162_rn(a, b);
+}
+__device__ __forceinline__ void put_both(__half* e, float a, float b) {
+  *reinterpret_cast<__half2*>(e) = __floats2half2_rn(a, b);
+}
+
 // A piece of a row for every kLanes threads, rows from the last to the first, so
 // that what the forward call read last is taken from L2 while it is there.
 template <class T, int kLanes>
-__global__ void __launch_bounds__(kLanes == 32 ? kWarpThreads : kThreads)
+__global__ void __launch_bounds__(kLanes == 32 ? kWarpThreads : kThreads, kLanes == 32 ? 7 : HKV_LB)
     backward_kernel(uint64_t rows, uint64_t vocab, const T* logits, uint64_t stride, uint64_t pieces,
                     const int64_t* __restrict__ labels, const float* __restrict__ lse,
                     const float* __restrict__ entropy, const float* __restrict__ dlogps,
@@ -552,6 +573,16 @@ __global__ void __launch_bounds__(kLanes == 32 ? kWarpThreads : kThreads)
       const float slope = -h * (max_nan(lp, -200.f) + ent);
       return at == hit ? fmaf(p, slope, g * (1.f - p)) : p * (slope - g);
     };
+    // The others in pairs: p = 2^(a - off), a = v log2 e - l log2 e by two multiply-adds,
+    // off what the rounded l log2 e (the same in every a) and l leave out; then the
+    // entry is 2^a (slope a + level).
+    const bool factored = fabsf(l) < kFactored;
+    const float scaled = l * kLog2e;
+    const float off = fmaf(rest, kLog2e, fmaf(l, kLog2eRest, fmaf(l, kLog2e, -scaled)));
+    const float back = exp2_of_minus(off);
+    const uint64_t log2e = both(kLog2e, kLog2e), more = both(kLog2eRest, kLog2eRest), minus = both(-scaled, -scaled);
+    const float slope1 = -h * 0.693147181f * back, level1 = (-h * fmaf(off, -0.693147181f, ent) - g) * back;
+    const uint64_t slope2 = both(slope1, slope1), level2 = both(level1, level1);
     auto one = [&](uint64_t at) { d[at] = from_f32<T>(counted ? value(to_f32(x[at]), at) : 0.f); };
     const uint32_t head = to_boundary(d, n);
     const bool alike = to_boundary(x, n) == head;
@@ -578,8 +609,19 @@ __global__ void __launch_bounds__(kLanes == 32 ? kWarpThreads : kThreads)
       } else {
         Chunk<T> in;
         in.w = w[u];
+        if (!factored || hit - (head + k * kN) < kN) {
 #pragma unroll
-        for (int i = 0; i < kN; ++i) e[i] = from_f32<T>(value(in.at(i), head + k * kN + i));
+          for (int i = 0; i < kN; ++i) e[i] = from_f32<T>(value(in.at(i), head + k * kN + i));
+        } else {
+          clamp(in);
+#pragma unroll
+          for (int i = 0; i < kN; i += 2) {
+            const uint64_t x2 = both(in.at(i), in.at(i + 1));
+            const uint64_t a2 = fma_both(x2, more, fma_both(x2, log2e, minus));
+            const float2 a = parts(a2), m = parts(fma_both(a2, slope2, level2));
+            put_both(e + i, exp2_approx(a.x) * m.x, exp2_approx(a.y) * m.y);
+          }
+        }
       }
       st_stream_v4(d + head + k * kN, o.w);
     }
