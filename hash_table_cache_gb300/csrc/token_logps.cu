@@ -41,6 +41,14 @@ __device__ __forceinline__ float max_nan(float a, float b) {
   return r;
 }
 
+// 2^x, 0 below 2^-126: one instruction, where powers down to 2^-149 take four.  (In
+// sums of powers whose largest is 1.)
+__device__ __forceinline__ float exp2_of(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+
 // A running maximum m, s = sum exp(x - m) and w = sum exp(x - m) (x - m).
 // Nothing seen, or only -inf: m = -inf, s = w = 0.  A NaN or +inf among the
 // values makes s NaN.
@@ -160,7 +168,7 @@ __device__ __forceinline__ Moments row_pass(const T* x, uint64_t n, int lane, T*
           const uint64_t x2 = both(c[u].at(i), c[u].at(i + 1));
           const uint64_t a2 = fma_both(x2, rest, fma_both(x2, l, minus));
           const float2 a = parts(a2);
-          const uint64_t e2 = both(exp2_approx(a.x), exp2_approx(a.y));
+          const uint64_t e2 = both(exp2_of(a.x), exp2_of(a.y));
           sum[i / 2 & 1] = add_both(sum[i / 2 & 1], e2);
           wsum[i / 2 & 1] = fma_both(e2, a2, wsum[i / 2 & 1]);
         }
