@@ -22,6 +22,9 @@
 #ifndef HKV_L1
 #define HKV_L1 5
 #endif
+#ifndef HKV_LU
+#define HKV_LU 4
+#endif
 #ifndef HKV_L0
 #define HKV_L0 6
 #endif
@@ -116,31 +119,28 @@ __device__ __forceinline__ void clamp(Chunk<T>& c) {
   }
 }
 
+// 16-byte loads of a round, in flight together.
+__host__ __device__ constexpr int loads(int lanes) { return lanes == 32 ? 8 : HKV_LU; }
+
 // Cells that a thread keeps at most of a row (a cell is one round of loads or, of
 // longer rows, several).
 template <class T, int kLanes>
-constexpr int cells_of() { return kLanes == 32 ? 4 : 64 / static_cast<int>(sizeof(T)); }
+constexpr int cells_of() { return kLanes == 32 ? 4 : 256 / loads(kLanes) / static_cast<int>(sizeof(T)); }
 
 // One thread's share of a row of n elements, taken by kLanes threads.  With kTop
 // cells[i * kLanes] gets the maximum of its rounds i * per .. (i + 1) * per - 1.
 template <class T, int kLanes, bool kTop>
 __device__ __forceinline__ Moments row_pass(const T* x, uint64_t n, int lane, T* cells, uint32_t per,
                                             uint32_t count) {
-  constexpr int kN = Chunk<T>::kN, kUnroll = unroll(kLanes);
+  constexpr int kN = Chunk<T>::kN, kUnroll = loads(kLanes);
   Moments r;
   const uint32_t head = to_boundary(x, n);
   if (lane < static_cast<int>(head)) r.one(to_f32(x[lane]));
-  const T* body = x + head;
-  const uint64_t chunks = (n - head) / kN;
+  const uint32_t chunks = static_cast<uint32_t>((n - head) / kN);
+  const T* from = x + head + static_cast<uint64_t>(lane) * kN;
   float cell = -INFINITY;
   uint32_t in_cell = 0, kept = 0;
-  for (uint64_t k = lane; k < chunks; k += kUnroll * kLanes) {
-    Chunk<T> c[kUnroll];
-#pragma unroll
-    for (int u = 0; u < kUnroll; ++u) {
-      if (k + u * kLanes < chunks) c[u].w = ld_stream_v4(body + (k + u * kLanes) * kN);
-      else c[u].fill_lowest();
-    }
+  auto round = [&](Chunk<T>(&c)[kUnroll]) {
     const float top = largest(c);
     const float base = r.raise(top);
     if constexpr (kTop) {
@@ -183,13 +183,29 @@ __device__ __forceinline__ Moments row_pass(const T* x, uint64_t n, int lane, T*
 #pragma unroll
         for (int i = 0; i < kN; ++i) r.add(c[u].at(i), base);
     }
+  };
+  uint32_t k = lane;
+  for (; k + (kUnroll - 1) * kLanes < chunks; k += kUnroll * kLanes, from += kUnroll * kLanes * kN) {
+    Chunk<T> c[kUnroll];
+#pragma unroll
+    for (int u = 0; u < kUnroll; ++u) c[u].w = ld_stream_v4(from + u * kLanes * kN);
+    round(c);
+  }
+  if (k < chunks) {
+    Chunk<T> c[kUnroll];
+#pragma unroll
+    for (int u = 0; u < kUnroll; ++u) {
+      if (k + u * kLanes < chunks) c[u].w = ld_stream_v4(from + u * kLanes * kN);
+      else c[u].fill_lowest();
+    }
+    round(c);
   }
   if constexpr (kTop)
     for (; kept < count; ++kept) {
       cells[kept * kLanes] = from_f32<T>(cell);
       cell = -INFINITY;
     }
-  const uint64_t tail = head + chunks * kN + lane;
+  const uint64_t tail = head + static_cast<uint64_t>(chunks) * kN + lane;
   if (tail < n) r.one(to_f32(x[tail]));
   return r;
 }
@@ -249,7 +265,7 @@ struct Team {
   }
   // Rounds of loads to a cell, and cells, of n elements from x on.
   static __device__ __forceinline__ void plan(const T* x, uint64_t n, uint32_t& per, uint32_t& count) {
-    constexpr uint64_t kRound = kLanes * unroll(kLanes);
+    constexpr uint64_t kRound = kLanes * loads(kLanes);
     const uint64_t chunks = (n - to_boundary(x, n)) / Chunk<T>::kN;
     const uint64_t rounds = (chunks + kRound - 1) / kRound;
     per = 1;
@@ -261,7 +277,7 @@ struct Team {
   // cells written.  All of the team's threads call it.
   __device__ __forceinline__ void pick(const T* x, uint64_t lo, uint64_t hi, float m, uint32_t per,
                                        uint32_t count, uint32_t top, uint32_t lane) {
-    constexpr int kN = Chunk<T>::kN, kUnroll = unroll(kLanes);
+    constexpr int kN = Chunk<T>::kN, kUnroll = loads(kLanes);
     most[lane] = m;
     if (lane < HKV_MAX_TOP) list[lane] = 0;
     if (lane == 0) items_found = keys_found = 0;
