@@ -74,6 +74,11 @@ struct Planes {
   static constexpr int kP = sizeof(T) == 4 ? 3 : 2;
 };
 
+// Blocks of an SM that shared memory has room for, so that registers do not fall
+// short of them.
+template <class T, int kRank>
+__host__ __device__ constexpr int blocks_of() { return sizeof(T) == 4 ? 2 : kRank == 64 ? 3 : 4; }
+
 // What the requests are, as the kernels take it.  (Read past L1: the second
 // product's kernel reads before it has waited.)
 struct Requests {
@@ -177,6 +182,16 @@ __device__ __forceinline__ void copy_tile(T* tile, const T* data, uint64_t strid
   static_assert(kAdapterThreads % kLanes == 0 && (kRows % kPass == 0 || kRows < kPass));
   const int row = threadIdx.x / kLanes, col = threadIdx.x % kLanes * 8;
   if (kRows < kPass && row >= kRows) return;
+  if (whole && rows >= kRows && cols >= kCols) {
+    const T* p = data + row * stride + col;
+    uint32_t at = smem_u32(tile + row * kPitch + col);
+#pragma unroll
+    for (int i = 0; i < (kRows + kPass - 1) / kPass; ++i, p += kPass * stride, at += kPass * kPitch * sizeof(T))
+#pragma unroll
+      for (int v = 0; v < static_cast<int>(sizeof(T)) / 2; ++v)
+        asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(at + v * 16), "l"(p + v * (16 / sizeof(T))) : "memory");
+    return;
+  }
   const int there = static_cast<int>(min(rows, static_cast<int64_t>(kRows))) - row;
   const int n = static_cast<int>(max(min(cols - col, static_cast<int64_t>(8)), static_cast<int64_t>(0)));
   const T* const from = data + row * stride + col;
@@ -285,33 +300,44 @@ template <class T>
 struct Sum {
   static constexpr bool kTwo = sizeof(T) == 4;
   float high[2][4] = {}, low[2][4] = {};
-  template <int kA, int kB, bool kF16 = false>
-  __device__ __forceinline__ void add(const uint32_t (&a)[kA][4], const uint32_t (&b)[kB][4]) {
-#pragma unroll
-    for (int i = 0; i < kA; ++i)
-#pragma unroll
-      for (int j = 0; j < kB; ++j) {
-        if (kTwo && i + j > 2) continue;
-#pragma unroll
-        for (int half = 0; half < 2; ++half)
-          mma<kF16>(kTwo && i + j > 0 ? low[half] : high[half], a[i], b[j][half * 2], b[j][half * 2 + 1]);
-      }
-  }
   __device__ __forceinline__ float at(int half, int i) const {
     return kTwo ? high[half][i] + low[half][i] : high[half][i];
   }
 };
-// Chains that go on from one stage to the next where they need not be short.
-template <class T, int kA, int kB, bool kF16>
-__device__ __forceinline__ void add_onto(float (&acc)[2][4], const uint32_t (&a)[kA][4], const uint32_t (&b)[kB][4]) {
-  Sum<T> d;
-  if constexpr (!Sum<T>::kTwo)
+// Adds one k16 step to kN pieces side by side; products that follow one another go to
+// different sums.
+template <class T, int kN, int kA, int kB, bool kF16 = false>
+__device__ __forceinline__ void add(Sum<T> (&d)[kN], const uint32_t (&a)[kA][4], const uint32_t (&b)[kN][kB][4]) {
 #pragma unroll
-    for (int i = 0; i < 8; ++i) d.high[i / 4][i % 4] = acc[i / 4][i % 4];
-  d.template add<kA, kB, kF16>(a, b);
+  for (int i = 0; i < kA; ++i)
 #pragma unroll
-  for (int i = 0; i < 8; ++i)
-    acc[i / 4][i % 4] = Sum<T>::kTwo ? acc[i / 4][i % 4] + d.at(i / 4, i % 4) : d.high[i / 4][i % 4];
+    for (int j = 0; j < kB; ++j) {
+      if (Sum<T>::kTwo && i + j > 2) continue;
+#pragma unroll
+      for (int n = 0; n < kN; ++n)
+#pragma unroll
+        for (int half = 0; half < 2; ++half)
+          mma<kF16>(Sum<T>::kTwo && i + j > 0 ? d[n].low[half] : d[n].high[half], a[i], b[n][j][half * 2], b[n][j][half * 2 + 1]);
+    }
+}
+// And to chains that go on from one stage to the next where they need not be short.
+template <class T, int kN, int kA, int kB, bool kF16>
+__device__ __forceinline__ void add_onto(float (&acc)[kN][2][4], const uint32_t (&a)[kA][4], const uint32_t (&b)[kN][kB][4]) {
+  Sum<T> d[kN];
+  if constexpr (!Sum<T>::kTwo) {
+#pragma unroll
+    for (int n = 0; n < kN; ++n)
+#pragma unroll
+      for (int i = 0; i < 8; ++i) d[n].high[i / 4][i % 4] = acc[n][i / 4][i % 4];
+  }
+  add<T, kN, kA, kB, kF16>(d, a, b);
+#pragma unroll
+  for (int n = 0; n < kN; ++n)
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      float& to = acc[n][i / 4][i % 4];
+      to = Sum<T>::kTwo ? to + d[n].at(i / 4, i % 4) : d[n].high[i / 4][i % 4];
+    }
 }
 
 // Two neighbouring elements in shared memory.
@@ -434,11 +460,13 @@ __device__ __forceinline__ void first_product(float (&acc)[kRank / 16][2][4], T*
       const int k = (other * kEach + s) * 16;
       uint32_t xa[P::kIn][4];
       rows_operand<T, P::kIn, S::kPitch>(xa, xs, row_warp * 16, k);
+      constexpr int kN = sizeof(T) == 4 ? 1 : kRank / 16;
 #pragma unroll
-      for (int n = 0; n < kRank / 16; ++n) {
-        uint32_t w[P::kIn][4];
-        cols_operand<T, P::kIn, S::kFirstPitch, kBack>(w, ws, n * 16, k);
-        add_onto<T, P::kIn, P::kIn, std::is_same_v<T, __half>>(acc[n], xa, w);
+      for (int n = 0; n < kRank / 16; n += kN) {
+        uint32_t w[kN][P::kIn][4];
+#pragma unroll
+        for (int i = 0; i < kN; ++i) cols_operand<T, P::kIn, S::kFirstPitch, kBack>(w[i], ws, (n + i) * 16, k);
+        add_onto<T, kN, P::kIn, P::kIn, std::is_same_v<T, __half>>(reinterpret_cast<float(&)[kN][2][4]>(acc[n]), xa, w);
       }
     }
   }
@@ -544,23 +572,33 @@ __device__ __forceinline__ void second_step(T* stage, const uint32_t (&h)[kRank 
   const uint32_t lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const uint32_t row_warp = warp % S::kRowWarps, other = warp / S::kRowWarps;
   if (adapts) {
+    constexpr int kN = sizeof(T) == 4 ? 1 : 2;
 #pragma unroll
-    for (int n = 0; n < S::kWarpCols; n += 16) {
+    for (int n = 0; n < S::kWarpCols; n += 16 * kN) {
       const int c = other * S::kWarpCols + n;
-      Sum<T> d;
+      T* const at = stage + (row_warp * 16 + lane / 4) * S::kPitch + c + lane % 4 * 2;
+      auto place = [&](int i) { return at + i % 2 * 8 * S::kPitch + i / 2 * 8; };  // of 4 kN pairs of base
+      Sum<T> d[kN];
+      if constexpr (!Sum<T>::kTwo) {  // sums start with base
+#pragma unroll
+        for (int i = 0; i < 4 * kN; ++i) {
+          const float2 v = pair_at(place(i));
+          d[i / 4].high[i / 2 % 2][i % 2 * 2] = v.x;
+          d[i / 4].high[i / 2 % 2][i % 2 * 2 + 1] = v.y;
+        }
+      }
 #pragma unroll
       for (int k = 0; k < kRank / 16; ++k) {
-        uint32_t w[P::kW][4];
-        cols_operand<T, P::kW, S::kSecondPitch, kBack>(w, stage + S::kBase, c, k * 16);
-        d.add(h[k], w);
-      }
-      // onto base, in its place
+        uint32_t w[kN][P::kW][4];
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        if (kTile == 16 && i % 2 && rows <= 8) continue;
-        T* const at = stage + (row_warp * 16 + lane / 4 + i % 2 * 8) * S::kPitch + c + i / 2 * 8 + lane % 4 * 2;
-        const float2 v = pair_at(at);
-        put_pair(at, v.x + d.at(i / 2, i % 2 * 2), v.y + d.at(i / 2, i % 2 * 2 + 1));
+        for (int i = 0; i < kN; ++i) cols_operand<T, P::kW, S::kSecondPitch, kBack>(w[i], stage + S::kBase, c + i * 16, k * 16);
+        add(d, h[k], w);
+      }
+#pragma unroll
+      for (int i = 0; i < 4 * kN; ++i) {
+        float2 v = make_float2(0.f, 0.f);
+        if constexpr (Sum<T>::kTwo) v = pair_at(place(i));
+        put_pair(place(i), v.x + d[i / 4].at(i / 2 % 2, i % 2 * 2), v.y + d[i / 4].at(i / 2 % 2, i % 2 * 2 + 1));
       }
     }
     __syncwarp();
@@ -588,7 +626,7 @@ __device__ __forceinline__ void second_step(T* stage, const uint32_t (&h)[kRank 
 }
 
 template <class T, int kRank, int kTile, bool kBack>
-__global__ void __launch_bounds__(kAdapterThreads)
+__global__ void __launch_bounds__(kAdapterThreads, blocks_of<T, kRank>())
     second_kernel(const __grid_constant__ Chain<T> a) {
   using S = SecondShape<T, kRank, kTile, kBack>;
   using P = Planes<T>;
@@ -681,7 +719,7 @@ struct ShortShape {
 };
 
 template <class T, int kRank, bool kBack>
-__global__ void __launch_bounds__(kAdapterThreads)
+__global__ void __launch_bounds__(kAdapterThreads, blocks_of<T, kRank>())
     short_kernel(const __grid_constant__ Chain<T> a) {
   using Shape = ShortShape<T, kRank, kBack>;
   using F = typename Shape::F;
@@ -1000,7 +1038,7 @@ __global__ void __launch_bounds__(kAdapterThreads, GradShape<T, kRank>::kBlocks)
     }
   };
   float acc[S::kWarpCols / 16][2][4] = {};
-  int in_stage[S::kStages];  // rows of the tile there
+  int in_stage[S::kStages] = {};  // rows of the tile there
   auto multiply = [&](int stage) {
     int rows = in_stage[0];
 #pragma unroll
@@ -1014,11 +1052,13 @@ __global__ void __launch_bounds__(kAdapterThreads, GradShape<T, kRank>::kBlocks)
 #pragma unroll
       for (int i = 0; i < P::kP; ++i)
         ldsm_t(h[i], smem_u32(ps + (i * S::kRows + t + lane % 8 + lane / 16 * 8) * S::kRankPitch + rank_warp * 16 + lane / 8 % 2 * 8));
+      constexpr int kN = sizeof(T) == 4 ? 1 : S::kWarpCols / 16;
 #pragma unroll
-      for (int n = 0; n < S::kWarpCols / 16; ++n) {
-        uint32_t w[P::kW][4];
-        cols_operand<T, P::kW, S::kPitch, true>(w, ms, col_warp * S::kWarpCols + n * 16, t);
-        add_onto<T, P::kP, P::kW, false>(acc[n], h, w);
+      for (int n = 0; n < S::kWarpCols / 16; n += kN) {
+        uint32_t w[kN][P::kW][4];
+#pragma unroll
+        for (int i = 0; i < kN; ++i) cols_operand<T, P::kW, S::kPitch, true>(w[i], ms, col_warp * S::kWarpCols + (n + i) * 16, t);
+        add_onto<T, kN, P::kP, P::kW, false>(reinterpret_cast<float(&)[kN][2][4]>(acc[n]), h, w);
       }
     }
   };

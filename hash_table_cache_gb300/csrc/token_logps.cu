@@ -19,18 +19,6 @@
 // where that is not enough (entries that repeat with the groups) once for each
 // alternative.
 #include "logits.cuh"
-#ifndef HKV_L1
-#define HKV_L1 5
-#endif
-#ifndef HKV_LU
-#define HKV_LU 4
-#endif
-#ifndef HKV_L0
-#define HKV_L0 6
-#endif
-#ifndef HKV_LB
-#define HKV_LB 7
-#endif
 
 namespace hkv {
 namespace {
@@ -120,7 +108,7 @@ __device__ __forceinline__ void clamp(Chunk<T>& c) {
 }
 
 // 16-byte loads of a round, in flight together.
-__host__ __device__ constexpr int loads(int lanes) { return lanes == 32 ? 8 : HKV_LU; }
+__host__ __device__ constexpr int loads(int lanes) { return lanes == 32 ? 8 : 4; }
 
 // Cells that a thread keeps at most of a row (a cell is one round of loads or, of
 // longer rows, several).
@@ -474,7 +462,7 @@ __global__ void __launch_bounds__(kWarpThreads)
 
 // A block per row, or the `parts` blocks of a cluster.
 template <class T, bool kTop>
-__global__ void __launch_bounds__(kThreads, kTop ? HKV_L1 : HKV_L0)
+__global__ void __launch_bounds__(kThreads, 6)
     long_rows_kernel(uint64_t vocab, const T* __restrict__ logits, uint64_t stride, uint32_t parts,
                      const int64_t* __restrict__ labels, uint32_t top, Out out) {
   constexpr int kWarps = kThreads / 32;
@@ -567,7 +555,7 @@ __device__ __forceinline__ void put_both(__half* e, float a, float b) {
 // A piece of a row for every kLanes threads, rows from the last to the first, so
 // that what the forward call read last is taken from L2 while it is there.
 template <class T, int kLanes>
-__global__ void __launch_bounds__(kLanes == 32 ? kWarpThreads : kThreads, kLanes == 32 ? 7 : HKV_LB)
+__global__ void __launch_bounds__(kLanes == 32 ? kWarpThreads : kThreads, kLanes == 32 ? 7 : 7)
     backward_kernel(uint64_t rows, uint64_t vocab, const T* logits, uint64_t stride, uint64_t pieces,
                     const int64_t* __restrict__ labels, const float* __restrict__ lse,
                     const float* __restrict__ entropy, const float* __restrict__ dlogps,
