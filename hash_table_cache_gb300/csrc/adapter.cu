@@ -5,32 +5,12 @@
 namespace hkv {
 namespace {
 
-// A matrix of rows of `cols` elements, `stride` from one to the next.
-struct Matrix {
-  const void* p;
-  uint64_t rows, cols, stride;
-  size_t size;
-  uint64_t begin() const { return reinterpret_cast<uintptr_t>(p); }
-  uint64_t end() const { return rows ? begin() + ((rows - 1) * stride + cols) * size : begin(); }
-};
 constexpr uint64_t kMaxStride = 1ull << 31, kMaxStep = 1ull << 40;  // byte offsets stay within 64 bits
 
 bool matrix_ok(const Matrix& m) {
   return m.stride >= m.cols && m.stride <= kMaxStride && (m.rows == 0 || (m.p && aligned(m.p, m.size)));
 }
 bool whole(const Matrix& m) { return aligned(m.p, 16) && m.stride * m.size % 16 == 0; }
-
-// Whether what is written as `a` may hold elements of `b`: columns of one buffer
-// beside one another do not meet.
-bool meet(const Matrix& a, const Matrix& b) {
-  if (a.end() <= b.begin() || b.end() <= a.begin() || !a.rows || !b.rows) return false;
-  if (a.stride != b.stride || a.size != b.size) return true;
-  const Matrix &lo = a.begin() <= b.begin() ? a : b, &hi = a.begin() <= b.begin() ? b : a;
-  const uint64_t apart = hi.begin() - lo.begin(), row = a.stride * a.size;
-  if (apart % a.size) return true;
-  const uint64_t at = apart % row;
-  return at < lo.cols * a.size || at + hi.cols * a.size > row;
-}
 bool same(const Matrix& a, const Matrix& b) { return a.p == b.p && a.stride == b.stride; }
 
 bool requests_ok(uint64_t tokens, uint64_t requests, const int64_t* offsets, const int64_t* which) {

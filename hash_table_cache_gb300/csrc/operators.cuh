@@ -23,6 +23,26 @@ inline hkv_status op_status(cudaError_t e) {
   return e == cudaErrorMemoryAllocation ? HKV_ERR_OOM : HKV_ERR_CUDA;
 }
 
+// A matrix of rows of `cols` elements, `stride` from one to the next.
+struct Matrix {
+  const void* p;
+  uint64_t rows, cols, stride;
+  size_t size;
+  uint64_t begin() const { return reinterpret_cast<uintptr_t>(p); }
+  uint64_t end() const { return rows ? begin() + ((rows - 1) * stride + cols) * size : begin(); }
+};
+// Whether what is written as `a` may hold elements of `b`: columns of one buffer
+// beside one another do not meet.
+inline bool meet(const Matrix& a, const Matrix& b) {
+  if (a.end() <= b.begin() || b.end() <= a.begin() || !a.rows || !b.rows) return false;
+  if (a.stride != b.stride || a.size != b.size) return true;
+  const Matrix &lo = a.begin() <= b.begin() ? a : b, &hi = a.begin() <= b.begin() ? b : a;
+  const uint64_t apart = hi.begin() - lo.begin(), row = a.stride * a.size;
+  if (apart % a.size) return true;
+  const uint64_t at = apart % row;
+  return at < lo.cols * a.size || at + hi.cols * a.size > row;
+}
+
 // Call f with a null pointer of the element type `type` stands for.
 template <class F>
 auto with_type(int type, F&& f) {

@@ -715,7 +715,8 @@ hkv_status hkv_token_logps_backward(uint64_t rows, uint64_t vocab, const void* l
   if (rows == 0) return HKV_OK;
   if (!lse || !entropy || !dlogits || !aligned(dlogits, type_size(type)) || (dlogps && !labels))
     return HKV_ERR_INVALID;
-  if (dlogits == logits && dstride != stride) return HKV_ERR_INVALID;
+  const Matrix from{logits, rows, vocab, stride, type_size(type)}, to{dlogits, rows, vocab, dstride, type_size(type)};
+  if (meet(to, from) && !(dlogits == logits && dstride == stride)) return HKV_ERR_INVALID;
   if (!aligned(labels, 8) || !aligned(lse, 4) || !aligned(entropy, 4) || !aligned(dlogps, 4) ||
       !aligned(dentropy, 4))
     return HKV_ERR_INVALID;

@@ -21,7 +21,7 @@ def lib():
 LOGPS = dict(rows=9, vocab=10, logits=P, type=0, stride=10, labels=P, top=3, logps=P, entropy=P, top_logps=P,
              top_ids=P, lse=P, stream=None)
 LOGPS_BACKWARD = dict(rows=9, vocab=10, logits=P, type=0, stride=10, labels=P, lse=P, entropy=P, dlogps=P, dentropy=P,
-                      dlogits=P, dstride=10, stream=None)
+                      dlogits=4 * P, dstride=10, stream=None)
 
 
 def _refused(lib, name, base, bad):
@@ -38,7 +38,7 @@ def test_token_logps(lib):
         dict(top_logps=P + 2), dict(top_ids=P + 4), dict(lse=P + 2)])
     _refused(lib, "hkv_token_logps_backward", LOGPS_BACKWARD, [
         dict(rows=BIG), dict(vocab=0), dict(logits=None), dict(logits=P + 2), dict(type=3), dict(stride=9), dict(labels=None),
-        dict(lse=None), dict(entropy=None), dict(dlogits=None), dict(dlogits=P + 2), dict(dstride=9), dict(dstride=11),
+        dict(lse=None), dict(entropy=None), dict(dlogits=None), dict(dlogits=4 * P + 2), dict(dstride=9), dict(dlogits=P, dstride=11), dict(dlogits=P + 4), dict(dlogits=P - 40),
         dict(lse=P + 2), dict(entropy=P + 2), dict(dlogps=P + 2), dict(dentropy=P + 2), dict(labels=P + 4)])
     good = [dict(LOGPS, rows=0)[k] for k in LOGPS]
     assert lib.hkv_token_logps(*good) == 0

@@ -92,7 +92,9 @@ def test_shapes(hkv, k, n, rank, dtype):
     ([1], [0]), ([1] * 7, [0, 2, 1, 1, -1, 3, 0]), ([1] * 300, [i % 5 - 1 for i in range(300)]),
     ([16] * 20, [1] * 20), ([17, 15, 16, 33, 31, 64, 65, 63], [0, 0, 0, 1, 1, 2, 2, 2]), ([500], [2]), ([200, 200], [1, 1]),
     ([0, 0, 0], [0, 1, 2]), ([0, 130, 0, 1, 0], [0, 1, 2, 1, 2]), ([3, 4], [-1, 7]), ([], []),
-    ([2] * 1100, [i * 7 % 3 for i in range(1100)]), ([40] * 70, [0] * 70)])
+    ([2] * 1100, [i * 7 % 3 for i in range(1100)]), ([40] * 70, [0] * 70),
+    ([0, 0, 1, 0, 2, 0, 0, 1] * 150, [i % 4 - 1 for i in range(1200)]),  # more requests than tokens
+    ([1] * 900, [i % 3 for i in range(900)]), ([3] * 40, [i % 3 for i in range(40)])])
 @pytest.mark.parametrize("dtype", TYPES)
 @pytest.mark.parametrize("rank", [8, 33])
 def test_requests(hkv, lengths, which, dtype, rank):

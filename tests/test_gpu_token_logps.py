@@ -279,8 +279,23 @@ def test_in_a_graph_and_on_another_stream(hkv):
         assert torch.equal(s.top_ids, want.top_ids) and torch.equal(ds, d)
 
 
+def _overlapping(x):
+    """A matrix that begins in the middle of x's first row."""
+    return x.as_strided(x.shape, x.stride(), x.storage_offset() + 20)
+
+
+def test_columns_of_one_buffer(hkv):
+    buf = _randn(1, (6, 80))
+    x = buf[:, :40]
+    labels = _labels(2, 6, 40)
+    f = hkv.token_logps(x, labels)
+    g = _randn(3, (6,))
+    want = hkv.token_logps_backward(f, g)
+    assert torch.equal(hkv.token_logps_backward(f, g, out=buf[:, 40:]), want)
+
+
 def test_refusals(hkv):
-    x = _randn(1, (6, 40))
+    x = _randn(1, (12, 40))[:6]
     labels = torch.zeros(6, dtype=torch.int64, device=DEV)
     f = hkv.token_logps(x, labels, 2)
     for bad in (lambda: hkv.token_logps(x.double(), labels), lambda: hkv.token_logps(x[0], labels),
@@ -293,6 +308,7 @@ def test_refusals(hkv):
                 lambda: hkv.token_logps_backward(f, dentropy=torch.zeros(6)),
                 lambda: hkv.token_logps_backward(f, out=torch.zeros((6, 41), device=DEV)),
                 lambda: hkv.token_logps_backward(f, out=torch.zeros((6, 40), dtype=BF16, device=DEV)),
-                lambda: hkv.token_logps_backward(f, out=torch.zeros((40, 6), device=DEV).t())):
+                lambda: hkv.token_logps_backward(f, out=torch.zeros((40, 6), device=DEV).t()),
+                lambda: hkv.token_logps_backward(f, out=_overlapping(x))):
         with pytest.raises((ValueError, hkv.HKVError)):
             bad()
