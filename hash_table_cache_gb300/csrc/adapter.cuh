@@ -31,7 +31,7 @@
 #include "operators.cuh"
 
 #ifndef HKV_PM
-#define HKV_PM 150
+#define HKV_PM 100
 #endif
 #ifndef HKV_GS
 #define HKV_GS 3
@@ -52,10 +52,19 @@
 #define HKV_GP 2
 #endif
 #ifndef HKV_GM
-#define HKV_GM 8
+#define HKV_GM 16
 #endif
 #ifndef HKV_EM
 #define HKV_EM 16
+#endif
+#ifndef HKV_FS
+#define HKV_FS 128
+#endif
+#ifndef HKV_FN
+#define HKV_FN 3
+#endif
+#ifndef HKV_S3
+#define HKV_S3 2
 #endif
 #ifndef HKV_S2
 #define HKV_S2 2
@@ -407,8 +416,8 @@ struct Chain {
 template <class T, int kRank, int kTile, bool kBack>
 struct FirstShape {
   static constexpr int kRowWarps = kTile / 16, kOther = 8 / kRowWarps;  // warps along rows, along columns of x
-  static constexpr int kStep = kTile == 64 ? 64 : 128;                  // columns of x to a stage
-  static constexpr int kStages = sizeof(T) == 4 ? 3 : 4;
+  static constexpr int kStep = kTile == 64 ? (sizeof(T) == 4 ? 64 : HKV_FS) : 128;  // columns of x to a stage
+  static constexpr int kStages = sizeof(T) == 4 ? 3 : kTile == 64 ? HKV_FN : 4;
   static constexpr int kPitch = kStep + 8, kFirstPitch = kBack ? kRank + 8 : kPitch;
   static constexpr int kX = kTile * kPitch, kFirst = (kBack ? kStep : kRank) * kFirstPitch;
   static constexpr int kStage = kX + kFirst;  // elements
@@ -551,7 +560,7 @@ struct SecondShape {
   static constexpr int kRowWarps = kTile / 16, kOther = 8 / kRowWarps;
   static constexpr int kWarpCols = kTile == 64 ? (sizeof(T) == 4 ? 32 : 64) : (sizeof(T) == 4 ? 16 : 32);
   static constexpr int kCols = kOther * kWarpCols;  // columns of y to a stage
-  static constexpr int kStages = sizeof(T) == 4 || kRank == 64 ? 2 : HKV_S2;
+  static constexpr int kStages = sizeof(T) == 4 ? 2 : kRank == 64 ? HKV_S3 : HKV_S2;
   static constexpr int kPitch = kCols + 8, kSecondPitch = kBack ? kPitch : kRank + 8, kHiddenPitch = kRank + 8;
   static constexpr int kBase = kTile * kPitch, kSecond = (kBack ? kRank : kCols) * kSecondPitch;
   static constexpr int kStage = kBase + kSecond;  // elements
