@@ -410,6 +410,18 @@ struct Chain {
   bool follows;           // the second product comes after a first one
 };
 
+// Four numbers of a row's c h or dh, as planes.
+template <class T, int kRank>
+__device__ __forceinline__ void put_hidden(__nv_bfloat16* hidden, uint64_t row, int col, float4 v, float scale) {
+  using P = Planes<T>;
+  uint32_t lo[P::kP], hi[P::kP];
+  split_pair<P::kP>(v.x * scale, v.y * scale, lo);
+  split_pair<P::kP>(v.z * scale, v.w * scale, hi);
+  __nv_bfloat16* const h = hidden + row * (P::kP * kRank) + col;
+#pragma unroll
+  for (int p = 0; p < P::kP; ++p) *reinterpret_cast<uint2*>(h + p * kRank) = make_uint2(lo[p], hi[p]);
+}
+
 // ---------------------------------------------------------------------------
 // the first product
 // ---------------------------------------------------------------------------
@@ -500,7 +512,6 @@ template <class T, int kRank, int kTile, bool kBack>
 __global__ void __launch_bounds__(kAdapterThreads)
     first_kernel(const __grid_constant__ Chain<T> a) {
   using S = FirstShape<T, kRank, kTile, kBack>;
-  using P = Planes<T>;
   extern __shared__ __align__(16) uint8_t smem[];
   const uint32_t tid = threadIdx.x, warp = tid >> 5;
   pdl_wait();
@@ -528,12 +539,7 @@ __global__ void __launch_bounds__(kAdapterThreads)
   auto put = [&](int i, float4 v) {
     const int row = i * 4 / kRank, col = i * 4 % kRank;
     if (row >= t.rows) return;
-    uint32_t lo[P::kP], hi[P::kP];
-    split_pair<P::kP>(v.x * scale, v.y * scale, lo);
-    split_pair<P::kP>(v.z * scale, v.w * scale, hi);
-    __nv_bfloat16* const h = a.hidden + (t.row0 + row) * (P::kP * kRank) + col;
-#pragma unroll
-    for (int p = 0; p < P::kP; ++p) *reinterpret_cast<uint2*>(h + p * kRank) = make_uint2(lo[p], hi[p]);
+    put_hidden<T, kRank>(a.hidden, t.row0 + row, col, v, scale);
   };
   if (a.parts == 1) {
     for (int i = tid; i < kQuads; i += kAdapterThreads) put(i, block_sum(i));
@@ -1164,8 +1170,8 @@ __global__ void __launch_bounds__(kAdapterThreads, GradShape<T, kRank>::kBlocks)
 // ---------------------------------------------------------------------------
 // launches
 // ---------------------------------------------------------------------------
-template <auto kKernel, class A>
-cudaError_t launch_clusters(const A& args, uint64_t blocks, uint32_t parts, int smem, cudaStream_t st) {
+template <auto kKernel, class... A>
+cudaError_t launch_clusters(uint64_t blocks, uint32_t parts, int threads, int smem, cudaStream_t st, const A&... args) {
   if (blocks > 0x7FFFFFFFull) return cudaErrorInvalidValue;
   if (smem > 40 * 1024) {  // static shared memory counts too; once for each device
     static std::atomic<uint64_t> allowed{0};
@@ -1181,7 +1187,7 @@ cudaError_t launch_clusters(const A& args, uint64_t blocks, uint32_t parts, int 
   }
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(static_cast<unsigned>(blocks));
-  cfg.blockDim = dim3(kAdapterThreads);
+  cfg.blockDim = dim3(threads);
   cfg.dynamicSmemBytes = smem;
   cfg.stream = st;
   cudaLaunchAttribute attr[2];
@@ -1192,83 +1198,7 @@ cudaError_t launch_clusters(const A& args, uint64_t blocks, uint32_t parts, int 
   attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
   cfg.attrs = attr;
   cfg.numAttrs = parts > 1 ? 2 : 1;
-  return cudaLaunchKernelEx(&cfg, kKernel, args);
-}
-
-template <class T, int kRank, int kTile, bool kBack>
-cudaError_t launch_chain(Chain<T> a, cudaStream_t st) {
-  using F = FirstShape<T, kRank, kTile, kBack>;
-  using S = SecondShape<T, kRank, kTile, kBack>;
-  const uint64_t slots = slots_of(a.q.tokens, a.q.requests, kTile);
-  const uint64_t tiles = a.q.tokens / kTile + (a.q.requests < a.q.tokens ? a.q.requests : a.q.tokens) + 1;
-  a.parts = 1;
-  // all blocks at once on the SMs, each with four stages of columns at least
-  const uint64_t room = sm_count() * (HKV_PM * 227ull * 1024 / (F::kBytes + 1024)) / 100;
-  while (a.parts < kAdapterParts && a.in >= 4ull * a.parts * F::kStep && 2 * tiles * a.parts <= room) a.parts *= 2;
-  a.part_in = ((a.in + a.parts - 1) / a.parts + 63) / 64 * 64;
-  a.follows = a.q.requests > 0;
-  if (a.follows) {  // (without a request all rows are base's)
-    const cudaError_t e = launch_clusters<first_kernel<T, kRank, kTile, kBack>>(a, slots * a.parts, a.parts, F::kBytes, st);
-    if (e != cudaSuccess) return e;
-  }
-  // blocks for every SM several times over, of up to eight stages
-  uint64_t steps = (a.out + S::kCols - 1) / S::kCols, each = (tiles * steps + HKV_GM * 1ull * sm_count() - 1) / (HKV_GM * 1ull * sm_count());
-  if (each > HKV_EM) each = HKV_EM;
-  a.groups = static_cast<uint32_t>((steps + each - 1) / each);
-  a.group_out = each * S::kCols;
-  return launch_clusters<second_kernel<T, kRank, kTile, kBack>>(a, slots * a.groups, 1, S::kBytes, st);
-}
-
-// Few rows: one kernel, clusters of as many blocks as fill the SMs, and several
-// clusters to a tile where its columns of y are many.
-template <auto kKernel, class T>
-cudaError_t launch_few(Chain<T> a, uint64_t slots, uint64_t tiles, uint64_t cols, int smem, cudaStream_t st) {
-  const uint64_t room = HKV_ROOM * sm_count();
-  a.parts = 1;
-  while (a.parts < kAdapterParts && 2 * tiles * a.parts <= room && (a.in >= 256ull * a.parts || a.out > cols * a.parts)) a.parts *= 2;
-  a.part_in = ((a.in + a.parts - 1) / a.parts + 63) / 64 * 64;
-  const uint64_t most = (a.out + cols * a.parts - 1) / (cols * a.parts);
-  uint64_t groups = (room + tiles * a.parts - 1) / (tiles * a.parts);
-  // every group has the first product anew
-  if (groups > 1 + a.out / a.in) groups = 1 + a.out / a.in;
-  if (groups > most) groups = most;
-  a.groups = static_cast<uint32_t>(groups);
-  a.group_out = ((a.out + groups * a.parts - 1) / (groups * a.parts) + 31) / 32 * 32;
-  return launch_clusters<kKernel>(a, slots * groups * a.parts, a.parts, smem, st);
-}
-
-template <class T, int kRank, bool kBack>
-cudaError_t chain_of(const Chain<T>& a, cudaStream_t st) {
-  const uint64_t tokens = a.q.tokens, requests = a.q.requests;
-  if constexpr (!kBack)
-    if (tokens <= requests && a.x_whole && a.first.whole && a.second.whole && a.in % 8 == 0 && a.rank % 8 == 0)
-      return launch_few<thin_kernel<T, kRank>>(a, slots_of(tokens, requests, 1), tokens, thin_columns<T, kRank>() * kAdapterThreads, 0, st);
-  if (tokens < 32 * requests)
-    return launch_few<short_kernel<T, kRank, kBack>>(a, slots_of(tokens, requests, 16), tokens / 16 + (requests < tokens ? requests : tokens) + 1,
-                                                     SecondShape<T, kRank, 16, kBack>::kCols, ShortShape<T, kRank, kBack>::kBytes, st);
-  return launch_chain<T, kRank, 64, kBack>(a, st);
-}
-template <class T, bool kBack>
-cudaError_t chain(const Chain<T>& a, cudaStream_t st) {
-  return a.rank <= 16 ? chain_of<T, 16, kBack>(a, st) : a.rank <= 32 ? chain_of<T, 32, kBack>(a, st) : chain_of<T, 64, kBack>(a, st);
-}
-
-template <class T, int kRank>
-cudaError_t launch_grads(Grads<T> a, cudaStream_t st) {
-  using S = GradShape<T, kRank>;
-  a.blocks[0] = a.out[0] ? (a.cols[0] + S::kCols - 1) / S::kCols : 0;
-  a.blocks[1] = a.out[1] ? (a.cols[1] + S::kCols - 1) / S::kCols : 0;
-  const uint64_t blocks = a.q.adapters * (a.blocks[0] + a.blocks[1]);
-  if (!blocks) return cudaSuccess;
-  a.parts = 1;
-  while (a.parts < kAdapterParts && blocks * a.parts < HKV_GP * 1ull * sm_count() &&
-         a.q.tokens >= 2ull * a.parts * S::kRows)
-    a.parts *= 2;  // (kRank is a multiple of it)
-  return launch_clusters<grads_kernel<T, kRank>>(a, blocks * a.parts, a.parts, S::kBytes, st);
-}
-template <class T>
-cudaError_t grads(const Grads<T>& a, cudaStream_t st) {
-  return a.rank <= 16 ? launch_grads<T, 16>(a, st) : a.rank <= 32 ? launch_grads<T, 32>(a, st) : launch_grads<T, 64>(a, st);
+  return cudaLaunchKernelEx(&cfg, kKernel, args...);
 }
 
 // adapter_f32.cu, adapter_bf16.cu, adapter_f16.cu
@@ -1276,5 +1206,8 @@ template <class T>
 cudaError_t run_chain(const Chain<T>& a, bool back, cudaStream_t st);
 template <class T>
 cudaError_t run_grads(const Grads<T>& a, cudaStream_t st);
+// Bounded waits of theirs that ran out, of the types that have any.
+template <class T>
+cudaError_t adapter_wait_timeouts(uint64_t* count);
 
 }  // namespace hkv

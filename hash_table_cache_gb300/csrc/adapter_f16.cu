@@ -1,5 +1,5 @@
 // adapter_f16.cu -- the adapters' kernels on __half matrices.
-#include "adapter.cuh"
+#include "adapter_launch.cuh"
 
 namespace hkv {
 
@@ -10,6 +10,11 @@ cudaError_t run_chain<__half>(const Chain<__half>& a, bool back, cudaStream_t st
 template <>
 cudaError_t run_grads<__half>(const Grads<__half>& a, cudaStream_t st) {
   return grads<__half>(a, st);
+}
+
+template <>
+cudaError_t adapter_wait_timeouts<__half>(uint64_t* count) {
+  return tensor::wait_timeouts(count);
 }
 
 }  // namespace hkv

@@ -32,6 +32,13 @@
 #include "mx.cuh"
 
 namespace hkv {
+
+// of the kernels of adapter_bf16.cu and adapter_f16.cu
+template <class T>
+cudaError_t adapter_wait_timeouts(uint64_t* count);
+extern template cudaError_t adapter_wait_timeouts<__nv_bfloat16>(uint64_t* count);
+extern template cudaError_t adapter_wait_timeouts<__half>(uint64_t* count);
+
 namespace {
 
 __device__ unsigned long long g_wait_timeouts;
@@ -858,8 +865,11 @@ hkv_status hkv_get_wait_timeouts(uint64_t* timeouts_host) {
   unsigned long long v = 0;
   cudaError_t e = cudaDeviceSynchronize();
   if (e == cudaSuccess) e = cudaMemcpyFromSymbol(&v, hkv::g_wait_timeouts, sizeof(v));
+  uint64_t more[2] = {};
+  if (e == cudaSuccess) e = hkv::adapter_wait_timeouts<__nv_bfloat16>(&more[0]);
+  if (e == cudaSuccess) e = hkv::adapter_wait_timeouts<__half>(&more[1]);
   if (e != cudaSuccess) return hkv::op_status(e);
-  *timeouts_host = v;
+  *timeouts_host = v += more[0] + more[1];
   return v ? HKV_ERR_TIMEOUT : HKV_OK;
 }
 
