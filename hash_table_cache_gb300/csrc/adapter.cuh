@@ -52,7 +52,7 @@
 #define HKV_GP 2
 #endif
 #ifndef HKV_GM
-#define HKV_GM 16
+#define HKV_GM 8
 #endif
 #ifndef HKV_EM
 #define HKV_EM 16

@@ -3,6 +3,15 @@
 
 #include "adapter_tensor.cuh"
 
+#ifndef HKV_TENSOR3
+#define HKV_TENSOR3 1
+#endif
+#ifndef HKV_GT
+#define HKV_GT 1
+#endif
+#ifndef HKV_TENSOR2
+#define HKV_TENSOR2 1
+#endif
 #ifndef HKV_TENSOR
 #define HKV_TENSOR 1
 #endif
@@ -19,7 +28,7 @@ cudaError_t launch_chain(Chain<T> a, cudaStream_t st) {
   a.follows = a.q.requests > 0 && a.q.adapters > 0;
   bool by_tensor = false;
   int bytes = F::kBytes;
-  tensor::Maps maps;
+  tensor::Maps maps{};
   if constexpr (sizeof(T) == 2) {
     by_tensor = HKV_TENSOR && a.follows && tensor::make_maps<T, kRank, kBack>(&maps, a);
     if (by_tensor) bytes = tensor::Shape<kRank>::kBytes;
@@ -43,6 +52,12 @@ cudaError_t launch_chain(Chain<T> a, cudaStream_t st) {
   if (each > HKV_EM) each = HKV_EM;
   a.groups = static_cast<uint32_t>((steps + each - 1) / each);
   a.group_out = each * S::kCols;
+  if constexpr (std::is_same_v<T, __nv_bfloat16>) {
+    tensor::SecondMaps maps{};
+    if (HKV_TENSOR2 && a.follows && tensor::make_maps<kRank, kBack>(&maps, a))
+      return launch_clusters<tensor::second_tensor_kernel<kRank, kBack>>(
+          slots * a.groups, 1, tensor::SecondShape<kRank>::kThreads, tensor::SecondShape<kRank>::kBytes, st, maps, a);
+  }
   return launch_clusters<second_kernel<T, kRank, kTile, kBack>>(slots * a.groups, 1, kAdapterThreads, S::kBytes, st, a);
 }
 
@@ -91,6 +106,14 @@ cudaError_t launch_grads(Grads<T> a, cudaStream_t st) {
   while (a.parts < kAdapterParts && blocks * a.parts < HKV_GP * 1ull * sm_count() &&
          a.q.tokens >= 2ull * a.parts * S::kRows)
     a.parts *= 2;  // (kRank is a multiple of it)
+  if constexpr (std::is_same_v<T, __nv_bfloat16>) {
+    tensor::GradMaps maps{};
+    if (HKV_TENSOR3 && a.q.requests && a.q.tokens >= HKV_GT * a.q.requests && tensor::make_maps<kRank>(&maps, a)) {
+      if (a.parts > kRank / 4) a.parts = kRank / 4;  // four ranks to a part at least
+      return launch_clusters<tensor::grads_tensor_kernel<kRank>>(blocks * a.parts, a.parts, tensor::GradShape<kRank>::kThreads,
+                                                                 tensor::GradShape<kRank>::kBytes, st, maps, a);
+    }
+  }
   return launch_clusters<grads_kernel<T, kRank>>(blocks * a.parts, a.parts, kAdapterThreads, S::kBytes, st, a);
 }
 template <class T>

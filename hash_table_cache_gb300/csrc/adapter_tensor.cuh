@@ -249,6 +249,438 @@ __global__ void __launch_bounds__(Shape<kRank>::kThreads)
   if (a.parts > 1) cluster_meet();  // the others stay until their sums are read
 }
 
+// ---------------------------------------------------------------------------
+// The second product of bfloat16 matrices: 128 columns of y in the lanes, the tile's 64
+// rows in the columns of TMEM, so that a warp's lanes are neighbouring columns of a row
+// and base and y are read and written row by row as they lie.  The two planes of c h (or
+// dh) are multiplied by the same columns of the second factor and added up in TMEM.
+// One thread loads (the factor's columns, base, and the planes once the first product is
+// done), one multiplies, four warps add onto base.
+// ---------------------------------------------------------------------------
+struct SecondMaps {  // the second factor; c h or dh: tokens x planes of kRank; base
+  CUtensorMap second, hidden, base;
+};
+
+template <int kRank>
+struct SecondShape {
+  static constexpr int kTile = 64, kCols = 128;
+  static constexpr int kGroups = 2, kAdding = 4 * kGroups, kThreads = 64 + 32 * kAdding;  // warps that add, by rows
+  static constexpr int kFactor = kCols * kRank * 2, kBase = kTile * kCols * 2, kStage = kFactor + kBase;
+  static constexpr int kPlane = kTile * kRank * 2, kPlanes = 2 * kPlane;
+  static constexpr int kStages = kRank == 16 ? 3 : 2;
+  static constexpr int kBytes = kPlanes + kStages * kStage + 1024;
+  static_assert(kPlane % 1024 == 0 && kFactor % 1024 == 0, "swizzle");
+};
+// Upper halves: rows of kRank numbers along k, in the swizzle of their length, groups of
+// 8 of them; and columns of y along the lanes in pieces of 64, a row of them for each k.
+template <int kRank>
+__host__ __device__ constexpr uint32_t rank_rows() { return along_rank<kRank>(); }
+
+template <int kRank, bool kBack>
+__global__ void __launch_bounds__(SecondShape<kRank>::kThreads, 3)
+    second_tensor_kernel(const __grid_constant__ SecondMaps maps, const __grid_constant__ Chain<__nv_bfloat16> a) {
+  using S = SecondShape<kRank>;
+  extern __shared__ uint8_t raw[];
+  uint8_t* const smem = raw + (1024 - (smem_u32(raw) & 1023)) % 1024;
+  uint8_t* const stages = smem + S::kPlanes;
+  __shared__ uint64_t full[S::kStages], empty[S::kStages], planes, ready[2], drained[2];
+  __shared__ uint32_t tmem_base;
+  const uint32_t tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  if (tid == 0) {
+    asm volatile("prefetch.tensormap [%0];" ::"l"(&maps.second) : "memory");
+    asm volatile("prefetch.tensormap [%0];" ::"l"(&maps.hidden) : "memory");
+    for (int s = 0; s < S::kStages; ++s) {
+      mbar_init(&full[s], 1);
+      mbar_init(&empty[s], 1 + S::kAdding);  // multiplied, and base read
+    }
+    mbar_init(&planes, 1);
+    for (int b = 0; b < 2; ++b) {
+      mbar_init(&ready[b], 1);
+      mbar_init(&drained[b], S::kAdding);
+    }
+    fence_proxy_async_smem();
+  }
+  if (warp == 1) {
+    asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], 128;" ::"r"(smem_u32(&tmem_base)) : "memory");
+    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;");
+  }
+  asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
+  __syncthreads();
+  asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
+  const uint32_t tmem = tmem_base;
+
+  // before the first product's end: its kernel lets this one start when all that came
+  // before is complete, and it writes `hidden` alone
+  const uint64_t col0 = static_cast<uint64_t>(blockIdx.x % a.groups) * a.group_out;
+  const uint64_t col1 = min(col0 + a.group_out, a.out);
+  Tile t;
+  const bool any = Tile::find<S::kTile>(a.q, blockIdx.x / a.groups, t) && col0 < col1;
+  const bool adapts = any && t.adapter >= 0;
+  const uint32_t steps = any && (adapts || a.y != a.base) ? static_cast<uint32_t>((col1 - col0 + S::kCols - 1) / S::kCols) : 0;
+  __syncwarp();
+  const bool has_base = a.base != nullptr;
+
+  if (warp == 0 && elect()) {
+    bool ok = true;
+    uint32_t step = 0;
+    for (; step < steps; ++step) {
+      const uint32_t s = step % S::kStages, round = step / S::kStages;
+      if (round > 0 && !wait(&empty[s], (round + 1) & 1)) {
+        ok = false;
+        break;
+      }
+      uint8_t* const stage = stages + s * S::kStage;
+      const int c = static_cast<int>(col0 + static_cast<uint64_t>(step) * S::kCols);
+      const uint32_t bytes = (adapts ? S::kFactor : 0) + (has_base ? S::kBase : 0);
+      mbar_arrive_expect_tx(&full[s], bytes);
+      if (adapts) {
+        if constexpr (kBack) {
+          load_box(stage, &maps.second, c, 0, static_cast<int>(t.adapter), &full[s]);
+          load_box(stage + S::kFactor / 2, &maps.second, c + 64, 0, static_cast<int>(t.adapter), &full[s]);
+        } else {
+          load_box(stage, &maps.second, 0, c, static_cast<int>(t.adapter), &full[s]);
+        }
+      }
+      if (has_base) load_box(stage + S::kFactor, &maps.base, c, static_cast<int>(t.row0), &full[s]);
+      if (adapts && (step + 1 == S::kStages || (step + 1 == steps && steps < S::kStages))) {
+        pdl_wait();  // the first product is done
+        mbar_arrive_expect_tx(&planes, S::kPlanes);
+        load_box(smem, &maps.hidden, 0, static_cast<int>(t.row0), &planes);
+        load_box(smem + S::kPlane, &maps.hidden, kRank, static_cast<int>(t.row0), &planes);
+      }
+    }
+    // before the block ends, the loads still in flight where a wait ran out
+    if (!ok) {
+      if (adapts) wait(&planes, 0);
+      for (uint32_t i = step - S::kStages; i < step; ++i)
+        if (!wait(&full[i % S::kStages], i / S::kStages & 1)) break;
+    }
+  } else if (warp == 1 && adapts && steps && elect()) {
+    bool ok = wait(&planes, 0);
+    const uint32_t units = (smem_u32(smem) & 0x3FFFF) >> 4, factors = (smem_u32(stages) & 0x3FFFF) >> 4;
+    constexpr uint32_t kIdesc = 1u << 4 | 1u << 7 | 1u << 10 | (kBack ? 1u : 0u) << 15 | (uint32_t)(S::kTile >> 3) << 17 | (128u >> 4) << 24;
+    uint32_t step = 0;
+    for (; ok && step < steps; ++step) {
+      const uint32_t s = step % S::kStages, b = step & 1;
+      if ((step >= 2 && !wait(&drained[b], (step / 2 + 1) & 1)) || !wait(&full[s], step / S::kStages & 1)) {
+        ok = false;
+        break;
+      }
+      asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
+      // (a factor's pieces of 64 columns are kRank rows of 128 bytes)
+      const uint32_t w = factors + s * (S::kStage / 16) + (kBack ? (uint32_t)(kRank * 8) << 16 : 0u);
+#pragma unroll
+      for (int p = 0; p < 2; ++p)
+#pragma unroll
+        for (int i = 0; i < kRank / 16; ++i)
+          asm volatile(
+              "{\n .reg .pred p;\n .reg .b64 a, b;\n setp.ne.u32 p, %4, 0;\n"
+              " mov.b64 a, {%1, %5};\n mov.b64 b, {%2, %6};\n"
+              " tcgen05.mma.cta_group::1.kind::f16 [%0], a, b, %3, p;\n}" ::"r"(tmem + b * 64),
+              "r"(w + i * (kBack ? 128 : 2)), "r"(units + p * (S::kPlane / 16) + 2 * i), "r"(kIdesc), "r"((uint32_t)(p + i)),
+              "n"(kBack ? kAlongK : rank_rows<kRank>()), "n"(rank_rows<kRank>())
+              : "memory");
+      commit(&empty[s]);
+      commit(&ready[b]);
+    }
+    // where a wait ran out, the loads that follow are waited for
+    if (!ok) {
+      wait(&planes, 0);
+      for (uint32_t i = step; i < steps && i < step + S::kStages; ++i)
+        if (!wait(&full[i % S::kStages], i / S::kStages & 1)) break;
+    }
+  } else if (warp >= 2) {
+    const uint32_t quarter = warp % 4;  // of the lanes, the only one that a warp can read
+    constexpr int kRows = S::kTile / S::kGroups;
+    const int first = (warp - 2) / 4 * kRows;
+    pdl_wait();
+    pdl_trigger();
+    __nv_bfloat16* const y = a.y + t.row0 * a.y_stride;
+    for (uint32_t step = 0; step < steps; ++step) {
+      const uint32_t s = step % S::kStages, b = step & 1;
+      const __nv_bfloat16* const base = reinterpret_cast<const __nv_bfloat16*>(stages + s * S::kStage + S::kFactor) + quarter * 32 + lane;
+      const uint64_t col = col0 + static_cast<uint64_t>(step) * S::kCols + quarter * 32 + lane;
+      if (!wait_warp(&full[s], step / S::kStages & 1)) break;
+      if (adapts && !wait_warp(&ready[b], step / 2 & 1)) break;
+      asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
+      const bool mine = col < col1;
+      __nv_bfloat16* to = y + col;
+#pragma unroll
+      for (int r = 0; r < kRows; r += 16) {
+        const int r0 = first + r;
+        if (r0 >= t.rows) break;
+        __syncwarp();
+        float v[16] = {};
+        if (adapts) {
+          uint32_t* const u = reinterpret_cast<uint32_t*>(v);
+          asm volatile(
+              "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15}, [%16];"
+              : "=r"(u[0]), "=r"(u[1]), "=r"(u[2]), "=r"(u[3]), "=r"(u[4]), "=r"(u[5]), "=r"(u[6]), "=r"(u[7]), "=r"(u[8]),
+                "=r"(u[9]), "=r"(u[10]), "=r"(u[11]), "=r"(u[12]), "=r"(u[13]), "=r"(u[14]), "=r"(u[15])
+              : "r"(tmem + b * 64 + (quarter * 32 << 16) + r0));
+          asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
+#pragma unroll
+          for (int i = 0; i < 16; ++i) asm volatile("" : "+f"(v[i]));  // used after the wait only
+        }
+        if (has_base)
+#pragma unroll
+          for (int i = 0; i < 16; ++i) v[i] += __bfloat162float(base[(r0 + i) * S::kCols]);
+        const int rows = mine ? t.rows - r0 : 0;
+        __nv_bfloat16* out = to + r0 * a.y_stride;
+        if (rows >= 16) {
+#pragma unroll
+          for (int i = 0; i < 16; ++i, out += a.y_stride) *out = __float2bfloat16_rn(v[i]);
+        } else {
+#pragma unroll
+          for (int i = 0; i < 16; ++i, out += a.y_stride)
+            if (i < rows) *out = __float2bfloat16_rn(v[i]);
+        }
+      }
+      asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
+      __syncwarp();
+      if (lane == 0) {
+        asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(smem_u32(&empty[s])) : "memory");
+        asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(smem_u32(&drained[b])) : "memory");
+        // (a stage of a tile without an adapter is not multiplied)
+        if (!adapts && warp == 2) asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(smem_u32(&empty[s])) : "memory");
+      }
+    }
+  }
+  asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
+  __syncthreads();
+  if (warp == 1) asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, 128;" ::"r"(tmem));
+}
+
+// ---------------------------------------------------------------------------
+// The adapters' gradients of bfloat16 matrices: 128 columns of x or dy in the lanes, the
+// ranks in the columns of TMEM, rows of the batch along k.  Both lie with their rows
+// apart, which the tensor core takes as it is.  Rows of a tile that are another
+// request's are made zeros in shared memory, of both operands.
+// ---------------------------------------------------------------------------
+struct GradMaps {  // x and dy; dh and c h
+  CUtensorMap m[2], p[2];
+};
+
+template <int kRank>
+struct GradShape {
+  static constexpr int kRows = 64, kCols = 128, kThreads = 128;
+  static constexpr int kPiece = kRows * 128, kM = 2 * kPiece, kPlane = kRows * kRank * 2, kStage = kM + 2 * kPlane;
+  static constexpr int kStages = kRank == 64 ? 2 : 3;
+  static constexpr int kPitch = kRank + 4, kSums = kCols * kPitch * 4;  // [cols][kPitch]
+  static constexpr int kColumns = kRank < 32 ? 32 : kRank;
+  static constexpr int kBytes = (kStages * kStage > 2 * kSums ? kStages * kStage : 2 * kSums) + 1024;
+};
+
+template <int kRank>
+__global__ void __launch_bounds__(GradShape<kRank>::kThreads)
+    grads_tensor_kernel(const __grid_constant__ GradMaps maps, const __grid_constant__ Grads<__nv_bfloat16> a) {
+  using S = GradShape<kRank>;
+  constexpr int kThreads = S::kThreads;
+  extern __shared__ uint8_t raw[];
+  uint8_t* const smem = raw + (1024 - (smem_u32(raw) & 1023)) % 1024;
+  __shared__ uint64_t full[S::kStages], empty[S::kStages], done;
+  __shared__ uint32_t tmem_base, multiplied;
+  __shared__ uint64_t from[kThreads], to[kThreads];  // rows of the adapter's requests
+  __shared__ uint32_t counts[kThreads / 32];
+  const uint32_t tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  if (tid == 0) {
+    for (int s = 0; s < S::kStages; ++s) {
+      mbar_init(&full[s], 1);
+      mbar_init(&empty[s], 1);
+    }
+    mbar_init(&done, 1);
+    multiplied = 0;
+    fence_proxy_async_smem();
+  }
+  if (warp == 1) {
+    asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(&tmem_base)),
+                 "n"(S::kColumns)
+                 : "memory");
+    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;");
+  }
+  asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
+  __syncthreads();
+  asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
+  const uint32_t tmem = tmem_base;
+  pdl_trigger();
+  pdl_wait();
+
+  const uint32_t part = blockIdx.x % a.parts;
+  const uint64_t all = a.blocks[0] + a.blocks[1];
+  const uint64_t adapter = blockIdx.x / a.parts / all;
+  uint64_t block = blockIdx.x / a.parts % all;
+  const int sel = block >= a.blocks[0];
+  if (sel) block -= a.blocks[0];
+  const uint64_t col0 = block * S::kCols, cols = a.cols[sel];
+
+  uint64_t tile = 0;         // of the adapter's, counted over its requests
+  uint32_t step = 0;         // of this block's tiles
+  bool ok = true;            // the loading thread's, and the multiplying warp's
+  for (uint64_t s0 = 0; s0 < a.q.requests; s0 += kThreads) {
+    // the requests of this adapter among the next ones, in their order
+    const uint64_t s = s0 + tid;
+    const bool mine = s < a.q.requests && a.q.adapter(s + 1) == static_cast<int64_t>(adapter);
+    const uint32_t votes = __ballot_sync(0xFFFFFFFFu, mine);
+    if (lane == 0) counts[warp] = __popc(votes);
+    __syncthreads();
+    uint32_t at = __popc(votes & ((1u << lane) - 1)), found = 0;
+    for (uint32_t w = 0; w < kThreads / 32; ++w) {
+      if (w < warp) at += counts[w];
+      found += counts[w];
+    }
+    if (mine) {
+      from[at] = a.q.start(s + 1);
+      to[at] = a.q.start(s + 2);
+    }
+    __syncthreads();
+    uint32_t i = 0;
+    uint64_t row = found ? from[0] : 0;
+    auto next = [&](uint64_t& row0, int& rows) {  // this block's next tile; false: none left
+      while (i < found) {
+        if (row >= to[i]) {
+          if (++i < found) row = from[i];
+          continue;
+        }
+        row0 = row;
+        rows = static_cast<int>(min(to[i] - row, static_cast<uint64_t>(S::kRows)));
+        row += S::kRows;
+        if (tile++ % a.parts == part) return true;
+      }
+      return false;
+    };
+    uint64_t row0;
+    int rows;
+    if (warp == 0) {
+      while (ok && next(row0, rows)) {
+        const uint32_t st = step % S::kStages, round = step / S::kStages;
+        if (round > 0 && !wait_warp(&empty[st], (round + 1) & 1)) {
+          ok = false;
+          break;
+        }
+        if (elect()) {
+          uint8_t* const b = smem + st * S::kStage;
+          const int y = static_cast<int>(row0), c = static_cast<int>(col0);
+          mbar_arrive_expect_tx(&full[st], S::kStage);
+          load_box(b, &maps.m[sel], c, y, &full[st]);
+          load_box(b + S::kPiece, &maps.m[sel], c + 64, y, &full[st]);
+          load_box(b + S::kM, &maps.p[sel], 0, y, &full[st]);
+          load_box(b + S::kM + S::kPlane, &maps.p[sel], kRank, y, &full[st]);
+        }
+        __syncwarp();
+        ++step;
+      }
+    } else if (warp == 1) {
+      while (ok && next(row0, rows)) {
+        const uint32_t st = step % S::kStages;
+        if (!wait_warp(&full[st], step / S::kStages & 1)) {
+          ok = false;
+          break;
+        }
+        uint8_t* const b = smem + st * S::kStage;
+        if (rows < S::kRows) {  // (a row's bytes change places within the row)
+          const uint4 zero = make_uint4(0, 0, 0, 0);
+          for (int e = rows * 8 + lane; e < S::kRows * 8; e += 32) {
+            reinterpret_cast<uint4*>(b)[e] = zero;
+            reinterpret_cast<uint4*>(b + S::kPiece)[e] = zero;
+          }
+          for (int e = rows * (kRank / 8) + lane; e < S::kRows * (kRank / 8); e += 32) {
+            reinterpret_cast<uint4*>(b + S::kM)[e] = zero;
+            reinterpret_cast<uint4*>(b + S::kM + S::kPlane)[e] = zero;
+          }
+          fence_proxy_async_smem();
+          __syncwarp();
+        }
+        asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
+        if (elect()) {
+          constexpr uint32_t kIdesc = 1u << 4 | 1u << 7 | 1u << 10 | 3u << 15 | (uint32_t)(kRank >> 3) << 17 | (128u >> 4) << 24;
+          const uint32_t m = ((smem_u32(b) & 0x3FFFF) >> 4) + ((uint32_t)(S::kPiece >> 4) << 16);
+          const uint32_t h = ((smem_u32(b + S::kM) & 0x3FFFF) >> 4) + ((uint32_t)kRank << 16);
+#pragma unroll
+          for (int p = 0; p < 2; ++p)
+#pragma unroll
+            for (int k = 0; k < S::kRows / 16; ++k)
+              asm volatile(
+                  "{\n .reg .pred p;\n .reg .b64 a, b;\n setp.ne.u32 p, %4, 0;\n"
+                  " mov.b64 a, {%1, %5};\n mov.b64 b, {%2, %6};\n"
+                  " tcgen05.mma.cta_group::1.kind::f16 [%0], a, b, %3, p;\n}" ::"r"(tmem),
+                  "r"(m + k * 128), "r"(h + p * (S::kPlane / 16) + k * 2 * kRank), "r"(kIdesc), "r"(step + p + k),
+                  "n"(kAlongK), "n"(along_rank<kRank>())
+                  : "memory");
+          commit(&empty[st]);
+        }
+        __syncwarp();
+        ++step;
+      }
+    }
+    __syncthreads();  // the lists are read
+  }
+  // before the block ends: the loads in flight where a wait ran out (the loading thread's
+  // last ones, which the multiplying warp has not seen), and the products
+  if (warp == 0 && !ok)
+    for (uint32_t i = step - S::kStages; i < step; ++i)
+      if (!wait(&full[i % S::kStages], i / S::kStages & 1)) break;
+  __syncwarp();
+  if (warp == 1) {
+    if (lane == 0) multiplied = ok && step > 0;
+    if (ok && step > 0 && elect()) commit(&done);
+    if (!ok && elect())
+      for (uint32_t i = step + 1; i < step + S::kStages; ++i)
+        if (!wait(&full[i % S::kStages], i / S::kStages & 1)) break;
+    __syncwarp();
+  }
+  __syncthreads();
+  // the sums of a column to a thread
+  float* const sums = reinterpret_cast<float*>(smem);
+  const bool summed = multiplied && wait_warp(&done, 0);
+  asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
+#pragma unroll
+  for (int c = 0; c < kRank; c += 16) {
+    uint32_t r[16] = {};
+    if (summed) {
+      asm volatile(
+          "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15}, [%16];"
+          : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]),
+            "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
+          : "r"(tmem + (warp * 32 << 16) + c));
+      asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
+#pragma unroll
+      for (int i = 0; i < 16; ++i) asm volatile("" : "+r"(r[i]));  // used after the wait only
+    }
+#pragma unroll
+    for (int i = 0; i < 16; i += 4)
+      *reinterpret_cast<uint4*>(sums + tid * S::kPitch + c + i) = make_uint4(r[i], r[i + 1], r[i + 2], r[i + 3]);
+  }
+  asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
+  __syncthreads();
+  if (warp == 1) asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "n"(S::kColumns));
+
+  // the parts' sums in a fixed order, and the result: a part's share are whole ranks
+  const int each = kRank / a.parts, r0 = part * each;
+  const float* total = sums;
+  if (a.parts > 1) {
+    cluster_meet();
+    float* const joined = sums + S::kSums / 4;
+    const int quads = each / 4;  // (at least one: the launch sees to it)
+    for (int e = tid; e < S::kCols * quads; e += kThreads) {
+      const int at = e / quads * S::kPitch + r0 + e % quads * 4;
+      float4 v = remote_f32x4(smem_u32(sums + at), 0);
+      for (uint32_t q = 1; q < a.parts; ++q) v = v + remote_f32x4(smem_u32(sums + at), q);
+      *reinterpret_cast<float4*>(joined + at) = v;
+    }
+    __syncthreads();
+    total = joined;
+  }
+  __nv_bfloat16* const out = a.out[sel];
+  for (int e = tid; e < each * S::kCols; e += kThreads) {
+    // neighbouring threads write neighbouring elements of either layout
+    const int r = r0 + (sel ? e % each : e / S::kCols), c = sel ? e / each : e % S::kCols;
+    if (r >= static_cast<int>(a.rank) || col0 + c >= cols) continue;
+    const uint64_t at = sel ? (adapter * cols + col0 + c) * a.rank + r : (adapter * a.rank + r) * cols + col0 + c;
+    out[at] = __float2bfloat16_rn(total[c * S::kPitch + r]);
+  }
+  if (a.parts > 1) cluster_meet();  // the others stay until their parts are read
+}
+
 using EncodeFn = decltype(&cuTensorMapEncodeTiled);
 inline EncodeFn encode_fn() {
   static EncodeFn fn = [] {
@@ -287,6 +719,59 @@ bool make_maps(Maps* maps, const Chain<T>& a) {
          f(&maps->first, kType, 3, const_cast<T*>(a.first.data), w_dims, w_strides, w_box, ones,
            CU_TENSOR_MAP_INTERLEAVE_NONE, kSwizzle, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
            CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+template <int kRank, bool kBack>
+bool make_maps(SecondMaps* maps, const Chain<__nv_bfloat16>& a) {
+  using S = SecondShape<kRank>;
+  if (!a.second.whole || (a.base && !a.base_whole)) return false;
+  const EncodeFn f = encode_fn();
+  if (!f) return false;
+  constexpr CUtensorMapDataType kType = CU_TENSOR_MAP_DATA_TYPE_BFLOAT16;
+  constexpr CUtensorMapSwizzle kRow =
+      kRank == 64 ? CU_TENSOR_MAP_SWIZZLE_128B : kRank == 32 ? CU_TENSOR_MAP_SWIZZLE_64B : CU_TENSOR_MAP_SWIZZLE_32B;
+  const cuuint32_t ones[3] = {1, 1, 1};
+  const cuuint64_t w_dims[3] = {kBack ? a.out : a.rank, kBack ? a.rank : a.out, a.q.adapters};
+  const cuuint64_t w_strides[2] = {a.second.stride * 2, a.second.step * 2};
+  const cuuint32_t w_box[3] = {kBack ? 64 : kRank, kBack ? kRank : S::kCols, 1};
+  const cuuint64_t h_dims[2] = {2 * kRank, a.q.tokens}, h_strides[1] = {4 * kRank};
+  const cuuint32_t h_box[2] = {kRank, S::kTile};
+  const cuuint64_t b_dims[2] = {a.out, a.q.tokens}, b_strides[1] = {a.base_stride * 2};
+  const cuuint32_t b_box[2] = {S::kCols, S::kTile};
+  if (a.base && f(&maps->base, kType, 2, const_cast<__nv_bfloat16*>(a.base), b_dims, b_strides, b_box, ones,
+                  CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_NONE, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                  CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) != CUDA_SUCCESS)
+    return false;
+  return f(&maps->second, kType, 3, const_cast<__nv_bfloat16*>(a.second.data), w_dims, w_strides, w_box, ones,
+           CU_TENSOR_MAP_INTERLEAVE_NONE, kBack ? CU_TENSOR_MAP_SWIZZLE_128B : kRow, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+           CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS &&
+         f(&maps->hidden, kType, 2, a.hidden, h_dims, h_strides, h_box, ones, CU_TENSOR_MAP_INTERLEAVE_NONE, kRow,
+           CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+template <int kRank>
+bool make_maps(GradMaps* maps, const Grads<__nv_bfloat16>& a) {
+  using S = GradShape<kRank>;
+  const EncodeFn f = encode_fn();
+  if (!f) return false;
+  constexpr CUtensorMapDataType kType = CU_TENSOR_MAP_DATA_TYPE_BFLOAT16;
+  constexpr CUtensorMapSwizzle kRow =
+      kRank == 64 ? CU_TENSOR_MAP_SWIZZLE_128B : kRank == 32 ? CU_TENSOR_MAP_SWIZZLE_64B : CU_TENSOR_MAP_SWIZZLE_32B;
+  const cuuint32_t ones[2] = {1, 1}, m_box[2] = {64, S::kRows}, p_box[2] = {kRank, S::kRows};
+  const cuuint64_t p_dims[2] = {2 * kRank, a.q.tokens}, p_strides[1] = {4 * kRank};
+  for (int i = 0; i < 2; ++i) {
+    if (!a.out[i]) continue;
+    const cuuint64_t m_dims[2] = {a.cols[i], a.q.tokens}, m_strides[1] = {a.stride[i] * 2};
+    if (!a.whole[i] ||
+        f(&maps->m[i], kType, 2, const_cast<__nv_bfloat16*>(a.m[i]), m_dims, m_strides, m_box, ones,
+          CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+          CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) != CUDA_SUCCESS ||
+        f(&maps->p[i], kType, 2, const_cast<__nv_bfloat16*>(a.p[i]), p_dims, p_strides, p_box, ones,
+          CU_TENSOR_MAP_INTERLEAVE_NONE, kRow, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+          CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) != CUDA_SUCCESS)
+      return false;
+  }
+  return true;
 }
 
 inline cudaError_t wait_timeouts(uint64_t* count) {
