@@ -30,45 +30,6 @@
 
 #include "operators.cuh"
 
-#ifndef HKV_PM
-#define HKV_PM 100
-#endif
-#ifndef HKV_GS
-#define HKV_GS 3
-#endif
-#ifndef HKV_ROOM
-#define HKV_ROOM 2
-#endif
-#ifndef HKV_TP
-#define HKV_TP 1
-#endif
-#ifndef HKV_TB
-#define HKV_TB 2
-#endif
-#ifndef HKV_TC
-#define HKV_TC 2
-#endif
-#ifndef HKV_GP
-#define HKV_GP 2
-#endif
-#ifndef HKV_GM
-#define HKV_GM 8
-#endif
-#ifndef HKV_EM
-#define HKV_EM 16
-#endif
-#ifndef HKV_FS
-#define HKV_FS 128
-#endif
-#ifndef HKV_FN
-#define HKV_FN 3
-#endif
-#ifndef HKV_S3
-#define HKV_S3 2
-#endif
-#ifndef HKV_S2
-#define HKV_S2 2
-#endif
 namespace hkv {
 
 constexpr int kAdapterThreads = 256;
@@ -428,8 +389,8 @@ __device__ __forceinline__ void put_hidden(__nv_bfloat16* hidden, uint64_t row, 
 template <class T, int kRank, int kTile, bool kBack>
 struct FirstShape {
   static constexpr int kRowWarps = kTile / 16, kOther = 8 / kRowWarps;  // warps along rows, along columns of x
-  static constexpr int kStep = kTile == 64 ? (sizeof(T) == 4 ? 64 : HKV_FS) : 128;  // columns of x to a stage
-  static constexpr int kStages = sizeof(T) == 4 ? 3 : kTile == 64 ? HKV_FN : 4;
+  static constexpr int kStep = kTile == 64 ? (sizeof(T) == 4 ? 64 : 128) : 128;  // columns of x to a stage
+  static constexpr int kStages = sizeof(T) == 4 || kTile == 64 ? 3 : 4;
   static constexpr int kPitch = kStep + 8, kFirstPitch = kBack ? kRank + 8 : kPitch;
   static constexpr int kX = kTile * kPitch, kFirst = (kBack ? kStep : kRank) * kFirstPitch;
   static constexpr int kStage = kX + kFirst;  // elements
@@ -566,7 +527,7 @@ struct SecondShape {
   static constexpr int kRowWarps = kTile / 16, kOther = 8 / kRowWarps;
   static constexpr int kWarpCols = kTile == 64 ? (sizeof(T) == 4 ? 32 : 64) : (sizeof(T) == 4 ? 16 : 32);
   static constexpr int kCols = kOther * kWarpCols;  // columns of y to a stage
-  static constexpr int kStages = sizeof(T) == 4 ? 2 : kRank == 64 ? HKV_S3 : HKV_S2;
+  static constexpr int kStages = 2;
   static constexpr int kPitch = kCols + 8, kSecondPitch = kBack ? kPitch : kRank + 8, kHiddenPitch = kRank + 8;
   static constexpr int kBase = kTile * kPitch, kSecond = (kBack ? kRank : kCols) * kSecondPitch;
   static constexpr int kStage = kBase + kSecond;  // elements
@@ -1001,7 +962,7 @@ template <class T, int kRank>
 struct GradShape {
   using P = Planes<T>;
   static constexpr int kRows = sizeof(T) == 4 ? 32 : 64, kCols = 128;
-  static constexpr int kStages = sizeof(T) == 4 ? 2 : HKV_GS;
+  static constexpr int kStages = sizeof(T) == 4 ? 2 : 3;
   static constexpr int kBlocks = sizeof(T) == 4 && kRank == 16 ? 3 : 2;  // of an SM
   static constexpr int kRankWarps = kRank / 16, kColWarps = 8 / kRankWarps, kWarpCols = kCols / kColWarps;
   static constexpr int kRankPitch = kRank + 8, kPitch = kCols + 8;
@@ -1020,7 +981,9 @@ __global__ void __launch_bounds__(kAdapterThreads, GradShape<T, kRank>::kBlocks)
   using P = Planes<T>;
   constexpr int kThreads = kAdapterThreads;
   extern __shared__ __align__(16) uint8_t smem[];
-  __shared__ uint64_t from[kThreads], to[kThreads];  // rows of the adapter's requests
+  // the adapter's requests: their first rows, and how many rows come before theirs
+  __shared__ uint64_t from[kThreads], before[kThreads], sums_before[kThreads / 32];
+  __shared__ uint64_t row_of[S::kStages][S::kRows];  // of the batch, for a tile's rows
   __shared__ uint32_t counts[kThreads / 32];
   const uint32_t tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const uint32_t rank_warp = warp % S::kRankWarps, col_warp = warp / S::kRankWarps;
@@ -1037,19 +1000,27 @@ __global__ void __launch_bounds__(kAdapterThreads, GradShape<T, kRank>::kBlocks)
   const __nv_bfloat16* const p = a.p[sel];
   const bool whole = a.whole[sel];
 
-  auto load = [&](int stage, uint64_t row0, int rows) {
+  auto load = [&](int stage, int rows) {
     uint8_t* const b = smem + stage * S::kStage;
-    copy_tile<T, S::kRows, S::kCols, S::kPitch>(reinterpret_cast<T*>(b), m + row0 * stride, stride, rows, cols - col0, whole);
+    constexpr int kLanes = S::kCols / 8, kPass = kThreads / kLanes;
+    const int first = tid / kLanes, col = tid % kLanes * 8;
+    const int n = static_cast<int>(max(min(static_cast<int64_t>(cols - col0) - col, static_cast<int64_t>(8)), static_cast<int64_t>(0)));
+#pragma unroll
+    for (int i = 0; i < S::kRows / kPass; ++i) {
+      const int row = first + i * kPass;
+      const bool has = row < rows && n > 0;
+      copy_eight(reinterpret_cast<T*>(b) + row * S::kPitch + col, has ? m + row_of[stage][row] * stride + col : m, has ? n : 0, whole);
+    }
     __nv_bfloat16* const planes = reinterpret_cast<__nv_bfloat16*>(b + S::kM);
     constexpr int kChunks = P::kP * S::kRows * kRank / 8;
 #pragma unroll
     for (int i = 0; i < (kChunks + kThreads - 1) / kThreads; ++i) {
       const int at = tid + i * kThreads;
       if (kChunks % kThreads && at >= kChunks) break;
-      const int row = at / (P::kP * kRank / 8), plane = at / (kRank / 8) % P::kP, col = at % (kRank / 8) * 8;
+      const int row = at / (P::kP * kRank / 8), plane = at / (kRank / 8) % P::kP, c = at % (kRank / 8) * 8;
       const bool there = row < rows;
-      copy_16(smem_u32(planes + (plane * S::kRows + row) * S::kRankPitch + col),
-              p + (row0 + (there ? row : 0)) * (P::kP * kRank) + plane * kRank + col, there ? 16 : 0);
+      copy_16(smem_u32(planes + (plane * S::kRows + row) * S::kRankPitch + c),
+              p + (there ? row_of[stage][row] : 0) * (P::kP * kRank) + plane * kRank + c, there ? 16 : 0);
     }
   };
   float acc[S::kWarpCols / 16][2][4] = {};
@@ -1078,38 +1049,60 @@ __global__ void __launch_bounds__(kAdapterThreads, GradShape<T, kRank>::kBlocks)
     }
   };
 
-  uint64_t tile = 0;  // of the adapter's, counted over its requests
+  uint64_t tile = 0;  // of the adapter's
   for (uint64_t s0 = 0; s0 < a.q.requests; s0 += kThreads) {
-    // the requests of this adapter among the next ones, in their order
+    // the requests of this adapter among the next ones, in their order, as one list of
+    // rows: tiles go across requests
     const uint64_t s = s0 + tid;
     const bool mine = s < a.q.requests && a.q.adapter(s + 1) == static_cast<int64_t>(adapter);
+    const uint64_t start = mine ? a.q.start(s + 1) : 0, end = mine ? a.q.start(s + 2) : 0;
+    const uint64_t length = end > start ? end - start : 0;
+    uint64_t upto = length;
+    for (int o = 1; o < 32; o *= 2) {
+      const uint64_t v = __shfl_up_sync(0xFFFFFFFFu, upto, o);
+      if (lane >= o) upto += v;
+    }
     const uint32_t votes = __ballot_sync(0xFFFFFFFFu, mine);
-    if (lane == 0) counts[warp] = __popc(votes);
+    if (lane == 31) {
+      counts[warp] = __popc(votes);
+      sums_before[warp] = upto;
+    }
     __syncthreads();
     uint32_t at = __popc(votes & ((1u << lane) - 1)), found = 0;
+    uint64_t left = 0, all_rows = 0;
     for (uint32_t w = 0; w < kThreads / 32; ++w) {
-      if (w < warp) at += counts[w];
+      if (w < warp) {
+        at += counts[w];
+        left += sums_before[w];
+      }
       found += counts[w];
+      all_rows += sums_before[w];
     }
     if (mine) {
-      from[at] = a.q.start(s + 1);
-      to[at] = a.q.start(s + 2);
+      from[at] = start;
+      before[at] = left + upto - length;
     }
     __syncthreads();
     // this block's tiles of theirs, the next ones' loads on the way
-    uint32_t i = 0;
-    uint64_t row = found ? from[0] : 0;
+    uint64_t row = 0;
     auto next = [&](int stage) {  // loads one; false: none left
-      while (i < found) {
-        if (row >= to[i]) {
-          if (++i < found) row = from[i];
-          continue;
-        }
+      while (row < all_rows) {
         const uint64_t row0 = row;
         row += S::kRows;
         if (tile++ % a.parts != part) continue;
-        const int rows = static_cast<int>(min(to[i] - row0, static_cast<uint64_t>(S::kRows)));
-        load(stage, row0, rows);
+        const int rows = static_cast<int>(min(all_rows - row0, static_cast<uint64_t>(S::kRows)));
+        if (static_cast<int>(tid) < rows) {
+          const uint64_t want = row0 + tid;
+          uint32_t lo = 0, hi = found;  // the last request with no more than `want` before it
+          while (hi - lo > 1) {
+            const uint32_t mid = (lo + hi) / 2;
+            if (before[mid] <= want) lo = mid;
+            else hi = mid;
+          }
+          row_of[stage][tid] = from[lo] + (want - before[lo]);
+        }
+        __syncthreads();
+        load(stage, rows);
 #pragma unroll
         for (int j = 0; j < S::kStages; ++j) in_stage[j] = stage == j ? rows : in_stage[j];
         return true;

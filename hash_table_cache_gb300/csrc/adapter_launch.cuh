@@ -1,73 +1,78 @@
 // adapter_launch.cuh -- which of the adapters' kernels a call takes, and their launches.
+//
+// Times of one call (GB300, bfloat16 unless said, CUDA graph replays; "base" and y in
+// memory, adapters in L2):
+//   one row, 4096 to 4096, rank 16                                4.2 us
+//   256 requests of one row, 64 adapters                          18 us
+//   8200 rows of 24 requests, 4096 to 8192, rank 32               67 us, 5.0 TB/s
+//   1637 rows of 16 requests, 64 to 131072, rank 8               132 us, 6.5 TB/s
+//   8224 rows of 32 requests, 4096 to 4096, rank 64               56 us, 3.6 TB/s
+//     and its backward pass                                       93 us: dx 56, gradients 36
+//   4000 rows of 333 requests, 128 to 128, rank 8, float32        10 and 21 us
 #pragma once
 
 #include "adapter_tensor.cuh"
 
-#ifndef HKV_TENSOR3
-#define HKV_TENSOR3 1
-#endif
-#ifndef HKV_GT
-#define HKV_GT 1
-#endif
-#ifndef HKV_TENSOR2
-#define HKV_TENSOR2 1
-#endif
-#ifndef HKV_TENSOR
-#define HKV_TENSOR 1
-#endif
-
 namespace hkv {
 
-template <class T, int kRank, int kTile, bool kBack>
-cudaError_t launch_chain(Chain<T> a, cudaStream_t st) {
+// Long requests: tiles of 64 rows, the two products one after the other.
+template <class T, int kRank, bool kBack>
+cudaError_t launch_long(Chain<T> a, cudaStream_t st) {
+  constexpr int kTile = 64;
   using F = FirstShape<T, kRank, kTile, kBack>;
   using S = SecondShape<T, kRank, kTile, kBack>;
   const uint64_t slots = slots_of(a.q.tokens, a.q.requests, kTile);
   const uint64_t tiles = a.q.tokens / kTile + (a.q.requests < a.q.tokens ? a.q.requests : a.q.tokens) + 1;
-  a.parts = 1;
-  a.follows = a.q.requests > 0 && a.q.adapters > 0;
-  bool by_tensor = false;
-  int bytes = F::kBytes;
-  tensor::Maps maps{};
-  if constexpr (sizeof(T) == 2) {
-    by_tensor = HKV_TENSOR && a.follows && tensor::make_maps<T, kRank, kBack>(&maps, a);
-    if (by_tensor) bytes = tensor::Shape<kRank>::kBytes;
-  }
-  // all blocks at once on the SMs, each with four stages of 128 columns at least
-  const uint64_t room = sm_count() * (HKV_PM * 227ull * 1024 / (bytes + 1024)) / 100;
-  while (a.parts < kAdapterParts && a.in >= 512ull * a.parts && 2 * tiles * a.parts <= room) a.parts *= 2;
-  a.part_in = ((a.in + a.parts - 1) / a.parts + 63) / 64 * 64;
-  if (a.follows) {  // (else all rows are base's)
-    cudaError_t e = cudaSuccess;
+  a.follows = a.q.requests > 0 && a.q.adapters > 0;  // else all rows are base's
+  if (a.follows) {
+    bool by_tensor = false;
+    int bytes = F::kBytes;
+    tensor::Maps maps{};
     if constexpr (sizeof(T) == 2) {
-      if (by_tensor)
-        e = launch_clusters<tensor::first_tensor_kernel<T, kRank, kBack>>(slots * a.parts, a.parts, tensor::Shape<kRank>::kThreads,
-                                                                          bytes, st, maps, a);
+      by_tensor = tensor::make_maps<T, kRank, kBack>(&maps, a);
+      if (by_tensor) bytes = tensor::Shape<kRank>::kBytes;
     }
-    if (!by_tensor) e = launch_clusters<first_kernel<T, kRank, kTile, kBack>>(slots * a.parts, a.parts, kAdapterThreads, F::kBytes, st, a);
+    // Clusters share a tile's columns, 512 to a block at least, while all blocks are on
+    // the SMs at once (estimated by shared memory, and from the tiles that the requests
+    // can have).  Half and twice as many blocks: 8224 rows by rank 64 with the second
+    // product 66 and 65 us against 61, 8200 rows by rank 32 73 and 74 against 70.
+    const uint64_t room = sm_count() * (227ull * 1024 / (bytes + 1024));
+    a.parts = 1;
+    while (a.parts < kAdapterParts && a.in >= 512ull * a.parts && 2 * tiles * a.parts <= room) a.parts *= 2;
+    a.part_in = ((a.in + a.parts - 1) / a.parts + 63) / 64 * 64;
+    cudaError_t e = cudaSuccess;
+    if (!by_tensor)
+      e = launch_clusters<first_kernel<T, kRank, kTile, kBack>>(slots * a.parts, a.parts, kAdapterThreads, bytes, st, a);
+    else if constexpr (sizeof(T) == 2)
+      e = launch_clusters<tensor::first_tensor_kernel<T, kRank, kBack>>(slots * a.parts, a.parts,
+                                                                        tensor::Shape<kRank>::kThreads, bytes, st, maps, a);
     if (e != cudaSuccess) return e;
   }
-  // blocks for every SM several times over, of up to eight stages
-  uint64_t steps = (a.out + S::kCols - 1) / S::kCols, each = (tiles * steps + HKV_GM * 1ull * sm_count() - 1) / (HKV_GM * 1ull * sm_count());
-  if (each > HKV_EM) each = HKV_EM;
+  // Eight blocks for every SM, of up to 16 stages of columns.  Four and twelve: 8224 rows
+  // by rank 64 59 and 62 us against 56, 8200 rows by rank 32 (stages of the time before) 90
+  // and 73 against 74.
+  const uint64_t steps = (a.out + S::kCols - 1) / S::kCols, blocks = 8ull * sm_count();
+  const uint64_t each = (tiles * steps + blocks - 1) / blocks > 16 ? 16 : (tiles * steps + blocks - 1) / blocks;
   a.groups = static_cast<uint32_t>((steps + each - 1) / each);
   a.group_out = each * S::kCols;
   if constexpr (std::is_same_v<T, __nv_bfloat16>) {
     tensor::SecondMaps maps{};
-    if (HKV_TENSOR2 && a.follows && tensor::make_maps<kRank, kBack>(&maps, a))
+    if (a.follows && tensor::make_maps<kRank, kBack>(&maps, a))
       return launch_clusters<tensor::second_tensor_kernel<kRank, kBack>>(
           slots * a.groups, 1, tensor::SecondShape<kRank>::kThreads, tensor::SecondShape<kRank>::kBytes, st, maps, a);
   }
   return launch_clusters<second_kernel<T, kRank, kTile, kBack>>(slots * a.groups, 1, kAdapterThreads, S::kBytes, st, a);
 }
 
-// Few rows: one kernel, clusters of as many blocks as fill the SMs, and several
-// clusters to a tile where its columns of y are many.
+// Few rows to a request: one kernel, clusters while there are no more than two blocks for
+// an SM (256 rows of 4096 by rank 16: 18 us; four 25, eight 35), and several clusters to a
+// tile where its columns of y are many.
 template <auto kKernel, class T>
 cudaError_t launch_few(Chain<T> a, uint64_t slots, uint64_t tiles, uint64_t cols, int smem, cudaStream_t st) {
-  const uint64_t room = HKV_ROOM * sm_count();
+  const uint64_t room = 2ull * sm_count();
   a.parts = 1;
-  while (a.parts < kAdapterParts && 2 * tiles * a.parts <= room && (a.in >= 256ull * a.parts || a.out > cols * a.parts)) a.parts *= 2;
+  while (a.parts < kAdapterParts && 2 * tiles * a.parts <= room && (a.in >= 256ull * a.parts || a.out > cols * a.parts))
+    a.parts *= 2;
   a.part_in = ((a.in + a.parts - 1) / a.parts + 63) / 64 * 64;
   const uint64_t most = (a.out + cols * a.parts - 1) / (cols * a.parts);
   uint64_t groups = (room + tiles * a.parts - 1) / (tiles * a.parts);
@@ -82,17 +87,25 @@ cudaError_t launch_few(Chain<T> a, uint64_t slots, uint64_t tiles, uint64_t cols
 template <class T, int kRank, bool kBack>
 cudaError_t chain_of(const Chain<T>& a, cudaStream_t st) {
   const uint64_t tokens = a.q.tokens, requests = a.q.requests;
+  // Single tokens, whose factors are read once: 256 of 4096 by rank 16 take 18 us, in
+  // tiles of 16 rows 38.
   if constexpr (!kBack)
     if (tokens <= requests && a.x_whole && a.first.whole && a.second.whole && a.in % 8 == 0 && a.rank % 8 == 0)
-      return launch_few<thin_kernel<T, kRank>>(a, slots_of(tokens, requests, 1), tokens, thin_columns<T, kRank>() * kAdapterThreads, 0, st);
-  if (tokens < 32 * requests)
-    return launch_few<short_kernel<T, kRank, kBack>>(a, slots_of(tokens, requests, 16), tokens / 16 + (requests < tokens ? requests : tokens) + 1,
-                                                     SecondShape<T, kRank, 16, kBack>::kCols, ShortShape<T, kRank, kBack>::kBytes, st);
-  return launch_chain<T, kRank, 64, kBack>(a, st);
+      return launch_few<thin_kernel<T, kRank>>(a, slots_of(tokens, requests, 1), tokens,
+                                               thin_columns<T, kRank>() * kAdapterThreads, 0, st);
+  // Few rows: with tiles of 16 and of 64 rows, bfloat16, 2048 to 2048 by rank 16, forward:
+  // 341 requests of 12 30.0 and 33.9 us, 256 of 16 29.7 and 32.3, 204 of 20 29.2 and 28.0, 128
+  // of 32 29.4 and 27.2; 170 of 12, 1024 to 1024 by rank 64, 27.0 and 22.1.
+  if (tokens < 20 * requests)
+    return launch_few<short_kernel<T, kRank, kBack>>(
+        a, slots_of(tokens, requests, 16), tokens / 16 + (requests < tokens ? requests : tokens) + 1,
+        SecondShape<T, kRank, 16, kBack>::kCols, ShortShape<T, kRank, kBack>::kBytes, st);
+  return launch_long<T, kRank, kBack>(a, st);
 }
 template <class T, bool kBack>
 cudaError_t chain(const Chain<T>& a, cudaStream_t st) {
-  return a.rank <= 16 ? chain_of<T, 16, kBack>(a, st) : a.rank <= 32 ? chain_of<T, 32, kBack>(a, st) : chain_of<T, 64, kBack>(a, st);
+  return a.rank <= 16 ? chain_of<T, 16, kBack>(a, st)
+         : a.rank <= 32 ? chain_of<T, 32, kBack>(a, st) : chain_of<T, 64, kBack>(a, st);
 }
 
 template <class T, int kRank>
@@ -102,13 +115,14 @@ cudaError_t launch_grads(Grads<T> a, cudaStream_t st) {
   a.blocks[1] = a.out[1] ? (a.cols[1] + S::kCols - 1) / S::kCols : 0;
   const uint64_t blocks = a.q.adapters * (a.blocks[0] + a.blocks[1]);
   if (!blocks) return cudaSuccess;
+  // Clusters share an adapter's rows, two tiles to a block at least, up to two blocks for
+  // an SM (8224 rows, 4 adapters of rank 64 and 4096 to 4096: 36 us; one 48, four 49).
   a.parts = 1;
-  while (a.parts < kAdapterParts && blocks * a.parts < HKV_GP * 1ull * sm_count() &&
-         a.q.tokens >= 2ull * a.parts * S::kRows)
-    a.parts *= 2;  // (kRank is a multiple of it)
+  while (a.parts < kAdapterParts && blocks * a.parts < 2ull * sm_count() && a.q.tokens >= 128ull * a.parts) a.parts *= 2;
+  // (TMA takes rows that follow one another: requests of 32 rows and more)
   if constexpr (std::is_same_v<T, __nv_bfloat16>) {
     tensor::GradMaps maps{};
-    if (HKV_TENSOR3 && a.q.requests && a.q.tokens >= HKV_GT * a.q.requests && tensor::make_maps<kRank>(&maps, a)) {
+    if (a.q.tokens >= 32 * a.q.requests && a.q.requests && tensor::make_maps<kRank>(&maps, a)) {
       if (a.parts > kRank / 4) a.parts = kRank / 4;  // four ranks to a part at least
       return launch_clusters<tensor::grads_tensor_kernel<kRank>>(blocks * a.parts, a.parts, tensor::GradShape<kRank>::kThreads,
                                                                  tensor::GradShape<kRank>::kBytes, st, maps, a);
