@@ -22,7 +22,8 @@ def hkv():
     from hash_table_cache_gb300 import _build
     _build.build()
     m.load()
-    return m
+    yield m
+    assert m.hkv_get_wait_timeouts() == (0, 0)
 
 
 def _gen(seed):
@@ -183,6 +184,26 @@ def test_what_is_not_of_a_request_has_no_effect(hkv, dtype, lengths):
     assert torch.equal(f.out[ends[0] + 1:], got["out"][ends[0] + 1:])
     dx, ddown, _ = hkv.adapter_matmul_backward(f, c.dy, base=c.dx_base)
     assert torch.equal(dx, got["dx"]) and ddown[0].isnan().all() and torch.equal(ddown[2], got["ddown"][2])
+
+
+@pytest.mark.parametrize("dtype", [BF16, F16])
+@pytest.mark.parametrize("rank", [5, 16, 32, 48, 64])
+@pytest.mark.parametrize("k,n", [(64, 128), (72, 200), (520, 1000), (1032, 136)])
+def test_long_requests(hkv, dtype, rank, k, n):
+    """Tiles that end in every part of their 64 rows, columns and ranks that end inside a
+    box of the loads."""
+    Case(dtype, k, n, rank, [64, 1, 63, 65, 0, 127, 128, 200], [0, 1, 2, 0, 1, -1, 2, 0], before=5, behind=70,
+         seed=rank).check(hkv)
+
+
+@pytest.mark.parametrize("lengths", [[300, 40], [70] * 6])
+def test_one_adapter_for_all(hkv, lengths):
+    """One adapter seen as several, a step of 0 between them; every request's gradient
+    is its own all the same."""
+    which = list(range(len(lengths)))
+    c = Case(BF16, 256, 320, 16, lengths, which, count=len(lengths))
+    c.down, c.up = (t[:1].expand(t.shape) for t in (c.down, c.up))
+    c.check(hkv)
 
 
 def test_numbers_at_the_ends_of_the_range(hkv):
