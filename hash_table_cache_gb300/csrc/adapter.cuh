@@ -47,7 +47,7 @@ struct Planes {
 // Blocks of an SM that shared memory has room for, so that registers do not fall
 // short of them.
 template <class T, int kRank>
-__host__ __device__ constexpr int blocks_of() { return sizeof(T) == 4 ? 2 : kRank == 64 ? 3 : 4; }
+__host__ __device__ constexpr int blocks_of() { return sizeof(T) == 4 ? (kRank == 16 ? 3 : 2) : kRank == 64 ? 3 : 4; }
 
 // What the requests are, as the kernels take it.  (Read past L1: the second
 // product's kernel reads before it has waited.)
