@@ -116,27 +116,47 @@ inline uint64_t slots_of(uint64_t tokens, uint64_t requests, int tile) {
 // tiles
 // ---------------------------------------------------------------------------
 // Eight neighbouring elements into shared memory, the first n of them and zeros
-// behind: asynchronous where 16 bytes lie on a boundary (`whole`).
+// behind: asynchronous, from a boundary of 16 bytes on.
 __device__ __forceinline__ void copy_16(uint32_t to, const void* from, int bytes) {
   asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(to), "l"(from), "r"(bytes) : "memory");
 }
 template <class T>
-__device__ __forceinline__ void copy_eight(T* to, const T* from, int n, bool whole) {
+__device__ __forceinline__ void copy_eight(T* to, const T* from, int n) {
   constexpr int kVecs = sizeof(T) / 2, kPer = 16 / sizeof(T);
-  if (whole) {
 #pragma unroll
-    for (int i = 0; i < kVecs; ++i)
-      copy_16(smem_u32(to + i * kPer), from + i * kPer,
-              (kVecs == 1 ? n : min(max(n - i * kPer, 0), kPer)) * static_cast<int>(sizeof(T)));
-  } else {
-    uint4 v[kVecs];
-    T* e = reinterpret_cast<T*>(v);
-#pragma unroll
-    for (int i = 0; i < 8; ++i) e[i] = i < n ? __ldcg(from + i) : from_f32<T>(0.f);
-#pragma unroll
-    for (int i = 0; i < kVecs; ++i) reinterpret_cast<uint4*>(to)[i] = v[i];
-  }
+  for (int i = 0; i < kVecs; ++i)
+    copy_16(smem_u32(to + i * kPer), from + i * kPer,
+            (kVecs == 1 ? n : min(max(n - i * kPer, 0), kPer)) * static_cast<int>(sizeof(T)));
 }
+// The same from anywhere: the 16-byte pieces that hold any of them, shifted.
+template <class T>
+struct Shifted {
+  static constexpr int kVecs = sizeof(T) / 2;
+  uint4 piece[kVecs + 1];
+  __device__ __forceinline__ void load(const T* from, int n) {
+    const uint32_t off = reinterpret_cast<uintptr_t>(from) & 15;
+    const uint4* const at = reinterpret_cast<const uint4*>(reinterpret_cast<uintptr_t>(from) - off);
+    const uint32_t end = off + n * static_cast<uint32_t>(sizeof(T));
+#pragma unroll
+    for (uint32_t i = 0; i <= kVecs; ++i) piece[i] = n > 0 && 16 * i < end ? __ldcg(at + i) : make_uint4(0, 0, 0, 0);
+  }
+  __device__ __forceinline__ void store(T* to, const T* from, int n) {
+    uint32_t x[4 * kVecs + 4];
+#pragma unroll
+    for (int i = 0; i <= kVecs; ++i) *reinterpret_cast<uint4*>(x + 4 * i) = piece[i];
+    shift_bytes(x, reinterpret_cast<uintptr_t>(from) & 15);
+    if (n < 8) {
+#pragma unroll
+      for (int i = 0; i < 8; ++i)
+        if (i >= n) {
+          if constexpr (sizeof(T) == 4) x[i] = 0;
+          else x[i / 2] &= i % 2 ? 0x0000FFFFu : 0xFFFF0000u;
+        }
+    }
+#pragma unroll
+    for (int i = 0; i < kVecs; ++i) reinterpret_cast<uint4*>(to)[i] = *reinterpret_cast<uint4*>(x + 4 * i);
+  }
+};
 __device__ __forceinline__ void copies_end() { asm volatile("cp.async.commit_group;" ::: "memory"); }
 template <int kLeft>
 __device__ __forceinline__ void copies_wait() {
@@ -145,14 +165,34 @@ __device__ __forceinline__ void copies_wait() {
 
 // kRows x kCols elements into a tile of that pitch by all threads: row r of the
 // matrix is at data + r * stride, `rows` rows and `cols` columns of it are there.
+// Rows that start anywhere (not `whole`) are read at once and shifted.
+template <class T, int kRows, int kCols, int kPitch>
+__device__ __noinline__ void copy_tile_shifted(T* tile, const T* data, uint64_t stride, int64_t rows, int64_t cols) {
+  constexpr int kLanes = kCols / 8, kPass = kAdapterThreads / kLanes, kPasses = (kRows + kPass - 1) / kPass;
+  const int row = threadIdx.x / kLanes, col = threadIdx.x % kLanes * 8;
+  if (kRows < kPass && row >= kRows) return;
+  const int there = static_cast<int>(min(rows, static_cast<int64_t>(kRows))) - row;
+  const int n = static_cast<int>(max(min(cols - col, static_cast<int64_t>(8)), static_cast<int64_t>(0)));
+  const T* const from = data + row * stride + col;
+  Shifted<T> v[kPasses];
+#pragma unroll
+  for (int i = 0; i < kPasses; ++i) v[i].load(from + i * kPass * stride, i * kPass < there ? n : 0);
+#pragma unroll
+  for (int i = 0; i < kPasses; ++i)
+    v[i].store(tile + (row + i * kPass) * kPitch + col, from + i * kPass * stride, i * kPass < there ? n : 0);
+}
 template <class T, int kRows, int kCols, int kPitch>
 __device__ __forceinline__ void copy_tile(T* tile, const T* data, uint64_t stride, int64_t rows, int64_t cols,
                                           bool whole) {
   constexpr int kLanes = kCols / 8, kPass = kAdapterThreads / kLanes;  // threads to a row, rows at a time
   static_assert(kAdapterThreads % kLanes == 0 && (kRows % kPass == 0 || kRows < kPass));
+  if (!whole) {
+    copy_tile_shifted<T, kRows, kCols, kPitch>(tile, data, stride, rows, cols);
+    return;
+  }
   const int row = threadIdx.x / kLanes, col = threadIdx.x % kLanes * 8;
   if (kRows < kPass && row >= kRows) return;
-  if (whole && rows >= kRows && cols >= kCols) {
+  if (rows >= kRows && cols >= kCols) {
     const T* p = data + row * stride + col;
     uint32_t at = smem_u32(tile + row * kPitch + col);
 #pragma unroll
@@ -169,7 +209,7 @@ __device__ __forceinline__ void copy_tile(T* tile, const T* data, uint64_t strid
 #pragma unroll
   for (int i = 0; i < (kRows + kPass - 1) / kPass; ++i) {
     const bool has = i * kPass < there && n > 0;
-    copy_eight(to + i * kPass * kPitch, has ? from + i * kPass * stride : data, has ? n : 0, whole);
+    copy_eight(to + i * kPass * kPitch, has ? from + i * kPass * stride : data, has ? n : 0);
   }
 }
 
@@ -579,6 +619,19 @@ __device__ __forceinline__ void second_step(T* stage, const uint32_t (&h)[kRank 
     }
     __syncwarp();
   }
+  if (!whole) {  // rows of y that start anywhere: neighbouring elements by neighbouring lanes
+    const uint64_t first = c0 + other * S::kWarpCols;
+    const int cols = static_cast<int>(min(static_cast<int64_t>(col1 - first), static_cast<int64_t>(S::kWarpCols)));
+    for (int r = 0; r < 16 && row_warp * 16 + r < rows; ++r) {
+      const int row = row_warp * 16 + r;
+      const T* const from = stage + row * S::kPitch + other * S::kWarpCols;
+      T* const out = y + row * stride + first;
+#pragma unroll
+      for (int c = lane; c < S::kWarpCols; c += 32)
+        if (c < cols) out[c] = from[c];
+    }
+    return;
+  }
   // a warp's rows of kWarpCols columns, eight to a lane
   constexpr int kLanes = S::kWarpCols / 8;
   const uint64_t col = c0 + other * S::kWarpCols + lane % kLanes * 8;
@@ -589,7 +642,7 @@ __device__ __forceinline__ void second_step(T* stage, const uint32_t (&h)[kRank 
     const int64_t n = col1 - col;
     const T* const from = stage + row * S::kPitch + other * S::kWarpCols + lane % kLanes * 8;
     T* const out = y + row * stride + col;
-    if (n >= 8 && whole) {
+    if (n >= 8) {
 #pragma unroll
       for (int i = 0; i < static_cast<int>(sizeof(T)) / 2; ++i)
         st_stream_v4(out + i * (16 / sizeof(T)), reinterpret_cast<const uint4*>(from)[i]);
@@ -1005,11 +1058,26 @@ __global__ void __launch_bounds__(kAdapterThreads, GradShape<T, kRank>::kBlocks)
     constexpr int kLanes = S::kCols / 8, kPass = kThreads / kLanes;
     const int first = tid / kLanes, col = tid % kLanes * 8;
     const int n = static_cast<int>(max(min(static_cast<int64_t>(cols - col0) - col, static_cast<int64_t>(8)), static_cast<int64_t>(0)));
+    T* const tile = reinterpret_cast<T*>(b) + first * S::kPitch + col;
+    constexpr int kPasses = S::kRows / kPass;
+    if (whole) {
 #pragma unroll
-    for (int i = 0; i < S::kRows / kPass; ++i) {
-      const int row = first + i * kPass;
-      const bool has = row < rows && n > 0;
-      copy_eight(reinterpret_cast<T*>(b) + row * S::kPitch + col, has ? m + row_of[stage][row] * stride + col : m, has ? n : 0, whole);
+      for (int i = 0; i < kPasses; ++i) {
+        const int row = first + i * kPass;
+        const bool has = row < rows && n > 0;
+        copy_eight(tile + i * kPass * S::kPitch, has ? m + row_of[stage][row] * stride + col : m, has ? n : 0);
+      }
+    } else {
+      Shifted<T> v[kPasses];
+      const T* at[kPasses];
+#pragma unroll
+      for (int i = 0; i < kPasses; ++i) {
+        const int row = first + i * kPass;
+        at[i] = row < rows ? m + row_of[stage][row] * stride + col : m;
+        v[i].load(at[i], row < rows ? n : 0);
+      }
+#pragma unroll
+      for (int i = 0; i < kPasses; ++i) v[i].store(tile + i * kPass * S::kPitch, at[i], first + i * kPass < rows ? n : 0);
     }
     __nv_bfloat16* const planes = reinterpret_cast<__nv_bfloat16*>(b + S::kM);
     constexpr int kChunks = P::kP * S::kRows * kRank / 8;

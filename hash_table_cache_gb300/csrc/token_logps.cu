@@ -554,8 +554,9 @@ __device__ __forceinline__ void put_both(__half* e, float a, float b) {
 
 // A piece of a row for every kLanes threads, rows from the last to the first, so
 // that what the forward call read last is taken from L2 while it is there.
-template <class T, int kLanes>
-__global__ void __launch_bounds__(kLanes == 32 ? kWarpThreads : kThreads, kLanes == 32 ? 7 : 7)
+// kAlike: every row of the gradient lies as the logits' does within 16 bytes.
+template <class T, int kLanes, bool kAlike>
+__global__ void __launch_bounds__(kLanes == 32 ? kWarpThreads : kThreads, kAlike ? 7 : 5)
     backward_kernel(uint64_t rows, uint64_t vocab, const T* logits, uint64_t stride, uint64_t pieces,
                     const int64_t* __restrict__ labels, const float* __restrict__ lse,
                     const float* __restrict__ entropy, const float* __restrict__ dlogps,
@@ -597,30 +598,15 @@ __global__ void __launch_bounds__(kLanes == 32 ? kWarpThreads : kThreads, kLanes
     const uint64_t slope2 = both(slope1, slope1), level2 = both(level1, level1);
     auto one = [&](uint64_t at) { d[at] = from_f32<T>(counted ? value(to_f32(x[at]), at) : 0.f); };
     const uint32_t head = to_boundary(d, n);
-    const bool alike = to_boundary(x, n) == head;
-    if (counted && !alike) {  // the two lie differently: one by one
-      for (uint64_t k = lane; k < n; k += kLanes) one(k);
-      continue;
-    }
     const uint32_t chunks = static_cast<uint32_t>((n - head) / kN);
-    uint4 w[kUnroll];
-#pragma unroll
-    for (int u = 0; u < kUnroll; ++u) {
-      const uint32_t k = lane + u * kLanes;
-      if (counted && k < chunks) w[u] = __ldcs(reinterpret_cast<const uint4*>(x + head + k * kN));
-    }
-    if (lane < head) one(lane);
-#pragma unroll
-    for (int u = 0; u < kUnroll; ++u) {
-      const uint32_t k = lane + u * kLanes;
-      if (k >= chunks) break;
+    auto emit = [&](uint32_t k, uint4 w) {  // chunk k of the gradient from the logits there
       Chunk<T> o;
       T* e = reinterpret_cast<T*>(&o.w);
       if (!counted) {
         o.w = make_uint4(0, 0, 0, 0);
       } else {
         Chunk<T> in;
-        in.w = w[u];
+        in.w = w;
         if (!factored || hit - (head + k * kN) < kN) {
 #pragma unroll
           for (int i = 0; i < kN; ++i) e[i] = from_f32<T>(value(in.at(i), head + k * kN + i));
@@ -636,6 +622,33 @@ __global__ void __launch_bounds__(kLanes == 32 ? kWarpThreads : kThreads, kLanes
         }
       }
       st_stream_v4(d + head + k * kN, o.w);
+    };
+    if (lane < head) one(lane);
+    if (!kAlike && counted) {
+      // the two may lie differently: the logits from the pieces of 16 bytes around them,
+      // which the next thread reads as well
+      const uint32_t off = static_cast<uint32_t>(reinterpret_cast<uintptr_t>(x + head) & 15);
+      const uint4* const from = reinterpret_cast<const uint4*>(reinterpret_cast<uintptr_t>(x + head) - off);
+#pragma unroll 1
+      for (uint32_t k = lane; k < chunks; k += kLanes) {
+        const uint4 lo = from[k], hi = off ? from[k + 1] : lo;
+        uint32_t v[8] = {lo.x, lo.y, lo.z, lo.w, hi.x, hi.y, hi.z, hi.w};
+        shift_bytes(v, off);
+        emit(k, make_uint4(v[0], v[1], v[2], v[3]));
+      }
+    } else {
+      uint4 w[kUnroll];
+#pragma unroll
+      for (int u = 0; u < kUnroll; ++u) {
+        const uint32_t k = lane + u * kLanes;
+        if (counted && k < chunks) w[u] = __ldcs(reinterpret_cast<const uint4*>(x + head + k * kN));
+      }
+#pragma unroll
+      for (int u = 0; u < kUnroll; ++u) {
+        const uint32_t k = lane + u * kLanes;
+        if (k >= chunks) break;
+        emit(k, w[u]);
+      }
     }
     const uint64_t tail = head + static_cast<uint64_t>(chunks) * kN + lane;
     if (tail < n) one(tail);
@@ -729,7 +742,10 @@ hkv_status hkv_token_logps_backward(uint64_t rows, uint64_t vocab, const void* l
     const uint64_t pieces = (vocab + piece - 1) / piece;
     const int threads = warps ? kWarpThreads : kThreads;
     const uint64_t blocks = (rows * pieces * lanes + threads - 1) / threads;
-    return launch_chained(warps ? backward_kernel<T, 32> : backward_kernel<T, kThreads>,
+    const bool alike = (reinterpret_cast<uintptr_t>(dlogits) - reinterpret_cast<uintptr_t>(logits)) % 16 == 0 &&
+                       (dstride - stride) * sizeof(T) % 16 == 0;
+    return launch_chained(alike ? warps ? backward_kernel<T, 32, true> : backward_kernel<T, kThreads, true>
+                                : warps ? backward_kernel<T, 32, false> : backward_kernel<T, kThreads, false>,
                           static_cast<unsigned>(blocks < 0x7FFFFFFF ? blocks : 0x7FFFFFFF), threads,
                           0, st, rows, vocab, static_cast<const T*>(logits), stride, pieces, labels,
                           lse, entropy, dlogps, dentropy, static_cast<T*>(dlogits), dstride);
