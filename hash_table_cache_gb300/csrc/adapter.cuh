@@ -6,23 +6,33 @@
 // scale c:
 //   h = c D x,  y = base + U h            dh = c U^T dy,  dx = base + D^T dh
 //   dD = sum_t dh_t x_t^T                 dU = sum_t dy_t h_t^T
-// Three kernels: the first product (x or dy with the first factor, its columns
-// shared by a cluster's blocks, whose sums meet in distributed shared memory in a
-// fixed order), the second product (onto base; it starts while the first one ends
-// and has its factor and base on their way by then), and the adapters' gradients.
+// Long requests take two kernels: the first product (x or dy with the first factor,
+// its columns shared by a cluster's blocks, whose sums meet in distributed shared
+// memory in a fixed order) and the second (onto base; it starts while the first one
+// ends and has its factor and base on their way by then).  Short requests and single
+// tokens, whose time is that of a launch and of a few latencies, take both in one
+// kernel.  A third has the adapters' gradients.
 //
 // The products are thin: 2 rank operations for each element that is read or
 // written, 16 to 64 where the tensor cores could take 280 and more, so memory is
-// the bound, and mma.sync, which takes ragged tiles, either order of either factor
-// and sums in registers, is enough.  It multiplies bfloat16 (float16 in the first
-// product of float16 matrices); what has more digits is split into two or three
-// bfloat16 numbers (planes), whose products are added in float32:
+// the bound.  16-bit matrices whose rows start on 16-byte boundaries go through
+// tcgen05 (adapter_tensor.cuh); here is what takes ragged rows, short requests,
+// float16 where it meets h, and float32: mma.sync, whose operands may be split in
+// registers.  It multiplies bfloat16 (float16 in the first product of float16
+// matrices); what has more digits is split into two or three bfloat16 numbers
+// (planes), whose products are added in float32:
 //   float32 = three planes exactly, products of planes i + j <= 2 (what is left
 //   out is below 2^-22 of a term); float16 = two planes exactly; h and dh, sums in
 //   float32, in two planes where matrices have 16 bits (below 2^-16 of it is left
 //   out, where a result is rounded to 2^-8 or 2^-11), in three where they have 32.
-// Tiles come by asynchronous copies as they lie in memory, and are split on the
-// way to the tensor core.
+// Tiles come by asynchronous copies as they lie in memory (rows that start anywhere
+// by the 16-byte pieces around them, shifted), and are split on the way to the tensor
+// core.  Times: adapter_launch.cuh.  What they were with fewer of these: both products
+// of long requests in one kernel of register-staged tiles 205 us where the two take 67
+// (8200 rows, 4096 to 8192, rank 32) and 124 where they take 56 (8224 rows, 4096 to 4096,
+// rank 64); single tokens in tiles of 16 rows 38 us, two kernels for them 20, one 18;
+// gradients by request 57 us, across requests 31 (4096 rows in requests of 8, 2048 to
+// 2048, rank 16); ragged x element by element 218 us, shifted 118.
 #pragma once
 
 #include <atomic>

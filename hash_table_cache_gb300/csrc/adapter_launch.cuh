@@ -8,7 +8,10 @@
 //   1637 rows of 16 requests, 64 to 131072, rank 8               132 us, 6.5 TB/s
 //   8224 rows of 32 requests, 4096 to 4096, rank 64               56 us, 3.6 TB/s
 //     and its backward pass                                       93 us: dx 56, gradients 36
-//   4000 rows of 333 requests, 128 to 128, rank 8, float32        10 and 21 us
+//   8224 rows as above, float16                                  88 and 208 us (mma.sync but
+//     for the forward call's and the backward call's first product)
+//   and float32                                                 227 and 443 us (six products)
+//   3919 rows of 333 requests, 128 to 128, rank 8, float32        10 and 23 us
 #pragma once
 
 #include "adapter_tensor.cuh"
@@ -35,8 +38,9 @@ cudaError_t launch_long(Chain<T> a, cudaStream_t st) {
     // Clusters share a tile's columns, 512 to a block at least, while all blocks are on
     // the SMs at once (estimated by shared memory, and from the tiles that the requests
     // can have).  Half and twice as many blocks: 8224 rows by rank 64 with the second
-    // product 66 and 65 us against 61, 8200 rows by rank 32 73 and 74 against 70.
-    const uint64_t room = sm_count() * (227ull * 1024 / (bytes + 1024));
+    // product 66 and 65 us against 61, 8200 rows by rank 32 73 and 74 against 70.  Float32,
+    // whose products are most of the time, twice as many: by rank 64 227 us against 340.
+    const uint64_t room = (sizeof(T) == 4 ? 2 : 1) * sm_count() * (227ull * 1024 / (bytes + 1024));
     a.parts = 1;
     while (a.parts < kAdapterParts && a.in >= 512ull * a.parts && 2 * tiles * a.parts <= room) a.parts *= 2;
     a.part_in = ((a.in + a.parts - 1) / a.parts + 63) / 64 * 64;
@@ -49,8 +53,7 @@ cudaError_t launch_long(Chain<T> a, cudaStream_t st) {
     if (e != cudaSuccess) return e;
   }
   // Eight blocks for every SM, of up to 16 stages of columns.  Four and twelve: 8224 rows
-  // by rank 64 59 and 62 us against 56, 8200 rows by rank 32 (stages of the time before) 90
-  // and 73 against 74.
+  // by rank 64 59 and 62 us against 56.
   const uint64_t steps = (a.out + S::kCols - 1) / S::kCols, blocks = 8ull * sm_count();
   const uint64_t each = (tiles * steps + blocks - 1) / blocks > 16 ? 16 : (tiles * steps + blocks - 1) / blocks;
   a.groups = static_cast<uint32_t>((steps + each - 1) / each);

@@ -1,16 +1,19 @@
-// adapter_tensor.cuh -- the first product of long requests with 16-bit matrices, on
-// the tensor cores of tcgen05 with loads by TMA (the rest is in adapter.cuh).
+// adapter_tensor.cuh -- the adapters' products of long requests with 16-bit matrices,
+// on the tensor cores of tcgen05 with loads by TMA (the rest is in adapter.cuh).
 //
-// A block has 64 rows of one request and a part of their columns: one thread brings
-// stages of 64 columns of x and of the adapter's first factor, one multiplies them
-// into kRank columns of TMEM, and two warps read the sums out, which the blocks of a
-// cluster join as in adapter.cuh.  The product is 128 rows high, the lowest that
-// gives a row to a lane; what the 64 lanes below the tile's rows are multiplied with
-// is whatever lies behind x in shared memory, and they are not read.
+// The first product: a block has 64 rows of one request and a part of their columns;
+// one thread brings stages of 64 columns of x and of the adapter's first factor, one
+// multiplies them into kRank columns of TMEM, and two warps read the sums out, which
+// the blocks of a cluster join as in adapter.cuh.  The product is 128 rows high, the
+// lowest that gives a row to a lane; what the 64 lanes below the tile's rows are
+// multiplied with is whatever lies behind x in shared memory, and they are not read.
 //
-// The loads are the bound (x from memory, the factor from L2), and this way they
-// cost no instructions of the warps: with asynchronous copies and mma.sync 8224 rows
-// of 4096 by rank 64 took 35 us.
+// The loads are the bound (x from memory, the factor from L2), and this way they cost
+// no instructions of the warps.  Kernels alone, cold, 8224 rows of 4096 to 4096 by rank
+// 64 bfloat16, here and with asynchronous copies and mma.sync: first product 19 us (3.5
+// TB/s of x; 35), second 38 us (3.5 TB/s of base and y; 42), gradients 38 us (3.5 TB/s of x
+// and dy; 73).  Half of a first product's time is its start and end: a block's search,
+// its first loads, and the joining of the sums.
 #pragma once
 
 #include <cuda.h>
@@ -255,7 +258,12 @@ __global__ void __launch_bounds__(Shape<kRank>::kThreads)
 // and base and y are read and written row by row as they lie.  The two planes of c h (or
 // dh) are multiplied by the same columns of the second factor and added up in TMEM.
 // One thread loads (the factor's columns, base, and the planes once the first product is
-// done), one multiplies, four warps add onto base.
+// done), one multiplies, eight warps add onto base.  What bounds it is those warps'
+// instructions (14 for an element) and how much base is on its way, which shared memory
+// holds: 1637 rows to 131072 columns by rank 8 131 us, 73% of the memory's cycles; 8200
+// rows to 8192 by rank 32 50 us.  Tried: four warps 68 us with the first product against
+// 67; a third stage of rank 32 instead of a third block 77; sums put together in shared
+// memory and stored 16 bytes at a time 75.
 // ---------------------------------------------------------------------------
 struct SecondMaps {  // the second factor; c h or dh: tokens x planes of kRank; base
   CUtensorMap second, hidden, base;
@@ -455,7 +463,8 @@ __global__ void __launch_bounds__(SecondShape<kRank>::kThreads, 3)
 // The adapters' gradients of bfloat16 matrices: 128 columns of x or dy in the lanes, the
 // ranks in the columns of TMEM, rows of the batch along k.  Both lie with their rows
 // apart, which the tensor core takes as it is.  Rows of a tile that are another
-// request's are made zeros in shared memory, of both operands.
+// request's are made zeros in shared memory, of both operands.  Each of the (k + n) / 128
+// blocks of an adapter reads the planes anew, from L2.
 // ---------------------------------------------------------------------------
 struct GradMaps {  // x and dy; dh and c h
   CUtensorMap m[2], p[2];

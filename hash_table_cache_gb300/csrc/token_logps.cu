@@ -18,6 +18,17 @@
 // are read once more for the groups' largest entries by value and index, and rows
 // where that is not enough (entries that repeat with the groups) once for each
 // alternative.
+//
+// Times (GB300, CUDA graph replays): 4096 x 131072 bfloat16, a tenth of the tokens
+// hidden, with 20 alternatives 161 us (6.0 TB/s of what is read, 76% of the memory's
+// cycles); 4096 x 32768 without 43 us (5.6 TB/s), its gradient 75 us (6.8 TB/s with what
+// L2 keeps; both bound by memory); 256 x 50257 10.3 us, with 20 13.8 (a row to a block,
+// 256 of them on 152 SMs), with 32 20.5, with all but 5 entries masked 42, entries that
+// repeat with the groups 369; one row of 131072 with 5 7.4 us; 32768 x 2000 44, 99 with 20
+// and 47; 4096 x 32768 float32 80, 92 with 20 and 153.  A gradient that lies otherwise
+// than its logits within 16 bytes, 4096 x 50257 of 50304 into a contiguous matrix: 196 us
+// for 121.  Before: alternatives by a pass each 6205 us for the first of these; powers with
+// subnormals 215; 64-bit steps and tests in whole rounds 173.
 #include "logits.cuh"
 
 namespace hkv {

@@ -3,7 +3,10 @@
 A training step on a table's rows is ``find`` -> ``mx_quantize`` ->
 ``mx_matmul`` -> ``preference_loss`` and its backward -> ``mx_matmul`` on the
 copies along the other axis -> ``clip_grad_norm`` -> ``assign``; a serving step
-scores hidden states against a 4-bit copy of rows.
+scores hidden states against a 4-bit copy of rows.  With an adapter for each user
+(a row of the table) it is ``find`` -> ``mx_matmul`` -> ``adapter_matmul`` ->
+``token_logps``, and learning goes back through ``token_logps_backward`` and
+``adapter_matmul_backward``.
 
 Every function takes tensors of one CUDA device and raises ``ValueError`` for
 a tensor it cannot take as it is (nothing is copied or cast behind the

@@ -324,8 +324,10 @@ hkv_status hkv_insert_or_assign_noalloc(hkv_table* table, uint64_t n, const uint
  *
  * A training step on a table's rows runs find -> 4-bit copies -> products ->
  * loss and gradient -> norm and clipping -> assign; a serving step scores
- * hidden states against 4-bit copies of rows.  The calls below are the steps
- * between the table's own.  They take no table: they run on the current
+ * hidden states against 4-bit copies of rows.  With an adapter for each user, a
+ * row of the table, the adapters' product goes onto the shared one, and log
+ * probabilities of the answers are taken from their logits.  The calls below are
+ * the steps between the table's own.  They take no table: they run on the current
  * device, which must be the device of `stream`, are asynchronous, allocate
  * nothing, keep nothing between calls and may be captured into a CUDA graph.
  * Argument errors are found on the host and enqueue nothing.  All matrices
