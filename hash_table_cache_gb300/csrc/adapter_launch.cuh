@@ -99,10 +99,13 @@ cudaError_t chain_of(const Chain<T>& a, cudaStream_t st) {
   // Few rows: with tiles of 16 and of 64 rows, bfloat16, 2048 to 2048 by rank 16, forward:
   // 341 requests of 12 30.0 and 33.9 us, 256 of 16 29.7 and 32.3, 204 of 20 29.2 and 28.0, 128
   // of 32 29.4 and 27.2; 170 of 12, 1024 to 1024 by rank 64, 27.0 and 22.1.
-  if (tokens < 20 * requests)
+  if (tokens < 20 * requests) {
+    Chain<T> b = a;
+    b.q.by_rows = requests > tokens;
     return launch_few<short_kernel<T, kRank, kBack>>(
-        a, slots_of(tokens, requests, 16), tokens / 16 + (requests < tokens ? requests : tokens) + 1,
+        b, slots_of(tokens, requests, b.q.by_rows ? 1 : 16), tokens / 16 + (requests < tokens ? requests : tokens) + 1,
         SecondShape<T, kRank, 16, kBack>::kCols, ShortShape<T, kRank, kBack>::kBytes, st);
+  }
   return launch_long<T, kRank, kBack>(a, st);
 }
 template <class T, bool kBack>

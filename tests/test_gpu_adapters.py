@@ -188,7 +188,7 @@ def test_what_is_not_of_a_request_has_no_effect(hkv, dtype, lengths):
 
 @pytest.mark.parametrize("dtype", [BF16, F16])
 @pytest.mark.parametrize("rank", [5, 16, 32, 48, 64])
-@pytest.mark.parametrize("k,n", [(64, 128), (72, 200), (520, 1000), (1032, 136)])
+@pytest.mark.parametrize("k,n", [(8, 16), (16, 8), (24, 40), (64, 128), (72, 200), (520, 1000), (1032, 136)])
 def test_long_requests(hkv, dtype, rank, k, n):
     """Tiles that end in every part of their 64 rows, columns and ranks that end inside a
     box of the loads."""
@@ -204,6 +204,15 @@ def test_one_adapter_for_all(hkv, lengths):
     c = Case(BF16, 256, 320, 16, lengths, which, count=len(lengths))
     c.down, c.up = (t[:1].expand(t.shape) for t in (c.down, c.up))
     c.check(hkv)
+
+
+@pytest.mark.parametrize("dtype", TYPES)
+@pytest.mark.parametrize("rank", [8, 9])
+def test_many_more_requests_than_rows(hkv, dtype, rank):
+    lengths = [0] * 3000
+    for i, v in ((5, 1), (700, 40), (701, 2), (2990, 17)):
+        lengths[i] = v
+    Case(dtype, 64, 72, rank, lengths, [i % 4 - 1 for i in range(3000)], before=3, behind=4).check(hkv)
 
 
 def test_numbers_at_the_ends_of_the_range(hkv):
