@@ -24,7 +24,7 @@
 // cycles); 4096 x 32768 without 43 us (5.6 TB/s), its gradient 75 us (6.8 TB/s with what
 // L2 keeps; both bound by memory); 256 x 50257 10.3 us, with 20 13.8 (a row to a block,
 // 256 of them on 152 SMs), with 32 20.5, with all but 5 entries masked 42, entries that
-// repeat with the groups 369; one row of 131072 with 5 7.4 us; 32768 x 2000 44, 99 with 20
+// repeat with the groups 369; one row of 131072 with 5 7.4 us; 32768 x 2000 35, 75 with 20
 // and 47; 4096 x 32768 float32 80, 92 with 20 and 153.  A gradient that lies otherwise
 // than its logits within 16 bytes, 4096 x 50257 of 50304 into a contiguous matrix: 196 us
 // for 121.  Before: alternatives by a pass each 6205 us for the first of these; powers with
@@ -119,19 +119,19 @@ __device__ __forceinline__ void clamp(Chunk<T>& c) {
 }
 
 // 16-byte loads of a round, in flight together.
-__host__ __device__ constexpr int loads(int lanes) { return lanes == 32 ? 8 : 4; }
+constexpr int kLoads = 4;
 
 // Cells that a thread keeps at most of a row (a cell is one round of loads or, of
 // longer rows, several).
 template <class T, int kLanes>
-constexpr int cells_of() { return kLanes == 32 ? 4 : 256 / loads(kLanes) / static_cast<int>(sizeof(T)); }
+constexpr int cells_of() { return kLanes == 32 ? 4 : 256 / kLoads / static_cast<int>(sizeof(T)); }
 
 // One thread's share of a row of n elements, taken by kLanes threads.  With kTop
 // cells[i * kLanes] gets the maximum of its rounds i * per .. (i + 1) * per - 1.
 template <class T, int kLanes, bool kTop>
 __device__ __forceinline__ Moments row_pass(const T* x, uint64_t n, int lane, T* cells, uint32_t per,
                                             uint32_t count) {
-  constexpr int kN = Chunk<T>::kN, kUnroll = loads(kLanes);
+  constexpr int kN = Chunk<T>::kN, kUnroll = kLoads;
   Moments r;
   const uint32_t head = to_boundary(x, n);
   if (lane < static_cast<int>(head)) r.one(to_f32(x[lane]));
@@ -264,7 +264,7 @@ struct Team {
   }
   // Rounds of loads to a cell, and cells, of n elements from x on.
   static __device__ __forceinline__ void plan(const T* x, uint64_t n, uint32_t& per, uint32_t& count) {
-    constexpr uint64_t kRound = kLanes * loads(kLanes);
+    constexpr uint64_t kRound = kLanes * kLoads;
     const uint64_t chunks = (n - to_boundary(x, n)) / Chunk<T>::kN;
     const uint64_t rounds = (chunks + kRound - 1) / kRound;
     per = 1;
@@ -276,7 +276,7 @@ struct Team {
   // cells written.  All of the team's threads call it.
   __device__ __forceinline__ void pick(const T* x, uint64_t lo, uint64_t hi, float m, uint32_t per,
                                        uint32_t count, uint32_t top, uint32_t lane) {
-    constexpr int kN = Chunk<T>::kN, kUnroll = loads(kLanes);
+    constexpr int kN = Chunk<T>::kN, kUnroll = kLoads;
     most[lane] = m;
     if (lane < HKV_MAX_TOP) list[lane] = 0;
     if (lane == 0) items_found = keys_found = 0;
@@ -438,9 +438,11 @@ __device__ __forceinline__ void no_top(uint64_t t, uint32_t top, uint32_t lane, 
   }
 }
 
-// A warp per row: short rows.
+// A warp per row: short rows.  Ten blocks to an SM: 32768 x 2000 bfloat16 takes 35 us, and
+// 51 with 5 and 75 with 20 alternatives; eight blocks 37, 54 and 83, twelve 34, 56
+// and 80.  With eight loads in flight and as many registers as they want it was 44, 75 and 99.
 template <class T, bool kTop>
-__global__ void __launch_bounds__(kWarpThreads)
+__global__ void __launch_bounds__(kWarpThreads, 10)
     short_rows_kernel(uint64_t rows, uint64_t vocab, const T* __restrict__ logits, uint64_t stride,
                       const int64_t* __restrict__ labels, uint32_t top, Out out) {
   using Warp = Team<T, 32>;
