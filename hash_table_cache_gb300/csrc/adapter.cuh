@@ -871,27 +871,79 @@ __global__ void __launch_bounds__(kAdapterThreads, blocks_of<T, kRank>())
 // lanes the columns, eight each; where there are fewer pairs of ranks than warps, the
 // others take other columns.  y = base + U h: a column to a thread at a time.
 // ---------------------------------------------------------------------------
-// Eight neighbouring elements from a 16-byte boundary on, or zeros.
-template <class T>
-struct Vector {
-  uint4 v[sizeof(T) / 2];
-  __device__ __forceinline__ void load(const T* p, bool there) {
+// kN neighbouring elements of a row, n of which there are: from a 16-byte boundary on, or
+// (not kWhole) the 16-byte pieces that hold any of them, to be shifted once they are there.
+template <class T, int kN, bool kWhole>
+struct Run {
+  static constexpr int kPieces = kN * static_cast<int>(sizeof(T)) / 16 + !kWhole;
+  uint32_t w[4 * kPieces];
+  __device__ __forceinline__ void load(const T* p, int n) {
+    const uint32_t off = kWhole ? 0 : reinterpret_cast<uintptr_t>(p) & 15;
+    const int end = n > 0 ? static_cast<int>(off) + n * static_cast<int>(sizeof(T)) : 0;
+    const char* const at = reinterpret_cast<const char*>(p) - off;
 #pragma unroll
-    for (int i = 0; i < static_cast<int>(sizeof(T)) / 2; ++i)
-      v[i] = there ? ld_nc_v4(p + i * (16 / sizeof(T))) : make_uint4(0, 0, 0, 0);
+    for (int i = 0; i < kPieces; ++i)
+      *reinterpret_cast<uint4*>(w + 4 * i) = 16 * i < end ? ld_nc_v4(at + 16 * i) : make_uint4(0, 0, 0, 0);
   }
-  __device__ __forceinline__ float2 pair(int i) const { return pair_at(reinterpret_cast<const T*>(v) + 2 * i); }
+  // Of the same p and n: zeros behind the n elements.
+  __device__ __forceinline__ void settle(const T* p, int n) {
+    if constexpr (!kWhole) {
+      shift_bytes(w, reinterpret_cast<uintptr_t>(p) & 15);
+      if (n >= kN) return;
+#pragma unroll
+      for (int i = 0; i < kN; ++i)
+        if (i >= n) {
+          if constexpr (sizeof(T) == 4) w[i] = 0;
+          else w[i / 2] &= i % 2 ? 0x0000FFFFu : 0xFFFF0000u;
+        }
+    }
+  }
+  __device__ __forceinline__ float2 pair(int i) const { return pair_at(reinterpret_cast<const T*>(w) + 2 * i); }
 };
+
+// A row's c h or dh in `hidden`, from the sums of `slices` shares of a block's columns and
+// of the cluster's blocks.
+template <class T, int kRank>
+__device__ __forceinline__ void thin_hidden(const Chain<T>& a, const Tile& t, uint32_t part, uint32_t group,
+                                            float (*sums)[kRank], uint32_t slices, float* hidden) {
+  using P = Planes<T>;
+  const uint32_t tid = threadIdx.x;
+  __syncthreads();
+  float v = 0.f;
+  if (tid < kRank)
+    for (uint32_t s = 0; s < slices; ++s) v += sums[s][tid];
+  if (a.parts > 1) {
+    __syncthreads();
+    if (tid < kRank) sums[0][tid] = v;
+    cluster_meet();
+    if (tid < kRank) {
+      v = 0.f;
+      for (uint32_t p = 0; p < a.parts; ++p) v += remote_f32(smem_u32(&sums[0][tid]), p);
+    }
+    cluster_arrive();
+  }
+  if (tid < kRank) {
+    hidden[tid] = v *= a.q.scales ? a.q.scales[t.adapter] : 1.f;
+    if (group == 0 && part == 0) {  // for the gradients
+      uint32_t w[P::kP];
+      split_pair<P::kP>(v, 0.f, w);
+#pragma unroll
+      for (int p = 0; p < P::kP; ++p)
+        reinterpret_cast<uint16_t*>(a.hidden)[t.row0 * (P::kP * kRank) + p * kRank + tid] = static_cast<uint16_t>(w[p]);
+    }
+  }
+  __syncthreads();
+}
 
 // Columns of y that a thread has on their way at a time.
 template <class T, int kRank>
 __host__ __device__ constexpr int thin_columns() { return kRank == 64 || (kRank == 32 && sizeof(T) == 4) ? 1 : 2; }
 
-template <class T, int kRank>
+template <class T, int kRank, bool kWhole>
 __global__ void __launch_bounds__(kAdapterThreads, 2)
     thin_kernel(const __grid_constant__ Chain<T> a) {
-  using P = Planes<T>;
-  constexpr int kWarps = kAdapterThreads / 32, kMost = 4;  // loads of a rank in flight
+  constexpr int kWarps = kAdapterThreads / 32;
+  constexpr int kMost = kWhole ? 4 : sizeof(T) == 2 ? 2 : 1;  // loads of a rank in flight
   constexpr int kEach = thin_columns<T, kRank>();
   __shared__ __align__(16) float sums[kWarps][kRank], hidden[kRank];
   const uint32_t tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
@@ -906,15 +958,13 @@ __global__ void __launch_bounds__(kAdapterThreads, 2)
   if (!adapts && a.y == a.base) return;
   const T* const second = a.second.data + (adapts ? t.adapter * a.second.step : 0);
   const T* const base = a.base + t.row0 * a.base_stride;
-  Vector<T> u[kEach][kRank / 8];
+  Run<T, kRank, kWhole> u[kEach];
   float onto[kEach];
   auto load_columns = [&](uint64_t c) {
 #pragma unroll
     for (int e = 0; e < kEach; ++e) {
       const uint64_t col = c + e * kAdapterThreads + tid;
-#pragma unroll
-      for (int i = 0; i < kRank / 8; ++i)
-        u[e][i].load(second + col * a.second.stride + i * 8, adapts && col < col1 && i * 8 < static_cast<int>(a.rank));
+      u[e].load(second + col * a.second.stride, adapts && col < col1 ? a.rank : 0);
       onto[e] = a.base && col < col1 ? to_f32(base[col]) : 0.f;
     }
   };
@@ -934,21 +984,28 @@ __global__ void __launch_bounds__(kAdapterThreads, 2)
       const bool two = 2 * pair + 1 < a.rank;
       float acc[2] = {};
       for (uint64_t k = in0 + slice * 256 + lane * 8; k < in1; k += slices * 256 * kMost) {
-        Vector<T> d[2][kMost];
+        Run<T, 8, kWhole> d[2][kMost], e[kWhole ? 1 : kMost];
+        auto there = [&](uint64_t at) {
+          return kWhole ? (at < in1 ? 8 : 0) : static_cast<int>(min(in1 - min(at, in1), static_cast<uint64_t>(8)));
+        };
 #pragma unroll
         for (int m = 0; m < kMost; ++m) {
           const uint64_t at = k + m * slices * 256;
-          d[0][m].load(d0 + at, at < in1);
-          d[1][m].load(d0 + a.first.stride + at, two && at < in1);
+          d[0][m].load(d0 + at, there(at));
+          d[1][m].load(d0 + a.first.stride + at, two ? there(at) : 0);
+          if constexpr (!kWhole) e[m].load(x + at, there(at));
         }
 #pragma unroll
         for (int m = 0; m < kMost; ++m) {
           const uint64_t at = k + m * slices * 256;
-          Vector<T> e;
-          e.load(x + at, at < in1);
+          if constexpr (kWhole) e[0].load(x + at, there(at));
+          auto& v8 = e[kWhole ? 0 : m];
+          v8.settle(x + at, there(at));
+          d[0][m].settle(d0 + at, there(at));
+          d[1][m].settle(d0 + a.first.stride + at, two ? there(at) : 0);
 #pragma unroll
           for (int i = 0; i < 4; ++i) {
-            const float2 v = e.pair(i), p = d[0][m].pair(i), q = d[1][m].pair(i);
+            const float2 v = v8.pair(i), p = d[0][m].pair(i), q = d[1][m].pair(i);
             acc[0] = fmaf(v.y, p.y, fmaf(v.x, p.x, acc[0]));
             acc[1] = fmaf(v.y, q.y, fmaf(v.x, q.x, acc[1]));
           }
@@ -960,31 +1017,7 @@ __global__ void __launch_bounds__(kAdapterThreads, 2)
         if (lane == 0 && (r == 0 || two)) sums[slice][2 * pair + r] = acc[r];
       }
     }
-    __syncthreads();
-    float v = 0.f;
-    if (tid < kRank)
-      for (uint32_t s = 0; s < slices; ++s) v += sums[s][tid];
-    if (a.parts > 1) {
-      __syncthreads();
-      if (tid < kRank) sums[0][tid] = v;
-      cluster_meet();
-      if (tid < kRank) {
-        v = 0.f;
-        for (uint32_t p = 0; p < a.parts; ++p) v += remote_f32(smem_u32(&sums[0][tid]), p);
-      }
-      cluster_arrive();
-    }
-    if (tid < kRank) {
-      hidden[tid] = v *= a.q.scales ? a.q.scales[t.adapter] : 1.f;
-      if (group == 0 && part == 0) {  // for the backward call
-        uint32_t w[P::kP];
-        split_pair<P::kP>(v, 0.f, w);
-#pragma unroll
-        for (int p = 0; p < P::kP; ++p)
-          reinterpret_cast<uint16_t*>(a.hidden)[t.row0 * (P::kP * kRank) + p * kRank + tid] = static_cast<uint16_t>(w[p]);
-      }
-    }
-    __syncthreads();
+    thin_hidden<T, kRank>(a, t, part, group, sums, slices, hidden);
   }
   T* const y = a.y + t.row0 * a.y_stride;
   for (uint64_t c = col0; c < col1; c += kEach * kAdapterThreads) {
@@ -993,14 +1026,109 @@ __global__ void __launch_bounds__(kAdapterThreads, 2)
     for (int e = 0; e < kEach; ++e) {
       const uint64_t col = c + e * kAdapterThreads + tid;
       float w = 0.f;
-      if (adapts)
+      if (adapts) {
+        u[e].settle(second + col * a.second.stride, a.rank);
 #pragma unroll
         for (int i = 0; i < kRank / 2; i += 2) {
           const float4 h = *reinterpret_cast<const float4*>(&hidden[2 * i]);
-          const float2 p = u[e][i / 4].pair(i % 4), q = u[e][i / 4].pair(i % 4 + 1);
+          const float2 p = u[e].pair(i), q = u[e].pair(i + 1);
           w = fmaf(h.w, q.y, fmaf(h.z, q.x, fmaf(h.y, p.y, fmaf(h.x, p.x, w))));
         }
+      }
       if (col < col1) y[col] = from_f32<T>(onto[e] + w);
+    }
+  }
+  if (adapts && a.parts > 1) cluster_wait();  // the others have read this block's sums
+}
+
+// The same of the backward pass.  dh = c U^T dy: a column of dy to a thread at a time, its
+// row of U times it onto sums of up to 32 ranks, which a warp's lanes put together by halves.
+// dx = base + D^T dh: columns of dx to a thread, whose elements of D are neighbours of the
+// other threads'.
+constexpr int kBackEach = 4;  // columns of dx to a thread at a time
+template <class T, int kRank, bool kWhole>
+__global__ void __launch_bounds__(kAdapterThreads, 2)
+    thin_back_kernel(const __grid_constant__ Chain<T> a) {
+  constexpr int kWarps = kAdapterThreads / 32, kMost = 2;
+  constexpr int kChunk = kRank < 32 ? kRank : 32, kHalves = kRank / kChunk, kLines = kWarps / kHalves;
+  __shared__ __align__(16) float sums[kLines][kRank], hidden[kRank];
+  const uint32_t tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  pdl_trigger();
+  pdl_wait();
+  const uint32_t part = blockIdx.x % a.parts, group = blockIdx.x / a.parts % a.groups;
+  Tile t;
+  if (!Tile::find<1>(a.q, blockIdx.x / a.parts / a.groups, t)) return;  // the whole cluster
+  const uint64_t col0 = (static_cast<uint64_t>(group) * a.parts + part) * a.group_out;
+  const uint64_t col1 = min(col0 + a.group_out, a.out);
+  const bool adapts = t.adapter >= 0;
+  if (!adapts && a.y == a.base) return;
+  if (adapts) {
+    const uint64_t in0 = min(part * a.part_in, a.in), in1 = min(in0 + a.part_in, a.in);
+    const uint32_t half = warp % kHalves, line = warp / kHalves;
+    const int n = min(static_cast<int>(a.rank) - static_cast<int>(half) * kChunk, kChunk);  // ranks; may be below 0
+    const T* const first = a.first.data + t.adapter * a.first.step + half * kChunk;
+    const T* const x = a.x + t.row0 * a.x_stride;
+    float acc[kChunk] = {};
+    for (uint64_t c = in0 + line * 32 + lane; c < in1; c += kLines * 32 * kMost) {
+      Run<T, kChunk, kWhole> u[kMost];
+      float v[kMost];
+#pragma unroll
+      for (int m = 0; m < kMost; ++m) {
+        const uint64_t at = c + m * kLines * 32;
+        u[m].load(first + at * a.first.stride, at < in1 ? n : 0);
+        v[m] = at < in1 ? to_f32(x[at]) : 0.f;
+      }
+#pragma unroll
+      for (int m = 0; m < kMost; ++m) {
+        u[m].settle(first + (c + m * kLines * 32) * a.first.stride, n);
+#pragma unroll
+        for (int i = 0; i < kChunk / 2; ++i) {
+          const float2 p = u[m].pair(i);
+          acc[2 * i] = fmaf(v[m], p.x, acc[2 * i]);
+          acc[2 * i + 1] = fmaf(v[m], p.y, acc[2 * i + 1]);
+        }
+      }
+    }
+    // every turn half as many sums, of twice as many lanes each
+#pragma unroll
+    for (int o = 16, left = kChunk; left > 1; o /= 2, left /= 2) {
+      const bool upper = lane & o;
+#pragma unroll
+      for (int i = 0; i < left / 2; ++i) {
+        const float keep = upper ? acc[i + left / 2] : acc[i], send = upper ? acc[i] : acc[i + left / 2];
+        acc[i] = keep + __shfl_xor_sync(0xFFFFFFFFu, send, o);
+      }
+    }
+    if constexpr (kChunk == 16) acc[0] += __shfl_xor_sync(0xFFFFFFFFu, acc[0], 1);
+    sums[line][half * kChunk + lane / (32 / kChunk)] = acc[0];
+    thin_hidden<T, kRank>(a, t, part, group, sums, kLines, hidden);
+  }
+  const T* const second = a.second.data + (adapts ? t.adapter * a.second.step : 0);
+  const T* const base = a.base + t.row0 * a.base_stride;
+  T* const y = a.y + t.row0 * a.y_stride;
+  for (uint64_t c = col0 + tid; c < col1; c += kBackEach * kAdapterThreads) {
+    float w[kBackEach], onto[kBackEach];
+#pragma unroll
+    for (int e = 0; e < kBackEach; ++e) {
+      const uint64_t col = c + e * kAdapterThreads;
+      onto[e] = a.base && col < col1 ? to_f32(base[col]) : 0.f;
+      w[e] = 0.f;
+    }
+    if (adapts) {
+#pragma unroll 4
+      for (uint32_t r = 0; r < a.rank; ++r) {
+        const float h = hidden[r];
+#pragma unroll
+        for (int e = 0; e < kBackEach; ++e) {
+          const uint64_t col = c + e * kAdapterThreads;
+          if (col < col1) w[e] = fmaf(h, to_f32(second[r * a.second.stride + col]), w[e]);
+        }
+      }
+    }
+#pragma unroll
+    for (int e = 0; e < kBackEach; ++e) {
+      const uint64_t col = c + e * kAdapterThreads;
+      if (col < col1) y[col] = from_f32<T>(onto[e] + w[e]);
     }
   }
   if (adapts && a.parts > 1) cluster_wait();  // the others have read this block's sums
@@ -1023,6 +1151,57 @@ struct Grads {
   T* out[2];            // adapters x rank x k, adapters x n x rank
   bool whole[2];
 };
+
+// The requests of an adapter among the kAdapterThreads from s0 on, in their order, as one
+// list of rows: their first rows, and how many come before theirs.  Returns the rows; all
+// threads call it.
+__device__ __forceinline__ uint64_t list_rows(const Requests& q, uint64_t adapter, uint64_t s0, uint64_t* from,
+                                              uint64_t* before, uint64_t* sums_before, uint32_t* counts,
+                                              uint32_t& found) {
+  const uint32_t tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const uint64_t s = s0 + tid;
+  const bool mine = s < q.requests && q.adapter(s + 1) == static_cast<int64_t>(adapter);
+  const uint64_t start = mine ? q.start(s + 1) : 0, end = mine ? q.start(s + 2) : 0;
+  const uint64_t length = end > start ? end - start : 0;
+  uint64_t upto = length;
+  for (int o = 1; o < 32; o *= 2) {
+    const uint64_t v = __shfl_up_sync(0xFFFFFFFFu, upto, o);
+    if (lane >= o) upto += v;
+  }
+  const uint32_t votes = __ballot_sync(0xFFFFFFFFu, mine);
+  if (lane == 31) {
+    counts[warp] = __popc(votes);
+    sums_before[warp] = upto;
+  }
+  __syncthreads();
+  uint32_t at = __popc(votes & ((1u << lane) - 1));
+  uint64_t left = 0, rows = 0;
+  found = 0;
+  for (uint32_t w = 0; w < kAdapterThreads / 32; ++w) {
+    if (w < warp) {
+      at += counts[w];
+      left += sums_before[w];
+    }
+    found += counts[w];
+    rows += sums_before[w];
+  }
+  if (mine) {
+    from[at] = start;
+    before[at] = left + upto - length;
+  }
+  __syncthreads();
+  return rows;
+}
+// The batch's row of the list's: the last request with no more than `want` before it.
+__device__ __forceinline__ uint64_t row_at(const uint64_t* from, const uint64_t* before, uint32_t found, uint64_t want) {
+  uint32_t lo = 0, hi = found;
+  while (hi - lo > 1) {
+    const uint32_t mid = (lo + hi) / 2;
+    if (before[mid] <= want) lo = mid;
+    else hi = mid;
+  }
+  return from[lo] + (want - before[lo]);
+}
 
 template <class T, int kRank>
 struct GradShape {
@@ -1132,38 +1311,9 @@ __global__ void __launch_bounds__(kAdapterThreads, GradShape<T, kRank>::kBlocks)
 
   uint64_t tile = 0;  // of the adapter's
   for (uint64_t s0 = 0; s0 < a.q.requests; s0 += kThreads) {
-    // the requests of this adapter among the next ones, in their order, as one list of
-    // rows: tiles go across requests
-    const uint64_t s = s0 + tid;
-    const bool mine = s < a.q.requests && a.q.adapter(s + 1) == static_cast<int64_t>(adapter);
-    const uint64_t start = mine ? a.q.start(s + 1) : 0, end = mine ? a.q.start(s + 2) : 0;
-    const uint64_t length = end > start ? end - start : 0;
-    uint64_t upto = length;
-    for (int o = 1; o < 32; o *= 2) {
-      const uint64_t v = __shfl_up_sync(0xFFFFFFFFu, upto, o);
-      if (lane >= o) upto += v;
-    }
-    const uint32_t votes = __ballot_sync(0xFFFFFFFFu, mine);
-    if (lane == 31) {
-      counts[warp] = __popc(votes);
-      sums_before[warp] = upto;
-    }
-    __syncthreads();
-    uint32_t at = __popc(votes & ((1u << lane) - 1)), found = 0;
-    uint64_t left = 0, all_rows = 0;
-    for (uint32_t w = 0; w < kThreads / 32; ++w) {
-      if (w < warp) {
-        at += counts[w];
-        left += sums_before[w];
-      }
-      found += counts[w];
-      all_rows += sums_before[w];
-    }
-    if (mine) {
-      from[at] = start;
-      before[at] = left + upto - length;
-    }
-    __syncthreads();
+    // (tiles go across requests)
+    uint32_t found;
+    const uint64_t all_rows = list_rows(a.q, adapter, s0, from, before, sums_before, counts, found);
     // this block's tiles of theirs, the next ones' loads on the way
     uint64_t row = 0;
     auto next = [&](int stage) {  // loads one; false: none left
@@ -1172,16 +1322,7 @@ __global__ void __launch_bounds__(kAdapterThreads, GradShape<T, kRank>::kBlocks)
         row += S::kRows;
         if (tile++ % a.parts != part) continue;
         const int rows = static_cast<int>(min(all_rows - row0, static_cast<uint64_t>(S::kRows)));
-        if (static_cast<int>(tid) < rows) {
-          const uint64_t want = row0 + tid;
-          uint32_t lo = 0, hi = found;  // the last request with no more than `want` before it
-          while (hi - lo > 1) {
-            const uint32_t mid = (lo + hi) / 2;
-            if (before[mid] <= want) lo = mid;
-            else hi = mid;
-          }
-          row_of[stage][tid] = from[lo] + (want - before[lo]);
-        }
+        if (static_cast<int>(tid) < rows) row_of[stage][tid] = row_at(from, before, found, row0 + tid);
         __syncthreads();
         load(stage, rows);
 #pragma unroll
@@ -1239,6 +1380,110 @@ __global__ void __launch_bounds__(kAdapterThreads, GradShape<T, kRank>::kBlocks)
     out[to_at] = from_f32<T>(total[r * S::kSumPitch + c]);
   }
   if (a.parts > 1) cluster_meet();  // the others stay until their parts are read
+}
+
+// The same where adapters have few rows: a column of m to a thread, whose sums over the
+// rows stay in its registers; a step takes kRows rows' p through shared memory.
+template <class T, int kRank>
+struct FewShape {
+  static constexpr int kCols = kAdapterThreads, kRows = 16;
+  static constexpr int kPitch = kRank + 4 / static_cast<int>(sizeof(T));  // no bank twice
+  // columns whose results are put in order at a time
+  static constexpr int kTurn = kCols * kPitch * sizeof(T) > 36 * 1024 ? kCols / 2 : kCols;
+};
+template <class T, int kRank>
+__global__ void __launch_bounds__(kAdapterThreads, kRank == 64 ? 2 : kRank == 16 ? 5 : sizeof(T) == 4 ? 3 : 4)
+    few_grads_kernel(const __grid_constant__ Grads<T> a) {
+  using S = FewShape<T, kRank>;
+  using P = Planes<T>;
+  constexpr int kThreads = kAdapterThreads, kRows = S::kRows;
+  __shared__ __align__(16) float ps[kRows][kRank];
+  __shared__ T results[S::kTurn][S::kPitch];
+  __shared__ uint64_t from[kThreads], before[kThreads], sums_before[kThreads / 32], row_of[kRows];
+  __shared__ uint32_t counts[kThreads / 32];
+  const uint32_t tid = threadIdx.x;
+  pdl_trigger();
+  pdl_wait();
+  const uint64_t all = a.blocks[0] + a.blocks[1];
+  const uint64_t adapter = blockIdx.x / all;
+  uint64_t block = blockIdx.x % all;
+  const int sel = block >= a.blocks[0];
+  if (sel) block -= a.blocks[0];
+  const uint64_t col0 = block * S::kCols, cols = a.cols[sel], col = col0 + tid, stride = a.stride[sel];
+  const T* const m = a.m[sel] + col;
+  const __nv_bfloat16* const p = a.p[sel];
+  float acc[kRank] = {};
+  for (uint64_t s0 = 0; s0 < a.q.requests; s0 += kThreads) {
+    uint32_t found;
+    const uint64_t rows = list_rows(a.q, adapter, s0, from, before, sums_before, counts, found);
+    for (uint64_t row0 = 0; row0 < rows; row0 += kRows) {
+      const int there = static_cast<int>(min(rows - row0, static_cast<uint64_t>(kRows)));
+      if (static_cast<int>(tid) < there) row_of[tid] = row_at(from, before, found, row0 + tid);
+      __syncthreads();
+      constexpr int kBatch = 8;  // rows of m in flight
+      float v[kBatch];
+      auto load = [&](int at) {
+#pragma unroll
+        for (int i = 0; i < kBatch; ++i) v[i] = at + i < there && col < cols ? to_f32(m[row_of[at + i] * stride]) : 0.f;
+      };
+      load(0);
+      for (int e = tid; e < there * kRank; e += kThreads) {
+        const __nv_bfloat16* const at = p + row_of[e / kRank] * (P::kP * kRank) + e % kRank;
+        float sum = 0.f;
+#pragma unroll
+        for (int i = P::kP - 1; i >= 0; --i) sum += to_f32(at[i * kRank]);
+        ps[e / kRank][e % kRank] = sum;
+      }
+      __syncthreads();
+      for (int at = 0; at < there; at += kBatch) {
+        if (at) load(at);
+#pragma unroll
+        for (int i = 0; i < kBatch; ++i) {
+          if (at + i >= there) break;
+#pragma unroll
+          for (int r = 0; r < kRank; r += 4) {
+            const float4 h = *reinterpret_cast<const float4*>(&ps[at + i][r]);
+            acc[r] = fmaf(h.x, v[i], acc[r]);
+            acc[r + 1] = fmaf(h.y, v[i], acc[r + 1]);
+            acc[r + 2] = fmaf(h.z, v[i], acc[r + 2]);
+            acc[r + 3] = fmaf(h.w, v[i], acc[r + 3]);
+          }
+        }
+      }
+      __syncthreads();
+    }
+  }
+  const int n = static_cast<int>(min(cols - col0, static_cast<uint64_t>(S::kCols)));
+  if (!sel) {
+    T* const out = a.out[0] + adapter * a.rank * cols + col;
+#pragma unroll
+    for (int r = 0; r < kRank; ++r)
+      if (r < static_cast<int>(a.rank) && col < cols) out[r * cols] = from_f32<T>(acc[r]);
+    return;
+  }
+  // the block's columns of the second gradient lie together
+#pragma unroll
+  for (int c0 = 0; c0 < S::kCols; c0 += S::kTurn) {
+    if (c0) __syncthreads();
+    const int mine = static_cast<int>(tid) - c0;
+    if (mine >= 0 && mine < S::kTurn)
+#pragma unroll
+      for (int r = 0; r < kRank; ++r) results[mine][r] = from_f32<T>(acc[r]);
+    __syncthreads();
+    T* const out = a.out[1] + (adapter * cols + col0 + c0) * a.rank;
+    const uint32_t end = max(min(n - c0, S::kTurn), 0) * a.rank;
+    uint32_t c = tid / a.rank, r = tid % a.rank;
+    const uint32_t on_c = kThreads / a.rank, on_r = kThreads % a.rank;
+    for (uint32_t e = tid; e < end; e += kThreads) {
+      out[e] = results[c][r];
+      c += on_c;
+      r += on_r;
+      if (r >= a.rank) {
+        r -= a.rank;
+        ++c;
+      }
+    }
+  }
 }
 
 // ---------------------------------------------------------------------------

@@ -90,12 +90,24 @@ cudaError_t launch_few(Chain<T> a, uint64_t slots, uint64_t tiles, uint64_t cols
 template <class T, int kRank, bool kBack>
 cudaError_t chain_of(const Chain<T>& a, cudaStream_t st) {
   const uint64_t tokens = a.q.tokens, requests = a.q.requests;
-  // Single tokens, whose factors are read once: 256 of 4096 by rank 16 take 18 us, in
-  // tiles of 16 rows 38.
-  if constexpr (!kBack)
-    if (tokens <= requests && a.x_whole && a.first.whole && a.second.whole && a.in % 8 == 0 && a.rank % 8 == 0)
-      return launch_few<thin_kernel<T, kRank>>(a, slots_of(tokens, requests, 1), tokens,
-                                               thin_columns<T, kRank>() * kAdapterThreads, 0, st);
+  // Few rows to a request, by row: factors are read once for each, past shared memory.  With
+  // rows alone and in tiles of 16, bfloat16, 128 requests, 2048 to 2048: of 1 row by rank 16
+  // 12 and 17 us (backward 9 and 19), of 4 14 and 21 (14 and 24), of 8 23 and 22 (22 and 20);
+  // of 1 row by rank 64 25 and 40 (19 and 39), of 2 32 and 40 (47 and 39), of 4 47 and 31 (57
+  // and 30).  Rows that start anywhere, 450 rows of 5437 to 2437 by rank 8: 25 and 93.
+  if (kRank * tokens <= 128 * requests) {
+    const uint64_t slots = slots_of(tokens, requests, 1);
+    if constexpr (kBack) {
+      constexpr int kCols = kBackEach * kAdapterThreads;
+      return a.first.whole && a.rank % 8 == 0 ? launch_few<thin_back_kernel<T, kRank, true>>(a, slots, tokens, kCols, 0, st)
+                                              : launch_few<thin_back_kernel<T, kRank, false>>(a, slots, tokens, kCols, 0, st);
+    } else {
+      constexpr int kCols = thin_columns<T, kRank>() * kAdapterThreads;
+      return a.x_whole && a.first.whole && a.second.whole && a.in % 8 == 0 && a.rank % 8 == 0
+                 ? launch_few<thin_kernel<T, kRank, true>>(a, slots, tokens, kCols, 0, st)
+                 : launch_few<thin_kernel<T, kRank, false>>(a, slots, tokens, kCols, 0, st);
+    }
+  }
   // Few rows: with tiles of 16 and of 64 rows, bfloat16, 2048 to 2048 by rank 16, forward:
   // 341 requests of 12 30.0 and 33.9 us, 256 of 16 29.7 and 32.3, 204 of 20 29.2 and 28.0, 128
   // of 32 29.4 and 27.2; 170 of 12, 1024 to 1024 by rank 64, 27.0 and 22.1.
@@ -117,6 +129,15 @@ cudaError_t chain(const Chain<T>& a, cudaStream_t st) {
 template <class T, int kRank>
 cudaError_t launch_grads(Grads<T> a, cudaStream_t st) {
   using S = GradShape<T, kRank>;
+  // Few rows to an adapter: 128 adapters, 2048 to 2048, bfloat16, of 1 row by rank 16 14 us
+  // where tiles of 64 rows take 57, of 16 rows 27 and 58; 32 adapters of 16 rows 11 and 19, of
+  // 64 rows 33 and 19.  (Adapters without rows: 191 of rank 5, 1599 to 1933, 9.5 and 48.)
+  if (a.q.tokens <= 16 * (a.q.adapters < a.q.requests ? a.q.adapters : a.q.requests)) {
+    constexpr int kCols = FewShape<T, kRank>::kCols;
+    for (int i = 0; i < 2; ++i) a.blocks[i] = a.out[i] ? (a.cols[i] + kCols - 1) / kCols : 0;
+    const uint64_t blocks = a.q.adapters * (a.blocks[0] + a.blocks[1]);
+    return blocks ? launch_clusters<few_grads_kernel<T, kRank>>(blocks, 1, kAdapterThreads, 0, st, a) : cudaSuccess;
+  }
   a.blocks[0] = a.out[0] ? (a.cols[0] + S::kCols - 1) / S::kCols : 0;
   a.blocks[1] = a.out[1] ? (a.cols[1] + S::kCols - 1) / S::kCols : 0;
   const uint64_t blocks = a.q.adapters * (a.blocks[0] + a.blocks[1]);

@@ -215,6 +215,62 @@ def test_many_more_requests_than_rows(hkv, dtype, rank):
     Case(dtype, 64, 72, rank, lengths, [i % 4 - 1 for i in range(3000)], before=3, behind=4).check(hkv)
 
 
+@pytest.mark.parametrize("k,n", [(1, 1), (9, 300), (264, 520), (70, 130), (513, 257), (2048, 1023), (31, 4100)])
+@pytest.mark.parametrize("rank", [1, 8, 13, 16, 31, 32, 48, 63, 64])
+@pytest.mark.parametrize("dtype", TYPES)
+def test_rows_alone(hkv, k, n, rank, dtype):
+    """Requests of one row, and of two by one adapter or several."""
+    Case(dtype, k, n, rank, [1] * 37, [i * 5 % 7 - 1 for i in range(37)], count=7, before=1, behind=2, seed=k + rank).check(hkv)
+    Case(dtype, k, n, rank, [2, 0, 3, 1, 2], [1, 0, -1, 1, 2], seed=n + rank).check(hkv)
+
+
+@pytest.mark.parametrize("k,n", [(264, 520), (261, 77)])
+@pytest.mark.parametrize("rank", [5, 24, 64])
+@pytest.mark.parametrize("dtype", TYPES)
+def test_few_rows_to_an_adapter(hkv, k, n, rank, dtype):
+    """More rows and requests than a step of the sums takes, adapters without any, and the
+    lengths around the rule's borders."""
+    lengths = [i * 7 % 6 for i in range(600)]
+    Case(dtype, k, n, rank, lengths, [i * i % 61 - 1 for i in range(600)], count=60, before=2, behind=1).check(hkv)
+    Case(dtype, k, n, rank, [3], [150], count=191).check(hkv)
+    for length in (15, 16, 17, 32):
+        Case(dtype, k, n, rank, [length] * 3, [2, 0, 1], seed=length).check(hkv)
+
+
+@pytest.mark.parametrize("k,n", [(1, 1), (70, 130), (513, 257), (1000, 77), (40, 3000)])
+@pytest.mark.parametrize("rank", [1, 13, 16, 24, 64])
+@pytest.mark.parametrize("dtype", TYPES)
+def test_many_rows_to_an_adapter(hkv, k, n, rank, dtype):
+    Case(dtype, k, n, rank, [5, 0, 150, 70, 3, 90], [2, 1, 0, 0, -1, 1], before=2, behind=3, seed=k + n + rank).check(hkv)
+
+
+@pytest.mark.parametrize("extra,shift", [(0, 1), (3, 5), (8, 8), (8, 4)])
+@pytest.mark.parametrize("dtype", [F32, F16])
+@pytest.mark.parametrize("rank", [7, 40])
+def test_strides_of_rows_alone(hkv, extra, shift, dtype, rank):
+    """What lies between the rows and around the factors' is neither used nor written."""
+    c = Case(dtype, 168, 136, rank, [1, 1, 2, 1], [0, 1, 2, 0], before=1, behind=2)
+    c.x, c.base, c.dy, c.dx_base = (_strided(t, extra, shift) for t in (c.x, c.base, c.dy, c.dx_base))
+    bank = torch.full((3, shift + rank * (168 + 136) + extra), math.nan, dtype=dtype, device=DEV)
+    down = bank[:, shift:shift + rank * 168].unflatten(1, (rank, 168))
+    up = bank[:, shift + rank * 168:shift + rank * 304].unflatten(1, (136, rank))
+    down.copy_(c.down)
+    up.copy_(c.up)
+    c.down, c.up = down, up
+    out, dx = (_strided(torch.zeros_like(t), extra, shift) for t in (c.base, c.x))
+    c.check(hkv, out=out, dx=dx)
+    for t in (out, dx):
+        whole = torch.empty(0, dtype=dtype, device=DEV).set_(t.untyped_storage())
+        assert int(whole.isnan().sum()) == shift + extra * len(t), "elements between the rows were written"
+    # NaN behind the last rank of every row, and behind the last column
+    tall = torch.full((3, 136, rank + 3), math.nan, dtype=dtype, device=DEV)
+    tall[:, :, :rank] = up
+    wide = torch.full((3, rank, 168 + 5), math.nan, dtype=dtype, device=DEV)
+    wide[:, :, :168] = down
+    c.down, c.up = wide[:, :, :168], tall[:, :, :rank]
+    c.check(hkv)
+
+
 def test_numbers_at_the_ends_of_the_range(hkv):
     """Hidden numbers above float16's largest and below its smallest, and float32's
     with all digits in use."""
