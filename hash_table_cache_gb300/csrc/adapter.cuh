@@ -30,7 +30,7 @@
 // core.  Times: adapter_launch.cuh.  What they were with fewer of these: both products
 // of long requests in one kernel of register-staged tiles 205 us where the two take 67
 // (8200 rows, 4096 to 8192, rank 32) and 124 where they take 56 (8224 rows, 4096 to 4096,
-// rank 64); single tokens in tiles of 16 rows 38 us, two kernels for them 20, one 18;
+// rank 64); single tokens in tiles of 16 rows 38 us, two kernels for them 20, one 12;
 // gradients by request 57 us, across requests 31 (4096 rows in requests of 8, 2048 to
 // 2048, rank 16); ragged x element by element 218 us, shifted 118.
 #pragma once
@@ -935,16 +935,20 @@ __device__ __forceinline__ void thin_hidden(const Chain<T>& a, const Tile& t, ui
   __syncthreads();
 }
 
-// Columns of y that a thread has on their way at a time.
-template <class T, int kRank>
-__host__ __device__ constexpr int thin_columns() { return kRank == 64 || (kRank == 32 && sizeof(T) == 4) ? 1 : 2; }
+// Columns of y that a thread has on their way at a time.  (Of eight ranks one, two and four:
+// 302 float16 requests of 3 rows, 1163 to 12920, 66, 52 and 49 us.)
+template <class T, int kUsed>
+__host__ __device__ constexpr int thin_columns() {
+  return kUsed == 8 ? 4 : kUsed == 64 || (kUsed == 32 && sizeof(T) == 4) ? 1 : 2;
+}
 
-template <class T, int kRank, bool kWhole>
+// (The adapters have kUsed ranks at most.)
+template <class T, int kRank, int kUsed, bool kWhole>
 __global__ void __launch_bounds__(kAdapterThreads, 2)
     thin_kernel(const __grid_constant__ Chain<T> a) {
   constexpr int kWarps = kAdapterThreads / 32;
   constexpr int kMost = kWhole ? 4 : sizeof(T) == 2 ? 2 : 1;  // loads of a rank in flight
-  constexpr int kEach = thin_columns<T, kRank>();
+  constexpr int kEach = thin_columns<T, kUsed>();
   __shared__ __align__(16) float sums[kWarps][kRank], hidden[kRank];
   const uint32_t tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   pdl_trigger();
@@ -958,7 +962,7 @@ __global__ void __launch_bounds__(kAdapterThreads, 2)
   if (!adapts && a.y == a.base) return;
   const T* const second = a.second.data + (adapts ? t.adapter * a.second.step : 0);
   const T* const base = a.base + t.row0 * a.base_stride;
-  Run<T, kRank, kWhole> u[kEach];
+  Run<T, kUsed, kWhole> u[kEach];
   float onto[kEach];
   auto load_columns = [&](uint64_t c) {
 #pragma unroll
@@ -1029,7 +1033,7 @@ __global__ void __launch_bounds__(kAdapterThreads, 2)
       if (adapts) {
         u[e].settle(second + col * a.second.stride, a.rank);
 #pragma unroll
-        for (int i = 0; i < kRank / 2; i += 2) {
+        for (int i = 0; i < kUsed / 2; i += 2) {
           const float4 h = *reinterpret_cast<const float4*>(&hidden[2 * i]);
           const float2 p = u[e].pair(i), q = u[e].pair(i + 1);
           w = fmaf(h.w, q.y, fmaf(h.z, q.x, fmaf(h.y, p.y, fmaf(h.x, p.x, w))));
@@ -1046,11 +1050,11 @@ __global__ void __launch_bounds__(kAdapterThreads, 2)
 // dx = base + D^T dh: columns of dx to a thread, whose elements of D are neighbours of the
 // other threads'.
 constexpr int kBackEach = 4;  // columns of dx to a thread at a time
-template <class T, int kRank, bool kWhole>
+template <class T, int kRank, int kUsed, bool kWhole>
 __global__ void __launch_bounds__(kAdapterThreads, 2)
     thin_back_kernel(const __grid_constant__ Chain<T> a) {
   constexpr int kWarps = kAdapterThreads / 32, kMost = 2;
-  constexpr int kChunk = kRank < 32 ? kRank : 32, kHalves = kRank / kChunk, kLines = kWarps / kHalves;
+  constexpr int kChunk = kUsed < 32 ? kUsed : 32, kHalves = kUsed / kChunk, kLines = kWarps / kHalves;
   __shared__ __align__(16) float sums[kLines][kRank], hidden[kRank];
   const uint32_t tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   pdl_trigger();
@@ -1099,7 +1103,9 @@ __global__ void __launch_bounds__(kAdapterThreads, 2)
         acc[i] = keep + __shfl_xor_sync(0xFFFFFFFFu, send, o);
       }
     }
-    if constexpr (kChunk == 16) acc[0] += __shfl_xor_sync(0xFFFFFFFFu, acc[0], 1);
+    for (int o = 32 / kChunk / 2; o > 0; o /= 2) acc[0] += __shfl_xor_sync(0xFFFFFFFFu, acc[0], o);
+    if (kUsed < kRank)
+      for (uint32_t i = lane + kUsed; i < kRank; i += 32) sums[line][i] = 0.f;
     sums[line][half * kChunk + lane / (32 / kChunk)] = acc[0];
     thin_hidden<T, kRank>(a, t, part, group, sums, kLines, hidden);
   }

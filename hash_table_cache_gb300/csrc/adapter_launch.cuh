@@ -3,7 +3,7 @@
 // Times of one call (GB300, bfloat16 unless said, CUDA graph replays; "base" and y in
 // memory, adapters in L2):
 //   one row, 4096 to 4096, rank 16                                4.2 us
-//   256 requests of one row, 64 adapters                          18 us
+//   256 requests of one row, 64 adapters                          12 us
 //   8200 rows of 24 requests, 4096 to 8192, rank 32               67 us, 5.0 TB/s
 //   1637 rows of 16 requests, 64 to 131072, rank 8               132 us, 6.5 TB/s
 //   8224 rows of 32 requests, 4096 to 4096, rank 64               56 us, 3.6 TB/s
@@ -68,17 +68,21 @@ cudaError_t launch_long(Chain<T> a, cudaStream_t st) {
 }
 
 // Few rows to a request: one kernel, clusters while there are no more than two blocks for
-// an SM (256 rows of 4096 by rank 16: 18 us; four 25, eight 35), and several clusters to a
-// tile where its columns of y are many.
+// an SM (256 rows of 4096 by rank 16: 12 us; four 25, eight 35), and several clusters to a
+// tile where its columns of y are many: of single rows as many as are on the SMs at once (64
+// rows of 4096 7 us and more of them 11, 128 of 512 to 8192 by rank 8 9 and 13), of tiles more
+// than that (float32, 100 requests of 16 rows, 512 to 8192 by rank 16, 84 us and fewer 102).
 template <auto kKernel, class T>
-cudaError_t launch_few(Chain<T> a, uint64_t slots, uint64_t tiles, uint64_t cols, int smem, cudaStream_t st) {
+cudaError_t launch_few(Chain<T> a, uint64_t slots, uint64_t tiles, uint64_t cols, bool at_once, int smem,
+                       cudaStream_t st) {
   const uint64_t room = 2ull * sm_count();
   a.parts = 1;
   while (a.parts < kAdapterParts && 2 * tiles * a.parts <= room && (a.in >= 256ull * a.parts || a.out > cols * a.parts))
     a.parts *= 2;
   a.part_in = ((a.in + a.parts - 1) / a.parts + 63) / 64 * 64;
   const uint64_t most = (a.out + cols * a.parts - 1) / (cols * a.parts);
-  uint64_t groups = (room + tiles * a.parts - 1) / (tiles * a.parts);
+  uint64_t groups = (room + (at_once ? 0 : tiles * a.parts - 1)) / (tiles * a.parts);
+  if (groups == 0) groups = 1;
   // every group has the first product anew
   if (groups > 1 + a.out / a.in) groups = 1 + a.out / a.in;
   if (groups > most) groups = most;
@@ -87,26 +91,36 @@ cudaError_t launch_few(Chain<T> a, uint64_t slots, uint64_t tiles, uint64_t cols
   return launch_clusters<kKernel>(slots * groups * a.parts, a.parts, kAdapterThreads, smem, st, a);
 }
 
+// (For eight ranks at most: 465 float32 requests of 2 rows, 29 to 19637 by rank 2, 90 us and
+// with sixteen 136; 302 float16 ones of 3, 1163 to 12920, by rank 8 48 us and by rank 10 78.)
+template <class T, int kRank, int kUsed, bool kBack>
+cudaError_t launch_thin(const Chain<T>& a, cudaStream_t st) {
+  const uint64_t tokens = a.q.tokens, slots = slots_of(tokens, a.q.requests, 1);
+  if constexpr (kBack) {
+    constexpr int kCols = kBackEach * kAdapterThreads;
+    return a.first.whole && a.rank % 8 == 0
+               ? launch_few<thin_back_kernel<T, kRank, kUsed, true>>(a, slots, tokens, kCols, true, 0, st)
+               : launch_few<thin_back_kernel<T, kRank, kUsed, false>>(a, slots, tokens, kCols, true, 0, st);
+  } else {
+    constexpr int kCols = thin_columns<T, kUsed>() * kAdapterThreads;
+    return a.x_whole && a.first.whole && a.second.whole && a.in % 8 == 0 && a.rank % 8 == 0
+               ? launch_few<thin_kernel<T, kRank, kUsed, true>>(a, slots, tokens, kCols, true, 0, st)
+               : launch_few<thin_kernel<T, kRank, kUsed, false>>(a, slots, tokens, kCols, true, 0, st);
+  }
+}
+
 template <class T, int kRank, bool kBack>
 cudaError_t chain_of(const Chain<T>& a, cudaStream_t st) {
   const uint64_t tokens = a.q.tokens, requests = a.q.requests;
   // Few rows to a request, by row: factors are read once for each, past shared memory.  With
   // rows alone and in tiles of 16, bfloat16, 128 requests, 2048 to 2048: of 1 row by rank 16
-  // 12 and 17 us (backward 9 and 19), of 4 14 and 21 (14 and 24), of 8 23 and 22 (22 and 20);
+  // 8 and 17 us (backward 9 and 19), of 4 14 and 21 (14 and 24), of 8 23 and 22 (22 and 20);
   // of 1 row by rank 64 25 and 40 (19 and 39), of 2 32 and 40 (47 and 39), of 4 47 and 31 (57
   // and 30).  Rows that start anywhere, 450 rows of 5437 to 2437 by rank 8: 25 and 93.
   if (kRank * tokens <= 128 * requests) {
-    const uint64_t slots = slots_of(tokens, requests, 1);
-    if constexpr (kBack) {
-      constexpr int kCols = kBackEach * kAdapterThreads;
-      return a.first.whole && a.rank % 8 == 0 ? launch_few<thin_back_kernel<T, kRank, true>>(a, slots, tokens, kCols, 0, st)
-                                              : launch_few<thin_back_kernel<T, kRank, false>>(a, slots, tokens, kCols, 0, st);
-    } else {
-      constexpr int kCols = thin_columns<T, kRank>() * kAdapterThreads;
-      return a.x_whole && a.first.whole && a.second.whole && a.in % 8 == 0 && a.rank % 8 == 0
-                 ? launch_few<thin_kernel<T, kRank, true>>(a, slots, tokens, kCols, 0, st)
-                 : launch_few<thin_kernel<T, kRank, false>>(a, slots, tokens, kCols, 0, st);
-    }
+    if constexpr (kRank == 16)
+      if (a.rank <= 8) return launch_thin<T, kRank, 8, kBack>(a, st);
+    return launch_thin<T, kRank, kRank, kBack>(a, st);
   }
   // Few rows: with tiles of 16 and of 64 rows, bfloat16, 2048 to 2048 by rank 16, forward:
   // 341 requests of 12 30.0 and 33.9 us, 256 of 16 29.7 and 32.3, 204 of 20 29.2 and 28.0, 128
@@ -116,7 +130,7 @@ cudaError_t chain_of(const Chain<T>& a, cudaStream_t st) {
     b.q.by_rows = requests > tokens;
     return launch_few<short_kernel<T, kRank, kBack>>(
         b, slots_of(tokens, requests, b.q.by_rows ? 1 : 16), tokens / 16 + (requests < tokens ? requests : tokens) + 1,
-        SecondShape<T, kRank, 16, kBack>::kCols, ShortShape<T, kRank, kBack>::kBytes, st);
+        SecondShape<T, kRank, 16, kBack>::kCols, false, ShortShape<T, kRank, kBack>::kBytes, st);
   }
   return launch_long<T, kRank, kBack>(a, st);
 }
