@@ -1156,17 +1156,79 @@ struct Grads {
   const __nv_bfloat16* p[2];  // dh, c h: tokens x planes x kRank
   T* out[2];            // adapters x rank x k, adapters x n x rank
   bool whole[2];
+  bool by_request;      // blocks are for the requests' adapters, where these are the fewer
 };
+
+// The adapter of a block's place, -1 where another place has it.  All threads call it.
+__device__ __forceinline__ int64_t adapter_at(const Requests& q, bool by_request, uint64_t place) {
+  if (!by_request) return static_cast<int64_t>(place);
+  const int64_t a = q.adapter(place + 1);
+  bool earlier = false;
+  for (uint64_t s = threadIdx.x; s < place; s += blockDim.x) earlier |= q.adapter(s + 1) == a;
+  return __syncthreads_or(earlier) ? -1 : a;
+}
+// Zeros for the adapters of no request: kFill elements to a block.
+constexpr uint32_t kFill = 32768;
+template <class T>
+__global__ void __launch_bounds__(kAdapterThreads) idle_grads_kernel(const __grid_constant__ Grads<T> a) {
+  pdl_trigger();
+  pdl_wait();
+  const uint64_t all = a.blocks[0] + a.blocks[1], adapter = blockIdx.x / all;
+  uint64_t block = blockIdx.x % all;
+  const int sel = block >= a.blocks[0];
+  if (sel) block -= a.blocks[0];
+  bool idle = true;
+  for (uint64_t s = threadIdx.x; s < a.q.requests; s += kAdapterThreads)
+    idle &= a.q.adapter(s + 1) != static_cast<int64_t>(adapter);
+  if (!__syncthreads_and(idle)) return;
+  const uint64_t count = a.rank * a.cols[sel];
+  T* const out = a.out[sel] + adapter * count + block * kFill;
+  const uint32_t n = static_cast<uint32_t>(min(count - block * kFill, static_cast<uint64_t>(kFill)));
+  constexpr uint32_t kPer = 16 / sizeof(T);
+  const uint32_t head = min(n, static_cast<uint32_t>(-reinterpret_cast<uintptr_t>(out) & 15) / static_cast<uint32_t>(sizeof(T)));
+  const uint32_t vecs = (n - head) / kPer, tail = head + vecs * kPer;
+  for (uint32_t i = threadIdx.x; i < vecs; i += kAdapterThreads)
+    reinterpret_cast<uint4*>(out + head)[i] = make_uint4(0, 0, 0, 0);
+  if (threadIdx.x < head) out[threadIdx.x] = from_f32<T>(0.f);
+  if (threadIdx.x < n - tail) out[tail + threadIdx.x] = from_f32<T>(0.f);
+}
+
+// Ranks r0 .. r0 + w - 1 of n columns of a gradient: neighbouring threads write neighbouring
+// elements of either layout.
+template <class T, int kThreads, class F>
+__device__ __forceinline__ void put_grads(const Grads<T>& a, int sel, uint64_t adapter, uint64_t col0, uint32_t n,
+                                          int r0, int w, const F& value) {
+  if (w <= 0) return;
+  const uint64_t cols = a.cols[sel];
+  if (!sel) {
+    T* const out = a.out[0] + (adapter * a.rank + r0) * cols + col0;
+    for (uint32_t r = threadIdx.x / 32; r < static_cast<uint32_t>(w); r += kThreads / 32)
+      for (uint32_t c = threadIdx.x % 32; c < n; c += 32) out[r * cols + c] = from_f32<T>(value(r, c));
+    return;
+  }
+  T* const out = a.out[1] + (adapter * cols + col0) * a.rank + r0;
+  uint32_t c = threadIdx.x / w, r = threadIdx.x % w;
+  const uint32_t on_c = kThreads / w, on_r = kThreads % w;
+  while (c < n) {
+    out[c * a.rank + r] = from_f32<T>(value(r, c));
+    c += on_c;
+    r += on_r;
+    if (r >= static_cast<uint32_t>(w)) {
+      r -= w;
+      ++c;
+    }
+  }
+}
 
 // The requests of an adapter among the kAdapterThreads from s0 on, in their order, as one
 // list of rows: their first rows, and how many come before theirs.  Returns the rows; all
 // threads call it.
-__device__ __forceinline__ uint64_t list_rows(const Requests& q, uint64_t adapter, uint64_t s0, uint64_t* from,
+__device__ __forceinline__ uint64_t list_rows(const Requests& q, int64_t adapter, uint64_t s0, uint64_t* from,
                                               uint64_t* before, uint64_t* sums_before, uint32_t* counts,
                                               uint32_t& found) {
   const uint32_t tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const uint64_t s = s0 + tid;
-  const bool mine = s < q.requests && q.adapter(s + 1) == static_cast<int64_t>(adapter);
+  const bool mine = s < q.requests && q.adapter(s + 1) == adapter;
   const uint64_t start = mine ? q.start(s + 1) : 0, end = mine ? q.start(s + 2) : 0;
   const uint64_t length = end > start ? end - start : 0;
   uint64_t upto = length;
@@ -1242,7 +1304,8 @@ __global__ void __launch_bounds__(kAdapterThreads, GradShape<T, kRank>::kBlocks)
   pdl_wait();
   const uint32_t part = blockIdx.x % a.parts;
   const uint64_t all = a.blocks[0] + a.blocks[1];
-  const uint64_t adapter = blockIdx.x / a.parts / all;
+  const int64_t adapter = adapter_at(a.q, a.by_request, blockIdx.x / a.parts / all);
+  if (adapter < 0) return;  // the whole cluster
   uint64_t block = blockIdx.x / a.parts % all;
   const int sel = block >= a.blocks[0];
   if (sel) block -= a.blocks[0];
@@ -1377,14 +1440,9 @@ __global__ void __launch_bounds__(kAdapterThreads, GradShape<T, kRank>::kBlocks)
   }
   __syncthreads();
   const float* const total = a.parts > 1 ? sums + S::kSums / 4 : sums;
-  T* const out = a.out[sel];
-  for (int e = tid; e < each * S::kCols; e += kThreads) {
-    // neighbouring threads write neighbouring elements of either layout
-    const int r = sel ? e % each : e / S::kCols, c = sel ? e / each : e % S::kCols;
-    if (r0 + r >= static_cast<int>(a.rank) || col0 + c >= cols) continue;
-    const uint64_t to_at = sel ? (adapter * cols + col0 + c) * a.rank + r0 + r : (adapter * a.rank + r0 + r) * cols + col0 + c;
-    out[to_at] = from_f32<T>(total[r * S::kSumPitch + c]);
-  }
+  put_grads<T, kThreads>(a, sel, adapter, col0, static_cast<uint32_t>(min(cols - col0, static_cast<uint64_t>(S::kCols))), r0,
+                         min(each, static_cast<int>(a.rank) - r0),
+                         [&](uint32_t r, uint32_t c) { return total[r * S::kSumPitch + c]; });
   if (a.parts > 1) cluster_meet();  // the others stay until their parts are read
 }
 
@@ -1411,7 +1469,8 @@ __global__ void __launch_bounds__(kAdapterThreads, kRank == 64 ? 2 : kRank == 16
   pdl_trigger();
   pdl_wait();
   const uint64_t all = a.blocks[0] + a.blocks[1];
-  const uint64_t adapter = blockIdx.x / all;
+  const int64_t adapter = adapter_at(a.q, a.by_request, blockIdx.x / all);
+  if (adapter < 0) return;
   uint64_t block = blockIdx.x % all;
   const int sel = block >= a.blocks[0];
   if (sel) block -= a.blocks[0];

@@ -143,18 +143,29 @@ cudaError_t chain(const Chain<T>& a, cudaStream_t st) {
 template <class T, int kRank>
 cudaError_t launch_grads(Grads<T> a, cudaStream_t st) {
   using S = GradShape<T, kRank>;
+  // More adapters than requests: blocks for the requests' ones, zeros for the others.
+  a.by_request = a.q.requests < a.q.adapters;
+  const uint64_t places = a.by_request ? a.q.requests : a.q.adapters;
+  if (a.by_request) {
+    for (int i = 0; i < 2; ++i) a.blocks[i] = a.out[i] ? (a.rank * a.cols[i] + kFill - 1) / kFill : 0;
+    const uint64_t blocks = a.q.adapters * (a.blocks[0] + a.blocks[1]);
+    if (blocks) {
+      const cudaError_t e = launch_clusters<idle_grads_kernel<T>>(blocks, 1, kAdapterThreads, 0, st, a);
+      if (e != cudaSuccess) return e;
+    }
+  }
   // Few rows to an adapter: 128 adapters, 2048 to 2048, bfloat16, of 1 row by rank 16 14 us
   // where tiles of 64 rows take 57, of 16 rows 27 and 58; 32 adapters of 16 rows 11 and 19, of
   // 64 rows 33 and 19.  (Adapters without rows: 191 of rank 5, 1599 to 1933, 9.5 and 48.)
-  if (a.q.tokens <= 16 * (a.q.adapters < a.q.requests ? a.q.adapters : a.q.requests)) {
+  if (a.q.tokens <= 16 * places) {
     constexpr int kCols = FewShape<T, kRank>::kCols;
     for (int i = 0; i < 2; ++i) a.blocks[i] = a.out[i] ? (a.cols[i] + kCols - 1) / kCols : 0;
-    const uint64_t blocks = a.q.adapters * (a.blocks[0] + a.blocks[1]);
+    const uint64_t blocks = places * (a.blocks[0] + a.blocks[1]);
     return blocks ? launch_clusters<few_grads_kernel<T, kRank>>(blocks, 1, kAdapterThreads, 0, st, a) : cudaSuccess;
   }
   a.blocks[0] = a.out[0] ? (a.cols[0] + S::kCols - 1) / S::kCols : 0;
   a.blocks[1] = a.out[1] ? (a.cols[1] + S::kCols - 1) / S::kCols : 0;
-  const uint64_t blocks = a.q.adapters * (a.blocks[0] + a.blocks[1]);
+  const uint64_t blocks = places * (a.blocks[0] + a.blocks[1]);
   if (!blocks) return cudaSuccess;
   // Clusters share an adapter's rows, two tiles to a block at least, up to two blocks for
   // an SM (8224 rows, 4 adapters of rank 64 and 4096 to 4096: 36 us; one 48, four 49).

@@ -516,7 +516,7 @@ __global__ void __launch_bounds__(GradShape<kRank>::kThreads)
 
   const uint32_t part = blockIdx.x % a.parts;
   const uint64_t all = a.blocks[0] + a.blocks[1];
-  const uint64_t adapter = blockIdx.x / a.parts / all;
+  const int64_t adapter = adapter_at(a.q, a.by_request, blockIdx.x / a.parts / all);
   uint64_t block = blockIdx.x / a.parts % all;
   const int sel = block >= a.blocks[0];
   if (sel) block -= a.blocks[0];
@@ -528,7 +528,7 @@ __global__ void __launch_bounds__(GradShape<kRank>::kThreads)
   for (uint64_t s0 = 0; s0 < a.q.requests; s0 += kThreads) {
     // the requests of this adapter among the next ones, in their order
     const uint64_t s = s0 + tid;
-    const bool mine = s < a.q.requests && a.q.adapter(s + 1) == static_cast<int64_t>(adapter);
+    const bool mine = s < a.q.requests && adapter >= 0 && a.q.adapter(s + 1) == adapter;
     const uint32_t votes = __ballot_sync(0xFFFFFFFFu, mine);
     if (lane == 0) counts[warp] = __popc(votes);
     __syncthreads();
@@ -679,14 +679,11 @@ __global__ void __launch_bounds__(GradShape<kRank>::kThreads)
     __syncthreads();
     total = joined;
   }
-  __nv_bfloat16* const out = a.out[sel];
-  for (int e = tid; e < each * S::kCols; e += kThreads) {
-    // neighbouring threads write neighbouring elements of either layout
-    const int r = r0 + (sel ? e % each : e / S::kCols), c = sel ? e / each : e % S::kCols;
-    if (r >= static_cast<int>(a.rank) || col0 + c >= cols) continue;
-    const uint64_t at = sel ? (adapter * cols + col0 + c) * a.rank + r : (adapter * a.rank + r) * cols + col0 + c;
-    out[at] = __float2bfloat16_rn(total[c * S::kPitch + r]);
-  }
+  if (adapter >= 0)
+    put_grads<__nv_bfloat16, kThreads>(a, sel, adapter, col0,
+                                       static_cast<uint32_t>(min(cols - col0, static_cast<uint64_t>(S::kCols))), r0,
+                                       min(each, static_cast<int>(a.rank) - r0),
+                                       [&](uint32_t r, uint32_t c) { return total[c * S::kPitch + r0 + r]; });
   if (a.parts > 1) cluster_meet();  // the others stay until their parts are read
 }
 
