@@ -44,6 +44,7 @@ namespace hkv {
 
 constexpr int kAdapterThreads = 256;
 constexpr int kAdapterParts = 8;  // blocks of a cluster at most
+constexpr int kGradParts = 16;    // and of one that shares an adapter's rows
 
 // Planes of the first product's operands, of a matrix that meets h or dh, and of
 // these.
@@ -1456,13 +1457,13 @@ struct FewShape {
   static constexpr int kTurn = kCols * kPitch * sizeof(T) > 36 * 1024 ? kCols / 2 : kCols;
 };
 template <class T, int kRank>
-__global__ void __launch_bounds__(kAdapterThreads, kRank == 64 ? 2 : kRank == 16 ? 5 : sizeof(T) == 4 ? 3 : 4)
+__global__ void __launch_bounds__(kAdapterThreads, kRank == 64 ? 2 : kRank == 32 ? 3 : 4)
     few_grads_kernel(const __grid_constant__ Grads<T> a) {
   using S = FewShape<T, kRank>;
   using P = Planes<T>;
   constexpr int kThreads = kAdapterThreads, kRows = S::kRows;
   __shared__ __align__(16) float ps[kRows][kRank];
-  __shared__ T results[S::kTurn][S::kPitch];
+  __shared__ __align__(16) T results[S::kTurn][S::kPitch];
   __shared__ uint64_t from[kThreads], before[kThreads], sums_before[kThreads / 32], row_of[kRows];
   __shared__ uint32_t counts[kThreads / 32];
   const uint32_t tid = threadIdx.x;
@@ -1536,18 +1537,24 @@ __global__ void __launch_bounds__(kAdapterThreads, kRank == 64 ? 2 : kRank == 16
       for (int r = 0; r < kRank; ++r) results[mine][r] = from_f32<T>(acc[r]);
     __syncthreads();
     T* const out = a.out[1] + (adapter * cols + col0 + c0) * a.rank;
-    const uint32_t end = max(min(n - c0, S::kTurn), 0) * a.rank;
-    uint32_t c = tid / a.rank, r = tid % a.rank;
-    const uint32_t on_c = kThreads / a.rank, on_r = kThreads % a.rank;
-    for (uint32_t e = tid; e < end; e += kThreads) {
-      out[e] = results[c][r];
-      c += on_c;
-      r += on_r;
-      if (r >= a.rank) {
-        r -= a.rank;
-        ++c;
+    auto put = [&](auto* to, uint32_t w) {  // w elements (or pairs) to a column
+      using V = std::remove_reference_t<decltype(*to)>;
+      uint32_t c = tid / w, r = tid % w;
+      const uint32_t on_c = kThreads / w, on_r = kThreads % w, end = max(min(n - c0, S::kTurn), 0);
+      for (uint32_t e = tid; c < end; e += kThreads) {
+        to[e] = reinterpret_cast<const V*>(results[c])[r];
+        c += on_c;
+        r += on_r;
+        if (r >= w) {
+          r -= w;
+          ++c;
+        }
       }
-    }
+    };
+    if (sizeof(T) == 2 && a.rank % 2 == 0 && reinterpret_cast<uintptr_t>(out) % 4 == 0)
+      put(reinterpret_cast<uint32_t*>(out), a.rank / 2);
+    else
+      put(out, a.rank);
   }
 }
 
@@ -1565,6 +1572,7 @@ cudaError_t launch_clusters(uint64_t blocks, uint32_t parts, int threads, int sm
     const uint64_t bit = device < 64 ? 1ull << device : 0;
     if (!(allowed.load(std::memory_order_relaxed) & bit)) {
       e = cudaFuncSetAttribute(kKernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+      if (e == cudaSuccess) e = cudaFuncSetAttribute(kKernel, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
       if (e != cudaSuccess) return e;
       allowed.fetch_or(bit, std::memory_order_relaxed);
     }

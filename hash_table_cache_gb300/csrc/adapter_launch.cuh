@@ -168,14 +168,15 @@ cudaError_t launch_grads(Grads<T> a, cudaStream_t st) {
   const uint64_t blocks = places * (a.blocks[0] + a.blocks[1]);
   if (!blocks) return cudaSuccess;
   // Clusters share an adapter's rows, two tiles to a block at least, up to two blocks for
-  // an SM (8224 rows, 4 adapters of rank 64 and 4096 to 4096: 36 us; one 48, four 49).
+  // an SM (8224 rows, 4 adapters of rank 64 and 4096 to 4096: 33 us; one 45, four 46).  Of
+  // sixteen blocks: 17000 rows of one adapter of rank 43, 480 to 721, 83 us and of eight 122.
   a.parts = 1;
-  while (a.parts < kAdapterParts && blocks * a.parts < 2ull * sm_count() && a.q.tokens >= 128ull * a.parts) a.parts *= 2;
+  while (a.parts < kGradParts && blocks * a.parts < 2ull * sm_count() && a.q.tokens >= 128ull * a.parts) a.parts *= 2;
   // (TMA takes rows that follow one another: requests of 32 rows and more)
   if constexpr (std::is_same_v<T, __nv_bfloat16>) {
     tensor::GradMaps maps{};
     if (a.q.tokens >= 32 * a.q.requests && a.q.requests && tensor::make_maps<kRank>(&maps, a)) {
-      if (a.parts > kRank / 4) a.parts = kRank / 4;  // four ranks to a part at least
+      while (a.parts > kAdapterParts || a.parts > kRank / 4) a.parts /= 2;  // four ranks to a part at least
       return launch_clusters<tensor::grads_tensor_kernel<kRank>>(blocks * a.parts, a.parts, tensor::GradShape<kRank>::kThreads,
                                                                  tensor::GradShape<kRank>::kBytes, st, maps, a);
     }

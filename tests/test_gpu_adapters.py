@@ -271,6 +271,18 @@ def test_strides_of_rows_alone(hkv, extra, shift, dtype, rank):
     c.check(hkv)
 
 
+@pytest.mark.parametrize("rank", [3, 20, 64])
+@pytest.mark.parametrize("dtype", TYPES)
+def test_many_adapters_of_few_requests(hkv, dtype, rank):
+    """Adapters of no request get zeros, whatever their gradients' memory held; two
+    requests of one adapter meet in one sum; rows shared by as many blocks as there are."""
+    junk = torch.full((3 << 20,), math.nan, device=DEV)
+    del junk
+    for lengths, which in (([3000, 40], [33, 2]), ([700, 0, 90, 64], [5, 30, 5, -1]), ([2, 1], [36, 36]), ([130], [99])):
+        Case(dtype, 72, 41, rank, lengths, which, count=37, before=1, behind=2).check(hkv)
+    Case(dtype, 1100, 1030, rank, [1, 50], [69, 0], count=70).check(hkv)
+
+
 def test_numbers_at_the_ends_of_the_range(hkv):
     """Hidden numbers above float16's largest and below its smallest, and float32's
     with all digits in use."""
