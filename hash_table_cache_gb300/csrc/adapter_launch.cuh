@@ -7,11 +7,11 @@
 //   8200 rows of 24 requests, 4096 to 8192, rank 32               67 us, 5.0 TB/s
 //   1637 rows of 16 requests, 64 to 131072, rank 8               132 us, 6.5 TB/s
 //   8224 rows of 32 requests, 4096 to 4096, rank 64               56 us, 3.6 TB/s
-//     and its backward pass                                       93 us: dx 56, gradients 36
-//   8224 rows as above, float16                                  88 and 208 us (mma.sync but
+//     and its backward pass                                       90 us: dx 56, gradients 33
+//   8224 rows as above, float16                                  91 and 203 us (mma.sync but
 //     for the forward call's and the backward call's first product)
-//   and float32                                                 227 and 443 us (six products)
-//   3919 rows of 333 requests, 128 to 128, rank 8, float32        10 and 23 us
+//   and float32                                                 230 and 440 us (six products)
+//   3919 rows of 333 requests, 128 to 128, rank 8, float32        10 and 20 us
 #pragma once
 
 #include "adapter_tensor.cuh"
@@ -113,11 +113,13 @@ template <class T, int kRank, bool kBack>
 cudaError_t chain_of(const Chain<T>& a, cudaStream_t st) {
   const uint64_t tokens = a.q.tokens, requests = a.q.requests;
   // Few rows to a request, by row: factors are read once for each, past shared memory.  With
-  // rows alone and in tiles of 16, bfloat16, 128 requests, 2048 to 2048: of 1 row by rank 16
-  // 8 and 17 us (backward 9 and 19), of 4 14 and 21 (14 and 24), of 8 23 and 22 (22 and 20);
-  // of 1 row by rank 64 25 and 40 (19 and 39), of 2 32 and 40 (47 and 39), of 4 47 and 31 (57
-  // and 30).  Rows that start anywhere, 450 rows of 5437 to 2437 by rank 8: 25 and 93.
-  if (kRank * tokens <= 128 * requests) {
+  // rows alone and in tiles of 16, bfloat16, 2048 to 2048: 128 requests of 1 row by rank 16 8
+  // and 17 us (backward 9 and 19), of 4 14 and 21 (14 and 24), of 8 23 and 22 (22 and 20), but
+  // 512 requests of 2 rows 21 and 30 (19 and 35), of 4 39 and 30 (32 and 35), of 6 58 and 31;
+  // by rank 64 128 of 1 row 25 and 40 (19 and 39), of 4 47 and 31, 512 of 2 81 and 78 (84 and
+  // 76; float32 150 and 184).  Rows that start anywhere, 450 rows of 5437 to 2437 by rank 8: 23
+  // and 93.
+  if (tokens <= (kRank == 16 ? 4 : 2) * requests || (kRank * tokens <= 16384 && kRank * tokens <= 128 * requests)) {
     if constexpr (kRank == 16)
       if (a.rank <= 8) return launch_thin<T, kRank, 8, kBack>(a, st);
     return launch_thin<T, kRank, kRank, kBack>(a, st);
