@@ -24,6 +24,7 @@ def hkv():
     m.load()
     yield m
     assert m.hkv_get_wait_timeouts() == (0, 0)
+    torch.cuda.empty_cache()
 
 
 def _gen(seed):
@@ -380,6 +381,32 @@ def test_in_a_graph_and_on_another_stream(hkv):
         d = hkv.adapter_matmul_backward(s, c.dy, base=c.dx_base, stream=stream)
         side.synchronize()
         assert torch.equal(s.out, g.out) and all(torch.equal(u, v) for u, v in zip(d, want))
+
+
+@pytest.mark.parametrize("k,n", [(512, 384), (511, 385)])
+def test_rows_alone_in_a_graph(hkv, k, n):
+    """Replayed with other adapters: the idle ones' zeros follow which adapters these are."""
+    c = Case(BF16, k, n, 16, [1] * 9, [i % 3 for i in range(9)], count=40, before=1, behind=2)
+    other = Case(BF16, k, n, 16, [1] * 9, [39, -1, 7, 7, 0, 12, 39, 5, -1], count=40, before=1, behind=2, seed=40)
+    hkv.adapter_matmul_backward(c.call(hkv), c.dy)
+    graph = torch.cuda.CUDAGraph()
+    torch.cuda.synchronize()
+    with torch.cuda.graph(graph):
+        f = c.call(hkv)
+        got = hkv.adapter_matmul_backward(f, c.dy, base=c.dx_base)
+    for name in ("x", "down", "up", "scales", "base", "dy", "dx_base", "offsets", "which"):
+        getattr(c, name).copy_(getattr(other, name))
+    for _ in range(2):
+        graph.replay()
+    torch.cuda.synchronize()
+    want = plain(c.x, c.down, c.up, c.offsets, c.which, c.scales, c.base, c.dy, c.dx_base)
+    for v, name in zip((f.out, *got), ("out", "dx", "ddown", "dup")):
+        near(v, *want[name], name)
+    side = torch.cuda.Stream()
+    g = c.call(hkv, stream=side)
+    d = hkv.adapter_matmul_backward(g, c.dy, base=c.dx_base, stream=side)
+    side.synchronize()
+    assert torch.equal(g.out, f.out) and all(torch.equal(u, v) for u, v in zip(got, d))
 
 
 def test_two_calls_at_once(hkv):
