@@ -118,8 +118,12 @@ cudaError_t chain_of(const Chain<T>& a, cudaStream_t st) {
   // 512 requests of 2 rows 21 and 30 (19 and 35), of 4 39 and 30 (32 and 35), of 6 58 and 31;
   // by rank 64 128 of 1 row 25 and 40 (19 and 39), of 4 47 and 31, 512 of 2 81 and 78 (84 and
   // 76; float32 150 and 184).  Rows that start anywhere, 450 rows of 5437 to 2437 by rank 8: 23
-  // and 93.
-  if (tokens <= (kRank == 16 ? 4 : 2) * requests || (kRank * tokens <= 16384 && kRank * tokens <= 128 * requests)) {
+  // and 93.  Up to eight ranks, whose tiles are half empty, 300 requests of 8 rows, 512 to 8192
+  // 60 and 68 us (float32 81 and 132), of 12 120 and 71 (126 and 152), but 512 of 6 rows, 2048
+  // to 2048, 43 and 33 (backward 35 and 39).
+  const bool half_empty = a.rank <= 8 && (sizeof(T) == 4 || kBack || a.out >= 4 * a.in);
+  const uint64_t most = kRank > 16 ? 2 : half_empty ? 8 : 4;
+  if (tokens <= most * requests || (kRank * tokens <= 16384 && kRank * tokens <= 128 * requests)) {
     if constexpr (kRank == 16)
       if (a.rank <= 8) return launch_thin<T, kRank, 8, kBack>(a, st);
     return launch_thin<T, kRank, kRank, kBack>(a, st);

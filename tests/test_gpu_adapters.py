@@ -225,6 +225,15 @@ def test_rows_alone(hkv, k, n, rank, dtype):
     Case(dtype, k, n, rank, [2, 0, 3, 1, 2], [1, 0, -1, 1, 2], seed=n + rank).check(hkv)
 
 
+@pytest.mark.parametrize("k,n", [(64, 260), (37, 1100), (130, 130)])
+@pytest.mark.parametrize("rank", [2, 8, 9])
+@pytest.mark.parametrize("dtype", TYPES)
+def test_more_rows_alone_than_tiles_take(hkv, k, n, rank, dtype):
+    """Eight rows to a request and nine, of more requests than a small call's."""
+    for length in (4, 5, 8, 9):
+        Case(dtype, k, n, rank, [length] * 260, [i * 7 % 5 - 1 for i in range(260)], count=4, behind=1, seed=length).check(hkv)
+
+
 @pytest.mark.parametrize("k,n", [(264, 520), (261, 77)])
 @pytest.mark.parametrize("rank", [5, 24, 64])
 @pytest.mark.parametrize("dtype", TYPES)
