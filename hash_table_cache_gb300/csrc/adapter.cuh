@@ -11,7 +11,8 @@
 // memory in a fixed order) and the second (onto base; it starts while the first one
 // ends and has its factor and base on their way by then).  Short requests and single
 // tokens, whose time is that of a launch and of a few latencies, take both in one
-// kernel.  A third has the adapters' gradients.
+// kernel.  A third has the adapters' gradients, in tiles of rows or, where adapters have
+// few of them, in sums of a thread's own.
 //
 // The products are thin: 2 rank operations for each element that is read or
 // written, 16 to 64 where the tensor cores could take 280 and more, so memory is
@@ -32,7 +33,7 @@
 // (8200 rows, 4096 to 8192, rank 32) and 124 where they take 56 (8224 rows, 4096 to 4096,
 // rank 64); single tokens in tiles of 16 rows 38 us, two kernels for them 20, one 12;
 // gradients by request 57 us, across requests 31 (4096 rows in requests of 8, 2048 to
-// 2048, rank 16); ragged x element by element 218 us, shifted 118.
+// 2048, rank 16), of 128 adapters of one row 57 and by thread 13; ragged x element by element 218 us, shifted 118.
 #pragma once
 
 #include <atomic>
@@ -867,8 +868,8 @@ __global__ void __launch_bounds__(kAdapterThreads, blocks_of<T, kRank>())
 }
 
 // ---------------------------------------------------------------------------
-// Single tokens: one row to a cluster, whose products are sums over factors that are
-// read once, past shared memory.  h = c D x: a warp takes two ranks at a time, its
+// Single tokens, and requests of few rows: one row to a cluster, whose products are sums
+// over factors that are read once, past shared memory, wherever their rows start.  h = c D x: a warp takes two ranks at a time, its
 // lanes the columns, eight each; where there are fewer pairs of ranks than warps, the
 // others take other columns.  y = base + U h: a column to a thread at a time.
 // ---------------------------------------------------------------------------
