@@ -33,7 +33,8 @@
 // (8200 rows, 4096 to 8192, rank 32) and 124 where they take 56 (8224 rows, 4096 to 4096,
 // rank 64); single tokens in tiles of 16 rows 38 us, two kernels for them 20, one 12;
 // gradients by request 57 us, across requests 31 (4096 rows in requests of 8, 2048 to
-// 2048, rank 16), of 128 adapters of one row 57 and by thread 13; ragged x element by element 218 us, shifted 118.
+// 2048, rank 16), of 128 adapters of one row 57 and by thread 13; ragged x element by
+// element 218 us, shifted 118.
 #pragma once
 
 #include <atomic>
