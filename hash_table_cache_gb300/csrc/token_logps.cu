@@ -99,20 +99,22 @@ __device__ __forceinline__ Moments join_lanes(Moments r) {
   return r;
 }
 
-// The clamp that keeps a product of 0 and -inf out of w: masks below it have
-// exponential 0 in any case where it is used (a maximum within kFactored).
+// The clamp that keeps products of 0 and an infinity out of w and out of the gradient:
+// masks below it (float16's lowest, for all types) have exponential 0 in any case where
+// it is used (a maximum or a log sum within kFactored).
+constexpr float kLowest = -65504.f;
 template <class T>
 __device__ __forceinline__ void clamp(Chunk<T>& c) {
   if constexpr (sizeof(T) == 4) {
     float* e = reinterpret_cast<float*>(&c.w);
 #pragma unroll
-    for (int i = 0; i < 4; ++i) e[i] = max_nan(e[i], kLeast);
+    for (int i = 0; i < 4; ++i) e[i] = max_nan(e[i], kLowest);
   } else {
     using T2 = std::conditional_t<std::is_same_v<T, __nv_bfloat16>, __nv_bfloat162, __half2>;
     T2* e = reinterpret_cast<T2*>(&c.w);
     T2 least;
-    if constexpr (std::is_same_v<T, __nv_bfloat16>) least = __float2bfloat162_rn(kLeast);
-    else least = __float2half2_rn(-65504.f);
+    if constexpr (std::is_same_v<T, __nv_bfloat16>) least = __float2bfloat162_rn(kLowest);
+    else least = __float2half2_rn(kLowest);
 #pragma unroll
     for (int i = 0; i < 4; ++i) e[i] = __hmax2_nan(e[i], least);
   }
@@ -565,6 +567,9 @@ __device__ __forceinline__ void put_both(__half* e, float a, float b) {
   *reinterpret_cast<__half2*>(e) = __floats2half2_rn(a, b);
 }
 
+// From here on dlogps and dentropy may be too large to meet an exponent before its power.
+constexpr float kSteep = 1e30f;
+
 // A piece of a row for every kLanes threads, rows from the last to the first, so
 // that what the forward call read last is taken from L2 while it is there.
 // kAlike: every row of the gradient lies as the logits' does within 16 bytes.
@@ -593,16 +598,17 @@ __global__ void __launch_bounds__(kLanes == 32 ? kWarpThreads : kThreads, kAlike
     const T* x = logits + t * stride + lo;
     T* d = dlogits + t * dstride + lo;
     const uint64_t n = min(vocab - lo, kPiece);
-    // p (-g - h (log p + H)), and g (1 - p) - h p (log p + H) for the label
+    // -p g - h p (log p + H), and g (1 - p) - h p (log p + H) for the label; p first, so
+    // that no product is larger than the gradient's terms are
     auto value = [&](float v, uint64_t at) {
       const float lp = (v - l) - rest, p = __expf(lp);
-      const float slope = -h * (max_nan(lp, -200.f) + ent);
-      return at == hit ? fmaf(p, slope, g * (1.f - p)) : p * (slope - g);
+      return fmaf(-h, p * (max_nan(lp, -200.f) + ent), at == hit ? g * (1.f - p) : -p * g);
     };
     // The others in pairs: p = 2^(a - off), a = v log2 e - l log2 e by two multiply-adds,
     // off what the rounded l log2 e (the same in every a) and l leave out; then the
-    // entry is 2^a (slope a + level).
-    const bool factored = fabsf(l) < kFactored;
+    // entry is 2^a (slope a + level).  (a is above -120000, so that the bracket is finite
+    // where g and h are below kSteep.)
+    const bool factored = fabsf(l) < kFactored && fabsf(g) < kSteep && fabsf(h) < kSteep;
     const float scaled = l * kLog2e;
     const float off = fmaf(rest, kLog2e, fmaf(l, kLog2eRest, fmaf(l, kLog2e, -scaled)));
     const float back = exp2_of_minus(off);
