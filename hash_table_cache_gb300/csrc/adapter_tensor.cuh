@@ -350,11 +350,13 @@ __global__ void __launch_bounds__(SecondShape<kRank>::kThreads, 3)
         }
       }
       if (has_base) load_box(stage + S::kFactor, &maps.base, c, static_cast<int>(t.row0), &full[s]);
-      if (adapts && (step + 1 == S::kStages || (step + 1 == steps && steps < S::kStages))) {
-        pdl_wait();  // the first product is done
-        mbar_arrive_expect_tx(&planes, S::kPlanes);
-        load_box(smem, &maps.hidden, 0, static_cast<int>(t.row0), &planes);
-        load_box(smem + S::kPlane, &maps.hidden, kRank, static_cast<int>(t.row0), &planes);
+      if (step + 1 == S::kStages || (step + 1 == steps && steps < S::kStages)) {
+        pdl_wait();  // the first product is done (limited waits begin here, in every role)
+        if (adapts) {
+          mbar_arrive_expect_tx(&planes, S::kPlanes);
+          load_box(smem, &maps.hidden, 0, static_cast<int>(t.row0), &planes);
+          load_box(smem + S::kPlane, &maps.hidden, kRank, static_cast<int>(t.row0), &planes);
+        }
       }
     }
     // before the block ends, the loads still in flight where a wait ran out
@@ -364,6 +366,7 @@ __global__ void __launch_bounds__(SecondShape<kRank>::kThreads, 3)
         if (!wait(&full[i % S::kStages], i / S::kStages & 1)) break;
     }
   } else if (warp == 1 && adapts && steps && elect()) {
+    pdl_wait();
     bool ok = wait(&planes, 0);
     const uint32_t units = (smem_u32(smem) & 0x3FFFF) >> 4, factors = (smem_u32(stages) & 0x3FFFF) >> 4;
     constexpr uint32_t kIdesc = 1u << 4 | 1u << 7 | 1u << 10 | (kBack ? 1u : 0u) << 15 | (uint32_t)(S::kTile >> 3) << 17 | (128u >> 4) << 24;
