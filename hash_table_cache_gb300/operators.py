@@ -14,7 +14,9 @@ caller's back) and ``HKVError`` for a status of the library.  ``stream``
 (default: the current stream of the tensors' device) is the stream the
 kernels run on and the one that results are allocated on.  Work on other
 streams that the call depends on is the caller's to order, as with any CUDA
-call; tensors passed with a ``stream`` may be dropped right after the call.
+call; tensors passed with a ``stream`` may be dropped right after the call, and
+so may a call's result after another one that takes it, on any stream (what such
+a result keeps for later calls is not a tensor of the caller's).
 
 The operators are outside autograd: a result carries no gradient function,
 also where an input requires a gradient (the backward passes are calls of
@@ -121,6 +123,15 @@ def _tensors(args):
             yield from (t for t in (a.logits, a.labels, a.entropy, a._lse) if t is not None)
 
 
+def _keep(s, f, *tensors):
+    """`tensors` are f's own, allocated on the stream f._stream: where this call runs on
+    another one, their memory is not used again before it is done."""
+    if f._stream is not None and s != f._stream:
+        now = torch.cuda.current_stream(tensors[0].device)
+        for t in tensors:
+            t.record_stream(now)
+
+
 # For tensors of the caller's that a kernel has written: autograd counts what it
 # sees written, and would otherwise use one that it had saved as if unchanged.
 _written = torch.autograd.graph.increment_version
@@ -140,7 +151,7 @@ class MXMatrix:
     """A 4-bit microscaled matrix (MXFP4) of ``rows`` x ``cols``: ``codes`` and
     ``scales`` are uint8 tensors in the layout of ``include/hkv.h``."""
 
-    __slots__ = ("rows", "cols", "device", "_codes", "_scales", "_base", "_at")
+    __slots__ = ("rows", "cols", "device", "_codes", "_scales", "_base", "_at", "_stream")
 
     def __init__(self, codes, scales, rows, cols):
         rows, cols = int(rows), int(cols)
@@ -152,10 +163,11 @@ class MXMatrix:
                 raise ValueError(f"{what}: {n} contiguous bytes for {rows} x {cols}")
         self.rows, self.cols = rows, cols
         self._codes, self._scales, self._base = codes, scales, None
+        self._stream = None  # the caller's tensors
         self._at = codes.data_ptr(), scales.data_ptr()
 
     @classmethod
-    def _empty(cls, rows, cols, device):
+    def _empty(cls, rows, cols, device, s):
         """A matrix to be written, codes and scales in one allocation of its own:
         of two copies from one call either may be kept without the other."""
         m = cls.__new__(cls)
@@ -167,6 +179,7 @@ class MXMatrix:
         m._codes = m._scales = None
         m._base = base, codes
         m._at = at, at + codes
+        m._stream = s
         return m
 
     def _piece(self, skip, size, shape):
@@ -206,6 +219,8 @@ def _dequantize(s, q, dtype, out):
     if rows != q.rows or cols != q.cols:
         raise ValueError(f"out: {q.rows} x {q.cols}")
     _same(out, q.device, "out")
+    if s != q._stream:
+        _keep(s, q, *_tensors((q,)))
     codes, scales = q._at
     _ok(_abi.load().hkv_mx_dequantize(rows, cols, codes, scales, out.data_ptr(), kind, stride, s),
         "hkv_mx_dequantize")
@@ -229,10 +244,10 @@ def _quantize(s, x, along):
     device = x.device
     codes = scales = codes_t = scales_t = None
     if along != "columns":
-        q = MXMatrix._empty(rows, cols, device)
+        q = MXMatrix._empty(rows, cols, device, s)
         codes, scales = q._at
     if along != "rows":
-        q_t = MXMatrix._empty(cols, rows, device)
+        q_t = MXMatrix._empty(cols, rows, device, s)
         codes_t, scales_t = q_t._at
     _ok(_abi.load().hkv_mx_quantize(rows, cols, x.data_ptr(), kind, stride, codes, scales, codes_t,
                                     scales_t, s), "hkv_mx_quantize")
@@ -261,6 +276,9 @@ def _matmul(s, a, b, dtype, out):
         if rows != m or cols != n:
             raise ValueError(f"out: {m} x {n}")
         _same(out, a.device, "out")
+    if s != a._stream or s != b._stream:
+        _keep(s, a, *_tensors((a,)))
+        _keep(s, b, *_tensors((b,)))
     at, bt = a._at, b._at
     _ok(_abi.load().hkv_mx_matmul(m, n, a.cols, at[0], at[1], bt[0], bt[1], out.data_ptr(), kind,
                                   stride, s), "hkv_mx_matmul")
@@ -273,7 +291,7 @@ class PreferenceLoss:
     """What ``preference_loss`` returns: ``losses`` [pairs], ``ratios`` [2 * pairs],
     ``logps`` [tokens], and what the backward call needs."""
 
-    __slots__ = ("losses", "ratios", "logps", "logits", "labels", "_saved")
+    __slots__ = ("losses", "ratios", "logps", "logits", "labels", "_saved", "_stream")
 
 
 def preference_loss(logits, labels, offsets, ref_logps=None, beta=0.1, label_smoothing=0.0,
@@ -301,7 +319,7 @@ def _loss(s, logits, labels, offsets, ref_logps, beta, label_smoothing, average)
     if ref_logps is not None:
         _vector(ref_logps, rows, torch.float32, "ref_logps", device)
     f = PreferenceLoss()
-    f.logits, f.labels = logits, labels
+    f.logits, f.labels, f._stream = logits, labels, s
     # what a caller may keep longer than the rest (the losses of every step, a
     # reference's logps) has memory of its own
     base = torch.empty(3 * pairs, dtype=torch.float32, device=device)
@@ -341,6 +359,7 @@ def _loss_backward(s, loss, dlosses, out):
             raise ValueError(f"out: {rows} x {vocab} of {logits.dtype}")
         _same(out, device, "out")
         dstride = _matrix(out, "out")[2]
+    _keep(s, loss, loss._saved)
     saved = loss._saved.data_ptr()
     _ok(_abi.load().hkv_preference_loss_backward(
         pairs, rows, vocab, logits.data_ptr(), _TYPES[logits.dtype], stride, loss.labels.data_ptr(),
@@ -356,7 +375,7 @@ class TokenLogps:
     ``entropy`` [tokens], ``top_logps`` and int64 ``top_ids`` [tokens, top] (None where
     ``top`` is 0), and what the backward call needs."""
 
-    __slots__ = ("logps", "entropy", "top_logps", "top_ids", "logits", "labels", "_lse")
+    __slots__ = ("logps", "entropy", "top_logps", "top_ids", "logits", "labels", "_lse", "_stream")
 
 
 def token_logps(logits, labels=None, top=0, stream=None):
@@ -378,7 +397,7 @@ def _token_logps(s, logits, labels, top):
         raise ValueError(f"top: 0 to {min(vocab, _abi.MAX_TOP)}, not {top}")
     empty, f32 = torch.empty, torch.float32
     f = TokenLogps()
-    f.logits, f.labels = logits, labels
+    f.logits, f.labels, f._stream = logits, labels, s
     f.entropy = entropy = empty(rows, dtype=f32, device=device)
     f._lse = lse = empty(2 * rows, dtype=f32, device=device)
     f.logps = f.top_logps = f.top_ids = at_labels = at_logps = at_top = at_ids = None
@@ -422,6 +441,7 @@ def _token_logps_backward(s, f, dlogps, dentropy, out):
             raise ValueError(f"out: {rows} x {vocab} of {logits.dtype}")
         _same(out, device, "out")
         dstride = _matrix(out, "out")[2]
+    _keep(s, f, f._lse, f.entropy)
     at = [None if t is None else t.data_ptr() for t in (f.labels, dlogps, dentropy)]
     _ok(_abi.load().hkv_token_logps_backward(
         rows, vocab, logits.data_ptr(), _TYPES[logits.dtype], stride, at[0], f._lse.data_ptr(),
@@ -435,7 +455,8 @@ class AdapterMatmul:
     """What ``adapter_matmul`` returns: ``out`` [tokens, n], and what the backward call
     needs."""
 
-    __slots__ = ("out", "x", "down", "up", "offsets", "which", "scales", "_adapters", "_shape", "_hidden")
+    __slots__ = ("out", "x", "down", "up", "offsets", "which", "scales", "_adapters", "_shape", "_hidden",
+                 "_stream")
 
 
 def adapter_matmul(x, down, up, offsets, which, scales=None, base=None, out=None, stream=None):
@@ -517,6 +538,7 @@ def _adapter_matmul(s, x, down, up, offsets, which, scales, base, out):
     f._adapters = adapters = array("Q", (count, down.data_ptr(), down_step, down_stride, up.data_ptr(),
                                          up_step, up_stride, at_scales or 0, rank))
     f._shape = tokens, k, n, kind, x_stride, requests, count, rank
+    f._stream = s
     _ok(_abi.load().hkv_adapter_matmul(
         tokens, k, n, kind, adapters.buffer_info()[0], requests, offsets.data_ptr(), which.data_ptr(),
         x.data_ptr(), x_stride, at_base, base_stride, out.data_ptr(), stride, hidden.data_ptr(), s),
@@ -554,6 +576,7 @@ def _adapter_matmul_backward(s, f, dout, base, out):
     ddown = torch.empty((count, rank, k), dtype=dtype, device=device)
     dup = torch.empty((count, n, rank), dtype=dtype, device=device)
     dhidden = torch.empty_like(f._hidden)
+    _keep(s, f, f._hidden)
     _ok(_abi.load().hkv_adapter_matmul_backward(
         tokens, k, n, kind, adapters.buffer_info()[0], requests, f.offsets.data_ptr(), f.which.data_ptr(),
         x.data_ptr(), x_stride, dout.data_ptr(), d_stride, f._hidden.data_ptr(), at_base, base_stride,
