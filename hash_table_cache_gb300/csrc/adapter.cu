@@ -82,7 +82,7 @@ hkv_status hkv_adapter_matmul(uint64_t tokens, uint64_t k, uint64_t n, int type,
   if ((tokens && !hidden) || !aligned(hidden, 16)) return HKV_ERR_INVALID;
   if (meet(my, mx) || (meet(my, mb) && !same(my, mb))) return HKV_ERR_INVALID;
   if (tokens == 0) return HKV_OK;
-  const Requests q{tokens, requests, adapters->count, offsets, which, adapters->scales, false};
+  const Requests q{tokens, requests, adapters->count, offsets, which, adapters->scales};
   return op_status(run(false, type, q, *adapters, mx, mb, my, hidden, static_cast<cudaStream_t>(stream)));
 }
 
@@ -107,7 +107,7 @@ hkv_status hkv_adapter_matmul_backward(uint64_t tokens, uint64_t k, uint64_t n, 
     return HKV_ERR_INVALID;
   if (meet(mdx, mx) || meet(mdx, md) || (meet(mdx, mb) && !same(mdx, mb))) return HKV_ERR_INVALID;
   cudaStream_t st = static_cast<cudaStream_t>(stream);
-  const Requests q{tokens, requests, adapters->count, offsets, which, adapters->scales, false};
+  const Requests q{tokens, requests, adapters->count, offsets, which, adapters->scales};
   cudaError_t e = cudaSuccess;
   if (tokens) e = run(true, type, q, *adapters, md, mb, mdx, dhidden, st);
   if (e == cudaSuccess && adapters->count && (ddown || dup))

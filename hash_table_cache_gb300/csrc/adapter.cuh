@@ -68,7 +68,6 @@ struct Requests {
   uint64_t tokens, requests, adapters;
   const int64_t *offsets, *which;
   const float* scales;
-  bool by_rows;  // as many slots of tiles as rows: where requests are more than rows
   // First row of segment s: the rows before the first request are segment 0, the
   // requests 1 .. requests, the rows behind the last one requests + 1.
   __device__ __forceinline__ uint64_t start(uint64_t s) const {
@@ -88,14 +87,14 @@ struct Requests {
 // The rows of a block's tile.  Segment s has the slots start(s) / kTile + s up to
 // start(s + 1) / kTile + s + 1, at least as many as it has tiles of kTile rows, so
 // that a block finds its rows by one search and no list of tiles has to be made.
-// (Tiles of one row, or by_rows: as many slots as rows, a tile's is its first row.)
+// (Tiles of one row: as many slots as rows, which need no request's number.)
 struct Tile {
   uint64_t row0;
   int rows;
   int64_t adapter;
   template <int kTile>
-  static __device__ __forceinline__ uint64_t first_slot(const Requests& q, uint64_t start, uint64_t seg) {
-    return kTile == 1 || q.by_rows ? start : start / kTile + seg;
+  static __device__ __forceinline__ uint64_t first_slot(uint64_t start, uint64_t seg) {
+    return kTile == 1 ? start : start / kTile + seg;
   }
   // False where the slot has none.  All threads of a warp call it.
   template <int kTile>
@@ -104,7 +103,7 @@ struct Tile {
     uint64_t lo = 0, hi = q.requests + 2;  // the segment is one of lo .. hi - 1
     while (hi - lo > 31) {  // every turn leaves a thirty-second part
       const uint64_t step = (hi - lo + 31) / 32, at = lo + (lane + 1) * step;
-      const bool before = at < hi && first_slot<kTile>(q, q.start(at), at) <= slot;
+      const bool before = at < hi && first_slot<kTile>(q.start(at), at) <= slot;
       const uint64_t n = __popc(__ballot_sync(0xFFFFFFFFu, before));
       lo += n * step;
       hi = min(lo + step, hi);
@@ -112,13 +111,12 @@ struct Tile {
     // the last ones all at once, with the next one's start and their adapters
     const uint64_t at = lo + lane, start = at <= hi ? q.start(at) : 0;
     const int64_t mine = at < hi ? q.adapter(at) : -1;
-    const uint32_t before = __ballot_sync(0xFFFFFFFFu, at < hi && first_slot<kTile>(q, start, at) <= slot);
+    const uint32_t before = __ballot_sync(0xFFFFFFFFu, at < hi && first_slot<kTile>(start, at) <= slot);
     const int seg = max(__popc(before) - 1, 0);
     const uint64_t from = __shfl_sync(0xFFFFFFFFu, start, seg), to = __shfl_sync(0xFFFFFFFFu, start, seg + 1);
     t.adapter = __shfl_sync(0xFFFFFFFFu, mine, seg);
-    const uint64_t ahead = slot - first_slot<kTile>(q, from, lo + seg);
-    if (q.by_rows && ahead % kTile) return false;
-    t.row0 = from + ahead * (q.by_rows ? 1 : kTile);
+    const uint64_t ahead = slot - first_slot<kTile>(from, lo + seg);
+    t.row0 = from + ahead * kTile;
     if (t.row0 < from || t.row0 >= to) return false;
     t.rows = static_cast<int>(min(to - t.row0, static_cast<uint64_t>(kTile)));
     return true;

@@ -25,7 +25,7 @@ cudaError_t launch_long(Chain<T> a, cudaStream_t st) {
   using F = FirstShape<T, kRank, kTile, kBack>;
   using S = SecondShape<T, kRank, kTile, kBack>;
   const uint64_t slots = slots_of(a.q.tokens, a.q.requests, kTile);
-  const uint64_t tiles = a.q.tokens / kTile + (a.q.requests < a.q.tokens ? a.q.requests : a.q.tokens) + 1;
+  const uint64_t tiles = a.q.tokens / kTile + a.q.requests + 1;
   a.follows = a.q.requests > 0 && a.q.adapters > 0;  // else all rows are base's
   if (a.follows) {
     bool by_tensor = false;
@@ -132,11 +132,9 @@ cudaError_t chain_of(const Chain<T>& a, cudaStream_t st) {
   // 341 requests of 12 30.0 and 33.9 us, 256 of 16 29.7 and 32.3, 204 of 20 29.2 and 28.0, 128
   // of 32 29.4 and 27.2; 170 of 12, 1024 to 1024 by rank 64, 27.0 and 22.1.
   if (tokens < 20 * requests) {
-    Chain<T> b = a;
-    b.q.by_rows = requests > tokens;
-    return launch_few<short_kernel<T, kRank, kBack>>(
-        b, slots_of(tokens, requests, b.q.by_rows ? 1 : 16), tokens / 16 + (requests < tokens ? requests : tokens) + 1,
-        SecondShape<T, kRank, 16, kBack>::kCols, false, ShortShape<T, kRank, kBack>::kBytes, st);
+    return launch_few<short_kernel<T, kRank, kBack>>(a, slots_of(tokens, requests, 16), tokens / 16 + requests + 1,
+                                                     SecondShape<T, kRank, 16, kBack>::kCols, false,
+                                                     ShortShape<T, kRank, kBack>::kBytes, st);
   }
   return launch_long<T, kRank, kBack>(a, st);
 }
