@@ -23,7 +23,7 @@
 // matrices); what has more digits is split into two or three bfloat16 numbers
 // (planes), whose products are added in float32:
 //   float32 = three planes exactly, products of planes i + j <= 2 (what is left
-//   out is below 2^-22 of a term); float16 = two planes exactly; h and dh, sums in
+//   out is at most 2^-21 of a term); float16 = two planes exactly; h and dh, sums in
 //   float32, in two planes where matrices have 16 bits (below 2^-16 of it is left
 //   out, where a result is rounded to 2^-8 or 2^-11), in three where they have 32.
 // Tiles come by asynchronous copies as they lie in memory (rows that start anywhere
