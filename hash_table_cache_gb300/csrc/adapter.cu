@@ -12,6 +12,17 @@ bool matrix_ok(const Matrix& m) {
 }
 bool whole(const Matrix& m) { return aligned(m.p, 16) && m.stride * m.size % 16 == 0; }
 bool same(const Matrix& a, const Matrix& b) { return a.p == b.p && a.stride == b.stride; }
+// What a call writes without gaps: h or dh of all rows, and the gradient of `rows` x `cols`
+// matrices of all adapters (more than any memory where the bytes pass 64 bits).
+Matrix hidden_run(const void* p, uint64_t tokens, uint32_t rank, int type) {
+  return run_of(p, HKV_ADAPTER_HIDDEN_BYTES(tokens, rank, type));
+}
+Matrix grad_run(const void* p, const hkv_adapters& w, uint64_t cols, size_t size) {
+  const uint64_t rows = p ? w.count * w.rank : 0, most = 1ull << 60;
+  return run_of(p, rows && cols * size > most / rows ? most : rows * cols * size);
+}
+template <class... M>
+bool run_meets_any(const Matrix& run, const M&... others) { return (run_meets(run, others) || ...); }
 
 bool requests_ok(uint64_t tokens, uint64_t requests, const int64_t* offsets, const int64_t* which) {
   return tokens <= HKV_MAX_BATCH && requests <= HKV_MAX_BATCH &&
@@ -81,6 +92,7 @@ hkv_status hkv_adapter_matmul(uint64_t tokens, uint64_t k, uint64_t n, int type,
   if (!matrix_ok(mx) || !matrix_ok(my) || !matrix_ok(mb)) return HKV_ERR_INVALID;
   if ((tokens && !hidden) || !aligned(hidden, 16)) return HKV_ERR_INVALID;
   if (meet(my, mx) || (meet(my, mb) && !same(my, mb))) return HKV_ERR_INVALID;
+  if (run_meets_any(hidden_run(hidden, tokens, adapters->rank, type), mx, mb, my)) return HKV_ERR_INVALID;
   if (tokens == 0) return HKV_OK;
   const Requests q{tokens, requests, adapters->count, offsets, which, adapters->scales};
   return op_status(run(false, type, q, *adapters, mx, mb, my, hidden, static_cast<cudaStream_t>(stream)));
@@ -106,6 +118,11 @@ hkv_status hkv_adapter_matmul_backward(uint64_t tokens, uint64_t k, uint64_t n, 
   if (!aligned(hidden, 16) || !aligned(dhidden, 16) || !aligned(ddown, size) || !aligned(dup, size))
     return HKV_ERR_INVALID;
   if (meet(mdx, mx) || meet(mdx, md) || (meet(mdx, mb) && !same(mdx, mb))) return HKV_ERR_INVALID;
+  const Matrix rh = hidden_run(hidden, tokens, adapters->rank, type), rdh = hidden_run(dhidden, tokens, adapters->rank, type);
+  const Matrix rd = grad_run(ddown, *adapters, k, size), ru = grad_run(dup, *adapters, n, size);
+  if (run_meets(rh, mdx) || run_meets_any(rdh, mx, md, mb, mdx, rh) || run_meets_any(rd, mx, md, mb, mdx, rh, rdh) ||
+      run_meets_any(ru, mx, md, mb, mdx, rh, rdh, rd))
+    return HKV_ERR_INVALID;
   cudaStream_t st = static_cast<cudaStream_t>(stream);
   const Requests q{tokens, requests, adapters->count, offsets, which, adapters->scales};
   cudaError_t e = cudaSuccess;

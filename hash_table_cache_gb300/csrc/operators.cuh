@@ -43,6 +43,16 @@ inline bool meet(const Matrix& a, const Matrix& b) {
   return at < lo.cols * a.size || at + hi.cols * a.size > row;
 }
 
+// Bytes one after the other, and whether they may hold elements of `b`: between two of
+// its rows they do not.
+inline Matrix run_of(const void* p, uint64_t bytes) { return {p, bytes ? 1u : 0u, bytes, bytes, 1}; }
+inline bool run_meets(const Matrix& run, const Matrix& b) {
+  if (!run.rows || !b.rows || run.end() <= b.begin() || b.end() <= run.begin()) return false;
+  if (run.begin() < b.begin() || b.rows == 1) return true;
+  const uint64_t row = b.stride * b.size, at = (run.begin() - b.begin()) % row;
+  return at < b.cols * b.size || at + run.cols > row;
+}
+
 // Call f with a null pointer of the element type `type` stands for.
 template <class F>
 auto with_type(int type, F&& f) {

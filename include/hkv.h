@@ -487,10 +487,10 @@ typedef struct hkv_adapters {
  * with sums in float32 and y rounded once.  base (NULL: zeros) may be y itself,
  * with the same stride.  Rows of no request, and of one whose which[s] lies
  * outside 0 .. count - 1, have y[t] = base[t]; where y is base they are left as
- * they are.  y must not overlap base otherwise, nor x (columns of one buffer side
- * by side do not).  hidden (device memory of HKV_ADAPTER_HIDDEN_BYTES, 16-byte
- * aligned) gets h for the backward call; of h, 16 digits go on for 16-bit
- * matrices, 24 for float32.  A row with an infinity in it may give NaN where the
+ * they are.  y must not overlap base otherwise, nor x, the adapters or the requests
+ * (columns of one buffer side by side do not).  hidden (device memory of
+ * HKV_ADAPTER_HIDDEN_BYTES, 16-byte aligned, which overlaps nothing else) gets h for
+ * the backward call; of h, 16 digits go on for 16-bit matrices, 24 for float32.  A row with an infinity in it may give NaN where the
  * formula gives an infinity.  `adapters` is read before the call returns. */
 #define HKV_ADAPTER_HIDDEN_BYTES(tokens, rank, type) \
   ((uint64_t)(tokens) * ((rank) <= 16 ? 16 : (rank) <= 32 ? 32 : 64) * ((type) == HKV_F32 ? 6 : 4))
@@ -506,8 +506,9 @@ hkv_status hkv_adapter_matmul(uint64_t tokens, uint64_t k, uint64_t n, int type,
  *   dup[a]   = sum of dy[t] h[t]^T
  * (base, tokens x k: as above).  ddown (count x rank x k) and dup (count x n x
  * rank) are contiguous, in the matrices' type, rounded once, and zero for an
- * adapter of no request; either may be NULL.  dhidden is scratch like hidden.  dx
- * must not overlap x or dy, nor base unless it is base. */
+ * adapter of no request; either may be NULL.  dhidden is scratch like hidden, of its
+ * own.  dx must not overlap x or dy, nor base unless it is base; ddown, dup and dhidden
+ * must not overlap one another or anything else. */
 hkv_status hkv_adapter_matmul_backward(uint64_t tokens, uint64_t k, uint64_t n, int type,
                                        const hkv_adapters* adapters, uint64_t requests,
                                        const int64_t* offsets, const int64_t* which, const void* x,
