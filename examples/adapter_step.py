@@ -31,7 +31,8 @@ def split(rows, rank, k, n):
 
 
 def step(table, users, x, offsets, labels, advantages, weight, rank, bonus=0.01, max_norm=1.0, lr=0.5, top=3):
-    """One step of the requests of `users`; returns what it has computed."""
+    """One step of the requests of `users` (each once: an adapter is written back by its
+    request); returns what it has computed."""
     tokens, k = x.shape
     n = weight.rows
     rows, found, _ = table.find(users)

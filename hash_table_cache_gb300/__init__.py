@@ -16,7 +16,8 @@ Two layers:
 
 The operators on looked-up rows (4-bit microscaled copies and their product,
 the preference loss and its gradient, token log probabilities and theirs,
-low-rank adapters and theirs, gradient clipping) have the same two layers: ``hkv_mx_quantize`` / ... here and ``mx_quantize`` / ... on tensors in
+low-rank adapters and theirs, gradient clipping) have the same two layers:
+``hkv_mx_quantize`` / ... here and ``mx_quantize`` / ... on tensors in
 ``hash_table_cache_gb300.operators``, exported here too.
 
 Semantics follow "HierarchicalKV: A GPU Hash Table with Cache Semantics for
@@ -522,8 +523,8 @@ class HashTable:
 # The operators work on torch tensors, and this module is of use without torch
 # (and is imported in 10 ms, not in seconds): they are imported when first named.
 _OPERATORS = ("AdapterMatmul", "MXMatrix", "PreferenceLoss", "TokenLogps", "adapter_matmul",
-              "adapter_matmul_backward", "clip_grad_norm", "mx_matmul", "mx_quantize", "preference_loss", "preference_loss_backward", "token_logps",
-              "token_logps_backward")
+              "adapter_matmul_backward", "clip_grad_norm", "mx_matmul", "mx_quantize",
+              "preference_loss", "preference_loss_backward", "token_logps", "token_logps_backward")
 
 
 def __getattr__(name):

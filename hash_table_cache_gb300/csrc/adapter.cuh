@@ -26,11 +26,18 @@
 //   out is at most 2^-21 of a term); float16 = two planes exactly; h and dh, sums in
 //   float32, in two planes where matrices have 16 bits (below 2^-16 of it is left
 //   out, where a result is rounded to 2^-8 or 2^-11), in three where they have 32.
+// Two planes are 16 of a sum's 24 digits, for a third less to read, to hold and to multiply
+// wherever h and dh are used.  (7935 rows by rank 64, 4096 to 4096, bfloat16: h is off by
+// 5.3e-6 of itself against 64 bits, 4.9e-6 of it by the planes, a product in 32 bits by
+// 2.0e-7.  One output in 600, and one number of the gradients in 200, is the neighbouring
+// bfloat16 number of what h in 32 bits gives; against 64 bits both are off by 1.57e-3 and
+// 1.66e-3, bfloat16's own.)  Single rows have h in 32 bits for y and dh for dx, and hand on
+// the planes to the gradients.
 // Tiles come by asynchronous copies as they lie in memory (rows that start anywhere
 // by the 16-byte pieces around them, shifted), and are split on the way to the tensor
 // core.  Times: adapter_launch.cuh.  What they were with fewer of these: both products
 // of long requests in one kernel of register-staged tiles 205 us where the two take 67
-// (8200 rows, 4096 to 8192, rank 32) and 124 where they take 56 (8224 rows, 4096 to 4096,
+// (7883 rows, 4096 to 8192, rank 32) and 124 where they take 56 (7935 rows, 4096 to 4096,
 // rank 64); single tokens in tiles of 16 rows 38 us, two kernels for them 20, one 12;
 // gradients by request 57 us, across requests 31 (4096 rows in requests of 8, 2048 to
 // 2048, rank 16), of 128 adapters of one row 57 and by thread 13; ragged x element by

@@ -4,14 +4,29 @@
 // memory, adapters in L2):
 //   one row, 4096 to 4096, rank 16                                4.2 us
 //   256 requests of one row, 64 adapters                          12 us
-//   8200 rows of 24 requests, 4096 to 8192, rank 32               67 us, 5.0 TB/s
-//   1637 rows of 16 requests, 64 to 131072, rank 8               132 us, 6.5 TB/s
-//   8224 rows of 32 requests, 4096 to 4096, rank 64               56 us, 3.6 TB/s
-//     and its backward pass                                       90 us: dx 56, gradients 33
-//   8224 rows as above, float16                                  91 and 203 us (mma.sync but
+//   7883 rows of 24 requests, 4096 to 8192, rank 32               67 us, 4.9 TB/s
+//   1447 rows of 16 requests, 64 to 131072, rank 8               132 us, 6.0 TB/s
+//   7935 rows of 32 requests, 4096 to 4096, rank 64               56 us, 3.5 TB/s
+//     and its backward pass                                       90 us: dx 56, gradients 34
+//   7935 rows as above, float16                                   88 and 203 us (mma.sync but
 //     for the forward call's and the backward call's first product)
-//   and float32                                                 230 and 440 us (six products)
-//   3919 rows of 333 requests, 128 to 128, rank 8, float32        10 and 20 us
+//   and float32                                                 227 and 435 us (six products)
+//   3905 rows of 333 requests, 128 to 128, rank 8, float32        10 and 20 us
+//
+// The lengths and the requests' adapters are on the device, so that the rules know how many
+// rows, requests and adapters there are, and no more: what they say of "rows to a request"
+// and "to an adapter" is the mean, and their figures are of equal lengths.  Uneven batches come
+// out as well, but slower (forward and backward; 2048 to 2048 by rank 16):
+//   a prompt of 500 rows and 255 single rows, by row              23 and 140 us
+//     the two alone                                               10 and 25, 10 and 20
+//   of 8192 rows, 4096 to 4096, in tiles of 64                    70 and 160
+//     the two alone                                               47 and 90, 14 and 33
+//   300 requests of 13 rows by one of 256 adapters                34 and 796
+//     spread over them, or by one of one                          34 and 89, 34 and 88
+//   3800 rows of one of 256 adapters, one of each other           33 and 812
+// Every block of the gradients reads all requests' adapters: an adapter each for 333, 1024,
+// 8192 and 32768 requests of a row, 128 to 128 by rank 8, float32, takes 15, 37, 992 and
+// 14085 us backward.
 #pragma once
 
 #include "adapter_tensor.cuh"
@@ -37,8 +52,8 @@ cudaError_t launch_long(Chain<T> a, cudaStream_t st) {
     }
     // Clusters share a tile's columns, 512 to a block at least, while all blocks are on
     // the SMs at once (estimated by shared memory, and from the tiles that the requests
-    // can have).  Half and twice as many blocks: 8224 rows by rank 64 with the second
-    // product 66 and 65 us against 61, 8200 rows by rank 32 73 and 74 against 70.  Float32,
+    // can have).  Half and twice as many blocks: 7935 rows by rank 64 with the second
+    // product 66 and 65 us against 61, 7883 rows by rank 32 73 and 74 against 70.  Float32,
     // whose products are most of the time, twice as many: by rank 64 227 us against 340.
     const uint64_t room = (sizeof(T) == 4 ? 2 : 1) * sm_count() * (227ull * 1024 / (bytes + 1024));
     a.parts = 1;
@@ -52,7 +67,7 @@ cudaError_t launch_long(Chain<T> a, cudaStream_t st) {
                                                                         tensor::Shape<kRank>::kThreads, bytes, st, maps, a);
     if (e != cudaSuccess) return e;
   }
-  // Eight blocks for every SM, of up to 16 stages of columns.  Four and twelve: 8224 rows
+  // Eight blocks for every SM, of up to 16 stages of columns.  Four and twelve: 7935 rows
   // by rank 64 59 and 62 us against 56.
   const uint64_t steps = (a.out + S::kCols - 1) / S::kCols, blocks = 8ull * sm_count();
   const uint64_t each = (tiles * steps + blocks - 1) / blocks > 16 ? 16 : (tiles * steps + blocks - 1) / blocks;
@@ -172,7 +187,7 @@ cudaError_t launch_grads(Grads<T> a, cudaStream_t st) {
   const uint64_t blocks = places * (a.blocks[0] + a.blocks[1]);
   if (!blocks) return cudaSuccess;
   // Clusters share an adapter's rows, two tiles to a block at least, up to two blocks for
-  // an SM (8224 rows, 4 adapters of rank 64 and 4096 to 4096: 33 us; one 45, four 46).  Of
+  // an SM (7935 rows, 4 adapters of rank 64 and 4096 to 4096: 33 us; one 45, four 46).  Of
   // sixteen blocks: 17000 rows of one adapter of rank 43, 480 to 721, 83 us and of eight 122.
   a.parts = 1;
   while (a.parts < kGradParts && blocks * a.parts < 2ull * sm_count() && a.q.tokens >= 128ull * a.parts) a.parts *= 2;

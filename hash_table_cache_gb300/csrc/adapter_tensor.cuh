@@ -9,9 +9,9 @@
 // multiplied with is whatever lies behind x in shared memory, and they are not read.
 //
 // The loads are the bound (x from memory, the factor from L2), and this way they cost
-// no instructions of the warps.  Kernels alone, cold, 8224 rows of 4096 to 4096 by rank
-// 64 bfloat16, here and with asynchronous copies and mma.sync: first product 19 us (3.5
-// TB/s of x; 35), second 38 us (3.5 TB/s of base and y; 42), gradients 38 us (3.5 TB/s of x
+// no instructions of the warps.  Kernels alone, cold, 7935 rows of 4096 to 4096 by rank
+// 64 bfloat16, here and with asynchronous copies and mma.sync: first product 19 us (3.4
+// TB/s of x; 35), second 38 us (3.4 TB/s of base and y; 42), gradients 38 us (3.4 TB/s of x
 // and dy; 73).  Half of a first product's time is its start and end: a block's search,
 // its first loads, and the joining of the sums.
 #pragma once
@@ -260,7 +260,7 @@ __global__ void __launch_bounds__(Shape<kRank>::kThreads)
 // One thread loads (the factor's columns, base, and the planes once the first product is
 // done), one multiplies, eight warps add onto base.  What bounds it is those warps'
 // instructions (14 for an element) and how much base is on its way, which shared memory
-// holds: 1637 rows to 131072 columns by rank 8 131 us, 73% of the memory's cycles; 8200
+// holds: 1447 rows to 131072 columns by rank 8 131 us, 73% of the memory's cycles; 7883
 // rows to 8192 by rank 32 50 us.  Tried: four warps 68 us with the first product against
 // 67; a third stage of rank 32 instead of a third block 77; sums put together in shared
 // memory and stored 16 bytes at a time 75.

@@ -24,7 +24,8 @@ constexpr float kLog2e = 1.44269504f, kLog2eRest = 1.92596299e-8f;
 // grows with the maximum (a mask such as -1e10 where a thread has met nothing
 // else), past 127 from 2e9 on, where one factor would be infinite and the other 0.
 constexpr float kFactored = 16384.f;
-// 2^-x for |x| below 0.0013
+// 2^-x for |x| below 0.002 (the gradient of token_logps.cu has in x what a float leaves
+// out of the log sum as well, up to 0.0007): three terms, and below 4.5e-10 left out
 __device__ __forceinline__ float exp2_of_minus(float x) {
   return fmaf(x * x, 0.240226507f, fmaf(-x, 0.693147181f, 1.f));
 }

@@ -22,12 +22,12 @@
 // Times (GB300, CUDA graph replays): 4096 x 131072 bfloat16, a tenth of the tokens
 // hidden, with 20 alternatives 161 us (6.0 TB/s of what is read, 76% of the memory's
 // cycles); 4096 x 32768 without 43 us (5.6 TB/s), its gradient 75 us (6.8 TB/s with what
-// L2 keeps; both bound by memory); 256 x 50257 10.3 us, with 20 13.8 (a row to a block,
-// 256 of them on 152 SMs), with 32 20.5, with all but 5 entries masked 42, entries that
-// repeat with the groups 369; one row of 131072 with 5 7.4 us; 32768 x 2000 35, 75 with 20
-// and 47; 4096 x 32768 float32 80, 92 with 20 and 153.  A gradient that lies otherwise
-// than its logits within 16 bytes, 4096 x 50257 of 50304 into a contiguous matrix: 196 us
-// for 121.  Before: alternatives by a pass each 6205 us for the first of these; powers with
+// L2 keeps; both bound by memory); 256 x 50257 10.3 us, with 20 14 to 18 (a row to a block,
+// 256 of them on 152 SMs), with 32 22 to 25, with all but 5 entries masked 42, entries that
+// repeat with the groups 369; one row of 131072 with 5 7.5 us; 32768 x 2000 37, 79 with 20
+// and 46; 4096 x 32768 float32 79, 91 with 20 and 154.  A gradient that lies otherwise
+// than its logits within 16 bytes, 4096 x 50257 of 50304 into a contiguous matrix: 200 us
+// for 119.  Before: alternatives by a pass each 6205 us for the first of these; powers with
 // subnormals 215; 64-bit steps and tests in whole rounds 173.
 #include "logits.cuh"
 
@@ -43,8 +43,11 @@ __device__ __forceinline__ float max_nan(float a, float b) {
   return r;
 }
 
-// 2^x, 0 below 2^-126: one instruction, where powers down to 2^-149 take four.  (In
-// sums of powers whose largest is 1.)
+// 2^x, 0 below 2^-126: one instruction, where powers down to 2^-149 take four.  In sums of
+// powers whose largest is 1, where neither that nor the power's error of some 2^-22 shows: the
+// results for 256 rows of 50257 are off by 5.2e-8 of themselves against 64 bits, for one row of
+// 131072 by 1.1e-7 (elementary operations in 32 bits: 6.4e-8 and 8.2e-8).  The same holds
+// for __expf, which takes what lies before and behind the whole loads and rows far from 0.
 __device__ __forceinline__ float exp2_of(float x) {
   float y;
   asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
@@ -440,8 +443,8 @@ __device__ __forceinline__ void no_top(uint64_t t, uint32_t top, uint32_t lane, 
   }
 }
 
-// A warp per row: short rows.  Ten blocks to an SM: 32768 x 2000 bfloat16 takes 35 us, and
-// 51 with 5 and 75 with 20 alternatives; eight blocks 37, 54 and 83, twelve 34, 56
+// A warp per row: short rows.  Ten blocks to an SM: 32768 x 2000 bfloat16 took 35 us, and
+// 51 with 5 and 75 with 20 alternatives (37 and 79 on another GPU, for 35 and 75); eight blocks 37, 54 and 83, twelve 34, 56
 // and 80.  With eight loads in flight and as many registers as they want it was 44, 75 and 99.
 template <class T, bool kTop>
 __global__ void __launch_bounds__(kWarpThreads, 10)

@@ -551,7 +551,8 @@ def _adapter_matmul(s, x, down, up, offsets, which, scales, base, out):
 def adapter_matmul_backward(f, dout, base=None, out=None, stream=None):
     """The gradients of ``(dout * f.out).sum()``: (dx, ddown, dup), in the matrices'
     type, from what ``adapter_matmul`` returned.  ``base`` [tokens, k] is added to dx
-    (the gradient through the shared projection), and may be ``out``, which takes dx."""
+    (the gradient through the shared projection), and may be ``out``, which takes dx.
+    Beyond some thousands of adapters and requests the time grows with their product."""
     return _call(f.x.device, stream, _adapter_matmul_backward, f, dout, base, out)
 
 

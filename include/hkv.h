@@ -443,7 +443,8 @@ hkv_status hkv_preference_loss_backward(uint64_t pairs, uint64_t rows, uint64_t 
  * a counted row that holds a NaN or +inf, or nothing above -inf, gives NaNs and
  * top_ids of -1.  For the backward call lse (NULL where it is not wanted) gets
  * two floats for each row, lse[t] and what that float leaves out of it.  top is
- * at most HKV_MAX_TOP and at most vocab. */
+ * at most HKV_MAX_TOP (the lanes of a warp, whose maxima bound it) and at most
+ * vocab. */
 #define HKV_MAX_TOP 32
 hkv_status hkv_token_logps(uint64_t rows, uint64_t vocab, const void* logits, int type,
                            uint64_t stride, const int64_t* labels, uint32_t top, float* logps,
@@ -467,7 +468,8 @@ hkv_status hkv_token_logps_backward(uint64_t rows, uint64_t vocab, const void* l
  * r * down_stride (up: up_step, up_stride) elements in, so that an adapter may
  * be a row of a larger buffer, as of a table's rows.  scales (device) has a
  * float32 factor for each adapter, NULL: 1.  1 <= rank <= HKV_MAX_RANK; strides
- * are at most 2^31, steps at most 2^40. */
+ * are at most 2^31, steps at most 2^40.  (64 ranks: a tile's sums by all ranks stay
+ * in a warp's registers and both factors' stages in shared memory.) */
 #define HKV_MAX_RANK 64
 typedef struct hkv_adapters {
   uint64_t count;
@@ -508,7 +510,9 @@ hkv_status hkv_adapter_matmul(uint64_t tokens, uint64_t k, uint64_t n, int type,
  * rank) are contiguous, in the matrices' type, rounded once, and zero for an
  * adapter of no request; either may be NULL.  dhidden is scratch like hidden, of its
  * own.  dx must not overlap x or dy, nor base unless it is base; ddown, dup and dhidden
- * must not overlap one another or anything else. */
+ * must not overlap one another or anything else.  Every adapter's blocks read all of
+ * which: beyond some thousands of adapters and requests that is most of the time, and
+ * it grows with their product. */
 hkv_status hkv_adapter_matmul_backward(uint64_t tokens, uint64_t k, uint64_t n, int type,
                                        const hkv_adapters* adapters, uint64_t requests,
                                        const int64_t* offsets, const int64_t* which, const void* x,
