@@ -94,3 +94,24 @@ def test_saved_memory_on_another_stream(hkv, make, given):
     torch.cuda.synchronize()
     assert all(torch.equal(u, v) for u, v in zip(got, want[0]))
     del junk
+
+
+@pytest.mark.parametrize("make", [_adapters, _logps, _preference, _matrix])
+def test_captured_after_an_eager_forward_call(hkv, make):
+    """The capturing stream is another than the forward call's."""
+    forward, backward, _ = make(hkv)
+    f = forward(None)
+    want = backward(f, None)
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        got = backward(f, None)
+    for t in got:
+        t.zero_()
+    for _ in range(2):
+        graph.replay()
+    torch.cuda.synchronize()
+    assert all(torch.equal(u, v) for u, v in zip(got, want))
+    del f, graph
+    assert forward(None) is not None
+    torch.cuda.synchronize()
